@@ -8,7 +8,9 @@ built, every call raises.
 
 Tensors are torch CUDA tensors, contiguous, in the layouts of ``gdn.h``:
 q, k [Ttot, Hk, dk]; v, out [Ttot, Hv, dv]; g, b [Ttot, Hv] (bf16 or fp32,
-all the same dtype); states [B, Hv, dv, dk] fp32; cu_seqlens int32 [B+1].
+all the same dtype); states [B, Hv, dv, dk] fp32; cu_seqlens int32 [B+1];
+paged caches [num_pages, Hkv, page_size, d] (the packed rows of the cache calls
+may have a token stride of their own).
 
 The per-call host cost is kept small because a decode step of a few
 sequences runs in a few microseconds on the GPU: the library handle and its
@@ -29,19 +31,22 @@ from . import _build
 __all__ = ["GDNError", "gdn_prefill", "gdn_prefill_ws", "gdn_prefill_workspace_size", "gdn_prefill_static",
            "gdn_prefill_from_host",
            "gdn_decode_step", "gdn_decode_step_slots", "gdn_prepass", "gdn_prefill_path",
+           "gdn_kv_write", "gdn_kv_read", "gdn_paged_attn", "gdn_paged_attn_workspace_size",
            "gdn_get_device_status", "gdn_status_string", "library", "library_path",
            "GDN_OK", "GDN_ERR_INVALID_ARG", "GDN_ERR_UNSUPPORTED", "GDN_ERR_CUDA",
-           "GDN_ERR_DEVICE_CHECK", "GDN_BF16", "GDN_F32"]
+           "GDN_ERR_DEVICE_CHECK", "GDN_BF16", "GDN_F32", "GDN_FP8", "GDN_INT8"]
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_DEVICE_CHECK = 0, -1, -2, -3, -4
-GDN_BF16, GDN_F32 = 0, 1
+GDN_BF16, GDN_F32, GDN_FP8, GDN_INT8 = 0, 1, 2, 3
 
 _lock = threading.Lock()
 _lib: ctypes.CDLL | None = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _DTYPE = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+_CACHE_DTYPE = {**_DTYPE, torch.float8_e4m3fn: GDN_FP8, torch.int8: GDN_INT8}
 # the current stream of a device as a raw cudaStream_t (falls back to the Stream object)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -86,6 +91,15 @@ def library() -> ctypes.CDLL:
             lib.gdn_prepass.restype = _I
             lib.gdn_prefill_path.argtypes = [_I] * 8
             lib.gdn_prefill_path.restype = _I
+            lib.gdn_kv_write.argtypes = [_P] * 9 + [_I] * 7 + [_L] * 2 + [_I] * 2 + [_P]
+            lib.gdn_kv_write.restype = _I
+            lib.gdn_kv_read.argtypes = [_P] * 9 + [_I] * 7 + [_L] * 2 + [_I] * 2 + [_P]
+            lib.gdn_kv_read.restype = _I
+            lib.gdn_paged_attn.argtypes = [_P] * 9 + [_I] * 8 + [_L, ctypes.c_float] + [_I] * 2 + \
+                [_P, ctypes.c_size_t, _P]
+            lib.gdn_paged_attn.restype = _I
+            lib.gdn_paged_attn_workspace_size.argtypes = [_I] * 6
+            lib.gdn_paged_attn_workspace_size.restype = ctypes.c_size_t
             lib.gdn_get_device_status.argtypes = [_P]
             lib.gdn_get_device_status.restype = _I
             lib.gdn_status_string.argtypes = [_I]
@@ -120,6 +134,15 @@ def _stream(stream, t: torch.Tensor | None = None):
             return _raw_stream(t.get_device() if t is not None else torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _torch_stream(stream, t: torch.Tensor):
+    """The torch stream object of `stream` (memory taken under it is not handed on before its work is done)."""
+    if stream is None:
+        return torch.cuda.current_stream(t.device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(_stream(stream), device=t.device)
 
 
 def _check(rc: int, where: str) -> None:
@@ -262,6 +285,109 @@ def gdn_prepass(q, k, g, b, rq, rk, beta, gcum, cu_seqlens=None, B=None, T=None,
                                chunk, _dtype_code(q), _ptr(rq), _ptr(rk), _ptr(beta), _ptr(gcum),
                                _stream(stream, q))
     _check(rc, "gdn_prepass")
+
+
+def _rows_ptr(t: torch.Tensor):
+    """Pointer of packed rows [Ttot, H, d] whose token stride is free (a slice of a fused projection)."""
+    if not t.is_cuda or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1) or \
+            (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+        raise ValueError("packed rows must be CUDA tensors [tokens, heads, d] with contiguous heads and elements")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _kv_sizes(rows, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, B, T):
+    """(B, T, Hkv, d, num_pages, page_size, max_pages, dtype, cache dtype) of a paged cache call."""
+    num_pages, Hkv, page_size, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must share one shape and dtype")
+    if rows.shape[2] != d:
+        raise ValueError(f"rows of {rows.shape[2]} elements for a cache of head dimension {d}")
+    cache_code = _CACHE_DTYPE.get(k_cache.dtype)
+    if cache_code is None:
+        raise TypeError(f"unsupported cache dtype {k_cache.dtype}: use the rows' dtype, float8_e4m3fn or int8")
+    if cache_code >= GDN_FP8:
+        for t in (k_scale, v_scale):
+            if t is None or t.dtype != torch.float32 or t.shape != k_cache.shape[:3]:
+                raise TypeError("an 8-bit cache needs fp32 k_scale and v_scale [num_pages, Hkv, page_size]")
+    if block_table.dtype != torch.int32 or kv_lens.dtype != torch.int32:
+        raise TypeError("block_table and kv_lens must be int32")
+    Ttot = rows.shape[0]
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype != torch.int32:
+            raise TypeError("cu_seqlens must be int32")
+        B, T = cu_seqlens.numel() - 1, Ttot
+    else:
+        B = kv_lens.numel() if B is None else B
+        T = (Ttot // B if B else 0) if T is None else T
+        if B * T != Ttot:
+            raise ValueError(f"{Ttot} tokens are not {B} sequences of {T}")
+    if kv_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("kv_lens must be [B] and block_table [B, max_pages]")
+    return B, T, Hkv, d, num_pages, page_size, block_table.shape[1], _dtype_code(rows), cache_code
+
+
+def gdn_kv_write(k, v, k_cache, v_cache, block_table, kv_lens, k_scale=None, v_scale=None, cu_seqlens=None,
+                 B=None, T=None, stream=None) -> None:
+    """Store new tokens' k, v [Ttot, Hkv, d] in paged caches [num_pages, Hkv, page_size, d] (of k's dtype,
+    float8_e4m3fn or int8; 8-bit caches with fp32 scales [num_pages, Hkv, page_size]). kv_lens counts the
+    new tokens in: token t of sequence n's T_n goes to position kv_lens[n] - T_n + t (negative: skipped)."""
+    lib = _lib or library()
+    if v.shape != k.shape or v.dtype != k.dtype or k.shape[1] != k_cache.shape[1]:
+        raise ValueError("k and v must share one dtype and the shape [tokens, Hkv, d]")
+    B, T, Hkv, d, pages, page, width, dt, cdt = _kv_sizes(k, k_cache, v_cache, k_scale, v_scale, block_table,
+                                                          kv_lens, cu_seqlens, B, T)
+    rc = lib.gdn_kv_write(_rows_ptr(k), _rows_ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                          _ptr(block_table), _ptr(kv_lens), _ptr(cu_seqlens), B, T, Hkv, d, pages, page, width,
+                          _row_stride(k), _row_stride(v), dt, cdt, _stream(stream, k))
+    if rc:
+        raise GDNError(rc, "gdn_kv_write")
+
+
+def gdn_kv_read(k_cache, v_cache, block_table, kv_lens, k, v, k_scale=None, v_scale=None, cu_seqlens=None,
+                B=None, T=None, stream=None) -> None:
+    """The last T_n cached rows of every sequence as values, into k, v [Ttot, Hkv, d] (padding: zeros)."""
+    lib = _lib or library()
+    if v.shape != k.shape or v.dtype != k.dtype or k.shape[1] != k_cache.shape[1]:
+        raise ValueError("k and v must share one dtype and the shape [tokens, Hkv, d]")
+    B, T, Hkv, d, pages, page, width, dt, cdt = _kv_sizes(k, k_cache, v_cache, k_scale, v_scale, block_table,
+                                                          kv_lens, cu_seqlens, B, T)
+    rc = lib.gdn_kv_read(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
+                         _ptr(kv_lens), _ptr(cu_seqlens), _rows_ptr(k), _rows_ptr(v), B, T, Hkv, d, pages, page,
+                         width, _row_stride(k), _row_stride(v), dt, cdt, _stream(stream, k))
+    if rc:
+        raise GDNError(rc, "gdn_kv_read")
+
+
+def gdn_paged_attn_workspace_size(B, T, Hq, Hkv, d, packed=False) -> int:
+    """Bytes of device workspace gdn_paged_attn needs (packed: cu_seqlens is given, T the packed total)."""
+    return int(library().gdn_paged_attn_workspace_size(B, T, int(packed), Hq, Hkv, d))
+
+
+def gdn_paged_attn(q, k_cache, v_cache, block_table, kv_lens, out, k_scale=None, v_scale=None, cu_seqlens=None,
+                   B=None, T=None, scale=None, workspace=None, stream=None) -> None:
+    """Causal attention of the new tokens' q [Ttot, Hq, d] over their sequences' paged caches, into `out`.
+    `scale` is d**-0.5 unless given. `workspace`: a uint8 CUDA tensor of gdn_paged_attn_workspace_size(...)
+    bytes that a program keeps; without one the call takes it from torch's allocator."""
+    lib = _lib or library()
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out must share one shape and dtype")
+    B, T, Hkv, d, pages, page, width, dt, cdt = _kv_sizes(q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                                          kv_lens, cu_seqlens, B, T)
+    Hq = q.shape[1]
+    if workspace is None:
+        need = lib.gdn_paged_attn_workspace_size(B, T, int(cu_seqlens is not None), Hq, Hkv, d)
+        with torch.cuda.device(q.device), torch.cuda.stream(_torch_stream(stream, q)):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    rc = lib.gdn_paged_attn(_rows_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                            _ptr(block_table), _ptr(kv_lens), _ptr(cu_seqlens), _ptr(out), B, T, Hq, Hkv, d, pages,
+                            page, width, _row_stride(q), d ** -0.5 if scale is None else scale, dt, cdt,
+                            _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream, q))
+    if rc:
+        raise GDNError(rc, "gdn_paged_attn")
 
 
 def gdn_prefill_path(B, T, Hk, Hv, dk, dv, chunk, dtype) -> int:

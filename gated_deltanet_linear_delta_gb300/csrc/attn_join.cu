@@ -1,0 +1,146 @@
+// attn_join.cu -- the parts of units that were split between CTAs become output rows.
+//
+// Part p of a row holds O_p = sum_j exp2(s_j - m_p) v_j, m_p and l_p = sum_j exp2(s_j - m_p) over
+// its keys; the row is (sum_p e^{m_p - m} O_p) / (sum_p e^{m_p - m} l_p), m = max_p m_p (base 2).
+//
+// A split unit is joined once, by the blocks of the first boundary between pieces that lies in
+// it. Each row takes a whole block: its 8 warps share the parts (one session's single token over a
+// long cache has about 75 parts, and they should be in flight together), then add up through
+// shared memory in a fixed order. Blocks whose boundary lies between units have nothing to do.
+// The kernel is launched so that it may become resident while the attention kernel runs, and
+// waits for it here, which hides its launch.
+#include "attn_plan.cuh"
+#include "attn_work.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kJoinThreads = 256;
+
+template <typename TOut, int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork w, TOut *out, int Hq) {
+    constexpr int E = D / 32, NW = kJoinThreads / 32;
+    __shared__ float acc[NW][D];
+    __shared__ float2 ml[NW];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x + 1, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const AttnRec r = w.rec[c];
+    if (c >= r.active || r.off == 0) return;
+    if (r.off > w.rec[c - 1].tiles) return;  // an earlier boundary lies in this unit too
+    SeqInfo s;
+    if (!seq_info(w.pg, r.n, &s)) return;
+    // last part: pieces c.. while the unit goes on
+    int last = c, have = r.off + r.tiles;
+    while (have < r.ntiles && last + 1 < r.active) have += w.rec[++last].tiles;
+    const int parts = last - c + 2;
+    const int t0 = r.i * w.TPT, rows = min(w.TPT, s.T - t0) * w.G;
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        const int t = t0 + row / w.G;
+        const bool live = s.len - s.T + t >= 0;  // the rows of padding tokens are written elsewhere
+        float m = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int k = wid; live && k < parts; k += NW) {
+            const long at = part_index(w, c - 1 + k, k == 0 ? 1 : 0, row);
+            const float2 pm = w.ml[at];
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+                const float2 f = *reinterpret_cast<const float2 *>(w.part + at * D + e * 32 + 2 * lane);
+                x[e] = f.x;
+                x[e + 1] = f.y;
+            }
+            if (pm.x == -INFINITY) continue;  // no key of this part is seen by the row
+            const float mn = fmaxf(m, pm.x);
+            const float a = exp2f(m - mn), b = exp2f(pm.x - mn);
+            m = mn;
+            l = l * a + pm.y * b;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = o[e] * a + x[e] * b;
+        }
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<float2 *>(&acc[wid][e * 32 + 2 * lane]) = make_float2(o[e], o[e + 1]);
+        if (lane == 0) ml[wid] = make_float2(m, l);
+        __syncthreads();
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) M = fmaxf(M, ml[k].x);
+        if (M == -INFINITY) M = 0.f;
+        float f[NW];
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            f[k] = exp2f(ml[k].x - M);
+            L += f[k] * ml[k].y;
+        }
+        const int h = r.h * w.G + row % w.G;
+        if (live)
+            for (int e = threadIdx.x; e < D; e += kJoinThreads) {
+                float x = 0.f;
+#pragma unroll
+                for (int k = 0; k < NW; ++k) x += f[k] * acc[k][e];
+                out[((s.bos + t) * Hq + h) * D + e] = from_f32<TOut>(L == 0.f ? 0.f : x / L);
+            }
+        __syncthreads();
+    }
+}
+
+template <typename TOut, int D>
+cudaError_t launch_t(const AttnWork &w, TOut *out, int Hq, int rows, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(kAttnCtas - 1, (unsigned)(rows < 16 ? rows : 16), 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<TOut, D>, w, out, Hq);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_join(const AttnArgs &a, const AttnWork &w, cudaStream_t s) {
+    const bool f32 = a.pg.dtype == GDN_F32;
+#define GDN_JOIN_CASE(DV)                                                                      \
+    case DV:                                                                                   \
+        return f32 ? launch_t<float, DV>(w, (float *)a.out, a.Hq, w.rows, s)                   \
+                   : launch_t<__nv_bfloat16, DV>(w, (__nv_bfloat16 *)a.out, a.Hq, w.rows, s);
+    switch (a.pg.d) { GDN_JOIN_CASE(64) GDN_JOIN_CASE(128) GDN_JOIN_CASE(256) }
+#undef GDN_JOIN_CASE
+    return cudaErrorInvalidValue;
+}
+
+namespace {
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+}  // namespace
+
+int attn_unit_rows(long tokens_per_seq, int G) {
+    const long rows = tokens_per_seq * G;
+    return (int)(rows < kAttnMaxRows ? rows : kAttnMaxRows / G * G);
+}
+
+size_t attn_workspace(long tokens_per_seq, int G, int d) {
+    const size_t parts = (size_t)kAttnCtas * 2 * attn_unit_rows(tokens_per_seq, G);
+    return up256(kAttnCtas * sizeof(AttnRec)) + up256(parts * sizeof(float2)) + parts * d * sizeof(float);
+}
+
+AttnWork attn_work(const AttnArgs &a, int tokens_per_tile, int min_tiles) {
+    AttnWork w{};
+    w.pg = a.pg;
+    w.G = a.Hq / a.pg.Hkv;
+    w.TPT = tokens_per_tile;
+    w.rows = attn_unit_rows(a.pg.cu ? a.pg.Ttot : a.pg.T, w.G);
+    w.min_tiles = min_tiles;
+    const size_t parts = (size_t)kAttnCtas * 2 * w.rows;
+    uint8_t *ws = static_cast<uint8_t *>(a.ws);
+    w.rec = reinterpret_cast<AttnRec *>(ws);
+    ws += up256(kAttnCtas * sizeof(AttnRec));
+    w.ml = reinterpret_cast<float2 *>(ws);
+    ws += up256(parts * sizeof(float2));
+    w.part = reinterpret_cast<float *>(ws);
+    return w;
+}
+
+}  // namespace gdn

@@ -1,0 +1,237 @@
+// attn_plan.cuh -- how the attention over a paged cache is cut into work, and the join of split
+// rows' parts.
+//
+// A unit is (sequence n, key head h, row tile i): the query heads that share h of TPT consecutive
+// new tokens, TPT * G rows, walked over key tiles of BN positions up to the last one any of its
+// rows sees. Units have very different lengths (one token over 100 or over 100,000 positions), and
+// the host does not know them (kv_lens is device data, and a captured graph replays with others),
+// so the cut is made on the device: all units' key tiles form one line, in the order n, h, i, and
+// each of at most kAttnCtas CTAs takes an equal piece of it. A CTA thus finishes some units alone
+// and shares at most two with its neighbours; of those it leaves the unnormalised output, the
+// running maximum and the sum in the workspace, and the joining kernel combines them. Every CTA
+// finds its piece from kv_lens alone: no counters, no atomics, and the same order of sums each time.
+#pragma once
+
+#include "kv_pages.cuh"
+
+namespace gdn {
+
+struct AttnRec {  // where CTA c's piece starts; read by the joining kernel
+    int n, h, i;   // unit
+    int off;       // key tiles of the unit before the piece (0: the unit starts here)
+    int ntiles;    // key tiles of the unit
+    int tiles;     // key tiles in the piece
+    int active;    // pieces in all
+    int pad;
+};
+
+struct AttnWork {
+    KvPages pg;
+    int G;         // query heads per key head
+    int TPT;       // tokens per row tile
+    int rows;      // workspace rows per part
+    int min_tiles; // a piece is not cut below this
+    AttnRec *rec;  // [kAttnCtas]
+    float2 *ml;    // [kAttnCtas][2][rows] running maximum (log2 domain) and sum
+    float *part;   // [kAttnCtas][2][rows][d]
+};
+
+// part of CTA c: 0 = it continues a unit begun before, 1 = it begins a unit that goes on after it
+__device__ __forceinline__ long part_index(const AttnWork &w, int c, int slot, int row) {
+    return ((long)c * 2 + slot) * w.rows + row;
+}
+
+// key tiles of row tile i of a sequence
+template <int BN>
+__device__ __forceinline__ int unit_tiles(const AttnWork &w, const SeqInfo &s, int i) {
+    const int t = min(s.T, (i + 1) * w.TPT);  // tokens up to the tile's last
+    const int keys = s.len - s.T + t;
+    return keys > 0 ? (keys + BN - 1) / BN : 0;
+}
+__device__ __forceinline__ int row_tiles(const AttnWork &w, const SeqInfo &s) { return (s.T + w.TPT - 1) / w.TPT; }
+
+// Key tiles of all row tiles of one head, of the sequence that each thread holds; a warp works
+// together on sequences of many row tiles.
+template <int BN>
+__device__ __forceinline__ long seq_tiles(const AttnWork &w, const SeqInfo &s) {
+    const int lane = threadIdx.x & 31, nq = row_tiles(w, s);
+    long sum = 0;
+    const bool big = nq > 4;
+    if (!big)
+        for (int i = 0; i < nq; ++i) sum += unit_tiles<BN>(w, s, i);
+    for (unsigned m = __ballot_sync(0xffffffffu, big); m; m &= m - 1) {
+        const int src = __ffs(m) - 1;
+        SeqInfo o;
+        o.bos = 0;
+        o.T = __shfl_sync(0xffffffffu, s.T, src);
+        o.len = __shfl_sync(0xffffffffu, s.len, src);
+        const int onq = __shfl_sync(0xffffffffu, nq, src);
+        long x = 0;
+        for (int i = lane; i < onq; i += 32) x += unit_tiles<BN>(w, o, i);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        if (lane == src) sum = x;
+    }
+    return sum;
+}
+
+// A CTA's piece and the unit it is at.
+struct Piece {
+    int n, h, i;     // unit
+    int off;         // its next key tile
+    int ntiles;      // its key tiles
+    long left;       // key tiles left in the piece
+    SeqInfo s;
+};
+
+struct PlanSmem {
+    long sum[32];
+    int found;
+    Piece piece;
+};
+
+// Finds this CTA's piece; every thread of the CTA calls it (NT threads, a multiple of 32, at most
+// 1024). The result is in sm->piece (left = 0: no work), and its record in the workspace.
+template <int BN, int NT>
+__device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    constexpr int NW = NT / 32;
+    const KvPages &p = w.pg;
+    // all key tiles; the first NT sequences' stay in registers
+    long mine = 0, first = 0;
+    SeqInfo s0{0, 0, 0};
+    for (int base = 0; base < p.B; base += NT) {
+        SeqInfo s{0, 0, 0};
+        if (base + tid < p.B) seq_info(p, base + tid, &s);
+        const long x = seq_tiles<BN>(w, s) * p.Hkv;
+        mine += x;
+        if (base == 0) { first = x; s0 = s; }
+    }
+    long x = mine;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    if (lane == 0) sm->sum[wid] = x;
+    if (tid == 0) sm->found = -1;
+    __syncthreads();
+    long total = 0;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) total += sm->sum[k];
+    __syncthreads();
+    const long want = (total + w.min_tiles - 1) / w.min_tiles;
+    const int active = (int)(want < (long)gridDim.x ? want : (long)gridDim.x);
+    const int c = blockIdx.x;
+    const long begin = c < active ? total * c / active : total;
+    long end = c < active ? total * (c + 1) / active : total;
+    // the sequence that holds `begin`
+    long before = 0;
+    if (begin < end) {
+        for (int base = 0; base < p.B; base += NT) {
+            SeqInfo s = s0;
+            long y = first;
+            if (base > 0) {
+                s = SeqInfo{0, 0, 0};
+                if (base + tid < p.B) seq_info(p, base + tid, &s);
+                y = seq_tiles<BN>(w, s) * p.Hkv;
+            }
+            long inc = y;  // inclusive scan over the CTA
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long o = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += o;
+            }
+            if (lane == 31) sm->sum[wid] = inc;
+            __syncthreads();
+            long pre = before, all = before;
+#pragma unroll
+            for (int k = 0; k < NW; ++k) {
+                if (k < wid) pre += sm->sum[k];
+                all += sm->sum[k];
+            }
+            pre += inc - y;
+            if (begin >= pre && begin < pre + y) {
+                sm->found = base + tid;
+                sm->piece.n = base + tid;
+                sm->piece.s = s;
+                sm->piece.left = begin - pre;  // for now: key tiles before the piece in this sequence
+            }
+            before = all;
+            __syncthreads();
+            if (sm->found >= 0) break;
+        }
+        if (sm->found < 0) end = begin;  // only if kv_lens changed under the call
+    }
+    if (wid == 0) {  // head and row tile within the sequence
+        Piece pc{};
+        if (begin < end) {
+            pc = sm->piece;
+            const int nq = row_tiles(w, pc.s);
+            long per_head = 0;
+            for (int i = lane; i < nq; i += 32) per_head += unit_tiles<BN>(w, pc.s, i);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) per_head += __shfl_xor_sync(0xffffffffu, per_head, d);
+            pc.h = (int)(pc.left / per_head);
+            long rem = pc.left % per_head;
+            for (int i0 = 0; i0 < nq; i0 += 32) {
+                const int t = i0 + lane < nq ? unit_tiles<BN>(w, pc.s, i0 + lane) : 0;
+                int inc = t;  // at most 32 * 2^31 / BN: fits
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, inc, d);
+                    if (lane >= d) inc += o;
+                }
+                const int chunk = __shfl_sync(0xffffffffu, inc, 31);
+                if (rem < chunk) {
+                    const unsigned m = __ballot_sync(0xffffffffu, rem < inc);
+                    const int src = __ffs(m) - 1;
+                    pc.i = i0 + src;
+                    pc.ntiles = __shfl_sync(0xffffffffu, t, src);
+                    pc.off = (int)rem - (__shfl_sync(0xffffffffu, inc, src) - pc.ntiles);
+                    break;
+                }
+                rem -= chunk;
+            }
+        }
+        pc.left = end - begin;
+        if (lane == 0) {
+            sm->piece = pc;
+            AttnRec r{pc.n, pc.h, pc.i, pc.off, pc.ntiles, (int)pc.left, active, 0};
+            w.rec[c] = r;
+        }
+    }
+    __syncthreads();
+}
+
+// The unit after the piece's current one that has any key tiles (left > 0 says there is one).
+template <int BN>
+__device__ __forceinline__ void next_unit(const AttnWork &w, Piece *pc) {
+    pc->off = 0;
+    do {
+        if (++pc->i >= row_tiles(w, pc->s)) {
+            pc->i = 0;
+            if (++pc->h >= w.pg.Hkv) {
+                pc->h = 0;
+                if (++pc->n >= w.pg.B) {  // kv_lens changed under the call: stop instead of running off
+                    pc->left = 0;
+                    return;
+                }
+                seq_info(w.pg, pc->n, &pc->s);  // no tokens where cu is inconsistent
+            }
+        }
+        pc->ntiles = pc->i < row_tiles(w, pc->s) ? unit_tiles<BN>(w, pc->s, pc->i) : 0;
+    } while (pc->ntiles == 0);
+}
+
+// Rows of padding tokens are zeros; no unit of work covers them.
+template <typename TOut>
+__device__ void zero_padding(const AttnWork &w, TOut *out, int Hq, int d) {
+    for (int n = blockIdx.x; n < w.pg.B; n += gridDim.x) {
+        SeqInfo s;
+        if (!seq_info(w.pg, n, &s)) continue;
+        const long idle = (long)min(s.T, max(0, s.T - s.len)) * Hq * d;
+        uint4 *p = reinterpret_cast<uint4 *>(out + s.bos * Hq * d);
+        const long pieces = idle * (long)sizeof(TOut) / 16;
+        for (long e = threadIdx.x; e < pieces; e += blockDim.x) p[e] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+}  // namespace gdn

@@ -1,0 +1,259 @@
+// attn_simt.cu -- attention over a paged cache on the CUDA cores, in fp32 throughout.
+//
+// A CTA of 256 threads holds a row tile of Q and walks key tiles of 64 positions: scores by register
+// tiles (each thread RT rows x 4 keys), softmax statistics per row by shuffles over the 16
+// threads that share it, and the output tile (RT rows x D/16 columns a thread) in registers,
+// rescaled when the running maximum grows. It is bound by shared-memory reads (5 to 8 16-byte reads
+// per 16 to 64 multiply-adds): correct and steady, but no performance path.
+#include <algorithm>
+
+#include "attn_plan.cuh"
+#include "attn_work.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int BN = 64;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T>
+struct SimtParams {
+    AttnWork w;
+    const T *q;
+    const void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    T *out;
+    int Hq;
+    long q_stride;
+    float scale2;  // softmax scale * log2 e
+};
+
+__device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+}
+
+// 4 elements of cached row `at` (page, head, offset flattened), dequantised; KIND is GDN_FP8,
+// GDN_INT8, or anything else for a cache of type T
+template <typename T, int KIND, int D>
+__device__ __forceinline__ float4 cached4(const void *cache, const float *scale, long at, int c) {
+    if constexpr (KIND != GDN_FP8 && KIND != GDN_INT8) {
+        return load4((const T *)cache + at * D + c);
+    } else {
+        const uint32_t code = *reinterpret_cast<const uint32_t *>((const uint8_t *)cache + at * D + c);
+        float x[4];
+        if (KIND == GDN_FP8) decode4_e4m3(code, x);
+        else decode4_int8(code, x);
+        const float s = scale[at];
+        return make_float4(x[0] * s, x[1] * s, x[2] * s, x[3] * s);
+    }
+}
+
+template <int D, int R>
+struct SimtSmem {
+    float q[R][D + 4];
+    float k[BN][D + 4];
+    float v[BN][D];
+    float p[R][BN + 4];
+    long at[BN];  // pool row of each key of the tile, or -1
+    PlanSmem plan;
+};
+
+template <typename T, int KIND, int D, int R>
+__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams<T> a) {
+    constexpr int RT = R / 16, CT = D / 64;  // rows and groups of 4 columns per thread
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    SimtSmem<D, R> &sm = *reinterpret_cast<SimtSmem<D, R> *>(smem_raw);
+    const AttnWork &w = a.w;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    plan_piece<BN, kThreads>(w, &sm.plan);
+    zero_padding(w, a.out, a.Hq, D);
+    Piece pc = sm.plan.piece;
+    for (bool begun = pc.off == 0; pc.left > 0; begun = true) {
+        const int t0 = pc.i * w.TPT, rows = min(w.TPT, pc.s.T - t0) * w.G;
+        const int off = pc.off, take = (int)min((long)(pc.ntiles - off), pc.left);
+        __syncthreads();
+        for (int e = tid; e < R * (D / 4); e += kThreads) {
+            const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < rows)
+                x = load4(a.q + (pc.s.bos + t0 + r / w.G) * a.q_stride + (long)(pc.h * w.G + r % w.G) * D + c);
+            *reinterpret_cast<float4 *>(&sm.q[r][c]) = x;
+        }
+        float m[RT], l[RT];
+        float4 o[RT][CT];
+        int limit[RT];  // last position the row sees
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+            limit[r] = pc.s.len - pc.s.T + t0 + (ty * RT + r) / w.G;
+            if (ty * RT + r >= rows) limit[r] = -1;
+#pragma unroll
+            for (int c = 0; c < CT; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int j = off; j < off + take; ++j) {
+            __syncthreads();  // the tile before is used up
+            if (tid < BN) {
+                const int pos = j * BN + tid;
+                long at = -1;
+                if (pos < pc.s.len) {
+                    const long pg = pool_page(w.pg, pc.n, pos);
+                    if (pg >= 0) at = (pg * w.pg.Hkv + pc.h) * w.pg.page_size + pos % w.pg.page_size;
+                }
+                sm.at[tid] = at;
+            }
+            __syncthreads();
+            for (int e = tid; e < BN * (D / 4); e += kThreads) {
+                const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+                const long at = sm.at[r];
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;  // a position past the end adds 0 * 0
+                if (at >= 0) {
+                    x = cached4<T, KIND, D>(a.k_cache, a.k_scale, at, c);
+                    y = cached4<T, KIND, D>(a.v_cache, a.v_scale, at, c);
+                }
+                *reinterpret_cast<float4 *>(&sm.k[r][c]) = x;
+                *reinterpret_cast<float4 *>(&sm.v[r][c]) = y;
+            }
+            __syncthreads();
+            float s[RT][4];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) s[r][c] = 0.f;
+#pragma unroll 4
+            for (int d = 0; d < D; d += 4) {
+                float4 kk[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) kk[c] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * c][d]);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const float4 qq = *reinterpret_cast<const float4 *>(&sm.q[ty * RT + r][d]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[r][c] += dot4(qq, kk[c]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    s[r][c] = j * BN + tx + 16 * c <= limit[r] ? s[r][c] * a.scale2 : -INFINITY;
+                    top = fmaxf(top, s[r][c]);
+                }
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const float mn = fmaxf(m[r], top), ref = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m[r] - ref);
+                m[r] = mn;
+                float add = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float e = exp2f(s[r][c] - ref);
+                    add += e;
+                    sm.p[ty * RT + r][tx + 16 * c] = e;
+                }
+                l[r] = l[r] * f + add;
+#pragma unroll
+                for (int c = 0; c < CT; ++c) { o[r][c].x *= f; o[r][c].y *= f; o[r][c].z *= f; o[r][c].w *= f; }
+            }
+            __syncwarp();  // a row's probabilities are written and read by the same half warp
+#pragma unroll 2
+            for (int k = 0; k < BN; k += 4) {
+                float4 pp[RT];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) pp[r] = *reinterpret_cast<const float4 *>(&sm.p[ty * RT + r][k]);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c) {
+                        const float4 vv = *reinterpret_cast<const float4 *>(&sm.v[k + kk][64 * c + 4 * tx]);
+#pragma unroll
+                        for (int r = 0; r < RT; ++r) {
+                            const float e = kk == 0 ? pp[r].x : kk == 1 ? pp[r].y : kk == 2 ? pp[r].z : pp[r].w;
+                            o[r][c].x += e * vv.x; o[r][c].y += e * vv.y; o[r][c].z += e * vv.z; o[r][c].w += e * vv.w;
+                        }
+                    }
+            }
+            __syncwarp();
+        }
+        const bool whole = begun && off + take == pc.ntiles;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            float sum = l[r];
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            const int row = ty * RT + r;
+            if (row >= rows) continue;
+            if (whole) {
+                if (limit[r] < 0) continue;  // padding: already zeros
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;  // scores that are all -inf: zeros
+                T *dst = a.out + ((pc.s.bos + t0 + row / w.G) * a.Hq + pc.h * w.G + row % w.G) * D;
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    store4(dst + 64 * c + 4 * tx,
+                           make_float4(o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv));
+            } else {
+                const long at = part_index(w, blockIdx.x, begun ? 1 : 0, row);
+                if (tx == 0) w.ml[at] = make_float2(m[r], sum);
+#pragma unroll
+                for (int c = 0; c < CT; ++c) *reinterpret_cast<float4 *>(w.part + at * D + 64 * c + 4 * tx) = o[r][c];
+            }
+        }
+        pc.left -= take;
+        if (pc.left > 0) next_unit<BN>(w, &pc);
+    }
+}
+
+template <typename T, int KIND, int D, int R>
+cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
+    const int G = a.Hq / a.pg.Hkv;
+    SimtParams<T> p{attn_work(a, R / G, 2), (const T *)a.q, a.k_cache, a.v_cache, a.k_scale, a.v_scale,
+                    (T *)a.out, a.Hq, a.q_stride, a.scale * kLog2e};
+    auto kernel = attn_simt_kernel<T, KIND, D, R>;
+    constexpr int bytes = sizeof(SimtSmem<D, R>);
+    static_assert(bytes <= 232448, "over the 227 KiB opt-in limit");
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<kAttnCtas, kThreads, bytes, s>>>(p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_attn_join(a, p.w, s);
+}
+
+template <typename T, int KIND, int D>
+cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
+    // a row tile of 16 where no sequence has more rows: a quarter of the products of the 64-row tile
+    const long rows = (a.pg.cu ? a.pg.Ttot : a.pg.T) * (a.Hq / a.pg.Hkv);
+    return rows <= 16 ? launch_t<T, KIND, D, 16>(a, s) : launch_t<T, KIND, D, 64>(a, s);
+}
+
+template <typename T, int KIND>
+cudaError_t launch_d(const AttnArgs &a, cudaStream_t s) {
+    switch (a.pg.d) {
+        case 64: return launch_rows<T, KIND, 64>(a, s);
+        case 128: return launch_rows<T, KIND, 128>(a, s);
+        case 256: return launch_rows<T, KIND, 256>(a, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t launch_kind(const AttnArgs &a, cudaStream_t s) {
+    switch (a.pg.cache_dtype) {
+        case GDN_FP8: return launch_d<T, GDN_FP8>(a, s);
+        case GDN_INT8: return launch_d<T, GDN_INT8>(a, s);
+        default: return launch_d<T, GDN_BF16>(a, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t s) {
+    return a.pg.dtype == GDN_F32 ? launch_kind<float>(a, s) : launch_kind<__nv_bfloat16>(a, s);
+}
+
+}  // namespace gdn

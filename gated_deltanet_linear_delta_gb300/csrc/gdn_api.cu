@@ -107,6 +107,63 @@ int prefill_checks(const void *q, const void *k, const void *v, const void *g, c
     return GDN_OK;
 }
 
+// What the three paged cache calls share. Sizes first (a call with no tokens touches no pointer),
+// then the pointers that every call reads.
+int kv_checks(int B, int T, const int32_t *cu, int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages,
+              int dtype, int cache_dtype, int64_t stride_a, int64_t stride_b) {
+    if (B < 0 || T < 0 || B > 65535 || num_pages < 0 || max_pages < 0) return GDN_ERR_INVALID_ARG;
+    if (Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || Hq > 65535) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_BF16 && dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+    if (cache_dtype != dtype && cache_dtype != GDN_FP8 && cache_dtype != GDN_INT8) return GDN_ERR_UNSUPPORTED;
+    if (d != 64 && d != 128 && d != 256) return GDN_ERR_UNSUPPORTED;
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1))) return GDN_ERR_UNSUPPORTED;
+    if (Hq / Hkv > 64) return GDN_ERR_UNSUPPORTED;
+    const long long Ttot = cu ? (long long)T : (long long)B * T;
+    if (Ttot * Hq > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
+    if ((long long)num_pages * Hkv > 0x7fffffffLL || (long long)max_pages * page_size > 0x7fffffffLL)
+        return GDN_ERR_INVALID_ARG;
+    const int64_t vec = dtype == GDN_BF16 ? 8 : 4;  // 16 bytes
+    if (stride_a < (int64_t)Hq * d || stride_a % vec || stride_b < (int64_t)Hkv * d || stride_b % vec)
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+int kv_pointers(const void *k_cache, const void *v_cache, const void *k_scale, const void *v_scale,
+                const int32_t *block_table, const int32_t *kv_lens, const int32_t *cu, int num_pages, int max_pages,
+                int dtype, int cache_dtype, const void *a, const void *b) {
+    const bool codes = cache_dtype != dtype;
+    if (!a || !b || !aligned16(a) || !aligned16(b)) return GDN_ERR_INVALID_ARG;
+    // lengths and tables may be slices of a larger batch's
+    if (!kv_lens || ((reinterpret_cast<uintptr_t>(kv_lens) | reinterpret_cast<uintptr_t>(block_table)) & 3u))
+        return GDN_ERR_INVALID_ARG;
+    if (num_pages > 0 && (!k_cache || !v_cache || (codes && (!k_scale || !v_scale)))) return GDN_ERR_INVALID_ARG;
+    if (max_pages > 0 && !block_table) return GDN_ERR_INVALID_ARG;
+    const void *ptrs[] = {k_cache, v_cache, k_scale, v_scale, cu};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+gdn::KvPages kv_pages(const int32_t *block_table, const int32_t *kv_lens, const int32_t *cu, int B, int T, int Hkv,
+                      int d, int num_pages, int page_size, int max_pages, int dtype, int cache_dtype, int *status) {
+    gdn::KvPages p{};
+    p.table = block_table;
+    p.kv_lens = kv_lens;
+    p.cu = cu;
+    p.B = B;
+    p.T = T;
+    p.Ttot = cu ? (long)T : (long)B * T;
+    p.Hkv = Hkv;
+    p.d = d;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.dtype = dtype;
+    p.cache_dtype = cache_dtype;
+    p.status = status;
+    return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -302,6 +359,86 @@ int gdn_prepass(const void *q, const void *k, const void *g, const void *b,
                        status};
     return gdn::launch_prepass(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK
                                                                                      : GDN_ERR_CUDA;
+}
+
+int gdn_kv_write(const void *k, const void *v, void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                 const int32_t *block_table, const int32_t *kv_lens, const int32_t *cu_seqlens, int B, int T,
+                 int Hkv, int d, int num_pages, int page_size, int max_pages, int64_t k_stride, int64_t v_stride,
+                 int dtype, int cache_dtype, void *stream) {
+    int rc = kv_checks(B, T, cu_seqlens, Hkv, Hkv, d, num_pages, page_size, max_pages, dtype, cache_dtype, k_stride,
+                       v_stride);
+    if (rc != GDN_OK || B == 0 || T == 0) return rc;
+    rc = kv_pointers(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, num_pages, max_pages, dtype,
+                     cache_dtype, k, v);
+    if (rc != GDN_OK) return rc;
+    int *status = status_ptr();
+    if (!status) return GDN_ERR_CUDA;
+    gdn::KvArgs a{kv_pages(block_table, kv_lens, cu_seqlens, B, T, Hkv, d, num_pages, page_size, max_pages, dtype,
+                           cache_dtype, status),
+                  const_cast<void *>(k), const_cast<void *>(v), k_cache, v_cache, k_scale, v_scale, (long)k_stride,
+                  (long)v_stride};
+    return gdn::launch_kv_write(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_kv_read(const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+                const int32_t *block_table, const int32_t *kv_lens, const int32_t *cu_seqlens, void *k, void *v,
+                int B, int T, int Hkv, int d, int num_pages, int page_size, int max_pages, int64_t k_stride,
+                int64_t v_stride, int dtype, int cache_dtype, void *stream) {
+    int rc = kv_checks(B, T, cu_seqlens, Hkv, Hkv, d, num_pages, page_size, max_pages, dtype, cache_dtype, k_stride,
+                       v_stride);
+    if (rc != GDN_OK || B == 0 || T == 0) return rc;
+    rc = kv_pointers(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, num_pages, max_pages, dtype,
+                     cache_dtype, k, v);
+    if (rc != GDN_OK) return rc;
+    int *status = status_ptr();
+    if (!status) return GDN_ERR_CUDA;
+    gdn::KvArgs a{kv_pages(block_table, kv_lens, cu_seqlens, B, T, Hkv, d, num_pages, page_size, max_pages, dtype,
+                           cache_dtype, status),
+                  k, v, const_cast<void *>(k_cache), const_cast<void *>(v_cache), const_cast<float *>(k_scale),
+                  const_cast<float *>(v_scale), (long)k_stride, (long)v_stride};
+    return gdn::launch_kv_read(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+size_t gdn_paged_attn_workspace_size(int B, int T, int packed, int Hq, int Hkv, int d) {
+    static const int32_t some = 0;
+    const int32_t *cu = packed ? &some : nullptr;
+    if (kv_checks(B, T, cu, Hq, Hkv, d, 1, 16, 1, GDN_BF16, GDN_BF16, (int64_t)Hq * d, (int64_t)Hkv * d) != GDN_OK ||
+        B == 0 || T == 0)
+        return 0;
+    return gdn::attn_workspace(T, Hq / Hkv, d);
+}
+
+int gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                   const float *v_scale, const int32_t *block_table, const int32_t *kv_lens,
+                   const int32_t *cu_seqlens, void *out, int B, int T, int Hq, int Hkv, int d, int num_pages,
+                   int page_size, int max_pages, int64_t q_stride, float scale, int dtype, int cache_dtype,
+                   void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = kv_checks(B, T, cu_seqlens, Hq, Hkv, d, num_pages, page_size, max_pages, dtype, cache_dtype, q_stride,
+                       (int64_t)Hkv * d);
+    if (rc != GDN_OK || B == 0 || T == 0) return rc;
+    if (num_pages == 0 || max_pages == 0) return GDN_ERR_INVALID_ARG;
+    rc = kv_pointers(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, num_pages, max_pages, dtype,
+                     cache_dtype, q, out);
+    if (rc != GDN_OK) return rc;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+        workspace_bytes < gdn::attn_workspace(T, Hq / Hkv, d))
+        return GDN_ERR_INVALID_ARG;
+    int *status = status_ptr();
+    if (!status) return GDN_ERR_CUDA;
+    gdn::AttnArgs a{};
+    a.pg = kv_pages(block_table, kv_lens, cu_seqlens, B, T, Hkv, d, num_pages, page_size, max_pages, dtype,
+                    cache_dtype, status);
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.out = out;
+    a.Hq = Hq;
+    a.q_stride = (long)q_stride;
+    a.scale = scale;
+    a.ws = workspace;
+    return gdn::launch_attn_simt(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 int gdn_get_device_status(void *stream) {

@@ -38,6 +38,46 @@ struct PrepassArgs {
     int *status;
 };
 
+// Paged key/value caches: pools [num_pages][Hkv][page_size][d], sequence n's position p on page
+// table[n][p / page_size]; new token t of T_n has position kv_lens[n] - T_n + t.
+struct KvPages {
+    const int32_t *table, *kv_lens, *cu;
+    int B;
+    long T, Ttot;  // tokens per sequence (cu null), tokens in all
+    int Hkv, d, num_pages, page_size, max_pages;
+    int dtype, cache_dtype;
+    int *status;
+};
+
+struct KvArgs {  // write: k, v -> caches; read: caches -> k, v
+    KvPages pg;
+    void *k, *v;
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    long k_stride, v_stride;  // elements between a token's rows and the next token's
+};
+
+struct AttnArgs {
+    KvPages pg;
+    const void *q;
+    const void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    void *out;
+    int Hq;
+    long q_stride;
+    float scale;
+    void *ws;
+};
+
+cudaError_t launch_kv_write(const KvArgs &a, cudaStream_t s);
+cudaError_t launch_kv_read(const KvArgs &a, cudaStream_t s);
+// scratch of the attention kernels: what the parts of a unit of work split between CTAs leave
+// for the joining kernel. `rows` bounds the query rows of a unit.
+constexpr int kAttnCtas = 152;  // one per SM
+constexpr int kAttnMaxRows = 128;
+size_t attn_workspace(long tokens_per_seq, int G, int d);
+cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t s);
+
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t s);
 cudaError_t launch_prepass(const PrepassArgs &a, cudaStream_t s);
 cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t s);

@@ -1,0 +1,127 @@
+// kv_pages.cuh -- device helpers of the paged key/value cache: where a token's row lies, and the
+// 8-bit codes of a cached row.
+//
+// Codes. A row x of d elements is stored as codes c and one fp32 scale s, x ~ c s:
+//   e4m3: s = 2^k, the smallest with amax / s <= 448. Division and product by a power of two are
+//         exact, so the only rounding is the code's own (relative 2^-4 at most); a scale between
+//         two powers of two would not make it smaller, since the format's precision is relative.
+//   int8: s = amax / 127, c = rint(x / s): the error is at most s / 2, relative to the row's
+//         largest element, so here the scale is not rounded to a power of two.
+// s is at least 2^-100, so that 1 / s and c s stay far from fp32's range; rows below that are
+// stored as zeros or subnormal multiples of it. A row that holds an infinity or a NaN gets scale
+// NaN and codes 0: it reads back as NaN throughout, never as something finite.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "gdn_common.cuh"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+constexpr float kMinKvScale = 7.8886090522101181e-31f;  // 2^-100
+
+// ---- sequences -------------------------------------------------------------------
+struct SeqInfo {
+    long bos;  // first packed token
+    int T;     // new tokens
+    int len;   // cached tokens, the new ones among them
+};
+
+// Sequence n of the call. False (flagged) when cu is inconsistent; a kv_len outside of the block
+// table's row is flagged and counts as 0, which makes the sequence's tokens padding.
+__device__ __forceinline__ bool seq_info(const KvPages &p, int n, SeqInfo *s) {
+    long eos;
+    if (!seq_bounds(p.cu, n, p.B, p.cu ? p.Ttot : p.T, &s->bos, &eos, p.status)) {
+        s->T = s->len = 0;
+        return false;
+    }
+    s->T = (int)(eos - s->bos);
+    int len = p.kv_lens[n];
+    if (len < 0 || len > (long)p.max_pages * p.page_size) {
+        flag_error(p.status);
+        len = 0;
+    }
+    s->len = len;
+    return true;
+}
+
+// The sequence of packed token i, found by a whole warp: the last n with cu[n] <= i (32 probes a
+// step, so 2 dependent reads for up to 1024 sequences).
+__device__ __forceinline__ int seq_of_token(const KvPages &p, long i) {
+    if (p.cu == nullptr) return (int)(i / p.T);
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = p.B;  // the answer lies in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int at = lo + lane * step;
+        const bool in = lane * step < n && (lane == 0 || p.cu[at] <= i);
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        const int k = 31 - __clz(m);  // for an increasing cu, lanes 0..k
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    return lo;
+}
+
+// Flags offsets that are not increasing from 0 to Ttot. (A token's own sequence is checked where it
+// is used; this finds the sequences that own no token because of their offsets.)
+__device__ __forceinline__ void check_offsets(const KvPages &p) {
+    if (p.cu == nullptr) return;
+    const long all = (long)gridDim.x * blockDim.x;
+    for (long n = (long)blockIdx.x * blockDim.x + threadIdx.x; n < p.B; n += all) {
+        long bos, eos;
+        seq_bounds(p.cu, (int)n, p.B, p.Ttot, &bos, &eos, p.status);
+    }
+}
+
+// Page of a position of sequence n, or -1 (flagged) when the table names no page.
+__device__ __forceinline__ long pool_page(const KvPages &p, int n, int pos) {
+    const int pg = p.table[(long)n * p.max_pages + pos / p.page_size];
+    if (pg < 0 || pg >= p.num_pages) {
+        flag_error(p.status);
+        return -1;
+    }
+    return pg;
+}
+
+// ---- codes -----------------------------------------------------------------------
+__device__ __forceinline__ float scale_e4m3(float amax) {
+    if (!(amax <= 3.4028234e38f)) return __int_as_float(0x7fffffff);
+    const uint32_t u = __float_as_uint(amax);
+    // amax = m 2^(e-127), m in [1, 2); 448 = 1.75 * 2^8 (a subnormal amax ends at the floor below)
+    const int e = (int)(u >> 23), k = e - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)(max(k, -100) + 127) << 23);
+}
+__device__ __forceinline__ float scale_int8(float amax) {
+    if (!(amax <= 3.4028234e38f)) return __int_as_float(0x7fffffff);
+    return fmaxf(__fdiv_rn(amax, 127.f), kMinKvScale);
+}
+
+// 4 codes of x[0..3] (x / s rounded to nearest even), the first in the lowest byte
+__device__ __forceinline__ uint32_t codes4_e4m3(const float *x, float inv) {  // inv = 1 / s, exact
+    const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
+    return (uint32_t)a | ((uint32_t)b << 16);
+}
+__device__ __forceinline__ uint32_t codes4_int8(const float *x, float s) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r |= ((uint32_t)__float2int_rn(__fdiv_rn(x[j], s)) & 0xffu) << (8 * j);
+    return r;
+}
+__device__ __forceinline__ void decode4_e4m3(uint32_t c, float *x) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> (16 * j)), __NV_E4M3);
+        const float2 f = __half22float2(__half2(h));
+        x[2 * j] = f.x;
+        x[2 * j + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void decode4_int8(uint32_t c, float *x) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = (float)(int8_t)(c >> (8 * j));
+}
+
+}  // namespace gdn

@@ -61,7 +61,12 @@ typedef enum {
     GDN_ERR_DEVICE_CHECK = -4  /* a kernel found inconsistent device data    */
 } gdn_status;
 
-typedef enum { GDN_BF16 = 0, GDN_F32 = 1 } gdn_dtype;
+typedef enum {
+    GDN_BF16 = 0,
+    GDN_F32 = 1,
+    GDN_FP8 = 2, /* e4m3 codes with one scale per cached row: cache_dtype only */
+    GDN_INT8 = 3 /* int8 codes with one scale per cached row: cache_dtype only */
+} gdn_dtype;
 
 /*
  * gdn_prefill -- run the recurrence over whole prompts (chunked prefill).
@@ -294,6 +299,108 @@ GDN_API int gdn_prepass(const void *q, const void *k, const void *g, const void 
  * negative = the gdn_status gdn_prefill would return. Host-only, no device work.
  */
 GDN_API int gdn_prefill_path(int B, int T, int Hk, int Hv, int dk, int dv, int chunk, int dtype);
+
+/*
+ * The paged key/value cache of the attention layers beside the gated delta rule layers.
+ * ------------------------------------------------------------------------------------
+ * A hybrid model interleaves the fixed-size states above with attention layers whose keys and
+ * values grow by one row per token and head. Three calls keep and read them: gdn_kv_write stores
+ * new tokens (quantising them on the way, if the cache is 8-bit), gdn_kv_read brings rows back,
+ * gdn_paged_attn is the attention of new tokens (one each, a few, or a prompt's fragment) over
+ * everything cached. The caches are pools of pages that any sequence may own:
+ *
+ *     k_cache, v_cache  [num_pages][Hkv][page_size][d]   of type cache_dtype
+ *     k_scale, v_scale  [num_pages][Hkv][page_size] fp32 with 8-bit caches; else unused (NULL)
+ *     block_table       [B][max_pages] int32: page of positions page_size*j .. of sequence n
+ *     kv_lens           [B] int32: tokens of sequence n in the cache, THIS CALL'S NEW ONES INCLUDED
+ *
+ * Packed tokens follow cu_seqlens (int32 [B+1], with T the packed total) or, when it is NULL, are
+ * B sequences of T tokens each, as for gdn_prefill. New token t of sequence n, of its T_n, has
+ * position kv_lens[n] - T_n + t. A negative position marks padding (kv_lens[n] = 0: an idle row of
+ * a decode batch): it is not written, reads as zeros, and its attention output is zeros. Entries
+ * of block_table past a sequence's last page are never read. block_table and kv_lens need 4-byte
+ * alignment only, so that they can be slices of a larger batch's; all else 16-byte, as above.
+ *
+ *   dtype       : GDN_BF16 or GDN_F32, the type of k, v, q and out.
+ *   cache_dtype : dtype itself, GDN_FP8 or GDN_INT8.
+ *   d           : 64, 128 or 256. page_size: 16, 32, 64, 128 or 256. Hq: a multiple of Hkv, at
+ *                 most 64 times it; query head h reads key head h / (Hq/Hkv).
+ *   *_stride    : elements from a token's rows to the next token's, for tensors that are slices of
+ *                 a fused projection: at least heads*d and a multiple of 16 bytes. A token's heads
+ *                 and a head's elements are contiguous.
+ * Codes: a row x (d elements of one token and head) is stored as codes c and a scale s, x ~ c*s:
+ *   GDN_FP8 : s = 2^k, the smallest with max|x| / s <= 448; c = x/s rounded to nearest even (e4m3);
+ *   GDN_INT8: s = max|x| / 127; c = x/s rounded to nearest even.
+ * s is at least 2^-100. A row holding an infinity or a NaN gets s = NaN and codes 0, and reads back
+ * as NaN. Limits: B <= 65535, T_total*Hq, num_pages*Hkv and max_pages*page_size below 2^31; the
+ * pools themselves may be larger than 2^31 elements.
+ * Device-side checks (status word): inconsistent cu_seqlens (those sequences are skipped), a
+ * kv_len below 0 or above max_pages*page_size (the sequence's tokens count as padding), a page
+ * outside of the pool (not written; reads as zeros, in the attention as keys and values of zero).
+ * The calls allocate nothing and may be captured into a graph; kv_lens and block_table may change
+ * between replays.
+ */
+
+/*
+ * gdn_kv_write -- store the new tokens' keys and values at their positions.
+ *
+ *   k, v : [Ttot][Hkv][d], token strides k_stride and v_stride.
+ * One position must not be written twice by one call (two sequences that share a page).
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API int gdn_kv_write(const void *k, const void *v, void *k_cache, void *v_cache, float *k_scale,
+                         float *v_scale, const int32_t *block_table, const int32_t *kv_lens,
+                         const int32_t *cu_seqlens, int B, int T, int Hkv, int d, int num_pages,
+                         int page_size, int max_pages, int64_t k_stride, int64_t v_stride, int dtype,
+                         int cache_dtype, void *stream);
+
+/*
+ * gdn_kv_read -- the last T_n cached rows of every sequence, as values.
+ *
+ *   k, v : [Ttot][Hkv][d] outputs, token strides k_stride and v_stride: code times scale in fp32,
+ *          rounded once to dtype (a cache of type dtype is copied). With T_n = kv_lens[n] this is
+ *          the whole sequence.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API int gdn_kv_read(const void *k_cache, const void *v_cache, const float *k_scale,
+                        const float *v_scale, const int32_t *block_table, const int32_t *kv_lens,
+                        const int32_t *cu_seqlens, void *k, void *v, int B, int T, int Hkv, int d,
+                        int num_pages, int page_size, int max_pages, int64_t k_stride,
+                        int64_t v_stride, int dtype, int cache_dtype, void *stream);
+
+/*
+ * gdn_paged_attn -- attention of the new tokens over their sequences' caches.
+ *
+ * With j over positions 0 .. p of the sequence, p the token's own (causal; the new tokens' rows
+ * have to be in the cache, see gdn_kv_write):
+ *     out = sum_j w_j v_j,   w = softmax_j(scale * q . k_j)
+ * T = 1 is the decode step, T of a few the check of speculated tokens, a large T a fragment of a
+ * prompt over what is cached of it: a prompt cut into fragments gives the same result.
+ *   q   : [Ttot][Hq][d], token stride q_stride.   out : [Ttot][Hq][d], contiguous.
+ *   scale : the softmax scale, for instance d^-1/2.
+ *   workspace : DEVICE memory, 256-byte aligned, of at least
+ *         gdn_paged_attn_workspace_size(B, T, cu_seqlens != NULL, Hq, Hkv, d) bytes: scratch until
+ *         the call's work on `stream` has finished, whatever was in it before. Calls whose work may
+ *         overlap on the GPU must use different workspaces.
+ * Scores and softmax statistics are fp32. A row whose scores are all -infinity gives zeros. What
+ * lies in the cache at or past kv_lens[n] has no effect, whatever its value. The result does not
+ * depend on the order in which the GPU runs its parts.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API int gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache,
+                           const float *k_scale, const float *v_scale, const int32_t *block_table,
+                           const int32_t *kv_lens, const int32_t *cu_seqlens, void *out, int B, int T,
+                           int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages,
+                           int64_t q_stride, float scale, int dtype, int cache_dtype, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_paged_attn_workspace_size -- bytes of workspace gdn_paged_attn needs (0: none, or the sizes
+ * are invalid). `packed` says whether cu_seqlens is given (T is then the packed total). It does not
+ * depend on the lengths of the caches, and not on B: at most 128 rows of d fp32 per part of work,
+ * two parts per SM (40 MB for d = 256). Host-only.
+ */
+GDN_API size_t gdn_paged_attn_workspace_size(int B, int T, int packed, int Hq, int Hkv, int d);
 
 /*
  * gdn_get_device_status -- synchronise `stream`, then return and clear the
