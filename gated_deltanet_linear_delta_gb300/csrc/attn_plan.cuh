@@ -221,16 +221,16 @@ __device__ __forceinline__ void next_unit(const AttnWork &w, Piece *pc) {
     } while (pc->ntiles == 0);
 }
 
-// Rows of padding tokens are zeros; no unit of work covers them.
+// Rows of padding tokens are zeros; no unit of work covers them. (`threads` threads of each CTA call it.)
 template <typename TOut>
-__device__ void zero_padding(const AttnWork &w, TOut *out, int Hq, int d) {
+__device__ void zero_padding(const AttnWork &w, TOut *out, int Hq, int d, int thread, int threads) {
     for (int n = blockIdx.x; n < w.pg.B; n += gridDim.x) {
         SeqInfo s;
         if (!seq_info(w.pg, n, &s)) continue;
         const long idle = (long)min(s.T, max(0, s.T - s.len)) * Hq * d;
         uint4 *p = reinterpret_cast<uint4 *>(out + s.bos * Hq * d);
         const long pieces = idle * (long)sizeof(TOut) / 16;
-        for (long e = threadIdx.x; e < pieces; e += blockDim.x) p[e] = make_uint4(0, 0, 0, 0);
+        for (long e = thread; e < pieces; e += threads) p[e] = make_uint4(0, 0, 0, 0);
     }
 }
 

@@ -1,6 +1,7 @@
 // attn_simt.cu -- attention over a paged cache on the CUDA cores, in fp32 throughout.
 //
-// A CTA of 256 threads holds a row tile of Q and walks key tiles of 64 positions: scores by register
+// For fp32 inputs, whose results keep fp32's precision (bf16 inputs run on the tensor cores,
+// attn_tc.cu). A CTA of 256 threads holds a row tile of Q and walks key tiles of 64 positions: scores by register
 // tiles (each thread RT rows x 4 keys), softmax statistics per row by shuffles over the 16
 // threads that share it, and the output tile (RT rows x D/16 columns a thread) in registers,
 // rescaled when the running maximum grows. It is bound by shared-memory reads (5 to 8 16-byte reads
@@ -17,31 +18,23 @@ constexpr int kThreads = 256;
 constexpr int BN = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <typename T>
 struct SimtParams {
     AttnWork w;
-    const T *q;
+    const float *q;
     const void *k_cache, *v_cache;
     const float *k_scale, *v_scale;
-    T *out;
+    float *out;
     int Hq;
     long q_stride;
     float scale2;  // softmax scale * log2 e
 };
 
-__device__ __forceinline__ void store4(float *p, float4 x) { *reinterpret_cast<float4 *>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 x) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-}
-
 // 4 elements of cached row `at` (page, head, offset flattened), dequantised; KIND is GDN_FP8,
-// GDN_INT8, or anything else for a cache of type T
-template <typename T, int KIND, int D>
+// GDN_INT8 or GDN_F32
+template <int KIND, int D>
 __device__ __forceinline__ float4 cached4(const void *cache, const float *scale, long at, int c) {
-    if constexpr (KIND != GDN_FP8 && KIND != GDN_INT8) {
-        return load4((const T *)cache + at * D + c);
+    if constexpr (KIND == GDN_F32) {
+        return load4((const float *)cache + at * D + c);
     } else {
         const uint32_t code = *reinterpret_cast<const uint32_t *>((const uint8_t *)cache + at * D + c);
         float x[4];
@@ -62,8 +55,8 @@ struct SimtSmem {
     PlanSmem plan;
 };
 
-template <typename T, int KIND, int D, int R>
-__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams<T> a) {
+template <int KIND, int D, int R>
+__global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a) {
     constexpr int RT = R / 16, CT = D / 64;  // rows and groups of 4 columns per thread
     extern __shared__ __align__(16) uint8_t smem_raw[];
     SimtSmem<D, R> &sm = *reinterpret_cast<SimtSmem<D, R> *>(smem_raw);
@@ -71,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams<T>
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     plan_piece<BN, kThreads>(w, &sm.plan);
-    zero_padding(w, a.out, a.Hq, D);
+    zero_padding(w, a.out, a.Hq, D, tid, kThreads);
     Piece pc = sm.plan.piece;
     for (bool begun = pc.off == 0; pc.left > 0; begun = true) {
         const int t0 = pc.i * w.TPT, rows = min(w.TPT, pc.s.T - t0) * w.G;
@@ -113,8 +106,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams<T>
                 const long at = sm.at[r];
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;  // a position past the end adds 0 * 0
                 if (at >= 0) {
-                    x = cached4<T, KIND, D>(a.k_cache, a.k_scale, at, c);
-                    y = cached4<T, KIND, D>(a.v_cache, a.v_scale, at, c);
+                    x = cached4<KIND, D>(a.k_cache, a.k_scale, at, c);
+                    y = cached4<KIND, D>(a.v_cache, a.v_scale, at, c);
                 }
                 *reinterpret_cast<float4 *>(&sm.k[r][c]) = x;
                 *reinterpret_cast<float4 *>(&sm.v[r][c]) = y;
@@ -192,11 +185,11 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams<T>
             if (whole) {
                 if (limit[r] < 0) continue;  // padding: already zeros
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;  // scores that are all -inf: zeros
-                T *dst = a.out + ((pc.s.bos + t0 + row / w.G) * a.Hq + pc.h * w.G + row % w.G) * D;
+                float *dst = a.out + ((pc.s.bos + t0 + row / w.G) * a.Hq + pc.h * w.G + row % w.G) * D;
 #pragma unroll
                 for (int c = 0; c < CT; ++c)
-                    store4(dst + 64 * c + 4 * tx,
-                           make_float4(o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv));
+                    *reinterpret_cast<float4 *>(dst + 64 * c + 4 * tx) =
+                        make_float4(o[r][c].x * inv, o[r][c].y * inv, o[r][c].z * inv, o[r][c].w * inv);
             } else {
                 const long at = part_index(w, blockIdx.x, begun ? 1 : 0, row);
                 if (tx == 0) w.ml[at] = make_float2(m[r], sum);
@@ -209,12 +202,12 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams<T>
     }
 }
 
-template <typename T, int KIND, int D, int R>
+template <int KIND, int D, int R>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     const int G = a.Hq / a.pg.Hkv;
-    SimtParams<T> p{attn_work(a, R / G, 2), (const T *)a.q, a.k_cache, a.v_cache, a.k_scale, a.v_scale,
-                    (T *)a.out, a.Hq, a.q_stride, a.scale * kLog2e};
-    auto kernel = attn_simt_kernel<T, KIND, D, R>;
+    SimtParams p{attn_work(a, R / G, 2), (const float *)a.q, a.k_cache, a.v_cache, a.k_scale, a.v_scale,
+                 (float *)a.out, a.Hq, a.q_stride, a.scale * kLog2e};
+    auto kernel = attn_simt_kernel<KIND, D, R>;
     constexpr int bytes = sizeof(SimtSmem<D, R>);
     static_assert(bytes <= 232448, "over the 227 KiB opt-in limit");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -224,36 +217,31 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     return e != cudaSuccess ? e : launch_attn_join(a, p.w, s);
 }
 
-template <typename T, int KIND, int D>
+template <int KIND, int D>
 cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
     // a row tile of 16 where no sequence has more rows: a quarter of the products of the 64-row tile
     const long rows = (a.pg.cu ? a.pg.Ttot : a.pg.T) * (a.Hq / a.pg.Hkv);
-    return rows <= 16 ? launch_t<T, KIND, D, 16>(a, s) : launch_t<T, KIND, D, 64>(a, s);
+    return rows <= 16 ? launch_t<KIND, D, 16>(a, s) : launch_t<KIND, D, 64>(a, s);
 }
 
-template <typename T, int KIND>
+template <int KIND>
 cudaError_t launch_d(const AttnArgs &a, cudaStream_t s) {
     switch (a.pg.d) {
-        case 64: return launch_rows<T, KIND, 64>(a, s);
-        case 128: return launch_rows<T, KIND, 128>(a, s);
-        case 256: return launch_rows<T, KIND, 256>(a, s);
+        case 64: return launch_rows<KIND, 64>(a, s);
+        case 128: return launch_rows<KIND, 128>(a, s);
+        case 256: return launch_rows<KIND, 256>(a, s);
     }
     return cudaErrorInvalidValue;
-}
-
-template <typename T>
-cudaError_t launch_kind(const AttnArgs &a, cudaStream_t s) {
-    switch (a.pg.cache_dtype) {
-        case GDN_FP8: return launch_d<T, GDN_FP8>(a, s);
-        case GDN_INT8: return launch_d<T, GDN_INT8>(a, s);
-        default: return launch_d<T, GDN_BF16>(a, s);
-    }
 }
 
 }  // namespace
 
 cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t s) {
-    return a.pg.dtype == GDN_F32 ? launch_kind<float>(a, s) : launch_kind<__nv_bfloat16>(a, s);
+    switch (a.pg.cache_dtype) {
+        case GDN_FP8: return launch_d<GDN_FP8>(a, s);
+        case GDN_INT8: return launch_d<GDN_INT8>(a, s);
+        default: return launch_d<GDN_F32>(a, s);
+    }
 }
 
 }  // namespace gdn

@@ -120,7 +120,7 @@ int kv_checks(int B, int T, const int32_t *cu, int Hq, int Hkv, int d, int num_p
     if (Hq / Hkv > 64) return GDN_ERR_UNSUPPORTED;
     const long long Ttot = cu ? (long long)T : (long long)B * T;
     if (Ttot * Hq > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
-    if ((long long)num_pages * Hkv > 0x7fffffffLL || (long long)max_pages * page_size > 0x7fffffffLL)
+    if ((long long)num_pages * Hkv > 0x7fffffffLL || (long long)max_pages * page_size > (1LL << 30))
         return GDN_ERR_INVALID_ARG;
     const int64_t vec = dtype == GDN_BF16 ? 8 : 4;  // 16 bytes
     if (stride_a < (int64_t)Hq * d || stride_a % vec || stride_b < (int64_t)Hkv * d || stride_b % vec)
@@ -438,7 +438,9 @@ int gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     a.q_stride = (long)q_stride;
     a.scale = scale;
     a.ws = workspace;
-    return gdn::launch_attn_simt(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    const cudaError_t e = dtype == GDN_BF16 ? gdn::launch_attn_tc(a, static_cast<cudaStream_t>(stream))
+                                            : gdn::launch_attn_simt(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 int gdn_get_device_status(void *stream) {

@@ -76,7 +76,8 @@ cudaError_t launch_kv_read(const KvArgs &a, cudaStream_t s);
 constexpr int kAttnCtas = 152;  // one per SM
 constexpr int kAttnMaxRows = 128;
 size_t attn_workspace(long tokens_per_seq, int G, int d);
-cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t s);  // fp32
+cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t s);    // bf16
 
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t s);
 cudaError_t launch_prepass(const PrepassArgs &a, cudaStream_t s);

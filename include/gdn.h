@@ -332,8 +332,8 @@ GDN_API int gdn_prefill_path(int B, int T, int Hk, int Hv, int dk, int dv, int c
  *   GDN_FP8 : s = 2^k, the smallest with max|x| / s <= 448; c = x/s rounded to nearest even (e4m3);
  *   GDN_INT8: s = max|x| / 127; c = x/s rounded to nearest even.
  * s is at least 2^-100. A row holding an infinity or a NaN gets s = NaN and codes 0, and reads back
- * as NaN. Limits: B <= 65535, T_total*Hq, num_pages*Hkv and max_pages*page_size below 2^31; the
- * pools themselves may be larger than 2^31 elements.
+ * as NaN. Limits: B <= 65535, T_total*Hq and num_pages*Hkv below 2^31, max_pages*page_size at most
+ * 2^30; the pools themselves may be larger than 2^31 elements.
  * Device-side checks (status word): inconsistent cu_seqlens (those sequences are skipped), a
  * kv_len below 0 or above max_pages*page_size (the sequence's tokens count as padding), a page
  * outside of the pool (not written; reads as zeros, in the attention as keys and values of zero).
