@@ -26,37 +26,46 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
     const int c = blockIdx.x + 1, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const AttnRec r = w.rec[c];
     if (c >= r.active || r.off == 0) return;
-    if (r.off > w.rec[c - 1].tiles) return;  // an earlier boundary lies in this unit too
-    SeqInfo s;
-    if (!seq_info(w.pg, r.n, &s)) return;
-    // last part: pieces c.. while the unit goes on
-    int last = c, have = r.off + r.tiles;
-    while (have < r.ntiles && last + 1 < r.active) have += w.rec[++last].tiles;
-    const int parts = last - c + 2;
-    const int t0 = r.i * w.TPT, rows = min(w.TPT, s.T - t0) * w.G;
+    if (r.begin - r.off < piece_begin(r.total, c - 1, r.active)) return;  // an earlier boundary lies in this unit too
+    // the piece that holds the unit's last key tile
+    const long end = r.begin - r.off + r.ntiles - 1;
+    int last = (int)(end * r.active / r.total);
+    while (last + 1 < r.active && piece_begin(r.total, last + 1, r.active) <= end) ++last;
+    while (piece_begin(r.total, last, r.active) > end) --last;
+    const int parts = last - c + 2, rows = r.tokens * w.G;
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-        const int t = t0 + row / w.G;
-        const bool live = s.len - s.T + t >= 0;  // the rows of padding tokens are written elsewhere
+        const int t = row / w.G;
+        const bool live = r.pos + t >= 0;  // the rows of padding tokens are written elsewhere
         float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.f;
-        for (int k = wid; live && k < parts; k += NW) {
-            const long at = part_index(w, c - 1 + k, k == 0 ? 1 : 0, row);
-            const float2 pm = w.ml[at];
-            float x[E];
+        for (int k0 = wid; live && k0 < parts; k0 += 4 * NW) {
+            float2 pm[4];
+            float x[4][E];
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 f = *reinterpret_cast<const float2 *>(w.part + at * D + e * 32 + 2 * lane);
-                x[e] = f.x;
-                x[e + 1] = f.y;
+            for (int u = 0; u < 4; ++u) {  // four parts' loads in flight
+                const int k = k0 + u * NW;
+                pm[u] = make_float2(-INFINITY, 0.f);
+                if (k >= parts) continue;
+                const long at = part_index(w, c - 1 + k, k == 0 ? 1 : 0, row);
+                pm[u] = w.ml[at];
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 f = *reinterpret_cast<const float2 *>(w.part + at * D + e * 32 + 2 * lane);
+                    x[u][e] = f.x;
+                    x[u][e + 1] = f.y;
+                }
             }
-            if (pm.x == -INFINITY) continue;  // no key of this part is seen by the row
-            const float mn = fmaxf(m, pm.x);
-            const float a = exp2f(m - mn), b = exp2f(pm.x - mn);
-            m = mn;
-            l = l * a + pm.y * b;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = o[e] * a + x[e] * b;
+            for (int u = 0; u < 4; ++u) {
+                if (pm[u].x == -INFINITY && pm[u].y == 0.f) continue;  // no key of this part is seen by the row
+                const float mn = fmaxf(m, pm[u].x);
+                const float a = exp2f(m - mn), b = exp2f(pm[u].x - mn);
+                m = mn;
+                l = l * a + pm[u].y * b;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = o[e] * a + x[u][e] * b;
+            }
         }
 #pragma unroll
         for (int e = 0; e < E; e += 2)
@@ -79,7 +88,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
                 float x = 0.f;
 #pragma unroll
                 for (int k = 0; k < NW; ++k) x += f[k] * acc[k][e];
-                out[((s.bos + t) * Hq + h) * D + e] = from_f32<TOut>(L == 0.f ? 0.f : x / L);
+                out[((r.token + t) * Hq + h) * D + e] = from_f32<TOut>(L == 0.f ? 0.f : x / L);
             }
         __syncthreads();
     }

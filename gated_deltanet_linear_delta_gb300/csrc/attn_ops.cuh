@@ -1,0 +1,108 @@
+// attn_ops.cuh -- what the two attention kernels of bf16 inputs share: constants, the exponential,
+// 8-bit codes as fp16, the scaling of Q, and the tensor maps of the caches.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <cstdlib>
+
+#include "attn_plan.cuh"
+#include "attn_work.h"
+#include "tc_ops.cuh"
+
+namespace gdn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.f;  // the softmax reference moves when the maximum has grown by 2^8
+constexpr long long kWaitDefault = 2000000000LL;  // SM cycles (about 1 s) before a wait gives up
+constexpr long long kDrainBudget = 200000000LL;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 4 codes to fp16 (exact)
+template <int KIND>
+__device__ __forceinline__ void codes4_to_f16(uint32_t c, uint32_t &h0, uint32_t &h1) {
+    if constexpr (KIND == GDN_FP8) {
+        asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\ncvt.rn.f16x2.e4m3x2 %0, lo;\ncvt.rn.f16x2.e4m3x2 %1, hi;\n}"
+            : "=r"(h0), "=r"(h1)
+            : "r"(c));
+    } else {
+        // c + 128 as the low byte of an fp16 in [1024, 2048), whose unit is 1; minus 1152 gives c, exactly
+        const uint32_t u = c ^ 0x80808080u;
+        const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
+        const uint32_t w0 = __byte_perm(u, 0x64646464u, 0x4140), w1 = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&w0), bias);
+        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&w1), bias);
+        h0 = *reinterpret_cast<const uint32_t *>(&x);
+        h1 = *reinterpret_cast<const uint32_t *>(&y);
+    }
+}
+
+// Exponent e such that a row of largest magnitude amax, times 2^e, has it in [2^13, 2^14): in fp16
+// the largest elements are far from overflow and all that count are normal.
+__device__ __forceinline__ int f16_row_exponent(float amax) {
+    if (!(amax > 0.f && amax < 3.4e38f)) return 0;
+    return max(-100, min(100, 13 - ((int)(__float_as_uint(amax) >> 23) - 127)));
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+inline long long wait_budget() {
+    if (const char *env = getenv("GDN_TEST_WAIT_CYCLES")) {  // test hook: a short limit makes the waits run out
+        const long long x = atoll(env);
+        if (x > 0) return x;
+    }
+    return kWaitDefault;
+}
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn tiled_encoder() {
+    static EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<EncodeTiledFn>(f);
+    }();
+    return fn;
+}
+
+// A cache as [page, head][lines of `line` bytes] -> 3-D map, box (128 bytes, `lines` lines, 1), 128B
+// swizzle. A line is a position's row, or two positions' where a row has only 64 bytes.
+inline bool page_map(CUtensorMap *m, const void *base, const KvPages &pg, int line, int lines) {
+    EncodeTiledFn enc = tiled_encoder();
+    if (!enc) return false;
+    const int elem = pg.cache_dtype == GDN_BF16 ? 2 : 1;
+    const cuuint64_t page = (cuuint64_t)pg.page_size * pg.d * elem;
+    const cuuint64_t gdim[3] = {(cuuint64_t)(line / elem), page / line, (cuuint64_t)pg.num_pages * pg.Hkv};
+    const cuuint64_t gstride[2] = {(cuuint64_t)line, page};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / elem), (cuuint32_t)lines, 1};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    return enc(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3,
+               const_cast<void *>(base), gdim, gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A running softmax reference m of a row (log2 domain), given its maximum over more keys: moved when
+// that has grown by more than 2^kGrow. Returns the factor for what was summed before.
+__device__ __forceinline__ bool grow_reference(float &m, float top, float &f) {
+    const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
+    f = 1.f;
+    if (grow) {
+        f = ex2(m - top);  // m = -inf: 0
+        m = top;
+    }
+    return grow;
+}
+
+}  // namespace gdn

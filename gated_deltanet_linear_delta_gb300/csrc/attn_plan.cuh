@@ -16,14 +16,20 @@
 
 namespace gdn {
 
-struct AttnRec {  // where CTA c's piece starts; read by the joining kernel
-    int n, h, i;   // unit
+struct __align__(16) AttnRec {  // where CTA c's piece starts; read by the joining kernel
     int off;       // key tiles of the unit before the piece (0: the unit starts here)
     int ntiles;    // key tiles of the unit
-    int tiles;     // key tiles in the piece
     int active;    // pieces in all
-    int pad;
+    int h;         // key head of the unit
+    long begin;    // key tiles of all units before the piece
+    long total;    // key tiles of all units
+    long token;    // packed token of the unit's first row
+    int tokens;    // its new tokens
+    int pos;       // position of the first (negative: padding)
 };
+
+// First key tile of piece c of `active` equal ones.
+__device__ __forceinline__ long piece_begin(long total, int c, int active) { return total * c / active; }
 
 struct AttnWork {
     KvPages pg;
@@ -120,8 +126,8 @@ __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
     const long want = (total + w.min_tiles - 1) / w.min_tiles;
     const int active = (int)(want < (long)gridDim.x ? want : (long)gridDim.x);
     const int c = blockIdx.x;
-    const long begin = c < active ? total * c / active : total;
-    long end = c < active ? total * (c + 1) / active : total;
+    const long begin = c < active ? piece_begin(total, c, active) : total;
+    long end = c < active ? piece_begin(total, c + 1, active) : total;
     // the sequence that holds `begin`
     long before = 0;
     if (begin < end) {
@@ -194,8 +200,9 @@ __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
         pc.left = end - begin;
         if (lane == 0) {
             sm->piece = pc;
-            AttnRec r{pc.n, pc.h, pc.i, pc.off, pc.ntiles, (int)pc.left, active, 0};
-            w.rec[c] = r;
+            const int t0 = pc.i * w.TPT;
+            w.rec[c] = AttnRec{pc.off, pc.ntiles, active, pc.h, begin, total, pc.s.bos + t0, min(w.TPT, pc.s.T - t0),
+                               pc.s.len - pc.s.T + t0};
         }
     }
     __syncthreads();

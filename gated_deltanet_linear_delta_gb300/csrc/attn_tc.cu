@@ -15,11 +15,11 @@
 // the softmax of one tile hides behind the products of its neighbours.
 //
 // Layout. TMEM holds O (D columns), two S buffers (P_j overlays S_j) and Q as the 16-bit A operand,
-// 512 columns in all for D = 256; with Q in TMEM, shared memory is one ring of K and V tiles, and the
+// 512 columns in all for D = 256; with Q in TMEM, shared memory is two rings of K and V tiles, and the
 // S products read 64 bytes of it a cycle instead of 192. S_{j+1} is issued before O += P_j V_j, so
 // the tensor cores work on it while the softmax of tile j runs.
-// Warps: 0..7 softmax (two threads per row, half of the columns each), 8 loads, 9 issues the
-// products; with an 8-bit cache 10..13 convert tiles. All CTAs are persistent over their piece of
+// Warps: 0..7 softmax (two threads per row, half of the columns each), 8 and 9 load K and V, 10
+// issues the products; with an 8-bit cache 11..14 convert tiles. All CTAs are persistent over their piece of
 // the work, and every wait has a limit, after which the CTA flags the status word and leaves.
 //
 // 8-bit caches. Codes are exact in fp16, so K and V tiles hold codes converted to fp16 (bf16 would
@@ -32,24 +32,16 @@
 // Masks. A row sees positions up to its own; scores past it are replaced (not multiplied), so what
 // K holds there has no effect. Rows of V past the sequence's end are zeroed in shared memory before
 // the product, since 0 * NaN would reach the sum.
-#include <cuda.h>
-#include <cstdlib>
-#include <cuda_fp16.h>
+#include <type_traits>
 
-#include "attn_plan.cuh"
-#include "attn_work.h"
-#include "tc_ops.cuh"
+#include "attn_ops.cuh"
 
 namespace gdn {
 namespace {
 
 using namespace tc;
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGrow = 8.f;  // the reference moves when the maximum has grown by 2^8
-constexpr long long kWaitDefault = 2000000000LL;  // SM cycles (about 1 s) before a wait gives up
-constexpr long long kDrainBudget = 200000000LL;
-constexpr int kSoftWarps = 8, kLoadWarp = 8, kMmaWarp = 9, kConvWarp0 = 10, kConvWarps = 4;
+constexpr int kSoftWarps = 8, kLoadWarp = 8 /* K, then V */, kMmaWarp = 10, kConvWarp0 = 11, kConvWarps = 4;
 
 template <int D, int KIND>
 struct Cfg {
@@ -58,24 +50,27 @@ struct Cfg {
     static constexpr int HC = BN / 2;                      // columns of S per softmax thread
     static constexpr int NB = D / 64;                      // 128-byte wide blocks of a tile
     static constexpr uint32_t SLOT = BN * D * 2;           // a 16-bit K or V tile
-    static constexpr uint32_t RAW = BN * D + 2 * BN * 4;   // a tile's codes, and K and V scales (K fills)
-    static constexpr int NS = kCodes ? (D == 64 ? 4 : 3) : (D == 64 ? 12 : 6);
-    static constexpr int NR = kCodes ? (D == 64 ? 12 : 7) : 0;
-    // Column scales, a buffer per tile: tile j's are written once ring fill (K_j) - NS is used up. With NS = 3
-    // that follows the softmax of tile j - 3, with NS = 4 that of tile j - 4.
-    static constexpr int COLS = NS;
+    static constexpr uint32_t RAW_K = BN * D + 2 * BN * 4;  // a K tile's codes, and K and V scales
+    static constexpr uint32_t RAW_V = BN * D;
+    // ring slots: 16-bit tiles of K and of V, and with an 8-bit cache their codes
+    static constexpr int NK = kCodes ? 2 : (D == 64 ? 6 : 3), NV = NK;
+    static constexpr int NR = kCodes ? (D == 64 ? 6 : 2) : 0;
+    static constexpr int COLS = 4;                         // column scales, a buffer per tile
     static constexpr int THREADS = 32 * (kCodes ? kConvWarp0 + kConvWarps : kConvWarp0);
     static constexpr uint32_t TM_O = 0, TM_S = D == 256 ? 256 : 128, TM_Q = 384;
     // shared memory, from a 1 KiB aligned base
-    static constexpr uint32_t SM_RAW = NS * SLOT;
-    static constexpr uint32_t SM_COL = SM_RAW + NR * RAW;                    // [COLS][3][BN] a, b, 1 / vs
+    static constexpr uint32_t SM_V = NK * SLOT, SM_RK = SM_V + NV * SLOT, SM_RV = SM_RK + NR * RAW_K;
+    static constexpr uint32_t SM_COL = SM_RV + NR * RAW_V;                   // [COLS][3][BN] a, b, 1 / vs
     static constexpr uint32_t SM_X = SM_COL + (kCodes ? COLS * 3 * BN * 4 : 0);  // [2][2][128] row exchange
     static constexpr uint32_t SM_BAR = SM_X + 2 * 2 * 128 * 4;
-    static constexpr int B_FULL = 0, B_EMPTY = NS, B_RFULL = 2 * NS, B_REMPTY = B_RFULL + NR, B_COL = B_REMPTY + NR,
-                         B_S = B_COL + COLS, B_P = B_S + 2, B_PV = B_P + 2, B_Q = B_PV + 2, B_FIN = B_Q + 1,
-                         B_COUNT = B_FIN + 1;
-    static constexpr uint32_t SM_INFO = SM_BAR + B_COUNT * 8;                // [NR] valid rows, page mask
-    static constexpr uint32_t SM_TMEM = SM_INFO + (NR ? NR : 1) * 8;
+    // S_j and O += P_j V_j done, by tile modulo 8: they also say that K_j's and V_j's slots are free. (Whoever fills
+    // a slot looks back at most 6 tiles, so a barrier is never two phases ahead of its reader.)
+    static constexpr int kTurns = 8;
+    static constexpr int B_FK = 0, B_FV = B_FK + NK, B_RK = B_FV + NV, B_RV = B_RK + NR, B_REK = B_RV + NR,
+                         B_REV = B_REK + NR, B_COL = B_REV + NR, B_S = B_COL + COLS, B_PV = B_S + kTurns,
+                         B_P = B_PV + kTurns, B_Q = B_P + 2, B_FIN = B_Q + 1, B_COUNT = B_FIN + 1;
+    static constexpr uint32_t SM_INFO = SM_BAR + B_COUNT * 8;                // [2][NR] valid rows, page mask
+    static constexpr uint32_t SM_TMEM = SM_INFO + (NR ? 2 * NR : 1) * 8;
     static constexpr uint32_t SM_PLAN = (SM_TMEM + 8 + 15) & ~15u;
     static constexpr uint32_t SM_BYTES = SM_PLAN + sizeof(PlanSmem) + 1024;
     static_assert(SM_BYTES <= 232448, "over the 227 KiB opt-in limit");
@@ -94,11 +89,6 @@ struct TcParams {
     long long budget;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ uint32_t bf2(float a, float b) { return bf2_bits(__floats2bfloat162_rn(a, b)); }
 
 // A wait whose outcome the whole warp shares
@@ -124,90 +114,120 @@ __device__ __forceinline__ bool walk_next(const AttnWork &w, Walk *k) {
     return k->pc.left > 0;
 }
 
-// ---- loads ------------------------------------------------------------------------
-// Fill order is the order of use: K_0, then K_{j+1}, V_j.
+// A ring's slot and phase, counted on instead of divided out of the tile's number.
+template <int N>
+struct Ring {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+// barrier and phase of tile t's S (or PV) product
 template <int D, int KIND>
-__device__ void load_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, const CUtensorMap *mk,
-                          const CUtensorMap *mv) {
+__device__ __forceinline__ bool product_done(uint64_t *bar, int which, uint32_t t, long long budget) {
+    using C = Cfg<D, KIND>;
+    return mbar_wait_spin(bar + which + (t & (C::kTurns - 1)), (t / C::kTurns) & 1, budget);
+}
+
+// ---- loads ------------------------------------------------------------------------
+// One warp loads K tiles, another V tiles.
+template <int D, int KIND, bool IS_V>
+__device__ void load_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, const CUtensorMap *map) {
     using C = Cfg<D, KIND>;
     constexpr int BN = C::BN;
     const KvPages &pg = p.w.pg;
-    const int lane = threadIdx.x & 31, P = pg.page_size;
+    const int lane = threadIdx.x & 31, P = pg.page_size, P_shift = 31 - __clz(P);
     const int box = min(P, BN), per_tile = BN / box;       // rows of a page's piece, pieces of a tile
     constexpr int NP = C::kCodes ? 1 : C::NB;              // copies per piece
     const int piece = lane / NP, blk = lane % NP;
-    constexpr int NSLOT = C::kCodes ? C::NR : C::NS;
-    constexpr int FULL = C::kCodes ? C::B_RFULL : C::B_FULL, EMPTY = C::kCodes ? C::B_REMPTY : C::B_EMPTY;
-    uint32_t fill = 0;
+    const bool issues = piece < per_tile;
+    constexpr int N = C::kCodes ? C::NR : (IS_V ? C::NV : C::NK);
+    constexpr int FULL = C::kCodes ? (IS_V ? C::B_RV : C::B_RK) : (IS_V ? C::B_FV : C::B_FK);
+    const uint32_t dst0 = C::kCodes ? (uint32_t)(IS_V ? C::SM_RV : C::SM_RK) + piece * box * D
+                                    : (IS_V ? C::SM_V : 0) + blk * (BN * 128) + piece * (box * 128);
+    constexpr uint32_t STRIDE = C::kCodes ? (IS_V ? C::RAW_V : C::RAW_K) : C::SLOT;
+    Ring<N> ring;
+    uint32_t t = 0;  // tiles loaded
     bool ok = true;
     if (k.pc.left > 0) do {
         const int n = k.take(), len = k.pc.s.len;
-        // page of this lane's piece of tile j: an index into the pool, -1 for none (past the end), -2 for a bad one
-        auto page_of = [&](int j) -> int {
-            const int pos = j * BN + piece * box;
-            if (piece >= per_tile || pos >= len) return -1;
-            const int x = pg.table[(long)k.pc.n * pg.max_pages + pos / P];
-            if (x >= 0 && x < pg.num_pages) return x;
-            flag_error(pg.status);
-            return -2;
+        // The sequence's table entries, 32 pages at a time: a window in use and the next one on its way, so
+        // that no tile waits for them.
+        const int32_t *table = pg.table + (long)k.pc.n * pg.max_pages;
+        const int used = (len + P - 1) >> P_shift;
+        auto entries = [&](int window) -> int {
+            const int i = window * 32 + lane;
+            return i < used ? table[i] : -1;
         };
-        auto issue = [&](int j, int page, bool is_v) {
-            const int s = fill % NSLOT;
-            ok = warp_wait(bar + EMPTY + s, ((fill / NSLOT) & 1) ^ 1, p.budget);
-            if (!ok) return;
-            const int pos = j * BN + piece * box, row0 = pos & (P - 1);
+        int window = ((k.pc.off * BN) >> P_shift) >> 5, win = entries(window), win_next = entries(window + 1);
+        int pos = k.pc.off * BN + piece * box;
+        for (int jj = 0; jj < n; ++jj, ++t, pos += BN) {
+            const int first = (pos - piece * box) >> P_shift;
+            if ((first >> 5) != window) {  // (a tile's pages share a window)
+                ++window;
+                win = win_next;
+                win_next = entries(window + 1);
+            }
+            const int page = __shfl_sync(0xffffffffu, win, (first + piece) & 31);
+            const bool here = issues && pos < len;
+            const bool good = (unsigned)page < (unsigned)pg.num_pages;
+            if (here && !good) flag_error(pg.status);
+            const int row0 = pos & (P - 1);
+            if constexpr (C::kCodes) {
+                ok = warp_wait(bar + (IS_V ? C::B_REV : C::B_REK) + ring.slot, ring.phase ^ 1, p.budget);
+            } else if (t >= N) {
+                ok = __all_sync(0xffffffffu, product_done<D, KIND>(bar, IS_V ? C::B_PV : C::B_S, t - N, p.budget));
+            }
+            if (!ok) break;
             if constexpr (!C::kCodes) {
-                const int pieces = __popc(__ballot_sync(0xffffffffu, page != -1 && blk == 0));
-                if (lane == 0) mbar_expect_tx(bar + FULL + s, (uint32_t)pieces * box * D * 2);
+                // pieces past the end are left out; a bad page is read outside of the map: zeros
+                const int left = len - (pos - piece * box);
+                const int pieces = left >= BN ? per_tile : (left + box - 1) / box;
+                if (lane == 0) mbar_expect_tx(bar + FULL + ring.slot, (uint32_t)pieces * box * D * 2);
                 __syncwarp();
-                // a bad page is read at a coordinate outside of the map: zeros
-                if (page != -1)
-                    tma_load_3d(sm + s * C::SLOT + blk * (BN * 128) + piece * (box * 128), is_v ? mv : mk, blk * 64, row0,
-                                page == -2 ? -1 : page * pg.Hkv + k.pc.h, bar + FULL + s);
+                if (here)
+                    tma_load_3d(sm + dst0 + ring.slot * STRIDE, map, blk * 64, row0, good ? page * pg.Hkv + k.pc.h : -1,
+                                bar + FULL + ring.slot);
             } else {
-                const bool live = page >= 0;
+                const bool live = here && good;
                 const uint32_t rows = live ? (uint32_t)min(box, len - pos) : 0u;
                 const uint32_t srows = (rows + 3) & ~3u;  // scales: whole 16-byte pieces, within the page
-                uint32_t bytes = rows * D + (is_v ? 0 : 2 * srows * 4);
+                uint32_t bytes = rows * D + (IS_V ? 0 : 2 * srows * 4);
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, d);
+                for (int d = 4; d > 0; d >>= 1) bytes += __shfl_xor_sync(0xffffffffu, bytes, d);  // at most 8 pieces
                 const unsigned mask = __ballot_sync(0xffffffffu, live);
-                uint8_t *raw = sm + C::SM_RAW + s * C::RAW;
+                uint8_t *raw = sm + dst0 + ring.slot * STRIDE;
                 if (lane == 0) {
-                    reinterpret_cast<int2 *>(sm + C::SM_INFO)[s] = make_int2(min(BN, len - j * BN), (int)mask);
-                    mbar_expect_tx(bar + FULL + s, bytes);
+                    reinterpret_cast<int2 *>(sm + C::SM_INFO)[(IS_V ? C::NR : 0) + ring.slot] = make_int2(min(BN, len - pos), (int)mask);
+                    mbar_expect_tx(bar + FULL + ring.slot, bytes);
                 }
                 __syncwarp();
                 if (live) {
                     const long at = ((long)page * pg.Hkv + k.pc.h) * P + row0;
-                    bulk_load(raw + piece * box * D, (is_v ? p.v_cache : p.k_cache) + at * D, rows * D, bar + FULL + s);
-                    if (!is_v) {
-                        bulk_load(raw + BN * D + piece * box * 4, p.k_scale + at, srows * 4, bar + FULL + s);
-                        bulk_load(raw + BN * D + BN * 4 + piece * box * 4, p.v_scale + at, srows * 4, bar + FULL + s);
+                    bulk_load(raw, (IS_V ? p.v_cache : p.k_cache) + at * D, rows * D, bar + FULL + ring.slot);
+                    if (!IS_V) {
+                        uint8_t *sc = raw - piece * box * D + BN * D + piece * box * 4;
+                        bulk_load(sc, p.k_scale + at, srows * 4, bar + FULL + ring.slot);
+                        bulk_load(sc + BN * 4, p.v_scale + at, srows * 4, bar + FULL + ring.slot);
                     }
                 }
             }
-            ++fill;
-        };
-        int next = page_of(k.pc.off), cur = -1, prev = -1;
-        for (int jj = 0; jj <= n && ok; ++jj) {
-            if (jj < n) {
-                cur = next;
-                if (jj + 1 < n) next = page_of(k.pc.off + jj + 1);
-                issue(k.pc.off + jj, cur, false);
-            }
-            if (jj > 0 && ok) issue(k.pc.off + jj - 1, prev, true);
-            prev = cur;
+            ring.next();
         }
     } while (ok && walk_next<BN>(p.w, &k));
     if (!ok && lane == 0) flag_error(pg.status);
     // the copies in flight must land before the CTA leaves, also if another warp has given up
-    for (uint32_t f = fill > NSLOT ? fill - NSLOT : 0; f < fill; ++f)
-        mbar_wait(bar + FULL + f % NSLOT, (f / NSLOT) & 1, kDrainBudget);
+    for (uint32_t f = t > N ? t - N : 0; f < t; ++f) mbar_wait(bar + FULL + f % N, (f / N) & 1, kDrainBudget);
     __syncwarp();
 }
 
 // ---- products ---------------------------------------------------------------------
+// One thread issues everything, in the order S_0, S_1, O(0), S_2, O(1), ..: what it does between two
+// products is time that the tensor cores may stand still, so slots and phases are counted on, not
+// divided out, and each product signals one barrier.
 template <int D, int KIND>
 __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *bar, Walk k, uint32_t tmem) {
     using C = Cfg<D, KIND>;
@@ -215,60 +235,63 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
     constexpr uint32_t ID_S = C::kCodes ? idesc_f16(128, BN, 0, 0) : idesc_bf16(128, BN, 0, 0);
     constexpr uint32_t ID_O = C::kCodes ? idesc_f16(128, D, 0, 1) : idesc_bf16(128, D, 0, 1);
     const int lane = threadIdx.x & 31;
-    uint32_t fill = 0, it = 0, unit = 0;
+    const uint64_t desc_k = desc_sw128(sb, 16, 1024), desc_v = desc_sw128(sb + C::SM_V, BN * 128, 1024);  // of slots 0
+    Ring<C::NK> rk;
+    Ring<C::NV> rv;
+    uint32_t it = 0, unit = 0;  // tiles and units begun
+    auto product_s = [&](uint32_t t) -> bool {
+        if (!mbar_wait_spin(bar + C::B_FK + rk.slot, rk.phase, p.budget)) return false;
+        tc_fence_after();
+        const uint64_t d = desc_k + (uint64_t)(rk.slot * (C::SLOT >> 4));
+        const uint32_t to = tmem + C::TM_S + (t & 1) * BN;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+            mma_f16_ts(to, tmem + C::TM_Q + 8 * ks, d + (uint64_t)(((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), ID_S,
+                       ks > 0);
+        mma_commit(bar + C::B_S + (t & (C::kTurns - 1)));
+        rk.next();
+        return true;
+    };
+    auto product_o = [&](uint32_t t, bool first) -> bool {
+        if (!mbar_wait_spin(bar + C::B_FV + rv.slot, rv.phase, p.budget) ||
+            !mbar_wait_spin(bar + C::B_P + (t & 1), (t >> 1) & 1, p.budget))
+            return false;
+        tc_fence_after();
+        const uint64_t d = desc_v + (uint64_t)(rv.slot * (C::SLOT >> 4));
+        const uint32_t a = tmem + C::TM_S + (t & 1) * BN;
+#pragma unroll
+        for (int ks = 0; ks < BN / 16; ++ks)
+            mma_f16_ts(tmem + C::TM_O, a + 8 * ks, d + (uint64_t)(ks * 128), ID_O, !first || ks > 0);
+        mma_commit(bar + C::B_PV + (t & (C::kTurns - 1)));
+        rv.next();
+        return true;
+    };
     bool ok = true;
     if (k.pc.left > 0) do {
         const int n = k.take();
-        ok = warp_wait_spin(bar + C::B_Q, unit & 1, p.budget);
-        ++unit;
-        for (int jj = 0; jj <= n && ok; ++jj) {
-            if (jj < n) {
-                const uint32_t s = fill % C::NS, b = (it + jj) & 1;
-                ok = warp_wait_spin(bar + C::B_FULL + s, (fill / C::NS) & 1, p.budget);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_f16_ts(tmem + C::TM_S + b * BN, tmem + C::TM_Q + 8 * ks,
-                                   desc_sw128(sb + s * C::SLOT + (ks >> 2) * (BN * 128) + (ks & 3) * 32, 16, 1024), ID_S,
-                                   ks > 0);
-                    mma_commit(bar + C::B_EMPTY + s);
-                    mma_commit(bar + C::B_S + b);
-                }
-                ++fill;
-            }
-            if (jj > 0) {
-                const uint32_t s = fill % C::NS, b = (it + jj - 1) & 1;
-                ok = warp_wait_spin(bar + C::B_FULL + s, (fill / C::NS) & 1, p.budget);
-                if (!ok) break;
-                if constexpr (!C::kCodes) {
-                    const int valid = k.pc.s.len - (k.pc.off + jj - 1) * BN;
-                    if (valid < BN) {  // rows of V past the end: zeros
-                        const int dead = (BN - valid) * 8;
-                        for (int e = lane; e < dead * C::NB; e += 32)
-                            *reinterpret_cast<uint4 *>(sm + s * C::SLOT + (e / dead) * (BN * 128) + valid * 128 +
-                                                       (e % dead) * 16) = make_uint4(0, 0, 0, 0);
-                        fence_async_smem();
-                        __syncwarp();
-                    }
-                }
-                ok = warp_wait_spin(bar + C::B_P + b, ((it + jj - 1) >> 1) & 1, p.budget);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
-#pragma unroll
-                    for (int ks = 0; ks < BN / 16; ++ks)
-                        mma_f16_ts(tmem + C::TM_O, tmem + C::TM_S + b * BN + 8 * ks,
-                                   desc_sw128(sb + s * C::SLOT + ks * 2048, BN * 128, 1024), ID_O, jj > 1 || ks > 0);
-                    mma_commit(bar + C::B_EMPTY + s);
-                    mma_commit(bar + C::B_PV + b);
-                }
-                ++fill;
-            }
-            __syncwarp();
+        if (lane == 0) {
+            ok = mbar_wait_spin(bar + C::B_Q, unit & 1, p.budget) && product_s(it);
+            for (int jj = 1; jj < n && ok; ++jj) ok = product_s(it + jj) && product_o(it + jj - 1, jj == 1);
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if constexpr (!C::kCodes) {  // rows of V past the end: zeros
+            const int valid = k.pc.s.len - (k.pc.off + n - 1) * BN;
+            const uint32_t slot = __shfl_sync(0xffffffffu, rv.slot, 0), phase = __shfl_sync(0xffffffffu, rv.phase, 0);
+            if (ok && valid < BN) {
+                ok = warp_wait_spin(bar + C::B_FV + slot, phase, p.budget);
+                const int dead = (BN - valid) * 8;
+                if (ok)
+                    for (int e = lane; e < dead * C::NB; e += 32)
+                        *reinterpret_cast<uint4 *>(sm + C::SM_V + slot * C::SLOT + (e / dead) * (BN * 128) + valid * 128 +
+                                                   (e % dead) * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+            }
+        }
+        if (lane == 0 && ok) ok = product_o(it + n - 1, n == 1);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         it += n;
+        ++unit;
     } while (ok && walk_next<BN>(p.w, &k));
     if (!ok && lane == 0) flag_error(p.w.pg.status);
     if (lane == 0) {  // all products done before TMEM is given back
@@ -279,89 +302,101 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
 }
 
 // ---- 8-bit tiles to fp16 --------------------------------------------------------------
-template <int KIND>
-__device__ __forceinline__ void codes4_to_f16(uint32_t c, uint32_t *h) {
-    if constexpr (KIND == GDN_FP8) {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3);
-        h[0] = (uint32_t)a.x | ((uint32_t)a.y << 16);
-        h[1] = (uint32_t)b.x | ((uint32_t)b.y << 16);
-    } else {
-        // c + 128 as the low byte of an fp16 in [1024, 2048), whose unit is 1; minus 1152 gives c, exactly
-        const uint32_t u = c ^ 0x80808080u;
-        const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
-        uint32_t w0 = __byte_perm(u, 0x64646464u, 0x4140), w1 = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&w0), bias), y = __hsub2(*reinterpret_cast<__half2 *>(&w1), bias);
-        h[0] = *reinterpret_cast<const uint32_t *>(&x);
-        h[1] = *reinterpret_cast<const uint32_t *>(&y);
+// 16 codes a thread and step, from `raw` to the two swizzled 16-byte pieces. Eight lanes take the
+// halves (4 pieces) of two rows that lie in different banks of both the codes and the tile; from
+// one step to the next the row moves by a multiple of 8, which leaves the swizzle as it is.
+template <int D, int KIND>
+__device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst0, uint8_t *dst1, int row, int valid,
+                                             int pages, int box_shift) {
+    using C = Cfg<D, KIND>;
+    constexpr int STEPS = C::BN * D / 16 / (kConvWarps * 32), ROWS = kConvWarps * 32 / (D / 16);
+    static_assert(ROWS % 8 == 0 && STEPS % 4 == 0, "the swizzle must not change between steps");
+#pragma unroll
+    for (int st = 0; st < STEPS; st += 4) {
+        uint4 q[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) q[u] = *reinterpret_cast<const uint4 *>(raw + (st + u) * ROWS * D);
+        if (valid >= 0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int r = row + (st + u) * ROWS;
+                if (r >= valid || !((pages >> (r >> box_shift)) & 1)) q[u] = make_uint4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            uint32_t h[8];
+            codes4_to_f16<KIND>(q[u].x, h[0], h[1]);
+            codes4_to_f16<KIND>(q[u].y, h[2], h[3]);
+            codes4_to_f16<KIND>(q[u].z, h[4], h[5]);
+            codes4_to_f16<KIND>(q[u].w, h[6], h[7]);
+            *reinterpret_cast<uint4 *>(dst0 + (st + u) * ROWS * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4 *>(dst1 + (st + u) * ROWS * 128) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
     }
 }
 
 template <int D, int KIND>
 __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k) {
     using C = Cfg<D, KIND>;
-    constexpr int BN = C::BN, NT = kConvWarps * 32;
+    constexpr int BN = C::BN;
     const int tid = threadIdx.x - kConvWarp0 * 32, lane = tid & 31;
-    const int P = p.w.pg.page_size, box_shift = 31 - __clz(min(P, BN));
-    uint32_t fill = 0, tile = 0;
+    const int box = min(p.w.pg.page_size, BN), box_shift = 31 - __clz(box), all_pages = (1 << (BN / box)) - 1;
+    const int e8 = tid & 7, g8 = tid >> 3, row0 = 2 * (g8 / C::NB) + (e8 >> 2);
+    const int blk = C::NB == 1 ? 0 : (g8 % C::NB) ^ (e8 >> 2), c = e8 & 3;
+    const uint32_t src0 = row0 * D + blk * 64 + c * 16;
+    const uint32_t dst0 = blk * (BN * 128) + swz(row0, 2 * c), dst1 = blk * (BN * 128) + swz(row0, 2 * c + 1);
+    Ring<C::NK> rk;
+    Ring<C::NV> rv;
+    Ring<C::NR> rr[2];
+    uint32_t t[2] = {0, 0};  // tiles converted
     bool ok = true;
+    auto convert = [&](auto is_v) -> bool {
+        constexpr bool IS_V = decltype(is_v)::value;
+        constexpr int N = IS_V ? C::NV : C::NK;
+        const uint32_t r = rr[IS_V].slot, s = IS_V ? rv.slot : rk.slot;
+        bool got = mbar_wait_spin(bar + (IS_V ? C::B_RV : C::B_RK) + r, rr[IS_V].phase, p.budget);
+        if (t[IS_V] >= N) got = got && product_done<D, KIND>(bar, IS_V ? C::B_PV : C::B_S, t[IS_V] - N, p.budget);
+        if (!__all_sync(0xffffffffu, got)) return false;
+        const uint8_t *raw = sm + (IS_V ? C::SM_RV + r * C::RAW_V : C::SM_RK + r * C::RAW_K);
+        uint8_t *dst = sm + (IS_V ? C::SM_V : 0) + s * C::SLOT;
+        const int2 info = reinterpret_cast<const int2 *>(sm + C::SM_INFO)[(IS_V ? C::NR : 0) + r];
+        // A tile that is whole takes no checks; rows past the end and bad pages become zeros.
+        const bool whole = info.x == BN && info.y == all_pages;
+        convert_tile<D, KIND>(raw + src0, dst + dst0, dst + dst1, row0, whole ? -1 : info.x, info.y, box_shift);
+        if constexpr (!IS_V) {
+            const uint32_t cb = t[0] % C::COLS;
+            if (tid < BN) {
+                const float *sc = reinterpret_cast<const float *>(raw + BN * D);
+                const bool live = tid < info.x && ((info.y >> (tid >> box_shift)) & 1);
+                const float ks = live ? sc[tid] : 0.f;
+                float vs = live ? sc[BN + tid] : kMinKvScale;
+                if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
+                float *col = reinterpret_cast<float *>(sm + C::SM_COL) + cb * 3 * BN;
+                col[tid] = ks * p.scale2;
+                col[BN + tid] = __log2f(vs);
+                col[2 * BN + tid] = vs == vs ? __frcp_rn(vs) : 0.f;  // a NaN enters by b, and not where it is masked
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + C::B_COL + cb);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bar + (IS_V ? C::B_FV : C::B_FK) + s);
+            mbar_arrive(bar + (IS_V ? C::B_REV : C::B_REK) + r);
+        }
+        if (IS_V) rv.next();
+        else rk.next();
+        rr[IS_V].next();
+        ++t[IS_V];
+        return true;
+    };
     if (k.pc.left > 0) do {
         const int n = k.take();
-        for (int jj = 0; jj <= n && ok; ++jj) {
-#pragma unroll 1
-            for (int is_v = 0; is_v < 2 && ok; ++is_v) {
-                if (is_v ? jj == 0 : jj == n) continue;
-                const uint32_t r = fill % C::NR, s = fill % C::NS;
-                ok = warp_wait(bar + C::B_RFULL + r, (fill / C::NR) & 1, p.budget) &&
-                     warp_wait(bar + C::B_EMPTY + s, ((fill / C::NS) & 1) ^ 1, p.budget);
-                if (!ok) break;
-                const uint8_t *raw = sm + C::SM_RAW + r * C::RAW;
-                uint8_t *dst = sm + s * C::SLOT;
-                const int2 info = reinterpret_cast<const int2 *>(sm + C::SM_INFO)[r];
-                // 16 codes a step. Eight lanes take the halves (4 pieces) of two rows that lie in
-                // different banks of both the codes and the swizzled tile.
-#pragma unroll 4
-                for (int e = tid; e < BN * D / 16; e += NT) {
-                    const int i = e & 7, g = e >> 3;
-                    const int row = 2 * (g / C::NB) + (i >> 2);
-                    const int blk = C::NB == 1 ? 0 : (g % C::NB) ^ (i >> 2), c = i & 3;
-                    uint4 q = *reinterpret_cast<const uint4 *>(raw + row * D + blk * 64 + c * 16);
-                    if (row >= info.x || !((info.y >> (row >> box_shift)) & 1)) q = make_uint4(0, 0, 0, 0);
-                    uint32_t h[8];
-                    codes4_to_f16<KIND>(q.x, h);
-                    codes4_to_f16<KIND>(q.y, h + 2);
-                    codes4_to_f16<KIND>(q.z, h + 4);
-                    codes4_to_f16<KIND>(q.w, h + 6);
-                    uint8_t *d = dst + blk * (BN * 128);
-                    *reinterpret_cast<uint4 *>(d + swz(row, 2 * c)) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4 *>(d + swz(row, 2 * c + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-                }
-                if (!is_v) {
-                    const uint32_t cb = tile % C::COLS;
-                    if (tid < BN) {
-                        const float *sc = reinterpret_cast<const float *>(raw + BN * D);
-                        const bool live = tid < info.x && ((info.y >> (tid >> box_shift)) & 1);
-                        const float ks = live ? sc[tid] : 0.f;
-                        float vs = live ? sc[BN + tid] : kMinKvScale;
-                        if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
-                        float *col = reinterpret_cast<float *>(sm + C::SM_COL) + cb * 3 * BN;
-                        col[tid] = ks * p.scale2;
-                        col[BN + tid] = log2f(vs);
-                        col[2 * BN + tid] = 1.f / vs;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar + C::B_COL + cb);
-                    ++tile;
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar + C::B_FULL + s);
-                    mbar_arrive(bar + C::B_REMPTY + r);
-                }
-                ++fill;
-            }
-        }
+        ok = convert(std::false_type{});
+        for (int jj = 1; jj < n && ok; ++jj) ok = convert(std::false_type{}) && convert(std::true_type{});
+        ok = ok && convert(std::true_type{});
     } while (ok && walk_next<BN>(p.w, &k));
     if (!ok && lane == 0) flag_error(p.w.pg.status);
 }
@@ -410,12 +445,9 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
                 bar_any(bar_id, 64, false);
                 amax = fmaxf(amax, xch[turn & 1][g ^ 1][row]);
                 ++turn;
-                // amax 2^e in [2^13, 2^14): the largest elements far from overflow, the smallest normal
-                int e = 13 - ((int)(__float_as_uint(amax) >> 23) - 127);
-                if (!(amax > 0.f && amax < 3.4e38f)) e = 0;
-                e = max(-100, min(100, e));
-                const float f = __uint_as_float((uint32_t)(127 + e) << 23);
-                rs = __uint_as_float((uint32_t)(127 - e) << 23);
+                const int e = f16_row_exponent(amax);
+                const float f = pow2i(e);
+                rs = pow2i(-e);
 #pragma unroll
                 for (int c = 0; c < W; ++c)
                     r[c] = h2_bits(f * __uint_as_float(r[c] << 16), f * __uint_as_float(r[c] & 0xffff0000u));
@@ -432,9 +464,9 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
         if (lane == 0) mbar_arrive(bar + C::B_Q);
         float m = -INFINITY, l = 0.f;
         for (int jj = 0; jj < n && !failed; ++jj, ++it) {
-            const uint32_t b = it & 1, ph = (it >> 1) & 1;
-            late |= !mbar_wait(bar + C::B_S + b, ph, p.budget);
-            if constexpr (C::kCodes) late = late || !mbar_wait(bar + C::B_COL + it % C::COLS, (it / C::COLS) & 1, p.budget);
+            const uint32_t b = it & 1;
+            late |= !product_done<D, KIND>(bar, C::B_S, it, p.budget);
+            if constexpr (C::kCodes) late = late || !mbar_wait_spin(bar + C::B_COL + it % C::COLS, (it / C::COLS) & 1, p.budget);
             if (!live_warp) {
                 failed = __any_sync(0xffffffffu, late);
                 if (lane == 0 && !failed) mbar_arrive(bar + C::B_P + b);
@@ -477,15 +509,12 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
             ++turn;
             const float sc = C::kCodes ? 1.f : p.scale2;
             const float mt = top * sc;
-            const bool grow = mt > m + kGrow || (m == -INFINITY && mt > m);
-            const float f = grow ? ex2(m - mt) : 1.f;  // m = -inf: 0
-            if (grow) {
-                m = mt;
-                l *= f;
-            }
+            float f;
+            const bool grow = grow_reference(m, mt, f);
+            l *= f;
             if (jj > 0 && __any_sync(0xffffffffu, grow)) {
                 // O holds the tiles up to jj - 1
-                late |= !mbar_wait(bar + C::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1, p.budget);
+                late |= !product_done<D, KIND>(bar, C::B_PV, it - 1, p.budget);
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < D / 2; c += 32) {
@@ -525,7 +554,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
         }
         if (failed) break;
         // the unit's last product, then the row
-        late |= !mbar_wait(bar + C::B_PV + ((it - 1) & 1), ((it - 1) >> 1) & 1, p.budget);
+        late |= !product_done<D, KIND>(bar, C::B_PV, it - 1, p.budget);
         if (live_warp) {
             tc_fence_after();
             xch[turn & 1][g][row] = l;
@@ -581,20 +610,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     const int tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
-        for (int s = 0; s < C::NS; ++s) {
-            mbar_init(bar + C::B_FULL + s, C::kCodes ? kConvWarps : 1);
-            mbar_init(bar + C::B_EMPTY + s, 1);
-        }
+        for (int s = 0; s < C::NK; ++s) mbar_init(bar + C::B_FK + s, C::kCodes ? kConvWarps : 1);
+        for (int s = 0; s < C::NV; ++s) mbar_init(bar + C::B_FV + s, C::kCodes ? kConvWarps : 1);
         for (int s = 0; s < C::NR; ++s) {
-            mbar_init(bar + C::B_RFULL + s, 1);
-            mbar_init(bar + C::B_REMPTY + s, kConvWarps);
+            mbar_init(bar + C::B_RK + s, 1);
+            mbar_init(bar + C::B_RV + s, 1);
+            mbar_init(bar + C::B_REK + s, kConvWarps);
+            mbar_init(bar + C::B_REV + s, kConvWarps);
         }
         for (int s = 0; s < C::COLS; ++s) mbar_init(bar + C::B_COL + s, kConvWarps);
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < C::kTurns; ++s) {
             mbar_init(bar + C::B_S + s, 1);
-            mbar_init(bar + C::B_P + s, kSoftWarps);
             mbar_init(bar + C::B_PV + s, 1);
         }
+        for (int s = 0; s < 2; ++s) mbar_init(bar + C::B_P + s, kSoftWarps);
         mbar_init(bar + C::B_Q, kSoftWarps);
         mbar_init(bar + C::B_FIN, 1);
         fence_mbar_init();
@@ -608,7 +637,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     if (warp < kSoftWarps) {
         soft_role<D, KIND>(p, sm, bar, k, tmem);
     } else if (warp == kLoadWarp) {
-        load_role<D, KIND>(p, sm, bar, k, &mk, &mv);
+        load_role<D, KIND, false>(p, sm, bar, k, &mk);
+    } else if (warp == kLoadWarp + 1) {
+        load_role<D, KIND, true>(p, sm, bar, k, &mv);
     } else if (warp == kMmaWarp) {
         zero_padding(p.w, p.out, p.Hq, D, tid & 31, 32);  // while the first tiles are on their way
         mma_role<D, KIND>(p, sm, sb, bar, k, tmem);
@@ -622,36 +653,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 }
 
 // ---- host side ------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encoder() {
-    static EncodeTiledFn fn = []() -> EncodeTiledFn {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            return nullptr;
-        return reinterpret_cast<EncodeTiledFn>(f);
-    }();
-    return fn;
-}
-
-// [page, head][page_size][d] bf16 -> 3-D map, box (64 elements, `rows` positions, 1), 128B swizzle
-bool page_map(CUtensorMap *m, const void *base, const KvPages &pg, int rows) {
-    EncodeTiledFn enc = encoder();
-    if (!enc) return false;
-    const cuuint64_t gdim[3] = {(cuuint64_t)pg.d, (cuuint64_t)pg.page_size, (cuuint64_t)pg.num_pages * pg.Hkv};
-    const cuuint64_t gstride[2] = {(cuuint64_t)pg.d * 2, (cuuint64_t)pg.page_size * pg.d * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
-    const cuuint32_t estride[3] = {1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), gdim, gstride, box, estride,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, int KIND>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     using C = Cfg<D, KIND>;
@@ -669,15 +670,12 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     p.negate = a.scale < 0.f;
     // a scale of 0 must not meet the -inf of a masked score in a product: so small that no score counts
     p.scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
-    p.budget = kWaitDefault;
-    if (const char *env = getenv("GDN_TEST_WAIT_CYCLES")) {  // test hook: a short limit makes the waits run out
-        const long long x = atoll(env);
-        if (x > 0) p.budget = x;
-    }
+    p.budget = wait_budget();
     CUtensorMap mk{}, mv{};
     if (!C::kCodes) {
         const int rows = a.pg.page_size < C::BN ? a.pg.page_size : C::BN;
-        if (!page_map(&mk, a.k_cache, a.pg, rows) || !page_map(&mv, a.v_cache, a.pg, rows)) return cudaErrorInvalidValue;
+        if (!page_map(&mk, a.k_cache, a.pg, D * 2, rows) || !page_map(&mv, a.v_cache, a.pg, D * 2, rows))
+            return cudaErrorInvalidValue;
     }
     auto kernel = attn_tc_kernel<D, KIND>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);

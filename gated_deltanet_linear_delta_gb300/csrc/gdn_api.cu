@@ -438,8 +438,10 @@ int gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     a.q_stride = (long)q_stride;
     a.scale = scale;
     a.ws = workspace;
-    const cudaError_t e = dtype == GDN_BF16 ? gdn::launch_attn_tc(a, static_cast<cudaStream_t>(stream))
-                                            : gdn::launch_attn_simt(a, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype != GDN_BF16 ? gdn::launch_attn_simt(a, s)
+                          : gdn::attn_rows_supported(a) ? gdn::launch_attn_rows(a, s)
+                                                        : gdn::launch_attn_tc(a, s);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

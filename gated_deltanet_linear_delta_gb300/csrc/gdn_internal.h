@@ -78,6 +78,8 @@ constexpr int kAttnMaxRows = 128;
 size_t attn_workspace(long tokens_per_seq, int G, int d);
 cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t s);  // fp32
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t s);    // bf16
+bool attn_rows_supported(const AttnArgs &a);                      // bf16, few rows per key head
+cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t s);
 
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t s);
 cudaError_t launch_prepass(const PrepassArgs &a, cudaStream_t s);

@@ -168,6 +168,24 @@ def test_what_a_nan_key_reaches(dtype, cache):
     assert_attention(out[keep], ref[keep], mag[keep], err[keep])
 
 
+@pytest.mark.parametrize("T", [5, 40])
+@pytest.mark.parametrize("cache", ["fp8", "int8"])
+def test_what_a_row_stored_as_nan_reaches(cache, T):
+    """A value row that was not finite when it was stored (scale NaN): NaN for the rows that see it, and
+    nothing for those before it, although it lies in their key tile."""
+    case = Paged([100, 100], 1, 64, 16, cache, "bf16", seed=6)
+    kc, vc, ks, vs, table, lens = case.tensors()
+    pos = 97
+    vs[int(table[0, pos // 16]), 0, pos % 16] = float("nan")
+    q = torch.randn(2 * T, 3, 64, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    out = torch.empty(q.shape, dtype=q.dtype, device=DEV)
+    gdn.gdn_paged_attn(q.to(DEV), kc, vc, table, lens, out, ks, vs)
+    assert torch.isnan(out[T - 3:T]).all()
+    ref, mag, err = reference(case, q, [T, T], 64 ** -0.5)
+    keep = [i for i in range(2 * T) if i < T - 3 or i >= T]
+    assert_attention(out[keep], ref[keep], mag[keep], err[keep])
+
+
 def test_offsets_past_32_bits():
     Hkv, d, page = 8, 256, 256
     pages = 2 ** 31 // (Hkv * page * d) + 9
