@@ -25,13 +25,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x + 1, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const AttnRec r = w.rec[c];
-    if (c >= r.active || r.off == 0) return;
-    if (r.begin - r.off < piece_begin(r.total, c - 1, r.active)) return;  // an earlier boundary lies in this unit too
-    // the piece that holds the unit's last key tile
-    const long end = r.begin - r.off + r.ntiles - 1;
-    int last = (int)(end * r.active / r.total);
-    while (last + 1 < r.active && piece_begin(r.total, last + 1, r.active) <= end) ++last;
-    while (piece_begin(r.total, last, r.active) > end) --last;
+    if (c >= r.cut.active || r.off == 0) return;
+    if (r.begin - r.off < r.cut.begin(c - 1)) return;  // an earlier boundary lies in this unit too
+    const int last = r.cut.piece_of(r.begin - r.off + r.ntiles - 1);  // the piece that holds the unit's last key tile
     const int parts = last - c + 2, rows = r.tokens * w.G;
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
         const int t = row / w.G;
@@ -95,12 +91,12 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
 }
 
 template <typename TOut, int D>
-cudaError_t launch_t(const AttnWork &w, TOut *out, int Hq, int rows, cudaStream_t s) {
+cudaError_t launch_t(const AttnWork &w, TOut *out, int Hq, int rows, int ctas, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(kAttnCtas - 1, (unsigned)(rows < 16 ? rows : 16), 1);
+    cfg.gridDim = dim3((unsigned)ctas - 1, (unsigned)(rows < 16 ? rows : 16), 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = &attr;
@@ -110,12 +106,13 @@ cudaError_t launch_t(const AttnWork &w, TOut *out, int Hq, int rows, cudaStream_
 
 }  // namespace
 
-cudaError_t launch_attn_join(const AttnArgs &a, const AttnWork &w, cudaStream_t s) {
+cudaError_t launch_attn_join(const AttnArgs &a, const AttnWork &w, int ctas, cudaStream_t s) {
+    if (ctas <= 1) return cudaSuccess;  // one piece: nothing is split
     const bool f32 = a.pg.dtype == GDN_F32;
 #define GDN_JOIN_CASE(DV)                                                                      \
     case DV:                                                                                   \
-        return f32 ? launch_t<float, DV>(w, (float *)a.out, a.Hq, w.rows, s)                   \
-                   : launch_t<__nv_bfloat16, DV>(w, (__nv_bfloat16 *)a.out, a.Hq, w.rows, s);
+        return f32 ? launch_t<float, DV>(w, (float *)a.out, a.Hq, w.rows, ctas, s)                   \
+                   : launch_t<__nv_bfloat16, DV>(w, (__nv_bfloat16 *)a.out, a.Hq, w.rows, ctas, s);
     switch (a.pg.d) { GDN_JOIN_CASE(64) GDN_JOIN_CASE(128) GDN_JOIN_CASE(256) }
 #undef GDN_JOIN_CASE
     return cudaErrorInvalidValue;
@@ -133,6 +130,16 @@ int attn_unit_rows(long tokens_per_seq, int G) {
 size_t attn_workspace(long tokens_per_seq, int G, int d) {
     const size_t parts = (size_t)kAttnCtas * 2 * attn_unit_rows(tokens_per_seq, G);
     return up256(kAttnCtas * sizeof(AttnRec)) + up256(parts * sizeof(float2)) + parts * d * sizeof(float);
+}
+
+// CTAs that can have a piece at all, going by what the host knows (the block table's width)
+int attn_ctas(const AttnArgs &a, const AttnWork &w, int BN) {
+    const long positions = (long)a.pg.max_pages * a.pg.page_size;
+    const long units = (a.pg.cu ? a.pg.B + a.pg.Ttot / w.TPT : (long)a.pg.B * ((a.pg.T + w.TPT - 1) / w.TPT)) * a.pg.Hkv;
+    const long tiles = (positions + BN - 1) / BN;
+    const long pieces = units > kAttnCtas || tiles > kAttnCtas ? (long)kAttnCtas * w.min_tiles : units * tiles;
+    const long ctas = (pieces + w.min_tiles - 1) / w.min_tiles;
+    return (int)(ctas < kAttnCtas ? ctas : kAttnCtas);
 }
 
 AttnWork attn_work(const AttnArgs &a, int tokens_per_tile, int min_tiles) {

@@ -24,6 +24,18 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// base-2 logarithm and reciprocal of a cached scale, to the hardware's 2^-22: their errors cancel in
+// nothing but a relative 2^-21 of each probability
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // 4 codes to fp16 (exact)
 template <int KIND>
 __device__ __forceinline__ void codes4_to_f16(uint32_t c, uint32_t &h0, uint32_t &h1) {

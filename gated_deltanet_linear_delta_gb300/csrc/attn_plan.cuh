@@ -16,20 +16,34 @@
 
 namespace gdn {
 
+// The line of `total` key tiles as `active` pieces whose sizes differ by one at most: piece c begins
+// at c q + min(c, r).
+struct Cut {
+    long q;
+    int r, active;
+    __device__ __forceinline__ long begin(int c) const { return c * q + min(c, r); }
+    __device__ __forceinline__ int piece_of(long tile) const {  // the piece that holds a tile
+        const long wide = r * (q + 1);
+        if (tile < wide) return (int)div(tile, q + 1);
+        return r + (int)div(tile - wide, q);
+    }
+    // a 64-bit division takes hundreds of cycles; nearly all of these fit 32 bits
+    __device__ __forceinline__ static long div(long a, long b) {
+        if ((a | b) >> 31) return a / b;
+        return (long)((uint32_t)a / (uint32_t)b);
+    }
+};
+
 struct __align__(16) AttnRec {  // where CTA c's piece starts; read by the joining kernel
+    Cut cut;       // the same in every record
+    long begin;    // key tiles of all units before the piece
     int off;       // key tiles of the unit before the piece (0: the unit starts here)
     int ntiles;    // key tiles of the unit
-    int active;    // pieces in all
-    int h;         // key head of the unit
-    long begin;    // key tiles of all units before the piece
-    long total;    // key tiles of all units
     long token;    // packed token of the unit's first row
     int tokens;    // its new tokens
     int pos;       // position of the first (negative: padding)
+    int h;         // key head of the unit
 };
-
-// First key tile of piece c of `active` equal ones.
-__device__ __forceinline__ long piece_begin(long total, int c, int active) { return total * c / active; }
 
 struct AttnWork {
     KvPages pg;
@@ -93,117 +107,147 @@ struct Piece {
 struct PlanSmem {
     long sum[32];
     int found;
+    int padding;  // some sequence has more new tokens than positions
     Piece piece;
 };
 
 // Finds this CTA's piece; every thread of the CTA calls it (NT threads, a multiple of 32, at most
-// 1024). The result is in sm->piece (left = 0: no work), and its record in the workspace.
+// 1024). The result is in sm->piece (left = 0: no work), and its record in the workspace. It stands
+// before all other work of the call, so it is kept short: one pass over the sequences (a second
+// where there are more than NT), two or three barriers, 32-bit divisions.
 template <int BN, int NT>
 __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     constexpr int NW = NT / 32;
     const KvPages &p = w.pg;
-    // all key tiles; the first NT sequences' stay in registers
-    long mine = 0, first = 0;
+    const bool one_pass = p.B <= NT;
+    long mine = 0;
     SeqInfo s0{0, 0, 0};
+    bool pad = false;
     for (int base = 0; base < p.B; base += NT) {
         SeqInfo s{0, 0, 0};
         if (base + tid < p.B) seq_info(p, base + tid, &s);
-        const long x = seq_tiles<BN>(w, s) * p.Hkv;
-        mine += x;
-        if (base == 0) { first = x; s0 = s; }
+        pad |= s.T > s.len;
+        mine += seq_tiles<BN>(w, s) * p.Hkv;
+        s0 = s;
     }
-    long x = mine;
+    auto scan = [&](long y) {  // inclusive, over the warp
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    if (lane == 0) sm->sum[wid] = x;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long o = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) y += o;
+        }
+        return y;
+    };
+    long inc = scan(mine);
+    if (lane == 31) sm->sum[wid] = inc;
     if (tid == 0) sm->found = -1;
-    __syncthreads();
-    long total = 0;
+    const int any_pad = __syncthreads_or(pad);
+    if (tid == 0) sm->padding = any_pad;
+    long total = 0, pre = inc - mine;
 #pragma unroll
-    for (int k = 0; k < NW; ++k) total += sm->sum[k];
-    __syncthreads();
-    const long want = (total + w.min_tiles - 1) / w.min_tiles;
-    const int active = (int)(want < (long)gridDim.x ? want : (long)gridDim.x);
+    for (int k = 0; k < NW; ++k) {
+        if (k < wid) pre += sm->sum[k];
+        total += sm->sum[k];
+    }
+    const long want = Cut::div(total + w.min_tiles - 1, w.min_tiles);
+    Cut cut;
+    cut.active = (int)(want < (long)gridDim.x ? want : (long)gridDim.x);
+    cut.q = cut.active ? Cut::div(total, cut.active) : 0;
+    cut.r = (int)(total - cut.q * cut.active);
     const int c = blockIdx.x;
-    const long begin = c < active ? piece_begin(total, c, active) : total;
-    long end = c < active ? piece_begin(total, c + 1, active) : total;
-    // the sequence that holds `begin`
-    long before = 0;
-    if (begin < end) {
-        for (int base = 0; base < p.B; base += NT) {
-            SeqInfo s = s0;
-            long y = first;
-            if (base > 0) {
-                s = SeqInfo{0, 0, 0};
-                if (base + tid < p.B) seq_info(p, base + tid, &s);
-                y = seq_tiles<BN>(w, s) * p.Hkv;
+    const long begin = c < cut.active ? cut.begin(c) : total, end = c < cut.active ? cut.begin(c + 1) : total;
+    long y = mine;
+    auto own = [&](int n) {  // this thread's sequence holds `begin`: head, and row tile if there are few
+        Piece pc;
+        const long per_head = Cut::div(y, p.Hkv);
+        long rem = begin - pre;
+        pc.n = n;
+        pc.s = s0;
+        pc.h = (int)Cut::div(rem, per_head);
+        rem -= pc.h * per_head;
+        pc.i = 0;
+        pc.ntiles = unit_tiles<BN>(w, s0, 0);
+        const int nq = row_tiles(w, s0);
+        if (nq <= 4) {
+            while (rem >= pc.ntiles) {
+                rem -= pc.ntiles;
+                pc.ntiles = unit_tiles<BN>(w, s0, ++pc.i);
             }
-            long inc = y;  // inclusive scan over the CTA
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const long o = __shfl_up_sync(0xffffffffu, inc, d);
-                if (lane >= d) inc += o;
-            }
+        } else {
+            pc.i = -1;
+        }
+        pc.off = (int)rem;  // (below 2^31: a head's tiles; checked below where there are many row tiles)
+        pc.left = rem;
+        sm->piece = pc;
+        sm->found = n;
+    };
+    if (one_pass) {
+        if (begin < end && begin >= pre && begin < pre + mine) own(tid);
+        __syncthreads();
+    } else {
+        long before = 0;
+        __syncthreads();
+        for (int base = 0; base < p.B && begin < end; base += NT) {
+            s0 = SeqInfo{0, 0, 0};
+            if (base + tid < p.B) seq_info(p, base + tid, &s0);
+            y = seq_tiles<BN>(w, s0) * p.Hkv;
+            inc = scan(y);
             if (lane == 31) sm->sum[wid] = inc;
             __syncthreads();
-            long pre = before, all = before;
+            pre = before + inc - y;
 #pragma unroll
             for (int k = 0; k < NW; ++k) {
                 if (k < wid) pre += sm->sum[k];
-                all += sm->sum[k];
+                before += sm->sum[k];
             }
-            pre += inc - y;
-            if (begin >= pre && begin < pre + y) {
-                sm->found = base + tid;
-                sm->piece.n = base + tid;
-                sm->piece.s = s;
-                sm->piece.left = begin - pre;  // for now: key tiles before the piece in this sequence
-            }
-            before = all;
+            if (begin >= pre && begin < pre + y) own(base + tid);
             __syncthreads();
             if (sm->found >= 0) break;
         }
-        if (sm->found < 0) end = begin;  // only if kv_lens changed under the call
     }
-    if (wid == 0) {  // head and row tile within the sequence
-        Piece pc{};
-        if (begin < end) {
-            pc = sm->piece;
+    const bool work = begin < end && sm->found >= 0;  // (not found: only if kv_lens changed under the call)
+    if (work && sm->piece.i < 0) {  // many row tiles: a warp walks over them, 32 at a time
+        __syncthreads();
+        if (wid == 0) {
+            Piece pc = sm->piece;
             const int nq = row_tiles(w, pc.s);
-            long per_head = 0;
-            for (int i = lane; i < nq; i += 32) per_head += unit_tiles<BN>(w, pc.s, i);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) per_head += __shfl_xor_sync(0xffffffffu, per_head, d);
-            pc.h = (int)(pc.left / per_head);
-            long rem = pc.left % per_head;
+            long rem = pc.left;
             for (int i0 = 0; i0 < nq; i0 += 32) {
                 const int t = i0 + lane < nq ? unit_tiles<BN>(w, pc.s, i0 + lane) : 0;
-                int inc = t;  // at most 32 * 2^31 / BN: fits
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, inc, d);
-                    if (lane >= d) inc += o;
-                }
-                const int chunk = __shfl_sync(0xffffffffu, inc, 31);
+                long sum = scan(t);
+                const long chunk = __shfl_sync(0xffffffffu, sum, 31);
                 if (rem < chunk) {
-                    const unsigned m = __ballot_sync(0xffffffffu, rem < inc);
+                    const unsigned m = __ballot_sync(0xffffffffu, rem < sum);
                     const int src = __ffs(m) - 1;
                     pc.i = i0 + src;
                     pc.ntiles = __shfl_sync(0xffffffffu, t, src);
-                    pc.off = (int)rem - (__shfl_sync(0xffffffffu, inc, src) - pc.ntiles);
+                    pc.off = (int)(rem - (__shfl_sync(0xffffffffu, sum, src) - pc.ntiles));
                     break;
                 }
                 rem -= chunk;
             }
+            __syncwarp();
+            if (lane == 0) sm->piece = pc;
         }
-        pc.left = end - begin;
-        if (lane == 0) {
-            sm->piece = pc;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        AttnRec r{cut, begin, 0, 0, 0, 0, 0, 0};
+        if (work) {
+            const Piece &pc = sm->piece;
             const int t0 = pc.i * w.TPT;
-            w.rec[c] = AttnRec{pc.off, pc.ntiles, active, pc.h, begin, total, pc.s.bos + t0, min(w.TPT, pc.s.T - t0),
-                               pc.s.len - pc.s.T + t0};
+            r.off = pc.off;
+            r.ntiles = pc.ntiles;
+            r.token = pc.s.bos + t0;
+            r.tokens = min(w.TPT, pc.s.T - t0);
+            r.pos = pc.s.len - pc.s.T + t0;
+            r.h = pc.h;
+            sm->piece.left = end - begin;
+        } else {
+            sm->piece = Piece{};
         }
+        w.rec[c] = r;
     }
     __syncthreads();
 }
@@ -228,7 +272,8 @@ __device__ __forceinline__ void next_unit(const AttnWork &w, Piece *pc) {
     } while (pc->ntiles == 0);
 }
 
-// Rows of padding tokens are zeros; no unit of work covers them. (`threads` threads of each CTA call it.)
+// Rows of padding tokens are zeros; no unit of work covers them. (`threads` threads of each CTA call
+// it, if the plan has found any.)
 template <typename TOut>
 __device__ void zero_padding(const AttnWork &w, TOut *out, int Hq, int d, int thread, int threads) {
     for (int n = blockIdx.x; n < w.pg.B; n += gridDim.x) {

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     plan_piece<BN, kThreads>(w, &sm.plan);
-    zero_padding(w, a.out, a.Hq, D, tid, kThreads);
+    if (sm.plan.padding) zero_padding(w, a.out, a.Hq, D, tid, kThreads);
     Piece pc = sm.plan.piece;
     for (bool begun = pc.off == 0; pc.left > 0; begun = true) {
         const int t0 = pc.i * w.TPT, rows = min(w.TPT, pc.s.T - t0) * w.G;
@@ -212,9 +212,10 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     static_assert(bytes <= 232448, "over the 227 KiB opt-in limit");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    kernel<<<kAttnCtas, kThreads, bytes, s>>>(p);
+    const int ctas = attn_ctas(a, p.w, BN);
+    kernel<<<ctas, kThreads, bytes, s>>>(p);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_attn_join(a, p.w, s);
+    return e != cudaSuccess ? e : launch_attn_join(a, p.w, ctas, s);
 }
 
 template <int KIND, int D>

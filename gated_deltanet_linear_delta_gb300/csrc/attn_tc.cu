@@ -374,8 +374,8 @@ __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk
                 if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
                 float *col = reinterpret_cast<float *>(sm + C::SM_COL) + cb * 3 * BN;
                 col[tid] = ks * p.scale2;
-                col[BN + tid] = __log2f(vs);
-                col[2 * BN + tid] = vs == vs ? __frcp_rn(vs) : 0.f;  // a NaN enters by b, and not where it is masked
+                col[BN + tid] = lg2(vs);
+                col[2 * BN + tid] = vs == vs ? rcp(vs) : 0.f;  // a NaN enters by b, and not where it is masked
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + C::B_COL + cb);
@@ -610,6 +610,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     const int tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
+        prefetch_tmap(&mk);
+        prefetch_tmap(&mv);
+    }
+    if (tid == 0) {
         for (int s = 0; s < C::NK; ++s) mbar_init(bar + C::B_FK + s, C::kCodes ? kConvWarps : 1);
         for (int s = 0; s < C::NV; ++s) mbar_init(bar + C::B_FV + s, C::kCodes ? kConvWarps : 1);
         for (int s = 0; s < C::NR; ++s) {
@@ -641,7 +645,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     } else if (warp == kLoadWarp + 1) {
         load_role<D, KIND, true>(p, sm, bar, k, &mv);
     } else if (warp == kMmaWarp) {
-        zero_padding(p.w, p.out, p.Hq, D, tid & 31, 32);  // while the first tiles are on their way
+        if (plan->padding) zero_padding(p.w, p.out, p.Hq, D, tid & 31, 32);  // while the first tiles are on their way
         mma_role<D, KIND>(p, sm, sb, bar, k, tmem);
     } else if constexpr (C::kCodes) {
         convert_role<D, KIND>(p, sm, bar, k);
@@ -680,9 +684,10 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     auto kernel = attn_tc_kernel<D, KIND>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);
     if (e != cudaSuccess) return e;
-    kernel<<<kAttnCtas, C::THREADS, C::SM_BYTES, s>>>(mk, mv, p);
+    const int ctas = attn_ctas(a, p.w, C::BN);
+    kernel<<<ctas, C::THREADS, C::SM_BYTES, s>>>(mk, mv, p);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_attn_join(a, p.w, s);
+    return e != cudaSuccess ? e : launch_attn_join(a, p.w, ctas, s);
 }
 
 template <int KIND>
