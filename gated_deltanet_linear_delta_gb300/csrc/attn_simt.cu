@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
                 const int pos = j * BN + tid;
                 long at = -1;
                 if (pos < pc.s.len) {
-                    const long pg = pool_page(w.pg, pc.n, pos);
+                    const long pg = pool_page(w.pg, pc.n, pos / w.pg.page_size);
                     if (pg >= 0) at = (pg * w.pg.Hkv + pc.h) * w.pg.page_size + pos % w.pg.page_size;
                 }
                 sm.at[tid] = at;

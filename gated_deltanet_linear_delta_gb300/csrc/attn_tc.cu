@@ -225,9 +225,10 @@ __device__ void load_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
 }
 
 // ---- products ---------------------------------------------------------------------
-// One thread issues everything, in the order S_0, S_1, O(0), S_2, O(1), ..: what it does between two
-// products is time that the tensor cores may stand still, so slots and phases are counted on, not
-// divided out, and each product signals one barrier.
+// One lane issues everything, in the order S_0, S_1, O(0), S_2, O(1), ..: what stands between two
+// products is time that the tensor cores may stand still, so the warp walks together (descriptors in
+// uniform registers), slots and phases are counted on instead of divided out, and each product signals
+// one barrier.
 template <int D, int KIND>
 __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *bar, Walk k, uint32_t tmem) {
     using C = Cfg<D, KIND>;
@@ -235,69 +236,63 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
     constexpr uint32_t ID_S = C::kCodes ? idesc_f16(128, BN, 0, 0) : idesc_bf16(128, BN, 0, 0);
     constexpr uint32_t ID_O = C::kCodes ? idesc_f16(128, D, 0, 1) : idesc_bf16(128, D, 0, 1);
     const int lane = threadIdx.x & 31;
+    const uint32_t lead = elect_one();
     const uint64_t desc_k = desc_sw128(sb, 16, 1024), desc_v = desc_sw128(sb + C::SM_V, BN * 128, 1024);  // of slots 0
     Ring<C::NK> rk;
     Ring<C::NV> rv;
     uint32_t it = 0, unit = 0;  // tiles and units begun
     auto product_s = [&](uint32_t t) -> bool {
-        if (!mbar_wait_spin(bar + C::B_FK + rk.slot, rk.phase, p.budget)) return false;
+        if (!warp_wait_spin(bar + C::B_FK + rk.slot, rk.phase, p.budget)) return false;
         tc_fence_after();
         const uint64_t d = desc_k + (uint64_t)(rk.slot * (C::SLOT >> 4));
         const uint32_t to = tmem + C::TM_S + (t & 1) * BN;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-            mma_f16_ts(to, tmem + C::TM_Q + 8 * ks, d + (uint64_t)(((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4), ID_S,
-                       ks > 0);
-        mma_commit(bar + C::B_S + (t & (C::kTurns - 1)));
+            mma_f16_ts_by(lead, to, tmem + C::TM_Q + 8 * ks, d + (uint64_t)(((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4),
+                          ID_S, ks > 0);
+        mma_commit_by(lead, bar + C::B_S + (t & (C::kTurns - 1)));
         rk.next();
         return true;
     };
     auto product_o = [&](uint32_t t, bool first) -> bool {
-        if (!mbar_wait_spin(bar + C::B_FV + rv.slot, rv.phase, p.budget) ||
-            !mbar_wait_spin(bar + C::B_P + (t & 1), (t >> 1) & 1, p.budget))
+        if (!warp_wait_spin(bar + C::B_FV + rv.slot, rv.phase, p.budget) ||
+            !warp_wait_spin(bar + C::B_P + (t & 1), (t >> 1) & 1, p.budget))
             return false;
         tc_fence_after();
         const uint64_t d = desc_v + (uint64_t)(rv.slot * (C::SLOT >> 4));
         const uint32_t a = tmem + C::TM_S + (t & 1) * BN;
 #pragma unroll
         for (int ks = 0; ks < BN / 16; ++ks)
-            mma_f16_ts(tmem + C::TM_O, a + 8 * ks, d + (uint64_t)(ks * 128), ID_O, !first || ks > 0);
-        mma_commit(bar + C::B_PV + (t & (C::kTurns - 1)));
+            mma_f16_ts_by(lead, tmem + C::TM_O, a + 8 * ks, d + (uint64_t)(ks * 128), ID_O, !first || ks > 0);
+        mma_commit_by(lead, bar + C::B_PV + (t & (C::kTurns - 1)));
         rv.next();
         return true;
     };
     bool ok = true;
     if (k.pc.left > 0) do {
         const int n = k.take();
-        if (lane == 0) {
-            ok = mbar_wait_spin(bar + C::B_Q, unit & 1, p.budget) && product_s(it);
-            for (int jj = 1; jj < n && ok; ++jj) ok = product_s(it + jj) && product_o(it + jj - 1, jj == 1);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = warp_wait_spin(bar + C::B_Q, unit & 1, p.budget) && product_s(it);
+        for (int jj = 1; jj < n && ok; ++jj) ok = product_s(it + jj) && product_o(it + jj - 1, jj == 1);
         if constexpr (!C::kCodes) {  // rows of V past the end: zeros
             const int valid = k.pc.s.len - (k.pc.off + n - 1) * BN;
-            const uint32_t slot = __shfl_sync(0xffffffffu, rv.slot, 0), phase = __shfl_sync(0xffffffffu, rv.phase, 0);
             if (ok && valid < BN) {
-                ok = warp_wait_spin(bar + C::B_FV + slot, phase, p.budget);
+                ok = warp_wait_spin(bar + C::B_FV + rv.slot, rv.phase, p.budget);
                 const int dead = (BN - valid) * 8;
                 if (ok)
                     for (int e = lane; e < dead * C::NB; e += 32)
-                        *reinterpret_cast<uint4 *>(sm + C::SM_V + slot * C::SLOT + (e / dead) * (BN * 128) + valid * 128 +
+                        *reinterpret_cast<uint4 *>(sm + C::SM_V + rv.slot * C::SLOT + (e / dead) * (BN * 128) + valid * 128 +
                                                    (e % dead) * 16) = make_uint4(0, 0, 0, 0);
                 fence_async_smem();
                 __syncwarp();
             }
         }
-        if (lane == 0 && ok) ok = product_o(it + n - 1, n == 1);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ok = ok && product_o(it + n - 1, n == 1);
         it += n;
         ++unit;
     } while (ok && walk_next<BN>(p.w, &k));
     if (!ok && lane == 0) flag_error(p.w.pg.status);
-    if (lane == 0) {  // all products done before TMEM is given back
-        mma_commit(bar + C::B_FIN);
-        mbar_wait(bar + C::B_FIN, 0, kDrainBudget);
-    }
+    mma_commit_by(lead, bar + C::B_FIN);  // all products done before TMEM is given back
+    mbar_wait(bar + C::B_FIN, 0, kDrainBudget);
     __syncwarp();
 }
 
@@ -499,9 +494,12 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
                 for (int c = 0; c < HC; ++c)
                     if (c0 + c > limit) x[c] = -INFINITY;
             }
-            float top = x[0];
+            float t4[4] = {x[0], x[1], x[2], x[3]};  // four chains
 #pragma unroll
-            for (int c = 1; c < HC; ++c) top = fmaxf(top, x[c]);
+            for (int c = 4; c < HC; c += 8)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) t4[y] = c + 4 + y < HC ? fmaxf(fmaxf(t4[y], x[c + y]), x[c + 4 + y]) : fmaxf(t4[y], x[c + y]);
+            float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
             xch[turn & 1][g][row] = top;
             failed = bar_any(bar_id, 64, late);
             if (failed) break;
@@ -528,9 +526,10 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
             }
             const float ref = m == -INFINITY ? 0.f : m;
             uint32_t pk[HC / 2];
-            float l0 = 0.f, l1 = 0.f;
+            float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < HC; c += 2) {
+                float &l0 = l4[c & 2], &l1 = l4[(c & 2) + 1];
                 const float e0 = ex2(C::kCodes ? x[c] - ref : fmaf(x[c], sc, -ref));
                 const float e1 = ex2(C::kCodes ? x[c + 1] - ref : fmaf(x[c + 1], sc, -ref));
                 if constexpr (C::kCodes) {
@@ -544,7 +543,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
                     pk[c / 2] = bf2(e0, e1);
                 }
             }
-            l += l0 + l1;
+            l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
 #pragma unroll
             for (int c = 0; c < HC / 2; c += 16) tmem_st16(tl + C::TM_S + b * BN + g * (HC / 2) + c, pk + c);
             tmem_wait_st();

@@ -4,198 +4,229 @@
 // read, its largest magnitude is reduced across the lanes that hold it, and the codes and one
 // scale are written; reading back is code times scale. (formulas: kv_pages.cuh)
 //
-// Work split: a warp takes one token and up to 4 passes over its rows (its Hkv keys, then its Hkv
-// values; a pass is as many rows as fit the warp at one 16-byte piece of the narrower side a
-// lane). Where the token lies (its sequence, kv_lens, the page) is found once per warp, and in
-// the write the rows' loads are issued before it, since they do not depend on it.
+// Work split: a CTA takes a run of tokens. Where each lies (its sequence, kv_lens, the page) is found
+// first, by a warp per token, into shared memory; then the CTA's lanes stream over the run's rows
+// (each token's Hkv keys, then its Hkv values), 4 rows' pieces in flight per lane before any is used.
+// Runs get longer with the number of tokens, up to 32: many small runs give a decode step's few tokens
+// a CTA each, long ones spread the look-up over more bytes (a token per warp read 3.4 TB/s of a long
+// session, because the look-up's three dependent reads stood before every 1 KiB).
 #include "kv_pages.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int kPasses = 4;
 
-// E consecutive elements (E a multiple of 8) as fp32
-template <int E>
-__device__ __forceinline__ void load_row(const __nv_bfloat16 *p, float *x) {
+// 16 bytes of rows as fp32
+__device__ __forceinline__ void unpack16(uint4 r, float (&x)[8]) {  // bf16
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int j = 0; j < E / 8; ++j) {
-        const uint4 r = __ldcs(reinterpret_cast<const uint4 *>(p) + j);
-        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[8 * j + 2 * i] = __uint_as_float(w[i] << 16);
-            x[8 * j + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
-template <int E>
-__device__ __forceinline__ void load_row(const float *p, float *x) {
+__device__ __forceinline__ void unpack16(uint4 r, float (&x)[4]) {  // fp32
+    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y); x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
+}
+__device__ __forceinline__ uint4 pack16(const float (&x)[8]) {
+    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < E / 4; ++j) {
-        const float4 r = __ldcs(reinterpret_cast<const float4 *>(p) + j);
-        x[4 * j] = r.x; x[4 * j + 1] = r.y; x[4 * j + 2] = r.z; x[4 * j + 3] = r.w;
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <int E>
-__device__ __forceinline__ void store_row(__nv_bfloat16 *p, const float *x) {
-#pragma unroll
-    for (int j = 0; j < E / 8; ++j) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[8 * j + 2 * i], x[8 * j + 2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        }
-        reinterpret_cast<uint4 *>(p)[j] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
-template <int E>
-__device__ __forceinline__ void store_row(float *p, const float *x) {
-#pragma unroll
-    for (int j = 0; j < E / 4; ++j)
-        reinterpret_cast<float4 *>(p)[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
-}
-// 8 or 16 code bytes
-template <int E>
-__device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t *w) {
-    if constexpr (E == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint4 pack16(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
-// KIND: GDN_BF16 / GDN_F32 here mean "as the inputs"
-template <typename TIn, int KIND, int D>
-__global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvArgs a) {
-    constexpr int E = 8, LPR = D / E, RPW = 32 / LPR;
-    constexpr bool kCodes = KIND == GDN_FP8 || KIND == GDN_INT8;
-    const KvPages &p = a.pg;
-    const int lane = threadIdx.x & 31, c = (lane % LPR) * E, sub = lane / LPR;
-    const int chunks = (2 * p.Hkv + RPW * kPasses - 1) / (RPW * kPasses);
-    const long w = (long)blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
-    const long i = w / chunks;
-    const int j0 = (int)(w % chunks) * RPW * kPasses + sub;
-    check_offsets(p);
-    if (i >= p.Ttot) return;
-
-    float x[kPasses][E];
-#pragma unroll
-    for (int r = 0; r < kPasses; ++r) {
-        const int j = j0 + r * RPW;
-        if (j < 2 * p.Hkv)
-            load_row<E>(j < p.Hkv ? (const TIn *)a.k + i * a.k_stride + (long)j * D + c
-                                  : (const TIn *)a.v + i * a.v_stride + (long)(j - p.Hkv) * D + c, x[r]);
-    }
+// Pool row (page, row in it, head 0) of packed token i, by a whole warp: -1 padding, -2 not to be touched
+__device__ __forceinline__ long token_row(const KvPages &p, long i, int page_shift) {
     const int n = seq_of_token(p, i);
     SeqInfo s;
-    if (!seq_info(p, n, &s)) return;
+    if (!seq_info(p, n, &s)) return -2;
     if (i < s.bos || i >= s.bos + s.T) {  // a token that cu gives to no sequence
         flag_error(p.status);
-        return;
+        return -2;
     }
     const int pos = s.len - s.T + (int)(i - s.bos);
-    if (pos < 0) return;  // padding
-    const long pg = pool_page(p, n, pos);
-    if (pg < 0) return;
-    const int row = pos % p.page_size;
-#pragma unroll
-    for (int r = 0; r < kPasses; ++r) {
-        const int j = j0 + r * RPW;
-        const bool live = j < 2 * p.Hkv;
-        const int h = j < p.Hkv ? j : j - p.Hkv;
-        const long at = (pg * p.Hkv + h) * p.page_size + row;
-        uint8_t *cache = (uint8_t *)(j < p.Hkv ? a.k_cache : a.v_cache);
-        if constexpr (!kCodes) {
-            if (live) store_row<E>((TIn *)cache + at * D + c, x[r]);
-        } else {
-            float amax = 0.f;
-            bool bad = false;
-            if (live) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    amax = fmaxf(amax, fabsf(x[r][e]));
-                    bad |= !(fabsf(x[r][e]) <= 3.4028234e38f);
-                }
-            }
-            if (bad) amax = __int_as_float(0x7f800000);
-#pragma unroll
-            for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            if (!live) continue;
-            const float sc = KIND == GDN_FP8 ? scale_e4m3(amax) : scale_int8(amax);
-            uint32_t code[E / 4];
-#pragma unroll
-            for (int e = 0; e < E / 4; ++e)
-                code[e] = sc != sc ? 0u : KIND == GDN_FP8 ? codes4_e4m3(x[r] + 4 * e, 1.f / sc) : codes4_int8(x[r] + 4 * e, sc);
-            store_codes<E>(cache + at * D + c, code);
-            if (c == 0) (j < p.Hkv ? a.k_scale : a.v_scale)[at] = sc;
-        }
-    }
+    if (pos < 0) return -1;
+    const long pg = pool_page(p, n, pos >> page_shift);
+    return pg < 0 ? -3 : ((pg * p.Hkv) << page_shift) + (pos & (p.page_size - 1));
 }
 
-template <typename TOut, int KIND, int D>
-__global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvArgs a) {
+constexpr int kMaxRun = 32;
+
+// KIND: GDN_FP8, GDN_INT8, or anything else for a cache of the rows' type
+template <bool WRITE, typename T, int KIND, int D>
+__global__ void __launch_bounds__(kKvThreads, 4) kv_copy_kernel(const KvArgs a, int run, int page_shift) {
     constexpr bool kCodes = KIND == GDN_FP8 || KIND == GDN_INT8;
-    constexpr int E = kCodes ? 16 : 8, LPR = D / E, RPW = 32 / LPR;
+    // A lane has 16 elements of a row, as pieces whose rows' side is 16 bytes: consecutive lanes' pieces are
+    // consecutive, so that both sides' accesses are whole lines.
+    constexpr int E = 16, PE = 16 / (int)sizeof(T), NP = E / PE, LPR = D / E, ROWS = kKvThreads / LPR;
+    constexpr int kFlight = WRITE && kCodes ? 2 : 4;  // rows in flight per lane
+    __shared__ long where[kMaxRun];
     const KvPages &p = a.pg;
-    const int lane = threadIdx.x & 31, c = (lane % LPR) * E, sub = lane / LPR;
-    const int chunks = (2 * p.Hkv + RPW * kPasses - 1) / (RPW * kPasses);
-    const long w = (long)blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5);
-    const long i = w / chunks;
-    const int j0 = (int)(w % chunks) * RPW * kPasses + sub;
+    const int tid = threadIdx.x, lane = tid & 31, c = (tid % LPR) * PE, sub = tid / LPR;
+    const long first = (long)blockIdx.x * run;
+    const int tokens = (int)min((long)run, p.Ttot - first), heads = 2 * p.Hkv;
     check_offsets(p);
-    if (i >= p.Ttot) return;
-    const int n = seq_of_token(p, i);
-    SeqInfo s;
-    if (!seq_info(p, n, &s)) return;
-    if (i < s.bos || i >= s.bos + s.T) {
-        flag_error(p.status);
-        return;
+    // This thread's rows, a pass at a time: whole tokens' rows side by side if a pass holds some, else a token's
+    // rows in several passes.
+    struct At {
+        int t, j;
+    };
+    const int per_pass = ROWS / heads;
+    At at0{per_pass ? sub / heads : 0, per_pass ? sub % heads : sub};
+    if (per_pass && at0.t >= per_pass) at0.t = kMaxRun;  // no row of its own
+    auto next = [&](At &r) {
+        if (per_pass) {
+            r.t += per_pass;
+        } else if ((r.j += ROWS) >= heads) {
+            r.j = sub;
+            ++r.t;
+        }
+    };
+    const int passes = per_pass ? (tokens + per_pass - 1) / per_pass : tokens * ((heads + ROWS - 1) / ROWS);
+    auto live = [&](const At &r) { return r.t < tokens && r.j < heads; };
+    auto outside = [&](const At &r) -> T * {  // the row in k or v
+        const bool is_v = r.j >= p.Hkv;
+        return (is_v ? (T *)a.v + (first + r.t) * a.v_stride : (T *)a.k + (first + r.t) * a.k_stride) +
+               (long)(is_v ? r.j - p.Hkv : r.j) * D + c;
+    };
+    uint4 x[kFlight][NP];
+    auto load_rows = [&](At r) {  // (a write's rows do not depend on where they go)
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f, next(r)) {
+            if (!live(r)) continue;
+            const T *src = outside(r);
+#pragma unroll
+            for (int g = 0; g < NP; ++g) x[f][g] = __ldcs(reinterpret_cast<const uint4 *>(src + g * LPR * PE));
+        }
+    };
+    if (WRITE) load_rows(at0);
+    for (int t = tid >> 5; t < tokens; t += kKvThreads / 32) {
+        const long w = token_row(p, first + t, page_shift);
+        if (lane == 0) where[t] = w;
     }
-    const int pos = s.len - s.T + (int)(i - s.bos);
-    const long pg = pos < 0 ? -1 : pool_page(p, n, pos);
-    const int row = pos < 0 ? 0 : pos % p.page_size;
-    float x[kPasses][E];
+    __syncthreads();
+    At r0 = at0;
+    for (int pass = 0; pass < passes; pass += kFlight) {
+        if (WRITE && pass) load_rows(r0);
+        At r = r0;
+        if constexpr (WRITE) {
 #pragma unroll
-    for (int r = 0; r < kPasses; ++r) {
-        const int j = j0 + r * RPW;
+            for (int f = 0; f < kFlight; ++f, next(r)) {
+                const long w = live(r) ? where[r.t] : -2;
+                const bool is_v = r.j >= p.Hkv;
+                const long at = w + ((long)(is_v ? r.j - p.Hkv : r.j) << page_shift);
+                uint8_t *cache = (uint8_t *)(is_v ? a.v_cache : a.k_cache);
+                if constexpr (!kCodes) {
+                    if (w < 0) continue;
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[r][e] = 0.f;  // padding reads as zeros
-        if (j >= 2 * p.Hkv || pg < 0) continue;
-        const int h = j < p.Hkv ? j : j - p.Hkv;
-        const long at = (pg * p.Hkv + h) * p.page_size + row;
-        const uint8_t *cache = (const uint8_t *)(j < p.Hkv ? a.k_cache : a.v_cache);
-        if constexpr (!kCodes) {
-            load_row<E>((const TOut *)cache + at * D + c, x[r]);
+                    for (int g = 0; g < NP; ++g) *reinterpret_cast<uint4 *>((T *)cache + at * D + c + g * LPR * PE) = x[f][g];
+                } else {
+                    float amax = 0.f, y[NP][PE];
+                    if (w >= 0) {
+                        bool bad = false;
+#pragma unroll
+                        for (int g = 0; g < NP; ++g) {
+                            unpack16(x[f][g], y[g]);
+#pragma unroll
+                            for (int e = 0; e < PE; ++e) {
+                                amax = fmaxf(amax, fabsf(y[g][e]));
+                                bad |= !(fabsf(y[g][e]) <= 3.4028234e38f);
+                            }
+                        }
+                        if (bad) amax = __int_as_float(0x7f800000);
+                    }
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    if (w < 0) continue;
+                    const float sc = KIND == GDN_FP8 ? scale_e4m3(amax) : scale_int8(amax);
+                    const float inv = __frcp_rn(sc);  // (of a power of two: exact)
+#pragma unroll
+                    for (int g = 0; g < NP; ++g) {
+                        uint32_t code[PE / 4];
+#pragma unroll
+                        for (int e = 0; e < PE / 4; ++e)
+                            code[e] = sc != sc ? 0u : KIND == GDN_FP8 ? codes4_e4m3(y[g] + 4 * e, inv) : codes4_int8(y[g] + 4 * e, sc, inv);
+                        uint8_t *dst = cache + at * D + c + g * LPR * PE;
+                        if constexpr (PE == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
+                        else *reinterpret_cast<uint32_t *>(dst) = code[0];
+                    }
+                    if (c == 0) (is_v ? a.v_scale : a.k_scale)[at] = sc;
+                }
+            }
         } else {
-            const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(cache + at * D + c));
-            const float sc = (j < p.Hkv ? a.k_scale : a.v_scale)[at];
-            const uint32_t code[4] = {q.x, q.y, q.z, q.w};
+            uint32_t code[kFlight][E / 4];
+            float sc[kFlight];
+            long w[kFlight];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (KIND == GDN_FP8) decode4_e4m3(code[e], x[r] + 4 * e);
-                else decode4_int8(code[e], x[r] + 4 * e);
+            for (int f = 0; f < kFlight; ++f, next(r)) {
+                w[f] = live(r) ? where[r.t] : -2;
+                if (w[f] < 0) continue;
+                const bool is_v = r.j >= p.Hkv;
+                const long at = w[f] + ((long)(is_v ? r.j - p.Hkv : r.j) << page_shift);
+                const uint8_t *cache = (const uint8_t *)(is_v ? a.v_cache : a.k_cache);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) x[r][4 * e + m] *= sc;
+                for (int g = 0; g < NP; ++g) {
+                    if constexpr (!kCodes) {
+                        x[f][g] = __ldcs(reinterpret_cast<const uint4 *>((const T *)cache + at * D + c + g * LPR * PE));
+                    } else if constexpr (PE == 8) {
+                        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(cache + at * D + c + g * LPR * PE));
+                        code[f][2 * g] = v.x;
+                        code[f][2 * g + 1] = v.y;
+                    } else {
+                        code[f][g] = __ldcs(reinterpret_cast<const uint32_t *>(cache + at * D + c + g * LPR * PE));
+                    }
+                }
+                if constexpr (kCodes) sc[f] = __ldcs((is_v ? a.v_scale : a.k_scale) + at);
+            }
+            r = r0;
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f, next(r)) {
+                if (w[f] == -2) continue;
+                T *dst = outside(r);
+#pragma unroll
+                for (int g = 0; g < NP; ++g) {
+                    uint4 out = make_uint4(0, 0, 0, 0);  // padding, and pages outside of the pool
+                    if (w[f] >= 0) {
+                        if constexpr (kCodes) {
+                            float y[PE];
+#pragma unroll
+                            for (int e = 0; e < PE / 4; ++e) {
+                                if (KIND == GDN_FP8) decode4_e4m3(code[f][g * (PE / 4) + e], y + 4 * e);
+                                else decode4_int8(code[f][g * (PE / 4) + e], y + 4 * e);
+                            }
+#pragma unroll
+                            for (int e = 0; e < PE; ++e) y[e] *= sc[f];
+                            out = pack16(y);
+                        } else {
+                            out = x[f][g];
+                        }
+                    }
+                    __stcs(reinterpret_cast<uint4 *>(dst + g * LPR * PE), out);
+                }
             }
         }
-    }
 #pragma unroll
-    for (int r = 0; r < kPasses; ++r) {
-        const int j = j0 + r * RPW;
-        if (j < 2 * p.Hkv)
-            store_row<E>(j < p.Hkv ? (TOut *)a.k + i * a.k_stride + (long)j * D + c
-                                   : (TOut *)a.v + i * a.v_stride + (long)(j - p.Hkv) * D + c, x[r]);
+        for (int f = 0; f < kFlight; ++f) next(r0);
     }
 }
 
 template <bool WRITE, typename T, int KIND, int D>
 cudaError_t launch_kv(const KvArgs &a, cudaStream_t s) {
-    constexpr int E = !WRITE && (KIND == GDN_FP8 || KIND == GDN_INT8) ? 16 : 8, RPW = 32 / (D / E);
-    const long chunks = (2L * a.pg.Hkv + RPW * kPasses - 1) / (RPW * kPasses);
-    const long blocks = (a.pg.Ttot * chunks + kKvThreads / 32 - 1) / (kKvThreads / 32);
+    // a CTA per token until there are 8 per SM, then runs of up to 32
+    const long per = a.pg.Ttot / (152 * 8);
+    const int run = (int)(per < 1 ? 1 : per < kMaxRun ? per : kMaxRun);
+    const long blocks = (a.pg.Ttot + run - 1) / run;
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
-    if (WRITE) kv_write_kernel<T, KIND, D><<<(unsigned)blocks, kKvThreads, 0, s>>>(a);
-    else kv_read_kernel<T, KIND, D><<<(unsigned)blocks, kKvThreads, 0, s>>>(a);
+    int shift = 0;
+    while ((1 << shift) < a.pg.page_size) ++shift;
+    kv_copy_kernel<WRITE, T, KIND, D><<<(unsigned)blocks, kKvThreads, 0, s>>>(a, run, shift);
     return cudaGetLastError();
 }
 

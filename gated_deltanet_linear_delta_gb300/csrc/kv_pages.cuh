@@ -49,7 +49,7 @@ __device__ __forceinline__ bool seq_info(const KvPages &p, int n, SeqInfo *s) {
 // The sequence of packed token i, found by a whole warp: the last n with cu[n] <= i (32 probes a
 // step, so 2 dependent reads for up to 1024 sequences).
 __device__ __forceinline__ int seq_of_token(const KvPages &p, long i) {
-    if (p.cu == nullptr) return (int)(i / p.T);
+    if (p.cu == nullptr) return (int)((uint32_t)i / (uint32_t)p.T);  // (fewer than 2^31 tokens)
     const int lane = threadIdx.x & 31;
     int lo = 0, n = p.B;  // the answer lies in [lo, lo + n)
     while (n > 1) {
@@ -75,9 +75,9 @@ __device__ __forceinline__ void check_offsets(const KvPages &p) {
     }
 }
 
-// Page of a position of sequence n, or -1 (flagged) when the table names no page.
-__device__ __forceinline__ long pool_page(const KvPages &p, int n, int pos) {
-    const int pg = p.table[(long)n * p.max_pages + pos / p.page_size];
+// The index-th page of sequence n, or -1 (flagged) when the table names none of the pool's.
+__device__ __forceinline__ long pool_page(const KvPages &p, int n, int index) {
+    const int pg = p.table[(long)n * p.max_pages + index];
     if (pg < 0 || pg >= p.num_pages) {
         flag_error(p.status);
         return -1;
@@ -104,11 +104,25 @@ __device__ __forceinline__ uint32_t codes4_e4m3(const float *x, float inv) {  //
     const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
     return (uint32_t)a | ((uint32_t)b << 16);
 }
-__device__ __forceinline__ uint32_t codes4_int8(const float *x, float s) {
-    uint32_t r = 0;
+// The code is the quotient x / s, correctly rounded to fp32, rounded to an integer. x (1 / s) is within
+// 2^-16 of it, so only where such a product comes that close to the middle between two integers are
+// the four divided. (Adding 1.5 * 2^23 rounds to an integer, and leaves it in the low bits.)
+__device__ __forceinline__ uint32_t codes4_int8(const float *x, float s, float inv) {
+    constexpr float kRound = 12582912.f;
+    float y[4], off = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r |= ((uint32_t)__float2int_rn(__fdiv_rn(x[j], s)) & 0xffu) << (8 * j);
-    return r;
+    for (int j = 0; j < 4; ++j) {
+        const float t = x[j] * inv;
+        y[j] = __fadd_rn(t, kRound);
+        off = fmaxf(off, fabsf(t - __fsub_rn(y[j], kRound)));
+    }
+    if (off > 0.4999f) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = __fadd_rn(__fdiv_rn(x[j], s), kRound);
+    }
+    const uint32_t lo = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
 }
 __device__ __forceinline__ void decode4_e4m3(uint32_t c, float *x) {
 #pragma unroll
