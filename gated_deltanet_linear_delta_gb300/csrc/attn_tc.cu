@@ -16,11 +16,15 @@
 //
 // Layout. TMEM holds O (D columns), two S buffers (P_j overlays S_j) and Q as the 16-bit A operand,
 // 512 columns in all for D = 256; with Q in TMEM, shared memory is two rings of K and V tiles, and the
-// S products read 64 bytes of it a cycle instead of 192. S_{j+1} is issued before O += P_j V_j, so
-// the tensor cores work on it while the softmax of tile j runs.
-// Warps: 0..7 softmax (two threads per row, half of the columns each), 8 and 9 load K and V, 10
-// issues the products; with an 8-bit cache 11..14 convert tiles. All CTAs are persistent over their piece of
-// the work, and every wait has a limit, after which the CTA flags the status word and leaves.
+// S products read 64 bytes of it a cycle instead of 192.
+//
+// Warps, in groups of four: two take the softmax, a thread per row and half of a tile's columns, which
+// meet once per tile for the row's maximum; one brings the rows' Q into TMEM and takes finished rows
+// out, beside the softmax of the neighbouring units; one has a warp each for the loads of K and V and
+// for the products; with an 8-bit cache one converts K tiles and one V tiles. The products run S_0, S_1,
+// O(0), S_2, O(1), .. across units, so that the tensor cores work on S_{j+1} while the softmax of tile j
+// runs. All CTAs are persistent over their piece of the work, and every wait has a limit, after which
+// the CTA flags the status word and leaves.
 //
 // 8-bit caches. Codes are exact in fp16, so K and V tiles hold codes converted to fp16 (bf16 would
 // take four times the conversion instructions for e4m3), Q is rounded to fp16 after an exact
@@ -41,13 +45,13 @@ namespace {
 
 using namespace tc;
 
-constexpr int kSoftWarps = 8, kLoadWarp = 8 /* K, then V */, kMmaWarp = 10, kConvWarp0 = 11, kConvWarps = 4;
+constexpr int kGroup = 4, kRowWarp0 = 8, kLoadWarp = 12 /* K, then V */, kMmaWarp = 14, kPadWarp = 15,
+              kConvWarp0 = 16 /* K, then V */;
 
 template <int D, int KIND>
 struct Cfg {
     static constexpr bool kCodes = KIND == GDN_FP8 || KIND == GDN_INT8;
     static constexpr int BN = D == 256 ? 64 : 128;
-    static constexpr int HC = BN / 2;                      // columns of S per softmax thread
     static constexpr int NB = D / 64;                      // 128-byte wide blocks of a tile
     static constexpr uint32_t SLOT = BN * D * 2;           // a 16-bit K or V tile
     static constexpr uint32_t RAW_K = BN * D + 2 * BN * 4;  // a K tile's codes, and K and V scales
@@ -55,20 +59,27 @@ struct Cfg {
     // ring slots: 16-bit tiles of K and of V, and with an 8-bit cache their codes
     static constexpr int NK = kCodes ? 2 : (D == 64 ? 6 : 3), NV = NK;
     static constexpr int NR = kCodes ? (D == 64 ? 6 : 2) : 0;
+    // Scores and 32-bit columns of Q that a thread has at hand at a time. With the converting warps there are 80
+    // registers a thread, and the scores are read twice, for the maximum and for the probabilities; else there are
+    // 128, and one reading serves both.
+    static constexpr int CW = kCodes ? 16 : BN / 2, QC = kCodes ? 16 : 64;
     static constexpr int COLS = 4;                         // column scales, a buffer per tile
-    static constexpr int THREADS = 32 * (kCodes ? kConvWarp0 + kConvWarps : kConvWarp0);
+    static constexpr int THREADS = 32 * (kCodes ? kConvWarp0 + 2 * kGroup : kConvWarp0);
     static constexpr uint32_t TM_O = 0, TM_S = D == 256 ? 256 : 128, TM_Q = 384;
     // shared memory, from a 1 KiB aligned base
     static constexpr uint32_t SM_V = NK * SLOT, SM_RK = SM_V + NV * SLOT, SM_RV = SM_RK + NR * RAW_K;
     static constexpr uint32_t SM_COL = SM_RV + NR * RAW_V;                   // [COLS][3][BN] a, b, 1 / vs
-    static constexpr uint32_t SM_X = SM_COL + (kCodes ? COLS * 3 * BN * 4 : 0);  // [2][2][128] row exchange
-    static constexpr uint32_t SM_BAR = SM_X + 2 * 2 * 128 * 4;
+    static constexpr uint32_t SM_X = SM_COL + (kCodes ? COLS * 3 * BN * 4 : 0);  // [2][2][128] maxima of a tile's halves
+    static constexpr uint32_t SM_STAT = SM_X + 2 * 2 * 128 * 4;              // [2][2][128] a unit's m, l by half
+    static constexpr uint32_t SM_RS = SM_STAT + 2 * 2 * 128 * 8;             // [4][128] Q's row scales (8-bit caches)
+    static constexpr uint32_t SM_BAR = SM_RS + 4 * 128 * 4;
     // S_j and O += P_j V_j done, by tile modulo 8: they also say that K_j's and V_j's slots are free. (Whoever fills
     // a slot looks back at most 6 tiles, so a barrier is never two phases ahead of its reader.)
     static constexpr int kTurns = 8;
     static constexpr int B_FK = 0, B_FV = B_FK + NK, B_RK = B_FV + NV, B_RV = B_RK + NR, B_REK = B_RV + NR,
                          B_REV = B_REK + NR, B_COL = B_REV + NR, B_S = B_COL + COLS, B_PV = B_S + kTurns,
-                         B_P = B_PV + kTurns, B_Q = B_P + 2, B_FIN = B_Q + 1, B_COUNT = B_FIN + 1;
+                         B_P = B_PV + kTurns, B_ST = B_P + 2, B_SF = B_ST + 2,
+                         B_Q = B_SF + 2, B_OF = B_Q + 1, B_FIN = B_OF + 1, B_COUNT = B_FIN + 1;
     static constexpr uint32_t SM_INFO = SM_BAR + B_COUNT * 8;                // [2][NR] valid rows, page mask
     static constexpr uint32_t SM_TMEM = SM_INFO + (NR ? 2 * NR : 1) * 8;
     static constexpr uint32_t SM_PLAN = (SM_TMEM + 8 + 15) & ~15u;
@@ -225,10 +236,10 @@ __device__ void load_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
 }
 
 // ---- products ---------------------------------------------------------------------
-// One lane issues everything, in the order S_0, S_1, O(0), S_2, O(1), ..: what stands between two
-// products is time that the tensor cores may stand still, so the warp walks together (descriptors in
-// uniform registers), slots and phases are counted on instead of divided out, and each product signals
-// one barrier.
+// One lane issues everything, in the order S_0, S_1, O(0), S_2, O(1), .. over all units: what stands
+// between two products is time that the tensor cores may stand still, so the warp walks together
+// (descriptors in uniform registers), slots and phases are counted on instead of divided out, and each
+// product signals one barrier.
 template <int D, int KIND>
 __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *bar, Walk k, uint32_t tmem) {
     using C = Cfg<D, KIND>;
@@ -240,9 +251,10 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
     const uint64_t desc_k = desc_sw128(sb, 16, 1024), desc_v = desc_sw128(sb + C::SM_V, BN * 128, 1024);  // of slots 0
     Ring<C::NK> rk;
     Ring<C::NV> rv;
-    uint32_t it = 0, unit = 0;  // tiles and units begun
-    auto product_s = [&](uint32_t t) -> bool {
-        if (!warp_wait_spin(bar + C::B_FK + rk.slot, rk.phase, p.budget)) return false;
+    uint32_t t = 0, unit = 0, o_free = 0;  // tiles whose S is issued, units begun, phase of B_OF
+    // The waits for tiles come before the one for P, which is the last to be met: what follows it is issued at once.
+    auto k_ready = [&]() -> bool { return warp_wait_spin(bar + C::B_FK + rk.slot, rk.phase, p.budget); };
+    auto product_s = [&]() {
         tc_fence_after();
         const uint64_t d = desc_k + (uint64_t)(rk.slot * (C::SLOT >> 4));
         const uint32_t to = tmem + C::TM_S + (t & 1) * BN;
@@ -252,44 +264,56 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
                           ID_S, ks > 0);
         mma_commit_by(lead, bar + C::B_S + (t & (C::kTurns - 1)));
         rk.next();
+        ++t;
+    };
+    // V of tile o, `first` of its unit, with `valid` positions before the end, ready to be multiplied
+    auto v_ready = [&](uint32_t o, bool first, int valid) -> bool {
+        if (!warp_wait_spin(bar + C::B_FV + rv.slot, rv.phase, p.budget)) return false;
+        if (!C::kCodes && valid < BN) {  // rows of V past the end: zeros
+            const int dead = (BN - valid) * 8;
+            for (int e = lane; e < dead * C::NB; e += 32)
+                *reinterpret_cast<uint4 *>(sm + C::SM_V + rv.slot * C::SLOT + (e / dead) * (BN * 128) + valid * 128 +
+                                           (e % dead) * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_smem();
+            __syncwarp();
+        }
+        if (first && o > 0) {  // the unit before has been taken out of O
+            if (!warp_wait_spin(bar + C::B_OF, o_free, p.budget)) return false;
+            o_free ^= 1;
+        }
         return true;
     };
-    auto product_o = [&](uint32_t t, bool first) -> bool {
-        if (!warp_wait_spin(bar + C::B_FV + rv.slot, rv.phase, p.budget) ||
-            !warp_wait_spin(bar + C::B_P + (t & 1), (t >> 1) & 1, p.budget))
-            return false;
+    auto product_o = [&](uint32_t o, bool first) -> bool {
+        if (!warp_wait_spin(bar + C::B_P + (o & 1), (o >> 1) & 1, p.budget)) return false;
         tc_fence_after();
         const uint64_t d = desc_v + (uint64_t)(rv.slot * (C::SLOT >> 4));
-        const uint32_t a = tmem + C::TM_S + (t & 1) * BN;
+        const uint32_t a = tmem + C::TM_S + (o & 1) * BN;
 #pragma unroll
         for (int ks = 0; ks < BN / 16; ++ks)
-            mma_f16_ts_by(lead, tmem + C::TM_O, a + 8 * ks, d + (uint64_t)(ks * 128), ID_O, !first || ks > 0);
-        mma_commit_by(lead, bar + C::B_PV + (t & (C::kTurns - 1)));
+            mma_f16_ts_by(lead, tmem + C::TM_O, a + (ks < BN / 32 ? 8 * ks : BN / 2 + 8 * (ks - BN / 32)),
+                          d + (uint64_t)(ks * 128), ID_O, !first || ks > 0);
+        mma_commit_by(lead, bar + C::B_PV + (o & (C::kTurns - 1)));
         rv.next();
         return true;
     };
-    bool ok = true;
-    if (k.pc.left > 0) do {
-        const int n = k.take();
-        ok = warp_wait_spin(bar + C::B_Q, unit & 1, p.budget) && product_s(it);
-        for (int jj = 1; jj < n && ok; ++jj) ok = product_s(it + jj) && product_o(it + jj - 1, jj == 1);
-        if constexpr (!C::kCodes) {  // rows of V past the end: zeros
-            const int valid = k.pc.s.len - (k.pc.off + n - 1) * BN;
-            if (ok && valid < BN) {
-                ok = warp_wait_spin(bar + C::B_FV + rv.slot, rv.phase, p.budget);
-                const int dead = (BN - valid) * 8;
-                if (ok)
-                    for (int e = lane; e < dead * C::NB; e += 32)
-                        *reinterpret_cast<uint4 *>(sm + C::SM_V + rv.slot * C::SLOT + (e / dead) * (BN * 128) + valid * 128 +
-                                                   (e % dead) * 16) = make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-                __syncwarp();
+    bool ok = true, prev_first = false;
+    int prev_valid = BN;
+    if (k.pc.left > 0) {
+        do {
+            const int n = k.take(), left = k.pc.s.len - k.pc.off * BN;
+            ok = warp_wait_spin(bar + C::B_Q, unit & 1, p.budget) && (t > 0 || k_ready());
+            ++unit;
+            for (int jj = 0; jj < n && ok; ++jj) {
+                const bool more = jj + 1 < n || k.pc.left > n;  // another tile follows in the piece
+                product_s();
+                if (t > 1) ok = v_ready(t - 2, prev_first, prev_valid) && product_o(t - 2, prev_first);
+                if (ok && more) ok = k_ready();
+                prev_first = jj == 0;
+                prev_valid = left - jj * BN;
             }
-        }
-        ok = ok && product_o(it + n - 1, n == 1);
-        it += n;
-        ++unit;
-    } while (ok && walk_next<BN>(p.w, &k));
+        } while (ok && walk_next<BN>(p.w, &k));
+        ok = ok && v_ready(t - 1, prev_first, prev_valid) && product_o(t - 1, prev_first);
+    }
     if (!ok && lane == 0) flag_error(p.w.pg.status);
     mma_commit_by(lead, bar + C::B_FIN);  // all products done before TMEM is given back
     mbar_wait(bar + C::B_FIN, 0, kDrainBudget);
@@ -304,7 +328,7 @@ template <int D, int KIND>
 __device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst0, uint8_t *dst1, int row, int valid,
                                              int pages, int box_shift) {
     using C = Cfg<D, KIND>;
-    constexpr int STEPS = C::BN * D / 16 / (kConvWarps * 32), ROWS = kConvWarps * 32 / (D / 16);
+    constexpr int STEPS = C::BN * D / 16 / (kGroup * 32), ROWS = kGroup * 32 / (D / 16);
     static_assert(ROWS % 8 == 0 && STEPS % 4 == 0, "the swizzle must not change between steps");
 #pragma unroll
     for (int st = 0; st < STEPS; st += 4) {
@@ -331,268 +355,337 @@ __device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst0, 
     }
 }
 
-template <int D, int KIND>
+template <int D, int KIND, bool IS_V>
 __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k) {
     using C = Cfg<D, KIND>;
-    constexpr int BN = C::BN;
-    const int tid = threadIdx.x - kConvWarp0 * 32, lane = tid & 31;
+    constexpr int BN = C::BN, N = IS_V ? C::NV : C::NK;
+    const int tid = threadIdx.x & (kGroup * 32 - 1), lane = tid & 31;
     const int box = min(p.w.pg.page_size, BN), box_shift = 31 - __clz(box), all_pages = (1 << (BN / box)) - 1;
     const int e8 = tid & 7, g8 = tid >> 3, row0 = 2 * (g8 / C::NB) + (e8 >> 2);
     const int blk = C::NB == 1 ? 0 : (g8 % C::NB) ^ (e8 >> 2), c = e8 & 3;
+    const uint8_t *src = sm + (IS_V ? C::SM_RV : C::SM_RK);
     const uint32_t src0 = row0 * D + blk * 64 + c * 16;
-    const uint32_t dst0 = blk * (BN * 128) + swz(row0, 2 * c), dst1 = blk * (BN * 128) + swz(row0, 2 * c + 1);
-    Ring<C::NK> rk;
-    Ring<C::NV> rv;
-    Ring<C::NR> rr[2];
-    uint32_t t[2] = {0, 0};  // tiles converted
+    uint8_t *dst = sm + (IS_V ? C::SM_V : 0) + blk * (BN * 128);
+    const uint32_t dst0 = swz(row0, 2 * c), dst1 = swz(row0, 2 * c + 1);
+    Ring<N> ring;
+    Ring<C::NR> raw;
+    uint32_t t = 0;  // tiles converted
     bool ok = true;
-    auto convert = [&](auto is_v) -> bool {
-        constexpr bool IS_V = decltype(is_v)::value;
-        constexpr int N = IS_V ? C::NV : C::NK;
-        const uint32_t r = rr[IS_V].slot, s = IS_V ? rv.slot : rk.slot;
-        bool got = mbar_wait_spin(bar + (IS_V ? C::B_RV : C::B_RK) + r, rr[IS_V].phase, p.budget);
-        if (t[IS_V] >= N) got = got && product_done<D, KIND>(bar, IS_V ? C::B_PV : C::B_S, t[IS_V] - N, p.budget);
-        if (!__all_sync(0xffffffffu, got)) return false;
-        const uint8_t *raw = sm + (IS_V ? C::SM_RV + r * C::RAW_V : C::SM_RK + r * C::RAW_K);
-        uint8_t *dst = sm + (IS_V ? C::SM_V : 0) + s * C::SLOT;
-        const int2 info = reinterpret_cast<const int2 *>(sm + C::SM_INFO)[(IS_V ? C::NR : 0) + r];
-        // A tile that is whole takes no checks; rows past the end and bad pages become zeros.
-        const bool whole = info.x == BN && info.y == all_pages;
-        convert_tile<D, KIND>(raw + src0, dst + dst0, dst + dst1, row0, whole ? -1 : info.x, info.y, box_shift);
-        if constexpr (!IS_V) {
-            const uint32_t cb = t[0] % C::COLS;
-            if (tid < BN) {
-                const float *sc = reinterpret_cast<const float *>(raw + BN * D);
-                const bool live = tid < info.x && ((info.y >> (tid >> box_shift)) & 1);
-                const float ks = live ? sc[tid] : 0.f;
-                float vs = live ? sc[BN + tid] : kMinKvScale;
-                if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
-                float *col = reinterpret_cast<float *>(sm + C::SM_COL) + cb * 3 * BN;
-                col[tid] = ks * p.scale2;
-                col[BN + tid] = lg2(vs);
-                col[2 * BN + tid] = vs == vs ? rcp(vs) : 0.f;  // a NaN enters by b, and not where it is masked
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar + C::B_COL + cb);
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(bar + (IS_V ? C::B_FV : C::B_FK) + s);
-            mbar_arrive(bar + (IS_V ? C::B_REV : C::B_REK) + r);
-        }
-        if (IS_V) rv.next();
-        else rk.next();
-        rr[IS_V].next();
-        ++t[IS_V];
-        return true;
-    };
     if (k.pc.left > 0) do {
         const int n = k.take();
-        ok = convert(std::false_type{});
-        for (int jj = 1; jj < n && ok; ++jj) ok = convert(std::false_type{}) && convert(std::true_type{});
-        ok = ok && convert(std::true_type{});
+        for (int jj = 0; jj < n; ++jj, ++t) {
+            bool got = mbar_wait_spin(bar + (IS_V ? C::B_RV : C::B_RK) + raw.slot, raw.phase, p.budget);
+            if (t >= N) got = got && product_done<D, KIND>(bar, IS_V ? C::B_PV : C::B_S, t - N, p.budget);
+            ok = __all_sync(0xffffffffu, got);
+            if (!ok) break;
+            const uint8_t *from = src + raw.slot * (IS_V ? C::RAW_V : C::RAW_K);
+            const int2 info = reinterpret_cast<const int2 *>(sm + C::SM_INFO)[(IS_V ? C::NR : 0) + raw.slot];
+            if constexpr (!IS_V) {
+                const uint32_t cb = t % C::COLS;
+                if (tid < BN) {
+                    const float *sc = reinterpret_cast<const float *>(from + BN * D);
+                    const bool live = tid < info.x && ((info.y >> (tid >> box_shift)) & 1);
+                    const float ks = live ? sc[tid] : 0.f;
+                    float vs = live ? sc[BN + tid] : kMinKvScale;
+                    if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
+                    float *col = reinterpret_cast<float *>(sm + C::SM_COL) + cb * 3 * BN;
+                    col[tid] = ks * p.scale2;
+                    col[BN + tid] = lg2(vs);
+                    col[2 * BN + tid] = vs == vs ? rcp(vs) : 0.f;  // a NaN enters by b, and not where it is masked
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + C::B_COL + cb);
+            }
+            // A tile that is whole takes no checks; rows past the end and bad pages become zeros.
+            const bool whole = info.x == BN && info.y == all_pages;
+            uint8_t *to = dst + ring.slot * C::SLOT;
+            convert_tile<D, KIND>(from + src0, to + dst0, to + dst1, row0, whole ? -1 : info.x, info.y, box_shift);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar + (IS_V ? C::B_FV : C::B_FK) + ring.slot);
+                mbar_arrive(bar + (IS_V ? C::B_REV : C::B_REK) + raw.slot);
+            }
+            ring.next();
+            raw.next();
+        }
     } while (ok && walk_next<BN>(p.w, &k));
     if (!ok && lane == 0) flag_error(p.w.pg.status);
 }
 
-// ---- softmax, rescaling, output -----------------------------------------------------------
+// ---- softmax ----------------------------------------------------------------------------
 template <int D, int KIND>
 __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, uint32_t tmem) {
     using C = Cfg<D, KIND>;
-    constexpr int BN = C::BN, HC = C::HC;
+    constexpr int BN = C::BN, HC = BN / 2, CW = C::CW;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = warp >> 2, pair = warp & 3, row = pair * 32 + lane;
-    const int bar_id = 1 + pair;
-    const uint32_t tl = tmem + ((uint32_t)(pair * 32) << 16);  // this warp's TMEM lanes
-    float(*xch)[2][128] = reinterpret_cast<float(*)[2][128]>(sm + C::SM_X);
-    uint32_t it = 0, turn = 0;
-    // A wait that ran out is shared with the row's other warp at the next exchange, so that both leave there
-    // (`failed` is the same for all their threads, `late` is a thread's own).
-    bool failed = false, late = false;
+    const int half = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+    const int bar_id = 1 + quarter;                               // of the two warps that share these rows
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);  // this warp's TMEM lanes
+    float *xch = reinterpret_cast<float *>(sm + C::SM_X) + row;
+    float2 *stat = reinterpret_cast<float2 *>(sm + C::SM_STAT) + half * 128 + row;
+    const float *rsq = reinterpret_cast<const float *>(sm + C::SM_RS) + row;
+    uint32_t t = 0, unit = 0;
+    // A wait that ran out (`late`, a thread's own) is shared with the rows' other warp at the next meeting, so that
+    // both leave there (`ok` is the same for all their threads).
+    bool ok = true, late = false;
     if (k.pc.left > 0) do {
         const int n = k.take(), t0 = k.pc.i * p.w.TPT;
         const int rows = min(p.w.TPT, k.pc.s.T - t0) * p.w.G;
-        const bool live_warp = pair * 32 < rows;
-        const int t = t0 + row / p.w.G, h = k.pc.h * p.w.G + row % p.w.G;
-        const int limit = row < rows ? k.pc.s.len - k.pc.s.T + t : -1;  // last position the row sees
-        const int sure = k.pc.s.len - k.pc.s.T + t0;                    // ... and every row of the unit
-        float rs = 1.f;  // power of two that Q's row was divided by (8-bit caches)
-        if (live_warp) {  // Q to TMEM: 16-bit pairs, D / 4 columns of this half
-            constexpr int W = D / 4;
-            uint32_t r[W];
-#pragma unroll
-            for (int c = 0; c < W; ++c) r[c] = 0;
-            if (row < rows) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (k.pc.s.bos + t) * p.q_stride + (long)h * D + g * (D / 2));
-#pragma unroll
-                for (int c = 0; c < W / 4; ++c) {
-                    const uint4 x = __ldg(src + c);
-                    r[4 * c] = x.x; r[4 * c + 1] = x.y; r[4 * c + 2] = x.z; r[4 * c + 3] = x.w;
-                }
-            }
-            if constexpr (C::kCodes) {
-                float amax = 0.f;
-#pragma unroll
-                for (int c = 0; c < W; ++c)
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(r[c] << 16)), fabsf(__uint_as_float(r[c] & 0xffff0000u))));
-                xch[turn & 1][g][row] = amax;
-                bar_any(bar_id, 64, false);
-                amax = fmaxf(amax, xch[turn & 1][g ^ 1][row]);
-                ++turn;
-                const int e = f16_row_exponent(amax);
-                const float f = pow2i(e);
-                rs = pow2i(-e);
-#pragma unroll
-                for (int c = 0; c < W; ++c)
-                    r[c] = h2_bits(f * __uint_as_float(r[c] << 16), f * __uint_as_float(r[c] & 0xffff0000u));
-            }
-            if (p.negate)
-#pragma unroll
-                for (int c = 0; c < W; ++c) r[c] ^= 0x80008000u;
-#pragma unroll
-            for (int c = 0; c < W; c += 16) tmem_st16(tl + C::TM_Q + g * W + c, r + c);
-            tmem_wait_st();
-            tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar + C::B_Q);
+        const bool live_warp = quarter * 32 < rows;
+        const int sure = k.pc.s.len - k.pc.s.T + t0;               // last position that every row of the unit sees
+        const int limit = row < rows ? sure + row / p.w.G : -1;    // ... that this row sees
         float m = -INFINITY, l = 0.f;
-        for (int jj = 0; jj < n && !failed; ++jj, ++it) {
-            const uint32_t b = it & 1;
-            late |= !product_done<D, KIND>(bar, C::B_S, it, p.budget);
-            if constexpr (C::kCodes) late = late || !mbar_wait_spin(bar + C::B_COL + it % C::COLS, (it / C::COLS) & 1, p.budget);
+        for (int jj = 0; jj < n; ++jj, ++t) {
+            const uint32_t b = t & 1;
+            if (!late) late = !product_done<D, KIND>(bar, C::B_S, t, p.budget);
+            if (C::kCodes && !late) late = !mbar_wait_spin(bar + C::B_COL + t % C::COLS, (t / C::COLS) & 1, p.budget);
             if (!live_warp) {
-                failed = __any_sync(0xffffffffu, late);
-                if (lane == 0 && !failed) mbar_arrive(bar + C::B_P + b);
+                if (lane == 0) mbar_arrive(bar + C::B_P + b);
                 continue;
             }
             tc_fence_after();
-            const int c0 = (k.pc.off + jj) * BN + g * HC;  // position of this thread's first column
-            float x[HC];
-            {
-                uint32_t r[HC];
+            const uint32_t ts = tl + C::TM_S + b * BN + half * HC;
+            const int pos0 = (k.pc.off + jj) * BN + half * HC;
+            const bool masked = pos0 + HC - 1 > sure;
+            const float *col = reinterpret_cast<const float *>(sm + C::SM_COL) + (t % C::COLS) * 3 * BN + half * HC;
+            const float rs = C::kCodes ? rsq[(unit & 3) * 128] : 1.f;
+            // CW scores from column c of the half on, in the log2 domain for 8-bit caches, masked
+            auto scores = [&](float(&x)[CW], int c) {
+                uint32_t r[CW];
+                if constexpr (CW == 16) {
+                    tmem_ld16_nw(ts + c, r);
+                } else {
 #pragma unroll
-                for (int c = 0; c < HC; c += 32) tmem_ld32_nw(tl + C::TM_S + b * BN + g * HC + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
+                    for (int e = 0; e < CW; e += 32) tmem_ld32_nw(ts + c + e, *reinterpret_cast<uint32_t(*)[32]>(r + e));
+                }
                 tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < HC; ++c) x[c] = __uint_as_float(r[c]);
-            }
-            const float *col = reinterpret_cast<const float *>(sm + C::SM_COL) + (it % C::COLS) * 3 * BN + g * HC;
-            if constexpr (C::kCodes) {
+                for (int e = 0; e < CW; ++e) x[e] = __uint_as_float(r[e]);
+                if constexpr (C::kCodes) {
 #pragma unroll
-                for (int c = 0; c < HC; c += 4) {
-                    const float4 a = *reinterpret_cast<const float4 *>(col + c), lv = *reinterpret_cast<const float4 *>(col + BN + c);
-                    x[c] = fmaf(x[c] * rs, a.x, lv.x);
-                    x[c + 1] = fmaf(x[c + 1] * rs, a.y, lv.y);
-                    x[c + 2] = fmaf(x[c + 2] * rs, a.z, lv.z);
-                    x[c + 3] = fmaf(x[c + 3] * rs, a.w, lv.w);
+                    for (int e = 0; e < CW; e += 4) {
+                        const float4 a = *reinterpret_cast<const float4 *>(col + c + e), lv = *reinterpret_cast<const float4 *>(col + BN + c + e);
+                        x[e] = fmaf(x[e] * rs, a.x, lv.x);
+                        x[e + 1] = fmaf(x[e + 1] * rs, a.y, lv.y);
+                        x[e + 2] = fmaf(x[e + 2] * rs, a.z, lv.z);
+                        x[e + 3] = fmaf(x[e + 3] * rs, a.w, lv.w);
+                    }
                 }
+                if (masked) {
+                    const int last = limit - pos0 - c;
+#pragma unroll
+                    for (int e = 0; e < CW; ++e)
+                        if (e > last) x[e] = -INFINITY;
+                }
+            };
+            float x[CW];
+            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
+#pragma unroll 1
+            for (int c = 0; c < HC; c += CW) {
+                scores(x, c);
+#pragma unroll
+                for (int e = 0; e < CW; e += 8)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) t4[y] = fmaxf(fmaxf(t4[y], x[e + y]), x[e + 4 + y]);
             }
-            if ((k.pc.off + jj + 1) * BN - 1 > sure) {
-#pragma unroll
-                for (int c = 0; c < HC; ++c)
-                    if (c0 + c > limit) x[c] = -INFINITY;
-            }
-            float t4[4] = {x[0], x[1], x[2], x[3]};  // four chains
-#pragma unroll
-            for (int c = 4; c < HC; c += 8)
-#pragma unroll
-                for (int y = 0; y < 4; ++y) t4[y] = c + 4 + y < HC ? fmaxf(fmaxf(t4[y], x[c + y]), x[c + 4 + y]) : fmaxf(t4[y], x[c + y]);
-            float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-            xch[turn & 1][g][row] = top;
-            failed = bar_any(bar_id, 64, late);
-            if (failed) break;
-            top = fmaxf(top, xch[turn & 1][g ^ 1][row]);
-            ++turn;
             const float sc = C::kCodes ? 1.f : p.scale2;
-            const float mt = top * sc;
+            float *xb = xch + (t & 1) * 256;
+            xb[half * 128] = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+            ok = !bar_any(bar_id, 64, late);
+            if (!ok) break;
             float f;
-            const bool grow = grow_reference(m, mt, f);
+            const bool grow = grow_reference(m, fmaxf(xb[0], xb[128]) * sc, f);
             l *= f;
-            if (jj > 0 && __any_sync(0xffffffffu, grow)) {
-                // O holds the tiles up to jj - 1
-                late |= !product_done<D, KIND>(bar, C::B_PV, it - 1, p.budget);
+            if (jj > 0 && __any_sync(0xffffffffu, grow)) {  // O holds the unit's tiles up to the one before
+                late = !product_done<D, KIND>(bar, C::B_PV, t - 1, p.budget);
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < D / 2; c += 32) {
-                    uint32_t r[32];
-                    tmem_ld32_nw(tl + C::TM_O + g * (D / 2) + c, r);
+                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16_nw(tl + C::TM_O + c, r);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                    tmem_st32(tl + C::TM_O + g * (D / 2) + c, r);
+                    for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                    tmem_st16(tl + C::TM_O + c, r);
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            uint32_t pk[HC / 2];
             float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int c = 0; c < HC; c += CW) {  // P lies over the half's own scores, which have been read
+                uint32_t pk[CW / 2];
+                if constexpr (CW < HC) scores(x, c);
 #pragma unroll
-            for (int c = 0; c < HC; c += 2) {
-                float &l0 = l4[c & 2], &l1 = l4[(c & 2) + 1];
-                const float e0 = ex2(C::kCodes ? x[c] - ref : fmaf(x[c], sc, -ref));
-                const float e1 = ex2(C::kCodes ? x[c + 1] - ref : fmaf(x[c + 1], sc, -ref));
-                if constexpr (C::kCodes) {
-                    const float2 iv = *reinterpret_cast<const float2 *>(col + 2 * BN + c);
-                    l0 = fmaf(e0, iv.x, l0);
-                    l1 = fmaf(e1, iv.y, l1);
-                    pk[c / 2] = h2_bits(e0, e1);
+                for (int e = 0; e < CW; e += 2) {
+                    const float e0 = ex2(C::kCodes ? x[e] - ref : fmaf(x[e], sc, -ref));
+                    const float e1 = ex2(C::kCodes ? x[e + 1] - ref : fmaf(x[e + 1], sc, -ref));
+                    if constexpr (C::kCodes) {
+                        const float2 iv = *reinterpret_cast<const float2 *>(col + 2 * BN + c + e);
+                        l4[e & 2] = fmaf(e0, iv.x, l4[e & 2]);
+                        l4[(e & 2) + 1] = fmaf(e1, iv.y, l4[(e & 2) + 1]);
+                        pk[e / 2] = h2_bits(e0, e1);
+                    } else {
+                        l4[e & 2] += e0;
+                        l4[(e & 2) + 1] += e1;
+                        pk[e / 2] = bf2(e0, e1);
+                    }
+                }
+                if constexpr (CW == 16) {
+                    tmem_st8(ts + c / 2, pk);
                 } else {
-                    l0 += e0;
-                    l1 += e1;
-                    pk[c / 2] = bf2(e0, e1);
+#pragma unroll
+                    for (int e = 0; e < CW / 2; e += 16) tmem_st16(ts + c / 2 + e, pk + e);
                 }
             }
             l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-#pragma unroll
-            for (int c = 0; c < HC / 2; c += 16) tmem_st16(tl + C::TM_S + b * BN + g * (HC / 2) + c, pk + c);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + C::B_P + b);
         }
-        if (failed) break;
-        // the unit's last product, then the row
-        late |= !product_done<D, KIND>(bar, C::B_PV, it - 1, p.budget);
-        if (live_warp) {
-            tc_fence_after();
-            xch[turn & 1][g][row] = l;
-            failed = bar_any(bar_id, 64, late);
-            if (failed) break;
-            l += xch[turn & 1][g ^ 1][row];
-            ++turn;
-            const bool whole = k.begun && k.pc.off + n == k.pc.ntiles;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const bool store = row < rows && (!whole || limit >= 0);
-            const long part = part_index(p.w, blockIdx.x, k.begun ? 1 : 0, row);
-            if (!whole && row < rows && g == 0) p.w.ml[part] = make_float2(m, l);
-#pragma unroll 1
-            for (int c = 0; c < D / 2; c += 32) {
-                float o[32];
-                tmem_ld32(tl + C::TM_O + g * (D / 2) + c, o);
-                if (!store) continue;
-                const int at = g * (D / 2) + c;
-                if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((k.pc.s.bos + t) * p.Hq + h) * D + at);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float *y = o + 8 * e;
-                        dst[e] = make_uint4(bf2(y[0] * inv, y[1] * inv), bf2(y[2] * inv, y[3] * inv),
-                                            bf2(y[4] * inv, y[5] * inv), bf2(y[6] * inv, y[7] * inv));
-                    }
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.w.part + part * D + at);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                }
-            }
-            tc_fence_before();
-        } else {
-            failed = __any_sync(0xffffffffu, late);
-            if (failed) break;
-        }
+        if (!ok) break;
+        if (unit >= 2 && !late) late = !mbar_wait_spin(bar + C::B_SF + (unit & 1), ((unit >> 1) - 1) & 1, p.budget);
+        ok = !bar_any(bar_id, 64, late);
+        if (!ok) break;
+        stat[(unit & 1) * 256] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + C::B_ST + (unit & 1));
+        ++unit;
     } while (walk_next<BN>(p.w, &k));
-    if (failed && lane == 0) flag_error(p.w.pg.status);
+    if (!ok && lane == 0) flag_error(p.w.pg.status);
+}
+
+// ---- rows: Q in, O out ----------------------------------------------------------------------
+template <int D, int KIND>
+__device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, uint32_t tmem) {
+    using C = Cfg<D, KIND>;
+    constexpr int BN = C::BN;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
+    const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+    const float2 *stat = reinterpret_cast<const float2 *>(sm + C::SM_STAT) + row;
+    float *rsq = reinterpret_cast<float *>(sm + C::SM_RS) + row;
+    constexpr int QC = D / 2 < C::QC ? D / 2 : C::QC;  // 32-bit columns of Q at a time
+    auto unit_rows = [&](const Walk &w) { return min(p.w.TPT, w.pc.s.T - w.pc.i * p.w.TPT) * p.w.G; };
+    auto q_row = [&](const Walk &w) {
+        const int t = w.pc.i * p.w.TPT + row / p.w.G, h = w.pc.h * p.w.G + row % p.w.G;
+        return reinterpret_cast<const uint4 *>(p.q + (w.pc.s.bos + t) * p.q_stride + (long)h * D);
+    };
+    auto load = [&](const Walk &w, int part, uint32_t(&r)[QC]) {
+        const bool here = row < unit_rows(w);
+        const uint4 *src = q_row(w) + part * (QC / 4);
+#pragma unroll
+        for (int c = 0; c < QC / 4; ++c) {
+            const uint4 x = here ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            r[4 * c] = x.x; r[4 * c + 1] = x.y; r[4 * c + 2] = x.z; r[4 * c + 3] = x.w;
+        }
+    };
+    auto largest = [&](const uint32_t(&r)[QC]) {
+        float a = 0.f;
+#pragma unroll
+        for (int c = 0; c < QC; ++c)
+            a = fmaxf(a, fmaxf(fabsf(__uint_as_float(r[c] << 16)), fabsf(__uint_as_float(r[c] & 0xffff0000u))));
+        return a;
+    };
+    // Q of a unit, whose first part has been loaded, into TMEM
+    auto put = [&](const Walk &w, uint32_t(&r)[QC], uint32_t unit) {
+        if (quarter * 32 < unit_rows(w)) {
+            float f = 1.f;
+            if constexpr (C::kCodes) {  // to fp16, by the row's power of two
+                float amax = largest(r);
+                if constexpr (D / 2 > QC) {
+#pragma unroll 1
+                    for (int part = 1; part < D / 2 / QC; ++part) {
+                        load(w, part, r);
+                        amax = fmaxf(amax, largest(r));
+                    }
+                    load(w, 0, r);
+                }
+                const int e = f16_row_exponent(amax);
+                f = pow2i(e);
+                rsq[(unit & 3) * 128] = pow2i(-e);
+            }
+#pragma unroll 1
+            for (int part = 0; part < D / 2 / QC; ++part) {
+                if (part > 0) load(w, part, r);
+                if constexpr (C::kCodes) {
+#pragma unroll
+                    for (int c = 0; c < QC; ++c)
+                        r[c] = h2_bits(f * __uint_as_float(r[c] << 16), f * __uint_as_float(r[c] & 0xffff0000u));
+                }
+                if (p.negate)
+#pragma unroll
+                    for (int c = 0; c < QC; ++c) r[c] ^= 0x80008000u;
+#pragma unroll
+                for (int c = 0; c < QC; c += 16) tmem_st16(tl + C::TM_Q + part * QC + c, r + c);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + C::B_Q);
+    };
+    bool ok = true;
+    if (k.pc.left > 0) {
+        uint32_t r[QC];
+        load(k, 0, r);
+        put(k, r, 0);
+        uint32_t t = 0;
+        bool more = true;
+        for (uint32_t unit = 0; more; ++unit) {
+            const int n = k.take();
+            t += n;
+            Walk next = k;
+            more = walk_next<BN>(p.w, &next);
+            if (more) load(next, 0, r);
+            ok = __all_sync(0xffffffffu, product_done<D, KIND>(bar, C::B_S, t - 1, p.budget));  // Q has been used
+            if (!ok) break;
+            tc_fence_after();
+            if (more) put(next, r, unit + 1);
+            ok = warp_wait_spin(bar + C::B_ST + (unit & 1), (unit >> 1) & 1, p.budget);
+            if (!ok) break;
+            const float2 a = stat[(unit & 1) * 256], b = stat[(unit & 1) * 256 + 128];
+            const float m = a.x, l = a.y + b.y;  // (both halves have the same reference)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + C::B_SF + (unit & 1));
+            ok = __all_sync(0xffffffffu, product_done<D, KIND>(bar, C::B_PV, t - 1, p.budget));
+            if (!ok) break;
+            const int rows = unit_rows(k);
+            if (quarter * 32 < rows) {
+                tc_fence_after();
+                const int tok = k.pc.i * p.w.TPT + row / p.w.G, h = k.pc.h * p.w.G + row % p.w.G;
+                const bool whole = k.begun && k.pc.off + n == k.pc.ntiles;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const bool store = row < rows && (!whole || k.pc.s.len - k.pc.s.T + tok >= 0);  // (padding: zeros already)
+                const long part = part_index(p.w, blockIdx.x, k.begun ? 1 : 0, row);
+                if (!whole && store) p.w.ml[part] = make_float2(m, l);
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    tmem_ld32(tl + C::TM_O + c, o);
+                    if (!store) continue;
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((k.pc.s.bos + tok) * p.Hq + h) * D + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float *y = o + 8 * e;
+                            dst[e] = make_uint4(bf2(y[0] * inv, y[1] * inv), bf2(y[2] * inv, y[3] * inv),
+                                                bf2(y[4] * inv, y[5] * inv), bf2(y[6] * inv, y[7] * inv));
+                        }
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.w.part + part * D + c);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + C::B_OF);
+            k = next;
+        }
+    }
+    if (!ok && lane == 0) flag_error(p.w.pg.status);
 }
 
 template <int D, int KIND>
@@ -613,21 +706,26 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         prefetch_tmap(&mv);
     }
     if (tid == 0) {
-        for (int s = 0; s < C::NK; ++s) mbar_init(bar + C::B_FK + s, C::kCodes ? kConvWarps : 1);
-        for (int s = 0; s < C::NV; ++s) mbar_init(bar + C::B_FV + s, C::kCodes ? kConvWarps : 1);
+        for (int s = 0; s < C::NK; ++s) mbar_init(bar + C::B_FK + s, C::kCodes ? kGroup : 1);
+        for (int s = 0; s < C::NV; ++s) mbar_init(bar + C::B_FV + s, C::kCodes ? kGroup : 1);
         for (int s = 0; s < C::NR; ++s) {
             mbar_init(bar + C::B_RK + s, 1);
             mbar_init(bar + C::B_RV + s, 1);
-            mbar_init(bar + C::B_REK + s, kConvWarps);
-            mbar_init(bar + C::B_REV + s, kConvWarps);
+            mbar_init(bar + C::B_REK + s, kGroup);
+            mbar_init(bar + C::B_REV + s, kGroup);
         }
-        for (int s = 0; s < C::COLS; ++s) mbar_init(bar + C::B_COL + s, kConvWarps);
+        for (int s = 0; s < C::COLS; ++s) mbar_init(bar + C::B_COL + s, kGroup);
         for (int s = 0; s < C::kTurns; ++s) {
             mbar_init(bar + C::B_S + s, 1);
             mbar_init(bar + C::B_PV + s, 1);
         }
-        for (int s = 0; s < 2; ++s) mbar_init(bar + C::B_P + s, kSoftWarps);
-        mbar_init(bar + C::B_Q, kSoftWarps);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar + C::B_P + s, 2 * kGroup);
+            mbar_init(bar + C::B_ST + s, 2 * kGroup);
+            mbar_init(bar + C::B_SF + s, kGroup);
+        }
+        mbar_init(bar + C::B_Q, kGroup);
+        mbar_init(bar + C::B_OF, kGroup);
         mbar_init(bar + C::B_FIN, 1);
         fence_mbar_init();
     }
@@ -635,19 +733,29 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     tc_fence_before();
     plan_piece<C::BN, C::THREADS>(p.w, plan);  // (synchronises the CTA)
     tc_fence_after();
-    const uint32_t tmem = *slot;
+    // All 512 columns are this CTA's, so the allocation starts at column 0, and addresses are constants (in uniform
+    // registers; as a loaded value, each product's issue took about 45 cycles instead of ).
+    constexpr uint32_t tmem = 0;
     Walk k{plan->piece, plan->piece.off == 0};
-    if (warp < kSoftWarps) {
+    if (*slot != tmem) {
+        if (tid == 0) flag_error(p.w.pg.status);
+        k.pc.left = 0;
+    }
+    if (warp < kRowWarp0) {
         soft_role<D, KIND>(p, sm, bar, k, tmem);
+    } else if (warp < kLoadWarp) {
+        row_role<D, KIND>(p, sm, bar, k, tmem);
     } else if (warp == kLoadWarp) {
         load_role<D, KIND, false>(p, sm, bar, k, &mk);
     } else if (warp == kLoadWarp + 1) {
         load_role<D, KIND, true>(p, sm, bar, k, &mv);
     } else if (warp == kMmaWarp) {
-        if (plan->padding) zero_padding(p.w, p.out, p.Hq, D, tid & 31, 32);  // while the first tiles are on their way
         mma_role<D, KIND>(p, sm, sb, bar, k, tmem);
+    } else if (warp == kPadWarp) {
+        if (plan->padding) zero_padding(p.w, p.out, p.Hq, D, tid & 31, 32);
     } else if constexpr (C::kCodes) {
-        convert_role<D, KIND>(p, sm, bar, k);
+        if (warp < kConvWarp0 + kGroup) convert_role<D, KIND, false>(p, sm, bar, k);
+        else convert_role<D, KIND, true>(p, sm, bar, k);
     }
     tc_fence_before();
     __syncthreads();
