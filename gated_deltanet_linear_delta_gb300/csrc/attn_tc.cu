@@ -45,8 +45,11 @@ namespace {
 
 using namespace tc;
 
-constexpr int kGroup = 4, kRowWarp0 = 8, kLoadWarp = 12 /* K, then V */, kMmaWarp = 14, kPadWarp = 15,
+constexpr int kGroup = 4, kRowWarp0 = 8, kLoadWarp = 12 /* K, then V */, kMmaWarp = 14,
               kConvWarp0 = 16 /* K, then V */;
+// With the converting groups the launch gives a thread 80 registers; the softmax groups, whose threads hold 64
+// scores, take what the converting groups leave of theirs: 2 * 112 + 2 * 80 + 2 * 48 = 6 * 80.
+constexpr int kSoftRegs = 112, kConvRegs = 48;
 
 template <int D, int KIND>
 struct Cfg {
@@ -59,10 +62,6 @@ struct Cfg {
     // ring slots: 16-bit tiles of K and of V, and with an 8-bit cache their codes
     static constexpr int NK = kCodes ? 2 : (D == 64 ? 6 : 3), NV = NK;
     static constexpr int NR = kCodes ? (D == 64 ? 6 : 2) : 0;
-    // Scores and 32-bit columns of Q that a thread has at hand at a time. With the converting warps there are 80
-    // registers a thread, and the scores are read twice, for the maximum and for the probabilities; else there are
-    // 128, and one reading serves both.
-    static constexpr int CW = kCodes ? 16 : BN / 2, QC = kCodes ? 16 : 64;
     static constexpr int COLS = 4;                         // column scales, a buffer per tile
     static constexpr int THREADS = 32 * (kCodes ? kConvWarp0 + 2 * kGroup : kConvWarp0);
     static constexpr uint32_t TM_O = 0, TM_S = D == 256 ? 256 : 128, TM_Q = 384;
@@ -72,14 +71,16 @@ struct Cfg {
     static constexpr uint32_t SM_X = SM_COL + (kCodes ? COLS * 3 * BN * 4 : 0);  // [2][2][128] maxima of a tile's halves
     static constexpr uint32_t SM_STAT = SM_X + 2 * 2 * 128 * 4;              // [2][2][128] a unit's m, l by half
     static constexpr uint32_t SM_RS = SM_STAT + 2 * 2 * 128 * 8;             // [4][128] Q's row scales (8-bit caches)
-    static constexpr uint32_t SM_BAR = SM_RS + 4 * 128 * 4;
+    static constexpr uint32_t SM_Q = (SM_RS + (kCodes ? 4 * 128 * 4 : 0) + 1023) & ~1023u;  // [128 rows][128 B] of Q
+    static constexpr uint32_t SM_BAR = SM_Q + 128 * 128;
     // S_j and O += P_j V_j done, by tile modulo 8: they also say that K_j's and V_j's slots are free. (Whoever fills
     // a slot looks back at most 6 tiles, so a barrier is never two phases ahead of its reader.)
     static constexpr int kTurns = 8;
     static constexpr int B_FK = 0, B_FV = B_FK + NK, B_RK = B_FV + NV, B_RV = B_RK + NR, B_REK = B_RV + NR,
                          B_REV = B_REK + NR, B_COL = B_REV + NR, B_S = B_COL + COLS, B_PV = B_S + kTurns,
                          B_P = B_PV + kTurns, B_ST = B_P + 2, B_SF = B_ST + 2,
-                         B_Q = B_SF + 2, B_OF = B_Q + 1, B_FIN = B_OF + 1, B_COUNT = B_FIN + 1;
+                         B_Q = B_SF + 2, B_OF = B_Q + 1, B_QF = B_OF + 1, B_QE = B_QF + 1,
+                         B_FIN = B_QE + 1, B_COUNT = B_FIN + 1;
     static constexpr uint32_t SM_INFO = SM_BAR + B_COUNT * 8;                // [2][NR] valid rows, page mask
     static constexpr uint32_t SM_TMEM = SM_INFO + (NR ? 2 * NR : 1) * 8;
     static constexpr uint32_t SM_PLAN = (SM_TMEM + 8 + 15) & ~15u;
@@ -89,12 +90,10 @@ struct Cfg {
 
 struct TcParams {
     AttnWork w;
-    const __nv_bfloat16 *q;
     const uint8_t *k_cache, *v_cache;  // 8-bit caches
     const float *k_scale, *v_scale;
     __nv_bfloat16 *out;
     int Hq;
-    long q_stride;
     float scale2;  // |softmax scale| * log2 e
     int negate;    // the scale is negative: Q is negated
     long long budget;
@@ -330,7 +329,7 @@ __device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst0, 
     using C = Cfg<D, KIND>;
     constexpr int STEPS = C::BN * D / 16 / (kGroup * 32), ROWS = kGroup * 32 / (D / 16);
     static_assert(ROWS % 8 == 0 && STEPS % 4 == 0, "the swizzle must not change between steps");
-#pragma unroll
+#pragma unroll 1
     for (int st = 0; st < STEPS; st += 4) {
         uint4 q[4];
 #pragma unroll
@@ -356,7 +355,7 @@ __device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst0, 
 }
 
 template <int D, int KIND, bool IS_V>
-__device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k) {
+__device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, uint32_t tiles) {
     using C = Cfg<D, KIND>;
     constexpr int BN = C::BN, N = IS_V ? C::NV : C::NK;
     const int tid = threadIdx.x & (kGroup * 32 - 1), lane = tid & 31;
@@ -369,47 +368,43 @@ __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk
     const uint32_t dst0 = swz(row0, 2 * c), dst1 = swz(row0, 2 * c + 1);
     Ring<N> ring;
     Ring<C::NR> raw;
-    uint32_t t = 0;  // tiles converted
     bool ok = true;
-    if (k.pc.left > 0) do {
-        const int n = k.take();
-        for (int jj = 0; jj < n; ++jj, ++t) {
-            bool got = mbar_wait_spin(bar + (IS_V ? C::B_RV : C::B_RK) + raw.slot, raw.phase, p.budget);
-            if (t >= N) got = got && product_done<D, KIND>(bar, IS_V ? C::B_PV : C::B_S, t - N, p.budget);
-            ok = __all_sync(0xffffffffu, got);
-            if (!ok) break;
-            const uint8_t *from = src + raw.slot * (IS_V ? C::RAW_V : C::RAW_K);
-            const int2 info = reinterpret_cast<const int2 *>(sm + C::SM_INFO)[(IS_V ? C::NR : 0) + raw.slot];
-            if constexpr (!IS_V) {
-                const uint32_t cb = t % C::COLS;
-                if (tid < BN) {
-                    const float *sc = reinterpret_cast<const float *>(from + BN * D);
-                    const bool live = tid < info.x && ((info.y >> (tid >> box_shift)) & 1);
-                    const float ks = live ? sc[tid] : 0.f;
-                    float vs = live ? sc[BN + tid] : kMinKvScale;
-                    if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
-                    float *col = reinterpret_cast<float *>(sm + C::SM_COL) + cb * 3 * BN;
-                    col[tid] = ks * p.scale2;
-                    col[BN + tid] = lg2(vs);
-                    col[2 * BN + tid] = vs == vs ? rcp(vs) : 0.f;  // a NaN enters by b, and not where it is masked
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar + C::B_COL + cb);
+    for (uint32_t t = 0; t < tiles; ++t) {  // all the piece's, whatever units they belong to
+        bool got = mbar_wait_spin(bar + (IS_V ? C::B_RV : C::B_RK) + raw.slot, raw.phase, p.budget);
+        if (t >= N) got = got && product_done<D, KIND>(bar, IS_V ? C::B_PV : C::B_S, t - N, p.budget);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) break;
+        const uint8_t *from = src + raw.slot * (IS_V ? C::RAW_V : C::RAW_K);
+        const int2 info = reinterpret_cast<const int2 *>(sm + C::SM_INFO)[(IS_V ? C::NR : 0) + raw.slot];
+        if constexpr (!IS_V) {
+            const uint32_t cb = t % C::COLS;
+            if (tid < BN) {
+                const float *sc = reinterpret_cast<const float *>(from + BN * D);
+                const bool live = tid < info.x && ((info.y >> (tid >> box_shift)) & 1);
+                const float ks = live ? sc[tid] : 0.f;
+                float vs = live ? sc[BN + tid] : kMinKvScale;
+                if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
+                float *col = reinterpret_cast<float *>(sm + C::SM_COL) + cb * 3 * BN;
+                col[tid] = ks * p.scale2;
+                col[BN + tid] = lg2(vs);
+                col[2 * BN + tid] = vs == vs ? rcp(vs) : 0.f;  // a NaN enters by b, and not where it is masked
             }
-            // A tile that is whole takes no checks; rows past the end and bad pages become zeros.
-            const bool whole = info.x == BN && info.y == all_pages;
-            uint8_t *to = dst + ring.slot * C::SLOT;
-            convert_tile<D, KIND>(from + src0, to + dst0, to + dst1, row0, whole ? -1 : info.x, info.y, box_shift);
-            fence_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar + (IS_V ? C::B_FV : C::B_FK) + ring.slot);
-                mbar_arrive(bar + (IS_V ? C::B_REV : C::B_REK) + raw.slot);
-            }
-            ring.next();
-            raw.next();
+            if (lane == 0) mbar_arrive(bar + C::B_COL + cb);
         }
-    } while (ok && walk_next<BN>(p.w, &k));
+        // A tile that is whole takes no checks; rows past the end and bad pages become zeros.
+        const bool whole = info.x == BN && info.y == all_pages;
+        uint8_t *to = dst + ring.slot * C::SLOT;
+        convert_tile<D, KIND>(from + src0, to + dst0, to + dst1, row0, whole ? -1 : info.x, info.y, box_shift);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(bar + (IS_V ? C::B_FV : C::B_FK) + ring.slot);
+            mbar_arrive(bar + (IS_V ? C::B_REV : C::B_REK) + raw.slot);
+        }
+        ring.next();
+        raw.next();
+    }
     if (!ok && lane == 0) flag_error(p.w.pg.status);
 }
 
@@ -417,7 +412,7 @@ __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk
 template <int D, int KIND>
 __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, uint32_t tmem) {
     using C = Cfg<D, KIND>;
-    constexpr int BN = C::BN, HC = BN / 2, CW = C::CW;
+    constexpr int BN = C::BN, HC = BN / 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int half = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
     const int bar_id = 1 + quarter;                               // of the two warps that share these rows
@@ -450,45 +445,35 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
             const bool masked = pos0 + HC - 1 > sure;
             const float *col = reinterpret_cast<const float *>(sm + C::SM_COL) + (t % C::COLS) * 3 * BN + half * HC;
             const float rs = C::kCodes ? rsq[(unit & 3) * 128] : 1.f;
-            // CW scores from column c of the half on, in the log2 domain for 8-bit caches, masked
-            auto scores = [&](float(&x)[CW], int c) {
-                uint32_t r[CW];
-                if constexpr (CW == 16) {
-                    tmem_ld16_nw(ts + c, r);
-                } else {
+            float x[HC];  // the scores, in the log2 domain for 8-bit caches, masked
+            {
+                uint32_t r[HC];
 #pragma unroll
-                    for (int e = 0; e < CW; e += 32) tmem_ld32_nw(ts + c + e, *reinterpret_cast<uint32_t(*)[32]>(r + e));
-                }
+                for (int e = 0; e < HC; e += 32) tmem_ld32_nw(ts + e, *reinterpret_cast<uint32_t(*)[32]>(r + e));
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < CW; ++e) x[e] = __uint_as_float(r[e]);
-                if constexpr (C::kCodes) {
-#pragma unroll
-                    for (int e = 0; e < CW; e += 4) {
-                        const float4 a = *reinterpret_cast<const float4 *>(col + c + e), lv = *reinterpret_cast<const float4 *>(col + BN + c + e);
-                        x[e] = fmaf(x[e] * rs, a.x, lv.x);
-                        x[e + 1] = fmaf(x[e + 1] * rs, a.y, lv.y);
-                        x[e + 2] = fmaf(x[e + 2] * rs, a.z, lv.z);
-                        x[e + 3] = fmaf(x[e + 3] * rs, a.w, lv.w);
-                    }
-                }
-                if (masked) {
-                    const int last = limit - pos0 - c;
-#pragma unroll
-                    for (int e = 0; e < CW; ++e)
-                        if (e > last) x[e] = -INFINITY;
-                }
-            };
-            float x[CW];
-            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
-#pragma unroll 1
-            for (int c = 0; c < HC; c += CW) {
-                scores(x, c);
-#pragma unroll
-                for (int e = 0; e < CW; e += 8)
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) t4[y] = fmaxf(fmaxf(t4[y], x[e + y]), x[e + 4 + y]);
+                for (int e = 0; e < HC; ++e) x[e] = __uint_as_float(r[e]);
             }
+            if constexpr (C::kCodes) {
+                const F2 rs2 = f2(rs, rs);
+#pragma unroll
+                for (int e = 0; e < HC; e += 4) {
+                    const float4 a = *reinterpret_cast<const float4 *>(col + e), lv = *reinterpret_cast<const float4 *>(col + BN + e);
+                    f2_get(f2_fma(f2_mul(f2(x[e], x[e + 1]), rs2), f2(a.x, a.y), f2(lv.x, lv.y)), x[e], x[e + 1]);
+                    f2_get(f2_fma(f2_mul(f2(x[e + 2], x[e + 3]), rs2), f2(a.z, a.w), f2(lv.z, lv.w)), x[e + 2], x[e + 3]);
+                }
+            }
+            if (masked) {
+                const int last = limit - pos0;
+#pragma unroll
+                for (int e = 0; e < HC; ++e)
+                    if (e > last) x[e] = -INFINITY;
+            }
+            float t4[4] = {x[0], x[1], x[2], x[3]};  // four chains
+#pragma unroll
+            for (int e = 4; e < HC; e += 4)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) t4[y] = fmaxf(t4[y], x[e + y]);
             const float sc = C::kCodes ? 1.f : p.scale2;
             float *xb = xch + (t & 1) * 256;
             xb[half * 128] = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
@@ -511,34 +496,33 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
-            float l4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int c = 0; c < HC; c += CW) {  // P lies over the half's own scores, which have been read
-                uint32_t pk[CW / 2];
-                if constexpr (CW < HC) scores(x, c);
+            F2 l2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+            const F2 sc2 = f2(sc, sc), ref2 = f2(-ref, -ref);
+            uint32_t pk[HC / 2];
 #pragma unroll
-                for (int e = 0; e < CW; e += 2) {
-                    const float e0 = ex2(C::kCodes ? x[e] - ref : fmaf(x[e], sc, -ref));
-                    const float e1 = ex2(C::kCodes ? x[e + 1] - ref : fmaf(x[e + 1], sc, -ref));
-                    if constexpr (C::kCodes) {
-                        const float2 iv = *reinterpret_cast<const float2 *>(col + 2 * BN + c + e);
-                        l4[e & 2] = fmaf(e0, iv.x, l4[e & 2]);
-                        l4[(e & 2) + 1] = fmaf(e1, iv.y, l4[(e & 2) + 1]);
-                        pk[e / 2] = h2_bits(e0, e1);
-                    } else {
-                        l4[e & 2] += e0;
-                        l4[(e & 2) + 1] += e1;
-                        pk[e / 2] = bf2(e0, e1);
-                    }
-                }
-                if constexpr (CW == 16) {
-                    tmem_st8(ts + c / 2, pk);
+            for (int e = 0; e < HC; e += 2) {
+                const F2 y = C::kCodes ? f2_add(f2(x[e], x[e + 1]), ref2) : f2_fma(f2(x[e], x[e + 1]), sc2, ref2);
+                float e0, e1;
+                f2_get(y, e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                F2 &acc = l2[(e >> 1) & 1];
+                if constexpr (C::kCodes) {
+                    const float2 iv = *reinterpret_cast<const float2 *>(col + 2 * BN + e);
+                    acc = f2_fma(f2(e0, e1), f2(iv.x, iv.y), acc);
+                    pk[e / 2] = h2_bits(e0, e1);
                 } else {
-#pragma unroll
-                    for (int e = 0; e < CW / 2; e += 16) tmem_st16(ts + c / 2 + e, pk + e);
+                    acc = f2_add(f2(e0, e1), acc);
+                    pk[e / 2] = bf2(e0, e1);
                 }
             }
-            l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+#pragma unroll
+            for (int e = 0; e < HC / 2; e += 16) tmem_st16(ts + e, pk + e);  // over the half's own scores
+            {
+                float a, d;
+                f2_get(f2_add(l2[0], l2[1]), a, d);
+                l += a + d;
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -557,92 +541,102 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
 }
 
 // ---- rows: Q in, O out ----------------------------------------------------------------------
+// A thread of this group stands for a row of TMEM. Q comes by TMA, 128 bytes of all the unit's rows at a
+// time (box: 64 elements, the G heads of the key head, the unit's tokens, which lie in shared memory as
+// rows), and goes on into TMEM from there; finished rows are stored straight from TMEM.
 template <int D, int KIND>
-__device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, uint32_t tmem) {
+__device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, uint32_t tmem, const CUtensorMap *mq) {
     using C = Cfg<D, KIND>;
-    constexpr int BN = C::BN;
+    constexpr int BN = C::BN, PARTS = D / 64;
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, row = quarter * 32 + lane;
+    const int tok = row / p.w.G, head = row % p.w.G;
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const float2 *stat = reinterpret_cast<const float2 *>(sm + C::SM_STAT) + row;
     float *rsq = reinterpret_cast<float *>(sm + C::SM_RS) + row;
-    constexpr int QC = D / 2 < C::QC ? D / 2 : C::QC;  // 32-bit columns of Q at a time
+    const bool issuer = quarter == 0 && lane == 0;
+    const uint32_t bytes = (uint32_t)(p.w.TPT * p.w.G) * 128;
+    uint32_t fills = 0;  // of the stage so far
+    bool ok = true;
     auto unit_rows = [&](const Walk &w) { return min(p.w.TPT, w.pc.s.T - w.pc.i * p.w.TPT) * p.w.G; };
-    auto q_row = [&](const Walk &w) {
-        const int t = w.pc.i * p.w.TPT + row / p.w.G, h = w.pc.h * p.w.G + row % p.w.G;
-        return reinterpret_cast<const uint4 *>(p.q + (w.pc.s.bos + t) * p.q_stride + (long)h * D);
-    };
-    auto load = [&](const Walk &w, int part, uint32_t(&r)[QC]) {
-        const bool here = row < unit_rows(w);
-        const uint4 *src = q_row(w) + part * (QC / 4);
-#pragma unroll
-        for (int c = 0; c < QC / 4; ++c) {
-            const uint4 x = here ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-            r[4 * c] = x.x; r[4 * c + 1] = x.y; r[4 * c + 2] = x.z; r[4 * c + 3] = x.w;
-        }
-    };
-    auto largest = [&](const uint32_t(&r)[QC]) {
-        float a = 0.f;
-#pragma unroll
-        for (int c = 0; c < QC; ++c)
-            a = fmaxf(a, fmaxf(fabsf(__uint_as_float(r[c] << 16)), fabsf(__uint_as_float(r[c] & 0xffff0000u))));
-        return a;
-    };
-    // Q of a unit, whose first part has been loaded, into TMEM
-    auto put = [&](const Walk &w, uint32_t(&r)[QC], uint32_t unit) {
-        if (quarter * 32 < unit_rows(w)) {
-            float f = 1.f;
-            if constexpr (C::kCodes) {  // to fp16, by the row's power of two
-                float amax = largest(r);
-                if constexpr (D / 2 > QC) {
-#pragma unroll 1
-                    for (int part = 1; part < D / 2 / QC; ++part) {
-                        load(w, part, r);
-                        amax = fmaxf(amax, largest(r));
-                    }
-                    load(w, 0, r);
-                }
-                const int e = f16_row_exponent(amax);
-                f = pow2i(e);
-                rsq[(unit & 3) * 128] = pow2i(-e);
+    // 128 bytes of the unit's rows into the stage, once the four warps have read what was there
+    auto fetch = [&](const Walk &w, int part) {
+        if (issuer) {
+            if (fills > 0) ok = ok && mbar_wait(bar + C::B_QE, (fills - 1) & 1, p.budget);
+            if (ok) {
+                mbar_expect_tx(bar + C::B_QF, bytes);
+                tma_load_3d(sm + C::SM_Q, mq, part * 64, w.pc.h * p.w.G, (int)(w.pc.s.bos + w.pc.i * p.w.TPT), bar + C::B_QF);
             }
-#pragma unroll 1
-            for (int part = 0; part < D / 2 / QC; ++part) {
-                if (part > 0) load(w, part, r);
-                if constexpr (C::kCodes) {
-#pragma unroll
-                    for (int c = 0; c < QC; ++c)
-                        r[c] = h2_bits(f * __uint_as_float(r[c] << 16), f * __uint_as_float(r[c] & 0xffff0000u));
-                }
-                if (p.negate)
-#pragma unroll
-                    for (int c = 0; c < QC; ++c) r[c] ^= 0x80008000u;
-#pragma unroll
-                for (int c = 0; c < QC; c += 16) tmem_st16(tl + C::TM_Q + part * QC + c, r + c);
-            }
-            tmem_wait_st();
-            tc_fence_before();
         }
+        ++fills;
+    };
+    auto read = [&](uint32_t(&x)[32]) {  // this row's
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar + C::B_QF, (fills - 1) & 1, p.budget));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(sm + C::SM_Q + swz(row, c));
+            x[4 * c] = v.x; x[4 * c + 1] = v.y; x[4 * c + 2] = v.z; x[4 * c + 3] = v.w;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + C::B_QE);
+    };
+    // A unit's first part of Q on its way, and with an 8-bit cache its row's exponent, while the unit before is at work
+    auto prepare = [&](const Walk &w) -> int {
+        int e = 0;
+        fetch(w, 0);
+        if constexpr (C::kCodes) {
+            float a = 0.f;
+#pragma unroll 1
+            for (int part = 1; part <= PARTS && ok; ++part) {
+                uint32_t x[32];
+                read(x);
+                fetch(w, part % PARTS);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    a = fmaxf(a, fmaxf(fabsf(__uint_as_float(x[c] << 16)), fabsf(__uint_as_float(x[c] & 0xffff0000u))));
+            }
+            e = f16_row_exponent(a);
+        }
+        return e;
+    };
+    // Q into TMEM; to fp16, by the row's power of two, with an 8-bit cache
+    auto put = [&](const Walk &w, int e, uint32_t unit) {
+        const float f = pow2i(e);
+        if (C::kCodes) rsq[(unit & 3) * 128] = pow2i(-e);
+#pragma unroll 1
+        for (int part = 0; part < PARTS && ok; ++part) {
+            uint32_t x[32];
+            read(x);
+            if (part + 1 < PARTS) fetch(w, part + 1);
+            if constexpr (C::kCodes) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    x[c] = h2_bits(f * __uint_as_float(x[c] << 16), f * __uint_as_float(x[c] & 0xffff0000u));
+            }
+            if (p.negate)
+#pragma unroll
+                for (int c = 0; c < 32; ++c) x[c] ^= 0x80008000u;
+            tmem_st32(tl + C::TM_Q + part * 32, x);
+        }
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar + C::B_Q);
     };
-    bool ok = true;
     if (k.pc.left > 0) {
-        uint32_t r[QC];
-        load(k, 0, r);
-        put(k, r, 0);
+        put(k, prepare(k), 0);
         uint32_t t = 0;
         bool more = true;
-        for (uint32_t unit = 0; more; ++unit) {
+        for (uint32_t unit = 0; more && ok; ++unit) {
             const int n = k.take();
             t += n;
             Walk next = k;
             more = walk_next<BN>(p.w, &next);
-            if (more) load(next, 0, r);
-            ok = __all_sync(0xffffffffu, product_done<D, KIND>(bar, C::B_S, t - 1, p.budget));  // Q has been used
+            const int e = more ? prepare(next) : 0;
+            ok = __all_sync(0xffffffffu, ok && product_done<D, KIND>(bar, C::B_S, t - 1, p.budget));  // Q has been used
             if (!ok) break;
             tc_fence_after();
-            if (more) put(next, r, unit + 1);
-            ok = warp_wait_spin(bar + C::B_ST + (unit & 1), (unit >> 1) & 1, p.budget);
+            if (more) put(next, e, unit + 1);
+            ok = ok && warp_wait(bar + C::B_ST + (unit & 1), (unit >> 1) & 1, p.budget);
             if (!ok) break;
             const float2 a = stat[(unit & 1) * 256], b = stat[(unit & 1) * 256 + 128];
             const float m = a.x, l = a.y + b.y;  // (both halves have the same reference)
@@ -653,29 +647,30 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
             const int rows = unit_rows(k);
             if (quarter * 32 < rows) {
                 tc_fence_after();
-                const int tok = k.pc.i * p.w.TPT + row / p.w.G, h = k.pc.h * p.w.G + row % p.w.G;
+                const int t0 = k.pc.i * p.w.TPT;
                 const bool whole = k.begun && k.pc.off + n == k.pc.ntiles;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                const bool store = row < rows && (!whole || k.pc.s.len - k.pc.s.T + tok >= 0);  // (padding: zeros already)
+                const bool store = row < rows && (!whole || k.pc.s.len - k.pc.s.T + t0 + tok >= 0);  // (padding: zeros already)
                 const long part = part_index(p.w, blockIdx.x, k.begun ? 1 : 0, row);
                 if (!whole && store) p.w.ml[part] = make_float2(m, l);
+                __nv_bfloat16 *out = p.out + ((k.pc.s.bos + t0 + tok) * p.Hq + k.pc.h * p.w.G + head) * D;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
                     tmem_ld32(tl + C::TM_O + c, o);
                     if (!store) continue;
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((k.pc.s.bos + tok) * p.Hq + h) * D + c);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float *y = o + 8 * e;
-                            dst[e] = make_uint4(bf2(y[0] * inv, y[1] * inv), bf2(y[2] * inv, y[3] * inv),
-                                                bf2(y[4] * inv, y[5] * inv), bf2(y[6] * inv, y[7] * inv));
+                        for (int x = 0; x < 4; ++x) {
+                            const float *y = o + 8 * x;
+                            reinterpret_cast<uint4 *>(out + c)[x] =
+                                make_uint4(bf2(y[0] * inv, y[1] * inv), bf2(y[2] * inv, y[3] * inv),
+                                           bf2(y[4] * inv, y[5] * inv), bf2(y[6] * inv, y[7] * inv));
                         }
                     } else {
                         float4 *dst = reinterpret_cast<float4 *>(p.w.part + part * D + c);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
                     }
                 }
                 tc_fence_before();
@@ -686,11 +681,14 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
         }
     }
     if (!ok && lane == 0) flag_error(p.w.pg.status);
+    if (fills > 0) mbar_wait(bar + C::B_QF, (fills - 1) & 1, kDrainBudget);  // a copy in flight lands before the CTA leaves
+    __syncwarp();
 }
 
 template <int D, int KIND>
 __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, 1)
-attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TcParams p) {
+attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+               const __grid_constant__ CUtensorMap mv, const TcParams p) {
     using C = Cfg<D, KIND>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
@@ -702,8 +700,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     const int tid = threadIdx.x, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) {
-        prefetch_tmap(&mk);
-        prefetch_tmap(&mv);
+        prefetch_tmap(&mq);
+        if (!C::kCodes) {
+            prefetch_tmap(&mk);
+            prefetch_tmap(&mv);
+        }
     }
     if (tid == 0) {
         for (int s = 0; s < C::NK; ++s) mbar_init(bar + C::B_FK + s, C::kCodes ? kGroup : 1);
@@ -726,6 +727,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         }
         mbar_init(bar + C::B_Q, kGroup);
         mbar_init(bar + C::B_OF, kGroup);
+        mbar_init(bar + C::B_QF, 1);
+        mbar_init(bar + C::B_QE, kGroup);
         mbar_init(bar + C::B_FIN, 1);
         fence_mbar_init();
     }
@@ -741,21 +744,26 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         if (tid == 0) flag_error(p.w.pg.status);
         k.pc.left = 0;
     }
-    if (warp < kRowWarp0) {
+    const int group = warp / kGroup;
+    if (group < kRowWarp0 / kGroup) {
+        if constexpr (C::kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         soft_role<D, KIND>(p, sm, bar, k, tmem);
-    } else if (warp < kLoadWarp) {
-        row_role<D, KIND>(p, sm, bar, k, tmem);
-    } else if (warp == kLoadWarp) {
-        load_role<D, KIND, false>(p, sm, bar, k, &mk);
-    } else if (warp == kLoadWarp + 1) {
-        load_role<D, KIND, true>(p, sm, bar, k, &mv);
-    } else if (warp == kMmaWarp) {
-        mma_role<D, KIND>(p, sm, sb, bar, k, tmem);
-    } else if (warp == kPadWarp) {
-        if (plan->padding) zero_padding(p.w, p.out, p.Hq, D, tid & 31, 32);
+    } else if (group == kRowWarp0 / kGroup) {
+        row_role<D, KIND>(p, sm, bar, k, tmem, &mq);
+    } else if (group == kLoadWarp / kGroup) {
+        if (warp == kLoadWarp) {
+            load_role<D, KIND, false>(p, sm, bar, k, &mk);
+        } else if (warp == kLoadWarp + 1) {
+            load_role<D, KIND, true>(p, sm, bar, k, &mv);
+        } else if (warp == kMmaWarp) {
+            mma_role<D, KIND>(p, sm, sb, bar, k, tmem);
+        } else {
+            if (plan->padding) zero_padding(p.w, p.out, p.Hq, D, tid & 31, 32);
+        }
     } else if constexpr (C::kCodes) {
-        if (warp < kConvWarp0 + kGroup) convert_role<D, KIND, false>(p, sm, bar, k);
-        else convert_role<D, KIND, true>(p, sm, bar, k);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+        if (group == kConvWarp0 / kGroup) convert_role<D, KIND, false>(p, sm, bar, (uint32_t)k.pc.left);
+        else convert_role<D, KIND, true>(p, sm, bar, (uint32_t)k.pc.left);
     }
     tc_fence_before();
     __syncthreads();
@@ -770,19 +778,18 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     const int G = a.Hq / a.pg.Hkv;
     TcParams p{};
     p.w = attn_work(a, kAttnMaxRows / G, 2);
-    p.q = (const __nv_bfloat16 *)a.q;
     p.k_cache = (const uint8_t *)a.k_cache;
     p.v_cache = (const uint8_t *)a.v_cache;
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
     p.out = (__nv_bfloat16 *)a.out;
     p.Hq = a.Hq;
-    p.q_stride = a.q_stride;
     p.negate = a.scale < 0.f;
     // a scale of 0 must not meet the -inf of a masked score in a product: so small that no score counts
     p.scale2 = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
     p.budget = wait_budget();
-    CUtensorMap mk{}, mv{};
+    CUtensorMap mq, mk{}, mv{};
+    if (!rows_map(&mq, a.q, D, a.Hq, a.pg.Ttot, a.q_stride, G, p.w.TPT)) return cudaErrorInvalidValue;
     if (!C::kCodes) {
         const int rows = a.pg.page_size < C::BN ? a.pg.page_size : C::BN;
         if (!page_map(&mk, a.k_cache, a.pg, D * 2, rows) || !page_map(&mv, a.v_cache, a.pg, D * 2, rows))
@@ -792,7 +799,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);
     if (e != cudaSuccess) return e;
     const int ctas = attn_ctas(a, p.w, C::BN);
-    kernel<<<ctas, C::THREADS, C::SM_BYTES, s>>>(mk, mv, p);
+    kernel<<<ctas, C::THREADS, C::SM_BYTES, s>>>(mq, mk, mv, p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_join(a, p.w, ctas, s);
 }
