@@ -16,11 +16,14 @@ The per-call host cost is kept small because a decode step of a few
 sequences runs in a few microseconds on the GPU: the library handle and its
 function objects are looked up once, pointers go to ctypes as plain integers,
 and the current stream is read as a raw handle. Size and alignment checks are
-the C library's (it returns an error before queueing anything).
+the C library's (it returns an error before queueing anything). The paged cache
+calls, which have the most tensors, are marshalled in C++ (csrc/binding.cpp).
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -45,8 +48,8 @@ _lib: ctypes.CDLL | None = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
+_calls = None
 _DTYPE = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
-_CACHE_DTYPE = {**_DTYPE, torch.float8_e4m3fn: GDN_FP8, torch.int8: GDN_INT8}
 # the current stream of a device as a raw cudaStream_t (falls back to the Stream object)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -287,83 +290,20 @@ def gdn_prepass(q, k, g, b, rq, rk, beta, gcum, cu_seqlens=None, B=None, T=None,
     _check(rc, "gdn_prepass")
 
 
-def _refuse_kv(rows, rows2, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, B, T):
-    """Raise what is wrong with a paged cache call's tensors (the calls' own check only finds that something is)."""
-    for t in (rows, rows2):
-        if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError("packed rows must be tensors [tokens, heads, d] with contiguous heads and elements")
-    if rows.dtype not in _DTYPE:
-        raise TypeError(f"unsupported dtype {rows.dtype}: use bfloat16 or float32")
-    if rows2.shape != rows.shape or rows2.dtype != rows.dtype:
-        raise ValueError("the call's packed rows (k and v, or q and out) must share one shape and dtype")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must share one dtype and the shape [num_pages, Hkv, page_size, d]")
-    if rows.shape[2] != k_cache.shape[3]:
-        raise ValueError(f"rows of {rows.shape[2]} elements for a cache of head dimension {k_cache.shape[3]}")
-    if k_cache.dtype not in _CACHE_DTYPE:
-        raise TypeError(f"unsupported cache dtype {k_cache.dtype}: use the rows' dtype, float8_e4m3fn or int8")
-    if _CACHE_DTYPE[k_cache.dtype] >= GDN_FP8:
-        for t in (k_scale, v_scale):
-            if t is None or t.dtype != torch.float32 or t.shape != k_cache.shape[:3]:
-                raise TypeError("an 8-bit cache needs fp32 k_scale and v_scale [num_pages, Hkv, page_size]")
-    if block_table.dtype != torch.int32 or kv_lens.dtype != torch.int32 or \
-            (cu_seqlens is not None and cu_seqlens.dtype != torch.int32):
-        raise TypeError("block_table, kv_lens and cu_seqlens must be int32")
-    if kv_lens.dim() != 1 or block_table.dim() != 2 or kv_lens.shape[0] != B or block_table.shape[0] != B or \
-            (cu_seqlens is not None and cu_seqlens.numel() != B + 1):
-        raise ValueError("kv_lens must be [B], block_table [B, max_pages] and cu_seqlens [B + 1]")
-    if cu_seqlens is None and B * T != rows.shape[0]:
-        raise ValueError(f"{rows.shape[0]} tokens are not {B} sequences of {T}")
-    for t in (rows, rows2, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens):
-        if t is not None and (not t.is_cuda or t.device != rows.device):
-            raise ValueError("tensors must be CUDA tensors of one device")
-    raise ValueError("caches, scales, block_table, kv_lens, cu_seqlens and the attention's output must be contiguous")
-
-
-def _kv_args(rows, rows2, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, B, T):
-    """Sizes and pointers of a paged cache call, checked: (B, T, heads of rows, Hkv, d, num_pages, page_size,
-    max_pages, dtype, cache dtype, pointers of k_cache, v_cache, k_scale, v_scale, block_table, kv_lens,
-    cu_seqlens). Each attribute of a tensor is read once: a decode step is shorter than a careless check."""
-    shape, cache = rows.shape, k_cache.shape
-    dt, cdt = _DTYPE.get(rows.dtype), _CACHE_DTYPE.get(k_cache.dtype)
-    dev = rows.get_device()
-    if cu_seqlens is not None:
-        B, T, cu = cu_seqlens.shape[0] - 1, shape[0], cu_seqlens.data_ptr()
-        ok = cu_seqlens.dtype is torch.int32 and cu_seqlens.is_contiguous() and cu_seqlens.get_device() == dev
-    else:
-        B = kv_lens.shape[0] if B is None else B
-        T = (shape[0] // B if B else 0) if T is None else T
-        cu = None
-        ok = B * T == shape[0]
-    ks = vs = None
-    if cdt is not None and cdt >= GDN_FP8 and k_scale is not None and v_scale is not None:
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-        ok = (ok and k_scale.shape == cache[:3] and v_scale.shape == cache[:3] and k_scale.dtype is torch.float32
-              and v_scale.dtype is torch.float32 and k_scale.is_contiguous() and v_scale.is_contiguous()
-              and k_scale.get_device() == dev and v_scale.get_device() == dev)
-    elif cdt is not None and cdt >= GDN_FP8:
-        ok = False
-    table = block_table.shape
-    if not (ok and dt is not None and cdt is not None and dev >= 0 and len(shape) == 3 and len(cache) == 4
-            and len(table) == 2 and rows2.shape == shape and rows2.dtype is rows.dtype and v_cache.shape == cache
-            and v_cache.dtype is k_cache.dtype and shape[2] == cache[3] and kv_lens.shape == (B,) and table[0] == B
-            and block_table.dtype is torch.int32 and kv_lens.dtype is torch.int32
-            and k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()
-            and kv_lens.is_contiguous() and rows2.get_device() == dev and k_cache.get_device() == dev
-            and v_cache.get_device() == dev and block_table.get_device() == dev and kv_lens.get_device() == dev):
-        _refuse_kv(rows, rows2, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, B, T)
-    return (B, T, shape[1], cache[1], cache[3], cache[0], cache[2], table[1], dt, cdt, k_cache.data_ptr(),
-            v_cache.data_ptr(), ks, vs, block_table.data_ptr(), kv_lens.data_ptr(), cu)
-
-
-def _token_stride(t: torch.Tensor, packed: int):
-    """Elements from a token's rows to the next token's; None if heads or elements are not contiguous."""
-    if t.is_contiguous():
-        return packed
-    shape, stride = t.shape, t.stride()
-    if (shape[2] > 1 and stride[2] != 1) or (shape[1] > 1 and stride[1] != shape[2]):
-        return None
-    return stride[0] if shape[0] > 1 else packed
+def _load_calls():
+    """The CPython module with the paged cache calls (it checks their tensors; built beside the library)."""
+    global _calls
+    library()  # the module is linked against it
+    with _lock:
+        if _calls is None:
+            path = _build.calls_path()
+            if not os.path.exists(path):
+                raise RuntimeError(f"the binding {path} is not built; run __graft_entry__.build()")
+            loader = importlib.machinery.ExtensionFileLoader("_calls", path)
+            spec = importlib.util.spec_from_file_location("_calls", path, loader=loader)
+            _calls = importlib.util.module_from_spec(spec)
+            loader.exec_module(_calls)
+        return _calls
 
 
 def gdn_kv_write(k, v, k_cache, v_cache, block_table, kv_lens, k_scale=None, v_scale=None, cu_seqlens=None,
@@ -371,14 +311,8 @@ def gdn_kv_write(k, v, k_cache, v_cache, block_table, kv_lens, k_scale=None, v_s
     """Store new tokens' k, v [Ttot, Hkv, d] in paged caches [num_pages, Hkv, page_size, d] (of k's dtype,
     float8_e4m3fn or int8; 8-bit caches with fp32 scales [num_pages, Hkv, page_size]). kv_lens counts the
     new tokens in: token t of sequence n's T_n goes to position kv_lens[n] - T_n + t (negative: skipped)."""
-    lib = _lib or library()
-    B, T, H, Hkv, d, pages, page, width, dt, cdt, kc, vc, ks, vs, table, lens, cu = _kv_args(
-        k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, B, T)
-    k_stride, v_stride = _token_stride(k, H * d), _token_stride(v, H * d)
-    if H != Hkv or k_stride is None or v_stride is None:
-        raise ValueError(f"k and v must be [tokens, {Hkv}, {d}] with contiguous heads and elements")
-    rc = lib.gdn_kv_write(k.data_ptr(), v.data_ptr(), kc, vc, ks, vs, table, lens, cu, B, T, Hkv, d, pages, page, width,
-                          k_stride, v_stride, dt, cdt, _stream(stream, k))
+    rc = (_calls or _load_calls()).kv_write(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens,
+                                            B, T, _stream(stream, k) if k.is_cuda else 0)
     if rc:
         raise GDNError(rc, "gdn_kv_write")
 
@@ -386,14 +320,8 @@ def gdn_kv_write(k, v, k_cache, v_cache, block_table, kv_lens, k_scale=None, v_s
 def gdn_kv_read(k_cache, v_cache, block_table, kv_lens, k, v, k_scale=None, v_scale=None, cu_seqlens=None,
                 B=None, T=None, stream=None) -> None:
     """The last T_n cached rows of every sequence as values, into k, v [Ttot, Hkv, d] (padding: zeros)."""
-    lib = _lib or library()
-    B, T, H, Hkv, d, pages, page, width, dt, cdt, kc, vc, ks, vs, table, lens, cu = _kv_args(
-        k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, B, T)
-    k_stride, v_stride = _token_stride(k, H * d), _token_stride(v, H * d)
-    if H != Hkv or k_stride is None or v_stride is None:
-        raise ValueError(f"k and v must be [tokens, {Hkv}, {d}] with contiguous heads and elements")
-    rc = lib.gdn_kv_read(kc, vc, ks, vs, table, lens, cu, k.data_ptr(), v.data_ptr(), B, T, Hkv, d, pages, page, width,
-                         k_stride, v_stride, dt, cdt, _stream(stream, k))
+    rc = (_calls or _load_calls()).kv_read(k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens,
+                                           B, T, _stream(stream, k) if k.is_cuda else 0)
     if rc:
         raise GDNError(rc, "gdn_kv_read")
 
@@ -408,21 +336,15 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, kv_lens, out, k_scale=None,
     """Causal attention of the new tokens' q [Ttot, Hq, d] over their sequences' paged caches, into `out`.
     `scale` is d**-0.5 unless given. `workspace`: a uint8 CUDA tensor of gdn_paged_attn_workspace_size(...)
     bytes that a program keeps; without one the call takes it from torch's allocator."""
-    lib = _lib or library()
-    B, T, Hq, Hkv, d, pages, page, width, dt, cdt, kc, vc, ks, vs, table, lens, cu = _kv_args(
-        q, out, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, B, T)
-    q_stride = _token_stride(q, Hq * d)
-    if q_stride is None or not out.is_contiguous():
-        raise ValueError("q must have contiguous heads and elements, and out must be contiguous")
-    if workspace is None:
-        need = lib.gdn_paged_attn_workspace_size(B, T, int(cu is not None), Hq, Hkv, d)
+    if workspace is None and q.is_cuda:
+        packed = cu_seqlens is not None
+        n = kv_lens.numel() if B is None else B
+        need = gdn_paged_attn_workspace_size(n, q.shape[0] if packed else (q.shape[0] // n if n else 0), q.shape[1],
+                                             k_cache.shape[1], k_cache.shape[-1], packed)
         with torch.cuda.device(q.device), torch.cuda.stream(_torch_stream(stream, q)):
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != q.get_device() or not workspace.is_contiguous():
-        raise ValueError("the workspace must be a contiguous CUDA tensor of q's device")
-    rc = lib.gdn_paged_attn(q.data_ptr(), kc, vc, ks, vs, table, lens, cu, out.data_ptr(), B, T, Hq, Hkv, d, pages, page,
-                            width, q_stride, d ** -0.5 if scale is None else scale, dt, cdt, workspace.data_ptr(),
-                            workspace.nbytes, _stream(stream, q))
+    rc = (_calls or _load_calls()).paged_attn(q, out, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens,
+                                              B, T, scale, workspace, _stream(stream, q) if q.is_cuda else 0)
     if rc:
         raise GDNError(rc, "gdn_paged_attn")
 

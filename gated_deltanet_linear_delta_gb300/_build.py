@@ -2,8 +2,9 @@
 
 Each .cu file is compiled to an object in parallel, then linked into one
 shared library with the CUDA runtime linked statically, so the library needs
-only the NVIDIA driver at run time. The result lives in ``_lib/`` next to
-this file (git-ignored).
+only the NVIDIA driver at run time. binding.cpp becomes the CPython module
+``_calls`` beside it, linked against that library and torch. The results live
+in ``_lib/`` next to this file (git-ignored).
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB_NAME = "libgdn_gb300.so"
+CALLS_NAME = "_calls.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -36,8 +39,19 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def _torch_flags() -> tuple[list[str], list[str]]:
+    """Compiler and linker flags of a CPython module that takes torch tensors."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    return ([f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+             f"-I{sysconfig.get_paths()['include']}", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"],
+            [f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"])
+
+
 def _fingerprint() -> str:
-    h = hashlib.sha256()
+    import torch
+    h = hashlib.sha256(f"{torch.__version__} {sysconfig.get_python_version()}".encode())
     for d in (CSRC, INCLUDE):
         for f in sorted(os.listdir(d)):
             p = os.path.join(d, f)
@@ -53,12 +67,16 @@ def lib_path() -> str:
     return os.path.join(OUT_DIR, LIB_NAME)
 
 
+def calls_path() -> str:
+    return os.path.join(OUT_DIR, CALLS_NAME)
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
     """Compile every .cu under csrc/ and link libgdn_gb300.so. Returns its path."""
     os.makedirs(OUT_DIR, exist_ok=True)
     stamp = os.path.join(OUT_DIR, "build.stamp")
     fp = _fingerprint()
-    if not force and os.path.exists(lib_path()) and os.path.exists(stamp):
+    if not force and os.path.exists(lib_path()) and os.path.exists(calls_path()) and os.path.exists(stamp):
         with open(stamp) as f:
             if f.read().strip() == fp:
                 return lib_path()
@@ -75,15 +93,33 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -
             print(r.stdout + r.stderr)
         return obj
 
+    def compile_binding():
+        obj = os.path.join(OUT_DIR, "binding.o")
+        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-I{INCLUDE}",
+               *_torch_flags()[0], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj
+
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = lib_path() + f".{os.getpid()}.tmp"
-    cmd = [nv, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+    cmd = [nv, *ARCH, "-shared", "-cudart", "static", "-Xlinker", f"-soname={LIB_NAME}", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib_path())
+    tmp = calls_path() + f".{os.getpid()}.tmp"
+    cmd = [shutil.which("g++") or "c++", "-shared", "-o", tmp, binding_obj, f"-L{OUT_DIR}", f"-l:{LIB_NAME}",
+           "-Wl,-rpath,$ORIGIN", *_torch_flags()[1]]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, calls_path())
     with open(stamp, "w") as f:
         f.write(fp)
     return lib_path()

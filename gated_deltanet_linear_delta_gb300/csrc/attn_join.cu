@@ -96,6 +96,8 @@ cudaError_t launch_t(const AttnWork &w, TOut *out, int Hq, int rows, int ctas, c
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
+    // a block per row of few: with 4 rows a block, 64-row units took 46 us instead of 35 us in all, and one long
+    // session's 8 rows 45 us instead of 41 us
     cfg.gridDim = dim3((unsigned)ctas - 1, (unsigned)(rows < 16 ? rows : 16), 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = s;
