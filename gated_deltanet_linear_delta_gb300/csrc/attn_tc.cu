@@ -80,7 +80,7 @@ struct Cfg {
                          B_REV = B_REK + NR, B_COL = B_REV + NR, B_S = B_COL + COLS, B_PV = B_S + kTurns,
                          B_P = B_PV + kTurns, B_ST = B_P + 2, B_SF = B_ST + 2,
                          B_Q = B_SF + 2, B_OF = B_Q + 1, B_QF = B_OF + 1, B_QE = B_QF + 1,
-                         B_FIN = B_QE + 1, B_COUNT = B_FIN + 1;
+                         B_US = B_QE + 1 /* all S of a unit */, B_UO = B_US + 1 /* all of its O */, B_FIN = B_UO + 1, B_COUNT = B_FIN + 1;
     static constexpr uint32_t SM_INFO = SM_BAR + B_COUNT * 8;                // [2][NR] valid rows, page mask
     static constexpr uint32_t SM_TMEM = SM_INFO + (NR ? 2 * NR : 1) * 8;
     static constexpr uint32_t SM_PLAN = (SM_TMEM + 8 + 15) & ~15u;
@@ -135,7 +135,8 @@ struct Ring {
         }
     }
 };
-// barrier and phase of tile t's S (or PV) product
+// Wait for tile t's S (or PV) product. The barrier's phases come round: only for a reader that follows the
+// tiles closely (it knows that tile t - 8's is done, and tile t + 8's waits for itself).
 template <int D, int KIND>
 __device__ __forceinline__ bool product_done(uint64_t *bar, int which, uint32_t t, long long budget) {
     using C = Cfg<D, KIND>;
@@ -253,7 +254,7 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
     uint32_t t = 0, unit = 0, o_free = 0;  // tiles whose S is issued, units begun, phase of B_OF
     // The waits for tiles come before the one for P, which is the last to be met: what follows it is issued at once.
     auto k_ready = [&]() -> bool { return warp_wait_spin(bar + C::B_FK + rk.slot, rk.phase, p.budget); };
-    auto product_s = [&]() {
+    auto product_s = [&](bool last) {
         tc_fence_after();
         const uint64_t d = desc_k + (uint64_t)(rk.slot * (C::SLOT >> 4));
         const uint32_t to = tmem + C::TM_S + (t & 1) * BN;
@@ -262,6 +263,7 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
             mma_f16_ts_by(lead, to, tmem + C::TM_Q + 8 * ks, d + (uint64_t)(((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4),
                           ID_S, ks > 0);
         mma_commit_by(lead, bar + C::B_S + (t & (C::kTurns - 1)));
+        if (last) mma_commit_by(lead, bar + C::B_US);
         rk.next();
         ++t;
     };
@@ -282,7 +284,7 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
         }
         return true;
     };
-    auto product_o = [&](uint32_t o, bool first) -> bool {
+    auto product_o = [&](uint32_t o, bool first, bool last) -> bool {
         if (!warp_wait_spin(bar + C::B_P + (o & 1), (o >> 1) & 1, p.budget)) return false;
         tc_fence_after();
         const uint64_t d = desc_v + (uint64_t)(rv.slot * (C::SLOT >> 4));
@@ -292,10 +294,11 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
             mma_f16_ts_by(lead, tmem + C::TM_O, a + (ks < BN / 32 ? 8 * ks : BN / 2 + 8 * (ks - BN / 32)),
                           d + (uint64_t)(ks * 128), ID_O, !first || ks > 0);
         mma_commit_by(lead, bar + C::B_PV + (o & (C::kTurns - 1)));
+        if (last) mma_commit_by(lead, bar + C::B_UO);
         rv.next();
         return true;
     };
-    bool ok = true, prev_first = false;
+    bool ok = true, prev_first = false, prev_last = false;
     int prev_valid = BN;
     if (k.pc.left > 0) {
         do {
@@ -304,14 +307,15 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
             ++unit;
             for (int jj = 0; jj < n && ok; ++jj) {
                 const bool more = jj + 1 < n || k.pc.left > n;  // another tile follows in the piece
-                product_s();
-                if (t > 1) ok = v_ready(t - 2, prev_first, prev_valid) && product_o(t - 2, prev_first);
+                product_s(jj + 1 == n);
+                if (t > 1) ok = v_ready(t - 2, prev_first, prev_valid) && product_o(t - 2, prev_first, prev_last);
                 if (ok && more) ok = k_ready();
                 prev_first = jj == 0;
+                prev_last = jj + 1 == n;
                 prev_valid = left - jj * BN;
             }
         } while (ok && walk_next<BN>(p.w, &k));
-        ok = ok && v_ready(t - 1, prev_first, prev_valid) && product_o(t - 1, prev_first);
+        ok = ok && v_ready(t - 1, prev_first, prev_valid) && product_o(t - 1, prev_first, true);
     }
     if (!ok && lane == 0) flag_error(p.w.pg.status);
     mma_commit_by(lead, bar + C::B_FIN);  // all products done before TMEM is given back
@@ -624,15 +628,13 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
     };
     if (k.pc.left > 0) {
         put(k, prepare(k), 0);
-        uint32_t t = 0;
         bool more = true;
         for (uint32_t unit = 0; more && ok; ++unit) {
             const int n = k.take();
-            t += n;
             Walk next = k;
             more = walk_next<BN>(p.w, &next);
             const int e = more ? prepare(next) : 0;
-            ok = __all_sync(0xffffffffu, ok && product_done<D, KIND>(bar, C::B_S, t - 1, p.budget));  // Q has been used
+            ok = ok && warp_wait_spin(bar + C::B_US, unit & 1, p.budget);  // Q has been used
             if (!ok) break;
             tc_fence_after();
             if (more) put(next, e, unit + 1);
@@ -642,7 +644,7 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
             const float m = a.x, l = a.y + b.y;  // (both halves have the same reference)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + C::B_SF + (unit & 1));
-            ok = __all_sync(0xffffffffu, product_done<D, KIND>(bar, C::B_PV, t - 1, p.budget));
+            ok = warp_wait_spin(bar + C::B_UO, unit & 1, p.budget);
             if (!ok) break;
             const int rows = unit_rows(k);
             if (quarter * 32 < rows) {
@@ -728,6 +730,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         mbar_init(bar + C::B_Q, kGroup);
         mbar_init(bar + C::B_OF, kGroup);
         mbar_init(bar + C::B_QF, 1);
+        mbar_init(bar + C::B_US, 1);
+        mbar_init(bar + C::B_UO, 1);
         mbar_init(bar + C::B_QE, kGroup);
         mbar_init(bar + C::B_FIN, 1);
         fence_mbar_init();

@@ -112,6 +112,76 @@ def test_split_rows_do_not_depend_on_their_company(dtype, cache):
     assert_attention(outs[0], ref, mag, err)
 
 
+def formula64(q, k, v, lens, new, scale):
+    """(out, sum_j p_j |v_j|) in fp64 on the GPU, sequence by sequence; k, v: lists of [len, Hkv, d]."""
+    out, mag = torch.zeros(q.shape, dtype=torch.float64, device=DEV), torch.zeros(q.shape, dtype=torch.float64, device=DEV)
+    first = 0
+    for kk, vv, x, T in zip(k, v, lens, new):
+        for a in range(0, T if x else 0, 256):
+            b = min(T, a + 256)
+            qq = q[first + a:first + b].double().unflatten(1, (kk.shape[1], -1))
+            s = torch.einsum("tghd,jgd->tghj", qq, kk.double()) * scale
+            hidden = torch.arange(x, device=DEV)[None, :] > (x - T + torch.arange(a, b, device=DEV))[:, None]
+            p = s.masked_fill(hidden[:, None, None], -float("inf")).softmax(-1)
+            out[first + a:first + b] = torch.einsum("tghj,jgd->tghd", p, vv.double()).flatten(1, 2)
+            mag[first + a:first + b] = torch.einsum("tghj,jgd->tghd", p, vv.double().abs()).flatten(1, 2)
+        first += T
+    return out, mag
+
+
+@pytest.mark.parametrize("cache", sorted(CACHES))
+@pytest.mark.parametrize("lens,new,Hkv,G,d,page", [
+    ([9001], [700], 2, 8, 256, 64),                       # a fragment: long units, few per CTA
+    ([7000, 6500, 8003], [300, 1, 511], 4, 4, 128, 32),   # fragments of several sequences
+    ([3000], [3000], 2, 8, 64, 16),                       # a prompt: many units of every length per CTA
+    ([1025, 2047, 311, 64], [1025, 2047, 311, 64], 8, 4, 128, 128),
+    ([777] * 40, [1] * 40, 8, 4, 128, 16),                # decode with many units per CTA
+    ([20000, 15000], [2, 2], 1, 8, 256, 256),             # a few tokens over long caches
+    ([5000] * 3, [64] * 3, 1, 1, 64, 16),
+])
+def test_long_units(lens, new, Hkv, G, d, page, cache):
+    """Units of many key tiles and many units per CTA (the small cases above give a CTA a few tiles each)."""
+    gen = torch.Generator(device=DEV).manual_seed(len(lens) + d)
+    pages = [-(-x // page) for x in lens]
+    table = torch.full((len(lens), max(pages)), -7, dtype=torch.int32, device=DEV)
+    order = torch.randperm(sum(pages) + 2, generator=gen, device=DEV).to(torch.int32)
+    at = 0
+    for n, u in enumerate(pages):
+        table[n, :u] = order[at:at + u]
+        at += u
+    kv_lens = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    kind = CACHES[cache] or torch.bfloat16
+    pool = (sum(pages) + 2, Hkv, page, d)
+    kc, vc = (torch.full(pool, 0x7F, dtype=torch.uint8, device=DEV).view(kind) if cache != "same"
+              else torch.full(pool, float("nan"), dtype=kind, device=DEV) for _ in range(2))
+    ks, vs = ((torch.full(pool[:-1], float("nan"), device=DEV) if cache != "same" else None) for _ in range(2))
+    k, v = (torch.randn(sum(lens), Hkv, d, generator=gen, device=DEV).to(torch.bfloat16) for _ in range(2))
+    # scores that grow along the cache, so that the running maximum moves in many tiles
+    ramp = torch.cat([torch.linspace(0.3, 2.0, x, device=DEV) for x in lens])
+    k = (k.float() * ramp[:, None, None]).to(torch.bfloat16)
+    gdn.gdn_kv_write(k, v, kc, vc, table, kv_lens, ks, vs, cu_seqlens=cu_of(lens))
+    kr, vr = (torch.empty(k.shape, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    gdn.gdn_kv_read(kc, vc, table, kv_lens, kr, vr, ks, vs, cu_seqlens=cu_of(lens))
+    if cache == "int8":  # values of more than 8 bits: their bf16 rounding is not what the attention sees
+        rows = torch.cat([torch.stack([table[n, torch.arange(x, device=DEV) // page].long(),
+                                       torch.arange(x, device=DEV) % page], 1) for n, x in enumerate(lens)])
+        kr, vr = (c[rows[:, 0], :, rows[:, 1]].double() * s[rows[:, 0], :, rows[:, 1]].double()[..., None]
+                  for c, s in ((kc, ks), (vc, vs)))
+    q = torch.randn(sum(new), Hkv * G, d, generator=gen, device=DEV).to(torch.bfloat16)
+    out = torch.full_like(q, float("nan"))
+    cu = None if len(set(new)) == 1 else cu_of(new)
+    gdn.gdn_paged_attn(q, kc, vc, table, kv_lens, out, ks, vs, cu_seqlens=cu)
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    cut = lambda x: list(torch.split(x, lens))  # noqa: E731
+    ref, mag = formula64(q, cut(kr), cut(vr), lens, new, d ** -0.5)
+    bound = 2.0 ** -8 * (ref.abs() + mag)
+    excess = ((out.double() - ref).abs() - bound).max().item()
+    assert excess <= 0, f"over the bound by {excess:.3e}"
+    again = torch.full_like(q, float("nan"))
+    gdn.gdn_paged_attn(q, kc, vc, table, kv_lens, again, ks, vs, cu_seqlens=cu)
+    assert torch.equal(out, again)
+
+
 def test_fragments_of_a_prompt_equal_the_whole():
     """A prompt stored and attended in fragments gives what the whole prompt gives at once."""
     Hq, Hkv, d, T = 8, 2, 256, 333
