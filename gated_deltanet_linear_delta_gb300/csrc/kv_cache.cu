@@ -7,9 +7,11 @@
 // Work split: a CTA takes a run of tokens. Where each lies (its sequence, kv_lens, the page) is found
 // first, by a warp per token, into shared memory; then the CTA's lanes stream over the run's rows
 // (each token's Hkv keys, then its Hkv values), 4 rows' pieces in flight per lane before any is used.
-// Runs get longer with the number of tokens, up to 32: many small runs give a decode step's few tokens
-// a CTA each, long ones spread the look-up over more bytes (a token per warp read 3.4 TB/s of a long
-// session, because the look-up's three dependent reads stood before every 1 KiB).
+// Runs get longer with the number of tokens: many small runs give a decode step's few tokens a CTA
+// each, long ones spread the look-up over more bytes (with a token per warp, whose three dependent
+// reads stood before every 1 KiB, a long session was read at 3.4 TB/s; with runs at 6.0).
+#include <algorithm>
+
 #include "kv_pages.cuh"
 
 namespace gdn {
@@ -219,9 +221,10 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv_copy_kernel(const KvArgs a, 
 
 template <bool WRITE, typename T, int KIND, int D>
 cudaError_t launch_kv(const KvArgs &a, cudaStream_t s) {
-    // a CTA per token until there are 8 per SM, then runs of up to 32
-    const long per = a.pg.Ttot / (152 * 8);
-    const int run = (int)(per < 1 ? 1 : per < kMaxRun ? per : kMaxRun);
+    // A CTA per token until there are 8 per SM, then runs of up to 128 rows: of 2 key heads' tokens 32 (reading a
+    // long session: 67 us, at 32 rows a run 129 us), of 8 key heads' 8 (a prompt's write 33 us, at 512 rows 37 us).
+    const long per = a.pg.Ttot / (152 * 8), most = 128 / (2 * a.pg.Hkv);
+    const int run = (int)std::max(1L, std::min(std::min(per, most), (long)kMaxRun));
     const long blocks = (a.pg.Ttot + run - 1) / run;
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     int shift = 0;
