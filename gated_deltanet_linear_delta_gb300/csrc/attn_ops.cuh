@@ -24,6 +24,21 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Wait for a phase, with a limit in SM cycles. The limit is looked at before the thread first sleeps
+// inside try_wait, so that a limit of a few cycles makes every wait run out that is not over already.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t phase, long long budget) {
+    if (tc::mbar_test_wait(bar, phase)) return true;
+    const long long t0 = clock64();
+    do {
+        if (clock64() - t0 > budget) return false;
+    } while (!tc::mbar_try_wait(bar, phase));
+    return true;
+}
+// ... whose outcome the whole warp shares
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, long long budget) {
+    return __all_sync(0xffffffffu, wait_for(bar, phase, budget));
+}
+
 // two fp32 operations in one instruction
 struct F2 {
     unsigned long long v;

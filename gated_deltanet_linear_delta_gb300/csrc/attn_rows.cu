@@ -213,7 +213,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             --fills;
         };
         auto wait_full = [&] {
-            if (!failed) failed = !mbar_wait_spin(bar + uslot, uphase, p.budget);
+            if (!failed) failed = !wait_for(bar + uslot, uphase, p.budget);
             failed = __any_sync(0xffffffffu, failed);
         };
         auto release = [&] {  // the slot at hand has been read

@@ -101,14 +101,6 @@ struct TcParams {
 
 __device__ __forceinline__ uint32_t bf2(float a, float b) { return bf2_bits(__floats2bfloat162_rn(a, b)); }
 
-// A wait whose outcome the whole warp shares
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t phase, long long budget) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, phase, budget));
-}
-__device__ __forceinline__ bool warp_wait_spin(uint64_t *bar, uint32_t phase, long long budget) {
-    return __all_sync(0xffffffffu, mbar_wait_spin(bar, phase, budget));
-}
-
 // every thread's view of the walk over the piece's units
 struct Walk {
     Piece pc;
@@ -140,7 +132,7 @@ struct Ring {
 template <int D, int KIND>
 __device__ __forceinline__ bool product_done(uint64_t *bar, int which, uint32_t t, long long budget) {
     using C = Cfg<D, KIND>;
-    return mbar_wait_spin(bar + which + (t & (C::kTurns - 1)), (t / C::kTurns) & 1, budget);
+    return wait_for(bar + which + (t & (C::kTurns - 1)), (t / C::kTurns) & 1, budget);
 }
 
 // ---- loads ------------------------------------------------------------------------
@@ -253,7 +245,7 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
     Ring<C::NV> rv;
     uint32_t t = 0, unit = 0, o_free = 0;  // tiles whose S is issued, units begun, phase of B_OF
     // The waits for tiles come before the one for P, which is the last to be met: what follows it is issued at once.
-    auto k_ready = [&]() -> bool { return warp_wait_spin(bar + C::B_FK + rk.slot, rk.phase, p.budget); };
+    auto k_ready = [&]() -> bool { return warp_wait(bar + C::B_FK + rk.slot, rk.phase, p.budget); };
     auto product_s = [&](bool last) {
         tc_fence_after();
         const uint64_t d = desc_k + (uint64_t)(rk.slot * (C::SLOT >> 4));
@@ -269,7 +261,7 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
     };
     // V of tile o, `first` of its unit, with `valid` positions before the end, ready to be multiplied
     auto v_ready = [&](uint32_t o, bool first, int valid) -> bool {
-        if (!warp_wait_spin(bar + C::B_FV + rv.slot, rv.phase, p.budget)) return false;
+        if (!warp_wait(bar + C::B_FV + rv.slot, rv.phase, p.budget)) return false;
         if (!C::kCodes && valid < BN) {  // rows of V past the end: zeros
             const int dead = (BN - valid) * 8;
             for (int e = lane; e < dead * C::NB; e += 32)
@@ -279,13 +271,13 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
             __syncwarp();
         }
         if (first && o > 0) {  // the unit before has been taken out of O
-            if (!warp_wait_spin(bar + C::B_OF, o_free, p.budget)) return false;
+            if (!warp_wait(bar + C::B_OF, o_free, p.budget)) return false;
             o_free ^= 1;
         }
         return true;
     };
     auto product_o = [&](uint32_t o, bool first, bool last) -> bool {
-        if (!warp_wait_spin(bar + C::B_P + (o & 1), (o >> 1) & 1, p.budget)) return false;
+        if (!warp_wait(bar + C::B_P + (o & 1), (o >> 1) & 1, p.budget)) return false;
         tc_fence_after();
         const uint64_t d = desc_v + (uint64_t)(rv.slot * (C::SLOT >> 4));
         const uint32_t a = tmem + C::TM_S + (o & 1) * BN;
@@ -303,7 +295,7 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
     if (k.pc.left > 0) {
         do {
             const int n = k.take(), left = k.pc.s.len - k.pc.off * BN;
-            ok = warp_wait_spin(bar + C::B_Q, unit & 1, p.budget) && (t > 0 || k_ready());
+            ok = warp_wait(bar + C::B_Q, unit & 1, p.budget) && (t > 0 || k_ready());
             ++unit;
             for (int jj = 0; jj < n && ok; ++jj) {
                 const bool more = jj + 1 < n || k.pc.left > n;  // another tile follows in the piece
@@ -374,7 +366,7 @@ __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, uint
     Ring<C::NR> raw;
     bool ok = true;
     for (uint32_t t = 0; t < tiles; ++t) {  // all the piece's, whatever units they belong to
-        bool got = mbar_wait_spin(bar + (IS_V ? C::B_RV : C::B_RK) + raw.slot, raw.phase, p.budget);
+        bool got = wait_for(bar + (IS_V ? C::B_RV : C::B_RK) + raw.slot, raw.phase, p.budget);
         if (t >= N) got = got && product_done<D, KIND>(bar, IS_V ? C::B_PV : C::B_S, t - N, p.budget);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
@@ -438,7 +430,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
         for (int jj = 0; jj < n; ++jj, ++t) {
             const uint32_t b = t & 1;
             if (!late) late = !product_done<D, KIND>(bar, C::B_S, t, p.budget);
-            if (C::kCodes && !late) late = !mbar_wait_spin(bar + C::B_COL + t % C::COLS, (t / C::COLS) & 1, p.budget);
+            if (C::kCodes && !late) late = !wait_for(bar + C::B_COL + t % C::COLS, (t / C::COLS) & 1, p.budget);
             if (!live_warp) {
                 if (lane == 0) mbar_arrive(bar + C::B_P + b);
                 continue;
@@ -533,7 +525,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
             if (lane == 0) mbar_arrive(bar + C::B_P + b);
         }
         if (!ok) break;
-        if (unit >= 2 && !late) late = !mbar_wait_spin(bar + C::B_SF + (unit & 1), ((unit >> 1) - 1) & 1, p.budget);
+        if (unit >= 2 && !late) late = !wait_for(bar + C::B_SF + (unit & 1), ((unit >> 1) - 1) & 1, p.budget);
         ok = !bar_any(bar_id, 64, late);
         if (!ok) break;
         stat[(unit & 1) * 256] = make_float2(m, l);
@@ -565,7 +557,7 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
     // 128 bytes of the unit's rows into the stage, once the four warps have read what was there
     auto fetch = [&](const Walk &w, int part) {
         if (issuer) {
-            if (fills > 0) ok = ok && mbar_wait(bar + C::B_QE, (fills - 1) & 1, p.budget);
+            if (fills > 0) ok = ok && wait_for(bar + C::B_QE, (fills - 1) & 1, p.budget);
             if (ok) {
                 mbar_expect_tx(bar + C::B_QF, bytes);
                 tma_load_3d(sm + C::SM_Q, mq, part * 64, w.pc.h * p.w.G, (int)(w.pc.s.bos + w.pc.i * p.w.TPT), bar + C::B_QF);
@@ -574,7 +566,7 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
         ++fills;
     };
     auto read = [&](uint32_t(&x)[32]) {  // this row's
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(bar + C::B_QF, (fills - 1) & 1, p.budget));
+        ok = __all_sync(0xffffffffu, ok && wait_for(bar + C::B_QF, (fills - 1) & 1, p.budget));
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             const uint4 v = *reinterpret_cast<const uint4 *>(sm + C::SM_Q + swz(row, c));
@@ -634,7 +626,7 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
             Walk next = k;
             more = walk_next<BN>(p.w, &next);
             const int e = more ? prepare(next) : 0;
-            ok = ok && warp_wait_spin(bar + C::B_US, unit & 1, p.budget);  // Q has been used
+            ok = ok && warp_wait(bar + C::B_US, unit & 1, p.budget);  // Q has been used
             if (!ok) break;
             tc_fence_after();
             if (more) put(next, e, unit + 1);
@@ -644,7 +636,7 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
             const float m = a.x, l = a.y + b.y;  // (both halves have the same reference)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + C::B_SF + (unit & 1));
-            ok = warp_wait_spin(bar + C::B_UO, unit & 1, p.budget);
+            ok = warp_wait(bar + C::B_UO, unit & 1, p.budget);
             if (!ok) break;
             const int rows = unit_rows(k);
             if (quarter * 32 < rows) {
@@ -741,7 +733,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     plan_piece<C::BN, C::THREADS>(p.w, plan);  // (synchronises the CTA)
     tc_fence_after();
     // All 512 columns are this CTA's, so the allocation starts at column 0, and addresses are constants (in uniform
-    // registers; as a loaded value, each product's issue took about 45 cycles instead of ).
+    // registers; from a loaded value, the issue of each product took about 45 cycles).
     constexpr uint32_t tmem = 0;
     Walk k{plan->piece, plan->piece.off == 0};
     if (*slot != tmem) {

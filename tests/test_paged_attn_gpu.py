@@ -182,6 +182,32 @@ def test_long_units(lens, new, Hkv, G, d, page, cache):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("G,dtype,cache", [(2, "bf16", "same"), (2, "bf16", "int8"), (64, "bf16", "same"), (2, "f32", "same")])
+def test_more_sequences_than_threads(G, dtype, cache):
+    """1500 sequences, some idle: more than the kernels' threads, so the work is cut in a second pass over them."""
+    r = np.random.RandomState(8)
+    lens = [int(x) for x in r.randint(0, 60, 1500)]
+    lens[700], lens[1499] = 900, 300
+    case = Paged(lens, 1, 64, 16, cache, dtype, seed=8)
+    q, out = run(case, [1] * 1500, G)
+    assert_attention(out, *reference(case, q, [1] * 1500, 64 ** -0.5))
+
+
+@pytest.mark.parametrize("T", [1, 30])
+def test_another_stream(T):
+    """All on a stream of its own, without a workspace: torch's allocator gives it to that stream."""
+    case = Paged([400, 90], 2, 128, 16, "fp8", seed=3)
+    q = torch.randn(2 * T, 8, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        kc, vc, ks, vs, table, lens = case.tensors()
+        qd = q.to(DEV)
+        out = torch.full_like(qd, float("nan"))
+    gdn.gdn_paged_attn(qd, kc, vc, table, lens, out, ks, vs, stream=s)
+    s.synchronize()
+    assert_attention(out, *reference(case, q, [T, T], 128 ** -0.5))
+
+
 def test_fragments_of_a_prompt_equal_the_whole():
     """A prompt stored and attended in fragments gives what the whole prompt gives at once."""
     Hq, Hkv, d, T = 8, 2, 256, 333
