@@ -164,8 +164,9 @@ inline bool rows_map(CUtensorMap *m, const void *base, int d, int heads, long to
 
 // A running softmax reference m of a row (log2 domain), given its maximum over more keys: moved when
 // that has grown by more than 2^kGrow. Returns the factor for what was summed before.
+__device__ __forceinline__ bool above_reference(float m, float top) { return top > m + kGrow; }  // (-inf: any score)
 __device__ __forceinline__ bool grow_reference(float &m, float top, float &f) {
-    const bool grow = top > m + kGrow || (m == -INFINITY && top > m);
+    const bool grow = above_reference(m, top);
     f = 1.f;
     if (grow) {
         f = ex2(m - top);  // m = -inf: 0

@@ -4,20 +4,24 @@
 // With at most 16 rows (the G query heads of a key head, of a few tokens) every cached row is read
 // for 16 rows' worth of products at most, 16 to 32 flops a byte, so the kernel is bound by the bytes
 // of the cache and, for short ones, by the length of its own dependent chain. It therefore keeps
-// everything of a key chunk inside one warp: a CTA's 8 warps take 16 positions each of a 128-position
-// tile, every warp has its own ring of tiles in flight (TMA, one box per 128 bytes of row, 128B
-// swizzle), its own running softmax and its own 16 x D output in registers, and meets the others
-// only once per unit of work, in shared memory. The products are m16n8k16 (mma.sync): 16 rows fill
-// its M, where tcgen05's M of 128 would be padded 8 to 16 times and needs hand-overs between warps
-// for each tile.
+// everything of a key chunk inside one warp: a CTA's warps take 16 or 32 positions each of a tile,
+// every warp has its own ring of tiles in flight (TMA, one box per 128 bytes of row, 128B swizzle),
+// its own running softmax and its own output in registers, and meets the others only once per unit of
+// work, in shared memory. The products are m16n8k16 (mma.sync) with the cached rows as M,
+//     S^T = K Q^T,   O^T = V^T P^T,
+// so that N holds 8 query rows (R = 8) or twice 8 (R = 16) and nothing is padded to more;
+// tcgen05's M of 128 would be padded 8 to 16 times and needs hand-overs between warps for each tile.
 //
 // Fragments without shuffles. The sums over d and over keys may run in any order, so both are
 // permuted such that a thread's operands are 16-byte pieces of a row, free of bank conflicts:
-//   S = Q K^T : of a piece of row n, each 4 elements in turn are the thread's k indexes of one
-//               product; Q's fragments are laid out in the same order, once per unit;
-//   O += P V  : column n of product t is d = 8 n + t of a 64-wide block (bf16; 16 n + t of 128 for
-//               8-bit codes), so that a thread ends with 16 (32) consecutive elements of its rows;
-//   position r of a chunk stands at column c with r = g(c), g = 0 4 2 6 5 1 7 3.
+//   S^T: of a piece of a row, each 4 elements in turn are the thread's k indexes of one product;
+//        Q's fragments are laid out in the same order, once per unit;
+//   O^T: rows n and n + 8 of product t are d = 8 n + 2 t and 8 n + 2 t + 1 of a 64-wide block (bf16;
+//        16 n + 2 t of 128 for 8-bit codes), so that a thread ends with 8 (16) consecutive elements
+//        of its rows;
+//   slot c of 8 positions holds position r = g(c), g = 0 4 2 6 5 1 7 3.
+// P^T leaves the softmax as S^T's layout has it (a position's rows side by side) and becomes the B
+// operand by movmatrix, 8 x 8 at a time.
 // 8-bit codes become fp16 in registers (attn_tc.cu says why fp16, and how the scales enter).
 #include <climits>
 
@@ -28,36 +32,43 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr uint32_t kRingBytes = 24576;  // of each warp
-
-template <int D, int KIND>
+template <int D, int KIND, int R>
 struct RCfg {
     static constexpr bool kCodes = KIND == GDN_FP8 || KIND == GDN_INT8;
     static constexpr int ROWB = D * (kCodes ? 1 : 2);           // bytes of a row
+    static constexpr int NT = R / 8;                            // row tiles
+    // Codes cost a warp 300 to 500 instructions per 16 positions, and two warps per scheduler issue one every two to
+    // three cycles, so more warps help as long as registers and rings allow: int8, d = 128, 8 rows (32 sequences of
+    // 8192 positions, 8 key heads): 113, 99 and 108 us with 8, 12 and 16 warps; fp8, d = 64 (twice the positions): 161,
+    // 126 and 131. At d = 256 the output fills the registers (101, 102 and 106 us; 16 rows: 118 and 156 with 8 and 12
+    // warps), and bf16 is bound by memory with any number.
+    static constexpr int WARPS = kCodes && D < 256 ? 12 : 8;
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr uint32_t RINGB = 196608 / WARPS;           // a warp's ring
     // Positions per chunk. 32 spread what a chunk costs beside its products (waits, loads, softmax steps: half of a
     // 16-position chunk's instructions at 128-byte rows); wider rows need 16 for at least two chunks in flight.
-    static constexpr int CH = ROWB <= 128 ? 32 : 16;
-    static constexpr int U = CH / 8;                            // score tiles of a chunk
-    static constexpr int BN = kWarps * CH;                      // positions per tile of work
+    static constexpr int CH = 4 * 32 * ROWB <= RINGB ? 32 : 16;
+    static constexpr int U = CH / 16;                           // score tiles of a chunk
+    static constexpr int BN = WARPS * CH;                       // positions per tile of work
     static constexpr int BOXES = ROWB >= 128 ? ROWB / 128 : 1;  // TMA boxes per 16 positions
     static constexpr int LINES = ROWB >= 128 ? CH : CH / 2;     // 128-byte lines of a chunk per 128 bytes of row
     static constexpr uint32_t SLOT = CH * ROWB;                 // K or V of a chunk
     // A chunk's K and V come as one stage of the ring, unless that leaves less than two stages (bf16, D = 256):
     // then K and V take turns in slots of their own.
-    static constexpr bool kPair = kRingBytes / (2 * SLOT) >= 2;
+    static constexpr bool kPair = RINGB / (2 * SLOT) >= 2;
     static constexpr uint32_t STAGE = kPair ? 2 * SLOT : SLOT;
-    static constexpr int NSL = kRingBytes / STAGE;
+    static constexpr int NSL = RINGB / STAGE;
+    static_assert(NSL >= 2 && (kPair || CH == 16), "ring");
     static constexpr int KS = D / 16;                           // products per score tile
     static constexpr int VE = kCodes ? (D == 64 ? 8 : 16) : 8;  // elements per piece of V
     static constexpr int MSTRIDE = D + 4;                       // floats per row where warps meet
-    static constexpr uint32_t RING = kWarps * NSL * STAGE, MEET = kWarps * 16 * MSTRIDE * 4;
-    static constexpr uint32_t SM_Q = RING > MEET ? RING : MEET;  // Q fragments [KS][32 lanes][16 bytes]
-    static constexpr uint32_t SM_SC = SM_Q + KS * 512;           // [warp][NSL][k, v][CH] scales
-    static constexpr uint32_t SM_ML = SM_SC + (kCodes ? kWarps * NSL * 2 * CH * 4 : 0);  // [warp][16] m, l
-    static constexpr uint32_t SM_RS = SM_ML + kWarps * 16 * 8;   // [16] Q row scales, and factors
-    static constexpr uint32_t SM_BAR = SM_RS + 16 * 4;
-    static constexpr uint32_t SM_PLAN = SM_BAR + kWarps * NSL * 8;
+    static constexpr uint32_t RING = WARPS * NSL * STAGE, MEET = WARPS * R * MSTRIDE * 4;
+    static constexpr uint32_t SM_Q = RING > MEET ? RING : MEET;  // Q fragments [KS / 2][NT][32 lanes][16 bytes]
+    static constexpr uint32_t SM_SC = SM_Q + KS * NT * 256;      // [warp][NSL][k, v][CH] scales
+    static constexpr uint32_t SM_ML = SM_SC + (kCodes ? WARPS * NSL * 2 * CH * 4 : 0);  // [warp][R] m, l
+    static constexpr uint32_t SM_RS = SM_ML + WARPS * R * 8;     // [R] Q row scales
+    static constexpr uint32_t SM_BAR = SM_RS + R * 4;
+    static constexpr uint32_t SM_PLAN = SM_BAR + WARPS * NSL * 8;
     static constexpr uint32_t SM_BYTES = SM_PLAN + sizeof(PlanSmem) + 1024;
     static_assert(SM_BYTES <= 232448, "over the 227 KiB opt-in limit");
 };
@@ -83,22 +94,29 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) {
 }
 
 template <bool F16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
     if (F16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {  // of 16-bit elements; every lane of the warp
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int D, int KIND, int R>
+__global__ void __launch_bounds__(RCfg<D, KIND, R>::THREADS, 1)
 attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const RowParams p) {
-    using C = RCfg<D, KIND>;
-    constexpr int CH = C::CH, U = C::U, BN = C::BN;
+    using C = RCfg<D, KIND, R>;
+    constexpr int CH = C::CH, U = C::U, BN = C::BN, NT = C::NT, kThreads = C::THREADS, kWarps = C::WARPS;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     uint8_t *sm = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
@@ -181,8 +199,11 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 if (box < C::BOXES)
                     tma_load_3d(to + box * (C::LINES * 128), map, box * (C::kCodes ? 128 : 64), row0,
                                 good ? page * pg.Hkv + pc.h : -1, bar + fslot);
-                if (C::kCodes && good && box == 15)
-                    bulk_load(sc + (mine_v ? CH : 0), (mine_v ? p.v_scale : p.k_scale) + at, CH * 4, bar + fslot);
+                if constexpr (C::kCodes) {  // the scales of both come with K
+                    const bool of_v = C::kPair ? mine_v : lane == 14;
+                    if (good && (C::kPair ? box == 15 : !is_v && (lane & ~1) == 14))
+                        bulk_load(sc + (of_v ? CH : 0), (of_v ? p.v_scale : p.k_scale) + at, CH * 4, bar + fslot);
+                }
             } else {
                 // two boxes of 16 positions each: they may lie on two pages, and the second may lie past the end
                 const int half = box & 1, blk = box >> 1, pos = fill_pos + 16 * half;
@@ -228,7 +249,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         while (fills > 0 && filled - used_up < (uint32_t)C::NSL) issue();
 
         // Q fragments, by the whole CTA: a row's 16 bytes to the lanes that hold its elements
-        for (int e = tid; e < 16 * (D / 8); e += kThreads) {
+        for (int e = tid; e < R * (D / 8); e += kThreads) {
             const int r = e / (D / 8), c = e % (D / 8);  // row, piece of 8 elements
             uint32_t x[4] = {0, 0, 0, 0};
             if (r < rows) {
@@ -253,136 +274,186 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             if (p.negate)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] ^= 0x80008000u;
-            // elements 8 c + 4 s ..: of product ks, lane (r % 8, qq); registers r / 8 and 2 + r / 8
+            // elements 8 c + 4 s ..: of product ks, row tile r / 8, lane (r % 8, qq)
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int ks = C::kCodes ? (c / 8) * 4 + (c & 1) * 2 + s : (c / 4) * 2 + s;
                 const int qq = C::kCodes ? (c / 2) & 3 : c & 3;
-                uint32_t *dst = qf + (ks * 32 + (r & 7) * 4 + qq) * 4 + (r >> 3);
-                dst[0] = x[2 * s];
-                dst[2] = x[2 * s + 1];
+                *reinterpret_cast<uint2 *>(qf + (((ks >> 1) * NT + (r >> 3)) * 32 + (r & 7) * 4 + qq) * 4 + (ks & 1) * 2) =
+                    make_uint2(x[2 * s], x[2 * s + 1]);
             }
         }
         __syncthreads();
 
-        float o[D / 8][4];
+        // of row tile y: rows 8 y + 2 q + (i & 1), elements (tile t of 16) of n's piece, 2 t + (i >> 1)
+        float o[D / 16][NT][4];
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t)
+        for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        int limit[2];  // last position that rows n and n + 8 see
-        float rsc[2] = {1.f, 1.f};
+            for (int y = 0; y < NT; ++y)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = n + 8 * i;
-            limit[i] = r < rows ? len - pc.s.T + t0 + r / w.G : INT_MAX;  // (rows past the last are not read)
-            if (C::kCodes) rsc[i] = rs[r];
-        }
+                for (int i = 0; i < 4; ++i) o[t][y][i] = 0.f;
+        float m[NT][2], l[NT][2], rsc[NT][2];
+        int limit[NT][2];  // last position that the thread's rows see
+#pragma unroll
+        for (int y = 0; y < NT; ++y)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * y + 2 * q + i;
+                m[y][i] = -INFINITY;
+                l[y][i] = 0.f;
+                limit[y][i] = r < rows ? len - pc.s.T + t0 + r / w.G : INT_MAX;  // (rows past the last are not read)
+                rsc[y][i] = C::kCodes ? rs[r] * p.scale2 : p.scale2;
+            }
         const int sure = len - pc.s.T + t0;  // every row sees up to here
         for (int ch = 0; ch < chunks && !failed; ++ch) {
             const int pos0 = start + ch * BN;
             wait_full();
             if (failed) break;
-            constexpr int SPLIT = U == 2 ? 2 : 1;  // chains of products per score tile
-            float s[U][SPLIT][4];
+            constexpr int SPLIT = 4 / (U * NT);  // chains of products per score tile
+            float s[U][NT][SPLIT][4];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int y = 0; y < SPLIT; ++y)
+                for (int y = 0; y < NT; ++y)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s[u][y][i] = 0.f;
+                    for (int z = 0; z < SPLIT; ++z)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[u][y][z][i] = 0.f;
             const uint8_t *kc = ring + uslot * C::STAGE;
             constexpr int KP = C::kCodes ? 4 : 2;  // products per piece
 #pragma unroll
             for (int i = 0; i < C::KS / KP; ++i) {
-                uint4 a[KP];
+                uint4 b[KP / 2][NT];
 #pragma unroll
-                for (int x = 0; x < KP; ++x) a[x] = *reinterpret_cast<const uint4 *>(qf + ((i * KP + x) * 32 + lane) * 4);
+                for (int x = 0; x < KP / 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < NT; ++y)
+                        b[x][y] = *reinterpret_cast<const uint4 *>(qf + (((i * KP / 2 + x) * NT + y) * 32 + lane) * 4);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const uint4 b = *reinterpret_cast<const uint4 *>(kc + piece_at<C::ROWB, CH>(u * 8 + gn, 4 * i + q));
+                    const uint4 k0 = *reinterpret_cast<const uint4 *>(kc + piece_at<C::ROWB, CH>(u * 16 + gn, 4 * i + q));
+                    const uint4 k1 = *reinterpret_cast<const uint4 *>(kc + piece_at<C::ROWB, CH>(u * 16 + 8 + gn, 4 * i + q));
                     if constexpr (C::kCodes) {
-                        const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+                        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            uint32_t h0, h1;
-                            codes4_to_f16<KIND>(bw[x], h0, h1);
-                            mma16816<true>(s[u][x & (SPLIT - 1)], a[x], h0, h1);
+                            uint32_t a0, a1, a2, a3;
+                            codes4_to_f16<KIND>(w0[x], a0, a2);
+                            codes4_to_f16<KIND>(w1[x], a1, a3);
+#pragma unroll
+                            for (int y = 0; y < NT; ++y) {
+                                const uint4 &c = b[x >> 1][y];
+                                mma16816<true>(s[u][y][x & (SPLIT - 1)], a0, a1, a2, a3, x & 1 ? c.z : c.x, x & 1 ? c.w : c.y);
+                            }
                         }
                     } else {
-                        mma16816<false>(s[u][0], a[0], b.x, b.y);
-                        mma16816<false>(s[u][SPLIT - 1], a[1], b.z, b.w);
+#pragma unroll
+                        for (int y = 0; y < NT; ++y) {
+                            mma16816<false>(s[u][y][2 * i & (SPLIT - 1)], k0.x, k1.x, k0.y, k1.y, b[0][y].x, b[0][y].y);
+                            mma16816<false>(s[u][y][2 * i + 1 & (SPLIT - 1)], k0.z, k1.z, k0.w, k1.w, b[0][y].z, b[0][y].w);
+                        }
                     }
                 }
             }
             float iv[U][2];
-            float x[U][4];  // [score tile]: rows n, n, n + 8, n + 8; columns 2 q, 2 q + 1, ..
+            float x[U][NT][4];  // [score tile][row tile]: position 16 u + gn: 2 rows, then 16 u + 8 + gn: 2 rows
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[u][i] = SPLIT == 2 ? s[u][0][i] + s[u][SPLIT - 1][i] : s[u][0][i];
+                for (int y = 0; y < NT; ++y)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[u][y][i] = s[u][y][0][i];
+#pragma unroll
+                        for (int z = 1; z < SPLIT; ++z) x[u][y][i] += s[u][y][z][i];
+                    }
                 if constexpr (C::kCodes) {
-                    const float *sc = scales + uslot * 2 * CH + u * 8;
+                    const float *sc = scales + uslot * 2 * CH + u * 16 + gn;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float a = sc[g2 ^ (4 * j)] * p.scale2;
-                        float vs = sc[CH + (g2 ^ (4 * j))];
+                        const float a = sc[8 * j];
+                        float vs = sc[CH + 8 * j];
                         if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
                         const float lv = lg2(vs);
                         iv[u][j] = vs == vs ? rcp(vs) : 0.f;  // a NaN enters by lv, and not where it is masked
-                        x[u][j] = fmaf(x[u][j] * rsc[0], a, lv);
-                        x[u][2 + j] = fmaf(x[u][2 + j] * rsc[1], a, lv);
+#pragma unroll
+                        for (int y = 0; y < NT; ++y)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) x[u][y][2 * j + i] = fmaf(x[u][y][2 * j + i] * rsc[y][i], a, lv);
                     }
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[u][i] *= p.scale2;
+                    for (int y = 0; y < NT; ++y)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[u][y][i] *= rsc[y][i & 1];
                 }
             }
             if (!C::kPair) release();
             if (pos0 + CH - 1 > sure) {
-                const int lim[2] = {limit[0] - pos0 - g2, limit[1] - pos0 - g2}, lim4[2] = {limit[0] - pos0 - (g2 ^ 4), limit[1] - pos0 - (g2 ^ 4)};
+#pragma unroll
+                for (int y = 0; y < NT; ++y)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int lim = limit[y][i & 1] - pos0 - gn;
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            if (u * 16 + 8 * (i >> 1) > lim) x[u][y][i] = -INFINITY;
+                    }
+            }
+            // The reference moves when a score is far above it (kGrow), so each lane looks at its own scores, and the
+            // rows' maxima are brought together over the lanes only when one of them found such a score.
+            float top[NT][2];
+            bool grow = false;
+#pragma unroll
+            for (int y = 0; y < NT; ++y)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    top[y][i] = fmaxf(x[0][y][i], x[0][y][2 + i]);
+#pragma unroll
+                    for (int u = 1; u < U; ++u) top[y][i] = fmaxf(top[y][i], fmaxf(x[u][y][i], x[u][y][2 + i]));
+                    grow |= above_reference(m[y][i], top[y][i]);
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+                float f[NT][2];
+#pragma unroll
+                for (int y = 0; y < NT; ++y)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                        for (int d = 4; d < 32; d *= 2)
+                            top[y][i] = fmaxf(top[y][i], __shfl_xor_sync(0xffffffffu, top[y][i], d));
+                        grow_reference(m[y][i], top[y][i], f[y][i]);
+                        l[y][i] *= f[y][i];
+                    }
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                    for (int y = 0; y < NT; ++y)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[t][y][i] *= f[y][i & 1];
+            }
+            uint32_t pt[U][NT][2];  // P^T as the B operand
+#pragma unroll
+            for (int y = 0; y < NT; ++y) {
+                const float ref0 = m[y][0] == -INFINITY ? 0.f : m[y][0], ref1 = m[y][1] == -INFINITY ? 0.f : m[y][1];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (u * 8 > ((i & 1) ? lim4[i >> 1] : lim[i >> 1])) x[u][i] = -INFINITY;
-            }
-            float f[2];
-            bool grow = false;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float top = fmaxf(x[0][2 * i], x[0][2 * i + 1]);
-#pragma unroll
-                for (int u = 1; u < U; ++u) top = fmaxf(top, fmaxf(x[u][2 * i], x[u][2 * i + 1]));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                grow |= grow_reference(m[i], top, f[i]);
-                l[i] *= f[i];
-            }
-            if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                for (int t = 0; t < D / 8; ++t) {
-                    o[t][0] *= f[0]; o[t][1] *= f[0];
-                    o[t][2] *= f[1]; o[t][3] *= f[1];
-                }
-            }
-            uint32_t pr[U / 2][4];  // P as the A operand of U / 2 products
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float ref = m[i] == -INFINITY ? 0.f : m[i];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float e0 = ex2(x[u][2 * i] - ref), e1 = ex2(x[u][2 * i + 1] - ref);
-                    if constexpr (C::kCodes) {
-                        l[i] = fmaf(e0, iv[u][0], l[i]);
-                        l[i] = fmaf(e1, iv[u][1], l[i]);
-                        pr[u >> 1][2 * (u & 1) + i] = h2_bits(e0, e1);
-                    } else {
-                        l[i] += e0 + e1;
-                        pr[u >> 1][2 * (u & 1) + i] = bf2_bits(__floats2bfloat162_rn(e0, e1));
+                    for (int j = 0; j < 2; ++j) {
+                        const float e0 = ex2(x[u][y][2 * j] - ref0), e1 = ex2(x[u][y][2 * j + 1] - ref1);
+                        uint32_t both;
+                        if constexpr (C::kCodes) {
+                            l[y][0] = fmaf(e0, iv[u][j], l[y][0]);
+                            l[y][1] = fmaf(e1, iv[u][j], l[y][1]);
+                            both = h2_bits(e0, e1);
+                        } else {
+                            l[y][0] += e0;
+                            l[y][1] += e1;
+                            both = bf2_bits(__floats2bfloat162_rn(e0, e1));
+                        }
+                        pt[u][y][j] = transpose8x8(both);
                     }
-                }
             }
             if constexpr (!C::kPair) {
                 wait_full();
@@ -391,14 +462,13 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             const uint8_t *vc = ring + uslot * C::STAGE + (C::kPair ? C::SLOT : 0);
             const bool tail = pos0 + CH > len;  // rows past the end: zeros
 #pragma unroll
-            for (int hk = 0; hk < U / 2; ++hk) {
-                const uint4 pa = make_uint4(pr[hk][0], pr[hk][1], pr[hk][2], pr[hk][3]);
+            for (int u = 0; u < U; ++u) {
 #pragma unroll
                 for (int b = 0; b < D / (8 * C::VE); ++b) {
                     uint32_t v[4][4];  // positions g2, g2 ^ 4, 8 + g2, 8 + (g2 ^ 4)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int r = hk * 16 + (j >> 1) * 8 + (g2 ^ (4 * (j & 1)));
+                        const int r = u * 16 + (j >> 1) * 8 + (g2 ^ (4 * (j & 1)));
                         if (C::VE * (C::kCodes ? 1 : 2) == 16) {
                             const uint4 y = *reinterpret_cast<const uint4 *>(vc + piece_at<C::ROWB, CH>(r, b * 8 + n));
                             v[j][0] = y.x; v[j][1] = y.y; v[j][2] = y.z; v[j][3] = y.w;
@@ -408,26 +478,22 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         }
                         if (tail && pos0 + r >= len) v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
                     }
-                    if constexpr (C::kCodes) {
 #pragma unroll
-                        for (int wd = 0; wd < C::VE / 4; ++wd) {
-#pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {  // elements 4 wd + 2 hf, + 1
-                                uint32_t b0[2], b1[2];
-                                codes4_to_f16<KIND>(__byte_perm(v[0][wd], v[1][wd], hf ? 0x7362 : 0x5140), b0[0], b0[1]);
-                                codes4_to_f16<KIND>(__byte_perm(v[2][wd], v[3][wd], hf ? 0x7362 : 0x5140), b1[0], b1[1]);
-#pragma unroll
-                                for (int y = 0; y < 2; ++y)
-                                    mma16816<true>(o[b * C::VE + 4 * wd + 2 * hf + y], pa, b0[y], b1[y]);
-                            }
+                    for (int t = 0; t < C::VE / 2; ++t) {  // elements 2 t, 2 t + 1 of the pieces
+                        uint32_t a0, a1, a2, a3;
+                        if constexpr (C::kCodes) {
+                            const int wd = t >> 1, sel = t & 1 ? 0x7362 : 0x5140;
+                            codes4_to_f16<KIND>(__byte_perm(v[0][wd], v[1][wd], sel), a0, a1);
+                            codes4_to_f16<KIND>(__byte_perm(v[2][wd], v[3][wd], sel), a2, a3);
+                        } else {
+                            a0 = __byte_perm(v[0][t], v[1][t], 0x5410);
+                            a1 = __byte_perm(v[0][t], v[1][t], 0x7632);
+                            a2 = __byte_perm(v[2][t], v[3][t], 0x5410);
+                            a3 = __byte_perm(v[2][t], v[3][t], 0x7632);
                         }
-                    } else {
 #pragma unroll
-                        for (int t = 0; t < 8; ++t) {
-                            const uint32_t sel = t & 1 ? 0x7632 : 0x5410;
-                            mma16816<false>(o[b * 8 + t], pa, __byte_perm(v[0][t / 2], v[1][t / 2], sel),
-                                            __byte_perm(v[2][t / 2], v[3][t / 2], sel));
-                        }
+                        for (int y = 0; y < NT; ++y)
+                            mma16816<C::kCodes>(o[b * (C::VE / 2) + t][y], a0, a1, a2, a3, pt[u][y][0], pt[u][y][1]);
                     }
                 }
             }
@@ -436,40 +502,39 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         // the warps meet: O over the rings, which are empty now
         if (__syncthreads_or(failed)) break;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = n + 8 * i;
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-            if (q == 0) ml[warp * 16 + r] = make_float2(m[i], l[i]);
-            if (r < rows && chunks > 0) {
-                // columns 2 q and 2 q + 1 of products 0 .. VE - 1 of a block: 2 VE consecutive elements
-                float *dst = reinterpret_cast<float *>(sm) + (warp * 16 + r) * C::MSTRIDE + q * 2 * C::VE;
+        for (int y = 0; y < NT; ++y)
 #pragma unroll
-                for (int b = 0; b < D / (8 * C::VE); ++b)
+            for (int i = 0; i < 2; ++i) {
+                const int r = 8 * y + 2 * q + i;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                for (int d = 4; d < 32; d *= 2) l[y][i] += __shfl_xor_sync(0xffffffffu, l[y][i], d);
+                if (n == 0) ml[warp * R + r] = make_float2(m[y][i], l[y][i]);
+                if (r < rows && chunks > 0) {
+                    float *dst = reinterpret_cast<float *>(sm) + (warp * R + r) * C::MSTRIDE + n * C::VE;
 #pragma unroll
-                        for (int t = 0; t < C::VE; t += 4)
-                            *reinterpret_cast<float4 *>(dst + b * 8 * C::VE + j * C::VE + t) =
-                                make_float4(o[b * C::VE + t][2 * i + j], o[b * C::VE + t + 1][2 * i + j],
-                                            o[b * C::VE + t + 2][2 * i + j], o[b * C::VE + t + 3][2 * i + j]);
+                    for (int b = 0; b < D / (8 * C::VE); ++b)
+#pragma unroll
+                        for (int t = 0; t < C::VE / 2; t += 2) {
+                            const float(&lo)[4] = o[b * (C::VE / 2) + t][y], (&hi)[4] = o[b * (C::VE / 2) + t + 1][y];
+                            *reinterpret_cast<float4 *>(dst + b * 8 * C::VE + 2 * t) = make_float4(lo[i], lo[2 + i], hi[i], hi[2 + i]);
+                        }
+                }
             }
-        }
         __syncthreads();
         const bool whole = begun && off + take == pc.ntiles;
         for (int e = tid; e < rows * (D / 4); e += kThreads) {
             const int r = e / (D / 4), c = (e % (D / 4)) * 4;
             float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int x = 0; x < kWarps; ++x) M = fmaxf(M, ml[x * 16 + r].x);
+            for (int x = 0; x < kWarps; ++x) M = fmaxf(M, ml[x * R + r].x);
             const float ref = M == -INFINITY ? 0.f : M;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int x = 0; x < kWarps; ++x) {
-                const float2 a = ml[x * 16 + r];
+                const float2 a = ml[x * R + r];
                 if (a.x == -INFINITY && a.y == 0.f) continue;  // nothing seen
                 const float f = ex2(a.x - ref);
-                const float4 z = *reinterpret_cast<const float4 *>(reinterpret_cast<float *>(sm) + (x * 16 + r) * C::MSTRIDE + c);
+                const float4 z = *reinterpret_cast<const float4 *>(reinterpret_cast<float *>(sm) + (x * R + r) * C::MSTRIDE + c);
                 L = fmaf(f, a.y, L);
                 y.x = fmaf(f, z.x, y.x); y.y = fmaf(f, z.y, y.y); y.z = fmaf(f, z.z, y.z); y.w = fmaf(f, z.w, y.w);
             }
@@ -503,12 +568,12 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     if (plan->padding) zero_padding(w, p.out, p.Hq, D, tid, kThreads);
 }
 
-template <int D, int KIND>
+template <int D, int KIND, int R>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
-    using C = RCfg<D, KIND>;
+    using C = RCfg<D, KIND, R>;
     const int G = a.Hq / a.pg.Hkv;
     RowParams p{};
-    p.w = attn_work(a, 16 / G, C::CH == 16 ? 2 : 1);
+    p.w = attn_work(a, R / G, C::BN < 256 ? 2 : 1);
     p.q = (const __nv_bfloat16 *)a.q;
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
@@ -523,21 +588,24 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     const int lines = C::LINES * 16 / C::CH;  // a box holds 16 positions, which always share a page
     if (!page_map(&mk, a.k_cache, a.pg, line, lines) || !page_map(&mv, a.v_cache, a.pg, line, lines))
         return cudaErrorInvalidValue;
-    auto kernel = attn_rows_kernel<D, KIND>;
+    auto kernel = attn_rows_kernel<D, KIND, R>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);
     if (e != cudaSuccess) return e;
     const int ctas = attn_ctas(a, p.w, C::BN);
-    kernel<<<ctas, kThreads, C::SM_BYTES, s>>>(mk, mv, p);
+    kernel<<<ctas, C::THREADS, C::SM_BYTES, s>>>(mk, mv, p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_attn_join(a, p.w, ctas, s);
 }
 
 template <int KIND>
 cudaError_t launch_d(const AttnArgs &a, cudaStream_t s) {
+    // up to 8 rows on average: half of the products, exponentials and accumulators
+    const int G = a.Hq / a.pg.Hkv;
+    const bool r8 = G <= 8 && a.pg.Ttot * G <= 8L * a.pg.B;
     switch (a.pg.d) {
-        case 64: return launch_t<64, KIND>(a, s);
-        case 128: return launch_t<128, KIND>(a, s);
-        case 256: return launch_t<256, KIND>(a, s);
+        case 64: return r8 ? launch_t<64, KIND, 8>(a, s) : launch_t<64, KIND, 16>(a, s);
+        case 128: return r8 ? launch_t<128, KIND, 8>(a, s) : launch_t<128, KIND, 16>(a, s);
+        case 256: return r8 ? launch_t<256, KIND, 8>(a, s) : launch_t<256, KIND, 16>(a, s);
     }
     return cudaErrorInvalidValue;
 }
