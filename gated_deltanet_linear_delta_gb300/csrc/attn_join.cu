@@ -4,9 +4,12 @@
 // its keys; the row is (sum_p e^{m_p - m} O_p) / (sum_p e^{m_p - m} l_p), m = max_p m_p (base 2).
 //
 // A split unit is joined once, by the blocks of the first boundary between pieces that lies in
-// it. Each row takes a whole block: its 8 warps share the parts (one session's single token over a
-// long cache has about 75 parts, and they should be in flight together), then add up through
-// shared memory in a fixed order. Blocks whose boundary lies between units have nothing to do.
+// it. Each row takes a team of 1, 2, 4 or 8 warps, as many as leave all of a unit's rows with the
+// blocks at once. With few rows that is a block: its warps share the parts (one session's single
+// token over a long cache has about 75 parts, and they should be in flight together) and add up
+// through shared memory in a fixed order. With 128 rows it is one warp, without any meeting: prompts
+// leave two or three parts a row, and a block for each took 37 us of their 143 us (8 prompts of 1024
+// tokens, 32 heads, d = 128). Blocks whose boundary lies between units have nothing to do.
 // The kernel is launched so that it may become resident while the attention kernel runs, and
 // waits for it here, which hides its launch.
 #include "attn_plan.cuh"
@@ -16,6 +19,11 @@ namespace gdn {
 namespace {
 
 constexpr int kJoinThreads = 256;
+
+__device__ __forceinline__ void store2(__nv_bfloat16 *to, float x, float y) {
+    *reinterpret_cast<__nv_bfloat162 *>(to) = __floats2bfloat162_rn(x, y);
+}
+__device__ __forceinline__ void store2(float *to, float x, float y) { *reinterpret_cast<float2 *>(to) = make_float2(x, y); }
 
 template <typename TOut, int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork w, TOut *out, int Hq) {
@@ -29,18 +37,21 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
     if (r.begin - r.off < r.cut.begin(c - 1)) return;  // an earlier boundary lies in this unit too
     const int last = r.cut.piece_of(r.begin - r.off + r.ntiles - 1);  // the piece that holds the unit's last key tile
     const int parts = last - c + 2, rows = r.tokens * w.G;
-    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-        const int t = row / w.G;
-        const bool live = r.pos + t >= 0;  // the rows of padding tokens are written elsewhere
+    int team = NW;
+    while (team > 1 && rows * team > (int)gridDim.y * NW) team >>= 1;
+    const int per_block = NW / team, sub = wid % team;
+    for (int base = blockIdx.y * per_block; base < rows; base += gridDim.y * per_block) {
+        const int row = base + wid / team, t = row / w.G;
+        const bool live = row < rows && r.pos + t >= 0;  // the rows of padding tokens are written elsewhere
         float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = 0.f;
-        for (int k0 = wid; live && k0 < parts; k0 += 4 * NW) {
+        for (int k0 = sub; live && k0 < parts; k0 += 4 * team) {
             float2 pm[4];
             float x[4][E];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {  // four parts' loads in flight
-                const int k = k0 + u * NW;
+                const int k = k0 + u * team;
                 pm[u] = make_float2(-INFINITY, 0.f);
                 if (k >= parts) continue;
                 const long at = part_index(w, c - 1 + k, k == 0 ? 1 : 0, row);
@@ -63,28 +74,36 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
                 for (int e = 0; e < E; ++e) o[e] = o[e] * a + x[u][e] * b;
             }
         }
+        TOut *to = out + ((r.token + t) * Hq + r.h * w.G + row % w.G) * D;
+        if (team == 1) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (live)
+#pragma unroll
+                for (int e = 0; e < E; e += 2) store2(to + e * 32 + 2 * lane, o[e] * inv, o[e + 1] * inv);
+            continue;
+        }
 #pragma unroll
         for (int e = 0; e < E; e += 2)
             *reinterpret_cast<float2 *>(&acc[wid][e * 32 + 2 * lane]) = make_float2(o[e], o[e + 1]);
         if (lane == 0) ml[wid] = make_float2(m, l);
         __syncthreads();
-        float M = -INFINITY, L = 0.f;
-#pragma unroll
-        for (int k = 0; k < NW; ++k) M = fmaxf(M, ml[k].x);
+        const int first = wid - sub;  // the team's warps
+        float M = -INFINITY, L = 0.f, f[NW];
+        for (int k = 0; k < team; ++k) M = fmaxf(M, ml[first + k].x);
         if (M == -INFINITY) M = 0.f;
-        float f[NW];
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
-            f[k] = exp2f(ml[k].x - M);
-            L += f[k] * ml[k].y;
+            f[k] = k < team ? exp2f(ml[first + k].x - M) : 0.f;
+            if (k < team) L += f[k] * ml[first + k].y;
         }
-        const int h = r.h * w.G + row % w.G;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
         if (live)
-            for (int e = threadIdx.x; e < D; e += kJoinThreads) {
+            for (int e = sub * 32 + lane; e < D; e += team * 32) {
                 float x = 0.f;
 #pragma unroll
-                for (int k = 0; k < NW; ++k) x += f[k] * acc[k][e];
-                out[((r.token + t) * Hq + h) * D + e] = from_f32<TOut>(L == 0.f ? 0.f : x / L);
+                for (int k = 0; k < NW; ++k)
+                    if (k < team) x += f[k] * acc[first + k][e];
+                to[e] = from_f32<TOut>(x * inv);
             }
         __syncthreads();
     }
@@ -96,8 +115,7 @@ cudaError_t launch_t(const AttnWork &w, TOut *out, int Hq, int rows, int ctas, c
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    // a block per row of few: with 4 rows a block, 64-row units took 46 us instead of 35 us in all, and one long
-    // session's 8 rows 45 us instead of 41 us
+    // (4 rows a block, one after another: one long session's 8 rows took 45 us instead of 41 us in all)
     cfg.gridDim = dim3((unsigned)ctas - 1, (unsigned)(rows < 16 ? rows : 16), 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = s;
