@@ -65,6 +65,8 @@ struct Cfg {
     static constexpr int COLS = 4;                         // column scales, a buffer per tile
     static constexpr int THREADS = 32 * (kCodes ? kConvWarp0 + 2 * kGroup : kConvWarp0);
     static constexpr uint32_t TM_O = 0, TM_S = D == 256 ? 256 : 128, TM_Q = 384;
+    // Where there is room, the next unit's Q is put beside the one in use, so that its products follow without a gap.
+    static constexpr int NQ = D == 256 ? 1 : 2;
     // shared memory, from a 1 KiB aligned base
     static constexpr uint32_t SM_V = NK * SLOT, SM_RK = SM_V + NV * SLOT, SM_RV = SM_RK + NR * RAW_K;
     static constexpr uint32_t SM_COL = SM_RV + NR * RAW_V;                   // [COLS][3][BN] a, b, 1 / vs
@@ -79,7 +81,7 @@ struct Cfg {
     static constexpr int B_FK = 0, B_FV = B_FK + NK, B_RK = B_FV + NV, B_RV = B_RK + NR, B_REK = B_RV + NR,
                          B_REV = B_REK + NR, B_COL = B_REV + NR, B_S = B_COL + COLS, B_PV = B_S + kTurns,
                          B_P = B_PV + kTurns, B_ST = B_P + 2, B_SF = B_ST + 2,
-                         B_Q = B_SF + 2, B_OF = B_Q + 1, B_QF = B_OF + 1, B_QE = B_QF + 1,
+                         B_Q = B_SF + 2, B_OF = B_Q + NQ, B_QF = B_OF + 1, B_QE = B_QF + 1,
                          B_US = B_QE + 1 /* all S of a unit */, B_UO = B_US + 1 /* all of its O */, B_FIN = B_UO + 1, B_COUNT = B_FIN + 1;
     static constexpr uint32_t SM_INFO = SM_BAR + B_COUNT * 8;                // [2][NR] valid rows, page mask
     static constexpr uint32_t SM_TMEM = SM_INFO + (NR ? 2 * NR : 1) * 8;
@@ -243,19 +245,20 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
     const uint64_t desc_k = desc_sw128(sb, 16, 1024), desc_v = desc_sw128(sb + C::SM_V, BN * 128, 1024);  // of slots 0
     Ring<C::NK> rk;
     Ring<C::NV> rv;
-    uint32_t t = 0, unit = 0, o_free = 0;  // tiles whose S is issued, units begun, phase of B_OF
+    Ring<C::NQ> rq;
+    uint32_t t = 0, qslot = 0, o_free = 0;  // tiles whose S is issued, the unit's Q, phase of B_OF
     // The waits for tiles come before the one for P, which is the last to be met: what follows it is issued at once.
     auto k_ready = [&]() -> bool { return warp_wait(bar + C::B_FK + rk.slot, rk.phase, p.budget); };
     auto product_s = [&](bool last) {
         tc_fence_after();
         const uint64_t d = desc_k + (uint64_t)(rk.slot * (C::SLOT >> 4));
-        const uint32_t to = tmem + C::TM_S + (t & 1) * BN;
+        const uint32_t to = tmem + C::TM_S + (t & 1) * BN, tq = tmem + C::TM_Q + qslot * (D / 2);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-            mma_f16_ts_by(lead, to, tmem + C::TM_Q + 8 * ks, d + (uint64_t)(((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4),
+            mma_f16_ts_by(lead, to, tq + 8 * ks, d + (uint64_t)(((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4),
                           ID_S, ks > 0);
         mma_commit_by(lead, bar + C::B_S + (t & (C::kTurns - 1)));
-        if (last) mma_commit_by(lead, bar + C::B_US);
+        if (C::NQ == 1 && last) mma_commit_by(lead, bar + C::B_US);
         rk.next();
         ++t;
     };
@@ -295,8 +298,9 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
     if (k.pc.left > 0) {
         do {
             const int n = k.take(), left = k.pc.s.len - k.pc.off * BN;
-            ok = warp_wait(bar + C::B_Q, unit & 1, p.budget) && (t > 0 || k_ready());
-            ++unit;
+            ok = warp_wait(bar + C::B_Q + rq.slot, rq.phase, p.budget) && (t > 0 || k_ready());
+            qslot = rq.slot;
+            rq.next();
             for (int jj = 0; jj < n && ok; ++jj) {
                 const bool more = jj + 1 < n || k.pc.left > n;  // another tile follows in the piece
                 product_s(jj + 1 == n);
@@ -416,6 +420,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
     float *xch = reinterpret_cast<float *>(sm + C::SM_X) + row;
     float2 *stat = reinterpret_cast<float2 *>(sm + C::SM_STAT) + half * 128 + row;
     const float *rsq = reinterpret_cast<const float *>(sm + C::SM_RS) + row;
+    const int tok = row / p.w.G;
     uint32_t t = 0, unit = 0;
     // A wait that ran out (`late`, a thread's own) is shared with the rows' other warp at the next meeting, so that
     // both leave there (`ok` is the same for all their threads).
@@ -425,7 +430,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
         const int rows = min(p.w.TPT, k.pc.s.T - t0) * p.w.G;
         const bool live_warp = quarter * 32 < rows;
         const int sure = k.pc.s.len - k.pc.s.T + t0;               // last position that every row of the unit sees
-        const int limit = row < rows ? sure + row / p.w.G : -1;    // ... that this row sees
+        const int limit = row < rows ? sure + tok : -1;            // ... that this row sees
         float m = -INFINITY, l = 0.f;
         for (int jj = 0; jj < n; ++jj, ++t) {
             const uint32_t b = t & 1;
@@ -611,12 +616,12 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
             if (p.negate)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) x[c] ^= 0x80008000u;
-            tmem_st32(tl + C::TM_Q + part * 32, x);
+            tmem_st32(tl + C::TM_Q + (unit % C::NQ) * (D / 2) + part * 32, x);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar + C::B_Q);
+        if (lane == 0) mbar_arrive(bar + C::B_Q + unit % C::NQ);
     };
     if (k.pc.left > 0) {
         put(k, prepare(k), 0);
@@ -626,7 +631,8 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
             Walk next = k;
             more = walk_next<BN>(p.w, &next);
             const int e = more ? prepare(next) : 0;
-            ok = ok && warp_wait(bar + C::B_US, unit & 1, p.budget);  // Q has been used
+            // One Q: once all of this unit's S have used it. Two: the unit before, which used the other, is done.
+            if (C::NQ == 1) ok = ok && warp_wait(bar + C::B_US, unit & 1, p.budget);
             if (!ok) break;
             tc_fence_after();
             if (more) put(next, e, unit + 1);
@@ -719,7 +725,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             mbar_init(bar + C::B_ST + s, 2 * kGroup);
             mbar_init(bar + C::B_SF + s, kGroup);
         }
-        mbar_init(bar + C::B_Q, kGroup);
+        for (int s = 0; s < C::NQ; ++s) mbar_init(bar + C::B_Q + s, kGroup);
         mbar_init(bar + C::B_OF, kGroup);
         mbar_init(bar + C::B_QF, 1);
         mbar_init(bar + C::B_US, 1);
