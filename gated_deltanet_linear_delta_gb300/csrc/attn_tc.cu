@@ -101,6 +101,14 @@ struct TcParams {
     long long budget;
 };
 
+// 32 bytes to a 32-byte boundary. (A row's thread stores its own row, so a warp's store touches 32 lines whatever its
+// width, and the number of stores is what a unit's rows cost.)
+__device__ __forceinline__ void store32(void *to, const uint32_t *x) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t bf2(float a, float b) { return bf2_bits(__floats2bfloat162_rn(a, b)); }
 
 // every thread's view of the walk over the piece's units
@@ -580,62 +588,94 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
         __syncwarp();
         if (lane == 0) mbar_arrive(bar + C::B_QE);
     };
-    // A unit's first part of Q on its way, and with an 8-bit cache its row's exponent, while the unit before is at work
-    auto prepare = [&](const Walk &w) -> int {
-        int e = 0;
-        fetch(w, 0);
+    // 16-bit pairs of Q as they go into TMEM: with an 8-bit cache in fp16, times the row's power of two
+    auto pairs = [&](uint32_t(&x)[32], float f) {
         if constexpr (C::kCodes) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                x[c] = h2_bits(f * __uint_as_float(x[c] << 16), f * __uint_as_float(x[c] & 0xffff0000u));
+        }
+        if (p.negate)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] ^= 0x80008000u;
+    };
+    auto largest = [&](const uint32_t(&x)[32], float a) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            a = fmaxf(a, fmaxf(fabsf(__uint_as_float(x[c] << 16)), fabsf(__uint_as_float(x[c] & 0xffff0000u))));
+        return a;
+    };
+    // Q of unit number `unit`, whose first part has been fetched, into TMEM. One Q: once the unit before, the one at
+    // hand, has used it. Two: the unit before last, which used the same, is done.
+    auto bring = [&](const Walk &w, uint32_t unit) {
+        const uint32_t to = tl + C::TM_Q + (unit % C::NQ) * (D / 2);
+        auto used = [&] {
+            if (C::NQ == 1 && unit > 0) ok = ok && warp_wait(bar + C::B_US, (unit - 1) & 1, p.budget);
+            tc_fence_after();
+        };
+        if constexpr (C::kCodes && C::NQ == 2) {  // the row waits for its exponent in TMEM
             float a = 0.f;
+            used();
 #pragma unroll 1
-            for (int part = 1; part <= PARTS && ok; ++part) {
+            for (int part = 0; part < PARTS && ok; ++part) {
                 uint32_t x[32];
                 read(x);
-                fetch(w, part % PARTS);
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    a = fmaxf(a, fmaxf(fabsf(__uint_as_float(x[c] << 16)), fabsf(__uint_as_float(x[c] & 0xffff0000u))));
+                if (part + 1 < PARTS) fetch(w, part + 1);
+                a = largest(x, a);
+                tmem_st32(to + part * 32, x);
             }
-            e = f16_row_exponent(a);
-        }
-        return e;
-    };
-    // Q into TMEM; to fp16, by the row's power of two, with an 8-bit cache
-    auto put = [&](const Walk &w, int e, uint32_t unit) {
-        const float f = pow2i(e);
-        if (C::kCodes) rsq[(unit & 3) * 128] = pow2i(-e);
+            tmem_wait_st();
+            const int e = f16_row_exponent(a);
+            rsq[(unit & 3) * 128] = pow2i(-e);
 #pragma unroll 1
-        for (int part = 0; part < PARTS && ok; ++part) {
-            uint32_t x[32];
-            read(x);
-            if (part + 1 < PARTS) fetch(w, part + 1);
-            if constexpr (C::kCodes) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    x[c] = h2_bits(f * __uint_as_float(x[c] << 16), f * __uint_as_float(x[c] & 0xffff0000u));
+            for (int part = 0; part < PARTS; ++part) {
+                uint32_t x[32];
+                tmem_ld32_nw(to + part * 32, x);
+                tmem_wait_ld();
+                pairs(x, pow2i(e));
+                tmem_st32(to + part * 32, x);
             }
-            if (p.negate)
-#pragma unroll
-                for (int c = 0; c < 32; ++c) x[c] ^= 0x80008000u;
-            tmem_st32(tl + C::TM_Q + (unit % C::NQ) * (D / 2) + part * 32, x);
+        } else {
+            int e = 0;
+            if constexpr (C::kCodes) {
+                float a = 0.f;
+#pragma unroll 1
+                for (int part = 1; part <= PARTS && ok; ++part) {
+                    uint32_t x[32];
+                    read(x);
+                    fetch(w, part % PARTS);
+                    a = largest(x, a);
+                }
+                e = f16_row_exponent(a);
+                rsq[(unit & 3) * 128] = pow2i(-e);
+            }
+            used();
+#pragma unroll 1
+            for (int part = 0; part < PARTS && ok; ++part) {
+                uint32_t x[32];
+                read(x);
+                if (part + 1 < PARTS) fetch(w, part + 1);
+                pairs(x, pow2i(e));
+                tmem_st32(to + part * 32, x);
+            }
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar + C::B_Q + unit % C::NQ);
     };
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     if (k.pc.left > 0) {
-        put(k, prepare(k), 0);
-        bool more = true;
-        for (uint32_t unit = 0; more && ok; ++unit) {
-            const int n = k.take();
-            Walk next = k;
-            more = walk_next<BN>(p.w, &next);
-            const int e = more ? prepare(next) : 0;
-            // One Q: once all of this unit's S have used it. Two: the unit before, which used the other, is done.
-            if (C::NQ == 1) ok = ok && warp_wait(bar + C::B_US, unit & 1, p.budget);
-            if (!ok) break;
-            tc_fence_after();
-            if (more) put(next, e, unit + 1);
+        fetch(k, 0);
+        bring(k, 0);
+        Walk next = k;
+        bool more = walk_next<BN>(p.w, &next);
+        if (more) fetch(next, 0);
+        for (uint32_t unit = 0; ok; ++unit) {
+            if (more) bring(next, unit + 1);
+            Walk after = next;
+            const bool more2 = more && walk_next<BN>(p.w, &after);
+            if (more2) fetch(after, 0);
             ok = ok && warp_wait(bar + C::B_ST + (unit & 1), (unit >> 1) & 1, p.budget);
             if (!ok) break;
             const float2 a = stat[(unit & 1) * 256], b = stat[(unit & 1) * 256 + 128];
@@ -644,7 +684,7 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
             if (lane == 0) mbar_arrive(bar + C::B_SF + (unit & 1));
             ok = warp_wait(bar + C::B_UO, unit & 1, p.budget);
             if (!ok) break;
-            const int rows = unit_rows(k);
+            const int n = k.take(), rows = unit_rows(k);
             if (quarter * 32 < rows) {
                 tc_fence_after();
                 const int t0 = k.pc.i * p.w.TPT;
@@ -660,24 +700,31 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
                     tmem_ld32(tl + C::TM_O + c, o);
                     if (!store) continue;
                     if (whole) {
+                        uint32_t y[16];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float *y = o + 8 * x;
-                            reinterpret_cast<uint4 *>(out + c)[x] =
-                                make_uint4(bf2(y[0] * inv, y[1] * inv), bf2(y[2] * inv, y[3] * inv),
-                                           bf2(y[4] * inv, y[5] * inv), bf2(y[6] * inv, y[7] * inv));
+                        for (int x = 0; x < 16; ++x) y[x] = bf2(o[2 * x] * inv, o[2 * x + 1] * inv);
+                        if (wide) {
+                            store32(out + c, y);
+                            store32(out + c + 16, y + 8);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                reinterpret_cast<uint4 *>(out + c)[x] = make_uint4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
                         }
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.w.part + part * D + c);
+                        float *dst = p.w.part + part * D + c;
 #pragma unroll
-                        for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                        for (int x = 0; x < 32; x += 8) store32(dst + x, reinterpret_cast<const uint32_t *>(o) + x);
                     }
                 }
                 tc_fence_before();
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + C::B_OF);
+            if (!more) break;
             k = next;
+            next = after;
+            more = more2;
         }
     }
     if (!ok && lane == 0) flag_error(p.w.pg.status);
