@@ -193,6 +193,49 @@ def test_more_sequences_than_threads(G, dtype, cache):
     assert_attention(out, *reference(case, q, [1] * 1500, 64 ** -0.5))
 
 
+@pytest.mark.parametrize("cache", sorted(CACHES))
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 32), (256, 16)])
+@pytest.mark.parametrize("lens,new,G", [
+    ([1500, 40, 16, 1], [1] * 4, 8),                      # 8 rows, in one tile of 8
+    ([1500, 700], [1, 1], 9),                             # 9 rows
+    ([900, 33, 5], [4] * 3, 4),                           # 16 rows
+    ([700, 650, 20], [5] * 3, 3),                         # 15 rows
+    ([77] * 20 + [500], [1] * 20 + [9], 2),               # few rows on average, one sequence with several tiles of them
+])
+def test_few_rows(lens, new, G, d, page, cache):
+    case = Paged(lens, 2, d, page, cache, "bf16", seed=9)
+    q, out = run(case, new, 2 * G)
+    assert_attention(out, *reference(case, q, new, d ** -0.5))
+
+
+@pytest.mark.parametrize("dtype,cache", [("bf16", "same"), ("bf16", "int8"), ("f32", "same")])
+@pytest.mark.parametrize("lens,new,G", [([2900], [1], 8), ([2900], [3], 7), ([2900], [5], 8), ([2900], [13], 8),
+                                        ([2900], [40], 5), ([600, 590, 610], [70] * 3, 4)])
+def test_split_units_of_any_number_of_rows(lens, new, G, dtype, cache):
+    """8 to 128 rows of a unit whose keys are shared by many CTAs: each row is put together by 8 warps or fewer."""
+    case = Paged(lens, 1, 128, 64, cache, dtype, seed=11)
+    q, out = run(case, new, G)
+    assert_attention(out, *reference(case, q, new, 128 ** -0.5))
+
+
+@pytest.mark.parametrize("cache", sorted(CACHES))
+@pytest.mark.parametrize("T", [1, 3, 50])
+def test_output_on_a_16_byte_boundary(T, cache):
+    """Whole rows and rows of a piece, with an output that is not on a wider boundary: the same results."""
+    case = Paged([700, 90], 2, 128, 16, cache, "bf16", seed=12)
+    kc, vc, ks, vs, table, lens = case.tensors()
+    q = torch.randn(2 * T, 16, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(DEV)
+    aligned = torch.empty_like(q)
+    room = torch.zeros(q.numel() + 16, dtype=q.dtype, device=DEV)
+    out = room[8:8 + q.numel()].view(q.shape)
+    assert out.data_ptr() % 32 == 16 and aligned.data_ptr() % 32 == 0
+    for to in (aligned, out):
+        gdn.gdn_paged_attn(q, kc, vc, table, lens, to, ks, vs)
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    assert torch.equal(out, aligned)
+    assert not room[:8].any() and not room[8 + q.numel():].any()
+
+
 @pytest.mark.parametrize("T", [1, 30])
 def test_another_stream(T):
     """All on a stream of its own, without a workspace: torch's allocator gives it to that stream."""
