@@ -157,18 +157,18 @@ int attn_ctas(const AttnArgs &a, const AttnWork &w, int BN) {
     const long positions = (long)a.pg.max_pages * a.pg.page_size;
     const long units = (a.pg.cu ? a.pg.B + a.pg.Ttot / w.TPT : (long)a.pg.B * ((a.pg.T + w.TPT - 1) / w.TPT)) * a.pg.Hkv;
     const long tiles = (positions + BN - 1) / BN;
-    const long pieces = units > kAttnCtas || tiles > kAttnCtas ? (long)kAttnCtas * w.min_tiles : units * tiles;
-    const long ctas = (pieces + w.min_tiles - 1) / w.min_tiles;
+    const long pieces = units > kAttnCtas || tiles > kAttnCtas ? (long)kAttnCtas << w.min_shift : units * tiles;
+    const long ctas = (pieces + (1 << w.min_shift) - 1) >> w.min_shift;
     return (int)(ctas < kAttnCtas ? ctas : kAttnCtas);
 }
 
-AttnWork attn_work(const AttnArgs &a, int tokens_per_tile, int min_tiles) {
+AttnWork attn_work(const AttnArgs &a, int tokens_per_tile, int min_shift) {
     AttnWork w{};
     w.pg = a.pg;
     w.G = a.Hq / a.pg.Hkv;
     w.TPT = tokens_per_tile;
     w.rows = attn_unit_rows(a.pg.cu ? a.pg.Ttot : a.pg.T, w.G);
-    w.min_tiles = min_tiles;
+    w.min_shift = min_shift;
     const size_t parts = (size_t)kAttnCtas * 2 * w.rows;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     w.rec = reinterpret_cast<AttnRec *>(ws);

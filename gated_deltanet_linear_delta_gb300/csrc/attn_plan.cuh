@@ -50,7 +50,7 @@ struct AttnWork {
     int G;         // query heads per key head
     int TPT;       // tokens per row tile
     int rows;      // workspace rows per part
-    int min_tiles; // a piece is not cut below this
+    int min_shift; // a piece is not cut below 2^min_shift tiles
     AttnRec *rec;  // [kAttnCtas]
     float2 *ml;    // [kAttnCtas][2][rows] running maximum (log2 domain) and sum
     float *part;   // [kAttnCtas][2][rows][d]
@@ -122,14 +122,15 @@ __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
     constexpr int NW = NT / 32;
     const KvPages &p = w.pg;
     const bool one_pass = p.B <= NT;
-    long mine = 0;
+    long mine = 0, per_head = 0;  // key tiles of this thread's sequences; of one head of the last of them
     SeqInfo s0{0, 0, 0};
     bool pad = false;
     for (int base = 0; base < p.B; base += NT) {
         SeqInfo s{0, 0, 0};
         if (base + tid < p.B) seq_info(p, base + tid, &s);
         pad |= s.T > s.len;
-        mine += seq_tiles<BN>(w, s) * p.Hkv;
+        per_head = seq_tiles<BN>(w, s);
+        mine += per_head * p.Hkv;
         s0 = s;
     }
     auto scan = [&](long y) {  // inclusive, over the warp
@@ -151,17 +152,15 @@ __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
         if (k < wid) pre += sm->sum[k];
         total += sm->sum[k];
     }
-    const long want = Cut::div(total + w.min_tiles - 1, w.min_tiles);
+    const long want = (total + (1 << w.min_shift) - 1) >> w.min_shift;
     Cut cut;
     cut.active = (int)(want < (long)gridDim.x ? want : (long)gridDim.x);
     cut.q = cut.active ? Cut::div(total, cut.active) : 0;
     cut.r = (int)(total - cut.q * cut.active);
     const int c = blockIdx.x;
     const long begin = c < cut.active ? cut.begin(c) : total, end = c < cut.active ? cut.begin(c + 1) : total;
-    long y = mine;
     auto own = [&](int n) {  // this thread's sequence holds `begin`: head, and row tile if there are few
         Piece pc;
-        const long per_head = Cut::div(y, p.Hkv);
         long rem = begin - pre;
         pc.n = n;
         pc.s = s0;
@@ -193,7 +192,8 @@ __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
         for (int base = 0; base < p.B && begin < end; base += NT) {
             s0 = SeqInfo{0, 0, 0};
             if (base + tid < p.B) seq_info(p, base + tid, &s0);
-            y = seq_tiles<BN>(w, s0) * p.Hkv;
+            per_head = seq_tiles<BN>(w, s0);
+            const long y = per_head * p.Hkv;
             inc = scan(y);
             if (lane == 31) sm->sum[wid] = inc;
             __syncthreads();

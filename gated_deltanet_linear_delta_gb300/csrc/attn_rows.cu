@@ -1,7 +1,7 @@
 // attn_rows.cu -- attention over a paged cache for few query rows per key head (bf16 inputs): the
 // decode step and the check of a few speculated tokens.
 //
-// With at most 16 rows (the G query heads of a key head, of a few tokens) every cached row is read
+// With at most 16 rows (the G query heads of a key head, of few tokens) every cached row is read
 // for 16 rows' worth of products at most, 16 to 32 flops a byte, so the kernel is bound by the bytes
 // of the cache and, for short ones, by the length of its own dependent chain. It therefore keeps
 // everything of a key chunk inside one warp: a CTA's warps take 16 or 32 positions each of a tile,
@@ -573,7 +573,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     using C = RCfg<D, KIND, R>;
     const int G = a.Hq / a.pg.Hkv;
     RowParams p{};
-    p.w = attn_work(a, R / G, C::BN < 256 ? 2 : 1);
+    p.w = attn_work(a, R / G, C::BN < 256 ? 1 : 0);
     p.q = (const __nv_bfloat16 *)a.q;
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
@@ -597,32 +597,38 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     return e != cudaSuccess ? e : launch_attn_join(a, p.w, ctas, s);
 }
 
-template <int KIND>
+template <int KIND, int R>
 cudaError_t launch_d(const AttnArgs &a, cudaStream_t s) {
-    // up to 8 rows on average: half of the products, exponentials and accumulators
-    const int G = a.Hq / a.pg.Hkv;
-    const bool r8 = G <= 8 && a.pg.Ttot * G <= 8L * a.pg.B;
     switch (a.pg.d) {
-        case 64: return r8 ? launch_t<64, KIND, 8>(a, s) : launch_t<64, KIND, 16>(a, s);
-        case 128: return r8 ? launch_t<128, KIND, 8>(a, s) : launch_t<128, KIND, 16>(a, s);
-        case 256: return r8 ? launch_t<256, KIND, 8>(a, s) : launch_t<256, KIND, 16>(a, s);
+        case 64: return launch_t<64, KIND, R>(a, s);
+        case 128: return launch_t<128, KIND, R>(a, s);
+        case 256: return launch_t<256, KIND, R>(a, s);
     }
     return cudaErrorInvalidValue;
 }
 
-}  // namespace
-
-// Few rows: on average at most 16 per sequence and key head, and 16 query heads per key head at most.
-bool attn_rows_supported(const AttnArgs &a) {
+// on average at most `rows` query rows per sequence and key head, and no more of one token
+bool rows_fit(const AttnArgs &a, int rows) {
     const int G = a.Hq / a.pg.Hkv;
-    return G <= 16 && a.pg.Ttot * G <= 16L * a.pg.B;
+    return G <= rows && a.pg.Ttot * G <= (long)rows * a.pg.B;
 }
 
+}  // namespace
+
+// Few rows: at most 16 with an 8-bit cache, at most 8 with a bf16 one. Measured against attn_tc.cu with 16 rows: 128
+// sequences of 4096, d = 256, e4m3 121 and 146 us; 32 of 8192, 8 key heads, d = 128, int8 127 and 204 us; but bf16 191
+// and 186, 185 and 178 us. (With 32 rows, here two passes over the cache: e4m3 210 and 149 us, int8 221 and 222, bf16
+// 348 and 190.)
+bool attn_rows_supported(const AttnArgs &a) { return rows_fit(a, a.pg.cache_dtype == GDN_BF16 ? 8 : 16); }
+
+// Tiles of 8 rows where they do: half of the products, exponentials and accumulators (32 sequences of 8192, 8 key heads
+// with 4 query heads each, d = 128, int8: 97 us, 112 us in tiles of 16; 128 of 4096, d = 256, e4m3: 100 and 108 us).
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t s) {
+    const bool r8 = rows_fit(a, 8);
     switch (a.pg.cache_dtype) {
-        case GDN_FP8: return launch_d<GDN_FP8>(a, s);
-        case GDN_INT8: return launch_d<GDN_INT8>(a, s);
-        default: return launch_d<GDN_BF16>(a, s);
+        case GDN_FP8: return r8 ? launch_d<GDN_FP8, 8>(a, s) : launch_d<GDN_FP8, 16>(a, s);
+        case GDN_INT8: return r8 ? launch_d<GDN_INT8, 8>(a, s) : launch_d<GDN_INT8, 16>(a, s);
+        default: return launch_d<GDN_BF16, 8>(a, s);
     }
 }
 

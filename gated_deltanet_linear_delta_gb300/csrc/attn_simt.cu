@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
 template <int KIND, int D, int R>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     const int G = a.Hq / a.pg.Hkv;
-    SimtParams p{attn_work(a, R / G, 2), (const float *)a.q, a.k_cache, a.v_cache, a.k_scale, a.v_scale,
+    SimtParams p{attn_work(a, R / G, 1), (const float *)a.q, a.k_cache, a.v_cache, a.k_scale, a.v_scale,
                  (float *)a.out, a.Hq, a.q_stride, a.scale * kLog2e};
     auto kernel = attn_simt_kernel<KIND, D, R>;
     constexpr int bytes = sizeof(SimtSmem<D, R>);

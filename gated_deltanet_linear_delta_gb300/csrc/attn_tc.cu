@@ -826,7 +826,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     using C = Cfg<D, KIND>;
     const int G = a.Hq / a.pg.Hkv;
     TcParams p{};
-    p.w = attn_work(a, kAttnMaxRows / G, 2);
+    p.w = attn_work(a, kAttnMaxRows / G, 1);
     p.k_cache = (const uint8_t *)a.k_cache;
     p.v_cache = (const uint8_t *)a.v_cache;
     p.k_scale = a.k_scale;
