@@ -44,6 +44,38 @@ __device__ __forceinline__ uint4 pack16(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
+// The largest magnitude of a lane's pieces; infinity where one is not finite. bf16 by pairs (a maximum that keeps a NaN
+// takes half an instruction an element, a comparison of each in fp32 four).
+template <typename T, int NP>
+__device__ __forceinline__ float largest(const uint4 (&x)[NP]) {
+    if constexpr (sizeof(T) == 2) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int g = 0; g < NP; ++g) {
+            const uint32_t w[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                asm("{\n.reg .b32 t;\nabs.bf16x2 t, %1;\nmax.NaN.bf16x2 %0, %0, t;\n}" : "+r"(m) : "r"(w[i]));
+        }
+        const float a = __uint_as_float(m << 16), b = __uint_as_float(m & 0xffff0000u);
+        return a == a && b == b ? fmaxf(a, b) : __int_as_float(0x7f800000);
+    } else {
+        float m = 0.f;
+        bool bad = false;
+#pragma unroll
+        for (int g = 0; g < NP; ++g) {
+            float y[4];
+            unpack16(x[g], y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                m = fmaxf(m, fabsf(y[e]));
+                bad |= !(fabsf(y[e]) <= 3.4028234e38f);
+            }
+        }
+        return bad ? __int_as_float(0x7f800000) : m;
+    }
+}
+
 // Pool row (page, row in it, head 0) of packed token i, by a whole warp: -1 padding, -2 not to be touched
 __device__ __forceinline__ long token_row(const KvPages &p, long i, int page_shift) {
     const int n = seq_of_token(p, i);
@@ -130,31 +162,20 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv_copy_kernel(const KvArgs a, 
 #pragma unroll
                     for (int g = 0; g < NP; ++g) *reinterpret_cast<uint4 *>((T *)cache + at * D + c + g * LPR * PE) = x[f][g];
                 } else {
-                    float amax = 0.f, y[NP][PE];
-                    if (w >= 0) {
-                        bool bad = false;
-#pragma unroll
-                        for (int g = 0; g < NP; ++g) {
-                            unpack16(x[f][g], y[g]);
-#pragma unroll
-                            for (int e = 0; e < PE; ++e) {
-                                amax = fmaxf(amax, fabsf(y[g][e]));
-                                bad |= !(fabsf(y[g][e]) <= 3.4028234e38f);
-                            }
-                        }
-                        if (bad) amax = __int_as_float(0x7f800000);
-                    }
+                    float amax = w >= 0 ? largest<T, NP>(x[f]) : 0.f;
 #pragma unroll
                     for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                     if (w < 0) continue;
                     const float sc = KIND == GDN_FP8 ? scale_e4m3(amax) : scale_int8(amax);
-                    const float inv = __frcp_rn(sc);  // (of a power of two: exact)
+                    const float inv = KIND == GDN_FP8 ? inverse_pow2(sc) : rcp_near(sc);
 #pragma unroll
                     for (int g = 0; g < NP; ++g) {
+                        float y[PE];
+                        unpack16(x[f][g], y);
                         uint32_t code[PE / 4];
 #pragma unroll
                         for (int e = 0; e < PE / 4; ++e)
-                            code[e] = sc != sc ? 0u : KIND == GDN_FP8 ? codes4_e4m3(y[g] + 4 * e, inv) : codes4_int8(y[g] + 4 * e, sc, inv);
+                            code[e] = sc != sc ? 0u : KIND == GDN_FP8 ? codes4_e4m3(y + 4 * e, inv) : codes4_int8(y + 4 * e, sc, inv);
                         uint8_t *dst = cache + at * D + c + g * LPR * PE;
                         if constexpr (PE == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
                         else *reinterpret_cast<uint32_t *>(dst) = code[0];

@@ -98,6 +98,14 @@ __device__ __forceinline__ float scale_int8(float amax) {
     return fmaxf(__fdiv_rn(amax, 127.f), kMinKvScale);
 }
 
+// 1 / s: of a power of two of 2^-100 or more, exact; of any s, to 2 ulp
+__device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
+__device__ __forceinline__ float rcp_near(float s) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+    return y;
+}
+
 // 4 codes of x[0..3] (x / s rounded to nearest even), the first in the lowest byte
 __device__ __forceinline__ uint32_t codes4_e4m3(const float *x, float inv) {  // inv = 1 / s, exact
     const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[0] * inv, x[1] * inv), __NV_SATFINITE, __NV_E4M3);
