@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
     constexpr int E = D / 32, NW = kJoinThreads / 32;
     __shared__ float acc[NW][D];
     __shared__ float2 ml[NW];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    before_reading();
     const int c = blockIdx.x + 1, lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const AttnRec r = w.rec[c];
     if (c >= r.cut.active || r.off == 0) return;
@@ -111,17 +111,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
 
 template <typename TOut, int D>
 cudaError_t launch_t(const AttnWork &w, TOut *out, int Hq, int rows, int ctas, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
     // (4 rows a block, one after another: one long session's 8 rows took 45 us instead of 41 us in all)
-    cfg.gridDim = dim3((unsigned)ctas - 1, (unsigned)(rows < 16 ? rows : 16), 1);
-    cfg.blockDim = dim3(kJoinThreads, 1, 1);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<TOut, D>, w, out, Hq);
+    const dim3 grid((unsigned)ctas - 1, (unsigned)(rows < 16 ? rows : 16), 1);
+    return launch_early(attn_join_kernel<TOut, D>, grid, kJoinThreads, 0, s, w, out, Hq);
 }
 
 }  // namespace

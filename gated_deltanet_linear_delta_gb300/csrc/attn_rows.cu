@@ -138,7 +138,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     float2 *ml = reinterpret_cast<float2 *>(sm + C::SM_ML);
     float *rs = reinterpret_cast<float *>(sm + C::SM_RS);
     PlanSmem *plan = reinterpret_cast<PlanSmem *>(sm + C::SM_PLAN);
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    next_may_begin();
     if (tid == 0) {
         prefetch_tmap(&mk);
         prefetch_tmap(&mv);
@@ -147,6 +147,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         for (int s = 0; s < C::NSL; ++s) mbar_init(bar + s, 1);
         fence_mbar_init();
     }
+    before_reading();
     plan_piece<BN, kThreads>(w, plan);  // (synchronises the CTA)
     Piece pc = plan->piece;
     const int P_shift = 31 - __clz(pg.page_size);
@@ -598,8 +599,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);
     if (e != cudaSuccess) return e;
     const int ctas = attn_ctas(a, p.w, C::BN);
-    kernel<<<ctas, C::THREADS, C::SM_BYTES, s>>>(mk, mv, p);
-    e = cudaGetLastError();
+    e = launch_early(kernel, dim3(ctas), C::THREADS, C::SM_BYTES, s, mk, mv, p);
     return e != cudaSuccess ? e : launch_attn_join(a, p.w, ctas, s);
 }
 

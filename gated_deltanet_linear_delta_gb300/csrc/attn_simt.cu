@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
     SimtSmem<D, R> &sm = *reinterpret_cast<SimtSmem<D, R> *>(smem_raw);
     const AttnWork &w = a.w;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    next_may_begin();
+    before_reading();
     plan_piece<BN, kThreads>(w, &sm.plan);
     if (sm.plan.padding) zero_padding(w, a.out, a.Hq, D, tid, kThreads);
     Piece pc = sm.plan.piece;
@@ -259,8 +260,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const int ctas = attn_ctas(a, p.w, BN);
-    kernel<<<ctas, kThreads, bytes, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_early(kernel, dim3(ctas), kThreads, bytes, s, p);
     return e != cudaSuccess ? e : launch_attn_join(a, p.w, ctas, s);
 }
 

@@ -752,7 +752,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     uint32_t *slot = reinterpret_cast<uint32_t *>(sm + C::SM_TMEM);
     PlanSmem *plan = reinterpret_cast<PlanSmem *>(sm + C::SM_PLAN);
     const int tid = threadIdx.x, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    next_may_begin();
     if (tid == 0) {
         prefetch_tmap(&mq);
         if (!C::kCodes) {
@@ -788,6 +788,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         mbar_init(bar + C::B_FIN, 1);
         fence_mbar_init();
     }
+    before_reading();  // (and before TMEM is asked for: a kernel that ends may still hold it)
     if (warp == 0) tmem_alloc(slot, 512);
     tc_fence_before();
     plan_piece<C::BN, C::THREADS>(p.w, plan);  // (synchronises the CTA)
@@ -855,8 +856,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);
     if (e != cudaSuccess) return e;
     const int ctas = attn_ctas(a, p.w, C::BN);
-    kernel<<<ctas, C::THREADS, C::SM_BYTES, s>>>(mq, mk, mv, p);
-    e = cudaGetLastError();
+    e = launch_early(kernel, dim3(ctas), C::THREADS, C::SM_BYTES, s, mq, mk, mv, p);
     return e != cudaSuccess ? e : launch_attn_join(a, p.w, ctas, s);
 }
 

@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv_copy_kernel(const KvArgs a, 
     const int tid = threadIdx.x, lane = tid & 31, c = (tid % LPR) * PE, sub = tid / LPR;
     const long first = (long)blockIdx.x * run;
     const int tokens = (int)min((long)run, p.Ttot - first), heads = 2 * p.Hkv;
+    next_may_begin();
+    before_reading();
     check_offsets(p);
     // This thread's rows, a pass at a time: whole tokens' rows side by side if a pass holds some, else a token's
     // rows in several passes.
@@ -254,8 +256,7 @@ cudaError_t launch_kv(const KvArgs &a, cudaStream_t s) {
     if (blocks > 0x7fffffffL) return cudaErrorInvalidConfiguration;
     int shift = 0;
     while ((1 << shift) < a.pg.page_size) ++shift;
-    kv_copy_kernel<WRITE, T, KIND, D><<<(unsigned)blocks, kKvThreads, 0, s>>>(a, run, shift);
-    return cudaGetLastError();
+    return launch_early(kv_copy_kernel<WRITE, T, KIND, D>, dim3((unsigned)blocks), kKvThreads, 0, s, a, run, shift);
 }
 
 template <bool WRITE, typename T, int KIND>

@@ -22,6 +22,28 @@ namespace gdn {
 constexpr float kMinKvScale = 7.8886090522101181e-31f;  // 2^-100
 
 // ---- sequences -------------------------------------------------------------------
+// A launch that may begin while the kernel before it in its stream still runs, so that the start of one hides
+// behind the end of the other. A kernel so launched calls before_reading() before it touches any memory that other
+// kernels use, with all its threads: that waits until everything before it in the stream is done. (One
+// session's token 13.5 -> 11.6 us a call, a long read 67.6 -> 64.9.)
+template <typename... P>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t s, P... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void before_reading() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// the kernel after this one may begin (and wait for this one's end)
+__device__ __forceinline__ void next_may_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct SeqInfo {
     long bos;  // first packed token
     int T;     // new tokens
