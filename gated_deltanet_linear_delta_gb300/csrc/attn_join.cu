@@ -5,7 +5,7 @@
 //
 // A split unit is joined once, by the blocks of the first boundary between pieces that lies in
 // it. Each row takes a team of 1, 2, 4 or 8 warps, as many as leave all of a unit's rows with the
-// blocks at once. With few rows that is a block: its warps share the parts (one session's single
+// blocks at once and have two to four parts each, which a warp loads side by side. With few rows that is a block: its warps share the parts (one session's single
 // token over a long cache has about 75 parts, and they should be in flight together) and add up
 // through shared memory in a fixed order. With 128 rows it is one warp, without any meeting: prompts
 // leave two or three parts a row, and a block for each took 37 us of their 143 us (8 prompts of 1024
@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
     const int last = r.cut.piece_of(r.begin - r.off + r.ntiles - 1);  // the piece that holds the unit's last key tile
     const int parts = last - c + 2, rows = r.tokens * w.G;
     int team = NW;
-    while (team > 1 && rows * team > (int)gridDim.y * NW) team >>= 1;
+    while (team > 1 && (rows * team > (int)gridDim.y * NW || parts <= 2 * team)) team >>= 1;
     const int per_block = NW / team, sub = wid % team;
     for (int base = blockIdx.y * per_block; base < rows; base += gridDim.y * per_block) {
         const int row = base + wid / team, t = row / w.G;
@@ -121,10 +121,11 @@ cudaError_t launch_t(const AttnWork &w, TOut *out, int Hq, int rows, int ctas, c
 cudaError_t launch_attn_join(const AttnArgs &a, const AttnWork &w, int ctas, cudaStream_t s) {
     if (ctas <= 1) return cudaSuccess;  // one piece: nothing is split
     const bool f32 = a.pg.dtype == GDN_F32;
+    const int rows = w.rows < w.TPT * w.G ? w.rows : w.TPT * w.G;
 #define GDN_JOIN_CASE(DV)                                                                      \
     case DV:                                                                                   \
-        return f32 ? launch_t<float, DV>(w, (float *)a.out, a.Hq, w.rows, ctas, s)                   \
-                   : launch_t<__nv_bfloat16, DV>(w, (__nv_bfloat16 *)a.out, a.Hq, w.rows, ctas, s);
+        return f32 ? launch_t<float, DV>(w, (float *)a.out, a.Hq, rows, ctas, s)                     \
+                   : launch_t<__nv_bfloat16, DV>(w, (__nv_bfloat16 *)a.out, a.Hq, rows, ctas, s);
     switch (a.pg.d) { GDN_JOIN_CASE(64) GDN_JOIN_CASE(128) GDN_JOIN_CASE(256) }
 #undef GDN_JOIN_CASE
     return cudaErrorInvalidValue;
