@@ -25,9 +25,9 @@
 // 8-bit codes become fp16 in registers (attn_tc.cu says why fp16, and how the scales enter).
 //
 // Measured: 128 sessions of 4096, 2 key heads with 8 query heads each, D = 256: bf16 175 us (6.1 TB/s of
-// 6.7 measured), e4m3 100 us (5.4); 32 of 8192, 8 key heads with 4, D = 128: bf16 171, int8 97, e4m3 95
-// us (5.5, 5.6 TB/s), where the codes' conversion takes 0.55 instructions a cycle and scheduler; one
-// session of 131072, e4m3, D = 256: 38 us, of which memory 20; one of 1000: 13 us, a chain of the plan,
+// 6.7 measured), e4m3 100 us (5.4); 32 of 8192, 8 key heads with 4, D = 128: bf16 170, int8 95, e4m3 95
+// us (5.8 TB/s for codes), where the codes' conversion takes 0.55 instructions a cycle and scheduler; one
+// session of 131072, e4m3, D = 256: 35 us, of which memory 20; one of 1000: 11.5 us, a chain of the plan,
 // the table, the first tiles, the warps' meeting and the joining kernel.
 #include <climits>
 

@@ -6,7 +6,7 @@
 // threads that share it, and the output tile (RT rows x D/16 columns a thread) in registers,
 // rescaled when the running maximum grows. It is bound by shared-memory reads (5 to 8 16-byte reads
 // per 16 to 64 multiply-adds): correct and steady, but no performance path. 2 x 100 tokens over 1000, 8
-// heads on 2, d = 64: 31 us, about 3 key tiles per CTA after the plan and before the joining kernel (two
+// heads on 2, d = 64: 28 us, about 3 key tiles per CTA after the plan and before the joining kernel (two
 // CTAs per SM: 37 us).
 #include <algorithm>
 

@@ -17,7 +17,7 @@
 //
 // Measured, 2048 tokens over 32768, 16 query heads on 2: bf16 683, 357 and 323 us for D = 256, 128 and
 // 64 (1.56 PFLOP/s for 256, of 1.92 measured), e4m3 860 us for 256 and 656 for 128 (int8 678). 8 prompts
-// of 1024 tokens, 32 heads on 8, D = 128: bf16 101, e4m3 204 us: 14 units of 4 or 5 tiles per CTA, whose
+// of 1024 tokens, 32 heads on 8, D = 128: bf16 98, e4m3 201 us: 14 units of 4 or 5 tiles per CTA, whose
 // starts and ends (Q in, rows out) count for half of it.
 //
 // Layout. TMEM holds O (D columns), two S buffers (P_j overlays S_j) and Q as the 16-bit A operand,

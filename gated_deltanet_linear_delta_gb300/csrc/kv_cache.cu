@@ -11,9 +11,9 @@
 // each, long ones spread the look-up over more bytes (with a token per warp, whose three dependent
 // reads stood before every 1 KiB, a long session was read at 3.4 TB/s; with runs at 6.0).
 //
-// Measured: 131072 tokens of 2 heads, d = 256, e4m3 to bf16: 67.5 us, 90% of the measured copy rate; 24
-// sessions of 8 heads, d = 128, int8 to fp32: 65.6 us, 93%; 16384 tokens of 8 heads, d = 128 stored as
-// int8: 30.9 us, 3.3 TB/s, bound by the instructions that quantise (0.7 of 1 a cycle and scheduler).
+// Measured: 131072 tokens of 2 heads, d = 256, e4m3 to bf16: 64.9 us, 93% of the measured copy rate; 24
+// sessions of 8 heads, d = 128, int8 to fp32: 63.3 us, 96%; 16384 tokens of 8 heads, d = 128 stored as
+// int8: 28.7 us, 3.5 TB/s, bound by the instructions that quantise (0.7 of 1 a cycle and scheduler).
 #include <algorithm>
 
 #include "kv_pages.cuh"
