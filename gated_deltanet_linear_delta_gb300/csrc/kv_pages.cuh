@@ -120,7 +120,7 @@ __device__ __forceinline__ float scale_int8(float amax) {
     return fmaxf(__fdiv_rn(amax, 127.f), kMinKvScale);
 }
 
-// 1 / s: of a power of two of 2^-100 or more, exact; of any s, to 2 ulp
+// 1 / s: of a power of two of 2^-100 or more, exact; of any s, to 1 ulp
 __device__ __forceinline__ float inverse_pow2(float s) { return __uint_as_float((254u << 23) - __float_as_uint(s)); }
 __device__ __forceinline__ float rcp_near(float s) {
     float y;
@@ -134,19 +134,50 @@ __device__ __forceinline__ uint32_t codes4_e4m3(const float *x, float inv) {  //
     const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[2] * inv, x[3] * inv), __NV_SATFINITE, __NV_E4M3);
     return (uint32_t)a | ((uint32_t)b << 16);
 }
+// two fp32 operations in one instruction
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_mul(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 f2_add(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ void f2_get(F2 a, float &x, float &y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+
 // The code is the quotient x / s, correctly rounded to fp32, rounded to an integer. x (1 / s) is within
-// 2^-16 of it, so only where such a product comes that close to the middle between two integers are
-// the four divided. (Adding 1.5 * 2^23 rounds to an integer, and leaves it in the low bits.)
+// 2^-15 of it (127 times 1 ulp of the reciprocal and two halves), so only where such a product comes
+// that close to the middle between two integers are the four divided. (Adding 1.5 * 2^23 rounds to an integer, and leaves it in the low bits.)
 __device__ __forceinline__ uint32_t codes4_int8(const float *x, float s, float inv) {
     constexpr float kRound = 12582912.f;
     float y[4], off = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float t = x[j] * inv;
-        y[j] = __fadd_rn(t, kRound);
-        off = fmaxf(off, fabsf(t - __fsub_rn(y[j], kRound)));
+    for (int j = 0; j < 4; j += 2) {
+        const F2 t = f2_mul(f2(x[j], x[j + 1]), f2(inv, inv)), r = f2_add(t, f2(kRound, kRound));
+        const F2 d = f2_fma(f2_add(r, f2(-kRound, -kRound)), f2(-1.f, -1.f), t);
+        float d0, d1;
+        f2_get(d, d0, d1);
+        f2_get(r, y[j], y[j + 1]);
+        off = fmaxf(off, fmaxf(fabsf(d0), fabsf(d1)));
     }
-    if (off > 0.4999f) {
+    if (off > 0.49995f) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = __fadd_rn(__fdiv_rn(x[j], s), kRound);
     }
