@@ -64,7 +64,7 @@ struct RCfg {
     static constexpr bool kPair = RINGB / (2 * SLOT) >= 2;
     static constexpr uint32_t STAGE = kPair ? 2 * SLOT : SLOT;
     static constexpr int NSL = RINGB / STAGE;
-    static_assert(NSL >= 2 && (kPair || CH == 16), "ring");
+    static_assert(NSL >= 2 && (kPair || (CH == 16 && !kCodes)), "ring");
     static constexpr int KS = D / 16;                           // products per score tile
     static constexpr int VE = kCodes ? (D == 64 ? 8 : 16) : 8;  // elements per piece of V
     static constexpr int MSTRIDE = D + 4;                       // floats per row where warps meet
@@ -206,11 +206,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 if (box < C::BOXES)
                     tma_load_3d(to + box * (C::LINES * 128), map, box * (C::kCodes ? 128 : 64), row0,
                                 good ? page * pg.Hkv + pc.h : -1, bar + fslot);
-                if constexpr (C::kCodes) {  // the scales of both come with K
-                    const bool of_v = C::kPair ? mine_v : lane == 14;
-                    if (good && (C::kPair ? box == 15 : !is_v && (lane & ~1) == 14))
-                        bulk_load(sc + (of_v ? CH : 0), (of_v ? p.v_scale : p.k_scale) + at, CH * 4, bar + fslot);
-                }
+                if (C::kCodes && good && box == 15)
+                    bulk_load(sc + (mine_v ? CH : 0), (mine_v ? p.v_scale : p.k_scale) + at, CH * 4, bar + fslot);
             } else {
                 // two boxes of 16 positions each: they may lie on two pages, and the second may lie past the end
                 const int half = box & 1, blk = box >> 1, pos = fill_pos + 16 * half;
