@@ -569,16 +569,16 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
     const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
     const float2 *stat = reinterpret_cast<const float2 *>(sm + C::SM_STAT) + row;
     float *rsq = reinterpret_cast<float *>(sm + C::SM_RS) + row;
-    const bool issuer = quarter == 0 && lane == 0;
     const uint32_t bytes = (uint32_t)(p.w.TPT * p.w.G) * 128;
     uint32_t fills = 0;  // of the stage so far
-    bool ok = true;
+    bool ok = true;      // the same for a warp's lanes: what follows a wait is done by all of them or by none
     auto unit_rows = [&](const Walk &w) { return min(p.w.TPT, w.pc.s.T - w.pc.i * p.w.TPT) * p.w.G; };
-    // 128 bytes of the unit's rows into the stage, once the four warps have read what was there
+    // 128 bytes of the unit's rows into the stage, once the four warps have read what was there: one warp waits, a lane
+    // of it issues the copy
     auto fetch = [&](const Walk &w, int part) {
-        if (issuer) {
-            if (fills > 0) ok = ok && wait_for(bar + C::B_QE, (fills - 1) & 1, p.budget);
-            if (ok) {
+        if (quarter == 0) {
+            if (fills > 0) ok = ok && warp_wait(bar + C::B_QE, (fills - 1) & 1, p.budget);
+            if (ok && lane == 0) {
                 mbar_expect_tx(bar + C::B_QF, bytes);
                 tma_load_3d(sm + C::SM_Q, mq, part * 64, w.pc.h * p.w.G, (int)(w.pc.s.bos + w.pc.i * p.w.TPT), bar + C::B_QF);
             }
