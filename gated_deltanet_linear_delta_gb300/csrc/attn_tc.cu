@@ -570,7 +570,8 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
     const float2 *stat = reinterpret_cast<const float2 *>(sm + C::SM_STAT) + row;
     float *rsq = reinterpret_cast<float *>(sm + C::SM_RS) + row;
     const uint32_t bytes = (uint32_t)(p.w.TPT * p.w.G) * 128;
-    uint32_t fills = 0;  // of the stage so far
+    uint32_t fills = 0;   // of the stage so far
+    uint32_t issued = 0;  // copies that this warp has begun (fewer, after a wait that ran out)
     bool ok = true;      // the same for a warp's lanes: what follows a wait is done by all of them or by none
     auto unit_rows = [&](const Walk &w) { return min(p.w.TPT, w.pc.s.T - w.pc.i * p.w.TPT) * p.w.G; };
     // 128 bytes of the unit's rows into the stage, once the four warps have read what was there: one warp waits, a lane
@@ -578,9 +579,12 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
     auto fetch = [&](const Walk &w, int part) {
         if (quarter == 0) {
             if (fills > 0) ok = ok && warp_wait(bar + C::B_QE, (fills - 1) & 1, p.budget);
-            if (ok && lane == 0) {
-                mbar_expect_tx(bar + C::B_QF, bytes);
-                tma_load_3d(sm + C::SM_Q, mq, part * 64, w.pc.h * p.w.G, (int)(w.pc.s.bos + w.pc.i * p.w.TPT), bar + C::B_QF);
+            if (ok) {
+                ++issued;
+                if (lane == 0) {
+                    mbar_expect_tx(bar + C::B_QF, bytes);
+                    tma_load_3d(sm + C::SM_Q, mq, part * 64, w.pc.h * p.w.G, (int)(w.pc.s.bos + w.pc.i * p.w.TPT), bar + C::B_QF);
+                }
             }
         }
         ++fills;
@@ -735,7 +739,9 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
         }
     }
     if (!ok && lane == 0) flag_error(p.w.pg.status);
-    if (fills > 0) mbar_wait(bar + C::B_QF, (fills - 1) & 1, kDrainBudget);  // a copy in flight lands before the CTA leaves
+    // the copy in flight lands before the CTA leaves: the last one begun, which is not the last one asked for if a wait
+    // ran out in between
+    if (issued > 0) mbar_wait(bar + C::B_QF, (issued - 1) & 1, kDrainBudget);
     __syncwarp();
 }
 

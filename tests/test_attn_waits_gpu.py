@@ -46,3 +46,21 @@ def test_any_wait_may_run_out(T, G, d, cache, cycles, monkeypatch):
     call(out)
     assert gdn.gdn_get_device_status() == gdn.GDN_OK
     assert_attention(out, *want)
+
+
+@pytest.mark.parametrize("cache", sorted(CACHES))
+@pytest.mark.parametrize("T,G,d", [(40, 8, 256), (100, 8, 128), (64, 4, 64)])
+def test_a_call_queued_behind_one_that_gives_up(T, G, d, cache, monkeypatch):
+    """Copies of a call that gives up land before its blocks leave: the call right behind it uses the same shared
+    memory, and its results are right."""
+    call, out, want = setting(T, G, d, cache)
+    lost = torch.empty_like(out)
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    for _ in range(4):
+        torch.zeros(1 << 28, dtype=torch.uint8, device=DEV)  # (larger than L2: copies come from memory)
+        monkeypatch.setenv("GDN_TEST_WAIT_CYCLES", "1")
+        call(lost)
+        monkeypatch.delenv("GDN_TEST_WAIT_CYCLES")
+        call(out)
+        assert gdn.gdn_get_device_status() == gdn.GDN_ERR_DEVICE_CHECK
+        assert_attention(out, *want)
