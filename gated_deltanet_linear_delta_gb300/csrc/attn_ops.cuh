@@ -134,6 +134,40 @@ inline bool rows_map(CUtensorMap *m, const void *base, int d, int heads, long to
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Values at positions that some rows of a unit see and others do not. A masked probability is 0, and 0 times an
+// infinity or a NaN is NaN, so in a product that the rows share such elements are taken as 0, and afterwards the rows
+// that see them get them added to their output: any weight leaves them what they are. (What is rare is kept out of the
+// kernels' code, which is fetched anew by every launch: the same inlined cost 8 prompts of 1024 tokens 7%.)
+__device__ __forceinline__ bool rarely(bool x) { return __builtin_expect(x, false); }
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {  // the sign bits of a bf16 pair's that are not
+    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;  // (all ones in the exponent)
+}
+__device__ __forceinline__ bool any_not_finite(uint4 x) {
+    return (not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w)) != 0;
+}
+// Zeroes them in 16 bytes of shared memory.
+static __device__ __noinline__ void drop_not_finite(uint4 *at) {
+    uint32_t *w = reinterpret_cast<uint32_t *>(at);
+    for (int i = 0; i < 4; ++i) w[i] &= ~((not_finite(w[i]) >> 15) * 0xffffu);
+    tc::fence_async_smem();  // products and later copies see it
+}
+// Adds those of one key head's cached values, positions first .. last, columns c .. c + n - 1, to an output row.
+// table: the sequence's pages; shift: log2 of their size.
+template <typename T>
+static __device__ __noinline__ void add_not_finite(const int32_t *table, int num_pages, int Hkv, int h, int shift,
+                                                   const __nv_bfloat16 *v_cache, int d, int first, int last, int c, int n,
+                                                   T *row) {
+    for (int pos = first; pos <= last; ++pos) {
+        const int page = table[pos >> shift];
+        if ((unsigned)page >= (unsigned)num_pages) continue;  // (values of zero)
+        const __nv_bfloat16 *v = v_cache + ((((long)page * Hkv + h) << shift) + (pos & ((1 << shift) - 1))) * d;
+        for (int i = c; i < c + n; ++i) {
+            const float x = __bfloat162float(v[i]);
+            if (!(fabsf(x) < INFINITY)) row[i] = from_f32<T>((float)row[i] + x);
+        }
+    }
+}
+
 // A running softmax reference m of a row (log2 domain), given its maximum over more keys: moved when
 // that has grown by more than 2^kGrow. Returns the factor for what was summed before.
 __device__ __forceinline__ bool above_reference(float m, float top) { return top > m + kGrow; }  // (-inf: any score)

@@ -82,6 +82,7 @@ struct RCfg {
 struct RowParams {
     AttnWork w;
     const __nv_bfloat16 *q;
+    const __nv_bfloat16 *v_cache;  // bf16 caches
     const float *k_scale, *v_scale;
     __nv_bfloat16 *out;
     int Hq;
@@ -163,7 +164,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         if (lane == 0) flag_error(pg.status);
         if (C::kCodes) clear_scales(sc, at);
     };
-    for (bool begun = pc.off == 0; pc.left > 0; begun = true) {
+    bool begun = pc.off == 0, repair = false;
+    while (pc.left > 0) {
         const int t0 = pc.i * w.TPT, rows = min(w.TPT, pc.s.T - t0) * w.G, len = pc.s.len;
         const int off = pc.off, take = (int)min((long)(pc.ntiles - off), pc.left);
         // this warp's chunks: positions start + BN i
@@ -309,7 +311,12 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 limit[y][i] = r < rows ? len - pc.s.T + t0 + r / w.G : INT_MAX;  // (rows past the last are not read)
                 rsc[y][i] = C::kCodes ? rs[r] * p.scale2 : p.scale2;
             }
-        const int sure = len - pc.s.T + t0;  // every row sees up to here
+        const int sure = len - pc.s.T + t0;                      // every row sees up to here
+        const int seen = sure + min(w.TPT, pc.s.T - t0);         // no row sees this position or one after it
+        // A value between the two that is not finite makes rows that do not see it NaN (0 times it). So a unit whose
+        // output is not finite is done again without such values, which the rows that see them get at the end. (To look
+        // for them beforehand made 2 tokens of 16 sessions 5% slower.)
+        const bool check = !C::kCodes && !repair && seen - sure > 1;
         for (int ch = 0; ch < chunks && !failed; ++ch) {
             const int pos0 = start + ch * BN;
             wait_full();
@@ -464,7 +471,14 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 if (failed) break;
             }
             const uint8_t *vc = ring + uslot * C::STAGE + (C::kPair ? C::SLOT : 0);
-            const bool tail = pos0 + CH > len;  // rows past the end: zeros
+            const bool tail = pos0 + CH > seen;  // rows past the last that counts: zeros
+            if (!C::kCodes && rarely(repair && pos0 + CH - 1 > sure)) {
+                constexpr int PR = C::ROWB / 16;
+                const int from = max(sure + 1 - pos0, 0), to = min(seen - pos0, CH);
+                for (int e = lane; e < (to - from) * PR; e += 32)
+                    drop_not_finite(reinterpret_cast<uint4 *>(const_cast<uint8_t *>(vc) + piece_at<C::ROWB, CH>(from + e / PR, e % PR)));
+                __syncwarp();
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -480,7 +494,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                             const uint2 y = *reinterpret_cast<const uint2 *>(vc + piece_at<C::ROWB, CH>(r, n >> 1) + (n & 1) * 8);
                             v[j][0] = y.x; v[j][1] = y.y; v[j][2] = v[j][3] = 0;
                         }
-                        if (tail && pos0 + r >= len) v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
+                        if (tail && pos0 + r >= seen) v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
                     }
 #pragma unroll
                     for (int t = 0; t < C::VE / 2; ++t) {  // elements 2 t, 2 t + 1 of the pieces
@@ -525,6 +539,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 }
             }
         __syncthreads();
+        bool bad = false;
         const bool whole = begun && off + take == pc.ntiles;
         for (int e = tid; e < rows * (D / 4); e += kThreads) {
             const int r = e / (D / 4), c = (e % (D / 4)) * 4;
@@ -542,6 +557,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 L = fmaf(f, a.y, L);
                 y.x = fmaf(f, z.x, y.x); y.y = fmaf(f, z.y, y.y); y.z = fmaf(f, z.z, y.z); y.w = fmaf(f, z.w, y.w);
             }
+            bad |= !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
             if (whole) {
                 const int t = t0 + r / w.G;
                 if (len - pc.s.T + t < 0) continue;  // padding: written as zeros
@@ -555,10 +571,24 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 if (c == 0) w.ml[at] = make_float2(M, L);
             }
         }
+        if (!C::kCodes && rarely(repair)) {  // what was dropped, for the rows that see it
+            for (int e = tid; e < rows * (D / 4); e += kThreads) {
+                const int r = e / (D / 4), c = (e % (D / 4)) * 4, t = t0 + r / w.G;
+                const int first = max(max(sure + 1, off * BN), 0), last = min(len - pc.s.T + t, (off + take) * BN - 1);
+                if (whole)
+                    add_not_finite(table, pg.num_pages, pg.Hkv, pc.h, P_shift, p.v_cache, D, first, last, c, 4,
+                                   p.out + ((pc.s.bos + t) * p.Hq + pc.h * w.G + r % w.G) * D);
+                else
+                    add_not_finite(table, pg.num_pages, pg.Hkv, pc.h, P_shift, p.v_cache, D, first, last, c, 4,
+                                   w.part + part_index(w, blockIdx.x, begun ? 1 : 0, r) * D);
+            }
+        }
+        fence_async_smem();  // the rings held O: before the next unit's copies
+        repair = __syncthreads_or(check && bad);
+        if (rarely(repair)) continue;
         pc.left -= take;
         if (pc.left > 0) next_unit<BN>(w, &pc);
-        fence_async_smem();  // the rings held O: before the next unit's copies
-        __syncthreads();
+        begun = true;
     }
     if (failed && lane == 0) flag_error(pg.status);
     // copies in flight (after a wait that ran out) must land before the CTA leaves
@@ -579,6 +609,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     RowParams p{};
     p.w = attn_work(a, R / G, C::BN < 256 ? 1 : 0);
     p.q = (const __nv_bfloat16 *)a.q;
+    p.v_cache = (const __nv_bfloat16 *)a.v_cache;
     p.k_scale = a.k_scale;
     p.v_scale = a.v_scale;
     p.out = (__nv_bfloat16 *)a.out;

@@ -60,6 +60,8 @@ struct Raw4<GDN_F32> {
     __device__ __forceinline__ float4 get() const { return x; }
 };
 
+__device__ __forceinline__ float finite_or_zero(float x) { return fabsf(x) < INFINITY ? x : 0.f; }
+
 template <int D, int R>
 struct SimtSmem {
     float q[R][D + 4];
@@ -82,7 +84,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
     plan_piece<BN, kThreads>(w, &sm.plan);
     if (sm.plan.padding) zero_padding(w, a.out, a.Hq, D, tid, kThreads);
     Piece pc = sm.plan.piece;
-    for (bool begun = pc.off == 0; pc.left > 0; begun = true) {
+    bool begun = pc.off == 0, careful = false;
+    while (pc.left > 0) {
         const int t0 = pc.i * w.TPT, rows = min(w.TPT, pc.s.T - t0) * w.G;
         const int off = pc.off, take = (int)min((long)(pc.ntiles - off), pc.left);
         __syncthreads();
@@ -96,11 +99,12 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
         float m[RT], l[RT];
         float4 o[RT][CT];
         int limit[RT];  // last position the row sees
+        const int sure = pc.s.len - pc.s.T + t0;  // ... that every row of the unit sees
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.f;
-            limit[r] = pc.s.len - pc.s.T + t0 + (ty * RT + r) / w.G;
+            limit[r] = sure + (ty * RT + r) / w.G;
             if (ty * RT + r >= rows) limit[r] = -1;
 #pragma unroll
             for (int c = 0; c < CT; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -160,6 +164,12 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
                 if (tid < BN) sm.at[tid] = at_next;
             }
             at_next = pool_row(j + 2);
+            if (__builtin_expect(careful, false)) {
+#pragma unroll 1
+                for (int e = tid; e < BN * D; e += kThreads)
+                    if (j * BN + e / D > sure) sm.v[e / D][e % D] = finite_or_zero(sm.v[e / D][e % D]);
+                __syncthreads();
+            }
             float s[RT][4];
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -221,6 +231,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
             }
             __syncwarp();
         }
+        bool bad = false;  // a row's output is not finite
         const bool whole = begun && off + take == pc.ntiles;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -229,6 +240,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
             for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
             const int row = ty * RT + r;
             if (row >= rows) continue;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+                bad |= !(fabsf(o[r][c].x) + fabsf(o[r][c].y) + fabsf(o[r][c].z) + fabsf(o[r][c].w) < INFINITY);
             if (whole) {
                 if (limit[r] < 0) continue;  // padding: already zeros
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;  // scores that are all -inf: zeros
@@ -244,8 +258,37 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
                 for (int c = 0; c < CT; ++c) *reinterpret_cast<float4 *>(w.part + at * D + 64 * c + 4 * tx) = o[r][c];
             }
         }
-        pc.left -= take;
-        if (pc.left > 0) next_unit<BN>(w, &pc);
+        if (__builtin_expect(careful, false)) {
+#pragma unroll 1
+            for (int r = 0; r < RT; ++r) {
+                const int row = ty * RT + r, last = min(sure + row / w.G, (off + take) * BN - 1);
+                if (row >= rows) continue;
+                float *dst = whole ? a.out + ((pc.s.bos + t0 + row / w.G) * a.Hq + pc.h * w.G + row % w.G) * D
+                                   : w.part + part_index(w, blockIdx.x, begun ? 1 : 0, row) * D;
+#pragma unroll 1
+                for (int pos = max(max(sure + 1, off * BN), 0); pos <= last; ++pos) {
+                    const long pg = pool_page(w.pg, pc.n, pos / w.pg.page_size);
+                    if (pg < 0) continue;
+                    Raw4<KIND> v;
+#pragma unroll 1
+                    for (int c = 4 * tx; c < D; c += 64) {
+                        v.template load<D>(a.v_cache, a.v_scale, (pg * w.pg.Hkv + pc.h) * w.pg.page_size + pos % w.pg.page_size, c);
+                        const float4 x = v.get();
+                        dst[c] += x.x - finite_or_zero(x.x); dst[c + 1] += x.y - finite_or_zero(x.y);
+                        dst[c + 2] += x.z - finite_or_zero(x.z); dst[c + 3] += x.w - finite_or_zero(x.w);
+                    }
+                }
+            }
+        }
+        // A value that is not finite makes rows that do not see it NaN (0 times it), so a unit whose output is not finite is
+        // done again with care: without the values that some rows do not see and that are not finite, which the rows that
+        // see them get added above. (Where every row sees all that any sees, there is no need.)
+        careful = !careful && rows > w.G && __syncthreads_or(bad);
+        if (!careful) {
+            pc.left -= take;
+            if (pc.left > 0) next_unit<BN>(w, &pc);
+            begun = true;
+        }
     }
 }
 

@@ -27,8 +27,9 @@
 //
 // Warps, in groups of four: two take the softmax, a thread per row and half of a tile's columns, which
 // meet once per tile for the row's maximum; one brings the rows' Q into TMEM and takes finished rows
-// out, beside the softmax of the neighbouring units; one has a warp each for the loads of K and V and
-// for the products; with an 8-bit cache one converts K tiles and one V tiles. The products run S_0, S_1,
+// out, beside the softmax of the neighbouring units; one has a warp each for the loads of K and V, for
+// the products and, with a bf16 cache, for a look through V; with an 8-bit cache one converts K tiles
+// and one V tiles. The products run S_0, S_1,
 // O(0), S_2, O(1), .. across units, so that the tensor cores work on S_{j+1} while the softmax of tile j
 // runs. All CTAs are persistent over their piece of the work, and every wait has a limit, after which
 // the CTA flags the status word and leaves.
@@ -41,8 +42,10 @@
 // Taking vs_j into the exponent keeps P' near 1 for the keys that matter whatever the scales' range.
 //
 // Masks. A row sees positions up to its own; scores past it are replaced (not multiplied), so what
-// K holds there has no effect. Rows of V past the sequence's end are zeroed in shared memory before
-// the product, since 0 * NaN would reach the sum.
+// K holds there has no effect. Of V, where 0 * NaN would reach the sum (bf16 caches; codes are finite):
+// steps of 16 positions that no row of the unit sees are left out of the product, positions past the
+// sequence's end are zeroed in shared memory, and from the first row's last position on elements that
+// are not finite are taken as 0 and added to the rows that see them when these leave.
 #include <type_traits>
 
 #include "attn_ops.cuh"
@@ -89,9 +92,12 @@ struct Cfg {
                          B_REV = B_REK + NR, B_COL = B_REV + NR, B_S = B_COL + COLS, B_PV = B_S + kTurns,
                          B_P = B_PV + kTurns, B_ST = B_P + 2, B_SF = B_ST + 2,
                          B_Q = B_SF + 2, B_OF = B_Q + NQ, B_QF = B_OF + 1, B_QE = B_QF + 1,
-                         B_US = B_QE + 1 /* all S of a unit */, B_UO = B_US + 1 /* all of its O */, B_FIN = B_UO + 1, B_COUNT = B_FIN + 1;
-    static constexpr uint32_t SM_INFO = SM_BAR + B_COUNT * 8;                // [2][NR] valid rows, page mask
-    static constexpr uint32_t SM_TMEM = SM_INFO + (NR ? 2 * NR : 1) * 8;
+                         B_US = B_QE + 1 /* all S of a unit */, B_UO = B_US + 1 /* all of its O */, B_FIN = B_UO + 1,
+                         B_CV = B_FIN + 1 /* V looked through (bf16 caches) */, B_COUNT = B_CV + (kCodes ? 0 : NV);
+    // [2][NR] valid rows, page mask; bf16 caches: [8], by unit, whether it has values that are not finite and hidden from
+    // some of its rows
+    static constexpr uint32_t SM_INFO = SM_BAR + B_COUNT * 8;
+    static constexpr uint32_t SM_TMEM = SM_INFO + (NR ? 2 * NR : 4) * 8;
     static constexpr uint32_t SM_PLAN = (SM_TMEM + 8 + 15) & ~15u;
     static constexpr uint32_t SM_BYTES = SM_PLAN + sizeof(PlanSmem) + 1024;
     static_assert(SM_BYTES <= 232448, "over the 227 KiB opt-in limit");
@@ -99,7 +105,7 @@ struct Cfg {
 
 struct TcParams {
     AttnWork w;
-    const uint8_t *k_cache, *v_cache;  // 8-bit caches
+    const uint8_t *k_cache, *v_cache;  // 8-bit caches (and bf16 values that are not finite)
     const float *k_scale, *v_scale;
     __nv_bfloat16 *out;
     int Hq;
@@ -277,61 +283,120 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
         rk.next();
         ++t;
     };
-    // V of tile o, `first` of its unit, with `valid` positions before the end, ready to be multiplied
-    auto v_ready = [&](uint32_t o, bool first, int valid) -> bool {
-        if (!warp_wait(bar + C::B_FV + rv.slot, rv.phase, p.budget)) return false;
-        if (!C::kCodes && valid < BN) {  // rows of V past the end: zeros
-            const int dead = (BN - valid) * 8;
-            for (int e = lane; e < dead * C::NB; e += 32)
-                *reinterpret_cast<uint4 *>(sm + C::SM_V + rv.slot * C::SLOT + (e / dead) * (BN * 128) + valid * 128 +
-                                           (e % dead) * 16) = make_uint4(0, 0, 0, 0);
-            fence_async_smem();
-            __syncwarp();
-        }
+    // V of tile o, `first` of its unit, ready to be multiplied
+    auto v_ready = [&](uint32_t o, bool first) -> bool {
+        if (!warp_wait(bar + (C::kCodes ? C::B_FV : C::B_CV) + rv.slot, rv.phase, p.budget)) return false;
         if (first && o > 0) {  // the unit before has been taken out of O
             if (!warp_wait(bar + C::B_OF, o_free, p.budget)) return false;
             o_free ^= 1;
         }
         return true;
     };
-    auto product_o = [&](uint32_t o, bool first, bool last) -> bool {
+    auto product_o = [&](uint32_t o, bool first, bool last, int seen) -> bool {
         if (!warp_wait(bar + C::B_P + (o & 1), (o >> 1) & 1, p.budget)) return false;
         tc_fence_after();
         const uint64_t d = desc_v + (uint64_t)(rv.slot * (C::SLOT >> 4));
         const uint32_t a = tmem + C::TM_S + (o & 1) * BN;
-#pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks)
+        auto step = [&](int ks) {
             mma_f16_ts_by(lead, tmem + C::TM_O, a + (ks < BN / 32 ? 8 * ks : BN / 2 + 8 * (ks - BN / 32)),
                           d + (uint64_t)(ks * 128), ID_O, !first || ks > 0);
+        };
+        if (C::kCodes || seen >= BN) {
+#pragma unroll
+            for (int ks = 0; ks < BN / 16; ++ks) step(ks);
+        } else {
+#pragma unroll 1
+            for (int ks = 0; 16 * ks < seen; ++ks) step(ks);
+        }
         mma_commit_by(lead, bar + C::B_PV + (o & (C::kTurns - 1)));
-        if (last) mma_commit_by(lead, bar + C::B_UO);
+        if (last) {
+            mma_commit_by(lead, bar + C::B_UO);
+            if (!C::kCodes) {
+                if (lane == 0) mbar_arrive(bar + C::B_UO);
+                __syncwarp();
+            }
+        }
         rv.next();
         return true;
     };
     bool ok = true, prev_first = false, prev_last = false;
-    int prev_valid = BN;
+    int prev_seen = BN;
     if (k.pc.left > 0) {
         do {
-            const int n = k.take(), left = k.pc.s.len - k.pc.off * BN;
+            const int n = k.take();
+            // positions that a row of the unit sees, from the piece's first on
+            const int seen = k.pc.s.len - max(k.pc.s.T - (k.pc.i + 1) * p.w.TPT, 0) - k.pc.off * BN;
             ok = warp_wait(bar + C::B_Q + rq.slot, rq.phase, p.budget) && (t > 0 || k_ready());
             qslot = rq.slot;
             rq.next();
             for (int jj = 0; jj < n && ok; ++jj) {
                 const bool more = jj + 1 < n || k.pc.left > n;  // another tile follows in the piece
                 product_s(jj + 1 == n);
-                if (t > 1) ok = v_ready(t - 2, prev_first, prev_valid) && product_o(t - 2, prev_first, prev_last);
+                if (t > 1) ok = v_ready(t - 2, prev_first) && product_o(t - 2, prev_first, prev_last, prev_seen);
                 if (ok && more) ok = k_ready();
                 prev_first = jj == 0;
                 prev_last = jj + 1 == n;
-                prev_valid = left - jj * BN;
+                prev_seen = seen - jj * BN;
             }
         } while (ok && walk_next<BN>(p.w, &k));
-        ok = ok && v_ready(t - 1, prev_first, prev_valid) && product_o(t - 1, prev_first, true);
+        ok = ok && v_ready(t - 1, prev_first) && product_o(t - 1, prev_first, true, prev_seen);
     }
     if (!ok && lane == 0) flag_error(p.w.pg.status);
     mma_commit_by(lead, bar + C::B_FIN);  // all products done before TMEM is given back
     mbar_wait(bar + C::B_FIN, 0, kDrainBudget);
     __syncwarp();
+}
+
+// ---- V of bf16 caches, looked through ---------------------------------------------------
+// One warp passes V tiles on to the products, and on its way looks through what not all of a unit's rows see: elements
+// that are not finite become zeros (the rows group adds them to the rows that see them), and so do positions past the
+// end. (8 prompts of 1024 tokens, 32 heads on 8, D = 128: 100 us without such a look, 102 by this warp, 117 by the one
+// that issues the products.)
+template <int D, int KIND>
+__device__ void check_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k) {
+    using C = Cfg<D, KIND>;
+    constexpr int BN = C::BN, PR = 8 * C::NB;  // 16-byte pieces of a row
+    const int lane = threadIdx.x & 31;
+    int *flags = reinterpret_cast<int *>(sm + C::SM_INFO);
+    Ring<C::NV> ring;
+    uint32_t unit = 0;
+    bool ok = true;
+    if (k.pc.left > 0) do {
+        const int n = k.take(), t0 = k.pc.i * p.w.TPT;
+        // of the tile's positions: those before the end, those that every row sees, those that a row sees
+        int valid = k.pc.s.len - k.pc.off * BN, sure = valid - k.pc.s.T + t0 + 1;
+        int seen = sure + min(p.w.TPT, k.pc.s.T - t0) - 1;
+        bool dropped = false;
+        for (int jj = 0; jj < n; ++jj, valid -= BN, sure -= BN, seen -= BN) {
+            ok = warp_wait(bar + C::B_FV + ring.slot, ring.phase, p.budget);
+            if (!ok) break;
+            if (sure < BN) {
+                uint8_t *v = sm + C::SM_V + ring.slot * C::SLOT;
+                auto piece = [&](int row, int e) {
+                    return reinterpret_cast<uint4 *>(v + (e % PR / 8) * (BN * 128) + (row + e / PR) * 128 + (e & 7) * 16);
+                };
+                const int from = max(sure, 0), end = (min(seen, BN) + 15) & ~15, to = min(end, valid);
+                bool bad = false;
+                const uint4 *at = piece(from, lane);
+#pragma unroll 2
+                for (int e = lane; e < (to - from) * PR; e += 32, at += 32 / PR * 8) bad |= any_not_finite(*at);
+                if (rarely(__any_sync(0xffffffffu, bad))) {
+                    for (int e = lane; e < (to - from) * PR; e += 32) drop_not_finite(piece(from, e));
+                    dropped = true;
+                }
+                if (end > to) {
+                    for (int e = lane; e < (end - to) * PR; e += 32) *piece(to, e) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                }
+            }
+            if (jj + 1 == n && lane == 0) flags[unit & 7] = dropped;  // (this warp is at most NV units ahead of the products)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar + C::B_CV + ring.slot);
+            ring.next();
+        }
+        ++unit;
+    } while (ok && walk_next<BN>(p.w, &k));
+    if (!ok && lane == 0) flag_error(p.w.pg.status);
 }
 
 // ---- 8-bit tiles to fp16 --------------------------------------------------------------
@@ -701,6 +766,7 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
                 const int t0 = k.pc.i * p.w.TPT;
                 const bool whole = k.begun && k.pc.off + n == k.pc.ntiles;
                 const float inv = l == 0.f ? 0.f : 1.f / l;
+                const bool repair = !C::kCodes && reinterpret_cast<const volatile int *>(sm + C::SM_INFO)[unit & 7];
                 const bool store = row < rows && (!whole || k.pc.s.len - k.pc.s.T + t0 + tok >= 0);  // (padding: zeros already)
                 const long part = part_index(p.w, blockIdx.x, k.begun ? 1 : 0, row);
                 if (!whole && store) p.w.ml[part] = make_float2(m, l);
@@ -729,6 +795,15 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
                     }
                 }
                 tc_fence_before();
+                if (!C::kCodes && rarely(repair) && store) {  // what the products left out, for the row if it sees it
+                    const KvPages &pg = p.w.pg;
+                    const int sure = k.pc.s.len - k.pc.s.T + t0, shift = 31 - __clz(pg.page_size);
+                    const int first = max(max(sure + 1, k.pc.off * BN), 0), last = min(sure + tok, (k.pc.off + n) * BN - 1);
+                    const int32_t *table = pg.table + (long)k.pc.n * pg.max_pages;
+                    const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(p.v_cache);
+                    if (whole) add_not_finite(table, pg.num_pages, pg.Hkv, k.pc.h, shift, v, D, first, last, 0, D, out);
+                    else add_not_finite(table, pg.num_pages, pg.Hkv, k.pc.h, shift, v, D, first, last, 0, D, p.w.part + part * D);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + C::B_OF);
@@ -789,9 +864,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         mbar_init(bar + C::B_OF, kGroup);
         mbar_init(bar + C::B_QF, 1);
         mbar_init(bar + C::B_US, 1);
-        mbar_init(bar + C::B_UO, 1);
+        mbar_init(bar + C::B_UO, C::kCodes ? 1 : 2);  // (the products, and what SM_INFO says)
         mbar_init(bar + C::B_QE, kGroup);
         mbar_init(bar + C::B_FIN, 1);
+        if (!C::kCodes)
+            for (int s = 0; s < C::NV; ++s) mbar_init(bar + C::B_CV + s, 1);
         fence_mbar_init();
     }
     before_reading();  // (and before TMEM is asked for: a kernel that ends may still hold it)
@@ -820,14 +897,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             load_role<D, KIND, true>(p, sm, bar, k, &mv);
         } else if (warp == kMmaWarp) {
             mma_role<D, KIND>(p, sm, sb, bar, k, tmem);
-        } else {
+        } else if constexpr (C::kCodes) {
             if (plan->padding) zero_padding(p.w, p.out, p.Hq, D, tid & 31, 32);
+        } else {
+            check_role<D, KIND>(p, sm, bar, k);
         }
     } else if constexpr (C::kCodes) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
         if (group == kConvWarp0 / kGroup) convert_role<D, KIND, false>(p, sm, bar, (uint32_t)k.pc.left);
         else convert_role<D, KIND, true>(p, sm, bar, (uint32_t)k.pc.left);
     }
+    if (!C::kCodes && plan->padding) zero_padding(p.w, p.out, p.Hq, D, tid, C::THREADS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();

@@ -383,7 +383,9 @@ GDN_API int gdn_kv_read(const void *k_cache, const void *v_cache, const float *k
  *         the call's work on `stream` has finished, whatever was in it before. Calls whose work may
  *         overlap on the GPU must use different workspaces.
  * Scores and softmax statistics are fp32. A row whose scores are all -infinity gives zeros. What
- * lies in the cache at or past kv_lens[n] has no effect, whatever its value. The result does not
+ * lies in the cache past a token's position has no effect on it, whatever its value: an infinity or
+ * a NaN in a later token's rows, or anything at or past kv_lens[n]. (An 8-bit cache holds what
+ * gdn_kv_write stores, whose codes are finite.) The result does not
  * depend on the order in which the GPU runs its parts.
  * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
  */
