@@ -3,6 +3,7 @@
 // queued; a failed check returns its gdn_status and touches nothing.
 #include <stdint.h>
 
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
@@ -416,7 +417,7 @@ int gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
     int rc = kv_checks(B, T, cu_seqlens, Hq, Hkv, d, num_pages, page_size, max_pages, dtype, cache_dtype, q_stride,
                        (int64_t)Hkv * d);
     if (rc != GDN_OK || B == 0 || T == 0) return rc;
-    if (num_pages == 0 || max_pages == 0) return GDN_ERR_INVALID_ARG;
+    if (num_pages == 0 || max_pages == 0 || !std::isfinite(scale)) return GDN_ERR_INVALID_ARG;
     rc = kv_pointers(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, num_pages, max_pages, dtype,
                      cache_dtype, q, out);
     if (rc != GDN_OK) return rc;

@@ -377,7 +377,7 @@ GDN_API int gdn_kv_read(const void *k_cache, const void *v_cache, const float *k
  * T = 1 is the decode step, T of a few the check of speculated tokens, a large T a fragment of a
  * prompt over what is cached of it: a prompt cut into fragments gives the same result.
  *   q   : [Ttot][Hq][d], token stride q_stride.   out : [Ttot][Hq][d], contiguous.
- *   scale : the softmax scale, for instance d^-1/2.
+ *   scale : the softmax scale, for instance d^-1/2; finite.
  *   workspace : DEVICE memory, 256-byte aligned, of at least
  *         gdn_paged_attn_workspace_size(B, T, cu_seqlens != NULL, Hq, Hkv, d) bytes: scratch until
  *         the call's work on `stream` has finished, whatever was in it before. Calls whose work may
