@@ -3,9 +3,13 @@
 // A decode step's call on the GPU is shorter than reading twenty tensor attributes in Python and
 // converting twenty-six arguments (about 12 us of host time for gdn_paged_attn), so these three calls
 // check their tensors and marshal their arguments here; __init__.py declares them. Each returns the C
-// call's status; tensors that do not fit together raise TypeError or ValueError.
+// call's status; tensors that do not fit together raise TypeError or ValueError, and what torch throws
+// while they are read (C++ exceptions must not reach the interpreter) becomes a RuntimeError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+
+#include <cmath>
+#include <exception>
 
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -33,6 +37,8 @@ bool tensor(PyObject *o, const Tensor *&t, bool optional = false) {
     if (o == Py_None && optional) return true;
     if (!THPVariable_Check(o)) return refuse(PyExc_TypeError, "expected a torch tensor");
     t = &THPVariable_Unpack(o);
+    // (sparse and nested tensors have no strides to ask for)
+    if (t->layout() != at::kStrided || t->is_nested()) return refuse(PyExc_TypeError, "expected a dense tensor");
     return true;
 }
 
@@ -137,9 +143,25 @@ bool arguments(Py_ssize_t got, Py_ssize_t want) {
     return got == want || refuse(PyExc_TypeError, "wrong number of arguments");
 }
 
+// A call as the interpreter makes it, with what it throws as a Python exception. (It may throw only with the
+// interpreter's lock held.)
+template <PyObject *(*CALL)(PyObject *const *, Py_ssize_t)>
+PyObject *entry(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    try {
+        return CALL(a, n);
+    } catch (const c10::Error &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "unknown C++ exception");
+    }
+    return nullptr;
+}
+
 // (k, v, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, B, T, stream)
 template <bool WRITE>
-PyObject *kv_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *kv_copy(PyObject *const *a, Py_ssize_t n) {
     const Tensor *k, *v;
     Call c;
     if (!arguments(n, 12) || !tensor(a[0], k) || !tensor(a[1], v) || !kv_call(*k, *v, a + 2, c)) return nullptr;
@@ -149,22 +171,22 @@ PyObject *kv_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     void *stream = PyLong_AsVoidPtr(a[11]);
     if (PyErr_Occurred()) return nullptr;
+    void *kp = k->data_ptr(), *vp = v->data_ptr();
+    const int64_t ks = token_stride(*k), vs = token_stride(*v);
     int rc;
     Py_BEGIN_ALLOW_THREADS;
     if (WRITE)
-        rc = gdn_kv_write(k->data_ptr(), v->data_ptr(), c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table, c.lens, c.cu,
-                          c.B, c.T, c.Hkv, c.d, c.pages, c.page, c.width, token_stride(*k), token_stride(*v), c.dtype,
-                          c.cache_dtype, stream);
+        rc = gdn_kv_write(kp, vp, c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table, c.lens, c.cu, c.B, c.T, c.Hkv, c.d,
+                          c.pages, c.page, c.width, ks, vs, c.dtype, c.cache_dtype, stream);
     else
-        rc = gdn_kv_read(c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table, c.lens, c.cu, k->data_ptr(), v->data_ptr(),
-                         c.B, c.T, c.Hkv, c.d, c.pages, c.page, c.width, token_stride(*k), token_stride(*v), c.dtype,
-                         c.cache_dtype, stream);
+        rc = gdn_kv_read(c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table, c.lens, c.cu, kp, vp, c.B, c.T, c.Hkv, c.d,
+                         c.pages, c.page, c.width, ks, vs, c.dtype, c.cache_dtype, stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);
 }
 
 // (q, out, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, B, T, scale, workspace, stream)
-PyObject *paged_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
+PyObject *paged_attn(PyObject *const *a, Py_ssize_t n) {
     const Tensor *q, *out, *ws;
     Call c;
     if (!arguments(n, 14) || !tensor(a[0], q) || !tensor(a[1], out) || !kv_call(*q, *out, a + 2, c) || !tensor(a[12], ws))
@@ -176,19 +198,21 @@ PyObject *paged_attn(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const double scale = a[11] == Py_None ? 1.0 / std::sqrt((double)c.d) : PyFloat_AsDouble(a[11]);
     void *stream = PyLong_AsVoidPtr(a[13]);
     if (PyErr_Occurred()) return nullptr;
+    void *qp = q->data_ptr(), *op = out->data_ptr(), *wp = ws->data_ptr();
+    const int64_t stride = token_stride(*q);
+    const size_t bytes = ws->nbytes();
     int rc;
     Py_BEGIN_ALLOW_THREADS;
-    rc = gdn_paged_attn(q->data_ptr(), c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table, c.lens, c.cu, out->data_ptr(),
-                        c.B, c.T, c.H, c.Hkv, c.d, c.pages, c.page, c.width, token_stride(*q), (float)scale, c.dtype,
-                        c.cache_dtype, ws->data_ptr(), (size_t)ws->nbytes(), stream);
+    rc = gdn_paged_attn(qp, c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table, c.lens, c.cu, op, c.B, c.T, c.H, c.Hkv, c.d,
+                        c.pages, c.page, c.width, stride, (float)scale, c.dtype, c.cache_dtype, wp, bytes, stream);
     Py_END_ALLOW_THREADS;
     return PyLong_FromLong(rc);
 }
 
 PyMethodDef methods[] = {
-    {"kv_write", (PyCFunction)(void (*)(void))kv_copy<true>, METH_FASTCALL, "gdn_kv_write"},
-    {"kv_read", (PyCFunction)(void (*)(void))kv_copy<false>, METH_FASTCALL, "gdn_kv_read"},
-    {"paged_attn", (PyCFunction)(void (*)(void))paged_attn, METH_FASTCALL, "gdn_paged_attn"},
+    {"kv_write", (PyCFunction)(void (*)(void))entry<kv_copy<true>>, METH_FASTCALL, "gdn_kv_write"},
+    {"kv_read", (PyCFunction)(void (*)(void))entry<kv_copy<false>>, METH_FASTCALL, "gdn_kv_read"},
+    {"paged_attn", (PyCFunction)(void (*)(void))entry<paged_attn>, METH_FASTCALL, "gdn_paged_attn"},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "The paged cache calls for torch tensors.", -1, methods,
