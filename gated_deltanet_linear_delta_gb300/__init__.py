@@ -50,6 +50,7 @@ _I = ctypes.c_int
 _L = ctypes.c_int64
 _calls = None
 _DTYPE = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # the current stream of a device as a raw cudaStream_t (falls back to the Stream object)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -131,7 +132,10 @@ def _ptr(t: torch.Tensor | None):
 
 
 def _stream(stream, t: torch.Tensor | None = None):
-    """cudaStream_t of `stream`, or of the current stream of t's device (None: the current device)."""
+    """cudaStream_t of `stream`, or of the current stream. The library launches on the current device, so a call
+    whose tensor t lies on another one is refused here (its kernels would run where the tensors are not)."""
+    if t is not None and t.get_device() != _current_device():
+        raise ValueError("tensors must be on the current CUDA device (torch.cuda.set_device)")
     if stream is None:
         if _raw_stream is not None:
             return _raw_stream(t.get_device() if t is not None else torch.cuda.current_device())
@@ -336,15 +340,16 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, kv_lens, out, k_scale=None,
     """Causal attention of the new tokens' q [Ttot, Hq, d] over their sequences' paged caches, into `out`.
     `scale` is d**-0.5 unless given. `workspace`: a uint8 CUDA tensor of gdn_paged_attn_workspace_size(...)
     bytes that a program keeps; without one the call takes it from torch's allocator."""
+    on = _stream(stream, q) if q.is_cuda else 0
     if workspace is None and q.is_cuda:
         packed = cu_seqlens is not None
         n = kv_lens.numel() if B is None else B
         need = gdn_paged_attn_workspace_size(n, q.shape[0] if packed else (q.shape[0] // n if n else 0), q.shape[1],
                                              k_cache.shape[1], k_cache.shape[-1], packed)
-        with torch.cuda.device(q.device), torch.cuda.stream(_torch_stream(stream, q)):
+        with torch.cuda.stream(_torch_stream(stream, q)):
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     rc = (_calls or _load_calls()).paged_attn(q, out, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens,
-                                              B, T, scale, workspace, _stream(stream, q) if q.is_cuda else 0)
+                                              B, T, scale, workspace, on)
     if rc:
         raise GDNError(rc, "gdn_paged_attn")
 

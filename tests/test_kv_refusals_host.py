@@ -60,3 +60,19 @@ def test_tensors_without_a_plain_layout(lib, kind):  # noqa: F811
     """Sparse and nested tensors raise in Python; an exception that left the module would end the process."""
     r = subprocess.run([sys.executable, "-c", ODD, kind], capture_output=True, text=True, cwd=ROOT, timeout=300)
     assert r.returncode == 0 and "all refused" in r.stdout, (r.returncode, r.stderr[-2000:])
+
+
+def test_tensors_of_another_device(monkeypatch):
+    """The stream of every call is asked for with one of its tensors, which has to be on the current device."""
+    import gated_deltanet_linear_delta_gb300 as gdn
+
+    class Elsewhere:
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(gdn, "_current_device", lambda: 0, raising=False)
+    for stream in (None, 0, 1234):
+        with pytest.raises(ValueError):
+            gdn._stream(stream, Elsewhere())
+    monkeypatch.setattr(gdn, "_current_device", lambda: 1)
+    assert gdn._stream(1234, Elsewhere()) == 1234
