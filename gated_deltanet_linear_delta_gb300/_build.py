@@ -3,8 +3,9 @@
 Each .cu file is compiled to an object in parallel, then linked into one
 shared library with the CUDA runtime linked statically, so the library needs
 only the NVIDIA driver at run time. binding.cpp becomes the CPython module
-``_calls`` beside it, linked against that library and torch. The results live
-in ``_lib/`` next to this file (git-ignored).
+``_calls`` beside it, linked against that library and torch; where torch cannot
+be imported the library is built alone. The results live in ``_lib/`` next to
+this file (git-ignored).
 """
 from __future__ import annotations
 
@@ -22,6 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB_NAME = "libgdn_gb300.so"
 CALLS_NAME = "_calls.so"
+BINDING = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -39,9 +41,30 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _torch_flags() -> tuple[list[str], list[str]]:
-    """Compiler and linker flags of a CPython module that takes torch tensors."""
-    import torch
+def _hash(paths: list[str], *words: str) -> str:
+    h = hashlib.sha256(" ".join(words).encode())
+    for p in paths:
+        h.update(os.path.basename(p).encode())
+        with open(p, "rb") as fh:
+            h.update(fh.read())
+    return h.hexdigest()
+
+
+def _files(*dirs: str) -> list[str]:
+    return [p for d in dirs for p in (os.path.join(d, f) for f in sorted(os.listdir(d))) if os.path.isfile(p)]
+
+
+def _fingerprint() -> str:
+    """Of all that the library is made from."""
+    return _hash([p for p in _files(CSRC, INCLUDE) if p != BINDING], *ARCH, *NVCC_FLAGS)
+
+
+def _torch_flags():
+    """Compiler and linker flags of a CPython module that takes torch tensors; None without torch."""
+    try:
+        import torch
+    except ImportError:
+        return None
     root = os.path.dirname(torch.__file__)
     inc = os.path.join(root, "include")
     return ([f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
@@ -49,18 +72,13 @@ def _torch_flags() -> tuple[list[str], list[str]]:
             [f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"])
 
 
-def _fingerprint() -> str:
+def _binding_fingerprint():
+    """Of all that the module is made from; None without torch."""
+    flags = _torch_flags()
+    if flags is None:
+        return None
     import torch
-    h = hashlib.sha256(f"{torch.__version__} {sysconfig.get_python_version()}".encode())
-    for d in (CSRC, INCLUDE):
-        for f in sorted(os.listdir(d)):
-            p = os.path.join(d, f)
-            if os.path.isfile(p):
-                h.update(f.encode())
-                with open(p, "rb") as fh:
-                    h.update(fh.read())
-    h.update(" ".join(ARCH + NVCC_FLAGS).encode())
-    return h.hexdigest()
+    return _hash([BINDING, *_files(INCLUDE)], torch.__version__, sysconfig.get_python_version(), *flags[0], *flags[1])
 
 
 def lib_path() -> str:
@@ -71,57 +89,63 @@ def calls_path() -> str:
     return os.path.join(OUT_DIR, CALLS_NAME)
 
 
+def _fresh(stamp: str, built: str, fp: str) -> bool:
+    if not (os.path.exists(built) and os.path.exists(stamp)):
+        return False
+    with open(stamp) as f:
+        return f.read().strip() == fp
+
+
+def _run(cmd: list[str], what: str) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
+def _link(cmd: list[str], to: str, stamp: str, fp: str, what: str) -> None:
+    tmp = to + f".{os.getpid()}.tmp"
+    _run([*cmd[:1], "-shared", "-o", tmp, *cmd[1:]], what)
+    os.replace(tmp, to)
+    with open(stamp, "w") as f:
+        f.write(fp)
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None) -> str:
-    """Compile every .cu under csrc/ and link libgdn_gb300.so. Returns its path."""
+    """Compile every .cu under csrc/ and link libgdn_gb300.so, and with torch the module for its tensors. Returns the
+    library's path."""
     os.makedirs(OUT_DIR, exist_ok=True)
-    stamp = os.path.join(OUT_DIR, "build.stamp")
-    fp = _fingerprint()
-    if not force and os.path.exists(lib_path()) and os.path.exists(calls_path()) and os.path.exists(stamp):
-        with open(stamp) as f:
-            if f.read().strip() == fp:
-                return lib_path()
-    nv = nvcc()
-    objs = []
+    stamp, calls_stamp = os.path.join(OUT_DIR, "build.stamp"), os.path.join(OUT_DIR, "calls.stamp")
+    fp, calls_fp = _fingerprint(), _binding_fingerprint()
+    library = force or not _fresh(stamp, lib_path(), fp)
+    calls = calls_fp is not None and (force or not _fresh(calls_stamp, calls_path(), calls_fp))
+    cxx = shutil.which("g++") or "c++"
 
     def compile_one(src):
         obj = os.path.join(OUT_DIR, os.path.basename(src)[:-3] + ".o")
-        cmd = [nv, *ARCH, *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout.strip() or r.stderr.strip()):
-            print(r.stdout + r.stderr)
+        out = _run([nvcc(), *ARCH, *NVCC_FLAGS, f"-I{INCLUDE}", f"-I{CSRC}", "-c", src, "-o", obj],
+                   f"nvcc failed on {os.path.basename(src)}")
+        if verbose and out.strip():
+            print(out)
         return obj
 
     def compile_binding():
         obj = os.path.join(OUT_DIR, "binding.o")
-        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-I{INCLUDE}",
-               *_torch_flags()[0], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        _run([cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-I{INCLUDE}", *_torch_flags()[0], "-c", BINDING,
+              "-o", obj], "g++ failed on binding.cpp")
         return obj
 
-    srcs = sources()
+    srcs = sources() if library else []
     with cf.ThreadPoolExecutor(max_workers=jobs or min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(compile_binding)
+        binding = ex.submit(compile_binding) if calls else None
         objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
-    tmp = lib_path() + f".{os.getpid()}.tmp"
-    cmd = [nv, *ARCH, "-shared", "-cudart", "static", "-Xlinker", f"-soname={LIB_NAME}", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, lib_path())
-    tmp = calls_path() + f".{os.getpid()}.tmp"
-    cmd = [shutil.which("g++") or "c++", "-shared", "-o", tmp, binding_obj, f"-L{OUT_DIR}", f"-l:{LIB_NAME}",
-           "-Wl,-rpath,$ORIGIN", *_torch_flags()[1]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link of the binding failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, calls_path())
-    with open(stamp, "w") as f:
-        f.write(fp)
+        binding_obj = binding.result() if calls else None
+    if library:
+        _link([nvcc(), *ARCH, "-cudart", "static", "-Xlinker", f"-soname={LIB_NAME}", *objs], lib_path(), stamp, fp,
+              "link failed")
+    if calls:
+        _link([cxx, binding_obj, f"-L{OUT_DIR}", f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN", *_torch_flags()[1]], calls_path(),
+              calls_stamp, calls_fp, "link of the binding failed")
     return lib_path()
 
 
