@@ -1,7 +1,9 @@
 // attn_join.cu -- the parts of units that were split between CTAs become output rows.
 //
 // Part p of a row holds O_p = sum_j exp2(s_j - m_p) v_j, m_p and l_p = sum_j exp2(s_j - m_p) over
-// its keys; the row is (sum_p e^{m_p - m} O_p) / (sum_p e^{m_p - m} l_p), m = max_p m_p (base 2).
+// its keys; the row is (sum_p e^{m_p - m} O_p) / (sum_p e^{m_p - m} l_p), m = max_p m_p (base 2). (The
+// factors of l_p are taken in two halves: with an 8-bit cache, whose value scales are in m_p and l_p, they
+// may be smaller than a float and l_p as much larger.)
 //
 // A split unit is joined once, by the blocks of the first boundary between pieces that lies in
 // it. Each row takes a team of 1, 2, 4 or 8 warps, as many as leave all of a unit's rows with the
@@ -25,7 +27,16 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *to, float x, float y) {
 }
 __device__ __forceinline__ void store2(float *to, float x, float y) { *reinterpret_cast<float2 *>(to) = make_float2(x, y); }
 
-template <typename TOut, int D>
+// exp2(x) in two halves, for a factor of l; CODES: 8-bit caches of bf16 inputs
+template <bool CODES>
+struct Factor {
+    float h;
+    __device__ __forceinline__ explicit Factor(float x) : h(exp2f(CODES ? 0.5f * x : x)) {}
+    __device__ __forceinline__ float of(float l) const { return CODES ? l * h * h : l * h; }
+    __device__ __forceinline__ float whole() const { return CODES ? h * h : h; }
+};
+
+template <typename TOut, int D, bool CODES>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork w, TOut *out, int Hq) {
     constexpr int E = D / 32, NW = kJoinThreads / 32;
     __shared__ float acc[NW][D];
@@ -67,9 +78,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
             for (int u = 0; u < 4; ++u) {
                 if (pm[u].x == -INFINITY && pm[u].y == 0.f) continue;  // no key of this part is seen by the row
                 const float mn = fmaxf(m, pm[u].x);
-                const float a = exp2f(m - mn), b = exp2f(pm[u].x - mn);
+                const Factor<CODES> fa(m - mn), fb(pm[u].x - mn);
+                const float a = fa.whole(), b = fb.whole();
                 m = mn;
-                l = l * a + pm[u].y * b;
+                l = fa.of(l) + fb.of(pm[u].y);
 #pragma unroll
                 for (int e = 0; e < E; ++e) o[e] = o[e] * a + x[u][e] * b;
             }
@@ -93,8 +105,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
         if (M == -INFINITY) M = 0.f;
 #pragma unroll
         for (int k = 0; k < NW; ++k) {
-            f[k] = k < team ? exp2f(ml[first + k].x - M) : 0.f;
-            if (k < team) L += f[k] * ml[first + k].y;
+            const Factor<CODES> fk(k < team ? ml[first + k].x - M : -INFINITY);
+            f[k] = fk.whole();
+            if (k < team) L += fk.of(ml[first + k].y);
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         if (live)
@@ -109,23 +122,24 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnWork 
     }
 }
 
-template <typename TOut, int D>
+template <typename TOut, int D, bool CODES = false>
 cudaError_t launch_t(const AttnWork &w, TOut *out, int Hq, int rows, int ctas, cudaStream_t s) {
     // (4 rows a block, one after another: one long session's 8 rows took 45 us instead of 41 us in all)
     const dim3 grid((unsigned)ctas - 1, (unsigned)(rows < 16 ? rows : 16), 1);
-    return launch_early(attn_join_kernel<TOut, D>, grid, kJoinThreads, 0, s, w, out, Hq);
+    return launch_early(attn_join_kernel<TOut, D, CODES>, grid, kJoinThreads, 0, s, w, out, Hq);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_join(const AttnArgs &a, const AttnWork &w, int ctas, cudaStream_t s) {
     if (ctas <= 1) return cudaSuccess;  // one piece: nothing is split
-    const bool f32 = a.pg.dtype == GDN_F32;
+    const bool f32 = a.pg.dtype == GDN_F32, codes = a.pg.cache_dtype != a.pg.dtype;
     const int rows = w.rows < w.TPT * w.G ? w.rows : w.TPT * w.G;
 #define GDN_JOIN_CASE(DV)                                                                      \
     case DV:                                                                                   \
-        return f32 ? launch_t<float, DV>(w, (float *)a.out, a.Hq, rows, ctas, s)                     \
-                   : launch_t<__nv_bfloat16, DV>(w, (__nv_bfloat16 *)a.out, a.Hq, rows, ctas, s);
+        return f32     ? launch_t<float, DV>(w, (float *)a.out, a.Hq, rows, ctas, s)                 \
+               : codes ? launch_t<__nv_bfloat16, DV, true>(w, (__nv_bfloat16 *)a.out, a.Hq, rows, ctas, s) \
+                       : launch_t<__nv_bfloat16, DV>(w, (__nv_bfloat16 *)a.out, a.Hq, rows, ctas, s);
     switch (a.pg.d) { GDN_JOIN_CASE(64) GDN_JOIN_CASE(128) GDN_JOIN_CASE(256) }
 #undef GDN_JOIN_CASE
     return cudaErrorInvalidValue;

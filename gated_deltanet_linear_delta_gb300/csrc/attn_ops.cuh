@@ -51,6 +51,15 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// The sum of an 8-bit cache's softmax is taken from P' = P vs as P' / vs. P' is flushed to zero below 2^-126, which
+// matters where a key's scale is that much smaller than another's: a row of zeros (its scale is 2^-100) beside values of
+// 2^30. Between these bounds it does not (a flushed term is then 2^-36 of the sum at most). A scale beyond them has NaN
+// for its reciprocal, by which the sum shows that it has to be taken again, from P without vs.
+constexpr float kPlainScaleMin = 9.3132257e-10f, kPlainScaleMax = 1.1258999e15f;  // 2^-30, 2^50
+__device__ __forceinline__ float plain_reciprocal(float vs) {
+    return vs >= kPlainScaleMin && vs <= kPlainScaleMax ? rcp(vs) : __int_as_float(0x7fffffff);
+}
+
 // 4 codes to fp16 (exact)
 template <int KIND>
 __device__ __forceinline__ void codes4_to_f16(uint32_t c, uint32_t &h0, uint32_t &h1) {
@@ -169,13 +178,22 @@ static __device__ __noinline__ void add_not_finite(const int32_t *table, int num
 }
 
 // A running softmax reference m of a row (log2 domain), given its maximum over more keys: moved when
-// that has grown by more than 2^kGrow. Returns the factor for what was summed before.
+// that has grown by more than 2^kGrow. l, the sum so far, is brought to it; f is the factor for what was summed otherwise.
+// (In two halves: with an 8-bit cache the references of rows of zeros and of large values are further apart than a float's
+// exponents reach, and l is as much larger.)
 __device__ __forceinline__ bool above_reference(float m, float top) { return top > m + kGrow; }  // (-inf: any score)
-__device__ __forceinline__ bool grow_reference(float &m, float top, float &f) {
+template <bool CODES>
+__device__ __forceinline__ bool grow_reference(float &m, float top, float &f, float &l) {
     const bool grow = above_reference(m, top);
     f = 1.f;
     if (grow) {
         f = ex2(m - top);  // m = -inf: 0
+        if constexpr (CODES) {
+            const float h = ex2(0.5f * (m - top));
+            l = l * h * h;
+        } else {
+            l *= f;
+        }
         m = top;
     }
     return grow;

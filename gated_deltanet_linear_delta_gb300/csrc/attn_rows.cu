@@ -157,14 +157,14 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     bool failed = false;
     // 16 positions of a stage whose scales are not loaded: keys and values of zero
     auto clear_scales = [&](float *sc, int at) {
-        sc[(lane < 16 ? 0 : CH) + at + (lane & 15)] = lane < 16 ? 0.f : kMinKvScale;
+        sc[(lane < 16 ? 0 : CH) + at + (lane & 15)] = lane < 16 ? 0.f : 1.f;
         fence_async_smem();
     };
     auto bad_page = [&](float *sc, int at) {  // outside of the pool (the copies read zeros)
         if (lane == 0) flag_error(pg.status);
         if (C::kCodes) clear_scales(sc, at);
     };
-    bool begun = pc.off == 0, repair = false;
+    bool begun = pc.off == 0, repair = false;  // (repair: the unit is done a second time)
     while (pc.left > 0) {
         const int t0 = pc.i * w.TPT, rows = min(w.TPT, pc.s.T - t0) * w.G, len = pc.s.len;
         const int off = pc.off, take = (int)min((long)(pc.ntiles - off), pc.left);
@@ -313,10 +313,11 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
         const int sure = len - pc.s.T + t0;                      // every row sees up to here
         const int seen = sure + min(w.TPT, pc.s.T - t0);         // no row sees this position or one after it
-        // A value between the two that is not finite makes rows that do not see it NaN (0 times it). So a unit whose
-        // output is not finite is done again without such values, which the rows that see them get at the end. (To look
-        // for them beforehand made 2 tokens of 16 sessions 5% slower.)
-        const bool check = !C::kCodes && !repair && seen - sure > 1;
+        // What is rare shows in a unit's outcome, and the unit is done again with care. (To look for it beforehand made 2
+        // tokens of 16 sessions 5% slower.) bf16: a value between the two that is not finite makes rows that do not see it
+        // NaN (0 times it); it is left out then, and the rows that see it get it at the end. Codes: scales for which
+        // P' / vs may not do (plain_reciprocal) make the sum NaN.
+        const bool check = !repair && (C::kCodes || seen - sure > 1);
         for (int ch = 0; ch < chunks && !failed; ++ch) {
             const int pos0 = start + ch * BN;
             wait_full();
@@ -387,7 +388,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         float vs = sc[CH + 8 * j];
                         if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
                         const float lv = lg2(vs);
-                        iv[u][j] = vs == vs ? rcp(vs) : 0.f;  // a NaN enters by lv, and not where it is masked
+                        iv[u][j] = plain_reciprocal(vs);  // (a NaN enters by lv, and not where it is masked)
 #pragma unroll
                         for (int y = 0; y < NT; ++y)
 #pragma unroll
@@ -411,6 +412,12 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                         for (int u = 0; u < U; ++u)
                             if (u * 16 + 8 * (i >> 1) > lim) x[u][y][i] = -INFINITY;
                     }
+                if constexpr (C::kCodes)  // (whatever lies past the end must not show in the sum)
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (pos0 + u * 16 + 8 * j + gn >= len) iv[u][j] = 0.f;
             }
             // The reference moves when a score is far above it (kGrow), so each lane looks at its own scores, and the
             // rows' maxima are brought together over the lanes only when one of them found such a score.
@@ -434,8 +441,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2)
                             top[y][i] = fmaxf(top[y][i], __shfl_xor_sync(0xffffffffu, top[y][i], d));
-                        grow_reference(m[y][i], top[y][i], f[y][i]);
-                        l[y][i] *= f[y][i];
+                        grow_reference<C::kCodes>(m[y][i], top[y][i], f[y][i], l[y][i]);
                     }
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t)
@@ -443,6 +449,26 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     for (int y = 0; y < NT; ++y)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) o[t][y][i] *= f[y][i & 1];
+            }
+            if constexpr (C::kCodes) {
+                if (rarely(repair)) {  // P's sum from the scores without the scales
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float vs = scales[uslot * 2 * CH + CH + u * 16 + gn + 8 * j];
+                            if (vs < kMinKvScale) vs = kMinKvScale;
+                            const float lv = lg2(vs);
+                            iv[u][j] = 0.f;
+#pragma unroll
+                            for (int y = 0; y < NT; ++y)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const float s_lv = x[u][y][2 * j + i];
+                                    if (s_lv != -INFINITY) l[y][i] += ex2((s_lv - lv) - m[y][i]);
+                                }
+                        }
+                }
             }
             uint32_t pt[U][NT][2];  // P^T as the B operand
 #pragma unroll
@@ -548,16 +574,30 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             for (int x = 0; x < kWarps; ++x) M = fmaxf(M, ml[x * R + r].x);
             const float ref = M == -INFINITY ? 0.f : M;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int x = 0; x < kWarps; ++x) {
-                const float2 a = ml[x * R + r];
-                if (a.x == -INFINITY && a.y == 0.f) continue;  // nothing seen
-                const float f = ex2(a.x - ref);
+            auto add_part = [&](int x, float f) {
                 const float4 z = *reinterpret_cast<const float4 *>(reinterpret_cast<float *>(sm) + (x * R + r) * C::MSTRIDE + c);
-                L = fmaf(f, a.y, L);
                 y.x = fmaf(f, z.x, y.x); y.y = fmaf(f, z.y, y.y); y.z = fmaf(f, z.z, y.z); y.w = fmaf(f, z.w, y.w);
+            };
+            if (C::kCodes && rarely(repair)) {
+#pragma unroll 1
+                for (int x = 0; x < kWarps; ++x) {
+                    const float2 a = ml[x * R + r];
+                    if (a.x == -INFINITY && a.y == 0.f) continue;
+                    const float h = ex2(0.5f * (a.x - ref));  // (in two halves: grow_reference)
+                    L = fmaf(h * a.y, h, L);
+                    add_part(x, h * h);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) {
+                    const float2 a = ml[x * R + r];
+                    if (a.x == -INFINITY && a.y == 0.f) continue;  // nothing seen
+                    const float f = ex2(a.x - ref);
+                    L = fmaf(f, a.y, L);
+                    add_part(x, f);
+                }
             }
-            bad |= !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
+            bad |= C::kCodes ? !(L == L) : !(fabsf(y.x) + fabsf(y.y) + fabsf(y.z) + fabsf(y.w) < INFINITY);
             if (whole) {
                 const int t = t0 + r / w.G;
                 if (len - pc.s.T + t < 0) continue;  // padding: written as zeros

@@ -39,7 +39,8 @@
 // power-of-two scaling per row, and the cached rows' scales enter in fp32: with a_j = ks_j scale
 // log2 e and b_j = log2 vs_j,   y_j = (q.c_j) a_j + b_j,   P'_j = exp2(y_j - m') = P_j vs_j,
 //     O += P'_j C_j,   l += P'_j / vs_j.
-// Taking vs_j into the exponent keeps P' near 1 for the keys that matter whatever the scales' range.
+// Taking vs_j into the exponent keeps P' near 1 for the keys that matter whatever the scales' range. (l
+// needs P_j itself of tiles whose scales are very small or large: plain_reciprocal.)
 //
 // Masks. A row sees positions up to its own; scores past it are replaced (not multiplied), so what
 // K holds there has no effect. Of V, where 0 * NaN would reach the sum (bf16 caches; codes are finite):
@@ -80,7 +81,8 @@ struct Cfg {
     // shared memory, from a 1 KiB aligned base
     static constexpr uint32_t SM_V = NK * SLOT, SM_RK = SM_V + NV * SLOT, SM_RV = SM_RK + NR * RAW_K;
     static constexpr uint32_t SM_COL = SM_RV + NR * RAW_V;                   // [COLS][3][BN] a, b, 1 / vs
-    static constexpr uint32_t SM_X = SM_COL + (kCodes ? COLS * 3 * BN * 4 : 0);  // [2][2][128] maxima of a tile's halves
+    static constexpr uint32_t SM_ODD = SM_COL + (kCodes ? COLS * 3 * BN * 4 : 0);  // [COLS][kGroup] bytes: scales out of bounds
+    static constexpr uint32_t SM_X = SM_ODD + (kCodes ? COLS * kGroup : 0);  // [2][2][128] maxima of a tile's halves
     static constexpr uint32_t SM_STAT = SM_X + 2 * 2 * 128 * 4;              // [2][2][128] a unit's m, l by half
     static constexpr uint32_t SM_RS = SM_STAT + 2 * 2 * 128 * 8;             // [4][128] Q's row scales (8-bit caches)
     static constexpr uint32_t SM_Q = (SM_RS + (kCodes ? 4 * 128 * 4 : 0) + 1023) & ~1023u;  // [128 rows][128 B] of Q
@@ -448,7 +450,7 @@ __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, uint
     const uint32_t dst0 = swz(row0, 2 * c), dst1 = swz(row0, 2 * c + 1);
     Ring<N> ring;
     Ring<C::NR> raw;
-    bool ok = true;
+    bool ok = true, large = false;
     for (uint32_t t = 0; t < tiles; ++t) {  // all the piece's, whatever units they belong to
         bool got = wait_for(bar + (IS_V ? C::B_RV : C::B_RK) + raw.slot, raw.phase, p.budget);
         if (t >= N) got = got && product_done<D, KIND>(bar, IS_V ? C::B_PV : C::B_S, t - N, p.budget);
@@ -458,17 +460,23 @@ __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, uint
         const int2 info = reinterpret_cast<const int2 *>(sm + C::SM_INFO)[(IS_V ? C::NR : 0) + raw.slot];
         if constexpr (!IS_V) {
             const uint32_t cb = t % C::COLS;
+            bool odd = false;
             if (tid < BN) {
                 const float *sc = reinterpret_cast<const float *>(from + BN * D);
                 const bool live = tid < info.x && ((info.y >> (tid >> box_shift)) & 1);
                 const float ks = live ? sc[tid] : 0.f;
-                float vs = live ? sc[BN + tid] : kMinKvScale;
+                float vs = live ? sc[BN + tid] : 1.f;
                 if (vs < kMinKvScale) vs = kMinKvScale;  // (a NaN stays)
                 float *col = reinterpret_cast<float *>(sm + C::SM_COL) + cb * 3 * BN;
                 col[tid] = ks * p.scale2;
                 col[BN + tid] = lg2(vs);
                 col[2 * BN + tid] = vs == vs ? rcp(vs) : 0.f;  // a NaN enters by b, and not where it is masked
+                // (a large scale counts for the tiles after it too, whose references it may have moved)
+                large |= vs > kPlainScaleMax;
+                odd = large || vs < kPlainScaleMin;
             }
+            odd = __any_sync(0xffffffffu, odd);
+            if (lane == 0) sm[C::SM_ODD + cb * kGroup + (tid >> 5)] = odd;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar + C::B_COL + cb);
         }
@@ -489,6 +497,19 @@ __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, uint
 }
 
 // ---- softmax ----------------------------------------------------------------------------
+// The sum of P over a row's half tile from its products in TMEM, without the value scales. (last: the last column that
+// the row sees)
+template <int HC>
+__device__ __forceinline__ float exact_sum(uint32_t ts, const float *key_scale, float rs, float ref, int last) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < HC; ++c) {  // (few registers: this stands where the kernel has none to spare)
+        const float s = __uint_as_float(tmem_ld1(ts + c)) * rs;
+        if (c <= last) sum += ex2(s * key_scale[c] - ref);
+    }
+    return sum;
+}
+
 template <int D, int KIND>
 __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, uint32_t tmem) {
     using C = Cfg<D, KIND>;
@@ -526,6 +547,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
             const bool masked = pos0 + HC - 1 > sure;
             const float *col = reinterpret_cast<const float *>(sm + C::SM_COL) + (t % C::COLS) * 3 * BN + half * HC;
             const float rs = C::kCodes ? rsq[(unit & 3) * 128] : 1.f;
+            const bool odd = C::kCodes && *reinterpret_cast<const uint32_t *>(sm + C::SM_ODD + (t % C::COLS) * kGroup) != 0;
             float x[HC];  // the scores, in the log2 domain for 8-bit caches, masked
             {
                 uint32_t r[HC];
@@ -561,8 +583,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
             ok = !bar_any(bar_id, 64, late);
             if (!ok) break;
             float f;
-            const bool grow = grow_reference(m, fmaxf(xb[0], xb[128]) * sc, f);
-            l *= f;
+            const bool grow = grow_reference<C::kCodes>(m, fmaxf(xb[0], xb[128]) * sc, f, l);
             if (jj > 0 && __any_sync(0xffffffffu, grow)) {  // O holds the unit's tiles up to the one before
                 late = !product_done<D, KIND>(bar, C::B_PV, t - 1, p.budget);
                 tc_fence_after();
@@ -577,6 +598,9 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
                 }
             }
             const float ref = m == -INFINITY ? 0.f : m;
+            if constexpr (C::kCodes) {
+                if (rarely(odd)) l += exact_sum<HC>(ts, col, rs, ref, limit - pos0);
+            }
             F2 l2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
             const F2 sc2 = f2(sc, sc), ref2 = f2(-ref, -ref);
             uint32_t pk[HC / 2];
@@ -597,13 +621,12 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
                     pk[e / 2] = bf2(e0, e1);
                 }
             }
+            float a, d;
+            f2_get(f2_add(l2[0], l2[1]), a, d);
+            a += d;
+            l += C::kCodes && odd ? 0.f : a;
 #pragma unroll
             for (int e = 0; e < HC / 2; e += 16) tmem_st16(ts + e, pk + e);  // over the half's own scores
-            {
-                float a, d;
-                f2_get(f2_add(l2[0], l2[1]), a, d);
-                l += a + d;
-            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();

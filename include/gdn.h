@@ -385,7 +385,8 @@ GDN_API int gdn_kv_read(const void *k_cache, const void *v_cache, const float *k
  * Scores and softmax statistics are fp32. A row whose scores are all -infinity gives zeros. What
  * lies in the cache past a token's position has no effect on it, whatever its value: an infinity or
  * a NaN in a later token's rows, or anything at or past kv_lens[n]. (An 8-bit cache holds what
- * gdn_kv_write stores, whose codes are finite.) The result does not
+ * gdn_kv_write stores, whose codes are finite; value rows may have any scales, from rows of zeros up
+ * to values of 2^106.) The result does not
  * depend on the order in which the GPU runs its parts.
  * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
  */
