@@ -24,11 +24,11 @@
 // operand by movmatrix, 8 x 8 at a time.
 // 8-bit codes become fp16 in registers (attn_tc.cu says why fp16, and how the scales enter).
 //
-// Measured: 128 sessions of 4096, 2 key heads with 8 query heads each, D = 256: bf16 175 us (6.1 TB/s of
-// 6.7 measured), e4m3 100 us (5.4); 32 of 8192, 8 key heads with 4, D = 128: bf16 170, int8 95, e4m3 95
+// Measured: 128 sessions of 4096, 2 key heads with 8 query heads each, D = 256: bf16 170 us (6.3 TB/s of
+// 6.7 measured), e4m3 96 us (5.7); 32 of 8192, 8 key heads with 4, D = 128: bf16 168, int8 96, e4m3 94
 // us (5.8 TB/s for codes), where the codes' conversion takes 0.55 instructions a cycle and scheduler; one
-// session of 131072, e4m3, D = 256: 35 us, of which memory 20; one of 1000: 11.5 us, a chain of the plan,
-// the table, the first tiles, the warps' meeting and the joining kernel.
+// session of 131072, e4m3, D = 256: 35 us, of which memory 20; one of 1000: 10.6 us from a graph, a chain
+// of the plan, the table, the first tiles, the warps' meeting and the joining kernel.
 #include <climits>
 
 #include "attn_ops.cuh"
@@ -689,14 +689,16 @@ bool rows_fit(const AttnArgs &a, int rows) {
 
 }  // namespace
 
-// Few rows: at most 16 with an 8-bit cache, at most 8 with a bf16 one. Measured against attn_tc.cu with 16 rows: 128
-// sequences of 4096, d = 256, e4m3 121 and 146 us; 32 of 8192, 8 key heads, d = 128, int8 127 and 204 us; but bf16 191
-// and 186, 185 and 178 us. (With 32 rows, here two passes over the cache: e4m3 210 and 149 us, int8 221 and 222, bf16
-// 348 and 190.)
+// Few rows: at most 16 with an 8-bit cache, at most 8 with a bf16 one. Measured here and in attn_tc.cu: 128 sequences of
+// 4096, 2 key heads, d = 256, e4m3: 95 and 133 us with 8 rows, 113 and 136 with 16, 205 and 139 with 32 (here two passes
+// over the cache); 32 of 8192, 8 key heads, d = 128, int8: 118 and 190 us with 16, 216 and 201 with 32. A bf16 cache, 8
+// rows: 172 and 172, 170 and 167 us, one session of 1000 10.6 and 11.2 (from a graph); 16 rows (two passes): 323 and 175,
+// 324 and 169.
 bool attn_rows_supported(const AttnArgs &a) { return rows_fit(a, a.pg.cache_dtype == GDN_BF16 ? 8 : 16); }
 
 // Tiles of 8 rows where they do: half of the products, exponentials and accumulators (32 sequences of 8192, 8 key heads
-// with 4 query heads each, d = 128, int8: 97 us, 112 us in tiles of 16; 128 of 4096, d = 256, e4m3: 100 and 108 us).
+// with 4 query heads each, d = 128, int8: 97 us, 112 us in tiles of 16; 128 of 4096, d = 256, e4m3: 100 and 108 us, both
+// before later steps that made the tiles of 8 1 to 4 us faster).
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t s) {
     const bool r8 = rows_fit(a, 8);
     switch (a.pg.cache_dtype) {

@@ -15,10 +15,12 @@
 // memory: per tile of 128 positions at D = 128 the codes are read (256 cycles), written as fp16 (512),
 // read by the products (480) and scaled by columns (770), 85% of its cycles.
 //
-// Measured, 2048 tokens over 32768, 16 query heads on 2: bf16 683, 357 and 323 us for D = 256, 128 and
-// 64 (1.56 PFLOP/s for 256, of 1.92 measured), e4m3 860 us for 256 and 656 for 128 (int8 678). 8 prompts
-// of 1024 tokens, 32 heads on 8, D = 128: bf16 98, e4m3 201 us: 14 units of 4 or 5 tiles per CTA, whose
-// starts and ends (Q in, rows out) count for half of it.
+// Measured, 2048 tokens over 32768, 16 query heads on 2: bf16 651, 355 and 328 us for D = 256, 128 and
+// 64 (1.64 PFLOP/s for 256, of 1.92 measured; 712 us and 1.50 PFLOP/s in a run so long that power caps the
+// clock), e4m3 875 us for 256 and 637 for 128 (int8 668). 8 prompts of 1024 tokens, 32 heads on 8, D = 128:
+// bf16 101, e4m3 203 us: 14 units of 4 or 5 tiles per CTA, whose starts and ends (Q in, rows out) count for
+// half of it. The kernels of 8-bit caches spill 74 to 118 bytes of stores a thread: 768 threads leave 80
+// registers, and the softmax, which has 112 when it runs, is compiled within them.
 //
 // Layout. TMEM holds O (D columns), two S buffers (P_j overlays S_j) and Q as the 16-bit A operand,
 // 512 columns in all for D = 256 (and for D = 128 with the next unit's Q beside it); with Q in TMEM,

@@ -6,7 +6,7 @@
 //
 // Work split: a CTA takes a run of tokens. Where each lies (its sequence, kv_lens, the page) is found
 // first, by a warp per token, into shared memory; then the CTA's lanes stream over the run's rows
-// (each token's Hkv keys, then its Hkv values), 4 rows' pieces in flight per lane before any is used.
+// (each token's Hkv keys, then its Hkv values), 2 or 4 rows' pieces in flight per lane before any is used.
 // Runs get longer with the number of tokens: many small runs give a decode step's few tokens a CTA
 // each, long ones spread the look-up over more bytes (with a token per warp, whose three dependent
 // reads stood before every 1 KiB, a long session was read at 3.4 TB/s; with runs at 6.0).
@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kKvThreads, 4) kv_copy_kernel(const KvArgs a, 
     // consecutive, so that both sides' accesses are whole lines.
     constexpr int E = 16, PE = 16 / (int)sizeof(T), NP = E / PE, LPR = D / E, ROWS = kKvThreads / LPR;
     // rows in flight per lane, as many as fit its registers (fp32 copies of 16384 tokens, 8 heads, d = 128: 43 us with 2,
-    // 50 with 4; bf16 rows stored as codes: with 4, int8 d = 128 28 us instead of 29, but e4m3 d = 256 83 instead of 78)
+    // 50 with 4; bf16 rows stored as codes: with 4, the same tokens as int8 28 us instead of 29, but 131072 tokens of 2
+    // heads, d = 256, as e4m3 83 instead of 78)
     constexpr int kFlight = (kCodes ? WRITE : sizeof(T) == 4) ? 2 : 4;
     __shared__ long where[kMaxRun];
     const KvPages &p = a.pg;

@@ -375,19 +375,23 @@ GDN_API int gdn_kv_read(const void *k_cache, const void *v_cache, const float *k
  * have to be in the cache, see gdn_kv_write):
  *     out = sum_j w_j v_j,   w = softmax_j(scale * q . k_j)
  * T = 1 is the decode step, T of a few the check of speculated tokens, a large T a fragment of a
- * prompt over what is cached of it: a prompt cut into fragments gives the same result.
+ * prompt over what is cached of it: a prompt cut into fragments gives the same result, up to the
+ * order of its sums.
  *   q   : [Ttot][Hq][d], token stride q_stride.   out : [Ttot][Hq][d], contiguous.
  *   scale : the softmax scale, for instance d^-1/2; finite.
  *   workspace : DEVICE memory, 256-byte aligned, of at least
  *         gdn_paged_attn_workspace_size(B, T, cu_seqlens != NULL, Hq, Hkv, d) bytes: scratch until
  *         the call's work on `stream` has finished, whatever was in it before. Calls whose work may
  *         overlap on the GPU must use different workspaces.
- * Scores and softmax statistics are fp32. A row whose scores are all -infinity gives zeros. What
- * lies in the cache past a token's position has no effect on it, whatever its value: an infinity or
- * a NaN in a later token's rows, or anything at or past kv_lens[n]. (An 8-bit cache holds what
- * gdn_kv_write stores, whose codes are finite; value rows may have any scales, from rows of zeros up
- * to values of 2^106.) The result does not
- * depend on the order in which the GPU runs its parts.
+ * Scores, softmax statistics and sums are fp32. With fp32 inputs so is everything else. With bf16
+ * inputs the probabilities are rounded to bf16 before they meet the values; over an 8-bit cache both
+ * they (times their row's value scale) and q (times a power of two) are rounded to fp16, which is
+ * exact for q but for elements below 2^-30 of their row's largest. A row whose scores are all
+ * -infinity gives zeros. What lies in the cache past a token's position has no effect on it, whatever
+ * its value: an infinity or a NaN in a later token's rows, or anything at or past kv_lens[n]. (An
+ * 8-bit cache holds what gdn_kv_write stores, whose codes are finite; value rows may have any scales,
+ * from rows of zeros up to values of 2^106.) The result does not depend on the order in which the GPU
+ * runs its parts.
  * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
  */
 GDN_API int gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache,
