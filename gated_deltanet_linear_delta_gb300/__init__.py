@@ -50,7 +50,6 @@ _I = ctypes.c_int
 _L = ctypes.c_int64
 _calls = None
 _DTYPE = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 # the current stream of a device as a raw cudaStream_t (falls back to the Stream object)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -131,14 +130,22 @@ def _ptr(t: torch.Tensor | None):
     return t.data_ptr()
 
 
+def _current_device() -> int:
+    """The current CUDA device. The first call replaces this function by the quickest one that tells (of one device: 0)."""
+    global _current_device
+    _current_device = int if torch.cuda.device_count() == 1 else getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
+
+
 def _stream(stream, t: torch.Tensor | None = None):
     """cudaStream_t of `stream`, or of the current stream. The library launches on the current device, so a call
     whose tensor t lies on another one is refused here (its kernels would run where the tensors are not)."""
-    if t is not None and t.get_device() != _current_device():
+    device = _current_device()
+    if t is not None and t.get_device() != device:
         raise ValueError("tensors must be on the current CUDA device (torch.cuda.set_device)")
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(t.get_device() if t is not None else torch.cuda.current_device())
+            return _raw_stream(device)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
