@@ -19,7 +19,7 @@
 // 64 (1.64 PFLOP/s for 256, of 1.92 measured; 712 us and 1.50 PFLOP/s in a run so long that power caps the
 // clock), e4m3 875 us for 256 and 637 for 128 (int8 668). 8 prompts of 1024 tokens, 32 heads on 8, D = 128:
 // bf16 101, e4m3 203 us: 14 units of 4 or 5 tiles per CTA, whose starts and ends (Q in, rows out) count for
-// half of it. The kernels of 8-bit caches spill 74 to 118 bytes of stores a thread: 768 threads leave 80
+// half of it. The kernels of 8-bit caches spill 76 to 118 bytes of stores a thread: 768 threads leave 80
 // registers, and the softmax, which has 112 when it runs, is compiled within them.
 //
 // Layout. TMEM holds O (D columns), two S buffers (P_j overlays S_j) and Q as the 16-bit A operand,
@@ -31,10 +31,9 @@
 // meet once per tile for the row's maximum; one brings the rows' Q into TMEM and takes finished rows
 // out, beside the softmax of the neighbouring units; one has a warp each for the loads of K and V, for
 // the products and, with a bf16 cache, for a look through V; with an 8-bit cache one converts K tiles
-// and one V tiles. The products run S_0, S_1,
-// O(0), S_2, O(1), .. across units, so that the tensor cores work on S_{j+1} while the softmax of tile j
-// runs. All CTAs are persistent over their piece of the work, and every wait has a limit, after which
-// the CTA flags the status word and leaves.
+// and one V tiles. The products run S_0, S_1, O(0), S_2, O(1), .. across units, so that the tensor cores
+// work on S_{j+1} while the softmax of tile j runs. All CTAs are persistent over their piece of the work,
+// and every wait has a limit, after which the CTA flags the status word and leaves.
 //
 // 8-bit caches. Codes are exact in fp16, so K and V tiles hold codes converted to fp16 (bf16 would
 // take four times the conversion instructions for e4m3), Q is rounded to fp16 after an exact
