@@ -17,7 +17,8 @@ sequences runs in a few microseconds on the GPU: the library handle and its
 function objects are looked up once, pointers go to ctypes as plain integers,
 and the current stream is read as a raw handle. Size and alignment checks are
 the C library's (it returns an error before queueing anything). The paged cache
-calls, which have the most tensors, are marshalled in C++ (csrc/binding.cpp).
+calls and the calls on trees, which have the most tensors, are marshalled in C++
+(csrc/binding.cpp).
 """
 from __future__ import annotations
 
@@ -35,6 +36,7 @@ __all__ = ["GDNError", "gdn_prefill", "gdn_prefill_ws", "gdn_prefill_workspace_s
            "gdn_prefill_from_host",
            "gdn_decode_step", "gdn_decode_step_slots", "gdn_prepass", "gdn_prefill_path",
            "gdn_kv_write", "gdn_kv_read", "gdn_paged_attn", "gdn_paged_attn_workspace_size",
+           "gdn_tree_attn", "gdn_tree_scan", "gdn_tree_verify", "gdn_tree_advance", "gdn_kv_keep",
            "gdn_get_device_status", "gdn_status_string", "library", "library_path",
            "GDN_OK", "GDN_ERR_INVALID_ARG", "GDN_ERR_UNSUPPORTED", "GDN_ERR_CUDA",
            "GDN_ERR_DEVICE_CHECK", "GDN_BF16", "GDN_F32", "GDN_FP8", "GDN_INT8"]
@@ -103,6 +105,17 @@ def library() -> ctypes.CDLL:
             lib.gdn_paged_attn.restype = _I
             lib.gdn_paged_attn_workspace_size.argtypes = [_I] * 6
             lib.gdn_paged_attn_workspace_size.restype = ctypes.c_size_t
+            lib.gdn_tree_attn.argtypes = [_P] * 10 + [_I] * 8 + [_L, ctypes.c_float] + [_I] * 2 + \
+                [_P, ctypes.c_size_t, _P]
+            lib.gdn_tree_attn.restype = _I
+            lib.gdn_kv_keep.argtypes = [_P] * 9 + [_I] * 9 + [_P]
+            lib.gdn_kv_keep.restype = _I
+            lib.gdn_tree_scan.argtypes = [_P] * 10 + [_I] * 8 + [_P]
+            lib.gdn_tree_scan.restype = _I
+            lib.gdn_tree_advance.argtypes = [_P] * 10 + [_I] * 9 + [_P]
+            lib.gdn_tree_advance.restype = _I
+            lib.gdn_tree_verify.argtypes = [_P] * 10 + [_I] * 3 + [_L] * 2 + [_I, _P]
+            lib.gdn_tree_verify.restype = _I
             lib.gdn_get_device_status.argtypes = [_P]
             lib.gdn_get_device_status.restype = _I
             lib.gdn_status_string.argtypes = [_I]
@@ -302,7 +315,7 @@ def gdn_prepass(q, k, g, b, rq, rk, beta, gcum, cu_seqlens=None, B=None, T=None,
 
 
 def _load_calls():
-    """The CPython module with the paged cache calls (it checks their tensors; built beside the library)."""
+    """The CPython module with the paged cache calls and those on trees (it checks their tensors; built beside the library)."""
     global _calls
     library()  # the module is linked against it
     with _lock:
@@ -348,17 +361,79 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, kv_lens, out, k_scale=None,
     `scale` is d**-0.5 unless given. `workspace`: a uint8 CUDA tensor of gdn_paged_attn_workspace_size(...)
     bytes that a program keeps; without one the call takes it from torch's allocator."""
     on = _stream(stream, q) if q.is_cuda else 0
-    if workspace is None and q.is_cuda:
-        packed = cu_seqlens is not None
-        n = kv_lens.numel() if B is None else B
-        need = gdn_paged_attn_workspace_size(n, q.shape[0] if packed else (q.shape[0] // n if n else 0), q.shape[1],
-                                             k_cache.shape[1], k_cache.shape[-1], packed)
-        with torch.cuda.stream(_torch_stream(stream, q)):
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if workspace is None:
+        workspace = _attn_workspace(q, k_cache, kv_lens, cu_seqlens, B, stream)
     rc = (_calls or _load_calls()).paged_attn(q, out, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens,
                                               B, T, scale, workspace, on)
     if rc:
         raise GDNError(rc, "gdn_paged_attn")
+
+
+def _attn_workspace(q, k_cache, kv_lens, cu_seqlens, B, stream):
+    """A workspace for one call, from torch's allocator (None for tensors that the call is going to refuse)."""
+    if not q.is_cuda:
+        return None
+    packed = cu_seqlens is not None
+    n = kv_lens.numel() if B is None else B
+    need = gdn_paged_attn_workspace_size(n, q.shape[0] if packed else (q.shape[0] // n if n else 0), q.shape[1],
+                                         k_cache.shape[1], k_cache.shape[-1], packed)
+    with torch.cuda.stream(_torch_stream(stream, q)):
+        return torch.empty(need, dtype=torch.uint8, device=q.device)
+
+
+def gdn_tree_attn(q, k_cache, v_cache, block_table, kv_lens, parents, out, k_scale=None, v_scale=None, cu_seqlens=None,
+                  B=None, T=None, scale=None, workspace=None, stream=None) -> None:
+    """gdn_paged_attn of trees of at most 64 nodes a sequence: parents int32 [Ttot] names each node's parent by its
+    index within its sequence (-1: a root; below: padding). A node sees the context (the positions before the
+    sequence's last T_n) and the nodes on its path from the root."""
+    on = _stream(stream, q) if q.is_cuda else 0
+    if workspace is None:
+        workspace = _attn_workspace(q, k_cache, kv_lens, cu_seqlens, B, stream)
+    rc = (_calls or _load_calls()).tree_attn(q, out, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens,
+                                             B, T, scale, workspace, on, parents)
+    if rc:
+        raise GDNError(rc, "gdn_tree_attn")
+
+
+def gdn_kv_keep(k_cache, v_cache, block_table, kv_lens, path, counts, k_scale=None, v_scale=None, cu_seqlens=None,
+                T=None, stream=None) -> None:
+    """The accepted paths' cache rows (path int32 [B, P], counts int32 [B]: as gdn_tree_verify leaves them) move right
+    after their contexts. The step's nodes follow cu_seqlens, or T gives those of each sequence."""
+    rc = (_calls or _load_calls()).kv_keep(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, None, T,
+                                           path, counts, _stream(stream, k_cache) if k_cache.is_cuda else 0)
+    if rc:
+        raise GDNError(rc, "gdn_kv_keep")
+
+
+def gdn_tree_scan(q, k, v, g, b, state, parents, out, slots=None, cu_seqlens=None, B=None, T=None, stream=None) -> None:
+    """The gated delta rule over trees of at most 64 nodes a sequence (parents as for gdn_tree_attn): out of each node
+    is what the recurrence over its path gives, from the sequence's state, which is left as it is."""
+    rc = (_calls or _load_calls()).tree_scan(q, k, v, g, b, state, slots, parents, cu_seqlens, out, B, T,
+                                             _stream(stream, k) if k.is_cuda else 0)
+    if rc:
+        raise GDNError(rc, "gdn_tree_scan")
+
+
+def gdn_tree_advance(k, v, g, b, state_in, state_out, path, counts, slots=None, cu_seqlens=None, B=None, T=None,
+                     stream=None) -> None:
+    """The states after the recurrence over the accepted paths (path int32 [B, P], counts int32 [B]); state_out may be
+    state_in. With slots both are pools, of which sequence n's entry is slots[n]."""
+    rc = (_calls or _load_calls()).tree_advance(k, v, g, b, state_in, state_out, slots, path, counts, cu_seqlens, B, T,
+                                                _stream(stream, k) if k.is_cuda else 0)
+    if rc:
+        raise GDNError(rc, "gdn_tree_advance")
+
+
+def gdn_tree_verify(target_probs, draft_probs, tokens, parents, r, r_last, path, counts, next, cu_seqlens=None, B=None,
+                    T=None, stream=None) -> None:
+    """Which drafted tokens stand: walks each sequence's tree from node 0 by the target's and the draft's probabilities
+    [Ttot, V] fp32 (draft_probs None: each child was proposed for certain) and the random numbers r [Ttot], r_last [B].
+    Writes the accepted nodes, node 0 first, to path int32 [B, P] (-1 after them), their number to counts int32 [B]
+    and the token after them to next int32 [B]."""
+    rc = (_calls or _load_calls()).tree_verify(target_probs, draft_probs, tokens, parents, r, r_last, cu_seqlens, path, counts,
+                                               next, B, T, _stream(stream, target_probs) if target_probs.is_cuda else 0)
+    if rc:
+        raise GDNError(rc, "gdn_tree_verify")
 
 
 def gdn_prefill_path(B, T, Hk, Hv, dk, dv, chunk, dtype) -> int:

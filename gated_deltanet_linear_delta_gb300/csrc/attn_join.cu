@@ -172,6 +172,7 @@ int attn_ctas(const AttnArgs &a, const AttnWork &w, int BN) {
 AttnWork attn_work(const AttnArgs &a, int tokens_per_tile, int min_shift) {
     AttnWork w{};
     w.pg = a.pg;
+    w.parents = a.parents;
     w.G = a.Hq / a.pg.Hkv;
     w.TPT = tokens_per_tile;
     w.rows = attn_unit_rows(a.pg.cu ? a.pg.Ttot : a.pg.T, w.G);

@@ -10,6 +10,7 @@
 #include "attn_plan.cuh"
 #include "attn_work.h"
 #include "tc_ops.cuh"
+#include "tree.cuh"
 
 namespace gdn {
 
@@ -161,12 +162,13 @@ static __device__ __noinline__ void drop_not_finite(uint4 *at) {
     tc::fence_async_smem();  // products and later copies see it
 }
 // Adds those of one key head's cached values, positions first .. last, columns c .. c + n - 1, to an output row.
-// table: the sequence's pages; shift: log2 of their size.
-template <typename T>
+// table: the sequence's pages; shift: log2 of their size. TREE: from `base` on, only positions of nodes on the row's path.
+template <typename T, bool TREE = false>
 static __device__ __noinline__ void add_not_finite(const int32_t *table, int num_pages, int Hkv, int h, int shift,
                                                    const __nv_bfloat16 *v_cache, int d, int first, int last, int c, int n,
-                                                   T *row) {
+                                                   T *row, int base = 0, uint64_t path = 0) {
     for (int pos = first; pos <= last; ++pos) {
+        if (TREE && !on_path(path, pos - base)) continue;
         const int page = table[pos >> shift];
         if ((unsigned)page >= (unsigned)num_pages) continue;  // (values of zero)
         const __nv_bfloat16 *v = v_cache + ((((long)page * Hkv + h) << shift) + (pos & ((1 << shift) - 1))) * d;

@@ -47,6 +47,7 @@ struct __align__(16) AttnRec {  // where CTA c's piece starts; read by the joini
 
 struct AttnWork {
     KvPages pg;
+    const int32_t *parents;  // new tokens that form trees: their parents; else null
     int G;         // query heads per key head
     int TPT;       // tokens per row tile
     int rows;      // workspace rows per part
@@ -116,7 +117,7 @@ struct PlanSmem {
 // 1024). The result is in sm->piece (left = 0: no work), and its record in the workspace. It stands
 // before all other work of the call, so it is kept short: one pass over the sequences (a second
 // where there are more than NT), two or three barriers, 32-bit divisions.
-template <int BN, int NT>
+template <int BN, int NT, bool TREE = false>
 __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     constexpr int NW = NT / 32;
@@ -127,7 +128,7 @@ __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
     bool pad = false;
     for (int base = 0; base < p.B; base += NT) {
         SeqInfo s{0, 0, 0};
-        if (base + tid < p.B) seq_info(p, base + tid, &s);
+        if (base + tid < p.B) seq_info<TREE>(p, base + tid, &s);
         pad |= s.T > s.len;
         per_head = seq_tiles<BN>(w, s);
         mine += per_head * p.Hkv;
@@ -191,7 +192,7 @@ __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
         __syncthreads();
         for (int base = 0; base < p.B && begin < end; base += NT) {
             s0 = SeqInfo{0, 0, 0};
-            if (base + tid < p.B) seq_info(p, base + tid, &s0);
+            if (base + tid < p.B) seq_info<TREE>(p, base + tid, &s0);
             per_head = seq_tiles<BN>(w, s0);
             const long y = per_head * p.Hkv;
             inc = scan(y);
@@ -257,7 +258,7 @@ __device__ void plan_piece(const AttnWork &w, PlanSmem *sm) {
 // The unit after the piece's current one that has any key tiles (left > 0 says there is one). All warps
 // of a CTA take this step, between two units' work, so it divides only where the sequence changes (a
 // division per step made it 1500 cycles).
-template <int BN>
+template <int BN, bool TREE = false>
 __device__ __forceinline__ void next_unit(const AttnWork &w, Piece *pc) {
     pc->off = 0;
     do {
@@ -269,7 +270,7 @@ __device__ __forceinline__ void next_unit(const AttnWork &w, Piece *pc) {
                     pc->left = 0;
                     return;
                 }
-                seq_info(w.pg, pc->n, &pc->s);  // no tokens where cu is inconsistent
+                seq_info<TREE>(w.pg, pc->n, &pc->s);  // no tokens where cu is inconsistent
                 pc->nq = row_tiles(w, pc->s);
             }
         }
@@ -279,11 +280,11 @@ __device__ __forceinline__ void next_unit(const AttnWork &w, Piece *pc) {
 
 // Rows of padding tokens are zeros; no unit of work covers them. (`threads` threads of each CTA call
 // it, if the plan has found any.)
-template <typename TOut>
+template <bool TREE = false, typename TOut>
 __device__ void zero_padding(const AttnWork &w, TOut *out, int Hq, int d, int thread, int threads) {
     for (int n = blockIdx.x; n < w.pg.B; n += gridDim.x) {
         SeqInfo s;
-        if (!seq_info(w.pg, n, &s)) continue;
+        if (!seq_info<TREE>(w.pg, n, &s)) continue;
         const long idle = (long)min(s.T, max(0, s.T - s.len)) * Hq * d;
         uint4 *p = reinterpret_cast<uint4 *>(out + s.bos * Hq * d);
         const long pieces = idle * (long)sizeof(TOut) / 16;

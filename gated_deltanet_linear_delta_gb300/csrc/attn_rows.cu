@@ -119,7 +119,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {  // of 16-bit ele
     return y;
 }
 
-template <int D, int KIND, int R>
+template <int D, int KIND, int R, bool TREE>
 __global__ void __launch_bounds__(RCfg<D, KIND, R>::THREADS, 1)
 attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const RowParams p) {
     using C = RCfg<D, KIND, R>;
@@ -149,7 +149,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         fence_mbar_init();
     }
     before_reading();
-    plan_piece<BN, kThreads>(w, plan);  // (synchronises the CTA)
+    plan_piece<BN, kThreads, TREE>(w, plan);  // (synchronises the CTA)
     Piece pc = plan->piece;
     const int P_shift = 31 - __clz(pg.page_size);
     uint32_t filled = 0, used_up = 0;  // ring slots of this warp
@@ -253,6 +253,8 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             if (fills > 0) issue();
         };
         while (fills > 0 && filled - used_up < (uint32_t)C::NSL) issue();
+        Paths paths;
+        if constexpr (TREE) paths = tree_paths(w.parents + pc.s.bos, pc.s.T, pg.status);
 
         // Q fragments, by the whole CTA: a row's 16 bytes to the lanes that hold its elements
         for (int e = tid; e < R * (D / 8); e += kThreads) {
@@ -301,6 +303,7 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 for (int i = 0; i < 4; ++i) o[t][y][i] = 0.f;
         float m[NT][2], l[NT][2], rsc[NT][2];
         int limit[NT][2];  // last position that the thread's rows see
+        uint64_t path[NT][2];  // TREE: the rows' paths
 #pragma unroll
         for (int y = 0; y < NT; ++y)
 #pragma unroll
@@ -310,9 +313,11 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                 l[y][i] = 0.f;
                 limit[y][i] = r < rows ? len - pc.s.T + t0 + r / w.G : INT_MAX;  // (rows past the last are not read)
                 rsc[y][i] = C::kCodes ? rs[r] * p.scale2 : p.scale2;
+                if constexpr (TREE) path[y][i] = paths.at(min(t0 + r / w.G, pc.s.T - 1));
             }
-        const int sure = len - pc.s.T + t0;                      // every row sees up to here
-        const int seen = sure + min(w.TPT, pc.s.T - t0);         // no row sees this position or one after it
+        const int base = len - pc.s.T;                             // position of the first new token
+        const int sure = TREE ? base - 1 : base + t0;              // every row sees up to here
+        const int seen = base + t0 + min(w.TPT, pc.s.T - t0);      // no row sees this position or one after it
         // What is rare shows in a unit's outcome, and the unit is done again with care. (To look for it beforehand made 2
         // tokens of 16 sessions 5% slower.) bf16: a value between the two that is not finite makes rows that do not see it
         // NaN (0 times it); it is left out then, and the rows that see it get it at the end. Codes: scales for which
@@ -409,8 +414,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                     for (int i = 0; i < 4; ++i) {
                         const int lim = limit[y][i & 1] - pos0 - gn;
 #pragma unroll
-                        for (int u = 0; u < U; ++u)
-                            if (u * 16 + 8 * (i >> 1) > lim) x[u][y][i] = -INFINITY;
+                        for (int u = 0; u < U; ++u) {
+                            const int at = u * 16 + 8 * (i >> 1);
+                            if (TREE ? !on_path(path[y][i & 1], pos0 + gn + at - base) : at > lim) x[u][y][i] = -INFINITY;
+                        }
                     }
                 if constexpr (C::kCodes)  // (whatever lies past the end must not show in the sum)
 #pragma unroll
@@ -615,19 +622,20 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             for (int e = tid; e < rows * (D / 4); e += kThreads) {
                 const int r = e / (D / 4), c = (e % (D / 4)) * 4, t = t0 + r / w.G;
                 const int first = max(max(sure + 1, off * BN), 0), last = min(len - pc.s.T + t, (off + take) * BN - 1);
+                const uint64_t on = TREE ? path_of(w.parents + pc.s.bos, t) : 0;
                 if (whole)
-                    add_not_finite(table, pg.num_pages, pg.Hkv, pc.h, P_shift, p.v_cache, D, first, last, c, 4,
-                                   p.out + ((pc.s.bos + t) * p.Hq + pc.h * w.G + r % w.G) * D);
+                    add_not_finite<__nv_bfloat16, TREE>(table, pg.num_pages, pg.Hkv, pc.h, P_shift, p.v_cache, D, first, last, c, 4,
+                                                        p.out + ((pc.s.bos + t) * p.Hq + pc.h * w.G + r % w.G) * D, base, on);
                 else
-                    add_not_finite(table, pg.num_pages, pg.Hkv, pc.h, P_shift, p.v_cache, D, first, last, c, 4,
-                                   w.part + part_index(w, blockIdx.x, begun ? 1 : 0, r) * D);
+                    add_not_finite<float, TREE>(table, pg.num_pages, pg.Hkv, pc.h, P_shift, p.v_cache, D, first, last, c, 4,
+                                                w.part + part_index(w, blockIdx.x, begun ? 1 : 0, r) * D, base, on);
             }
         }
         fence_async_smem();  // the rings held O: before the next unit's copies
         repair = __syncthreads_or(check && bad);
         if (rarely(repair)) continue;
         pc.left -= take;
-        if (pc.left > 0) next_unit<BN>(w, &pc);
+        if (pc.left > 0) next_unit<BN, TREE>(w, &pc);
         begun = true;
     }
     if (failed && lane == 0) flag_error(pg.status);
@@ -639,10 +647,10 @@ attn_rows_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             uphase ^= 1;
         }
     }
-    if (plan->padding) zero_padding(w, p.out, p.Hq, D, tid, kThreads);
+    if (plan->padding) zero_padding<TREE>(w, p.out, p.Hq, D, tid, kThreads);
 }
 
-template <int D, int KIND, int R>
+template <int D, int KIND, int R, bool TREE>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     using C = RCfg<D, KIND, R>;
     const int G = a.Hq / a.pg.Hkv;
@@ -663,7 +671,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     const int lines = C::LINES * 16 / C::CH;  // a box holds 16 positions, which always share a page
     if (!page_map(&mk, a.k_cache, a.pg, line, lines) || !page_map(&mv, a.v_cache, a.pg, line, lines))
         return cudaErrorInvalidValue;
-    auto kernel = attn_rows_kernel<D, KIND, R>;
+    auto kernel = attn_rows_kernel<D, KIND, R, TREE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);
     if (e != cudaSuccess) return e;
     const int ctas = attn_ctas(a, p.w, C::BN);
@@ -674,9 +682,9 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
 template <int KIND, int R>
 cudaError_t launch_d(const AttnArgs &a, cudaStream_t s) {
     switch (a.pg.d) {
-        case 64: return launch_t<64, KIND, R>(a, s);
-        case 128: return launch_t<128, KIND, R>(a, s);
-        case 256: return launch_t<256, KIND, R>(a, s);
+        case 64: return a.parents ? launch_t<64, KIND, R, true>(a, s) : launch_t<64, KIND, R, false>(a, s);
+        case 128: return a.parents ? launch_t<128, KIND, R, true>(a, s) : launch_t<128, KIND, R, false>(a, s);
+        case 256: return a.parents ? launch_t<256, KIND, R, true>(a, s) : launch_t<256, KIND, R, false>(a, s);
     }
     return cudaErrorInvalidValue;
 }

@@ -12,6 +12,7 @@
 
 #include "attn_plan.cuh"
 #include "attn_work.h"
+#include "tree.cuh"
 
 namespace gdn {
 namespace {
@@ -72,7 +73,7 @@ struct SimtSmem {
     PlanSmem plan;
 };
 
-template <int KIND, int D, int R>
+template <int KIND, int D, int R, bool TREE>
 __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a) {
     constexpr int RT = R / 16, CT = D / 64;  // rows and groups of 4 columns per thread
     extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -81,8 +82,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     next_may_begin();
     before_reading();
-    plan_piece<BN, kThreads>(w, &sm.plan);
-    if (sm.plan.padding) zero_padding(w, a.out, a.Hq, D, tid, kThreads);
+    plan_piece<BN, kThreads, TREE>(w, &sm.plan);
+    if (sm.plan.padding) zero_padding<TREE>(w, a.out, a.Hq, D, tid, kThreads);
     Piece pc = sm.plan.piece;
     bool begun = pc.off == 0, careful = false;
     while (pc.left > 0) {
@@ -99,13 +100,18 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
         float m[RT], l[RT];
         float4 o[RT][CT];
         int limit[RT];  // last position the row sees
-        const int sure = pc.s.len - pc.s.T + t0;  // ... that every row of the unit sees
+        // last position that every row of the unit sees; of a tree's: the context's last
+        const int sure = pc.s.len - pc.s.T + (TREE ? -1 : t0);
+        uint64_t path[RT];  // TREE: the rows' paths
+        Paths paths;
+        if constexpr (TREE) paths = tree_paths(w.parents + pc.s.bos, pc.s.T, w.pg.status);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.f;
-            limit[r] = sure + (ty * RT + r) / w.G;
+            limit[r] = (TREE ? sure + 1 + t0 : sure) + (ty * RT + r) / w.G;
             if (ty * RT + r >= rows) limit[r] = -1;
+            if constexpr (TREE) path[r] = paths.at(min(t0 + (ty * RT + r) / w.G, pc.s.T - 1));
 #pragma unroll
             for (int c = 0; c < CT; ++c) o[r][c] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -192,7 +198,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
                 float top = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    s[r][c] = j * BN + tx + 16 * c <= limit[r] ? s[r][c] * a.scale2 : -INFINITY;
+                    if constexpr (TREE)
+                        s[r][c] = limit[r] >= 0 && on_path(path[r], j * BN + tx + 16 * c - sure - 1) ? s[r][c] * a.scale2 : -INFINITY;
+                    else
+                        s[r][c] = j * BN + tx + 16 * c <= limit[r] ? s[r][c] * a.scale2 : -INFINITY;
                     top = fmaxf(top, s[r][c]);
                 }
 #pragma unroll
@@ -261,12 +270,13 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
         if (__builtin_expect(careful, false)) {
 #pragma unroll 1
             for (int r = 0; r < RT; ++r) {
-                const int row = ty * RT + r, last = min(sure + row / w.G, (off + take) * BN - 1);
+                const int row = ty * RT + r, last = min((TREE ? sure + 1 + t0 : sure) + row / w.G, (off + take) * BN - 1);
                 if (row >= rows) continue;
                 float *dst = whole ? a.out + ((pc.s.bos + t0 + row / w.G) * a.Hq + pc.h * w.G + row % w.G) * D
                                    : w.part + part_index(w, blockIdx.x, begun ? 1 : 0, row) * D;
 #pragma unroll 1
                 for (int pos = max(max(sure + 1, off * BN), 0); pos <= last; ++pos) {
+                    if (TREE && !on_path(path[r], pos - sure - 1)) continue;
                     const long pg = pool_page(w.pg, pc.n, pos / w.pg.page_size);
                     if (pg < 0) continue;
                     Raw4<KIND> v;
@@ -283,21 +293,21 @@ __global__ void __launch_bounds__(kThreads) attn_simt_kernel(const SimtParams a)
         // A value that is not finite makes rows that do not see it NaN (0 times it), so a unit whose output is not finite is
         // done again with care: without the values that some rows do not see and that are not finite, which the rows that
         // see them get added above. (Where every row sees all that any sees, there is no need.)
-        careful = !careful && rows > w.G && __syncthreads_or(bad);
+        careful = !careful && (TREE || rows > w.G) && __syncthreads_or(bad);
         if (!careful) {
             pc.left -= take;
-            if (pc.left > 0) next_unit<BN>(w, &pc);
+            if (pc.left > 0) next_unit<BN, TREE>(w, &pc);
             begun = true;
         }
     }
 }
 
-template <int KIND, int D, int R>
+template <int KIND, int D, int R, bool TREE>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     const int G = a.Hq / a.pg.Hkv;
     SimtParams p{attn_work(a, R / G, 1), (const float *)a.q, a.k_cache, a.v_cache, a.k_scale, a.v_scale,
                  (float *)a.out, a.Hq, a.q_stride, a.scale * kLog2e};
-    auto kernel = attn_simt_kernel<KIND, D, R>;
+    auto kernel = attn_simt_kernel<KIND, D, R, TREE>;
     constexpr int bytes = sizeof(SimtSmem<D, R>);
     static_assert(bytes <= 232448, "over the 227 KiB opt-in limit");
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -307,21 +317,21 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     return e != cudaSuccess ? e : launch_attn_join(a, p.w, ctas, s);
 }
 
-template <int KIND, int D>
+template <int KIND, int D, bool TREE>
 cudaError_t launch_rows(const AttnArgs &a, cudaStream_t s) {
     // a row tile of 16 or 32 where no sequence has more rows: a quarter or half of the products of the 64-row tile (8
     // tokens of 4 sequences over 4000, 32 rows, d = 128: 38 us, 47 in the 64-row tile)
     const long rows = (a.pg.cu ? a.pg.Ttot : a.pg.T) * (a.Hq / a.pg.Hkv);
-    if (rows <= 16) return launch_t<KIND, D, 16>(a, s);
-    return rows <= 32 ? launch_t<KIND, D, 32>(a, s) : launch_t<KIND, D, 64>(a, s);
+    if (rows <= 16) return launch_t<KIND, D, 16, TREE>(a, s);
+    return rows <= 32 ? launch_t<KIND, D, 32, TREE>(a, s) : launch_t<KIND, D, 64, TREE>(a, s);
 }
 
 template <int KIND>
 cudaError_t launch_d(const AttnArgs &a, cudaStream_t s) {
     switch (a.pg.d) {
-        case 64: return launch_rows<KIND, 64>(a, s);
-        case 128: return launch_rows<KIND, 128>(a, s);
-        case 256: return launch_rows<KIND, 256>(a, s);
+        case 64: return a.parents ? launch_rows<KIND, 64, true>(a, s) : launch_rows<KIND, 64, false>(a, s);
+        case 128: return a.parents ? launch_rows<KIND, 128, true>(a, s) : launch_rows<KIND, 128, false>(a, s);
+        case 256: return a.parents ? launch_rows<KIND, 256, true>(a, s) : launch_rows<KIND, 256, false>(a, s);
     }
     return cudaErrorInvalidValue;
 }

@@ -133,11 +133,11 @@ struct Walk {
     bool begun;  // the unit at hand started in this CTA
     __device__ __forceinline__ int take() const { return (int)min((long)(pc.ntiles - pc.off), pc.left); }
 };
-template <int BN>
+template <int BN, bool TREE>
 __device__ __forceinline__ bool walk_next(const AttnWork &w, Walk *k) {
     k->pc.left -= k->take();
     if (k->pc.left <= 0) return false;
-    next_unit<BN>(w, &k->pc);
+    next_unit<BN, TREE>(w, &k->pc);
     k->begun = true;
     return k->pc.left > 0;
 }
@@ -163,7 +163,7 @@ __device__ __forceinline__ bool product_done(uint64_t *bar, int which, uint32_t 
 
 // ---- loads ------------------------------------------------------------------------
 // One warp loads K tiles, another V tiles.
-template <int D, int KIND, bool IS_V>
+template <int D, int KIND, bool TREE, bool IS_V>
 __device__ void load_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, const CUtensorMap *map) {
     using C = Cfg<D, KIND>;
     constexpr int BN = C::BN;
@@ -246,7 +246,7 @@ __device__ void load_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
             }
             ring.next();
         }
-    } while (ok && walk_next<BN>(p.w, &k));
+    } while (ok && walk_next<BN, TREE>(p.w, &k));
     if (!ok && lane == 0) flag_error(pg.status);
     // the copies in flight must land before the CTA leaves, also if another warp has given up
     for (uint32_t f = t > N ? t - N : 0; f < t; ++f) mbar_wait(bar + FULL + f % N, (f / N) & 1, kDrainBudget);
@@ -258,7 +258,7 @@ __device__ void load_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
 // between two products is time that the tensor cores may stand still, so the warp walks together
 // (descriptors in uniform registers), slots and phases are counted on instead of divided out, and each
 // product signals one barrier.
-template <int D, int KIND>
+template <int D, int KIND, bool TREE>
 __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *bar, Walk k, uint32_t tmem) {
     using C = Cfg<D, KIND>;
     constexpr int BN = C::BN;
@@ -341,7 +341,7 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
                 prev_last = jj + 1 == n;
                 prev_seen = seen - jj * BN;
             }
-        } while (ok && walk_next<BN>(p.w, &k));
+        } while (ok && walk_next<BN, TREE>(p.w, &k));
         ok = ok && v_ready(t - 1, prev_first) && product_o(t - 1, prev_first, true, prev_seen);
     }
     if (!ok && lane == 0) flag_error(p.w.pg.status);
@@ -355,7 +355,7 @@ __device__ void mma_role(const TcParams &p, uint8_t *sm, uint32_t sb, uint64_t *
 // that are not finite become zeros (the rows group adds them to the rows that see them), and so do positions past the
 // end. (8 prompts of 1024 tokens, 32 heads on 8, D = 128: 100 us without such a look, 102 by this warp, 117 by the one
 // that issues the products.)
-template <int D, int KIND>
+template <int D, int KIND, bool TREE>
 __device__ void check_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k) {
     using C = Cfg<D, KIND>;
     constexpr int BN = C::BN, PR = 8 * C::NB;  // 16-byte pieces of a row
@@ -367,8 +367,8 @@ __device__ void check_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k
     if (k.pc.left > 0) do {
         const int n = k.take(), t0 = k.pc.i * p.w.TPT;
         // of the tile's positions: those before the end, those that every row sees, those that a row sees
-        int valid = k.pc.s.len - k.pc.off * BN, sure = valid - k.pc.s.T + t0 + 1;
-        int seen = sure + min(p.w.TPT, k.pc.s.T - t0) - 1;
+        int valid = k.pc.s.len - k.pc.off * BN, sure = valid - k.pc.s.T + (TREE ? 0 : t0 + 1);
+        int seen = valid - k.pc.s.T + t0 + min(p.w.TPT, k.pc.s.T - t0);
         bool dropped = false;
         for (int jj = 0; jj < n; ++jj, valid -= BN, sure -= BN, seen -= BN) {
             ok = warp_wait(bar + C::B_FV + ring.slot, ring.phase, p.budget);
@@ -398,7 +398,7 @@ __device__ void check_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k
             ring.next();
         }
         ++unit;
-    } while (ok && walk_next<BN>(p.w, &k));
+    } while (ok && walk_next<BN, TREE>(p.w, &k));
     if (!ok && lane == 0) flag_error(p.w.pg.status);
 }
 
@@ -498,20 +498,20 @@ __device__ void convert_role(const TcParams &p, uint8_t *sm, uint64_t *bar, uint
 }
 
 // ---- softmax ----------------------------------------------------------------------------
-// The sum of P over a row's half tile from its products in TMEM, without the value scales. (last: the last column that
-// the row sees)
-template <int HC>
-__device__ __forceinline__ float exact_sum(uint32_t ts, const float *key_scale, float rs, float ref, int last) {
+// The sum of P over a row's half tile from its products in TMEM, without the value scales. (sees: whether the row sees a
+// column)
+template <int HC, typename F>
+__device__ __forceinline__ float exact_sum(uint32_t ts, const float *key_scale, float rs, float ref, F sees) {
     float sum = 0.f;
 #pragma unroll 1
     for (int c = 0; c < HC; ++c) {  // (few registers: this stands where the kernel has none to spare)
         const float s = __uint_as_float(tmem_ld1(ts + c)) * rs;
-        if (c <= last) sum += ex2(s * key_scale[c] - ref);
+        if (sees(c)) sum += ex2(s * key_scale[c] - ref);
     }
     return sum;
 }
 
-template <int D, int KIND>
+template <int D, int KIND, bool TREE>
 __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, uint32_t tmem) {
     using C = Cfg<D, KIND>;
     constexpr int BN = C::BN, HC = BN / 2;
@@ -531,8 +531,14 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
         const int n = k.take(), t0 = k.pc.i * p.w.TPT;
         const int rows = min(p.w.TPT, k.pc.s.T - t0) * p.w.G;
         const bool live_warp = quarter * 32 < rows;
-        const int sure = k.pc.s.len - k.pc.s.T + t0;               // last position that every row of the unit sees
+        const int base = k.pc.s.len - k.pc.s.T;                    // position of the first new token
+        const int sure = TREE ? base - 1 : base + t0;              // last position that every row of the unit sees
         const int limit = row < rows ? sure + tok : -1;            // ... that this row sees
+        uint64_t path = 0;                                         // TREE: the nodes on the row's path
+        if constexpr (TREE) {
+            const Paths paths = tree_paths(p.w.parents + k.pc.s.bos, k.pc.s.T, p.w.pg.status);
+            path = paths.at(min(t0 + tok, k.pc.s.T - 1));
+        }
         float m = -INFINITY, l = 0.f;
         for (int jj = 0; jj < n; ++jj, ++t) {
             const uint32_t b = t & 1;
@@ -567,7 +573,15 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
                     f2_get(f2_fma(f2_mul(f2(x[e + 2], x[e + 3]), rs2), f2(a.z, a.w), f2(lv.z, lv.w)), x[e + 2], x[e + 3]);
                 }
             }
-            if (masked) {
+            if constexpr (TREE) {
+                if (masked) {
+                    const uint64_t sees = path_window(path, pos0 - base);
+                    const uint32_t w[2] = {(uint32_t)sees, (uint32_t)(sees >> 32)};
+#pragma unroll
+                    for (int e = 0; e < HC; ++e)
+                        if (!(w[e >> 5] & (1u << (e & 31)))) x[e] = -INFINITY;
+                }
+            } else if (masked) {
                 const int last = limit - pos0;
 #pragma unroll
                 for (int e = 0; e < HC; ++e)
@@ -600,7 +614,12 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
             }
             const float ref = m == -INFINITY ? 0.f : m;
             if constexpr (C::kCodes) {
-                if (rarely(odd)) l += exact_sum<HC>(ts, col, rs, ref, limit - pos0);
+                if (rarely(odd)) {
+                    if constexpr (TREE)
+                        l += exact_sum<HC>(ts, col, rs, ref, [&](int c) { return on_path(path, pos0 + c - base); });
+                    else
+                        l += exact_sum<HC>(ts, col, rs, ref, [last = limit - pos0](int c) { return c <= last; });
+                }
             }
             F2 l2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
             const F2 sc2 = f2(sc, sc), ref2 = f2(-ref, -ref);
@@ -641,7 +660,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
         __syncwarp();
         if (lane == 0) mbar_arrive(bar + C::B_ST + (unit & 1));
         ++unit;
-    } while (walk_next<BN>(p.w, &k));
+    } while (walk_next<BN, TREE>(p.w, &k));
     if (!ok && lane == 0) flag_error(p.w.pg.status);
 }
 
@@ -649,7 +668,7 @@ __device__ void soft_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k,
 // A thread of this group stands for a row of TMEM. Q comes by TMA, 128 bytes of all the unit's rows at a
 // time (box: 64 elements, the G heads of the key head, the unit's tokens, which lie in shared memory as
 // rows), and goes on into TMEM from there; finished rows are stored straight from TMEM.
-template <int D, int KIND>
+template <int D, int KIND, bool TREE>
 __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, uint32_t tmem, const CUtensorMap *mq) {
     using C = Cfg<D, KIND>;
     constexpr int BN = C::BN, PARTS = D / 64;
@@ -769,12 +788,12 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
         fetch(k, 0);
         bring(k, 0);
         Walk next = k;
-        bool more = walk_next<BN>(p.w, &next);
+        bool more = walk_next<BN, TREE>(p.w, &next);
         if (more) fetch(next, 0);
         for (uint32_t unit = 0; ok; ++unit) {
             if (more) bring(next, unit + 1);
             Walk after = next;
-            const bool more2 = more && walk_next<BN>(p.w, &after);
+            const bool more2 = more && walk_next<BN, TREE>(p.w, &after);
             if (more2) fetch(after, 0);
             ok = ok && warp_wait(bar + C::B_ST + (unit & 1), (unit >> 1) & 1, p.budget);
             if (!ok) break;
@@ -821,12 +840,18 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
                 tc_fence_before();
                 if (!C::kCodes && rarely(repair) && store) {  // what the products left out, for the row if it sees it
                     const KvPages &pg = p.w.pg;
-                    const int sure = k.pc.s.len - k.pc.s.T + t0, shift = 31 - __clz(pg.page_size);
-                    const int first = max(max(sure + 1, k.pc.off * BN), 0), last = min(sure + tok, (k.pc.off + n) * BN - 1);
+                    const int base = k.pc.s.len - k.pc.s.T, shift = 31 - __clz(pg.page_size);
+                    const int first = max(max(TREE ? base : base + t0 + 1, k.pc.off * BN), 0);
+                    const int last = min(base + t0 + tok, (k.pc.off + n) * BN - 1);
+                    const uint64_t on = TREE ? path_of(p.w.parents + k.pc.s.bos, t0 + tok) : 0;
                     const int32_t *table = pg.table + (long)k.pc.n * pg.max_pages;
                     const __nv_bfloat16 *v = reinterpret_cast<const __nv_bfloat16 *>(p.v_cache);
-                    if (whole) add_not_finite(table, pg.num_pages, pg.Hkv, k.pc.h, shift, v, D, first, last, 0, D, out);
-                    else add_not_finite(table, pg.num_pages, pg.Hkv, k.pc.h, shift, v, D, first, last, 0, D, p.w.part + part * D);
+                    if (whole)
+                        add_not_finite<__nv_bfloat16, TREE>(table, pg.num_pages, pg.Hkv, k.pc.h, shift, v, D, first, last, 0, D, out,
+                                                            base, on);
+                    else
+                        add_not_finite<float, TREE>(table, pg.num_pages, pg.Hkv, k.pc.h, shift, v, D, first, last, 0, D,
+                                                    p.w.part + part * D, base, on);
                 }
             }
             __syncwarp();
@@ -844,7 +869,7 @@ __device__ void row_role(const TcParams &p, uint8_t *sm, uint64_t *bar, Walk k, 
     __syncwarp();
 }
 
-template <int D, int KIND>
+template <int D, int KIND, bool TREE>
 __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const TcParams p) {
@@ -898,7 +923,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     before_reading();  // (and before TMEM is asked for: a kernel that ends may still hold it)
     if (warp == 0) tmem_alloc(slot, 512);
     tc_fence_before();
-    plan_piece<C::BN, C::THREADS>(p.w, plan);  // (synchronises the CTA)
+    plan_piece<C::BN, C::THREADS, TREE>(p.w, plan);  // (synchronises the CTA)
     tc_fence_after();
     // All 512 columns are this CTA's, so the allocation starts at column 0, and addresses are constants (in uniform
     // registers; from a loaded value, the issue of each product took about 45 cycles).
@@ -911,27 +936,27 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
     const int group = warp / kGroup;
     if (group < kRowWarp0 / kGroup) {
         if constexpr (C::kCodes) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        soft_role<D, KIND>(p, sm, bar, k, tmem);
+        soft_role<D, KIND, TREE>(p, sm, bar, k, tmem);
     } else if (group == kRowWarp0 / kGroup) {
-        row_role<D, KIND>(p, sm, bar, k, tmem, &mq);
+        row_role<D, KIND, TREE>(p, sm, bar, k, tmem, &mq);
     } else if (group == kLoadWarp / kGroup) {
         if (warp == kLoadWarp) {
-            load_role<D, KIND, false>(p, sm, bar, k, &mk);
+            load_role<D, KIND, TREE, false>(p, sm, bar, k, &mk);
         } else if (warp == kLoadWarp + 1) {
-            load_role<D, KIND, true>(p, sm, bar, k, &mv);
+            load_role<D, KIND, TREE, true>(p, sm, bar, k, &mv);
         } else if (warp == kMmaWarp) {
-            mma_role<D, KIND>(p, sm, sb, bar, k, tmem);
+            mma_role<D, KIND, TREE>(p, sm, sb, bar, k, tmem);
         } else if constexpr (C::kCodes) {
-            if (plan->padding) zero_padding(p.w, p.out, p.Hq, D, tid & 31, 32);
+            if (plan->padding) zero_padding<TREE>(p.w, p.out, p.Hq, D, tid & 31, 32);
         } else {
-            check_role<D, KIND>(p, sm, bar, k);
+            check_role<D, KIND, TREE>(p, sm, bar, k);
         }
     } else if constexpr (C::kCodes) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
         if (group == kConvWarp0 / kGroup) convert_role<D, KIND, false>(p, sm, bar, (uint32_t)k.pc.left);
         else convert_role<D, KIND, true>(p, sm, bar, (uint32_t)k.pc.left);
     }
-    if (!C::kCodes && plan->padding) zero_padding(p.w, p.out, p.Hq, D, tid, C::THREADS);
+    if (!C::kCodes && plan->padding) zero_padding<TREE>(p.w, p.out, p.Hq, D, tid, C::THREADS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -939,7 +964,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 }
 
 // ---- host side ------------------------------------------------------------------
-template <int D, int KIND>
+template <int D, int KIND, bool TREE>
 cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
     using C = Cfg<D, KIND>;
     const int G = a.Hq / a.pg.Hkv;
@@ -962,7 +987,7 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
         if (!page_map(&mk, a.k_cache, a.pg, D * 2, rows) || !page_map(&mv, a.v_cache, a.pg, D * 2, rows))
             return cudaErrorInvalidValue;
     }
-    auto kernel = attn_tc_kernel<D, KIND>;
+    auto kernel = attn_tc_kernel<D, KIND, TREE>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);
     if (e != cudaSuccess) return e;
     const int ctas = attn_ctas(a, p.w, C::BN);
@@ -973,9 +998,9 @@ cudaError_t launch_t(const AttnArgs &a, cudaStream_t s) {
 template <int KIND>
 cudaError_t launch_d(const AttnArgs &a, cudaStream_t s) {
     switch (a.pg.d) {
-        case 64: return launch_t<64, KIND>(a, s);
-        case 128: return launch_t<128, KIND>(a, s);
-        case 256: return launch_t<256, KIND>(a, s);
+        case 64: return a.parents ? launch_t<64, KIND, true>(a, s) : launch_t<64, KIND, false>(a, s);
+        case 128: return a.parents ? launch_t<128, KIND, true>(a, s) : launch_t<128, KIND, false>(a, s);
+        case 256: return a.parents ? launch_t<256, KIND, true>(a, s) : launch_t<256, KIND, false>(a, s);
     }
     return cudaErrorInvalidValue;
 }

@@ -165,6 +165,81 @@ gdn::KvPages kv_pages(const int32_t *block_table, const int32_t *kv_lens, const 
     return p;
 }
 
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Sequences of a call on trees: nodes per sequence (or packed), and the accepted paths' rows where there are any.
+int tree_checks(int B, int T, const int32_t *cu, const int32_t *a, const int32_t *b, const int32_t *c) {
+    if (B < 0 || T < 0 || B > 65535) return GDN_ERR_INVALID_ARG;
+    if (!cu && T > gdn::kTreeMax) return GDN_ERR_UNSUPPORTED;
+    if (!aligned16(cu) || !aligned4(a) || !aligned4(b) || !aligned4(c)) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+// The states of a call on trees (in and out the same where they are only read), if any are used.
+int state_checks(bool used, const float *in, const float *out, const int32_t *slots, int B, int T, const int32_t *cu, int num_slots,
+                 int Hk, int Hv, int dk, int dv, int dtype) {
+    const int rc = common_checks(Hk, Hv, dk, dv, dtype);
+    if (rc != GDN_OK) return rc;
+    const long long states = slots ? (long long)num_slots : (long long)B;
+    if (num_slots < 0 || states * Hv * dv * dk > (1LL << 40)) return GDN_ERR_INVALID_ARG;
+    if ((long long)B * Hv > 0x7fffffffLL || (cu ? (long long)T : (long long)B * T) > 0x7fffffffLL) return GDN_ERR_INVALID_ARG;
+    if (B > 0 && states > 0 && used && (!in || !out || !aligned16(in) || !aligned16(out))) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+void tree_sizes(gdn::TreeArgs &a, const int32_t *cu, int B, int T, int num_slots, int Hk, int Hv, int dk, int dv, int dtype,
+                int *status) {
+    a.cu = cu;
+    a.B = B;
+    a.T = T;
+    a.Ttot = cu ? (long)T : (long)B * T;
+    a.num_slots = num_slots;
+    a.Hk = Hk;
+    a.Hv = Hv;
+    a.dk = dk;
+    a.dv = dv;
+    a.dtype = dtype;
+    a.status = status;
+}
+
+int paged_attn(const void *q, const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+               const int32_t *block_table, const int32_t *kv_lens, const int32_t *cu_seqlens, const int32_t *parents,
+               void *out, int B, int T, int Hq, int Hkv, int d, int num_pages, int page_size, int max_pages,
+               int64_t q_stride, float scale, int dtype, int cache_dtype, void *workspace, size_t workspace_bytes,
+               void *stream) {
+    int rc = kv_checks(B, T, cu_seqlens, Hq, Hkv, d, num_pages, page_size, max_pages, dtype, cache_dtype, q_stride,
+                       (int64_t)Hkv * d);
+    if (rc != GDN_OK || B == 0 || T == 0) return rc;
+    if (num_pages == 0 || max_pages == 0 || !std::isfinite(scale)) return GDN_ERR_INVALID_ARG;
+    rc = kv_pointers(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, num_pages, max_pages, dtype,
+                     cache_dtype, q, out);
+    if (rc != GDN_OK) return rc;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+        workspace_bytes < gdn::attn_workspace(T, Hq / Hkv, d))
+        return GDN_ERR_INVALID_ARG;
+    int *status = status_ptr();
+    if (!status) return GDN_ERR_CUDA;
+    gdn::AttnArgs a{};
+    a.pg = kv_pages(block_table, kv_lens, cu_seqlens, B, T, Hkv, d, num_pages, page_size, max_pages, dtype,
+                    cache_dtype, status);
+    a.parents = parents;
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.out = out;
+    a.Hq = Hq;
+    a.q_stride = (long)q_stride;
+    a.scale = scale;
+    a.ws = workspace;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype != GDN_BF16 ? gdn::launch_attn_simt(a, s)
+                          : gdn::attn_rows_supported(a) ? gdn::launch_attn_rows(a, s)
+                                                        : gdn::launch_attn_tc(a, s);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -414,36 +489,146 @@ int gdn_paged_attn(const void *q, const void *k_cache, const void *v_cache, cons
                    const int32_t *cu_seqlens, void *out, int B, int T, int Hq, int Hkv, int d, int num_pages,
                    int page_size, int max_pages, int64_t q_stride, float scale, int dtype, int cache_dtype,
                    void *workspace, size_t workspace_bytes, void *stream) {
-    int rc = kv_checks(B, T, cu_seqlens, Hq, Hkv, d, num_pages, page_size, max_pages, dtype, cache_dtype, q_stride,
-                       (int64_t)Hkv * d);
-    if (rc != GDN_OK || B == 0 || T == 0) return rc;
-    if (num_pages == 0 || max_pages == 0 || !std::isfinite(scale)) return GDN_ERR_INVALID_ARG;
-    rc = kv_pointers(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, num_pages, max_pages, dtype,
-                     cache_dtype, q, out);
+    return paged_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, nullptr, out, B, T, Hq, Hkv,
+                      d, num_pages, page_size, max_pages, q_stride, scale, dtype, cache_dtype, workspace, workspace_bytes,
+                      stream);
+}
+
+int gdn_tree_attn(const void *q, const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+                  const int32_t *block_table, const int32_t *kv_lens, const int32_t *cu_seqlens,
+                  const int32_t *parents, void *out, int B, int T, int Hq, int Hkv, int d, int num_pages,
+                  int page_size, int max_pages, int64_t q_stride, float scale, int dtype, int cache_dtype,
+                  void *workspace, size_t workspace_bytes, void *stream) {
+    const int rc = tree_checks(B, T, cu_seqlens, parents, nullptr, nullptr);
     if (rc != GDN_OK) return rc;
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
-        workspace_bytes < gdn::attn_workspace(T, Hq / Hkv, d))
-        return GDN_ERR_INVALID_ARG;
+    if (B > 0 && T > 0 && !parents) return GDN_ERR_INVALID_ARG;
+    return paged_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, parents, out, B, T, Hq, Hkv,
+                      d, num_pages, page_size, max_pages, q_stride, scale, dtype, cache_dtype, workspace, workspace_bytes,
+                      stream);
+}
+
+int gdn_kv_keep(void *k_cache, void *v_cache, float *k_scale, float *v_scale, const int32_t *block_table,
+                const int32_t *kv_lens, const int32_t *cu_seqlens, const int32_t *path, const int32_t *counts, int B,
+                int T, int path_stride, int Hkv, int d, int num_pages, int page_size, int max_pages, int cache_dtype,
+                void *stream) {
+    if (cu_seqlens) T = 1;  // (says nothing)
+    int rc = tree_checks(B, T, cu_seqlens, path, counts, nullptr);
+    if (rc != GDN_OK) return rc;
+    const int dtype = cache_dtype == GDN_F32 ? GDN_F32 : GDN_BF16;
+    rc = kv_checks(B, T, cu_seqlens, Hkv, Hkv, d, num_pages, page_size, max_pages, dtype, cache_dtype, (int64_t)Hkv * d,
+                   (int64_t)Hkv * d);
+    if (rc != GDN_OK) return rc;
+    if (path_stride < 0) return GDN_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) return GDN_OK;
+    static const int32_t __attribute__((aligned(16))) some[4] = {0};  // (no rows come with this call)
+    rc = kv_pointers(k_cache, v_cache, k_scale, v_scale, block_table, kv_lens, cu_seqlens, num_pages, max_pages, dtype,
+                     cache_dtype, some, some);
+    if (rc != GDN_OK) return rc;
+    if ((!path && path_stride > 0) || !counts) return GDN_ERR_INVALID_ARG;
     int *status = status_ptr();
     if (!status) return GDN_ERR_CUDA;
-    gdn::AttnArgs a{};
-    a.pg = kv_pages(block_table, kv_lens, cu_seqlens, B, T, Hkv, d, num_pages, page_size, max_pages, dtype,
-                    cache_dtype, status);
+    gdn::KeepArgs a{kv_pages(block_table, kv_lens, cu_seqlens, B, T, Hkv, d, num_pages, page_size, max_pages, dtype,
+                             cache_dtype, status),
+                    k_cache, v_cache, k_scale, v_scale, path, counts, path_stride};
+    return gdn::launch_kv_keep(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_tree_scan(const void *q, const void *k, const void *v, const void *g, const void *b, const float *state,
+                  const int32_t *slots, const int32_t *parents, const int32_t *cu_seqlens, void *out, int B, int T,
+                  int num_slots, int Hk, int Hv, int dk, int dv, int dtype, void *stream) {
+    gdn::TreeArgs a{};
+    int rc = tree_checks(B, T, cu_seqlens, slots, parents, nullptr);
+    if (rc == GDN_OK) rc = state_checks(T > 0, state, state, slots, B, T, cu_seqlens, num_slots, Hk, Hv, dk, dv, dtype);
+    if (rc != GDN_OK || B == 0 || T == 0) return rc;
+    const void *ptrs[] = {q, k, v, g, b, out};
+    for (const void *p : ptrs)
+        if (!p || !aligned16(p)) return GDN_ERR_INVALID_ARG;
+    if (!parents) return GDN_ERR_INVALID_ARG;
+    int *status = status_ptr();
+    if (!status) return GDN_ERR_CUDA;
     a.q = q;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.b = b;
+    a.state_in = state;
     a.out = out;
-    a.Hq = Hq;
-    a.q_stride = (long)q_stride;
-    a.scale = scale;
-    a.ws = workspace;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype != GDN_BF16 ? gdn::launch_attn_simt(a, s)
-                          : gdn::attn_rows_supported(a) ? gdn::launch_attn_rows(a, s)
-                                                        : gdn::launch_attn_tc(a, s);
-    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    a.slots = slots;
+    a.parents = parents;
+    tree_sizes(a, cu_seqlens, B, T, num_slots, Hk, Hv, dk, dv, dtype, status);
+    return gdn::launch_tree_scan(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_tree_advance(const void *k, const void *v, const void *g, const void *b, const float *state_in,
+                     float *state_out, const int32_t *slots, const int32_t *path, const int32_t *counts,
+                     const int32_t *cu_seqlens, int B, int T, int path_stride, int num_slots, int Hk, int Hv, int dk,
+                     int dv, int dtype, void *stream) {
+    gdn::TreeArgs a{};
+    int rc = tree_checks(B, T, cu_seqlens, slots, path, counts);
+    if (rc == GDN_OK) rc = state_checks(true, state_in, state_out, slots, B, T, cu_seqlens, num_slots, Hk, Hv, dk, dv, dtype);
+    if (rc != GDN_OK) return rc;
+    if (path_stride < 0) return GDN_ERR_INVALID_ARG;
+    if (B == 0) return GDN_OK;
+    const void *ptrs[] = {k, v, g, b};
+    for (const void *p : ptrs)
+        if (T > 0 && (!p || !aligned16(p))) return GDN_ERR_INVALID_ARG;
+    if ((!path && path_stride > 0) || !counts) return GDN_ERR_INVALID_ARG;
+    int *status = status_ptr();
+    if (!status) return GDN_ERR_CUDA;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.b = b;
+    a.state_in = state_in;
+    a.state_out = state_out;
+    a.slots = slots;
+    a.path = path;
+    a.counts = counts;
+    a.path_stride = path_stride;
+    tree_sizes(a, cu_seqlens, B, T, num_slots, Hk, Hv, dk, dv, dtype, status);
+    return gdn::launch_tree_advance(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+int gdn_tree_verify(const float *target_probs, const float *draft_probs, const int32_t *tokens, const int32_t *parents,
+                    const float *r, const float *r_last, const int32_t *cu_seqlens, int32_t *path, int32_t *counts,
+                    int32_t *next, int B, int T, int V, int64_t target_stride, int64_t draft_stride, int path_stride,
+                    void *stream) {
+    int rc = tree_checks(B, T, cu_seqlens, tokens, parents, path);
+    if (rc != GDN_OK) return rc;
+    if (V < 1) return GDN_ERR_INVALID_ARG;
+    if (V > gdn::kVerMaxVocab) return GDN_ERR_UNSUPPORTED;
+    if (target_stride < V || (draft_probs && draft_stride < V)) return GDN_ERR_INVALID_ARG;
+    if (path_stride < 0 || path_stride > (1 << 20) || (!cu_seqlens && path_stride < T)) return GDN_ERR_INVALID_ARG;
+    const long long tokens_all = cu_seqlens ? (long long)T : (long long)B * T;
+    const int64_t widest = draft_probs && draft_stride > target_stride ? draft_stride : target_stride;
+    if (widest > (1LL << 40) || tokens_all * (widest >> 8) > (1LL << 40)) return GDN_ERR_INVALID_ARG;
+    if (B == 0) return GDN_OK;
+    if (!aligned4(counts) || !aligned4(next) || !aligned4(r) || !aligned4(r_last)) return GDN_ERR_INVALID_ARG;
+    if (!counts || !next || !r_last || (!path && path_stride > 0)) return GDN_ERR_INVALID_ARG;
+    if (T > 0 && (!target_probs || !tokens || !parents || !r)) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(target_probs) || !aligned16(draft_probs)) return GDN_ERR_INVALID_ARG;
+    int *status = status_ptr();
+    if (!status) return GDN_ERR_CUDA;
+    gdn::VerifyArgs a{};
+    a.target = target_probs;
+    a.draft = draft_probs;
+    a.tokens = tokens;
+    a.parents = parents;
+    a.cu = cu_seqlens;
+    a.r = r;
+    a.r_last = r_last;
+    a.path = path;
+    a.counts = counts;
+    a.next = next;
+    a.B = B;
+    a.T = T;
+    a.Ttot = (long)tokens_all;
+    a.V = V;
+    a.target_stride = (long)target_stride;
+    a.draft_stride = (long)draft_stride;
+    a.path_stride = path_stride;
+    a.status = status;
+    return gdn::launch_tree_verify(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 int gdn_get_device_status(void *stream) {

@@ -57,8 +57,47 @@ struct KvArgs {  // write: k, v -> caches; read: caches -> k, v
     long k_stride, v_stride;  // elements between a token's rows and the next token's
 };
 
+constexpr int kTreeMax = 64;  // nodes of a sequence's tree of drafted tokens
+
+struct TreeArgs {  // the gated delta rule over trees: scan reads q .. b and state_in; advance k .. b, path and counts
+    const void *q, *k, *v, *g, *b;
+    const float *state_in;
+    float *state_out;
+    void *out;
+    const int32_t *slots, *parents, *path, *counts, *cu;
+    int B;
+    long T, Ttot;  // as for KvPages
+    int path_stride;
+    long num_slots;
+    int Hk, Hv, dk, dv, dtype;
+    int *status;
+};
+
+constexpr int kVerMaxVocab = 1 << 22;
+struct VerifyArgs {
+    const float *target, *draft;
+    const int32_t *tokens, *parents, *cu;
+    const float *r, *r_last;
+    int32_t *path, *counts, *next;
+    int B;
+    long T, Ttot;
+    int V;
+    long target_stride, draft_stride;
+    int path_stride;
+    int *status;
+};
+
+struct KeepArgs {
+    KvPages pg;
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    const int32_t *path, *counts;
+    int path_stride;
+};
+
 struct AttnArgs {
     KvPages pg;
+    const int32_t *parents = nullptr;  // of a tree of new tokens; null: each new token sees those before it
     const void *q;
     const void *k_cache, *v_cache;
     const float *k_scale, *v_scale;
@@ -80,6 +119,11 @@ cudaError_t launch_attn_simt(const AttnArgs &a, cudaStream_t s);  // fp32
 cudaError_t launch_attn_tc(const AttnArgs &a, cudaStream_t s);    // bf16
 bool attn_rows_supported(const AttnArgs &a);                      // bf16, few rows per key head
 cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t s);
+
+cudaError_t launch_kv_keep(const KeepArgs &a, cudaStream_t s);
+cudaError_t launch_tree_scan(const TreeArgs &a, cudaStream_t s);
+cudaError_t launch_tree_advance(const TreeArgs &a, cudaStream_t s);
+cudaError_t launch_tree_verify(const VerifyArgs &a, cudaStream_t s);
 
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t s);
 cudaError_t launch_prepass(const PrepassArgs &a, cudaStream_t s);

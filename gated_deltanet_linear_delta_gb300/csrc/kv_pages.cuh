@@ -50,11 +50,17 @@ struct SeqInfo {
     int len;   // cached tokens, the new ones among them
 };
 
-// Sequence n of the call. False (flagged) when cu is inconsistent; a kv_len outside of the block
+// Sequence n of the call. False (flagged) when cu is inconsistent or gives a tree too many nodes; a kv_len outside of the block
 // table's row is flagged and counts as 0, which makes the sequence's tokens padding.
+template <bool TREE = false>
 __device__ __forceinline__ bool seq_info(const KvPages &p, int n, SeqInfo *s) {
     long eos;
     if (!seq_bounds(p.cu, n, p.B, p.cu ? p.Ttot : p.T, &s->bos, &eos, p.status)) {
+        s->T = s->len = 0;
+        return false;
+    }
+    if (TREE && eos - s->bos > kTreeMax) {
+        flag_error(p.status);
         s->T = s->len = 0;
         return false;
     }

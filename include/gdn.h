@@ -410,6 +410,120 @@ GDN_API int gdn_paged_attn(const void *q, const void *k_cache, const void *v_cac
 GDN_API size_t gdn_paged_attn_workspace_size(int B, int T, int packed, int Hq, int Hkv, int d);
 
 /*
+ * Trees of drafted tokens.
+ * ------------------------
+ * A draft model proposes a tree of continuations, the model checks all of its nodes in one step, and the path that
+ * survives advances the session. A sequence's nodes are the packed tokens of the step (cu_seqlens int32 [B+1] with T
+ * the packed total, or NULL: T each), at most 64:
+ *
+ *     parents  [Ttot] int32: node t's parent, by its index within the sequence, 0 <= parents[t] < t; -1: a root, right
+ *              after the context. Anything below -1 makes a padding node (a fixed number of nodes in a captured
+ *              graph), whose path is empty, and so are its descendants'. parents[t] >= t is flagged, and padding.
+ *     path(t)  the nodes from the root to t, t among them
+ *
+ * Every layer takes the step's parents: gdn_tree_attn in attention layers (the nodes' rows written by gdn_kv_write),
+ * gdn_tree_scan in gated delta rule layers; gdn_tree_verify finds the accepted path and the next token; gdn_kv_keep and
+ * gdn_tree_advance bring the layers' caches and states up to it. An accepted path is
+ *
+ *     path     [B][path_stride] int32: sequence n's accepted nodes path[n][0 .. counts[n]), in increasing order
+ *     counts   [B] int32: 0 .. min(T_n, path_stride) (0: an idle row of the batch)
+ *
+ * These arrays, slots and tokens need 4-byte alignment only. More than 64 nodes of a sequence: GDN_ERR_UNSUPPORTED (cu_seqlens NULL),
+ * or flagged, and the sequence is skipped. The calls allocate nothing and may be captured into a graph; all that they
+ * read may change between replays. Their results do not depend on the order in which the GPU runs their parts.
+ */
+
+/*
+ * gdn_tree_attn -- gdn_paged_attn of trees: node t sees the context, positions 0 .. kv_lens[n] - T_n - 1, and of the
+ * new tokens those on path(t), node s at position kv_lens[n] - T_n + s. (A padding node sees the context alone.)
+ *   parents : above. All else, the workspace and its size among it, as for gdn_paged_attn; kv_lens counts all nodes in.
+ *             What a node does not see has no effect on it, whatever its value.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API int gdn_tree_attn(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                          const float *v_scale, const int32_t *block_table, const int32_t *kv_lens,
+                          const int32_t *cu_seqlens, const int32_t *parents, void *out, int B, int T, int Hq,
+                          int Hkv, int d, int num_pages, int page_size, int max_pages, int64_t q_stride,
+                          float scale, int dtype, int cache_dtype, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * gdn_kv_keep -- the cache rows of the accepted paths move right after their contexts: position base + path[n][i]
+ * becomes position base + i, base = kv_lens[n] - T_n, in k_cache and v_cache (and the scales of 8-bit caches), as they
+ * are stored. What lies past the accepted tokens stays as it was. kv_lens is the step's, all nodes counted in; after
+ * the call the sequence has base + counts[n] tokens.
+ *   path, counts : above; a sequence whose path is not increasing, or names no node, is flagged and left alone. With
+ *                  kv_lens[n] < T_n (an idle row of the batch) nothing moves.
+ *   T            : nodes of each sequence; not read with cu_seqlens.
+ *   cache_dtype  : GDN_BF16, GDN_F32, GDN_FP8 or GDN_INT8. Other arguments as for gdn_kv_write.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API int gdn_kv_keep(void *k_cache, void *v_cache, float *k_scale, float *v_scale, const int32_t *block_table,
+                        const int32_t *kv_lens, const int32_t *cu_seqlens, const int32_t *path,
+                        const int32_t *counts, int B, int T, int path_stride, int Hkv, int d, int num_pages,
+                        int page_size, int max_pages, int cache_dtype, void *stream);
+
+/*
+ * gdn_tree_scan -- the gated delta rule over trees: out of node t is S_t qh_t, with S_t the sequence's state after the
+ * recurrence over path(t). The states are only read (gdn_tree_advance moves them on).
+ *
+ *   q, k, v, g, b, out : packed, as for gdn_prefill.
+ *   state : [B][Hv][dv][dk] fp32, or with slots a pool [num_slots][Hv][dv][dk].
+ *   slots : device int32 [B] or NULL, as for gdn_decode_step_slots: sequence n's state is entry slots[n]; negative:
+ *           padding, whose nodes' outputs are zeros.
+ * With bf16 inputs the states enter the products with 16 bits of precision, the outputs' own rounding aside; with fp32
+ * inputs all is fp32.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API int gdn_tree_scan(const void *q, const void *k, const void *v, const void *g, const void *b,
+                          const float *state, const int32_t *slots, const int32_t *parents,
+                          const int32_t *cu_seqlens, void *out, int B, int T, int num_slots, int Hk, int Hv,
+                          int dk, int dv, int dtype, void *stream);
+
+/*
+ * gdn_tree_advance -- the states after the accepted paths: the recurrence over nodes path[n][0 .. counts[n]) in turn.
+ *
+ *   k, v, g, b : the step's packed inputs, as gdn_tree_scan took them.
+ *   state_in, state_out : states, or with slots pools, as for gdn_tree_scan; may be the same (in place). A sequence
+ *           with count 0 copies its state through; entries of a pool that no sequence names are left as they are.
+ *   path, counts : above (the nodes in any order; each names one of the sequence's). A count or a node out of range is
+ *           flagged, and the state passes through.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API int gdn_tree_advance(const void *k, const void *v, const void *g, const void *b, const float *state_in,
+                             float *state_out, const int32_t *slots, const int32_t *path, const int32_t *counts,
+                             const int32_t *cu_seqlens, int B, int T, int path_stride, int num_slots, int Hk,
+                             int Hv, int dk, int dv, int dtype, void *stream);
+
+/*
+ * gdn_tree_verify -- which drafted tokens stand, and the token after them, from given random numbers.
+ *
+ * A walk from node 0, the root, whose token is already the sequence's: at node t with target probabilities p and draft
+ * probabilities q (rows t), the children of t in increasing order, with w = p and Z = 1 at first:
+ *     child i with token x is accepted, and the walk goes on there, if  r[i] Z q(x) < w(x);
+ *     else  w <- max(w - Z q, 0),  Z <- sum w.
+ * With no child left the next token is the least x for which the sum of w up to x is above r_last[n] times the whole sum
+ * (of p, if w has no weight left). If each node's children were drawn from its q, independently, the accepted and next
+ * tokens are distributed as the target's. draft_probs NULL: each child was proposed for certain (q is one at its token).
+ * Weights and sums are kept to 48 bits.
+ *
+ *   target_probs, draft_probs : [Ttot][V] fp32, rows target_stride and draft_stride elements apart (at least V);
+ *           not negative, each row's sum 1. V: 1 .. 4194304.
+ *   tokens  : [Ttot] int32, the drafted tokens (node 0's is not read). A token outside of 0 .. V-1 is flagged, its node
+ *             never accepted.
+ *   r, r_last : [Ttot] and [B] fp32 in [0, 1): a number for each node (node 0's is not read) and for the next token.
+ *   path    : [B][path_stride] int32: node 0 and the accepted nodes; -1 after them. path_stride: at least the nodes of
+ *             any sequence, at most 2^20.
+ *   counts  : [B] int32: the entries of path. A sequence without nodes, or whose node 0 is padding, gets 0.
+ *   next    : [B] int32: the next token; -1 where counts is 0, or where p's sum is 0 or not finite (flagged).
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API int gdn_tree_verify(const float *target_probs, const float *draft_probs, const int32_t *tokens,
+                            const int32_t *parents, const float *r, const float *r_last,
+                            const int32_t *cu_seqlens, int32_t *path, int32_t *counts, int32_t *next, int B, int T,
+                            int V, int64_t target_stride, int64_t draft_stride, int path_stride, void *stream);
+
+/*
  * gdn_get_device_status -- synchronise `stream`, then return and clear the
  * device status word: GDN_OK, or GDN_ERR_DEVICE_CHECK if a kernel found
  * inconsistent device data since the last call; GDN_ERR_CUDA if the
