@@ -98,4 +98,19 @@ static __device__ __noinline__ uint64_t path_of(const int32_t *parents, int t) {
     return t == -1 ? path : 0;
 }
 
+// a + b as a rounded sum and what was lost
+__device__ __forceinline__ void add_exact(float &hi, float &lo, float x) {
+    const float s = hi + x, y = s - hi;
+    lo += (hi - (s - y)) + (x - y);
+    hi = s;
+}
+
+// Pool entry of sequence n; -1 for padding (flagged if it names none)
+__device__ __forceinline__ long state_slot(const TreeArgs &a, int n) {
+    if (a.slots == nullptr) return n;
+    const long s = a.slots[n];
+    if (s >= a.num_slots) flag_error(a.status);
+    return s < 0 || s >= a.num_slots ? -1 : s;
+}
+
 }  // namespace gdn

@@ -1,0 +1,63 @@
+// tree_mma.cuh -- what the tensor-core kernels of the gated delta rule over trees share: m16n8k16 products of bf16
+// (mma.sync), their operands from shared memory, and fp32 values split into bf16 terms.
+#pragma once
+
+#include "tc_ops.cuh"
+#include "tree.cuh"
+
+namespace gdn {
+
+// ---- products ----------------------------------------------------------------------
+// Lane (g = lane / 4, c = lane % 4): D and C hold rows g and g + 8, columns 2 c and 2 c + 1, as {g 2c, g 2c+1, g+8 2c,
+// g+8 2c+1}; A the same of both halves of its 16 columns; B rows 2 c .. and 2 c + 8 .. of column g.
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// four 8 x 8 matrices whose rows are 16 bytes at the lanes' addresses (lanes 0..7 the first's, 8..15 the second's, ..)
+__device__ __forceinline__ void load_matrices(uint32_t (&x)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void load_matrices_t(uint32_t (&x)[4], uint32_t addr) {  // each transposed
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// A pair of fp32 as bf16, and what that leaves of them
+__device__ __forceinline__ uint32_t split2(float &x, float &y) {
+    const uint32_t h = tc::bf2_bits(__floats2bfloat162_rn(x, y));
+    x -= __uint_as_float(h << 16);
+    y -= __uint_as_float(h & 0xffff0000u);
+    return h;
+}
+
+// ---- asynchronous copies -------------------------------------------------------------
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- layouts in shared memory: where the 16 bytes `ch` of row r lie ------------------------
+// rows of DK bf16: a row's pieces are spread by the row, so that the 8 rows of a matrix lie in different banks
+template <int DK>
+__device__ __forceinline__ uint32_t row_piece(int r, int ch) {
+    if (DK >= 64) return (uint32_t)(r * (DK * 2) + ((ch ^ (r & 7)) << 4));
+    return (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+}
+// 32 columns of a state, rows of 128 bytes: lanes of 4 rows 2 apart and 32 bytes each lie in different banks
+__device__ __forceinline__ uint32_t state_piece(int r, int ch) { return (uint32_t)(r * 128 + ((ch ^ (((r >> 1) & 3) << 1)) << 4)); }
+// block (i, j <= i) of 16 x 16 bf16 coefficients: 32 bytes a row
+__device__ __forceinline__ uint32_t coef_block(int i, int j) { return (uint32_t)((i * (i + 1) / 2 + j) * 512); }
+__device__ __forceinline__ uint32_t coef_piece(int r, int ch) { return (uint32_t)(r * 32 + ((ch ^ ((r >> 2) & 1)) << 4)); }
+
+}  // namespace gdn

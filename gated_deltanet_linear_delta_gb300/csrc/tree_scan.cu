@@ -12,21 +12,6 @@
 namespace gdn {
 namespace {
 
-// Pool entry of sequence n; -1 for padding (flagged if it names none)
-__device__ __forceinline__ long state_slot(const TreeArgs &a, int n) {
-    if (a.slots == nullptr) return n;
-    const long s = a.slots[n];
-    if (s >= a.num_slots) flag_error(a.status);
-    return s < 0 || s >= a.num_slots ? -1 : s;
-}
-
-// a + b as a rounded sum and what was lost
-__device__ __forceinline__ void add_exact(float &hi, float &lo, float x) {
-    const float s = hi + x, y = s - hi;
-    lo += (hi - (s - y)) + (x - y);
-    hi = s;
-}
-
 template <typename T, int DK, int DV>
 struct ScanSmem {
     float kh[kTreeMax][DK], qh[kTreeMax][DK];
@@ -225,7 +210,7 @@ cudaError_t launch_dk(const TreeArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_scan(const TreeArgs &a, cudaStream_t s) {
-    return a.dtype == GDN_F32 ? launch_dk<true, float>(a, s) : launch_dk<true, __nv_bfloat16>(a, s);
+    return a.dtype == GDN_F32 ? launch_dk<true, float>(a, s) : launch_tree_scan_tc(a, s);
 }
 cudaError_t launch_tree_advance(const TreeArgs &a, cudaStream_t s) {
     return a.dtype == GDN_F32 ? launch_dk<false, float>(a, s) : launch_dk<false, __nv_bfloat16>(a, s);
