@@ -22,13 +22,6 @@ __device__ __forceinline__ void load_matrices(uint32_t (&x)[4], uint32_t addr) {
                  : "r"(addr)
                  : "memory");
 }
-__device__ __forceinline__ void load_matrices_t(uint32_t (&x)[4], uint32_t addr) {  // each transposed
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
 // A pair of fp32 as bf16, and what that leaves of them
 __device__ __forceinline__ uint32_t split2(float &x, float &y) {
     const uint32_t h = tc::bf2_bits(__floats2bfloat162_rn(x, y));
@@ -56,8 +49,8 @@ __device__ __forceinline__ uint32_t row_piece(int r, int ch) {
 }
 // 32 columns of a state, rows of 128 bytes: lanes of 4 rows 2 apart and 32 bytes each lie in different banks
 __device__ __forceinline__ uint32_t state_piece(int r, int ch) { return (uint32_t)(r * 128 + ((ch ^ (((r >> 1) & 3) << 1)) << 4)); }
-// block (i, j <= i) of 16 x 16 bf16 coefficients: 32 bytes a row
-__device__ __forceinline__ uint32_t coef_block(int i, int j) { return (uint32_t)((i * (i + 1) / 2 + j) * 512); }
-__device__ __forceinline__ uint32_t coef_piece(int r, int ch) { return (uint32_t)(r * 32 + ((ch ^ ((r >> 2) & 1)) << 4)); }
+// block (i, j <= i) of 16 x 16 coefficients, 64 bytes a row (fp32, or two bf16 terms each); rows spread as above
+__device__ __forceinline__ uint32_t coef_block(int i, int j) { return (uint32_t)((i * (i + 1) / 2 + j) * 1024); }
+__device__ __forceinline__ uint32_t coef_piece(int r, int ch) { return (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)); }
 
 }  // namespace gdn

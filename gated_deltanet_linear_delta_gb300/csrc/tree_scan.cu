@@ -1,4 +1,4 @@
-// tree_scan.cu -- the gated delta rule over a tree of drafted tokens, and over the accepted path of one.
+// tree_scan.cu -- the gated delta rule over a tree of drafted tokens.
 //
 // Along the path of node t, with G_t the sum of g over it, S_t the state after it and S_0 the sequence's state,
 //     S_t = e^{G_t} S_0 + sum_{s on path(t)} e^{G_t - G_s} u_s kh_s^T,
@@ -121,88 +121,22 @@ __global__ void __launch_bounds__(128) tree_scan_kernel(const TreeArgs a) {
     }
 }
 
-template <typename T, int DK, int DV>
-__global__ void __launch_bounds__(128) tree_advance_kernel(const TreeArgs a) {
-    __shared__ float kh[DK], norm[4];
-    __shared__ int path[kTreeMax];
-    const int n = blockIdx.x / a.Hv, h = blockIdx.x % a.Hv, hk = h / (a.Hv / a.Hk), tid = threadIdx.x;
-    long bos;
-    int nodes;
-    if (!tree_bounds(a.cu, n, a.B, a.cu ? a.Ttot : a.T, &bos, &nodes, a.status)) return;
-    const long slot = state_slot(a, n);
-    if (slot < 0) return;
-    int count = a.counts[n];
-    bool bad = count < 0 || count > min(nodes, a.path_stride);
-    if (!bad && tid < count) {
-        path[tid] = a.path[(long)n * a.path_stride + tid];
-        bad = path[tid] < 0 || path[tid] >= nodes;
-    }
-    if (__syncthreads_or(bad)) {
-        if (tid == 0) flag_error(a.status);
-        count = 0;
-    }
-    float row[DK];
-    const long at = ((slot * a.Hv + h) * DV + min(tid, DV - 1)) * DK;
-#pragma unroll
-    for (int c = 0; c < DK; c += 4) {
-        const float4 x = load4(a.state_in + at + c);
-        row[c] = x.x; row[c + 1] = x.y; row[c + 2] = x.z; row[c + 3] = x.w;
-    }
-    for (int i = 0; i < count; ++i) {
-        const long tok = bos + path[i];
-        const float x = tid < DK ? to_f32(((const T *)a.k)[(tok * a.Hk + hk) * DK + tid]) : 0.f;
-        const float part = warp_sum(x * x);
-        __syncthreads();
-        if ((tid & 31) == 0) norm[tid >> 5] = part;
-        if (tid < DK) kh[tid] = x;
-        __syncthreads();
-        const float r = 1.f / sqrtf((norm[0] + norm[1]) + (norm[2] + norm[3]) + kNormEps);
-        const float alpha = expf(to_f32(((const T *)a.g)[tok * a.Hv + h])), beta = sigmoidf_(to_f32(((const T *)a.b)[tok * a.Hv + h]));
-        const float vi = tid < DV ? to_f32(((const T *)a.v)[(tok * a.Hv + h) * DV + tid]) : 0.f;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int c = 0; c < DK; ++c) s[c & 3] = fmaf(row[c], kh[c], s[c & 3]);
-        const float u = beta * (vi - alpha * r * ((s[0] + s[1]) + (s[2] + s[3]))) * r;
-#pragma unroll
-        for (int c = 0; c < DK; ++c) row[c] = fmaf(u, kh[c], alpha * row[c]);
-    }
-    if (tid < DV)
-#pragma unroll
-        for (int c = 0; c < DK; c += 4)
-            *reinterpret_cast<float4 *>(a.state_out + at + c) = make_float4(row[c], row[c + 1], row[c + 2], row[c + 3]);
-}
-
-template <bool SCAN, typename T, int DK, int DV>
+template <int DK, int DV>
 cudaError_t launch_t(const TreeArgs &a, cudaStream_t s) {
-    const unsigned grid = (unsigned)(a.B * a.Hv);
-    if constexpr (SCAN) {
-        auto kernel = tree_scan_kernel<T, DK, DV>;
-        constexpr int bytes = sizeof(ScanSmem<T, DK, DV>);
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return e;
-        kernel<<<grid, 128, bytes, s>>>(a);
-    } else {
-        tree_advance_kernel<T, DK, DV><<<grid, 128, 0, s>>>(a);
-    }
+    auto kernel = tree_scan_kernel<float, DK, DV>;
+    constexpr int bytes = sizeof(ScanSmem<float, DK, DV>);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(a.B * a.Hv), 128, bytes, s>>>(a);
     return cudaGetLastError();
 }
 
-template <bool SCAN, typename T, int DK>
+template <int DK>
 cudaError_t launch_dv(const TreeArgs &a, cudaStream_t s) {
     switch (a.dv) {
-        case 32: return launch_t<SCAN, T, DK, 32>(a, s);
-        case 64: return launch_t<SCAN, T, DK, 64>(a, s);
-        case 128: return launch_t<SCAN, T, DK, 128>(a, s);
-    }
-    return cudaErrorInvalidValue;
-}
-
-template <bool SCAN, typename T>
-cudaError_t launch_dk(const TreeArgs &a, cudaStream_t s) {
-    switch (a.dk) {
-        case 32: return launch_dv<SCAN, T, 32>(a, s);
-        case 64: return launch_dv<SCAN, T, 64>(a, s);
-        case 128: return launch_dv<SCAN, T, 128>(a, s);
+        case 32: return launch_t<DK, 32>(a, s);
+        case 64: return launch_t<DK, 64>(a, s);
+        case 128: return launch_t<DK, 128>(a, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -210,10 +144,13 @@ cudaError_t launch_dk(const TreeArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_scan(const TreeArgs &a, cudaStream_t s) {
-    return a.dtype == GDN_F32 ? launch_dk<true, float>(a, s) : launch_tree_scan_tc(a, s);
-}
-cudaError_t launch_tree_advance(const TreeArgs &a, cudaStream_t s) {
-    return a.dtype == GDN_F32 ? launch_dk<false, float>(a, s) : launch_dk<false, __nv_bfloat16>(a, s);
+    if (a.dtype != GDN_F32) return launch_tree_scan_tc(a, s);
+    switch (a.dk) {
+        case 32: return launch_dv<32>(a, s);
+        case 64: return launch_dv<64>(a, s);
+        case 128: return launch_dv<128>(a, s);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace gdn

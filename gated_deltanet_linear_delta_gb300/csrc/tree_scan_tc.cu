@@ -1,21 +1,26 @@
 // tree_scan_tc.cu -- the gated delta rule over trees for bf16 inputs, on the tensor cores (formulas: tree_scan.cu).
 //
-// Per (sequence, value head), with T nodes and S_0 (dv x dk fp32) read once:
-//     X = S_0 [K; Q]^T          S_0 split into two bf16 terms (16 bits), k and q as they are (exact)
-//     A_ts, P_ts                from K K^T and Q K^T (exact products), norms, gates and paths, for s on path(t)
-//     (I + A) U^T = diag(beta) V - diag(beta e^G rk) X_k^T    in blocks of 16 nodes
-//     O^T = diag(e^G rq) X_q^T + P U^T
-// The products are m16n8k16 (mma.sync) with 16 rows of the state a warp: the accumulator of X, columns the nodes, is
-// in the layout of the next products' operand, so U never leaves registers; a block's own 16 nodes are eliminated by
-// shuffles within the 4 lanes that share rows. tcgen05's M of 128 would take S_0's terms through shared memory, 64 KiB
-// more to write and read a head, and U through TMEM and back for each block.
+// Per (sequence, value head), with T nodes, on(t) the nodes on path(t) and S_0 (dv x dk fp32) read once:
+//     X = S_0 [K; Q]^T             S_0 split into two bf16 terms (16 bits), k and q as they are (exact)
+//     R_s = beta_s v_s - beta_s e^{G_s} rk_s X_k,s          what u_s is without the nodes above it
+//     O_t = e^{G_t} rq_t X_q,t + sum_{s in on(t)} W_ts R_s
+// W is P (I + A)^-1: a node's sum over the corrections u of its path, put in terms of R. Its rows are independent of
+// one another, and the decays and norms stand outside of them: W_ts = e^{G_t-G_s} rk_s w_s, where from t upwards
+//     w_s = rq_t (q_t.k_s) - sum_{s' in on(t), s' > s} w_s' beta_s' rk_s'^2 (k_s'.k_s),
+// with the raw products of K K^T and Q K^T. So a row costs L^2 / 2 multiply-adds for a path of L nodes, by four lanes,
+// once per head; and the dv rows of the state, 16 to a warp, take no elimination of their own, just products.
 //
-// What bounds it: S_0's bytes, 64 KiB a head, up to about 16 nodes; beyond, the products and the elimination.
-// CTAs are persistent, two to an SM, and S_0 comes as quarters (32 columns) through a ring of three, the next head's
-// while this one's nodes are eliminated.
+// The products are m16n8k16 (mma.sync): their accumulator, rows of the state by nodes, is in the layout of the next
+// product's operand, so that R goes from X to O within registers. tcgen05's M of 128 would take S_0's two terms through
+// shared memory (64 KiB more to write and read a head) and R through TMEM and back.
 //
-// Values that are not finite stay on their paths: a product with a coefficient of 0 would spread them, so a block
-// whose U is not finite is eliminated again with those left out, and rows that have them on their path become NaN.
+// What bounds it: S_0's bytes, 64 KiB a head, for few nodes; for many the products, 2 dk (2 T) dv multiply-adds a head
+// at mma.sync's 1024 a cycle and SM, and the instructions around them.
+// CTAs are persistent, two or three to an SM, and S_0 comes in parts of 32 columns through a ring of three, the next
+// head's during the end of this one's work.
+//
+// Values that are not finite stay on their paths: a product with a coefficient of 0 would spread them, so they are
+// left out of the products, and the outputs that have them on their path become NaN.
 #include "kv_pages.cuh"
 #include "tree_mma.cuh"
 
@@ -26,29 +31,28 @@ template <int DK, int DV, int TP>
 struct Cfg {
     static constexpr int WARPS = DV / 16, THREADS = 32 * WARPS;
     static constexpr int NB = TP / 16, NT = TP / 8;      // blocks and tiles of nodes
-    static constexpr int NQ = DK / 32, RING = 3;         // parts of a state; slots
+    static constexpr int NQ = DK / 32, RING = TP == 16 ? 4 : 3;  // parts of a state; slots
     static constexpr uint32_t SLOT = DV * 128;
     static constexpr int BLOCKS = NB * (NB + 1) / 2;
     // byte offsets
     static constexpr uint32_t SM_KQ = 0;                                      // [2 TP][DK] bf16: K, then Q
     static constexpr uint32_t SM_S = SM_KQ + 2 * TP * DK * 2;                  // [RING][DV][32] fp32
-    static constexpr uint32_t SM_A = SM_S + RING * SLOT;                       // -A: upper terms, lower terms
-    static constexpr uint32_t SM_P = SM_A + BLOCKS * 1024;                     // P
-    static constexpr uint32_t SM_D = SM_P + BLOCKS * 1024;                     // -A of the blocks' own nodes [NB][s][t] fp32
-    static constexpr uint32_t SM_SC = SM_D + NB * 1024;                        // per node: Scalars
+    static constexpr uint32_t SM_A = SM_S + RING * SLOT;                       // K K^T, blocks of 16 x 16 fp32
+    static constexpr uint32_t SM_W = SM_A + BLOCKS * 1024;                     // Q K^T, then W, fp32, then W as two terms
+    static constexpr uint32_t SM_SC = SM_W + BLOCKS * 1024;                    // per node: Scalars
     static constexpr uint32_t SM_PATH = SM_SC + TP * 32;                       // [TP] paths
     static constexpr uint32_t SM_G = SM_PATH + TP * 8;                         // [TP] g
-    static constexpr uint32_t SM_R = SM_G + TP * 4;                            // [2 TP] inverse norms of K, Q
-    static constexpr uint32_t SM_BYTES = SM_R + 2 * TP * 4;
+    static constexpr uint32_t SM_R = SM_G + TP * 4;                            // [TP] |q|^2
+    static constexpr uint32_t SM_BYTES = SM_R + TP * 4;
     static constexpr int FIT = 233472 / (SM_BYTES + 1024), PER_SM = FIT < 3 ? FIT : 3;  // CTAs to an SM
     static_assert(PER_SM >= 2, "two CTAs to an SM");
 };
 
 struct __align__(16) Scalars {  // of a node
-    float beta, x;      // beta;  beta e^G rk, the factor of X_k
-    float z, rk;        // e^G rq, the factor of X_q;  1 / |k|
-    float rq, g, g_lo;  // 1 / |q|;  G as a sum of two
-    float pad;
+    float beta, x;   // beta;  beta e^G rk, the factor of X_k
+    float z, rk;     // e^G rq, the factor of X_q;  1 / |k|
+    float rq, b2;    // 1 / |q|;  beta rk^2
+    float g, g_lo;   // G as a sum of two
 };
 
 struct Head {
@@ -64,7 +68,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     Scalars *sc = reinterpret_cast<Scalars *>(sm + C::SM_SC);
     uint64_t *paths = reinterpret_cast<uint64_t *>(sm + C::SM_PATH);
-    float *gs = reinterpret_cast<float *>(sm + C::SM_G), *norm = reinterpret_cast<float *>(sm + C::SM_R);
+    float *gs = reinterpret_cast<float *>(sm + C::SM_G), *qq = reinterpret_cast<float *>(sm + C::SM_R);
     const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q, *k = (const __nv_bfloat16 *)a.k, *v = (const __nv_bfloat16 *)a.v;
     const __nv_bfloat16 *ga = (const __nv_bfloat16 *)a.g, *be = (const __nv_bfloat16 *)a.b;
     __nv_bfloat16 *out = (__nv_bfloat16 *)a.out;
@@ -100,147 +104,177 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
         }
         copies_commit();
     };
-    auto load_state = [&](const Head &hd, int part, int slot) {
-        if (hd.slot >= 0) {
-            const float *src = a.state_in + (hd.slot * a.Hv + hd.h) * (long)(DV * DK) + part * 32;
+    auto state_of = [&](const Head &hd) { return hd.slot >= 0 ? a.state_in + (hd.slot * a.Hv + hd.h) * (long)(DV * DK) : nullptr; };
+    auto load_state = [&](const float *state, int part, int slot) {
+        if (state != nullptr) {
+            const float *src = state + part * 32;
             for (int e = tid; e < DV * 8; e += C::THREADS)
                 copy16(sb + C::SM_S + slot * C::SLOT + state_piece(e >> 3, e & 7), src + (e >> 3) * DK + (e & 7) * 4);
         }
         copies_commit();
     };
-    // this thread's node's gate and beta logit
+    // the node of a thread of the last warps, its gate and beta logit
+    const int node = tid - (C::THREADS - TP);
     auto load_gates = [&](const Head &hd, float &gv, float &bv) {
         gv = bv = 0.f;
-        if (hd.slot >= 0 && tid < hd.nodes) {
-            gv = to_f32(ga[(hd.bos + tid) * a.Hv + hd.h]);
-            bv = to_f32(be[(hd.bos + tid) * a.Hv + hd.h]);
+        if (hd.slot >= 0 && node >= 0 && node < hd.nodes) {
+            gv = to_f32(ga[(hd.bos + node) * a.Hv + hd.h]);
+            bv = to_f32(be[(hd.bos + node) * a.Hv + hd.h]);
         }
     };
 
-    // Parts follow one another through the ring, head by head: after a part is used, the one three further on is asked
-    // for; a head's keys and queries once those of the head before are, just before the part asked for at its last.
+    // Parts follow one another through the ring, head by head. When a head's products begin, as many parts as the ring
+    // has slots are there or on their way; each slot is filled again once all warps are past it, the last one behind the
+    // next head's keys and queries.
     int next_i = blockIdx.x;
-    Head cur = find(next_i), next{0, 0, 0, 0, -1}, ahead{0, 0, 0, 0, -1};
     auto step_to = [&](const Head &from) -> Head {
         if (from.slot < 0) return from;
         next_i += gridDim.x;
         return find(next_i);
     };
-    // with one or two parts to a head, three parts ahead is up to three heads ahead
     constexpr int AHEAD = (C::RING + C::NQ - 1) / C::NQ;  // heads to know of beside the one at hand
-    static_assert(AHEAD <= 3, "heads ahead");
-    Head more{0, 0, 0, 0, -1};
-    next = step_to(cur);
-    if (AHEAD > 1) ahead = step_to(next);
-    if (AHEAD > 2) more = step_to(ahead);
-    auto head_of = [&](int d) -> const Head & { return d == 0 ? cur : d == 1 ? next : d == 2 ? ahead : more; };
-    int slot = 0;  // of the part at hand
+    static_assert(AHEAD <= 4, "heads ahead");
+    Head hd[AHEAD + 1];
+    hd[0] = find(next_i);
 #pragma unroll
-    for (int i = -C::RING; i < 0; ++i) {
-        if ((i + 1) % C::NQ == 0) {
-            if (i == -1) load_kq(cur);
-            else copies_commit();
-        }
-        load_state(head_of((i + C::RING) / C::NQ), (i + C::RING) % C::NQ, i + C::RING);
+    for (int i = 0; i < AHEAD; ++i) hd[i + 1] = step_to(hd[i]);
+#pragma unroll
+    for (int i = 0; i < C::RING; ++i) {
+        if (i == C::RING - 1) load_kq(hd[0]);
+        load_state(state_of(hd[i / C::NQ]), i % C::NQ, i);
     }
+    auto state_ahead = [&](int d) {  // of the head d ahead
+        const float *s = state_of(hd[0]);
+#pragma unroll
+        for (int i = 1; i <= AHEAD; ++i)
+            if (d == i) s = state_of(hd[i]);
+        return s;
+    };
     float gv, bv;
-    load_gates(cur, gv, bv);
-    while (cur.slot >= 0) {
+    load_gates(hd[0], gv, bv);
+    int slot = 0;  // of the part at hand
+    while (hd[0].slot >= 0) {
+        const Head &cur = hd[0];
         const int T = cur.nodes, nb = (T + 15) / 16;
-        copies_wait<1>();  // keys and queries
-        if (tid < TP) gs[tid] = gv;
-        if (warp == 0) {
+        copies_wait<1>();  // keys and queries, and the parts before the ring's last
+        __syncthreads();
+        // ---- paths, K K^T and Q K^T block by block of 16 x 16, |q|^2 --------------------------------
+        if (warp == C::WARPS - 1) {
             const Paths p = tree_paths(a.parents + cur.bos, T, a.status);
             if (lane < TP) paths[lane] = p.of(0);
             if (TP > 32) paths[lane + 32] = p.of(1);
         }
-        __syncthreads();
-        // ---- norms, gates -----------------------------------------------------------
-        for (int row = warp * 16 + (lane >> 1); row < 2 * TP; row += C::WARPS * 16) {
-            float s = 0.f;
+        if (node >= 0) gs[node] = gv;
+        for (int u = warp; u < nb * (nb + 2); u += C::WARPS) {
+            const bool square = u >= nb * (nb + 1);  // Q Q^T of a block, for its diagonal
+            const bool is_q = square || (u & 1);
+            int i = 0, j = u >> 1;  // the block's rows and columns, j <= i
+            while (j > i) j -= ++i;
+            if (square) i = j = u - nb * (nb + 1);
+            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            const int ra = (is_q ? TP : 0) + 16 * i + (lane & 15), rb = (square ? TP : 0) + 16 * j + ((lane >> 4) << 3) + (lane & 7);
 #pragma unroll
-            for (int i = 0; i < DK / 16; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(sm + C::SM_KQ + row_piece<DK>(row, (lane & 1) * (DK / 16) + i));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float lo = __uint_as_float(w[j] << 16), hi = __uint_as_float(w[j] & 0xffff0000u);
-                    s = fmaf(lo, lo, s);
-                    s = fmaf(hi, hi, s);
-                }
+            for (int ks = 0; ks < DK / 16; ++ks) {
+                uint32_t x[4], y[4];
+                load_matrices(x, sb + C::SM_KQ + row_piece<DK>(ra, 2 * ks + (lane >> 4)));
+                load_matrices(y, sb + C::SM_KQ + row_piece<DK>(rb, 2 * ks + ((lane >> 3) & 1)));
+                mma_bf16_16816(acc[0], x, y[0], y[1]);
+                mma_bf16_16816(acc[1], x, y[2], y[3]);
             }
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            if (!(lane & 1)) norm[row] = 1.f / sqrtf(s + kNormEps);
+            if (square) {
+                if (c == g >> 1) {  // this lane's columns 2 c, 2 c + 1 hold the diagonal's of rows g and g + 8
+                    qq[16 * i + g] = acc[0][g & 1];
+                    qq[16 * i + 8 + g] = acc[1][2 + (g & 1)];
+                }
+                continue;
+            }
+            uint8_t *to = sm + (is_q ? C::SM_W : C::SM_A) + coef_block(i, j);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    *reinterpret_cast<float2 *>(to + coef_piece(g + 8 * half, 2 * n + (c >> 1)) + 8 * (c & 1)) =
+                        make_float2(acc[n][2 * half], acc[n][2 * half + 1]);
         }
-        float hi = 0.f, lo = 0.f;
-        if (tid < T)
-            for (uint64_t m = paths[tid]; m; m &= m - 1) add_exact(hi, lo, gs[__ffsll((long long)m) - 1]);
         __syncthreads();
-        if (tid < TP) {
+        // ---- per node: norms, gates -------------------------------------------------------------
+        if (node >= 0) {
+            float hi = 0.f, lo = 0.f, kk = 0.f;
+            if (node < T) {
+                for (uint64_t m = paths[node]; m; m &= m - 1) add_exact(hi, lo, gs[__ffsll((long long)m) - 1]);
+                kk = reinterpret_cast<const float *>(sm + C::SM_A + coef_block(node >> 4, node >> 4) +
+                                                     coef_piece(node & 15, (node & 15) >> 2))[node & 3];
+            }
             Scalars s;
             const float eg = expf(hi + lo);
             s.beta = sigmoidf_(bv);
-            s.rk = norm[tid];
-            s.rq = norm[TP + tid];
+            s.rk = 1.f / sqrtf(kk + kNormEps);
+            s.rq = 1.f / sqrtf(qq[node] + kNormEps);
             s.x = s.beta * eg * s.rk;
             s.z = eg * s.rq;
+            s.b2 = s.beta * s.rk * s.rk;
             s.g = hi;
             s.g_lo = lo;
-            s.pad = 0.f;
-            sc[tid] = s;
+            sc[node] = s;
         }
         __syncthreads();
-        // ---- A and P: 16 rows of K or Q with all nodes before them, a warp each -----------------
-        for (int mt = warp; mt < 2 * C::NB; mt += C::WARPS) {
-            const bool is_p = mt >= C::NB;
-            const int i = is_p ? mt - C::NB : mt;
-            if (i >= nb) continue;
-            float acc[C::NT][4];
+        // ---- W, a row of it by four lanes: lane `sub` holds columns 16 j + 4 sub .. + 3 ---------------------
+        for (int t = tid >> 2; t < 16 * nb; t += C::THREADS / 4) {
+            const int sub = tid & 3;
+            uint8_t *row = sm + C::SM_W + coef_block(t >> 4, 0);
+            const uint64_t on = t < T ? paths[t] : 0;
+            const Scalars st = sc[t];
+            float w[C::NB][4];
 #pragma unroll
-            for (int n = 0; n < C::NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks) {
-                uint32_t x[4];
-                load_matrices(x, sb + C::SM_KQ + row_piece<DK>((is_p ? TP : 0) + 16 * i + (lane & 15), 2 * ks + (lane >> 4)));
-#pragma unroll
-                for (int j = 0; j < C::NB; ++j)
-                    if (j <= i) {
-                        uint32_t y[4];
-                        load_matrices(y, sb + C::SM_KQ + row_piece<DK>(16 * j + ((lane >> 4) << 3) + (lane & 7), 2 * ks + ((lane >> 3) & 1)));
-                        mma_bf16_16816(acc[2 * j], x, y[0], y[1]);
-                        mma_bf16_16816(acc[2 * j + 1], x, y[2], y[3]);
-                    }
+            for (int j = 0; j < C::NB; ++j) {
+                const float4 x = j <= t >> 4 ? *reinterpret_cast<const float4 *>(row + j * 1024 + coef_piece(t & 15, sub))
+                                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                w[j][0] = st.rq * x.x; w[j][1] = st.rq * x.y; w[j][2] = st.rq * x.z; w[j][3] = st.rq * x.w;
             }
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int tr = g + 8 * half, t = 16 * i + tr;
-                const Scalars st = sc[t];
-                uint64_t on = t < T ? paths[t] : 0;
-                if (!is_p) on &= ~(1ull << t);
-                const float f = is_p ? st.rq : -st.beta * st.rk;
+            for (int j = C::NB - 1; j >= 0; --j) {
+                uint32_t left = (uint32_t)(on >> (16 * j)) & 0xffffu;
+                // (the warp's eight rows step together, each along its own path: rows that part ways would run one by one)
+                while (__any_sync(0xffffffffu, left != 0)) {
+                    const int s = 31 - __clz(left | 1);  // of the block's nodes; w[s] is final: take it out of the columns before it
+                    const int e = s & 3;
+                    const float own = e == 0 ? w[j][0] : e == 1 ? w[j][1] : e == 2 ? w[j][2] : w[j][3];
+                    const float ws = -__shfl_sync(0xffffffffu, own, (lane & ~3) | (s >> 2)) * sc[16 * j + s].b2;
+                    if (left != 0) {
+                        left &= ~(1u << s);
+                        const uint8_t *kr = sm + C::SM_A + coef_block(j, 0) + coef_piece(s, sub);
+                        const int before = s - 4 * sub;  // columns of this lane that stand before s, in s's own block
 #pragma unroll
-                for (int n = 0; n < C::NT; ++n) {
-                    if (n > 2 * i + 1) continue;
-                    float w[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int s = 8 * n + 2 * c + e;
-                        const Scalars ss = sc[s];
-                        const float d = __expf((st.g - ss.g) + (st.g_lo - ss.g_lo));
-                        w[e] = (on >> s) & 1 ? acc[n][2 * half + e] * (f * ss.rk) * d : 0.f;
-                    }
-                    if (!is_p && n >= 2 * i) {
-                        float *dg = reinterpret_cast<float *>(sm + C::SM_D) + i * 256 + (8 * (n & 1) + 2 * c) * 16 + tr;
-                        dg[0] = w[0];
-                        dg[16] = w[1];
-                    } else {
-                        const uint32_t at = (is_p ? C::SM_P : C::SM_A) + coef_block(i, n >> 1) + coef_piece(tr, n & 1) + 4 * c;
-                        *reinterpret_cast<uint32_t *>(sm + at) = split2(w[0], w[1]);
-                        *reinterpret_cast<uint32_t *>(sm + at + C::BLOCKS * 512) = tc::bf2_bits(__floats2bfloat162_rn(w[0], w[1]));
+                        for (int i = 0; i < C::NB; ++i) {
+                            if (i > j) continue;
+                            const float4 x = *reinterpret_cast<const float4 *>(kr + i * 1024);
+                            w[i][0] = fmaf(ws, i < j || before > 0 ? x.x : 0.f, w[i][0]);
+                            w[i][1] = fmaf(ws, i < j || before > 1 ? x.y : 0.f, w[i][1]);
+                            w[i][2] = fmaf(ws, i < j || before > 2 ? x.z : 0.f, w[i][2]);
+                            w[i][3] = fmaf(ws, i < j || before > 3 ? x.w : 0.f, w[i][3]);
+                        }
                     }
                 }
+            }
+            // as two bf16 terms, in place: a row's 64 bytes of a block become 16 upper and 16 lower terms
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < C::NB; ++j) {
+                if (j > t >> 4) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int s = 16 * j + 4 * sub + e;
+                    const Scalars ss = sc[s];
+                    const float d = __expf((st.g - ss.g) + (st.g_lo - ss.g_lo)) * ss.rk;
+                    w[j][e] = (on >> s) & 1 ? w[j][e] * d : 0.f;
+                }
+                uint2 up, low;
+                up.x = split2(w[j][0], w[j][1]);
+                up.y = split2(w[j][2], w[j][3]);
+                low.x = tc::bf2_bits(__floats2bfloat162_rn(w[j][0], w[j][1]));
+                low.y = tc::bf2_bits(__floats2bfloat162_rn(w[j][2], w[j][3]));
+                *reinterpret_cast<uint2 *>(row + j * 1024 + coef_piece(t & 15, sub >> 1) + 8 * (sub & 1)) = up;
+                *reinterpret_cast<uint2 *>(row + j * 1024 + coef_piece(t & 15, 2 + (sub >> 1)) + 8 * (sub & 1)) = low;
             }
         }
         // ---- X = S_0 [K; Q]^T, and the values on their way ---------------------------------------
@@ -259,13 +293,14 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) xk[n][e] = xq[n][e] = 0.f;
-#pragma unroll
+#pragma unroll 1
         for (int part = 0; part < C::NQ; ++part) {
-            constexpr int LATE0 = 2;  // groups after this part's: the two parts after it, and keys and queries in between
-            if (C::NQ == 1) copies_wait<LATE0 + 2>();
-            else if (C::NQ == 2 || part < 2) copies_wait<LATE0 + 1>();
-            else copies_wait<LATE0>();
-            __syncthreads();
+            if (part >= C::RING - 1) copies_wait<C::RING - 2>();
+            if (part >= 1) {
+                __syncthreads();
+                const int p = part + C::RING - 1;
+                load_state(state_ahead(p / C::NQ), p % C::NQ, slot == 0 ? C::RING - 1 : slot - 1);
+            }
             const uint8_t *s0 = sm + C::SM_S + slot * C::SLOT;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
@@ -295,103 +330,69 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
                         mma_bf16_16816(xq[2 * j + 1], al, y[2], y[3]);
                     }
             }
-            __syncthreads();  // the slot, and after the last part keys and queries, may be filled again
-            if (part + 1 == C::NQ) {
-                load_kq(next);
-                load_gates(next, gv, bv);
-            }
-            load_state(head_of((part + C::RING) / C::NQ), (part + C::RING) % C::NQ, slot);
             if (++slot == C::RING) slot = 0;
         }
-        // ---- U, and O block by block --------------------------------------------------------------
-        uint64_t bad0 = 0, bad1 = 0;  // nodes whose U is not finite in this lane's rows
+        __syncthreads();  // keys, queries and the last part's slot may be filled again
+        load_kq(hd[1]);
+        load_state(state_of(hd[(C::NQ + C::RING - 1) / C::NQ]), (C::NQ + C::RING - 1) % C::NQ, slot == 0 ? C::RING - 1 : slot - 1);
+        load_gates(hd[1], gv, bv);
+        // ---- R, and O ----------------------------------------------------------------------------------
+        uint64_t bad0 = 0, bad1 = 0;  // nodes whose R is not finite in this lane's rows
+        float sure = 0.f;
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = 8 * n + 2 * c + e;
                 const Scalars st = sc[t];
-                const bool live = t < T && paths[t] != 0;
                 const float v0 = __uint_as_float(vv[n][e] << 16), v1 = __uint_as_float(vv[n][e] & 0xffff0000u);
-                xk[n][e] = live ? st.beta * v0 - st.x * xk[n][e] : 0.f;
-                xk[n][2 + e] = live ? st.beta * v1 - st.x * xk[n][2 + e] : 0.f;
+                xk[n][e] = t < T ? st.beta * v0 - st.x * xk[n][e] : 0.f;
+                xk[n][2 + e] = t < T ? st.beta * v1 - st.x * xk[n][2 + e] : 0.f;
                 xq[n][e] *= st.z;
                 xq[n][2 + e] *= st.z;
+                sure = fmaf(xk[n][e], 0.f, sure);  // 0, or NaN
+                sure = fmaf(xk[n][2 + e], 0.f, sure);
             }
+        if (__any_sync(0xffffffffu, sure != 0.f)) {
+            uint32_t m[2][2] = {{0u, 0u}, {0u, 0u}};
+#pragma unroll
+            for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!(fabsf(xk[n][e]) < INFINITY)) {
+                        xk[n][e] = 0.f;
+                        m[e >> 1][n >> 2] |= 1u << ((8 * n + 2 * c + (e & 1)) & 31);
+                    }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[e >> 1][e & 1] |= __shfl_xor_sync(0xffffffffu, m[e >> 1][e & 1], o);
+            bad0 = (uint64_t)m[0][1] << 32 | m[0][0];
+            bad1 = (uint64_t)m[1][1] << 32 | m[1][0];
+        }
 #pragma unroll
         for (int j = 0; j < C::NB; ++j) {
             if (j >= nb) continue;
-            const float *dg = reinterpret_cast<const float *>(sm + C::SM_D) + j * 256;
-            float x[2][4], sure = 0.f;
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[y][e] = xk[2 * j + y][e];
-            auto eliminate = [&](bool careful) {
-#pragma unroll
-                for (int s = 0; s < 16; ++s) {
-                    const int owner = (lane & ~3) | ((s & 7) >> 1);
-                    float u0 = __shfl_sync(0xffffffffu, x[s >> 3][s & 1], owner), u1 = __shfl_sync(0xffffffffu, x[s >> 3][2 + (s & 1)], owner);
-                    if (careful) {
-                        if (!(fabsf(u0) < INFINITY)) {
-                            bad0 |= 1ull << (16 * j + s);
-                            u0 = 0.f;
-                        }
-                        if (!(fabsf(u1) < INFINITY)) {
-                            bad1 |= 1ull << (16 * j + s);
-                            u1 = 0.f;
-                        }
-                        if (lane == owner) {
-                            x[s >> 3][s & 1] = u0;
-                            x[s >> 3][2 + (s & 1)] = u1;
-                        }
-                    }
-#pragma unroll
-                    for (int y = s >> 3; y < 2; ++y) {
-                        const float2 w = *reinterpret_cast<const float2 *>(dg + s * 16 + 8 * y + 2 * c);
-                        x[y][0] = fmaf(w.x, u0, x[y][0]);
-                        x[y][1] = fmaf(w.y, u0, x[y][1]);
-                        x[y][2] = fmaf(w.x, u1, x[y][2]);
-                        x[y][3] = fmaf(w.y, u1, x[y][3]);
-                    }
-                }
-            };
-            eliminate(false);
-#pragma unroll
-            for (int y = 0; y < 2; ++y)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sure = fmaf(x[y][e], 0.f, sure);  // 0, or NaN
-            if (__any_sync(0xffffffffu, sure != 0.f)) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[y][e] = xk[2 * j + y][e];
-                eliminate(true);
-            }
             uint32_t uh[4], ul[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float lo0 = x[e >> 1][2 * (e & 1)], lo1 = x[e >> 1][2 * (e & 1) + 1];
-                uh[e] = split2(lo0, lo1);
-                ul[e] = tc::bf2_bits(__floats2bfloat162_rn(lo0, lo1));
+                float x = xk[2 * j + (e >> 1)][2 * (e & 1)], y = xk[2 * j + (e >> 1)][2 * (e & 1) + 1];
+                uh[e] = split2(x, y);
+                ul[e] = tc::bf2_bits(__floats2bfloat162_rn(x, y));
             }
-            const uint32_t at = sb + coef_piece(((lane >> 4) << 3) + (lane & 7), (lane >> 3) & 1);
+            const int tr = ((lane >> 4) << 3) + (lane & 7), ch = (lane >> 3) & 1;
 #pragma unroll
             for (int i = j; i < C::NB; ++i) {
                 if (i >= nb) continue;
                 uint32_t y[4];
-                auto products = [&](float (&d0)[4], float (&d1)[4], uint32_t from) {
-                    load_matrices(y, at + from + coef_block(i, j));
-                    mma_bf16_16816(d0, uh, y[0], y[1]);
-                    mma_bf16_16816(d1, uh, y[2], y[3]);
-                    mma_bf16_16816(d0, ul, y[0], y[1]);
-                    mma_bf16_16816(d1, ul, y[2], y[3]);
-                    load_matrices(y, at + from + C::BLOCKS * 512 + coef_block(i, j));
-                    mma_bf16_16816(d0, uh, y[0], y[1]);
-                    mma_bf16_16816(d1, uh, y[2], y[3]);
-                };
-                if (i > j) products(xk[2 * i], xk[2 * i + 1], C::SM_A);
-                products(xq[2 * i], xq[2 * i + 1], C::SM_P);
+                load_matrices(y, sb + C::SM_W + coef_block(i, j) + coef_piece(tr, ch));
+                mma_bf16_16816(xq[2 * i], uh, y[0], y[1]);
+                mma_bf16_16816(xq[2 * i + 1], uh, y[2], y[3]);
+                mma_bf16_16816(xq[2 * i], ul, y[0], y[1]);
+                mma_bf16_16816(xq[2 * i + 1], ul, y[2], y[3]);
+                load_matrices(y, sb + C::SM_W + coef_block(i, j) + coef_piece(tr, 2 + ch));
+                mma_bf16_16816(xq[2 * i], uh, y[0], y[1]);
+                mma_bf16_16816(xq[2 * i + 1], uh, y[2], y[3]);
             }
         }
         // ---- rows out -----------------------------------------------------------------------------
@@ -409,17 +410,9 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
                 }
                 *reinterpret_cast<uint32_t *>(out + vat + (long)t * a.Hv * DV) = tc::bf2_bits(__floats2bfloat162_rn(o0, o1));
             }
-        __syncthreads();  // paths, scalars and coefficients have been read
-        cur = next;
-        next = ahead;
-        if (AHEAD == 1) {
-            next = step_to(cur);
-        } else if (AHEAD == 2) {
-            ahead = step_to(next);
-        } else {
-            ahead = more;
-            more = step_to(ahead);
-        }
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) hd[i] = hd[i + 1];
+        hd[AHEAD] = step_to(hd[AHEAD - 1]);
     }
     copies_wait<0>();
 }

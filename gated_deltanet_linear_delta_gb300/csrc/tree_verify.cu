@@ -19,6 +19,7 @@
 namespace gdn {
 namespace {
 
+constexpr int kVerFlight = 4;  // loads of 16 bytes of a row in flight per lane
 constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32, kVerCluster = 8, kVerParts = kVerWarps * kVerCluster;
 constexpr int kVerSteps = kVerMaxVocab / 4 / kVerParts / 32 + 2;  // of 32 groups of 4, per warp
 static_assert(kVerParts == 64, "a lane holds two warps' sums");
@@ -50,12 +51,15 @@ __device__ __forceinline__ double warp_scan_f64(double x) {  // inclusive
     return x;
 }
 
-struct Two {  // hi + lo
-    float hi, lo;
+// Values of two elements at a time, as hi + lo each: one packed operation serves both.
+struct Two {
+    F2 hi, lo;
 };
-__device__ __forceinline__ void add(Two &a, float hi, float lo) {
-    const float s = a.hi + hi, y = s - a.hi;
-    a.lo += ((a.hi - (s - y)) + (hi - y)) + lo;
+__device__ __forceinline__ F2 less(F2 a, F2 b) { return f2_fma(b, f2(-1.f, -1.f), a); }  // a - b, rounded once
+__device__ __forceinline__ void add(Two &a, const Two &b) {
+    const F2 s = f2_add(a.hi, b.hi), y = less(s, a.hi);
+    const F2 e = f2_add(less(a.hi, less(s, y)), less(b.hi, y));  // what the rounding of s lost
+    a.lo = f2_add(a.lo, f2_add(e, b.lo));
     a.hi = s;
 }
 
@@ -97,16 +101,26 @@ struct Row {
             }
         }
     }
-    __device__ __forceinline__ Two weight(float x, float y, int e) const {
+    // of elements e and e + 1
+    __device__ __forceinline__ Two weights(float x0, float x1, float y0, float y1, int e) const {
         if (ch != 0.f) {
-            const float ph = ch * y, pl = fmaf(cl, y, fmaf(ch, y, -ph));
-            const float s = x - ph, z = s - x;
-            const float lo = ((x - (s - z)) - (ph + z)) - pl;
-            return s + lo <= 0.f ? Two{0.f, 0.f} : Two{s, lo};
+            const F2 x = f2(x0, x1), y = f2(y0, y1);
+            const F2 mh = f2_mul(f2(-ch, -ch), y);  // -c y = mh + ml
+            const F2 ml = f2_fma(f2(-cl, -cl), y, f2_fma(f2(-ch, -ch), y, f2_mul(mh, f2(-1.f, -1.f))));
+            const F2 s = f2_add(x, mh), z = less(x, s);  // x + mh and what that lost
+            const F2 lo = f2_add(f2_add(less(x, f2_add(s, z)), f2_add(z, mh)), ml);
+            float h0, h1, l0, l1;
+            f2_get(s, h0, h1);
+            f2_get(lo, l0, l1);
+            if (h0 + l0 <= 0.f) h0 = l0 = 0.f;
+            if (h1 + l1 <= 0.f) h1 = l1 = 0.f;
+            return Two{f2(h0, h1), f2(l0, l1)};
         }
-        for (int i = 0; i < ngone; ++i)
-            if (gone[i] == e) x = 0.f;
-        return Two{x, 0.f};
+        for (int i = 0; i < ngone; ++i) {
+            if (gone[i] == e) x0 = 0.f;
+            if (gone[i] == e + 1) x1 = 0.f;
+        }
+        return Two{f2(x0, x1), f2(0.f, 0.f)};
     }
 };
 
@@ -177,17 +191,31 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
             for (int i = 0; i < ngone; ++i)
                 if (sm.gone[i] >= e0 && sm.gone[i] < e1) row.ngone = ngone;
         }
-        Two acc{0.f, 0.f};
-        for (int j = g0 + lane; j < g1; j += 32) {
-            float x[4], y[4];
-            row.load(j, x, y);
+        Two acc[2] = {{f2(0.f, 0.f), f2(0.f, 0.f)}, {f2(0.f, 0.f), f2(0.f, 0.f)}};
+        for (int j = g0 + lane; j < g1; j += 32 * kVerFlight) {
+            float x[kVerFlight][4], y[kVerFlight][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Two v = row.weight(x[i], y[i], row.first(j) + i);
-                add(acc, v.hi, v.lo);
+            for (int f = 0; f < kVerFlight; ++f) {
+                if (j + 32 * f < g1) row.load(j + 32 * f, x[f], y[f]);
+                else x[f][0] = x[f][1] = x[f][2] = x[f][3] = y[f][0] = y[f][1] = y[f][2] = y[f][3] = 0.f;
+            }
+#pragma unroll
+            for (int f = 0; f < kVerFlight; ++f) {
+                const int e = row.first(j + 32 * f);
+                add(acc[0], row.weights(x[f][0], x[f][1], y[f][0], y[f][1], e));
+                add(acc[1], row.weights(x[f][2], x[f][3], y[f][2], y[f][3], e + 2));
             }
         }
-        const double mine = warp_sum_f64((double)acc.hi + (double)acc.lo);
+        float h[4], l[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f2_get(acc[i].hi, h[2 * i], h[2 * i + 1]);
+            f2_get(acc[i].lo, l[2 * i], l[2 * i + 1]);
+        }
+        double mine = 0.;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine += (double)h[i] + (double)l[i];
+        mine = warp_sum_f64(mine);
         double *part = sm.part[pass & 1];
         ++pass;
         if (lane < kVerCluster) store_remote(part + w, (uint32_t)lane, mine);
@@ -276,9 +304,13 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
         if (j < g1) {
             row.load(j, x, y);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Two v = row.weight(x[i], y[i], row.first(j) + i);
-                w[i] = (double)v.hi + (double)v.lo;
+            for (int i = 0; i < 4; i += 2) {
+                const Two v = row.weights(x[i], x[i + 1], y[i], y[i + 1], row.first(j) + i);
+                float h0, h1, l0, l1;
+                f2_get(v.hi, h0, h1);
+                f2_get(v.lo, l0, l1);
+                w[i] = (double)h0 + (double)l0;
+                w[i + 1] = (double)h1 + (double)l1;
             }
         } else {
             w[0] = w[1] = w[2] = w[3] = 0.;
