@@ -7,19 +7,20 @@
 // next token from what is left, costs one pass over the two rows. Without draft probabilities q is one at the child's
 // token: a rejection takes that token out and needs no pass.
 //
-// What bounds it: a row or two of V fp32 per sequence. A cluster of CTAs takes a sequence, each a run of the row, each
-// warp a part of that; what a pass finds is exchanged through distributed shared memory, and all CTAs take the same
-// decisions. Everything that the walk itself looks at is fetched at once beforehand.
+// What bounds it: a row or two of V fp32 per sequence, and for few sequences the chain of dependent steps (the tree, the
+// tokens' probabilities, a pass, the draw). A cluster of CTAs takes a sequence, each a run of the row, each warp a part
+// of that; what a pass finds is exchanged through distributed shared memory, and all CTAs take the same decisions.
+// Everything that the walk itself looks at is fetched at once beforehand.
 //
-// Precision. A draw compares r times a sum with partial sums over V values that lie close to one another, so sums and
-// weights are kept in two floats each (48 bits), which costs fp32 operations only; fp64 ones are few.
+// Precision. A draw compares r times a sum with partial sums over V values that lie close to one another, so weights
+// and sums are kept as two floats each (48 bits). In fp64, of which an SM does two operations a cycle, the sums over the
+// warps alone kept its unit busy for a third of the time.
 #include "kv_pages.cuh"
 #include "tree.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kVerFlight = 4;  // loads of 16 bytes of a row in flight per lane
 constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32, kVerCluster = 8, kVerParts = kVerWarps * kVerCluster;
 constexpr int kVerSteps = kVerMaxVocab / 4 / kVerParts / 32 + 2;  // of 32 groups of 4, per warp
 static_assert(kVerParts == 64, "a lane holds two warps' sums");
@@ -32,26 +33,48 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_meet() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void store_remote(double *at, uint32_t rank, double x) {
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(at)), "r"(rank));
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(x) : "memory");
+
+// ---- numbers of 48 bits: hi + lo, |lo| at most half a unit of hi -----------------------
+struct Wide {
+    float hi, lo;
+};
+__device__ __forceinline__ Wide wide(float x) { return Wide{x, 0.f}; }
+__device__ __forceinline__ Wide plus(Wide a, Wide b) {
+    const float s = a.hi + b.hi, y = s - a.hi;
+    const float e = ((a.hi - (s - y)) + (b.hi - y)) + (a.lo + b.lo);
+    const float h = s + e;
+    return Wide{h, e - (h - s)};
 }
-__device__ __forceinline__ double warp_sum_f64(double x) {
+__device__ __forceinline__ Wide minus(Wide a, Wide b) { return plus(a, Wide{-b.hi, -b.lo}); }
+__device__ __forceinline__ Wide times(Wide a, float f) {
+    const float p = a.hi * f, e = fmaf(a.lo, f, fmaf(a.hi, f, -p)), h = p + e;
+    return Wide{h, e - (h - p)};
+}
+__device__ __forceinline__ bool below(Wide a, Wide b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+__device__ __forceinline__ Wide shuffle(Wide a, int from) {
+    return Wide{__shfl_sync(0xffffffffu, a.hi, from), __shfl_sync(0xffffffffu, a.lo, from)};
+}
+__device__ __forceinline__ Wide warp_total(Wide a) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+    for (int o = 16; o > 0; o >>= 1)
+        a = plus(a, Wide{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
+    return a;
 }
-__device__ __forceinline__ double warp_scan_f64(double x) {  // inclusive
+__device__ __forceinline__ Wide warp_scan(Wide a) {  // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, o);
-        if ((int)(threadIdx.x & 31) >= o) x += y;
+        const Wide b{__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+        if ((int)(threadIdx.x & 31) >= o) a = plus(b, a);
     }
-    return x;
+    return a;
+}
+__device__ __forceinline__ void store_remote(Wide *at, uint32_t rank, Wide x) {
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(at)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(x.hi), "f"(x.lo) : "memory");
 }
 
-// Values of two elements at a time, as hi + lo each: one packed operation serves both.
+// Two such numbers side by side, without the last step that brings them into shape: one packed operation serves both.
 struct Two {
     F2 hi, lo;
 };
@@ -62,29 +85,37 @@ __device__ __forceinline__ void add(Two &a, const Two &b) {
     a.lo = f2_add(a.lo, f2_add(e, b.lo));
     a.hi = s;
 }
+__device__ __forceinline__ void get(const Two &a, Wide &x, Wide &y) {
+    float h0, h1, l0, l1;
+    f2_get(a.hi, h0, h1);
+    f2_get(a.lo, l0, l1);
+    x = plus(wide(h0), wide(l0));
+    y = plus(wide(h1), wide(l1));
+}
 
 struct VerSmem {
-    double part[2][kVerParts];  // a pass's sums by warp, two passes' by turns
-    double step[kVerSteps];
+    Wide part[2][kVerParts];  // a pass's sums by warp, two passes' by turns
+    Wide step[kVerSteps];
     int up[kTreeMax], token[kTreeMax], gone[kTreeMax], path[kTreeMax];
     float p[kTreeMax], q[kTreeMax], r[kTreeMax];
 };
 
-// The weights of a node's row: max(p - c q, 0), or p without the tokens that are gone.
+// The weights of a node's row: max(p - c q, 0) (DRAFT), or p without the tokens that are gone.
+template <bool DRAFT>
 struct Row {
     const float *p, *q;
-    int V, head;      // elements before p's first 16-byte boundary: group 0; group j > 0 has the 4 from head + 4 (j - 1)
-    bool same;        // q's boundaries are p's
-    float ch, cl;     // c
+    int V, head;   // elements before p's first 16-byte boundary: group 0; group j > 0 has the 4 from head + 4 (j - 1)
+    bool same;     // q's boundaries are p's
+    Wide c;
     const int *gone;
-    int ngone;        // (as far as they concern the warp at hand)
+    int ngone;     // (as far as they concern the warp at hand)
     __device__ __forceinline__ int first(int j) const { return j == 0 ? 0 : head + 4 * (j - 1); }
     __device__ __forceinline__ void load(int j, float (&x)[4], float (&y)[4]) const {
         const int e = first(j), n = j == 0 ? head : V - e;
         if (j > 0 && n >= 4) {
             const float4 a = __ldg(reinterpret_cast<const float4 *>(p + e));
             x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            if (ch != 0.f) {
+            if (DRAFT && c.hi != 0.f) {
                 if (same) {
                     const float4 b = __ldg(reinterpret_cast<const float4 *>(q + e));
                     y[0] = b.x; y[1] = b.y; y[2] = b.z; y[3] = b.w;
@@ -97,37 +128,43 @@ struct Row {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[i] = i < n ? __ldg(p + e + i) : 0.f;
-                y[i] = i < n && ch != 0.f ? __ldg(q + e + i) : 0.f;
+                y[i] = DRAFT && i < n && c.hi != 0.f ? __ldg(q + e + i) : 0.f;
             }
         }
     }
     // of elements e and e + 1
     __device__ __forceinline__ Two weights(float x0, float x1, float y0, float y1, int e) const {
-        if (ch != 0.f) {
-            const F2 x = f2(x0, x1), y = f2(y0, y1);
-            const F2 mh = f2_mul(f2(-ch, -ch), y);  // -c y = mh + ml
-            const F2 ml = f2_fma(f2(-cl, -cl), y, f2_fma(f2(-ch, -ch), y, f2_mul(mh, f2(-1.f, -1.f))));
-            const F2 s = f2_add(x, mh), z = less(x, s);  // x + mh and what that lost
-            const F2 lo = f2_add(f2_add(less(x, f2_add(s, z)), f2_add(z, mh)), ml);
-            float h0, h1, l0, l1;
-            f2_get(s, h0, h1);
-            f2_get(lo, l0, l1);
-            if (h0 + l0 <= 0.f) h0 = l0 = 0.f;
-            if (h1 + l1 <= 0.f) h1 = l1 = 0.f;
-            return Two{f2(h0, h1), f2(l0, l1)};
-        }
-        for (int i = 0; i < ngone; ++i) {
-            if (gone[i] == e) x0 = 0.f;
-            if (gone[i] == e + 1) x1 = 0.f;
+        if constexpr (DRAFT) {
+            if (c.hi != 0.f) {
+                const F2 x = f2(x0, x1), y = f2(y0, y1);
+                const F2 mh = f2_mul(f2(-c.hi, -c.hi), y);  // -c y = mh + ml
+                const F2 ml = f2_fma(f2(-c.lo, -c.lo), y, f2_fma(f2(-c.hi, -c.hi), y, f2_mul(mh, f2(-1.f, -1.f))));
+                const F2 s = f2_add(x, mh), z = less(x, s);  // x + mh and what that lost
+                const F2 lo = f2_add(f2_add(less(x, f2_add(s, z)), f2_add(z, mh)), ml);
+                float h0, h1, l0, l1;
+                f2_get(s, h0, h1);
+                f2_get(lo, l0, l1);
+                if (h0 + l0 <= 0.f) h0 = l0 = 0.f;
+                if (h1 + l1 <= 0.f) h1 = l1 = 0.f;
+                return Two{f2(h0, h1), f2(l0, l1)};
+            }
+        } else {
+            for (int i = 0; i < ngone; ++i) {
+                if (gone[i] == e) x0 = 0.f;
+                if (gone[i] == e + 1) x1 = 0.f;
+            }
         }
         return Two{f2(x0, x1), f2(0.f, 0.f)};
     }
 };
 
+template <bool DRAFT>
 __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyArgs a) {
+    constexpr int kFlight = DRAFT ? 4 : 8;  // groups of a row in flight per lane
     __shared__ VerSmem sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockIdx.x / kVerCluster;
     const uint32_t rank = cluster_rank();
+    next_may_begin();
     before_reading();
     long bos = 0;
     int nodes = 0;
@@ -137,9 +174,32 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
         nodes = 0;
     }
     int32_t *path = a.path + (long)n * a.path_stride;
-    const int root = nodes > 0 ? a.parents[bos] : -2;
-    if (root != -1) {  // nothing to walk from: an idle row
-        if (root >= 0) flag_error(a.status);
+    // (all that a node's thread can fetch without knowing more)
+    int up = -2, x = 0;
+    float rn = 0.f;
+    if (tid < nodes) {
+        up = a.parents[bos + tid];
+        if (tid > 0) {
+            x = a.tokens[bos + tid];
+            rn = a.r[bos + tid];
+        }
+    }
+    const float r_last = a.r_last[n];
+    if (tid < nodes) {
+        bool child = tid > 0 && up >= 0;
+        if (tid == 0 ? up >= 0 : child && (up >= tid || x < 0 || x >= a.V)) {
+            flag_error(a.status);
+            child = false;
+        }
+        sm.up[tid] = tid == 0 ? up : child ? up : -2;
+        sm.token[tid] = x;
+        sm.r[tid] = rn;
+        sm.p[tid] = child ? a.target[(bos + up) * a.target_stride + x] : 0.f;
+        sm.q[tid] = DRAFT && child ? a.draft[(bos + up) * a.draft_stride + x] : 1.f;
+        if (tid == 0) sm.path[0] = 0;
+    }
+    cluster_meet();  // (and the CTA)
+    if (nodes == 0 || sm.up[0] != -1) {  // nothing to walk from: an idle row
         if (rank == 0) {
             for (int i = tid; i < a.path_stride; i += kVerThreads) path[i] = -1;
             if (tid == 0) {
@@ -149,81 +209,58 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
         }
         return;
     }
-    if (tid < nodes) {
-        const int up = tid == 0 ? -1 : a.parents[bos + tid], x = tid == 0 ? 0 : a.tokens[bos + tid];
-        bool child = up >= 0;
-        if (child && (up >= tid || x < 0 || x >= a.V)) {
-            flag_error(a.status);
-            child = false;
-        }
-        sm.up[tid] = child ? up : -2;
-        sm.token[tid] = x;
-        sm.r[tid] = child ? a.r[bos + tid] : 0.f;
-        sm.p[tid] = child ? a.target[(bos + up) * a.target_stride + x] : 0.f;
-        sm.q[tid] = child && a.draft ? a.draft[(bos + up) * a.draft_stride + x] : 1.f;
-        if (tid == 0) sm.path[0] = 0;
-    }
-    cluster_meet();  // (and the CTA)
     int cur = 0, count = 1, ngone = 0, pass = 0;
-    double c = 0., Z = 1.;
-    Row row;
-    row.p = row.q = nullptr;
-    int g0 = 0, g1 = 0;         // this warp's groups
-    double below0, below1;      // lane: the sums of warps 0 .. 2 lane, .. 2 lane + 1
+    Wide c = wide(0.f), Z = wide(1.f);
+    Row<DRAFT> row;
+    int g0 = 0, g1 = 0;        // this warp's groups
+    Wide below0, below1;       // lane: the sums of parts 0 .. 2 lane, .. 2 lane + 1
     // Sums the current node's weights; the same result in every thread of the cluster.
-    auto sum_row = [&]() -> double {
+    auto sum_row = [&]() -> Wide {
         row.p = a.target + (bos + cur) * a.target_stride;
-        row.q = a.draft ? a.draft + (bos + cur) * a.draft_stride : nullptr;
+        row.q = DRAFT ? a.draft + (bos + cur) * a.draft_stride : nullptr;
         row.V = a.V;
-        const int off = (int)((reinterpret_cast<uintptr_t>(row.p) >> 2) & 3);
-        row.head = min((4 - off) & 3, a.V);
-        row.same = (((reinterpret_cast<uintptr_t>(row.p) ^ reinterpret_cast<uintptr_t>(row.q)) & 15) == 0);
-        row.ch = (float)c;
-        row.cl = (float)(c - (double)row.ch);
+        row.head = min((int)(-(reinterpret_cast<uintptr_t>(row.p) >> 2) & 3), a.V);
+        row.same = ((reinterpret_cast<uintptr_t>(row.p) ^ reinterpret_cast<uintptr_t>(row.q)) & 15) == 0;
+        row.c = c;
         row.gone = sm.gone;
         const int groups = 1 + (a.V - row.head + 3) / 4, per = (groups + kVerParts - 1) / kVerParts;
         const int w = (int)rank * kVerWarps + warp;
         g0 = min(w * per, groups);
         g1 = min(g0 + per, groups);
         row.ngone = 0;
-        if (ngone > 0) {
+        if (!DRAFT && ngone > 0) {
             const int e0 = row.first(g0), e1 = row.first(g1);
             for (int i = 0; i < ngone; ++i)
                 if (sm.gone[i] >= e0 && sm.gone[i] < e1) row.ngone = ngone;
         }
         Two acc[2] = {{f2(0.f, 0.f), f2(0.f, 0.f)}, {f2(0.f, 0.f), f2(0.f, 0.f)}};
-        for (int j = g0 + lane; j < g1; j += 32 * kVerFlight) {
-            float x[kVerFlight][4], y[kVerFlight][4];
+        for (int j = g0 + lane; j < g1; j += 32 * kFlight) {
+            float x[kFlight][4], y[kFlight][4];
 #pragma unroll
-            for (int f = 0; f < kVerFlight; ++f) {
+            for (int f = 0; f < kFlight; ++f) {
                 if (j + 32 * f < g1) row.load(j + 32 * f, x[f], y[f]);
                 else x[f][0] = x[f][1] = x[f][2] = x[f][3] = y[f][0] = y[f][1] = y[f][2] = y[f][3] = 0.f;
             }
 #pragma unroll
-            for (int f = 0; f < kVerFlight; ++f) {
+            for (int f = 0; f < kFlight; ++f) {
                 const int e = row.first(j + 32 * f);
                 add(acc[0], row.weights(x[f][0], x[f][1], y[f][0], y[f][1], e));
                 add(acc[1], row.weights(x[f][2], x[f][3], y[f][2], y[f][3], e + 2));
             }
         }
-        float h[4], l[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            f2_get(acc[i].hi, h[2 * i], h[2 * i + 1]);
-            f2_get(acc[i].lo, l[2 * i], l[2 * i + 1]);
-        }
-        double mine = 0.;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mine += (double)h[i] + (double)l[i];
-        mine = warp_sum_f64(mine);
-        double *part = sm.part[pass & 1];
+        Wide s0, s1, s2, s3;
+        get(acc[0], s0, s1);
+        get(acc[1], s2, s3);
+        const Wide mine = warp_total(plus(plus(s0, s1), plus(s2, s3)));
+        Wide *part = sm.part[pass & 1];
         ++pass;
         if (lane < kVerCluster) store_remote(part + w, (uint32_t)lane, mine);
         cluster_meet();
-        const double x0 = part[2 * lane], x1 = part[2 * lane + 1];
-        below1 = warp_scan_f64(x0 + x1);
-        below0 = below1 - x1;
-        return __shfl_sync(0xffffffffu, below1, 31);
+        const Wide x1 = part[2 * lane + 1];
+        const Wide two = plus(part[2 * lane], x1);
+        below1 = warp_scan(two);
+        below0 = plus(below1, Wide{-x1.hi, -x1.lo});
+        return shuffle(below1, 31);
     };
     bool stale = false;  // Z is not yet known
     for (int t = 1; t < nodes; ++t) {  // children come after their parents, so one walk over the nodes meets them in turn
@@ -233,112 +270,106 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
             stale = false;
         }
         const int x = sm.token[t];
-        const double p = (double)sm.p[t], q = (double)sm.q[t];
-        double w = p;
-        if (a.draft) {
-            w = p - c * q;
-            if (w < 0.) w = 0.;
+        const float p = sm.p[t], q = sm.q[t];
+        Wide w = wide(p);
+        if (DRAFT) {
+            w = minus(w, times(c, q));
+            if (w.hi < 0.f) w = wide(0.f);
         } else {
             for (int i = 0; i < ngone; ++i)
-                if (sm.gone[i] == x) w = 0.;
+                if (sm.gone[i] == x) w = wide(0.f);
         }
-        if ((double)sm.r[t] * Z * q < w) {
+        if (below(times(times(Z, q), sm.r[t]), w)) {
             cur = t;
             if (tid == 0) sm.path[count] = t;
             ++count;
-            c = 0.;
-            Z = 1.;
-            __syncthreads();  // (gone is read until here)
+            c = wide(0.f);
+            Z = wide(1.f);
+            if (!DRAFT) __syncthreads();  // (gone is read until here)
             ngone = 0;
-        } else if (a.draft) {
-            c += Z;
+        } else if (DRAFT) {
+            c = plus(c, Z);
             stale = true;
         } else {
-            Z -= w;
+            Z = minus(Z, w);
             __syncthreads();
             if (tid == 0) sm.gone[ngone] = x;
             ++ngone;
             __syncthreads();
         }
     }
-    double total = sum_row();
-    if (!(total > 0.) && (c > 0. || ngone > 0)) {  // nothing is left of it: from p
-        c = 0.;
+    Wide total = sum_row();
+    if (!(total.hi > 0.f) && (c.hi > 0.f || ngone > 0)) {  // nothing is left of it: from p
+        c = wide(0.f);
         ngone = 0;
         total = sum_row();
     }
     if (rank == 0)
         for (int i = tid; i < a.path_stride; i += kVerThreads) path[i] = i < count ? sm.path[i] : -1;
     if (rank == 0 && tid == 0) a.counts[n] = count;
-    if (!(total > 0. && total < (double)INFINITY)) {
+    if (!(total.hi > 0.f && total.hi < INFINITY)) {
         flag_error(a.status);
         if (rank == 0 && tid == 0) a.next[n] = -1;
         return;
     }
     // the part that holds the draw: the first whose end is above it, or else the last that has weight
-    const double draw = (double)a.r_last[n] * total;
-    const double below = __shfl_up_sync(0xffffffffu, below1, 1), start = lane == 0 ? 0. : below;
-    unsigned at0 = __ballot_sync(0xffffffffu, below0 > draw && below0 > start);
-    unsigned at1 = __ballot_sync(0xffffffffu, below1 > draw && below1 > below0);
+    const Wide draw = times(total, r_last);
+    Wide start{__shfl_up_sync(0xffffffffu, below1.hi, 1), __shfl_up_sync(0xffffffffu, below1.lo, 1)};
+    if (lane == 0) start = wide(0.f);
+    const bool some0 = sm.part[(pass - 1) & 1][2 * lane].hi > 0.f, some1 = sm.part[(pass - 1) & 1][2 * lane + 1].hi > 0.f;
+    unsigned at0 = __ballot_sync(0xffffffffu, some0 && below(draw, below0));
+    unsigned at1 = __ballot_sync(0xffffffffu, some1 && below(draw, below1));
     int owner;
     if (at0 | at1) {
         const int l0 = at0 ? __ffs(at0) - 1 : 64, l1 = at1 ? __ffs(at1) - 1 : 64;
         owner = l0 <= l1 ? 2 * l0 : 2 * l1 + 1;
     } else {
-        at0 = __ballot_sync(0xffffffffu, below0 > start);
-        at1 = __ballot_sync(0xffffffffu, below1 > below0);
+        at0 = __ballot_sync(0xffffffffu, some0);
+        at1 = __ballot_sync(0xffffffffu, some1);
         const int l0 = at0 ? 31 - __clz(at0) : -1, l1 = at1 ? 31 - __clz(at1) : -1;
         owner = l1 >= l0 ? 2 * l1 + 1 : 2 * l0;
     }
     if (owner / kVerWarps != (int)rank) return;
-    const double s0 = __shfl_sync(0xffffffffu, start, owner >> 1), s1 = __shfl_sync(0xffffffffu, below0, owner >> 1);
-    const double before = owner & 1 ? s1 : s0;
+    Wide base = owner & 1 ? shuffle(below0, owner >> 1) : shuffle(start, owner >> 1);
     // its steps of 128 elements, by all warps; then the step, by one
     const int groups = 1 + (a.V - row.head + 3) / 4, per = (groups + kVerParts - 1) / kVerParts;
     g0 = min(owner * per, groups);
     g1 = min(g0 + per, groups);
     row.ngone = ngone;
     const int steps = (g1 - g0 + 31) / 32;
-    auto group_weights = [&](int j, double (&w)[4]) -> double {
+    auto group_weights = [&](int j, Wide (&w)[4]) -> Wide {
         float x[4], y[4];
         if (j < g1) {
             row.load(j, x, y);
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                const Two v = row.weights(x[i], x[i + 1], y[i], y[i + 1], row.first(j) + i);
-                float h0, h1, l0, l1;
-                f2_get(v.hi, h0, h1);
-                f2_get(v.lo, l0, l1);
-                w[i] = (double)h0 + (double)l0;
-                w[i + 1] = (double)h1 + (double)l1;
-            }
+            get(row.weights(x[0], x[1], y[0], y[1], row.first(j)), w[0], w[1]);
+            get(row.weights(x[2], x[3], y[2], y[3], row.first(j) + 2), w[2], w[3]);
         } else {
-            w[0] = w[1] = w[2] = w[3] = 0.;
+            w[0] = w[1] = w[2] = w[3] = wide(0.f);
         }
-        return (w[0] + w[1]) + (w[2] + w[3]);
+        return plus(plus(w[0], w[1]), plus(w[2], w[3]));
     };
     for (int s = warp; s < steps; s += kVerWarps) {
-        double w[4];
-        const double x = warp_sum_f64(group_weights(g0 + 32 * s + lane, w));
+        Wide w[4];
+        const Wide x = warp_total(group_weights(g0 + 32 * s + lane, w));
         if (lane == 0) sm.step[s] = x;
     }
     __syncthreads();
     if (warp != 0) return;
-    double base = before, step_base = before;
     int step = -1, fallback = -1;
-    double fallback_base = before;
+    Wide step_base = base, fallback_base = base;
     for (int s = 0; s < steps && step < 0; s += 32) {
-        const double x = s + lane < steps ? sm.step[s + lane] : 0.;
-        const double end = base + warp_scan_f64(x);
-        const unsigned hit = __ballot_sync(0xffffffffu, x > 0. && end > draw), some = __ballot_sync(0xffffffffu, x > 0.);
+        const Wide x = s + lane < steps ? sm.step[s + lane] : wide(0.f);
+        const Wide end = plus(base, warp_scan(x));
+        const unsigned hit = __ballot_sync(0xffffffffu, x.hi > 0.f && below(draw, end)), some = __ballot_sync(0xffffffffu, x.hi > 0.f);
+        const Wide begin = minus(end, x);
         if (hit) {
             step = s + __ffs(hit) - 1;
-            step_base = __shfl_sync(0xffffffffu, end - x, __ffs(hit) - 1);
+            step_base = shuffle(begin, __ffs(hit) - 1);
         } else if (some) {
             fallback = s + 31 - __clz(some);
-            fallback_base = __shfl_sync(0xffffffffu, end - x, 31 - __clz(some));
+            fallback_base = shuffle(begin, 31 - __clz(some));
         }
-        base = __shfl_sync(0xffffffffu, end, 31);
+        base = shuffle(end, 31);
     }
     if (step < 0) {
         step = fallback;
@@ -351,17 +382,17 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
         }
         return;
     }
-    double w[4];
+    Wide w[4];
     const int j = g0 + 32 * step + lane;
-    const double x = group_weights(j, w), end = step_base + warp_scan_f64(x);
-    double sum = end - x;
+    const Wide x_all = group_weights(j, w);
+    Wide sum = minus(plus(step_base, warp_scan(x_all)), x_all);
     int pick = -1, last = -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        sum += w[i];
-        if (w[i] > 0.) {
+        sum = plus(sum, w[i]);
+        if (w[i].hi > 0.f) {
             last = row.first(j) + i;
-            if (pick < 0 && sum > draw) pick = last;
+            if (pick < 0 && below(draw, sum)) pick = last;
         }
     }
     const unsigned hit = __ballot_sync(0xffffffffu, pick >= 0), some = __ballot_sync(0xffffffffu, last >= 0);
@@ -385,7 +416,7 @@ cudaError_t launch_tree_verify(const VerifyArgs &a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, tree_verify_kernel, a);
+    return cudaLaunchKernelEx(&cfg, a.draft ? tree_verify_kernel<true> : tree_verify_kernel<false>, a);
 }
 
 }  // namespace gdn
