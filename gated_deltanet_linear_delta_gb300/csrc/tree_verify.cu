@@ -21,18 +21,24 @@
 namespace gdn {
 namespace {
 
-constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32, kVerCluster = 8, kVerParts = kVerWarps * kVerCluster;
-constexpr int kVerSteps = kVerMaxVocab / 4 / kVerParts / 32 + 2;  // of 32 groups of 4, per warp
-static_assert(kVerParts == 64, "a lane holds two warps' sums");
+constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32;
+
+// C: CTAs to a sequence. FLIGHT: groups of a row that a lane asks for at once. PER_SM: CTAs that an SM has to hold.
+template <bool DRAFT_, int C_, int FLIGHT_, int PER_SM_>
+struct Cfg {
+    static constexpr bool DRAFT = DRAFT_;
+    static constexpr int C = C_, FLIGHT = FLIGHT_, PER_SM = PER_SM_;
+    static constexpr int PARTS = kVerWarps * C, NP = PARTS / 32;                // warps of a sequence; ..' sums in a lane
+    static constexpr int STEPS = kVerMaxVocab / 4 / PARTS / 32 + 2;             // of 32 groups of 4, per warp
+};
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_meet() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // ---- numbers of 48 bits: hi + lo, |lo| at most half a unit of hi -----------------------
 struct Wide {
@@ -93,9 +99,10 @@ __device__ __forceinline__ void get(const Two &a, Wide &x, Wide &y) {
     y = plus(wide(h1), wide(l1));
 }
 
+template <typename C>
 struct VerSmem {
-    Wide part[2][kVerParts];  // a pass's sums by warp, two passes' by turns
-    Wide step[kVerSteps];
+    Wide part[2][C::PARTS];  // a pass's sums by warp, two passes' by turns
+    Wide step[C::STEPS];
     int up[kTreeMax], token[kTreeMax], gone[kTreeMax], path[kTreeMax];
     float p[kTreeMax], q[kTreeMax], r[kTreeMax];
 };
@@ -158,12 +165,14 @@ struct Row {
     }
 };
 
-template <bool DRAFT>
-__global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyArgs a) {
-    constexpr int kFlight = DRAFT ? 4 : 8;  // groups of a row in flight per lane
-    __shared__ VerSmem sm;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockIdx.x / kVerCluster;
+template <typename C>
+__global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(const VerifyArgs a) {
+    constexpr bool DRAFT = C::DRAFT;
+    constexpr int kFlight = C::FLIGHT, NP = C::NP;
+    __shared__ VerSmem<C> sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockIdx.x / C::C;
     const uint32_t rank = cluster_rank();
+    cluster_arrive();  // (waited for before anything is stored in another CTA)
     next_may_begin();
     before_reading();
     long bos = 0;
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
         sm.q[tid] = DRAFT && child ? a.draft[(bos + up) * a.draft_stride + x] : 1.f;
         if (tid == 0) sm.path[0] = 0;
     }
-    cluster_meet();  // (and the CTA)
+    __syncthreads();
     if (nodes == 0 || sm.up[0] != -1) {  // nothing to walk from: an idle row
         if (rank == 0) {
             for (int i = tid; i < a.path_stride; i += kVerThreads) path[i] = -1;
@@ -207,13 +216,14 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
                 a.next[n] = -1;
             }
         }
+        cluster_wait();
         return;
     }
     int cur = 0, count = 1, ngone = 0, pass = 0;
     Wide c = wide(0.f), Z = wide(1.f);
     Row<DRAFT> row;
     int g0 = 0, g1 = 0;        // this warp's groups
-    Wide below0, below1;       // lane: the sums of parts 0 .. 2 lane, .. 2 lane + 1
+    Wide ends[NP];             // lane: the sums of all parts up to NP lane + i
     // Sums the current node's weights; the same result in every thread of the cluster.
     auto sum_row = [&]() -> Wide {
         row.p = a.target + (bos + cur) * a.target_stride;
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
         row.same = ((reinterpret_cast<uintptr_t>(row.p) ^ reinterpret_cast<uintptr_t>(row.q)) & 15) == 0;
         row.c = c;
         row.gone = sm.gone;
-        const int groups = 1 + (a.V - row.head + 3) / 4, per = (groups + kVerParts - 1) / kVerParts;
+        const int groups = 1 + (a.V - row.head + 3) / 4, per = (groups + C::PARTS - 1) / C::PARTS;
         const int w = (int)rank * kVerWarps + warp;
         g0 = min(w * per, groups);
         g1 = min(g0 + per, groups);
@@ -253,14 +263,17 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
         get(acc[1], s2, s3);
         const Wide mine = warp_total(plus(plus(s0, s1), plus(s2, s3)));
         Wide *part = sm.part[pass & 1];
-        ++pass;
-        if (lane < kVerCluster) store_remote(part + w, (uint32_t)lane, mine);
-        cluster_meet();
-        const Wide x1 = part[2 * lane + 1];
-        const Wide two = plus(part[2 * lane], x1);
-        below1 = warp_scan(two);
-        below0 = plus(below1, Wide{-x1.hi, -x1.lo});
-        return shuffle(below1, 31);
+        if (pass++ == 0) cluster_wait();
+        if (lane < C::C) store_remote(part + w, (uint32_t)lane, mine);
+        cluster_arrive();
+        cluster_wait();
+        ends[0] = part[NP * lane];
+#pragma unroll
+        for (int i = 1; i < NP; ++i) ends[i] = plus(ends[i - 1], part[NP * lane + i]);
+        const Wide all = ends[NP - 1], before = minus(warp_scan(all), all);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) ends[i] = plus(before, ends[i]);
+        return shuffle(ends[NP - 1], 31);
     };
     bool stale = false;  // Z is not yet known
     for (int t = 1; t < nodes; ++t) {  // children come after their parents, so one walk over the nodes meets them in turn
@@ -314,25 +327,24 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
     }
     // the part that holds the draw: the first whose end is above it, or else the last that has weight
     const Wide draw = times(total, r_last);
-    Wide start{__shfl_up_sync(0xffffffffu, below1.hi, 1), __shfl_up_sync(0xffffffffu, below1.lo, 1)};
-    if (lane == 0) start = wide(0.f);
-    const bool some0 = sm.part[(pass - 1) & 1][2 * lane].hi > 0.f, some1 = sm.part[(pass - 1) & 1][2 * lane + 1].hi > 0.f;
-    unsigned at0 = __ballot_sync(0xffffffffu, some0 && below(draw, below0));
-    unsigned at1 = __ballot_sync(0xffffffffu, some1 && below(draw, below1));
-    int owner;
-    if (at0 | at1) {
-        const int l0 = at0 ? __ffs(at0) - 1 : 64, l1 = at1 ? __ffs(at1) - 1 : 64;
-        owner = l0 <= l1 ? 2 * l0 : 2 * l1 + 1;
-    } else {
-        at0 = __ballot_sync(0xffffffffu, some0);
-        at1 = __ballot_sync(0xffffffffu, some1);
-        const int l0 = at0 ? 31 - __clz(at0) : -1, l1 = at1 ? 31 - __clz(at1) : -1;
-        owner = l1 >= l0 ? 2 * l1 + 1 : 2 * l0;
+    int owner = kVerWarps * C::C, last_live = -1;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const bool live = sm.part[(pass - 1) & 1][NP * lane + i].hi > 0.f;
+        const unsigned at = __ballot_sync(0xffffffffu, live && below(draw, ends[i])), some = __ballot_sync(0xffffffffu, live);
+        if (at) owner = min(owner, NP * (__ffs(at) - 1) + i);
+        if (some) last_live = max(last_live, NP * (31 - __clz(some)) + i);
     }
+    if (owner == kVerWarps * C::C) owner = max(last_live, 0);
     if (owner / kVerWarps != (int)rank) return;
-    Wide base = owner & 1 ? shuffle(below0, owner >> 1) : shuffle(start, owner >> 1);
+    Wide base = wide(0.f);  // the sum of all parts before it
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const Wide e = shuffle(ends[i], (owner > 0 ? owner - 1 : 0) / NP);
+        if (owner > 0 && (owner - 1) % NP == i) base = e;
+    }
     // its steps of 128 elements, by all warps; then the step, by one
-    const int groups = 1 + (a.V - row.head + 3) / 4, per = (groups + kVerParts - 1) / kVerParts;
+    const int groups = 1 + (a.V - row.head + 3) / 4, per = (groups + C::PARTS - 1) / C::PARTS;
     g0 = min(owner * per, groups);
     g1 = min(g0 + per, groups);
     row.ngone = ngone;
@@ -401,22 +413,33 @@ __global__ void __launch_bounds__(kVerThreads) tree_verify_kernel(const VerifyAr
     if (lane == 0) a.next[n] = token;
 }
 
-}  // namespace
-
-cudaError_t launch_tree_verify(const VerifyArgs &a, cudaStream_t s) {
+template <typename C>
+cudaError_t launch_t(const VerifyArgs &a, cudaStream_t s) {
+    auto kernel = tree_verify_kernel<C>;
+    if (C::C > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kVerCluster;
+    attr[0].val.clusterDim.x = C::C;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)a.B * kVerCluster);
+    cfg.gridDim = dim3((unsigned)a.B * C::C);
     cfg.blockDim = dim3(kVerThreads);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, a.draft ? tree_verify_kernel<true> : tree_verify_kernel<false>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_verify(const VerifyArgs &a, cudaStream_t s) {
+    if (a.B <= 8) return a.draft ? launch_t<Cfg<true, 16, 5, 1>>(a, s) : launch_t<Cfg<false, 16, 10, 1>>(a, s);
+    return a.draft ? launch_t<Cfg<true, 8, 2, 4>>(a, s) : launch_t<Cfg<false, 8, 4, 4>>(a, s);
 }
 
 }  // namespace gdn
