@@ -35,14 +35,13 @@ struct Paths {
         return node & 32 ? (uint64_t)h1 << 32 | l1 : l0;  // (a node below 32 has none of 32.. on its path)
     }
 };
-__device__ __forceinline__ Paths tree_paths(const int32_t *parents, int nodes, int *status) {
+__device__ __forceinline__ Paths tree_paths(int up0, int up1, int *status) {  // from the two nodes' parents
     const int lane = threadIdx.x & 31;
     Paths p;
-    int up[2];
+    int up[2] = {up0, up1};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = lane + 32 * i;
-        up[i] = t < nodes ? parents[t] : -2;
         if (up[i] >= t) {  // no parent of its own
             flag_error(status);
             up[i] = -2;
@@ -75,6 +74,11 @@ __device__ __forceinline__ Paths tree_paths(const int32_t *parents, int nodes, i
     for (int i = 0; i < 2; ++i)
         if (up[i] != -1) p.lo[i] = p.hi[i] = 0u;
     return p;
+}
+
+__device__ __forceinline__ Paths tree_paths(const int32_t *parents, int nodes, int *status) {
+    const int lane = threadIdx.x & 31;
+    return tree_paths(lane < nodes ? parents[lane] : -2, lane + 32 < nodes ? parents[lane + 32] : -2, status);
 }
 
 // Whether a row with this path sees the position of node `i` of its sequence (below 0: the context, which all see)

@@ -30,25 +30,15 @@ __device__ __forceinline__ uint32_t split2(float &x, float &y) {
     return h;
 }
 
-// ---- asynchronous copies -------------------------------------------------------------
-__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {  // all but the last N groups have landed
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// ---- layouts in shared memory: where the 16 bytes `ch` of row r lie ------------------------
-// rows of DK bf16: a row's pieces are spread by the row, so that the 8 rows of a matrix lie in different banks
-template <int DK>
+// ---- layouts in shared memory: where the 16 bytes `ch` of row r lie (as the tensor maps' swizzles put them) ----
+// rows of DK bf16, in blocks of 64 columns of ROWS rows; the 8 rows of a matrix lie in different banks
+template <int DK, int ROWS>
 __device__ __forceinline__ uint32_t row_piece(int r, int ch) {
-    if (DK >= 64) return (uint32_t)(r * (DK * 2) + ((ch ^ (r & 7)) << 4));
+    if (DK >= 64) return (uint32_t)((ch >> 3) * (ROWS * 128) + r * 128 + (((ch ^ r) & 7) << 4));
     return (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
 }
-// 32 columns of a state, rows of 128 bytes: lanes of 4 rows 2 apart and 32 bytes each lie in different banks
-__device__ __forceinline__ uint32_t state_piece(int r, int ch) { return (uint32_t)(r * 128 + ((ch ^ (((r >> 1) & 3) << 1)) << 4)); }
+// 32 columns of a state, rows of 128 bytes: 32 bytes of 4 rows 2 apart lie in different banks
+__device__ __forceinline__ uint32_t state_piece(int r, int ch) { return (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4)); }
 // block (i, j <= i) of 16 x 16 coefficients, 64 bytes a row (fp32, or two bf16 terms each); rows spread as above
 __device__ __forceinline__ uint32_t coef_block(int i, int j) { return (uint32_t)((i * (i + 1) / 2 + j) * 1024); }
 __device__ __forceinline__ uint32_t coef_piece(int r, int ch) { return (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)); }

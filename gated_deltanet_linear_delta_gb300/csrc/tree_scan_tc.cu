@@ -16,12 +16,12 @@
 //
 // What bounds it: S_0's bytes, 64 KiB a head, for few nodes; for many the products, 2 dk (2 T) dv multiply-adds a head
 // at mma.sync's 1024 a cycle and SM, and the instructions around them.
-// CTAs are persistent, two or three to an SM, and S_0 comes in parts of 32 columns through a ring of three, the next
-// head's during the end of this one's work.
+// CTAs are persistent, two or three to an SM, and S_0 comes by TMA in parts of 32 columns through a ring, the next
+// head's during the end of this one's work. Every wait has a limit, after which the call flags the status word.
 //
 // Values that are not finite stay on their paths: a product with a coefficient of 0 would spread them, so they are
 // left out of the products, and the outputs that have them on their path become NaN.
-#include "kv_pages.cuh"
+#include "attn_ops.cuh"
 #include "tree_mma.cuh"
 
 namespace gdn {
@@ -34,16 +34,19 @@ struct Cfg {
     static constexpr int NQ = DK / 32, RING = TP == 16 ? 4 : 3;  // parts of a state; slots
     static constexpr uint32_t SLOT = DV * 128;
     static constexpr int BLOCKS = NB * (NB + 1) / 2;
+    static constexpr uint32_t KQ_BYTES = TP * DK * 2;
     // byte offsets
-    static constexpr uint32_t SM_KQ = 0;                                      // [2 TP][DK] bf16: K, then Q
-    static constexpr uint32_t SM_S = SM_KQ + 2 * TP * DK * 2;                  // [RING][DV][32] fp32
+    static constexpr uint32_t SM_KQ = 0;                                      // K, then Q [TP][DK] bf16
+    static constexpr uint32_t SM_S = (2 * KQ_BYTES + 1023) & ~1023u;           // [RING][DV][32] fp32
     static constexpr uint32_t SM_A = SM_S + RING * SLOT;                       // K K^T, blocks of 16 x 16 fp32
     static constexpr uint32_t SM_W = SM_A + BLOCKS * 1024;                     // Q K^T, then W, fp32, then W as two terms
     static constexpr uint32_t SM_SC = SM_W + BLOCKS * 1024;                    // per node: Scalars
     static constexpr uint32_t SM_PATH = SM_SC + TP * 32;                       // [TP] paths
     static constexpr uint32_t SM_G = SM_PATH + TP * 8;                         // [TP] g
     static constexpr uint32_t SM_R = SM_G + TP * 4;                            // [TP] |q|^2
-    static constexpr uint32_t SM_BYTES = SM_R + TP * 4;
+    static constexpr uint32_t SM_BAR = SM_R + TP * 4;                          // keys and queries; the slots
+    static constexpr uint32_t SM_UNIT = SM_BAR + (1 + RING) * 8;               // the next block of products
+    static constexpr uint32_t SM_BYTES = SM_UNIT + 8;
     static constexpr int FIT = 233472 / (SM_BYTES + 1024), PER_SM = FIT < 3 ? FIT : 3;  // CTAs to an SM
     static_assert(PER_SM >= 2, "two CTAs to an SM");
 };
@@ -61,123 +64,166 @@ struct Head {
 };
 
 template <int DK, int DV, int TP>
-__global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER_SM) tree_scan_tc_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER_SM)
+tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constant__ CUtensorMap mk,
+                    const __grid_constant__ CUtensorMap mq, const TreeArgs a, long long budget) {
     using C = Cfg<DK, DV, TP>;
-    extern __shared__ __align__(128) uint8_t sm[];
-    const uint32_t sb = tc::smem_u32(sm);
+    using namespace tc;
+    // (on a 1 KiB boundary, as all of it is asked for at launch: checked, as room to align it would cost the third CTA)
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     Scalars *sc = reinterpret_cast<Scalars *>(sm + C::SM_SC);
     uint64_t *paths = reinterpret_cast<uint64_t *>(sm + C::SM_PATH);
     float *gs = reinterpret_cast<float *>(sm + C::SM_G), *qq = reinterpret_cast<float *>(sm + C::SM_R);
-    const __nv_bfloat16 *q = (const __nv_bfloat16 *)a.q, *k = (const __nv_bfloat16 *)a.k, *v = (const __nv_bfloat16 *)a.v;
-    const __nv_bfloat16 *ga = (const __nv_bfloat16 *)a.g, *be = (const __nv_bfloat16 *)a.b;
+    uint64_t *bar_kq = reinterpret_cast<uint64_t *>(sm + C::SM_BAR), *bar_s = bar_kq + 1;
+    int *unit = reinterpret_cast<int *>(sm + C::SM_UNIT);
+    const __nv_bfloat16 *v = (const __nv_bfloat16 *)a.v, *ga = (const __nv_bfloat16 *)a.g, *be = (const __nv_bfloat16 *)a.b;
     __nv_bfloat16 *out = (__nv_bfloat16 *)a.out;
-    const int heads = a.B * a.Hv, r = a.Hv / a.Hk;
     next_may_begin();
+    if (tid == 0) {
+        prefetch_tmap(&ms);
+        prefetch_tmap(&mk);
+        prefetch_tmap(&mq);
+        for (int i = 0; i < 1 + C::RING; ++i) mbar_init(bar_kq + i, 1);
+        fence_mbar_init();
+        *unit = 0;
+    }
     before_reading();
+    __syncthreads();
+    if (sb & 1023u) {
+        flag_error(a.status);
+        return;
+    }
 
-    // The next head from `i` on that has nodes and a state; heads of padding sequences are written as zeros on the way.
-    auto find = [&](int &i) -> Head {
+    // Heads by turns over the CTAs. The next from (n, h) on that has nodes and a state; heads of padding sequences are
+    // written as zeros on the way.
+    const int dn = (int)(gridDim.x / a.Hv), dh = (int)(gridDim.x % a.Hv);
+    int at_n = (int)(blockIdx.x / a.Hv), at_h = (int)(blockIdx.x % a.Hv);
+    auto step = [&] {
+        at_n += dn;
+        if ((at_h += dh) >= a.Hv) {
+            at_h -= a.Hv;
+            ++at_n;
+        }
+    };
+    auto find = [&]() -> Head {
         Head hd{0, 0, 0, 0, -1};
-        for (; i < heads; i += gridDim.x) {
-            hd.n = i / a.Hv;
-            hd.h = i % a.Hv;
+        for (; at_n < a.B; step()) {
+            hd.n = at_n;
+            hd.h = at_h;
             if (!tree_bounds(a.cu, hd.n, a.B, a.cu ? a.Ttot : a.T, &hd.bos, &hd.nodes, a.status) || hd.nodes == 0) continue;
             hd.slot = state_slot(a, hd.n);
-            if (hd.slot >= 0) break;
+            if (hd.slot >= 0) return hd;
             for (int e = tid; e < hd.nodes * (DV / 8); e += C::THREADS)
                 reinterpret_cast<uint4 *>(out + ((hd.bos + e / (DV / 8)) * a.Hv + hd.h) * DV)[e % (DV / 8)] = make_uint4(0, 0, 0, 0);
         }
-        if (i >= heads) hd.slot = -1;
+        hd.slot = -1;
         return hd;
     };
+    auto step_to = [&](const Head &from) -> Head {
+        if (from.slot < 0) return from;
+        step();
+        return find();
+    };
+    // Copies, by one thread. Keys and queries of TP tokens, whatever a sequence's number of nodes.
+    uint32_t copies_kq = 0, copies_s = 0;  // begun
     auto load_kq = [&](const Head &hd) {
-        if (hd.slot >= 0) {
-            constexpr int PR = DK / 8;
-            const int hk = hd.h / r;
-            for (int e = tid; e < hd.nodes * PR; e += C::THREADS) {
-                const int t = e / PR, ch = e % PR;
-                const long at = ((hd.bos + t) * a.Hk + hk) * DK + 8 * ch;
-                copy16(sb + C::SM_KQ + row_piece<DK>(t, ch), k + at);
-                copy16(sb + C::SM_KQ + row_piece<DK>(TP + t, ch), q + at);
-            }
+        if (hd.slot < 0) return;
+        ++copies_kq;
+        if (tid != 0) return;
+        const int hk = hd.h / (a.Hv / a.Hk);
+        mbar_expect_tx(bar_kq, 2 * C::KQ_BYTES);
+#pragma unroll
+        for (int b = 0; b < (DK >= 64 ? DK / 64 : 1); ++b) {
+            tma_load_3d(sm + C::SM_KQ + b * (TP * 128), &mk, 64 * b, hk, (int)hd.bos, bar_kq);
+            tma_load_3d(sm + C::SM_KQ + C::KQ_BYTES + b * (TP * 128), &mq, 64 * b, hk, (int)hd.bos, bar_kq);
         }
-        copies_commit();
     };
-    auto state_of = [&](const Head &hd) { return hd.slot >= 0 ? a.state_in + (hd.slot * a.Hv + hd.h) * (long)(DV * DK) : nullptr; };
-    auto load_state = [&](const float *state, int part, int slot) {
-        if (state != nullptr) {
-            const float *src = state + part * 32;
-            for (int e = tid; e < DV * 8; e += C::THREADS)
-                copy16(sb + C::SM_S + slot * C::SLOT + state_piece(e >> 3, e & 7), src + (e >> 3) * DK + (e & 7) * 4);
-        }
-        copies_commit();
+    auto load_state = [&](bool any, int state, int part, int slot) {
+        if (!any) return;
+        ++copies_s;
+        if (tid != 0) return;
+        mbar_expect_tx(bar_s + slot, C::SLOT);
+        tma_load_3d(sm + C::SM_S + slot * C::SLOT, &ms, 32 * part, 0, state, bar_s + slot);
     };
-    // the node of a thread of the last warps, its gate and beta logit
+    auto state_of = [&](const Head &hd) { return (int)(hd.slot * a.Hv + hd.h); };
+    // The nodes' threads are those of the last warps; the last one works the paths out.
     const int node = tid - (C::THREADS - TP);
-    auto load_gates = [&](const Head &hd, float &gv, float &bv) {
+    int up0 = -2, up1 = -2;
+    float gv = 0.f, bv = 0.f;
+    auto load_nodes = [&](const Head &hd) {
+        up0 = up1 = -2;
         gv = bv = 0.f;
-        if (hd.slot >= 0 && node >= 0 && node < hd.nodes) {
+        if (hd.slot < 0) return;
+        if (node >= 0 && node < hd.nodes) {
             gv = to_f32(ga[(hd.bos + node) * a.Hv + hd.h]);
             bv = to_f32(be[(hd.bos + node) * a.Hv + hd.h]);
+        }
+        if (warp == C::WARPS - 1) {
+            if (lane < hd.nodes) up0 = a.parents[hd.bos + lane];
+            if (TP > 32 && lane + 32 < hd.nodes) up1 = a.parents[hd.bos + lane + 32];
         }
     };
 
     // Parts follow one another through the ring, head by head. When a head's products begin, as many parts as the ring
     // has slots are there or on their way; each slot is filled again once all warps are past it, the last one behind the
     // next head's keys and queries.
-    int next_i = blockIdx.x;
-    auto step_to = [&](const Head &from) -> Head {
-        if (from.slot < 0) return from;
-        next_i += gridDim.x;
-        return find(next_i);
-    };
     constexpr int AHEAD = (C::RING + C::NQ - 1) / C::NQ;  // heads to know of beside the one at hand
     static_assert(AHEAD <= 4, "heads ahead");
     Head hd[AHEAD + 1];
-    hd[0] = find(next_i);
+    hd[0] = find();
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) hd[i + 1] = step_to(hd[i]);
+    load_kq(hd[0]);
 #pragma unroll
-    for (int i = 0; i < C::RING; ++i) {
-        if (i == C::RING - 1) load_kq(hd[0]);
-        load_state(state_of(hd[i / C::NQ]), i % C::NQ, i);
-    }
-    auto state_ahead = [&](int d) {  // of the head d ahead
-        const float *s = state_of(hd[0]);
-#pragma unroll
-        for (int i = 1; i <= AHEAD; ++i)
-            if (d == i) s = state_of(hd[i]);
-        return s;
-    };
-    float gv, bv;
-    load_gates(hd[0], gv, bv);
-    int slot = 0;  // of the part at hand
+    for (int i = 0; i < C::RING; ++i) load_state(hd[i / C::NQ].slot >= 0, state_of(hd[i / C::NQ]), i % C::NQ, i);
+    load_nodes(hd[0]);
+    int slot = 0;                 // of the part at hand
+    uint32_t phase_kq = 0, phase_s = 0;
+    bool ok = true;
     while (hd[0].slot >= 0) {
         const Head &cur = hd[0];
         const int T = cur.nodes, nb = (T + 15) / 16;
-        copies_wait<1>();  // keys and queries, and the parts before the ring's last
-        __syncthreads();
-        // ---- paths, K K^T and Q K^T block by block of 16 x 16, |q|^2 --------------------------------
-        if (warp == C::WARPS - 1) {
-            const Paths p = tree_paths(a.parents + cur.bos, T, a.status);
-            if (lane < TP) paths[lane] = p.of(0);
-            if (TP > 32) paths[lane + 32] = p.of(1);
+        ok = wait_for(bar_kq, phase_kq, budget);
+        phase_kq ^= 1;
+        if (__syncthreads_or(!ok)) {  // (and what the nodes of the head before are known by has been read)
+            ok = false;
+            break;
         }
-        if (node >= 0) gs[node] = gv;
-        for (int u = warp; u < nb * (nb + 2); u += C::WARPS) {
+        // ---- paths and gates; beside them K K^T and Q K^T, block by block of 16 x 16, and |q|^2 ----------
+        float hi = 0.f, lo = 0.f;
+        if (node >= 0 || (TP < 32 && warp == C::WARPS - 1)) {
+            if (node >= 0) gs[node] = gv;
+            if (warp == C::WARPS - 1) {
+                const Paths p = tree_paths(up0, up1, a.status);
+                if (lane < TP) paths[lane] = p.of(0);
+                if (TP > 32) paths[lane + 32] = p.of(1);
+            }
+            if (TP > 32) bar_sync(1, 64);
+            else __syncwarp();
+            if (node >= 0 && node < T)
+                for (uint64_t m = paths[node]; m; m &= m - 1) add_exact(hi, lo, gs[__ffsll((long long)m) - 1]);
+            __syncwarp();
+        }
+        while (true) {
+            int u = 0;
+            if (lane == 0) u = atomicAdd(unit, 1);
+            u = __shfl_sync(0xffffffffu, u, 0);
+            if (u >= nb * (nb + 2)) break;
             const bool square = u >= nb * (nb + 1);  // Q Q^T of a block, for its diagonal
             const bool is_q = square || (u & 1);
             int i = 0, j = u >> 1;  // the block's rows and columns, j <= i
             while (j > i) j -= ++i;
             if (square) i = j = u - nb * (nb + 1);
             float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const int ra = (is_q ? TP : 0) + 16 * i + (lane & 15), rb = (square ? TP : 0) + 16 * j + ((lane >> 4) << 3) + (lane & 7);
+            const int ra = 16 * i + (lane & 15), rb = 16 * j + ((lane >> 4) << 3) + (lane & 7);
+            const uint32_t xa = sb + C::SM_KQ + (is_q ? C::KQ_BYTES : 0), xb = sb + C::SM_KQ + (square ? C::KQ_BYTES : 0);
 #pragma unroll
             for (int ks = 0; ks < DK / 16; ++ks) {
                 uint32_t x[4], y[4];
-                load_matrices(x, sb + C::SM_KQ + row_piece<DK>(ra, 2 * ks + (lane >> 4)));
-                load_matrices(y, sb + C::SM_KQ + row_piece<DK>(rb, 2 * ks + ((lane >> 3) & 1)));
+                load_matrices(x, xa + row_piece<DK, TP>(ra, 2 * ks + (lane >> 4)));
+                load_matrices(y, xb + row_piece<DK, TP>(rb, 2 * ks + ((lane >> 3) & 1)));
                 mma_bf16_16816(acc[0], x, y[0], y[1]);
                 mma_bf16_16816(acc[1], x, y[2], y[3]);
             }
@@ -197,19 +243,17 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
                         make_float2(acc[n][2 * half], acc[n][2 * half + 1]);
         }
         __syncthreads();
-        // ---- per node: norms, gates -------------------------------------------------------------
+        // ---- per node: norms ----------------------------------------------------------------------
+        if (tid == 0) *unit = 0;
         if (node >= 0) {
-            float hi = 0.f, lo = 0.f, kk = 0.f;
-            if (node < T) {
-                for (uint64_t m = paths[node]; m; m &= m - 1) add_exact(hi, lo, gs[__ffsll((long long)m) - 1]);
-                kk = reinterpret_cast<const float *>(sm + C::SM_A + coef_block(node >> 4, node >> 4) +
-                                                     coef_piece(node & 15, (node & 15) >> 2))[node & 3];
-            }
+            const float kk = node < T ? reinterpret_cast<const float *>(sm + C::SM_A + coef_block(node >> 4, node >> 4) +
+                                                                        coef_piece(node & 15, (node & 15) >> 2))[node & 3]
+                                      : 0.f;
             Scalars s;
-            const float eg = expf(hi + lo);
+            const float eg = __expf(hi + lo);
             s.beta = sigmoidf_(bv);
-            s.rk = 1.f / sqrtf(kk + kNormEps);
-            s.rq = 1.f / sqrtf(qq[node] + kNormEps);
+            s.rk = rsqrtf(kk + kNormEps);
+            s.rq = rsqrtf(qq[node] + kNormEps);
             s.x = s.beta * eg * s.rk;
             s.z = eg * s.rq;
             s.b2 = s.beta * s.rk * s.rk;
@@ -236,7 +280,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
                 uint32_t left = (uint32_t)(on >> (16 * j)) & 0xffffu;
                 // (the warp's eight rows step together, each along its own path: rows that part ways would run one by one)
                 while (__any_sync(0xffffffffu, left != 0)) {
-                    const int s = 31 - __clz(left | 1);  // of the block's nodes; w[s] is final: take it out of the columns before it
+                    const int s = 31 - __clz(left | 1);  // of the block's nodes; w_s is final
                     const int e = s & 3;
                     const float own = e == 0 ? w[j][0] : e == 1 ? w[j][1] : e == 2 ? w[j][2] : w[j][3];
                     const float ws = -__shfl_sync(0xffffffffu, own, (lane & ~3) | (s >> 2)) * sc[16 * j + s].b2;
@@ -261,18 +305,17 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
 #pragma unroll
             for (int j = 0; j < C::NB; ++j) {
                 if (j > t >> 4) continue;
+                const uint32_t mine = (uint32_t)(on >> (16 * j)) >> (4 * sub);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int s = 16 * j + 4 * sub + e;
-                    const Scalars ss = sc[s];
-                    const float d = __expf((st.g - ss.g) + (st.g_lo - ss.g_lo)) * ss.rk;
-                    w[j][e] = (on >> s) & 1 ? w[j][e] * d : 0.f;
+                    const Scalars ss = sc[16 * j + 4 * sub + e];
+                    w[j][e] = mine & (1u << e) ? w[j][e] * (__expf((st.g - ss.g) + (st.g_lo - ss.g_lo)) * ss.rk) : 0.f;
                 }
                 uint2 up, low;
                 up.x = split2(w[j][0], w[j][1]);
                 up.y = split2(w[j][2], w[j][3]);
-                low.x = tc::bf2_bits(__floats2bfloat162_rn(w[j][0], w[j][1]));
-                low.y = tc::bf2_bits(__floats2bfloat162_rn(w[j][2], w[j][3]));
+                low.x = bf2_bits(__floats2bfloat162_rn(w[j][0], w[j][1]));
+                low.y = bf2_bits(__floats2bfloat162_rn(w[j][2], w[j][3]));
                 *reinterpret_cast<uint2 *>(row + j * 1024 + coef_piece(t & 15, sub >> 1) + 8 * (sub & 1)) = up;
                 *reinterpret_cast<uint2 *>(row + j * 1024 + coef_piece(t & 15, 2 + (sub >> 1)) + 8 * (sub & 1)) = low;
             }
@@ -295,12 +338,20 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
             for (int e = 0; e < 4; ++e) xk[n][e] = xq[n][e] = 0.f;
 #pragma unroll 1
         for (int part = 0; part < C::NQ; ++part) {
-            if (part >= C::RING - 1) copies_wait<C::RING - 2>();
-            if (part >= 1) {
-                __syncthreads();
-                const int p = part + C::RING - 1;
-                load_state(state_ahead(p / C::NQ), p % C::NQ, slot == 0 ? C::RING - 1 : slot - 1);
+            if (part >= 1) {  // all warps are past the part before: its slot may be filled again
+                if (__syncthreads_or(!ok)) break;
+                const int p = part + C::RING - 1, d = p / C::NQ;
+                bool any = cur.slot >= 0;
+                int state = state_of(cur);
+#pragma unroll
+                for (int i = 1; i <= AHEAD; ++i)
+                    if (d == i) {
+                        any = hd[i].slot >= 0;
+                        state = state_of(hd[i]);
+                    }
+                load_state(any, state, p % C::NQ, slot == 0 ? C::RING - 1 : slot - 1);
             }
+            ok = wait_for(bar_s + slot, phase_s, budget);
             const uint8_t *s0 = sm + C::SM_S + slot * C::SLOT;
 #pragma unroll
             for (int kk = 0; kk < 2; ++kk) {
@@ -311,31 +362,41 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
                     float2 x = *reinterpret_cast<const float2 *>(s0 + state_piece(row0 + (e & 1), 4 * kk + 2 * (e >> 1) + (c >> 1)) +
                                                                  8 * (c & 1));
                     ah[e] = split2(x.x, x.y);
-                    al[e] = tc::bf2_bits(__floats2bfloat162_rn(x.x, x.y));
+                    al[e] = bf2_bits(__floats2bfloat162_rn(x.x, x.y));
                 }
 #pragma unroll
                 for (int j = 0; j < C::NB; ++j)
                     if (j < nb) {
                         const int rr = 16 * j + ((lane >> 4) << 3) + (lane & 7), ch = 2 * ks + ((lane >> 3) & 1);
                         uint32_t y[4];
-                        load_matrices(y, sb + C::SM_KQ + row_piece<DK>(rr, ch));
+                        load_matrices(y, sb + C::SM_KQ + row_piece<DK, TP>(rr, ch));
                         mma_bf16_16816(xk[2 * j], ah, y[0], y[1]);
                         mma_bf16_16816(xk[2 * j + 1], ah, y[2], y[3]);
                         mma_bf16_16816(xk[2 * j], al, y[0], y[1]);
                         mma_bf16_16816(xk[2 * j + 1], al, y[2], y[3]);
-                        load_matrices(y, sb + C::SM_KQ + row_piece<DK>(TP + rr, ch));
+                        load_matrices(y, sb + C::SM_KQ + C::KQ_BYTES + row_piece<DK, TP>(rr, ch));
                         mma_bf16_16816(xq[2 * j], ah, y[0], y[1]);
                         mma_bf16_16816(xq[2 * j + 1], ah, y[2], y[3]);
                         mma_bf16_16816(xq[2 * j], al, y[0], y[1]);
                         mma_bf16_16816(xq[2 * j + 1], al, y[2], y[3]);
                     }
             }
-            if (++slot == C::RING) slot = 0;
+            if (++slot == C::RING) {
+                slot = 0;
+                phase_s ^= 1;
+            }
         }
-        __syncthreads();  // keys, queries and the last part's slot may be filled again
+        if (__syncthreads_or(!ok)) {
+            ok = false;
+            break;
+        }
+        // keys, queries and the last part's slot may be filled again
         load_kq(hd[1]);
-        load_state(state_of(hd[(C::NQ + C::RING - 1) / C::NQ]), (C::NQ + C::RING - 1) % C::NQ, slot == 0 ? C::RING - 1 : slot - 1);
-        load_gates(hd[1], gv, bv);
+        {
+            const Head &far = hd[(C::NQ + C::RING - 1) / C::NQ];
+            load_state(far.slot >= 0, state_of(far), (C::NQ + C::RING - 1) % C::NQ, slot == 0 ? C::RING - 1 : slot - 1);
+        }
+        load_nodes(hd[1]);
         // ---- R, and O ----------------------------------------------------------------------------------
         uint64_t bad0 = 0, bad1 = 0;  // nodes whose R is not finite in this lane's rows
         float sure = 0.f;
@@ -378,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
             for (int e = 0; e < 4; ++e) {
                 float x = xk[2 * j + (e >> 1)][2 * (e & 1)], y = xk[2 * j + (e >> 1)][2 * (e & 1) + 1];
                 uh[e] = split2(x, y);
-                ul[e] = tc::bf2_bits(__floats2bfloat162_rn(x, y));
+                ul[e] = bf2_bits(__floats2bfloat162_rn(x, y));
             }
             const int tr = ((lane >> 4) << 3) + (lane & 7), ch = (lane >> 3) & 1;
 #pragma unroll
@@ -408,29 +469,61 @@ __global__ void __launch_bounds__(Cfg<DK, DV, TP>::THREADS, Cfg<DK, DV, TP>::PER
                     if (bad0 & paths[t]) o0 = __int_as_float(0x7fffffff);
                     if (bad1 & paths[t]) o1 = __int_as_float(0x7fffffff);
                 }
-                *reinterpret_cast<uint32_t *>(out + vat + (long)t * a.Hv * DV) = tc::bf2_bits(__floats2bfloat162_rn(o0, o1));
+                *reinterpret_cast<uint32_t *>(out + vat + (long)t * a.Hv * DV) = bf2_bits(__floats2bfloat162_rn(o0, o1));
             }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) hd[i] = hd[i + 1];
         hd[AHEAD] = step_to(hd[AHEAD - 1]);
     }
-    copies_wait<0>();
+    if (!ok) {
+        flag_error(a.status);
+        // copies in flight land before the CTA leaves
+        if (tid == 0) {
+            if (copies_kq > 0) mbar_wait(bar_kq, (copies_kq - 1) & 1, kDrainBudget);
+            for (uint32_t i = copies_s > C::RING ? copies_s - C::RING : 0; i < copies_s; ++i)
+                mbar_wait(bar_s + i % C::RING, (i / C::RING) & 1, kDrainBudget);
+        }
+        __syncthreads();
+    }
+}
+
+// x [outer][mid][inner] -> boxes of (32 or 64 columns, rows of one of the other dimensions), swizzled over their bytes
+bool scan_map(CUtensorMap *m, const void *base, bool f32, int inner, long mid, long outer, int box_inner, int box_mid, int box_outer) {
+    EncodeTiledFn enc = tiled_encoder();
+    if (!enc) return false;
+    const cuuint64_t elem = f32 ? 4 : 2;
+    const cuuint64_t gdim[3] = {(cuuint64_t)inner, (cuuint64_t)mid, (cuuint64_t)outer};
+    const cuuint64_t gstride[2] = {inner * elem, (cuuint64_t)mid * inner * elem};
+    const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_mid, (cuuint32_t)box_outer};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), gdim,
+               gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_inner * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DK, int DV, int TP>
 cudaError_t launch_t(const TreeArgs &a, cudaStream_t s) {
     using C = Cfg<DK, DV, TP>;
+    CUtensorMap ms, mk, mq;
+    const long states = (a.slots ? a.num_slots : (long)a.B) * a.Hv;
+    if (!scan_map(&ms, a.state_in, true, DK, DV, states > 0 ? states : 1, 32, DV, 1) ||
+        !scan_map(&mk, a.k, false, DK, a.Hk, a.Ttot, DK < 64 ? DK : 64, 1, TP) ||
+        !scan_map(&mq, a.q, false, DK, a.Hk, a.Ttot, DK < 64 ? DK : 64, 1, TP))
+        return cudaErrorInvalidValue;
     auto kernel = tree_scan_tc_kernel<DK, DV, TP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);
     if (e != cudaSuccess) return e;
     const long heads = (long)a.B * a.Hv, most = 152L * C::PER_SM;
-    return launch_early(kernel, dim3((unsigned)(heads < most ? heads : most)), C::THREADS, C::SM_BYTES, s, a);
+    return launch_early(kernel, dim3((unsigned)(heads < most ? heads : most)), C::THREADS, C::SM_BYTES, s, ms, mk, mq, a,
+                        wait_budget());
 }
 
 template <int DK, int DV>
 cudaError_t launch_tp(const TreeArgs &a, cudaStream_t s) {
     const long most = a.cu ? a.Ttot : a.T;  // nodes of a sequence
     if (most <= 16) return launch_t<DK, DV, 16>(a, s);
+    if (most <= 32 && DK == 128 && DV == 128) return launch_t<DK, DV, 32>(a, s);
     return launch_t<DK, DV, 64>(a, s);
 }
 
