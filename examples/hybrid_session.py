@@ -3,10 +3,12 @@
 Three of four layers are Gated DeltaNet layers, whose state has a fixed size; the fourth is an
 attention layer, whose keys and values go to a paged cache (bf16, or quantised to e4m3 or int8 as
 they are written). A prompt is taken in fragments, then tokens one at a time, the decode step from a
-captured CUDA graph whose lengths live on the device. The projections around the layers are plain
-matrix products with random weights: the point is how the calls fit together.
+captured CUDA graph whose lengths live on the device. Then the same tokens again by trees of drafts: all
+layers check a tree's nodes at once, the drafts are verified against the model's probabilities, and states
+and caches move on along the accepted path. The projections around the layers are plain matrix products
+with random weights: the point is how the calls fit together.
 
-    python examples/hybrid_session.py [--cache same|fp8|int8] [--sessions 4] [--prompt 700] [--tokens 16]
+    python examples/hybrid_session.py [--cache same|fp8|int8] [--sessions 4] [--prompt 700] [--tokens 16] [--nodes 8]
 """
 from __future__ import annotations
 
@@ -55,6 +57,16 @@ class GdnLayer:
         gdn.gdn_decode_step(q, k, v, g, b, self.state, out)
         return x + _linear(out.flatten(1), self.wo)
 
+    def tree(self, x, parents):
+        """Drafted nodes: their outputs, with the state as it is. What `accept` needs of them is kept."""
+        q, *self.nodes = self._inputs(x)
+        out = torch.empty_like(self.nodes[1])
+        gdn.gdn_tree_scan(q, *self.nodes, self.state, parents, out)
+        return x + _linear(out.flatten(1), self.wo)
+
+    def accept(self, path, counts):
+        gdn.gdn_tree_advance(*self.nodes, self.state, self.state, path, counts)
+
 
 class AttentionLayer:
     """x + W_o attention(x): 16 query heads and 2 key heads of 256 over a paged cache.
@@ -74,14 +86,20 @@ class AttentionLayer:
         if cache != "same":
             self.scales = {n: torch.empty(pool[:3], device=DEV) for n in ("k_scale", "v_scale")}
 
-    def __call__(self, x, table, kv_lens, workspace):
-        """The new tokens of x (B sessions of T each), whose positions end at kv_lens."""
+    def __call__(self, x, table, kv_lens, workspace, parents=None):
+        """The new tokens of x (B sessions of T each), whose positions end at kv_lens; with parents, nodes of trees."""
         qkv = _linear(x, self.wqkv)
         q, k, v = qkv.unflatten(1, (-1, self.d)).split([self.Hq, self.Hkv, self.Hkv], dim=1)
         gdn.gdn_kv_write(k, v, self.k_cache, self.v_cache, table, kv_lens, **self.scales)
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        gdn.gdn_paged_attn(q, self.k_cache, self.v_cache, table, kv_lens, out, workspace=workspace, **self.scales)
+        if parents is None:
+            gdn.gdn_paged_attn(q, self.k_cache, self.v_cache, table, kv_lens, out, workspace=workspace, **self.scales)
+        else:
+            gdn.gdn_tree_attn(q, self.k_cache, self.v_cache, table, kv_lens, parents, out, workspace=workspace, **self.scales)
         return x + _linear(out.flatten(1), self.wo)
+
+    def accept(self, table, kv_lens, path, counts, nodes):
+        gdn.gdn_kv_keep(self.k_cache, self.v_cache, table, kv_lens, path, counts, T=nodes, **self.scales)
 
 
 class HybridSession:
@@ -117,6 +135,26 @@ class HybridSession:
             y = self._forward(part.flatten(0, 1), step=False).view(part.shape)
         return y[:, -1]
 
+    def check(self, x, parents):
+        """Drafted nodes of every session, x [B, T, width], parents [B, T]: the stack's output at each node."""
+        self.kv_lens += x.shape[1]
+        y = x.flatten(0, 1)
+        for layer in self.layers:
+            if isinstance(layer, AttentionLayer):
+                y = layer(y, self.table, self.kv_lens, self.workspace, parents.flatten())
+            else:
+                y = layer.tree(y, parents.flatten())
+        return y.view(x.shape)
+
+    def accept(self, path, counts, nodes):
+        """After `check`: the sessions go on from their accepted paths, path [B, P] and counts [B]."""
+        for layer in self.layers:
+            if isinstance(layer, AttentionLayer):
+                layer.accept(self.table, self.kv_lens, path, counts, nodes)
+            else:
+                layer.accept(path, counts)
+        self.kv_lens += counts - nodes
+
     def decode(self, x):
         """One token of every session, x [B, width], from a graph captured at the first call."""
         if self.graph is None:
@@ -141,15 +179,35 @@ class HybridSession:
         return self.y
 
 
+def speculate(s, embed, token, nodes, rng):
+    """One step by drafts: a draft model that guesses proposes a tree under each session's last token, the stack checks
+    it, and the sessions move on by what stands. Returns the accepted tokens' number and the next tokens, both [B]."""
+    B, V = s.B, embed.shape[0]
+    parents = torch.arange(-1, nodes - 1, dtype=torch.int32, device=DEV).div(2, rounding_mode="floor").repeat(B, 1)
+    parents[:, 0] = -1  # (0 and its children 1, 2; 1 and its children 3, 4; ..)
+    drafts = torch.full((B * nodes, V), 1.0 / V, device=DEV)
+    tokens = torch.randint(V, (B, nodes), generator=rng, device=DEV).to(torch.int32)
+    tokens[:, 0] = token
+    y = s.check(embed[tokens.long()], parents)
+    target = torch.softmax(torch.nn.functional.rms_norm(y, y.shape[-1:]).flatten(0, 1).float() @ embed.float().T, -1)
+    path = torch.empty(B, nodes, dtype=torch.int32, device=DEV)
+    counts, token = (torch.empty(B, dtype=torch.int32, device=DEV) for _ in range(2))
+    r, last = (torch.rand(n, generator=rng, device=DEV) for n in (B * nodes, B))
+    gdn.gdn_tree_verify(target, drafts, tokens.flatten(), parents.flatten(), r, last, path, counts, token)
+    s.accept(path, counts, nodes)
+    return counts, token
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--cache", choices=("same", "fp8", "int8"), default="fp8")
     ap.add_argument("--sessions", type=int, default=4)
     ap.add_argument("--prompt", type=int, default=700)
     ap.add_argument("--tokens", type=int, default=16)
+    ap.add_argument("--nodes", type=int, default=8)
     a = ap.parse_args()
     width = 512
-    s = HybridSession(a.sessions, a.prompt + a.tokens, width, a.cache)
+    s = HybridSession(a.sessions, a.prompt + a.tokens + a.tokens * a.nodes, width, a.cache)
     x = torch.randn(a.sessions, a.prompt, width, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
     y = s.prompt(x, fragment=256)
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -163,6 +221,16 @@ def main():
         raise RuntimeError("the device status reports inconsistent data")
     print(f"{a.sessions} sessions, cache {a.cache}: {a.prompt} prompt tokens, then {a.tokens} tokens at "
           f"{start.elapsed_time(end) / max(1, a.tokens - 1) * 1e3:.1f} us a step; lengths {s.kv_lens.tolist()}")
+    rng = torch.Generator(device=DEV).manual_seed(2)
+    embed = torch.randn(32, width, generator=rng, device=DEV).to(torch.bfloat16)
+    token, steps, taken = torch.zeros(a.sessions, dtype=torch.int32, device=DEV), 0, torch.zeros(a.sessions, device=DEV)
+    while steps < a.tokens and taken.min() < a.tokens:
+        counts, token = speculate(s, embed, token, a.nodes, rng)
+        taken += counts
+        steps += 1
+    if gdn.gdn_get_device_status() != gdn.GDN_OK:
+        raise RuntimeError("the device status reports inconsistent data")
+    print(f"drafts, trees of {a.nodes}: {steps} steps, {taken.mean().item() / steps:.2f} tokens a step; lengths {s.kv_lens.tolist()}")
 
 
 if __name__ == "__main__":

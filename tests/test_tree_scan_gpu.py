@@ -216,6 +216,47 @@ def test_values_that_are_not_finite_stay_on_their_paths():
             assert not torch.isfinite(out[on]).any()
 
 
+@pytest.mark.parametrize("which", [0, 1])
+def test_keys_and_queries_that_are_not_finite_stay_on_their_paths(which):
+    """A key that is not finite concerns the nodes whose path holds it, a query its own node only."""
+    trees = make("wide") + make("packed")
+    for dtype in ("bf16", "f32"):
+        x = inputs(trees, 1, 2, 128, 128, dtype, seed=9)
+        clean = scan(x, trees)
+        y = x[which].clone()
+        y[4, 0, 3:5] = float("nan")
+        out = scan([y if i == which else t for i, t in enumerate(x)], trees)
+        on = [i for i in range(63) if (4 in paths(trees[0])[i] if which else i == 4)]
+        off = [i for i in range(y.shape[0]) if i not in on]
+        assert torch.equal(out[off], clean[off])
+        assert torch.isnan(out[on]).all()
+
+
+@pytest.mark.parametrize("T", [5, 20, 50])
+@pytest.mark.parametrize("cycles", ["1", "3000"])
+def test_waits_that_run_out_are_reported_and_the_next_call_is_right(T, cycles, monkeypatch):
+    """GDN_TEST_WAIT_CYCLES shortens the limit of the kernel's waits for its copies."""
+    trees = [random_tree(np.random.RandomState(n), T) for n in range(40)]
+    x = inputs(trees, 4, 8, 128, 128, "bf16", seed=14)
+    q, k, v, g, b, S = (t.to(DEV) for t in x)
+    parents, out = flat(trees), torch.empty_like(v)
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    monkeypatch.setenv("GDN_TEST_WAIT_CYCLES", cycles)
+    torch.zeros(1 << 29, dtype=torch.uint8, device=DEV)  # (larger than L2)
+    gdn.gdn_tree_scan(q, k, v, g, b, S, parents, out)
+    torch.cuda.synchronize()
+    status = gdn.gdn_get_device_status()
+    # (a wait sleeps in the hardware between looks at its limit, so 3000 cycles may pass unnoticed)
+    assert status == gdn.GDN_ERR_DEVICE_CHECK or (cycles == "3000" and status == gdn.GDN_OK)
+    monkeypatch.delenv("GDN_TEST_WAIT_CYCLES")
+    out.fill_(float("nan"))
+    gdn.gdn_tree_scan(q, k, v, g, b, S, parents, out)
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    first = [t[:T] for t in x[:5]] + [x[5][:1]]
+    assert_scan(out[:T], *tree_scan(*first, trees[:1]), 128)
+    assert torch.equal(out, scan(x, trees))
+
+
 def test_a_tree_in_pieces():
     """Scan, advance along a path, and the same path token by token by the decode step: one state."""
     trees = make("few")
