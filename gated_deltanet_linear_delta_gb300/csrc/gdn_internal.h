@@ -122,7 +122,8 @@ cudaError_t launch_attn_rows(const AttnArgs &a, cudaStream_t s);
 
 cudaError_t launch_kv_keep(const KeepArgs &a, cudaStream_t s);
 cudaError_t launch_tree_scan(const TreeArgs &a, cudaStream_t s);
-cudaError_t launch_tree_scan_tc(const TreeArgs &a, cudaStream_t s);  // bf16
+cudaError_t launch_tree_scan_tc(const TreeArgs &a, cudaStream_t s);    // bf16
+cudaError_t launch_tree_scan_umma(const TreeArgs &a, cudaStream_t s);  // bf16, dk = dv = 128
 cudaError_t launch_tree_advance(const TreeArgs &a, cudaStream_t s);
 cudaError_t launch_tree_verify(const VerifyArgs &a, cudaStream_t s);
 

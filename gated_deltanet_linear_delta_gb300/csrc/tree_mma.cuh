@@ -2,8 +2,7 @@
 // (mma.sync), their operands from shared memory, and fp32 values split into bf16 terms.
 #pragma once
 
-#include "tc_ops.cuh"
-#include "tree.cuh"
+#include "attn_ops.cuh"
 
 namespace gdn {
 
@@ -39,8 +38,263 @@ __device__ __forceinline__ uint32_t row_piece(int r, int ch) {
 }
 // 32 columns of a state, rows of 128 bytes: 32 bytes of 4 rows 2 apart lie in different banks
 __device__ __forceinline__ uint32_t state_piece(int r, int ch) { return (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4)); }
-// block (i, j <= i) of 16 x 16 coefficients, 64 bytes a row (fp32, or two bf16 terms each); rows spread as above
-__device__ __forceinline__ uint32_t coef_block(int i, int j) { return (uint32_t)((i * (i + 1) / 2 + j) * 1024); }
-__device__ __forceinline__ uint32_t coef_piece(int r, int ch) { return (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)); }
+// ---- coefficients between nodes: row t, columns s (a multiple of 4: 16 bytes of fp32, or 8 bytes of each bf16 term) -------
+// Blocks (i, j <= i) of 16 x 16, 64 bytes a row: for ldmatrix. Rows spread as above.
+struct CoefBlocks {
+    uint8_t *base;
+    __device__ __forceinline__ static uint32_t piece(int r, int ch) { return (uint32_t)(r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)); }
+    __device__ __forceinline__ static uint32_t block(int i, int j) { return (uint32_t)((i * (i + 1) / 2 + j) * 1024); }
+    __device__ __forceinline__ float *raw(int t, int s) const {
+        return reinterpret_cast<float *>(base + block(t >> 4, s >> 4) + piece(t & 15, (s & 15) >> 2));
+    }
+    // 4 upper and 4 lower terms, within the row's own 64 bytes of the block
+    __device__ __forceinline__ void store(int t, int s, uint2 up, uint2 low) const {
+        uint8_t *at = base + block(t >> 4, s >> 4);
+        const int ch = (s & 15) >> 3, half = 8 * ((s >> 2) & 1);
+        *reinterpret_cast<uint2 *>(at + piece(t & 15, ch) + half) = up;
+        *reinterpret_cast<uint2 *>(at + piece(t & 15, 2 + ch) + half) = low;
+    }
+    static constexpr bool kWhole = false;  // blocks above the diagonal do not exist
+};
+// Rows of 128 bytes, 128B swizzle: TP rows of upper terms, then TP of lower ones (a tcgen05 operand); as fp32 a row fills both.
+template <int TP>
+struct CoefRows {
+    uint8_t *base;
+    __device__ __forceinline__ static uint32_t piece(int r, int ch) { return (uint32_t)(r * 128 + ((ch ^ (r & 7)) << 4)); }
+    __device__ __forceinline__ float *raw(int t, int s) const {
+        return reinterpret_cast<float *>(base + (s >> 5) * (TP * 128) + piece(t, (s & 31) >> 2));
+    }
+    __device__ __forceinline__ void store(int t, int s, uint2 up, uint2 low) const {
+        uint8_t *at = base + piece(t, s >> 3) + 8 * ((s >> 2) & 1);
+        *reinterpret_cast<uint2 *>(at) = up;
+        *reinterpret_cast<uint2 *>(at + TP * 128) = low;
+    }
+    static constexpr bool kWhole = true;
+};
+
+// ---- the nodes of a head ---------------------------------------------------------------------------
+struct __align__(16) Scalars {  // of a node
+    float beta, x;   // beta;  beta e^G rk, the factor of X_k
+    float z, rk;     // e^G rq, the factor of X_q;  1 / |k|
+    float rq, b2;    // 1 / |q|;  beta rk^2
+    float g, g_lo;   // G as a sum of two
+};
+
+struct Head {
+    int n, h, nodes;
+    long bos, slot;
+};
+
+// Heads by turns over the CTAs; those of padding sequences are written as zeros on the way.
+template <int DV, int THREADS>
+struct Heads {
+    int n, h, dn, dh;
+    __device__ __forceinline__ explicit Heads(const TreeArgs &a)
+        : n((int)(blockIdx.x / a.Hv)), h((int)(blockIdx.x % a.Hv)), dn((int)(gridDim.x / a.Hv)), dh((int)(gridDim.x % a.Hv)) {}
+    __device__ __forceinline__ void step(const TreeArgs &a) {
+        n += dn;
+        if ((h += dh) >= a.Hv) {
+            h -= a.Hv;
+            ++n;
+        }
+    }
+    // the first from the one at hand on that has nodes and a state (slot < 0: none)
+    __device__ __forceinline__ Head find(const TreeArgs &a) {
+        Head hd{0, 0, 0, 0, -1};
+        for (; n < a.B; step(a)) {
+            hd.n = n;
+            hd.h = h;
+            if (!tree_bounds(a.cu, n, a.B, a.cu ? a.Ttot : a.T, &hd.bos, &hd.nodes, a.status) || hd.nodes == 0) continue;
+            hd.slot = state_slot(a, n);
+            if (hd.slot >= 0) return hd;
+            __nv_bfloat16 *out = (__nv_bfloat16 *)a.out;
+            for (int e = threadIdx.x; e < hd.nodes * (DV / 8); e += THREADS)
+                reinterpret_cast<uint4 *>(out + ((hd.bos + e / (DV / 8)) * a.Hv + h) * DV)[e % (DV / 8)] = make_uint4(0, 0, 0, 0);
+        }
+        hd.slot = -1;
+        return hd;
+    }
+    __device__ __forceinline__ Head after(const TreeArgs &a, const Head &from) {
+        if (from.slot < 0) return from;
+        step(a);
+        return find(a);
+    }
+};
+
+// What the nodes' threads know of a node ahead: the last TP threads of the CTA; the last warp works the paths out.
+template <int TP, int THREADS>
+struct Nodes {
+    int up0 = -2, up1 = -2;
+    float g = 0.f, b = 0.f;
+    __device__ __forceinline__ static int node() { return (int)threadIdx.x - (THREADS - TP); }
+    __device__ __forceinline__ void load(const TreeArgs &a, const Head &hd) {
+        up0 = up1 = -2;
+        g = b = 0.f;
+        if (hd.slot < 0) return;
+        const int t = node(), lane = threadIdx.x & 31;
+        if (t >= 0 && t < hd.nodes) {
+            g = to_f32(((const __nv_bfloat16 *)a.g)[(hd.bos + t) * a.Hv + hd.h]);
+            b = to_f32(((const __nv_bfloat16 *)a.b)[(hd.bos + t) * a.Hv + hd.h]);
+        }
+        if (threadIdx.x >= THREADS - 32) {
+            if (lane < hd.nodes) up0 = a.parents[hd.bos + lane];
+            if (TP > 32 && lane + 32 < hd.nodes) up1 = a.parents[hd.bos + lane + 32];
+        }
+    }
+    // Paths into `paths`, and the sum of g over the own node's; by the last warps alone.
+    __device__ __forceinline__ void sums(int T, uint64_t *paths, float *gs, int *status, float &hi, float &lo) const {
+        const int t = node(), lane = threadIdx.x & 31;
+        hi = lo = 0.f;
+        if (t < 0 && !(TP < 32 && threadIdx.x >= THREADS - 32)) return;
+        if (t >= 0) gs[t] = g;
+        if (threadIdx.x >= THREADS - 32) {
+            const Paths p = tree_paths(up0, up1, status);
+            if (lane < TP) paths[lane] = p.of(0);
+            if (TP > 32) paths[lane + 32] = p.of(1);
+        }
+        if (TP > 32) tc::bar_sync(1, 64);
+        else __syncwarp();
+        if (t >= 0 && t < T)
+            for (uint64_t m = paths[t]; m; m &= m - 1) add_exact(hi, lo, gs[__ffsll((long long)m) - 1]);
+        __syncwarp();
+    }
+    // ... and with the products' diagonals at hand, the rest
+    __device__ __forceinline__ void finish(int T, const CoefBlocks &kk, const float *qq, float hi, float lo, Scalars *sc) const {
+        const int t = node();
+        if (t < 0) return;
+        const float k2 = t < T ? kk.raw(t, t & ~3)[t & 3] : 0.f;
+        Scalars s;
+        const float eg = __expf(hi + lo);
+        s.beta = sigmoidf_(b);
+        s.rk = rsqrtf(k2 + kNormEps);
+        s.rq = rsqrtf(qq[t] + kNormEps);
+        s.x = s.beta * eg * s.rk;
+        s.z = eg * s.rq;
+        s.b2 = s.beta * s.rk * s.rk;
+        s.g = hi;
+        s.g_lo = lo;
+        sc[t] = s;
+    }
+};
+
+// K K^T into kk, Q K^T into w, block by block of 16 x 16, and |q|^2 into qq. K's rows are 0 .. of the tile at shared address
+// kq, Q's TP .. . Warps take blocks from the counter `unit`, so that those which are late take fewer.
+template <int DK, int TP, typename W>
+__device__ __forceinline__ void node_products(uint32_t kq, int nb, int *unit, const CoefBlocks &kk, const W &w, float *qq) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    while (true) {
+        int u = 0;
+        if (lane == 0) u = atomicAdd(unit, 1);
+        u = __shfl_sync(0xffffffffu, u, 0);
+        if (u >= nb * (nb + 2)) break;
+        const bool square = u >= nb * (nb + 1);  // Q Q^T of a block, for its diagonal
+        const bool is_q = square || (u & 1);
+        int i = 0, j = u >> 1;  // the block's rows and columns, j <= i
+        while (j > i) j -= ++i;
+        if (square) i = j = u - nb * (nb + 1);
+        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        const int ra = (is_q ? TP : 0) + 16 * i + (lane & 15), rb = (square ? TP : 0) + 16 * j + ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+        for (int ks = 0; ks < DK / 16; ++ks) {
+            uint32_t x[4], y[4];
+            load_matrices(x, kq + row_piece<DK, 2 * TP>(ra, 2 * ks + (lane >> 4)));
+            load_matrices(y, kq + row_piece<DK, 2 * TP>(rb, 2 * ks + ((lane >> 3) & 1)));
+            mma_bf16_16816(acc[0], x, y[0], y[1]);
+            mma_bf16_16816(acc[1], x, y[2], y[3]);
+        }
+        if (square) {
+            if (c == g >> 1) {  // this lane's columns 2 c, 2 c + 1 hold the diagonal's of rows g and g + 8
+                qq[16 * i + g] = acc[0][g & 1];
+                qq[16 * i + 8 + g] = acc[1][2 + (g & 1)];
+            }
+            continue;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int t = 16 * i + g + 8 * half, s = 16 * j + 8 * n + 4 * (c >> 1);
+                float *to = (is_q ? w.raw(t, s) : kk.raw(t, s)) + 2 * (c & 1);
+                *reinterpret_cast<float2 *>(to) = make_float2(acc[n][2 * half], acc[n][2 * half + 1]);
+            }
+    }
+}
+
+// Q K^T in w becomes W, as two bf16 terms. A row by four lanes: lane `sub` holds columns 16 j + 4 sub .. + 3.
+template <int TP, int THREADS, typename WT>
+__device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scalars *sc, const CoefBlocks &kk, const WT &wt) {
+    constexpr int NB = TP / 16;
+    const int lane = threadIdx.x & 31, sub = lane & 3, nb = (T + 15) / 16;
+    for (int t = (int)threadIdx.x >> 2; t < 16 * nb; t += THREADS / 4) {
+        const uint64_t on = t < T ? paths[t] : 0;
+        const Scalars st = sc[t];
+        float w[NB][4];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            const float4 x = j <= t >> 4 ? *reinterpret_cast<const float4 *>(wt.raw(t, 16 * j + 4 * sub))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+            w[j][0] = st.rq * x.x; w[j][1] = st.rq * x.y; w[j][2] = st.rq * x.z; w[j][3] = st.rq * x.w;
+        }
+#pragma unroll
+        for (int j = NB - 1; j >= 0; --j) {
+            uint32_t left = (uint32_t)(on >> (16 * j)) & 0xffffu;
+            // (the warp's eight rows step together, each along its own path: rows that part ways would run one by one)
+            while (__any_sync(0xffffffffu, left != 0)) {
+                const int s = 31 - __clz(left | 1);  // of the block's nodes; w_s is final
+                const int e = s & 3;
+                const float own = e == 0 ? w[j][0] : e == 1 ? w[j][1] : e == 2 ? w[j][2] : w[j][3];
+                const float ws = -__shfl_sync(0xffffffffu, own, (lane & ~3) | (s >> 2)) * sc[16 * j + s].b2;
+                if (left != 0) {
+                    left &= ~(1u << s);
+                    const int before = s - 4 * sub;  // columns of this lane that stand before s, in s's own block
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        if (i > j) continue;
+                        const float4 x = *reinterpret_cast<const float4 *>(kk.raw(16 * j + s, 16 * i + 4 * sub));
+                        w[i][0] = fmaf(ws, i < j || before > 0 ? x.x : 0.f, w[i][0]);
+                        w[i][1] = fmaf(ws, i < j || before > 1 ? x.y : 0.f, w[i][1]);
+                        w[i][2] = fmaf(ws, i < j || before > 2 ? x.z : 0.f, w[i][2]);
+                        w[i][3] = fmaf(ws, i < j || before > 3 ? x.w : 0.f, w[i][3]);
+                    }
+                }
+            }
+        }
+        __syncwarp();  // the row has been read by all of its lanes
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            if (!WT::kWhole && j > t >> 4) continue;
+            const uint32_t mine = (uint32_t)(on >> (16 * j)) >> (4 * sub);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Scalars ss = sc[16 * j + 4 * sub + e];
+                w[j][e] = mine & (1u << e) ? w[j][e] * (__expf((st.g - ss.g) + (st.g_lo - ss.g_lo)) * ss.rk) : 0.f;
+            }
+            uint2 up, low;
+            up.x = split2(w[j][0], w[j][1]);
+            up.y = split2(w[j][2], w[j][3]);
+            low.x = tc::bf2_bits(__floats2bfloat162_rn(w[j][0], w[j][1]));
+            low.y = tc::bf2_bits(__floats2bfloat162_rn(w[j][2], w[j][3]));
+            wt.store(t, 16 * j + 4 * sub, up, low);
+        }
+    }
+}
+
+// x [outer][mid][inner] -> boxes of box_inner columns and rows along one of the other dimensions, swizzled over their bytes
+inline bool scan_map(CUtensorMap *m, const void *base, bool f32, int inner, long mid, long outer, int box_inner, int box_mid,
+                     int box_outer) {
+    EncodeTiledFn enc = tiled_encoder();
+    if (!enc) return false;
+    const cuuint64_t elem = f32 ? 4 : 2, bytes = box_inner * elem;
+    const cuuint64_t gdim[3] = {(cuuint64_t)inner, (cuuint64_t)mid, (cuuint64_t)outer};
+    const cuuint64_t gstride[2] = {inner * elem, (cuuint64_t)mid * inner * elem};
+    const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_mid, (cuuint32_t)box_outer};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), gdim,
+               gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+               : bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                             : CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace gdn

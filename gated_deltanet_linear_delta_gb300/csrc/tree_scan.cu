@@ -144,7 +144,7 @@ cudaError_t launch_dv(const TreeArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_scan(const TreeArgs &a, cudaStream_t s) {
-    if (a.dtype != GDN_F32) return launch_tree_scan_tc(a, s);
+    if (a.dtype != GDN_F32) return a.dk == 128 && a.dv == 128 ? launch_tree_scan_umma(a, s) : launch_tree_scan_tc(a, s);
     switch (a.dk) {
         case 32: return launch_dv<32>(a, s);
         case 64: return launch_dv<64>(a, s);

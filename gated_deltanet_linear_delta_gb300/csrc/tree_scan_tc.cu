@@ -21,7 +21,6 @@
 //
 // Values that are not finite stay on their paths: a product with a coefficient of 0 would spread them, so they are
 // left out of the products, and the outputs that have them on their path become NaN.
-#include "attn_ops.cuh"
 #include "tree_mma.cuh"
 
 namespace gdn {
@@ -34,7 +33,7 @@ struct Cfg {
     static constexpr int NQ = DK / 32, RING = TP == 16 ? 4 : 3;  // parts of a state; slots
     static constexpr uint32_t SLOT = DV * 128;
     static constexpr int BLOCKS = NB * (NB + 1) / 2;
-    static constexpr uint32_t KQ_BYTES = TP * DK * 2;
+    static constexpr uint32_t KQ_BYTES = TP * DK * 2, ROW = DK >= 64 ? 128 : 64;  // bytes of a row of a block of columns
     // byte offsets
     static constexpr uint32_t SM_KQ = 0;                                      // K, then Q [TP][DK] bf16
     static constexpr uint32_t SM_S = (2 * KQ_BYTES + 1023) & ~1023u;           // [RING][DV][32] fp32
@@ -49,18 +48,6 @@ struct Cfg {
     static constexpr uint32_t SM_BYTES = SM_UNIT + 8;
     static constexpr int FIT = 233472 / (SM_BYTES + 1024), PER_SM = FIT < 3 ? FIT : 3;  // CTAs to an SM
     static_assert(PER_SM >= 2, "two CTAs to an SM");
-};
-
-struct __align__(16) Scalars {  // of a node
-    float beta, x;   // beta;  beta e^G rk, the factor of X_k
-    float z, rk;     // e^G rq, the factor of X_q;  1 / |k|
-    float rq, b2;    // 1 / |q|;  beta rk^2
-    float g, g_lo;   // G as a sum of two
-};
-
-struct Head {
-    int n, h, nodes;
-    long bos, slot;
 };
 
 template <int DK, int DV, int TP>
@@ -78,7 +65,7 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
     float *gs = reinterpret_cast<float *>(sm + C::SM_G), *qq = reinterpret_cast<float *>(sm + C::SM_R);
     uint64_t *bar_kq = reinterpret_cast<uint64_t *>(sm + C::SM_BAR), *bar_s = bar_kq + 1;
     int *unit = reinterpret_cast<int *>(sm + C::SM_UNIT);
-    const __nv_bfloat16 *v = (const __nv_bfloat16 *)a.v, *ga = (const __nv_bfloat16 *)a.g, *be = (const __nv_bfloat16 *)a.b;
+    const __nv_bfloat16 *v = (const __nv_bfloat16 *)a.v;
     __nv_bfloat16 *out = (__nv_bfloat16 *)a.out;
     next_may_begin();
     if (tid == 0) {
@@ -96,36 +83,7 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
         return;
     }
 
-    // Heads by turns over the CTAs. The next from (n, h) on that has nodes and a state; heads of padding sequences are
-    // written as zeros on the way.
-    const int dn = (int)(gridDim.x / a.Hv), dh = (int)(gridDim.x % a.Hv);
-    int at_n = (int)(blockIdx.x / a.Hv), at_h = (int)(blockIdx.x % a.Hv);
-    auto step = [&] {
-        at_n += dn;
-        if ((at_h += dh) >= a.Hv) {
-            at_h -= a.Hv;
-            ++at_n;
-        }
-    };
-    auto find = [&]() -> Head {
-        Head hd{0, 0, 0, 0, -1};
-        for (; at_n < a.B; step()) {
-            hd.n = at_n;
-            hd.h = at_h;
-            if (!tree_bounds(a.cu, hd.n, a.B, a.cu ? a.Ttot : a.T, &hd.bos, &hd.nodes, a.status) || hd.nodes == 0) continue;
-            hd.slot = state_slot(a, hd.n);
-            if (hd.slot >= 0) return hd;
-            for (int e = tid; e < hd.nodes * (DV / 8); e += C::THREADS)
-                reinterpret_cast<uint4 *>(out + ((hd.bos + e / (DV / 8)) * a.Hv + hd.h) * DV)[e % (DV / 8)] = make_uint4(0, 0, 0, 0);
-        }
-        hd.slot = -1;
-        return hd;
-    };
-    auto step_to = [&](const Head &from) -> Head {
-        if (from.slot < 0) return from;
-        step();
-        return find();
-    };
+    Heads<DV, C::THREADS> heads(a);
     // Copies, by one thread. Keys and queries of TP tokens, whatever a sequence's number of nodes.
     uint32_t copies_kq = 0, copies_s = 0;  // begun
     auto load_kq = [&](const Head &hd) {
@@ -136,8 +94,8 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
         mbar_expect_tx(bar_kq, 2 * C::KQ_BYTES);
 #pragma unroll
         for (int b = 0; b < (DK >= 64 ? DK / 64 : 1); ++b) {
-            tma_load_3d(sm + C::SM_KQ + b * (TP * 128), &mk, 64 * b, hk, (int)hd.bos, bar_kq);
-            tma_load_3d(sm + C::SM_KQ + C::KQ_BYTES + b * (TP * 128), &mq, 64 * b, hk, (int)hd.bos, bar_kq);
+            tma_load_3d(sm + C::SM_KQ + b * (2 * TP * 128), &mk, 64 * b, hk, (int)hd.bos, bar_kq);
+            tma_load_3d(sm + C::SM_KQ + b * (2 * TP * 128) + TP * C::ROW, &mq, 64 * b, hk, (int)hd.bos, bar_kq);
         }
     };
     auto load_state = [&](bool any, int state, int part, int slot) {
@@ -148,23 +106,8 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
         tma_load_3d(sm + C::SM_S + slot * C::SLOT, &ms, 32 * part, 0, state, bar_s + slot);
     };
     auto state_of = [&](const Head &hd) { return (int)(hd.slot * a.Hv + hd.h); };
-    // The nodes' threads are those of the last warps; the last one works the paths out.
-    const int node = tid - (C::THREADS - TP);
-    int up0 = -2, up1 = -2;
-    float gv = 0.f, bv = 0.f;
-    auto load_nodes = [&](const Head &hd) {
-        up0 = up1 = -2;
-        gv = bv = 0.f;
-        if (hd.slot < 0) return;
-        if (node >= 0 && node < hd.nodes) {
-            gv = to_f32(ga[(hd.bos + node) * a.Hv + hd.h]);
-            bv = to_f32(be[(hd.bos + node) * a.Hv + hd.h]);
-        }
-        if (warp == C::WARPS - 1) {
-            if (lane < hd.nodes) up0 = a.parents[hd.bos + lane];
-            if (TP > 32 && lane + 32 < hd.nodes) up1 = a.parents[hd.bos + lane + 32];
-        }
-    };
+    Nodes<TP, C::THREADS> nodes;
+    const CoefBlocks kk{sm + C::SM_A}, wt{sm + C::SM_W};
 
     // Parts follow one another through the ring, head by head. When a head's products begin, as many parts as the ring
     // has slots are there or on their way; each slot is filled again once all warps are past it, the last one behind the
@@ -172,13 +115,13 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
     constexpr int AHEAD = (C::RING + C::NQ - 1) / C::NQ;  // heads to know of beside the one at hand
     static_assert(AHEAD <= 4, "heads ahead");
     Head hd[AHEAD + 1];
-    hd[0] = find();
+    hd[0] = heads.find(a);
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) hd[i + 1] = step_to(hd[i]);
+    for (int i = 0; i < AHEAD; ++i) hd[i + 1] = heads.after(a, hd[i]);
     load_kq(hd[0]);
 #pragma unroll
     for (int i = 0; i < C::RING; ++i) load_state(hd[i / C::NQ].slot >= 0, state_of(hd[i / C::NQ]), i % C::NQ, i);
-    load_nodes(hd[0]);
+    nodes.load(a, hd[0]);
     int slot = 0;                 // of the part at hand
     uint32_t phase_kq = 0, phase_s = 0;
     bool ok = true;
@@ -191,135 +134,15 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
             ok = false;
             break;
         }
-        // ---- paths and gates; beside them K K^T and Q K^T, block by block of 16 x 16, and |q|^2 ----------
-        float hi = 0.f, lo = 0.f;
-        if (node >= 0 || (TP < 32 && warp == C::WARPS - 1)) {
-            if (node >= 0) gs[node] = gv;
-            if (warp == C::WARPS - 1) {
-                const Paths p = tree_paths(up0, up1, a.status);
-                if (lane < TP) paths[lane] = p.of(0);
-                if (TP > 32) paths[lane + 32] = p.of(1);
-            }
-            if (TP > 32) bar_sync(1, 64);
-            else __syncwarp();
-            if (node >= 0 && node < T)
-                for (uint64_t m = paths[node]; m; m &= m - 1) add_exact(hi, lo, gs[__ffsll((long long)m) - 1]);
-            __syncwarp();
-        }
-        while (true) {
-            int u = 0;
-            if (lane == 0) u = atomicAdd(unit, 1);
-            u = __shfl_sync(0xffffffffu, u, 0);
-            if (u >= nb * (nb + 2)) break;
-            const bool square = u >= nb * (nb + 1);  // Q Q^T of a block, for its diagonal
-            const bool is_q = square || (u & 1);
-            int i = 0, j = u >> 1;  // the block's rows and columns, j <= i
-            while (j > i) j -= ++i;
-            if (square) i = j = u - nb * (nb + 1);
-            float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const int ra = 16 * i + (lane & 15), rb = 16 * j + ((lane >> 4) << 3) + (lane & 7);
-            const uint32_t xa = sb + C::SM_KQ + (is_q ? C::KQ_BYTES : 0), xb = sb + C::SM_KQ + (square ? C::KQ_BYTES : 0);
-#pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks) {
-                uint32_t x[4], y[4];
-                load_matrices(x, xa + row_piece<DK, TP>(ra, 2 * ks + (lane >> 4)));
-                load_matrices(y, xb + row_piece<DK, TP>(rb, 2 * ks + ((lane >> 3) & 1)));
-                mma_bf16_16816(acc[0], x, y[0], y[1]);
-                mma_bf16_16816(acc[1], x, y[2], y[3]);
-            }
-            if (square) {
-                if (c == g >> 1) {  // this lane's columns 2 c, 2 c + 1 hold the diagonal's of rows g and g + 8
-                    qq[16 * i + g] = acc[0][g & 1];
-                    qq[16 * i + 8 + g] = acc[1][2 + (g & 1)];
-                }
-                continue;
-            }
-            uint8_t *to = sm + (is_q ? C::SM_W : C::SM_A) + coef_block(i, j);
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    *reinterpret_cast<float2 *>(to + coef_piece(g + 8 * half, 2 * n + (c >> 1)) + 8 * (c & 1)) =
-                        make_float2(acc[n][2 * half], acc[n][2 * half + 1]);
-        }
+        // ---- the nodes: paths and gates, beside them the products; norms; W --------------------------------
+        float hi, lo;
+        nodes.sums(T, paths, gs, a.status, hi, lo);
+        node_products<DK, TP>(sb + C::SM_KQ, nb, unit, kk, wt, qq);
         __syncthreads();
-        // ---- per node: norms ----------------------------------------------------------------------
         if (tid == 0) *unit = 0;
-        if (node >= 0) {
-            const float kk = node < T ? reinterpret_cast<const float *>(sm + C::SM_A + coef_block(node >> 4, node >> 4) +
-                                                                        coef_piece(node & 15, (node & 15) >> 2))[node & 3]
-                                      : 0.f;
-            Scalars s;
-            const float eg = __expf(hi + lo);
-            s.beta = sigmoidf_(bv);
-            s.rk = rsqrtf(kk + kNormEps);
-            s.rq = rsqrtf(qq[node] + kNormEps);
-            s.x = s.beta * eg * s.rk;
-            s.z = eg * s.rq;
-            s.b2 = s.beta * s.rk * s.rk;
-            s.g = hi;
-            s.g_lo = lo;
-            sc[node] = s;
-        }
+        nodes.finish(T, kk, qq, hi, lo, sc);
         __syncthreads();
-        // ---- W, a row of it by four lanes: lane `sub` holds columns 16 j + 4 sub .. + 3 ---------------------
-        for (int t = tid >> 2; t < 16 * nb; t += C::THREADS / 4) {
-            const int sub = tid & 3;
-            uint8_t *row = sm + C::SM_W + coef_block(t >> 4, 0);
-            const uint64_t on = t < T ? paths[t] : 0;
-            const Scalars st = sc[t];
-            float w[C::NB][4];
-#pragma unroll
-            for (int j = 0; j < C::NB; ++j) {
-                const float4 x = j <= t >> 4 ? *reinterpret_cast<const float4 *>(row + j * 1024 + coef_piece(t & 15, sub))
-                                             : make_float4(0.f, 0.f, 0.f, 0.f);
-                w[j][0] = st.rq * x.x; w[j][1] = st.rq * x.y; w[j][2] = st.rq * x.z; w[j][3] = st.rq * x.w;
-            }
-#pragma unroll
-            for (int j = C::NB - 1; j >= 0; --j) {
-                uint32_t left = (uint32_t)(on >> (16 * j)) & 0xffffu;
-                // (the warp's eight rows step together, each along its own path: rows that part ways would run one by one)
-                while (__any_sync(0xffffffffu, left != 0)) {
-                    const int s = 31 - __clz(left | 1);  // of the block's nodes; w_s is final
-                    const int e = s & 3;
-                    const float own = e == 0 ? w[j][0] : e == 1 ? w[j][1] : e == 2 ? w[j][2] : w[j][3];
-                    const float ws = -__shfl_sync(0xffffffffu, own, (lane & ~3) | (s >> 2)) * sc[16 * j + s].b2;
-                    if (left != 0) {
-                        left &= ~(1u << s);
-                        const uint8_t *kr = sm + C::SM_A + coef_block(j, 0) + coef_piece(s, sub);
-                        const int before = s - 4 * sub;  // columns of this lane that stand before s, in s's own block
-#pragma unroll
-                        for (int i = 0; i < C::NB; ++i) {
-                            if (i > j) continue;
-                            const float4 x = *reinterpret_cast<const float4 *>(kr + i * 1024);
-                            w[i][0] = fmaf(ws, i < j || before > 0 ? x.x : 0.f, w[i][0]);
-                            w[i][1] = fmaf(ws, i < j || before > 1 ? x.y : 0.f, w[i][1]);
-                            w[i][2] = fmaf(ws, i < j || before > 2 ? x.z : 0.f, w[i][2]);
-                            w[i][3] = fmaf(ws, i < j || before > 3 ? x.w : 0.f, w[i][3]);
-                        }
-                    }
-                }
-            }
-            // as two bf16 terms, in place: a row's 64 bytes of a block become 16 upper and 16 lower terms
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < C::NB; ++j) {
-                if (j > t >> 4) continue;
-                const uint32_t mine = (uint32_t)(on >> (16 * j)) >> (4 * sub);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Scalars ss = sc[16 * j + 4 * sub + e];
-                    w[j][e] = mine & (1u << e) ? w[j][e] * (__expf((st.g - ss.g) + (st.g_lo - ss.g_lo)) * ss.rk) : 0.f;
-                }
-                uint2 up, low;
-                up.x = split2(w[j][0], w[j][1]);
-                up.y = split2(w[j][2], w[j][3]);
-                low.x = bf2_bits(__floats2bfloat162_rn(w[j][0], w[j][1]));
-                low.y = bf2_bits(__floats2bfloat162_rn(w[j][2], w[j][3]));
-                *reinterpret_cast<uint2 *>(row + j * 1024 + coef_piece(t & 15, sub >> 1) + 8 * (sub & 1)) = up;
-                *reinterpret_cast<uint2 *>(row + j * 1024 + coef_piece(t & 15, 2 + (sub >> 1)) + 8 * (sub & 1)) = low;
-            }
-        }
+        form_w<TP, C::THREADS>(T, paths, sc, kk, wt);
         // ---- X = S_0 [K; Q]^T, and the values on their way ---------------------------------------
         const int row0 = 16 * warp + 2 * g;  // this lane's rows of the state (the products' rows g and g + 8): row0, row0 + 1
         uint32_t vv[C::NT][2];  // rows row0, row0 + 1 of nodes 8 n + 2 c, + 1
@@ -369,12 +192,12 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
                     if (j < nb) {
                         const int rr = 16 * j + ((lane >> 4) << 3) + (lane & 7), ch = 2 * ks + ((lane >> 3) & 1);
                         uint32_t y[4];
-                        load_matrices(y, sb + C::SM_KQ + row_piece<DK, TP>(rr, ch));
+                        load_matrices(y, sb + C::SM_KQ + row_piece<DK, 2 * TP>(rr, ch));
                         mma_bf16_16816(xk[2 * j], ah, y[0], y[1]);
                         mma_bf16_16816(xk[2 * j + 1], ah, y[2], y[3]);
                         mma_bf16_16816(xk[2 * j], al, y[0], y[1]);
                         mma_bf16_16816(xk[2 * j + 1], al, y[2], y[3]);
-                        load_matrices(y, sb + C::SM_KQ + C::KQ_BYTES + row_piece<DK, TP>(rr, ch));
+                        load_matrices(y, sb + C::SM_KQ + row_piece<DK, 2 * TP>(TP + rr, ch));
                         mma_bf16_16816(xq[2 * j], ah, y[0], y[1]);
                         mma_bf16_16816(xq[2 * j + 1], ah, y[2], y[3]);
                         mma_bf16_16816(xq[2 * j], al, y[0], y[1]);
@@ -396,7 +219,7 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
             const Head &far = hd[(C::NQ + C::RING - 1) / C::NQ];
             load_state(far.slot >= 0, state_of(far), (C::NQ + C::RING - 1) % C::NQ, slot == 0 ? C::RING - 1 : slot - 1);
         }
-        load_nodes(hd[1]);
+        nodes.load(a, hd[1]);
         // ---- R, and O ----------------------------------------------------------------------------------
         uint64_t bad0 = 0, bad1 = 0;  // nodes whose R is not finite in this lane's rows
         float sure = 0.f;
@@ -446,12 +269,12 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
             for (int i = j; i < C::NB; ++i) {
                 if (i >= nb) continue;
                 uint32_t y[4];
-                load_matrices(y, sb + C::SM_W + coef_block(i, j) + coef_piece(tr, ch));
+                load_matrices(y, sb + C::SM_W + CoefBlocks::block(i, j) + CoefBlocks::piece(tr, ch));
                 mma_bf16_16816(xq[2 * i], uh, y[0], y[1]);
                 mma_bf16_16816(xq[2 * i + 1], uh, y[2], y[3]);
                 mma_bf16_16816(xq[2 * i], ul, y[0], y[1]);
                 mma_bf16_16816(xq[2 * i + 1], ul, y[2], y[3]);
-                load_matrices(y, sb + C::SM_W + coef_block(i, j) + coef_piece(tr, 2 + ch));
+                load_matrices(y, sb + C::SM_W + CoefBlocks::block(i, j) + CoefBlocks::piece(tr, 2 + ch));
                 mma_bf16_16816(xq[2 * i], uh, y[0], y[1]);
                 mma_bf16_16816(xq[2 * i + 1], uh, y[2], y[3]);
             }
@@ -473,7 +296,7 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
             }
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i) hd[i] = hd[i + 1];
-        hd[AHEAD] = step_to(hd[AHEAD - 1]);
+        hd[AHEAD] = heads.after(a, hd[AHEAD - 1]);
     }
     if (!ok) {
         flag_error(a.status);
@@ -485,21 +308,6 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
         }
         __syncthreads();
     }
-}
-
-// x [outer][mid][inner] -> boxes of (32 or 64 columns, rows of one of the other dimensions), swizzled over their bytes
-bool scan_map(CUtensorMap *m, const void *base, bool f32, int inner, long mid, long outer, int box_inner, int box_mid, int box_outer) {
-    EncodeTiledFn enc = tiled_encoder();
-    if (!enc) return false;
-    const cuuint64_t elem = f32 ? 4 : 2;
-    const cuuint64_t gdim[3] = {(cuuint64_t)inner, (cuuint64_t)mid, (cuuint64_t)outer};
-    const cuuint64_t gstride[2] = {inner * elem, (cuuint64_t)mid * inner * elem};
-    const cuuint32_t box[3] = {(cuuint32_t)box_inner, (cuuint32_t)box_mid, (cuuint32_t)box_outer};
-    const cuuint32_t estride[3] = {1, 1, 1};
-    return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), gdim,
-               gstride, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               box_inner * elem == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DK, int DV, int TP>

@@ -1,0 +1,320 @@
+// tree_scan_umma.cu -- the gated delta rule over trees for bf16 inputs and heads of 128 x 128, on tcgen05.
+//
+// The products of tree_scan_tc.cu (whose head says what X, R and W are), with all 128 rows of the state as M:
+//     X = S_0 [K; Q]^T     A: S_0 split into two bf16 terms, in shared memory; B: keys and queries as they come by TMA
+//     D = R W^T            A: R as two bf16 terms, in TMEM; B: W as two terms (upper times upper, lower times upper, upper
+//                          times lower)
+// and o_t = e^{G_t} rq_t X_q,t + D_t. A thread stands for a row of the state and half of the nodes: it takes X_k out of
+// TMEM, forms R and puts it back, and takes X_q and D out at the end.
+//
+// Why this beside m16n8k16: there each warp feeds 16 rows with fragments of keys, queries and W (of 64 nodes 380
+// instructions for the products of a head alone, and as many around them), and with its accumulators in registers
+// only 16 warps fit an SM. Here the products are 40 instructions of one thread.
+//
+// A head's state comes to registers as two halves of 64 columns (the next head's first one early), and goes to shared
+// memory as terms, one half at a time, so that two CTAs fit an SM with 64 nodes and three with fewer.
+#include "tree_mma.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace tc;
+
+template <int TP>
+struct Cfg {
+    static constexpr int THREADS = 256, NB = TP / 16, HALF = TP / 2;  // blocks of nodes; a thread's nodes
+    static constexpr int BLOCKS = NB * (NB + 1) / 2;
+    static constexpr int CHUNK = HALF < 16 ? HALF : 16;               // nodes that a thread has in registers
+    // TMEM columns: X of keys and of queries, R's terms (two nodes a column), D
+    static constexpr uint32_t TM_X = 0, TM_R = 2 * TP, TM_D = 3 * TP, COLS = 4 * TP;
+    static constexpr uint32_t KQ_BLOCK = 2 * TP * 128, TERM = 128 * 128;
+    // byte offsets
+    static constexpr uint32_t SM_KQ = 0;                             // [2 blocks of 64 columns][K, Q: 2 TP rows] bf16
+    static constexpr uint32_t SM_X = SM_KQ + 2 * KQ_BLOCK;            // half of a state: upper terms, lower terms
+    static constexpr uint32_t SM_W = SM_X + 2 * TERM;                 // W: upper terms, lower terms (CoefRows)
+    static constexpr uint32_t SM_A = SM_W + 2 * TP * 128;             // K K^T (CoefBlocks)
+    static constexpr uint32_t SM_V = SM_A + BLOCKS * 1024;            // [TP][128] bf16
+    static constexpr uint32_t SM_SC = SM_V + TP * 256;                // per node: Scalars
+    static constexpr uint32_t SM_PATH = SM_SC + TP * 32;
+    static constexpr uint32_t SM_BAD = SM_PATH + TP * 8;              // [2][128] nodes whose R is not finite, by row
+    static constexpr uint32_t SM_G = SM_BAD + 1024;
+    static constexpr uint32_t SM_R = SM_G + TP * 4;                   // |q|^2
+    static constexpr uint32_t SM_BAR = SM_R + TP * 4;                 // keys, queries, values; X; D; the end
+    static constexpr uint32_t SM_UNIT = SM_BAR + 4 * 8, SM_TMEM = SM_UNIT + 4;
+    static constexpr uint32_t SM_BYTES = SM_TMEM + 4;
+    static constexpr int PER_SM = TP == 64 ? 2 : 3;
+    static_assert(PER_SM * (SM_BYTES + 1024) <= 233472 && PER_SM * COLS <= 512, "CTAs to an SM");
+};
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&x)[N]) {
+    uint32_t r[N];
+    if constexpr (N == 16) tmem_ld16_nw(at, r);
+    else tmem_ld8_nw(at, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
+}
+
+template <int TP>
+__global__ void __launch_bounds__(Cfg<TP>::THREADS, Cfg<TP>::PER_SM)
+tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mq,
+                      const __grid_constant__ CUtensorMap mv, const TreeArgs a, long long budget) {
+    using C = Cfg<TP>;
+    // (on a 1 KiB boundary, as all of it is asked for at launch: checked, as room to align it may cost a CTA)
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sb = smem_u32(sm);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Scalars *sc = reinterpret_cast<Scalars *>(sm + C::SM_SC);
+    uint64_t *paths = reinterpret_cast<uint64_t *>(sm + C::SM_PATH);
+    uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::SM_BAD);
+    float *gs = reinterpret_cast<float *>(sm + C::SM_G), *qq = reinterpret_cast<float *>(sm + C::SM_R);
+    uint64_t *bar_in = reinterpret_cast<uint64_t *>(sm + C::SM_BAR), *bar_x = bar_in + 1, *bar_d = bar_in + 2, *bar_end = bar_in + 3;
+    int *unit = reinterpret_cast<int *>(sm + C::SM_UNIT);
+    uint32_t *tmem_at = reinterpret_cast<uint32_t *>(sm + C::SM_TMEM);
+    __nv_bfloat16 *out = (__nv_bfloat16 *)a.out;
+    next_may_begin();
+    if (tid == 0) {
+        prefetch_tmap(&mk);
+        prefetch_tmap(&mq);
+        prefetch_tmap(&mv);
+        for (int i = 0; i < 4; ++i) mbar_init(bar_in + i, 1);
+        fence_mbar_init();
+        *unit = 0;
+    }
+    before_reading();  // (and before TMEM is asked for: a kernel that ends may still hold it)
+    if (warp == 0) tmem_alloc(tmem_at, C::COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+    if (sb & 1023u) {
+        flag_error(a.status);
+        if (warp == 0) tmem_dealloc(tmem, C::COLS);
+        return;
+    }
+    bool ok = true;  // the same for a warp's lanes
+
+    Heads<128, C::THREADS> heads(a);
+    Nodes<TP, C::THREADS> nodes;
+    const CoefBlocks kk{sm + C::SM_A};
+    const CoefRows<TP> wt{sm + C::SM_W};
+    uint32_t loads = 0;  // of keys, queries and values, begun
+    auto load_in = [&](const Head &hd) {
+        if (hd.slot < 0) return;
+        ++loads;
+        if (tid != 0) return;
+        const int hk = hd.h / (a.Hv / a.Hk);
+        mbar_expect_tx(bar_in, 2 * C::KQ_BLOCK + TP * 256);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            tma_load_3d(sm + C::SM_KQ + b * C::KQ_BLOCK, &mk, 64 * b, hk, (int)hd.bos, bar_in);
+            tma_load_3d(sm + C::SM_KQ + b * C::KQ_BLOCK + TP * 128, &mq, 64 * b, hk, (int)hd.bos, bar_in);
+        }
+        tma_load_3d(sm + C::SM_V, &mv, 0, hd.h, (int)hd.bos, bar_in);
+    };
+    // half of a state, 64 columns: this thread's 16 bytes (columns 4 ch ..) of 8 rows
+    const int sr = tid >> 4, ch = tid & 15;
+    float4 half[8];
+    auto load_half = [&](const Head &hd, int h) {
+        if (hd.slot < 0) return;
+        const float *src = a.state_in + (hd.slot * a.Hv + hd.h) * 16384 + sr * 128 + h * 64 + ch * 4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) half[i] = __ldcs(reinterpret_cast<const float4 *>(src + i * 16 * 128));
+    };
+    auto split_half = [&] {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = sr + 16 * i;
+            float4 x = half[i];
+            uint2 up, low;
+            up.x = split2(x.x, x.y);
+            up.y = split2(x.z, x.w);
+            low.x = bf2_bits(__floats2bfloat162_rn(x.x, x.y));
+            low.y = bf2_bits(__floats2bfloat162_rn(x.z, x.w));
+            uint8_t *at = sm + C::SM_X + swz(r, ch >> 1) + 8 * (ch & 1);
+            *reinterpret_cast<uint2 *>(at) = up;
+            *reinterpret_cast<uint2 *>(at + C::TERM) = low;
+        }
+        fence_async_smem();
+    };
+    auto product_x = [&](int h) {  // by one thread
+        constexpr uint32_t ID = idesc_bf16(128, 2 * TP, 0, 0);
+        const uint64_t x = desc_sw128(sb + C::SM_X, 16, 1024), y = desc_sw128(sb + C::SM_KQ + h * C::KQ_BLOCK, 16, 1024);
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                mma_bf16(tmem + C::TM_X, x + (uint64_t)((term * C::TERM + ks * 32) >> 4), y + (uint64_t)(ks * 2), ID,
+                         h > 0 || term > 0 || ks > 0);
+        mma_commit(bar_x);
+    };
+    auto product_d = [&] {  // by one thread
+        constexpr uint32_t ID = idesc_bf16(128, TP, 0, 0);
+        const uint64_t y = desc_sw128(sb + C::SM_W, 16, 1024);
+#pragma unroll
+        for (int term = 0; term < 3; ++term)  // R upper W upper, R lower W upper, R upper W lower
+#pragma unroll
+            for (int ks = 0; ks < TP / 16; ++ks)
+                mma_bf16_ts(tmem + C::TM_D, tmem + C::TM_R + (term == 1 ? TP / 2 : 0) + 8 * ks,
+                            y + (uint64_t)(((term == 2 ? TP * 128 : 0) + ks * 32) >> 4), ID, term > 0 || ks > 0);
+        mma_commit(bar_d);
+    };
+    const int part = warp >> 2, row = 32 * (warp & 3) + lane, t_first = part * C::HALF;  // this thread's row and nodes
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+
+    Head cur = heads.find(a), next = heads.after(a, cur);
+    load_in(cur);
+    load_half(cur, 0);
+    nodes.load(a, cur);
+    uint32_t phase_in = 0, phase_x = 0, phase_d = 0;
+    while (cur.slot >= 0) {
+        const int T = cur.nodes, nb = (T + 15) / 16;
+        // ---- the state's first half; then the nodes beside its products ---------------------------
+        split_half();
+        load_half(cur, 1);
+        ok = warp_wait(bar_in, phase_in, budget) && ok;
+        phase_in ^= 1;
+        tc_fence_before();
+        if (__syncthreads_or(!ok)) break;  // (and all that the head before has left has been read)
+        if (tid == 0) {
+            tc_fence_after();
+            product_x(0);
+        }
+        __syncwarp();
+        float hi, lo;
+        nodes.sums(T, paths, gs, a.status, hi, lo);
+        node_products<128, TP>(sb + C::SM_KQ, nb, unit, kk, wt, qq);
+        __syncthreads();
+        if (tid == 0) *unit = 0;
+        nodes.finish(T, kk, qq, hi, lo, sc);
+        // ---- its second half; W beside its products -------------------------------------------------
+        ok = warp_wait(bar_x, phase_x, budget);
+        phase_x ^= 1;
+        if (ok) split_half();
+        load_half(next, 0);
+        if (__syncthreads_or(!ok)) break;
+        if (tid == 0) {
+            tc_fence_after();
+            product_x(1);
+        }
+        __syncwarp();
+        form_w<TP, C::THREADS>(T, paths, sc, kk, wt);
+        fence_async_smem();
+        // ---- R ------------------------------------------------------------------------------------------
+        ok = warp_wait(bar_x, phase_x, budget);
+        phase_x ^= 1;
+        tc_fence_after();
+        uint32_t not_finite = 0;  // of this thread's nodes
+#pragma unroll
+        for (int c0 = 0; c0 < C::HALF; c0 += C::CHUNK) {
+            float x[C::CHUNK], sure = 0.f;
+            tmem_load(tl + C::TM_X + t_first + c0, x);
+#pragma unroll
+            for (int i = 0; i < C::CHUNK; ++i) {
+                const int t = t_first + c0 + i;
+                const float2 s = *reinterpret_cast<const float2 *>(sc + t);  // beta, x
+                const float v = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(sm + C::SM_V + t * 256 + row * 2) << 16);
+                x[i] = t < T ? s.x * v - s.y * x[i] : 0.f;
+                sure = fmaf(x[i], 0.f, sure);  // 0, or NaN
+            }
+            if (sure != 0.f) {
+#pragma unroll
+                for (int i = 0; i < C::CHUNK; ++i)
+                    if (!(fabsf(x[i]) < INFINITY)) {
+                        x[i] = 0.f;
+                        not_finite |= 1u << (c0 + i);
+                    }
+            }
+            uint32_t up[C::CHUNK / 2], low[C::CHUNK / 2];
+#pragma unroll
+            for (int i = 0; i < C::CHUNK; i += 2) {
+                up[i / 2] = split2(x[i], x[i + 1]);
+                low[i / 2] = bf2_bits(__floats2bfloat162_rn(x[i], x[i + 1]));
+            }
+            const uint32_t to = tl + C::TM_R + (t_first + c0) / 2;
+            if constexpr (C::CHUNK == 16) {
+                tmem_st8(to, up);
+                tmem_st8(to + TP / 2, low);
+            } else {
+                tmem_st4(to, up);
+                tmem_st4(to + TP / 2, low);
+            }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        uint64_t off = 0;  // nodes whose R is not finite in this thread's row
+        if (__syncthreads_or(!ok || not_finite != 0)) {
+            bad[part * 128 + row] = not_finite;
+            if (__syncthreads_or(!ok)) break;
+            off = (uint64_t)bad[128 + row] << C::HALF | bad[row];
+        }
+        if (tid == 0) {
+            tc_fence_after();
+            product_d();
+        }
+        __syncwarp();
+        load_in(next);
+        nodes.load(a, next);
+        // ---- rows out ------------------------------------------------------------------------------------
+        ok = warp_wait(bar_d, phase_d, budget);
+        phase_d ^= 1;
+        tc_fence_after();
+        if (ok) {
+            __nv_bfloat16 *to = out + ((cur.bos + t_first) * a.Hv + cur.h) * 128 + row;
+#pragma unroll
+            for (int c0 = 0; c0 < C::HALF; c0 += C::CHUNK) {
+                float x[C::CHUNK], d[C::CHUNK];
+                tmem_load(tl + C::TM_X + TP + t_first + c0, x);
+                tmem_load(tl + C::TM_D + t_first + c0, d);
+#pragma unroll
+                for (int i = 0; i < C::CHUNK; ++i) {
+                    const int t = t_first + c0 + i;
+                    float o = fmaf(sc[t].z, x[i], d[i]);
+                    if (off != 0 && (off & paths[t])) o = __int_as_float(0x7fffffff);
+                    if (t < T) to[(long)(c0 + i) * a.Hv * 128] = __float2bfloat16_rn(o);
+                }
+            }
+        }
+        tc_fence_before();
+        cur = next;
+        next = heads.after(a, cur);
+    }
+    const bool failed = __syncthreads_or(!ok);
+    if (failed) {
+        if (tid == 0) {
+            flag_error(a.status);
+            // copies and products in flight end before the CTA leaves
+            if (loads > 0) mbar_wait(bar_in, (loads - 1) & 1, kDrainBudget);
+            mma_commit(bar_end);
+            mbar_wait(bar_end, 0, kDrainBudget);
+        }
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == 0) tmem_dealloc(tmem, C::COLS);
+}
+
+template <int TP>
+cudaError_t launch_t(const TreeArgs &a, cudaStream_t s) {
+    using C = Cfg<TP>;
+    CUtensorMap mk, mq, mv;
+    if (!scan_map(&mk, a.k, false, 128, a.Hk, a.Ttot, 64, 1, TP) || !scan_map(&mq, a.q, false, 128, a.Hk, a.Ttot, 64, 1, TP) ||
+        !scan_map(&mv, a.v, false, 128, a.Hv, a.Ttot, 128, 1, TP))
+        return cudaErrorInvalidValue;
+    auto kernel = tree_scan_umma_kernel<TP>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SM_BYTES);
+    if (e != cudaSuccess) return e;
+    const long heads = (long)a.B * a.Hv, most = 152L * C::PER_SM;
+    return launch_early(kernel, dim3((unsigned)(heads < most ? heads : most)), C::THREADS, C::SM_BYTES, s, mk, mq, mv, a,
+                        wait_budget());
+}
+
+}  // namespace
+
+cudaError_t launch_tree_scan_umma(const TreeArgs &a, cudaStream_t s) {
+    const long most = a.cu ? a.Ttot : a.T;  // nodes of a sequence
+    return most <= 16 ? launch_t<16>(a, s) : most <= 32 ? launch_t<32>(a, s) : launch_t<64>(a, s);
+}
+
+}  // namespace gdn
