@@ -25,8 +25,8 @@ struct Cfg {
     static constexpr int THREADS = 256, NB = TP / 16, HALF = TP / 2;  // blocks of nodes; a thread's nodes
     static constexpr int BLOCKS = NB * (NB + 1) / 2;
     static constexpr int CHUNK = HALF < 16 ? HALF : 16;               // nodes that a thread has in registers
-    // TMEM columns: X of keys and of queries, R's terms (two nodes a column), D
-    static constexpr uint32_t TM_X = 0, TM_R = 2 * TP, TM_D = 3 * TP, COLS = 4 * TP;
+    // TMEM columns: X of keys and of queries; [K; Q] K^T, then R's terms (two nodes a column); D
+    static constexpr uint32_t TM_X = 0, TM_G = 2 * TP, TM_R = 2 * TP, TM_D = 3 * TP, COLS = 4 * TP;
     static constexpr uint32_t KQ_BLOCK = 2 * TP * 128, TERM = 128 * 128;
     // byte offsets
     static constexpr uint32_t SM_KQ = 0;                             // [2 blocks of 64 columns][K, Q: 2 TP rows] bf16
@@ -39,9 +39,9 @@ struct Cfg {
     static constexpr uint32_t SM_BAD = SM_PATH + TP * 8;              // [2][128] nodes whose R is not finite, by row
     static constexpr uint32_t SM_G = SM_BAD + 1024;
     static constexpr uint32_t SM_R = SM_G + TP * 4;                   // |q|^2
-    static constexpr uint32_t SM_BAR = SM_R + TP * 4;                 // keys, queries, values; X; D; the end
-    static constexpr uint32_t SM_UNIT = SM_BAR + 4 * 8, SM_TMEM = SM_UNIT + 4;
-    static constexpr uint32_t SM_BYTES = SM_TMEM + 4;
+    static constexpr uint32_t SM_BAR = SM_R + TP * 4;                 // keys, queries, values; [K; Q] K^T; X; D; the end
+    static constexpr uint32_t SM_TMEM = SM_BAR + 5 * 8;
+    static constexpr uint32_t SM_BYTES = SM_TMEM + 8;
     static constexpr int PER_SM = TP == 64 ? 2 : 3;
     static_assert(PER_SM * (SM_BYTES + 1024) <= 233472 && PER_SM * COLS <= 512, "CTAs to an SM");
 };
@@ -69,8 +69,8 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
     uint64_t *paths = reinterpret_cast<uint64_t *>(sm + C::SM_PATH);
     uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::SM_BAD);
     float *gs = reinterpret_cast<float *>(sm + C::SM_G), *qq = reinterpret_cast<float *>(sm + C::SM_R);
-    uint64_t *bar_in = reinterpret_cast<uint64_t *>(sm + C::SM_BAR), *bar_x = bar_in + 1, *bar_d = bar_in + 2, *bar_end = bar_in + 3;
-    int *unit = reinterpret_cast<int *>(sm + C::SM_UNIT);
+    uint64_t *bar_in = reinterpret_cast<uint64_t *>(sm + C::SM_BAR), *bar_g = bar_in + 1, *bar_x = bar_in + 2, *bar_d = bar_in + 3,
+             *bar_end = bar_in + 4;
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(sm + C::SM_TMEM);
     __nv_bfloat16 *out = (__nv_bfloat16 *)a.out;
     next_may_begin();
@@ -78,9 +78,8 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         prefetch_tmap(&mk);
         prefetch_tmap(&mq);
         prefetch_tmap(&mv);
-        for (int i = 0; i < 4; ++i) mbar_init(bar_in + i, 1);
+        for (int i = 0; i < 5; ++i) mbar_init(bar_in + i, 1);
         fence_mbar_init();
-        *unit = 0;
     }
     before_reading();  // (and before TMEM is asked for: a kernel that ends may still hold it)
     if (warp == 0) tmem_alloc(tmem_at, C::COLS);
@@ -138,6 +137,17 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         }
         fence_async_smem();
     };
+    // [K; Q] K^T: rows of A past 2 TP are whatever follows in shared memory, and their results are not looked at
+    auto product_g = [&] {  // by one thread
+        constexpr uint32_t ID = idesc_bf16(128, TP, 0, 0);
+        const uint64_t x = desc_sw128(sb + C::SM_KQ, 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+            const uint64_t at = x + (uint64_t)(((ks >> 2) * C::KQ_BLOCK + (ks & 3) * 32) >> 4);
+            mma_bf16(tmem + C::TM_G, at, at, ID, ks > 0);
+        }
+        mma_commit(bar_g);
+    };
     auto product_x = [&](int h) {  // by one thread
         constexpr uint32_t ID = idesc_bf16(128, 2 * TP, 0, 0);
         const uint64_t x = desc_sw128(sb + C::SM_X, 16, 1024), y = desc_sw128(sb + C::SM_KQ + h * C::KQ_BLOCK, 16, 1024);
@@ -167,9 +177,9 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
     load_in(cur);
     load_half(cur, 0);
     nodes.load(a, cur);
-    uint32_t phase_in = 0, phase_x = 0, phase_d = 0;
+    uint32_t phase_in = 0, phase_g = 0, phase_x = 0, phase_d = 0;
     while (cur.slot >= 0) {
-        const int T = cur.nodes, nb = (T + 15) / 16;
+        const int T = cur.nodes;
         // ---- the state's first half; then the nodes beside its products ---------------------------
         split_half();
         load_half(cur, 1);
@@ -179,14 +189,50 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         if (__syncthreads_or(!ok)) break;  // (and all that the head before has left has been read)
         if (tid == 0) {
             tc_fence_after();
+            product_g();
             product_x(0);
         }
         __syncwarp();
         float hi, lo;
         nodes.sums(T, paths, gs, a.status, hi, lo);
-        node_products<128, TP>(sb + C::SM_KQ, nb, unit, kk, wt, qq);
-        __syncthreads();
-        if (tid == 0) *unit = 0;
+        if ((tid >> 2) < TP) {  // |q|^2, a node by four lanes
+            const int t = tid >> 2;
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(sm + C::SM_KQ + row_piece<128, 2 * TP>(TP + t, 4 * (tid & 3) + i));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float y0 = __uint_as_float(w[j] << 16), y1 = __uint_as_float(w[j] & 0xffff0000u);
+                    s = fmaf(y0, y0, s);
+                    s = fmaf(y1, y1, s);
+                }
+            }
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            if ((tid & 3) == 0) qq[t] = s;
+        }
+        ok = warp_wait(bar_g, phase_g, budget);
+        phase_g ^= 1;
+        tc_fence_after();
+        if (32 * (warp & 3) < 2 * TP) {  // rows of K, then of Q: the products up to the row's own block
+            const bool is_q = row >= TP;
+            const int t = is_q ? row - TP : row;
+#pragma unroll
+            for (int c0 = 0; c0 < C::HALF; c0 += C::CHUNK) {
+                float x[C::CHUNK];
+                tmem_load(tl + C::TM_G + t_first + c0, x);
+#pragma unroll
+                for (int i = 0; i < C::CHUNK; i += 4) {
+                    const int s = t_first + c0 + i;
+                    if ((s >> 4) <= (t >> 4))
+                        *reinterpret_cast<float4 *>(is_q ? wt.raw(t, s) : kk.raw(t, s)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                }
+            }
+        }
+        tc_fence_before();  // (R is going to be where the products were)
+        if (__syncthreads_or(!ok)) break;
         nodes.finish(T, kk, qq, hi, lo, sc);
         // ---- its second half; W beside its products -------------------------------------------------
         ok = warp_wait(bar_x, phase_x, budget);
@@ -261,19 +307,21 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         phase_d ^= 1;
         tc_fence_after();
         if (ok) {
+            const long token = (long)a.Hv * 128;
             __nv_bfloat16 *to = out + ((cur.bos + t_first) * a.Hv + cur.h) * 128 + row;
 #pragma unroll
             for (int c0 = 0; c0 < C::HALF; c0 += C::CHUNK) {
                 float x[C::CHUNK], d[C::CHUNK];
                 tmem_load(tl + C::TM_X + TP + t_first + c0, x);
                 tmem_load(tl + C::TM_D + t_first + c0, d);
+                if (rarely(off != 0)) {
 #pragma unroll
-                for (int i = 0; i < C::CHUNK; ++i) {
-                    const int t = t_first + c0 + i;
-                    float o = fmaf(sc[t].z, x[i], d[i]);
-                    if (off != 0 && (off & paths[t])) o = __int_as_float(0x7fffffff);
-                    if (t < T) to[(long)(c0 + i) * a.Hv * 128] = __float2bfloat16_rn(o);
+                    for (int i = 0; i < C::CHUNK; ++i)
+                        if (off & paths[t_first + c0 + i]) d[i] = __int_as_float(0x7fffffff);
                 }
+#pragma unroll
+                for (int i = 0; i < C::CHUNK; ++i, to += token)
+                    if (c0 + i < T - t_first) *to = __float2bfloat16_rn(fmaf(sc[t_first + c0 + i].z, x[i], d[i]));
             }
         }
         tc_fence_before();
