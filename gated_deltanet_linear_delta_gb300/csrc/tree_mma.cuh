@@ -54,7 +54,7 @@ struct CoefBlocks {
         *reinterpret_cast<uint2 *>(at + piece(t & 15, ch) + half) = up;
         *reinterpret_cast<uint2 *>(at + piece(t & 15, 2 + ch) + half) = low;
     }
-    static constexpr bool kWhole = false;  // blocks above the diagonal do not exist
+    static constexpr bool kWhole = false, kPlain = false;  // blocks above the diagonal do not exist
 };
 // Rows of 128 bytes, 128B swizzle: TP rows of upper terms, then TP of lower ones (a tcgen05 operand); as fp32 a row fills both.
 template <int TP>
@@ -69,15 +69,23 @@ struct CoefRows {
         *reinterpret_cast<uint2 *>(at) = up;
         *reinterpret_cast<uint2 *>(at + TP * 128) = low;
     }
-    static constexpr bool kWhole = true;
+    static constexpr bool kWhole = true, kPlain = false;
+};
+// fp32 throughout, rows of 64 and 4 more, so that the same columns of 8 rows lie in different banks
+struct CoefPlain {
+    float *base;
+    static constexpr int kRow = kTreeMax + 4;
+    __device__ __forceinline__ float *raw(int t, int s) const { return base + t * kRow + s; }
+    static constexpr bool kWhole = false, kPlain = true;
 };
 
 // ---- the nodes of a head ---------------------------------------------------------------------------
-struct __align__(16) Scalars {  // of a node
-    float beta, x;   // beta;  beta e^G rk, the factor of X_k
-    float z, rk;     // e^G rq, the factor of X_q;  1 / |k|
-    float rq, b2;    // 1 / |q|;  beta rk^2
-    float g, g_lo;   // G as a sum of two
+template <int TP>
+struct __align__(16) Scalars {   // of each node (four nodes' are one access)
+    float beta[TP], x[TP];       // beta;  beta e^G rk, the factor of X_k
+    float z[TP], rk[TP];         // e^G rq, the factor of X_q;  1 / |k|
+    float rq[TP], b2[TP];        // 1 / |q|;  beta rk^2
+    float g[TP], g_lo[TP];       // G as a sum of two
 };
 
 struct Head {
@@ -159,21 +167,20 @@ struct Nodes {
         __syncwarp();
     }
     // ... and with the products' diagonals at hand, the rest
-    __device__ __forceinline__ void finish(int T, const CoefBlocks &kk, const float *qq, float hi, float lo, Scalars *sc) const {
+    __device__ __forceinline__ void finish(int T, const CoefBlocks &kk, const float *qq, float hi, float lo, Scalars<TP> &sc) const {
         const int t = node();
         if (t < 0) return;
         const float k2 = t < T ? kk.raw(t, t & ~3)[t & 3] : 0.f;
-        Scalars s;
-        const float eg = __expf(hi + lo);
-        s.beta = sigmoidf_(b);
-        s.rk = rsqrtf(k2 + kNormEps);
-        s.rq = rsqrtf(qq[t] + kNormEps);
-        s.x = s.beta * eg * s.rk;
-        s.z = eg * s.rq;
-        s.b2 = s.beta * s.rk * s.rk;
-        s.g = hi;
-        s.g_lo = lo;
-        sc[t] = s;
+        const float eg = __expf(hi + lo), beta = sigmoidf_(b);
+        const float rk = rsqrtf(k2 + kNormEps), rq = rsqrtf(qq[t] + kNormEps);
+        sc.beta[t] = beta;
+        sc.x[t] = beta * eg * rk;
+        sc.z[t] = eg * rq;
+        sc.rk[t] = rk;
+        sc.rq[t] = rq;
+        sc.b2[t] = beta * rk * rk;
+        sc.g[t] = hi;
+        sc.g_lo[t] = lo;
     }
 };
 
@@ -220,20 +227,21 @@ __device__ __forceinline__ void node_products(uint32_t kq, int nb, int *unit, co
     }
 }
 
-// Q K^T in w becomes W, as two bf16 terms. A row by four lanes: lane `sub` holds columns 16 j + 4 sub .. + 3.
-template <int TP, int THREADS, typename WT>
-__device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scalars *sc, const CoefBlocks &kk, const WT &wt) {
+// Q K^T in wt becomes W, as two bf16 terms. A row by four lanes: lane `sub` holds columns 16 j + 4 sub .. + 3.
+// (kPlain: as fp32.)
+template <int TP, int THREADS, typename KT, typename WT>
+__device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scalars<TP> &sc, const KT &kk, const WT &wt) {
     constexpr int NB = TP / 16;
     const int lane = threadIdx.x & 31, sub = lane & 3, nb = (T + 15) / 16;
     for (int t = (int)threadIdx.x >> 2; t < 16 * nb; t += THREADS / 4) {
         const uint64_t on = t < T ? paths[t] : 0;
-        const Scalars st = sc[t];
+        const float rq = sc.rq[t], g = sc.g[t], g_lo = sc.g_lo[t];
         float w[NB][4];
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             const float4 x = j <= t >> 4 ? *reinterpret_cast<const float4 *>(wt.raw(t, 16 * j + 4 * sub))
                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-            w[j][0] = st.rq * x.x; w[j][1] = st.rq * x.y; w[j][2] = st.rq * x.z; w[j][3] = st.rq * x.w;
+            w[j][0] = rq * x.x; w[j][1] = rq * x.y; w[j][2] = rq * x.z; w[j][3] = rq * x.w;
         }
 #pragma unroll
         for (int j = NB - 1; j >= 0; --j) {
@@ -243,7 +251,7 @@ __device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scala
                 const int s = 31 - __clz(left | 1);  // of the block's nodes; w_s is final
                 const int e = s & 3;
                 const float own = e == 0 ? w[j][0] : e == 1 ? w[j][1] : e == 2 ? w[j][2] : w[j][3];
-                const float ws = -__shfl_sync(0xffffffffu, own, (lane & ~3) | (s >> 2)) * sc[16 * j + s].b2;
+                const float ws = -__shfl_sync(0xffffffffu, own, (lane & ~3) | (s >> 2)) * sc.b2[16 * j + s];
                 if (left != 0) {
                     left &= ~(1u << s);
                     const int before = s - 4 * sub;  // columns of this lane that stand before s, in s's own block
@@ -264,17 +272,22 @@ __device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scala
         for (int j = 0; j < NB; ++j) {
             if (!WT::kWhole && j > t >> 4) continue;
             const uint32_t mine = (uint32_t)(on >> (16 * j)) >> (4 * sub);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const Scalars ss = sc[16 * j + 4 * sub + e];
-                w[j][e] = mine & (1u << e) ? w[j][e] * (__expf((st.g - ss.g) + (st.g_lo - ss.g_lo)) * ss.rk) : 0.f;
+            const float4 sg = load4(sc.g + 16 * j + 4 * sub), sl = load4(sc.g_lo + 16 * j + 4 * sub), rk = load4(sc.rk + 16 * j + 4 * sub);
+            auto decay = [](float x) { return WT::kPlain ? expf(x) : __expf(x); };
+            w[j][0] = mine & 1u ? w[j][0] * (decay((g - sg.x) + (g_lo - sl.x)) * rk.x) : 0.f;
+            w[j][1] = mine & 2u ? w[j][1] * (decay((g - sg.y) + (g_lo - sl.y)) * rk.y) : 0.f;
+            w[j][2] = mine & 4u ? w[j][2] * (decay((g - sg.z) + (g_lo - sl.z)) * rk.z) : 0.f;
+            w[j][3] = mine & 8u ? w[j][3] * (decay((g - sg.w) + (g_lo - sl.w)) * rk.w) : 0.f;
+            if constexpr (WT::kPlain) {
+                *reinterpret_cast<float4 *>(wt.raw(t, 16 * j + 4 * sub)) = make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
+            } else {
+                uint2 up, low;
+                up.x = split2(w[j][0], w[j][1]);
+                up.y = split2(w[j][2], w[j][3]);
+                low.x = tc::bf2_bits(__floats2bfloat162_rn(w[j][0], w[j][1]));
+                low.y = tc::bf2_bits(__floats2bfloat162_rn(w[j][2], w[j][3]));
+                wt.store(t, 16 * j + 4 * sub, up, low);
             }
-            uint2 up, low;
-            up.x = split2(w[j][0], w[j][1]);
-            up.y = split2(w[j][2], w[j][3]);
-            low.x = tc::bf2_bits(__floats2bfloat162_rn(w[j][0], w[j][1]));
-            low.y = tc::bf2_bits(__floats2bfloat162_rn(w[j][2], w[j][3]));
-            wt.store(t, 16 * j + 4 * sub, up, low);
         }
     }
 }

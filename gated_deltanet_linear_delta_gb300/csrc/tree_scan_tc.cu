@@ -1,4 +1,5 @@
-// tree_scan_tc.cu -- the gated delta rule over trees for bf16 inputs, on the tensor cores (formulas: tree_scan.cu).
+// tree_scan_tc.cu -- the gated delta rule over trees for bf16 inputs, on the tensor cores (formulas: tree_scan.cu). This kernel
+// serves head dimensions other than 128 x 128, for which tree_scan_umma.cu has the same products on tcgen05.
 //
 // Per (sequence, value head), with T nodes, on(t) the nodes on path(t) and S_0 (dv x dk fp32) read once:
 //     X = S_0 [K; Q]^T             S_0 split into two bf16 terms (16 bits), k and q as they are (exact)
@@ -8,15 +9,15 @@
 // one another, and the decays and norms stand outside of them: W_ts = e^{G_t-G_s} rk_s w_s, where from t upwards
 //     w_s = rq_t (q_t.k_s) - sum_{s' in on(t), s' > s} w_s' beta_s' rk_s'^2 (k_s'.k_s),
 // with the raw products of K K^T and Q K^T. So a row costs L^2 / 2 multiply-adds for a path of L nodes, by four lanes,
-// once per head; and the dv rows of the state, 16 to a warp, take no elimination of their own, just products.
+// once per head; and the dv rows of the state take no elimination of their own, just products. (A version that
+// eliminated blocks of 16 nodes by shuffles, in each warp for its own rows, took 144 us where this one took 118, for 64
+// sequences of 61 nodes and 32 heads of 128 x 128.)
 //
-// The products are m16n8k16 (mma.sync): their accumulator, rows of the state by nodes, is in the layout of the next
-// product's operand, so that R goes from X to O within registers. tcgen05's M of 128 would take S_0's two terms through
-// shared memory (64 KiB more to write and read a head) and R through TMEM and back.
+// The products are m16n8k16 (mma.sync), 16 rows of the state to a warp: their accumulator, rows of the state by nodes, is
+// in the layout of the next product's operand, so that R goes from X to O within registers.
 //
-// What bounds it: S_0's bytes, 64 KiB a head, for few nodes; for many the products, 2 dk (2 T) dv multiply-adds a head
-// at mma.sync's 1024 a cycle and SM, and the instructions around them.
-// CTAs are persistent, two or three to an SM, and S_0 comes by TMA in parts of 32 columns through a ring, the next
+// What bounds it: S_0's bytes for few nodes; for many the dependent steps of a head and the instructions around the
+// products. CTAs are persistent, two or three to an SM, and S_0 comes by TMA in parts of 32 columns through a ring, the next
 // head's during the end of this one's work. Every wait has a limit, after which the call flags the status word.
 //
 // Values that are not finite stay on their paths: a product with a coefficient of 0 would spread them, so they are
@@ -60,7 +61,7 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    Scalars *sc = reinterpret_cast<Scalars *>(sm + C::SM_SC);
+    Scalars<TP> &sc = *reinterpret_cast<Scalars<TP> *>(sm + C::SM_SC);
     uint64_t *paths = reinterpret_cast<uint64_t *>(sm + C::SM_PATH);
     float *gs = reinterpret_cast<float *>(sm + C::SM_G), *qq = reinterpret_cast<float *>(sm + C::SM_R);
     uint64_t *bar_kq = reinterpret_cast<uint64_t *>(sm + C::SM_BAR), *bar_s = bar_kq + 1;
@@ -228,12 +229,11 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int t = 8 * n + 2 * c + e;
-                const Scalars st = sc[t];
                 const float v0 = __uint_as_float(vv[n][e] << 16), v1 = __uint_as_float(vv[n][e] & 0xffff0000u);
-                xk[n][e] = t < T ? st.beta * v0 - st.x * xk[n][e] : 0.f;
-                xk[n][2 + e] = t < T ? st.beta * v1 - st.x * xk[n][2 + e] : 0.f;
-                xq[n][e] *= st.z;
-                xq[n][2 + e] *= st.z;
+                xk[n][e] = t < T ? sc.beta[t] * v0 - sc.x[t] * xk[n][e] : 0.f;
+                xk[n][2 + e] = t < T ? sc.beta[t] * v1 - sc.x[t] * xk[n][2 + e] : 0.f;
+                xq[n][e] *= sc.z[t];
+                xq[n][2 + e] *= sc.z[t];
                 sure = fmaf(xk[n][e], 0.f, sure);  // 0, or NaN
                 sure = fmaf(xk[n][2 + e], 0.f, sure);
             }
@@ -331,29 +331,23 @@ template <int DK, int DV>
 cudaError_t launch_tp(const TreeArgs &a, cudaStream_t s) {
     const long most = a.cu ? a.Ttot : a.T;  // nodes of a sequence
     if (most <= 16) return launch_t<DK, DV, 16>(a, s);
-    if (most <= 32 && DK == 128 && DV == 128) return launch_t<DK, DV, 32>(a, s);
     return launch_t<DK, DV, 64>(a, s);
-}
-
-template <int DK>
-cudaError_t launch_dv(const TreeArgs &a, cudaStream_t s) {
-    switch (a.dv) {
-        case 32: return launch_tp<DK, 32>(a, s);
-        case 64: return launch_tp<DK, 64>(a, s);
-        case 128: return launch_tp<DK, 128>(a, s);
-    }
-    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_tree_scan_tc(const TreeArgs &a, cudaStream_t s) {
-    switch (a.dk) {
-        case 32: return launch_dv<32>(a, s);
-        case 64: return launch_dv<64>(a, s);
-        case 128: return launch_dv<128>(a, s);
+    switch (a.dk * 1000 + a.dv) {
+        case 32032: return launch_tp<32, 32>(a, s);
+        case 32064: return launch_tp<32, 64>(a, s);
+        case 32128: return launch_tp<32, 128>(a, s);
+        case 64032: return launch_tp<64, 32>(a, s);
+        case 64064: return launch_tp<64, 64>(a, s);
+        case 64128: return launch_tp<64, 128>(a, s);
+        case 128032: return launch_tp<128, 32>(a, s);
+        case 128064: return launch_tp<128, 64>(a, s);
     }
-    return cudaErrorInvalidValue;
+    return cudaErrorInvalidValue;  // (128 x 128: tree_scan_umma.cu)
 }
 
 }  // namespace gdn

@@ -7,12 +7,18 @@
 // and o_t = e^{G_t} rq_t X_q,t + D_t. A thread stands for a row of the state and half of the nodes: it takes X_k out of
 // TMEM, forms R and puts it back, and takes X_q and D out at the end.
 //
-// Why this beside m16n8k16: there each warp feeds 16 rows with fragments of keys, queries and W (of 64 nodes 380
-// instructions for the products of a head alone, and as many around them), and with its accumulators in registers
-// only 16 warps fit an SM. Here the products are 40 instructions of one thread.
+// Why this beside m16n8k16: there each warp feeds 16 rows with fragments of keys, queries and W, and its accumulators in
+// registers leave room for 16 warps to an SM. Here the products are 40 instructions of one thread. The same
+// calls, m16n8k16 and this (64 sequences, 32 heads): 61 nodes 120 and 84 us, 32 nodes 61 and 53, 16 nodes 48 and 39, 8
+// nodes 46 and 36; one sequence of 16 nodes 10.9 and 9.8 with a cold L2.
+//
+// What bounds it: S_0's bytes are 20 us of those; the rest is the dependent steps of a head (about 20,000 cycles for 61
+// nodes, of which W's rows 5,000, R 5,000 with the wait for the last rows of W, rows out 3,300), of which two CTAs' run
+// side by side on an SM.
 //
 // A head's state comes to registers as two halves of 64 columns (the next head's first one early), and goes to shared
-// memory as terms, one half at a time, so that two CTAs fit an SM with 64 nodes and three with fewer.
+// memory as terms, one half at a time, so that two CTAs fit an SM, and three with up to 16 nodes (two: 43 us instead of 39;
+// with up to 32, three leave 80 registers: 73 us instead of 53).
 #include "tree_mma.cuh"
 
 namespace gdn {
@@ -42,7 +48,7 @@ struct Cfg {
     static constexpr uint32_t SM_BAR = SM_R + TP * 4;                 // keys, queries, values; [K; Q] K^T; X; D; the end
     static constexpr uint32_t SM_TMEM = SM_BAR + 5 * 8;
     static constexpr uint32_t SM_BYTES = SM_TMEM + 8;
-    static constexpr int PER_SM = TP == 64 ? 2 : 3;
+    static constexpr int PER_SM = TP >= 32 ? 2 : 3;
     static_assert(PER_SM * (SM_BYTES + 1024) <= 233472 && PER_SM * COLS <= 512, "CTAs to an SM");
 };
 
@@ -65,7 +71,7 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    Scalars *sc = reinterpret_cast<Scalars *>(sm + C::SM_SC);
+    Scalars<TP> &sc = *reinterpret_cast<Scalars<TP> *>(sm + C::SM_SC);
     uint64_t *paths = reinterpret_cast<uint64_t *>(sm + C::SM_PATH);
     uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::SM_BAD);
     float *gs = reinterpret_cast<float *>(sm + C::SM_G), *qq = reinterpret_cast<float *>(sm + C::SM_R);
@@ -257,12 +263,17 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
             float x[C::CHUNK], sure = 0.f;
             tmem_load(tl + C::TM_X + t_first + c0, x);
 #pragma unroll
-            for (int i = 0; i < C::CHUNK; ++i) {
+            for (int i = 0; i < C::CHUNK; i += 4) {
                 const int t = t_first + c0 + i;
-                const float2 s = *reinterpret_cast<const float2 *>(sc + t);  // beta, x
-                const float v = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(sm + C::SM_V + t * 256 + row * 2) << 16);
-                x[i] = t < T ? s.x * v - s.y * x[i] : 0.f;
-                sure = fmaf(x[i], 0.f, sure);  // 0, or NaN
+                const float4 b4 = load4(sc.beta + t), x4 = load4(sc.x + t);
+                const float be[4] = {b4.x, b4.y, b4.z, b4.w}, fx[4] = {x4.x, x4.y, x4.z, x4.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float v =
+                        __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(sm + C::SM_V + (t + e) * 256 + row * 2) << 16);
+                    x[i + e] = t + e < T ? be[e] * v - fx[e] * x[i + e] : 0.f;
+                    sure = fmaf(x[i + e], 0.f, sure);  // 0, or NaN
+                }
             }
             if (sure != 0.f) {
 #pragma unroll
@@ -320,8 +331,13 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
                         if (off & paths[t_first + c0 + i]) d[i] = __int_as_float(0x7fffffff);
                 }
 #pragma unroll
-                for (int i = 0; i < C::CHUNK; ++i, to += token)
-                    if (c0 + i < T - t_first) *to = __float2bfloat16_rn(fmaf(sc[t_first + c0 + i].z, x[i], d[i]));
+                for (int i = 0; i < C::CHUNK; i += 4) {
+                    const float4 z4 = load4(sc.z + t_first + c0 + i);
+                    const float z[4] = {z4.x, z4.y, z4.z, z4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e, to += token)
+                        if (c0 + i + e < T - t_first) *to = __float2bfloat16_rn(fmaf(z[e], x[i + e], d[i + e]));
+                }
             }
         }
         tc_fence_before();
