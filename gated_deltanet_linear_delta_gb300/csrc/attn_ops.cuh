@@ -1,5 +1,6 @@
 // attn_ops.cuh -- what the two attention kernels of bf16 inputs share: constants, the exponential,
-// 8-bit codes as fp16, the scaling of Q, and the tensor maps of the caches.
+// 8-bit codes as fp16, the scaling of Q, and the tensor maps of the caches. (The gated delta rule over trees takes its
+// bounded waits and the encoder of tensor maps from here.)
 #pragma once
 
 #include <cuda.h>

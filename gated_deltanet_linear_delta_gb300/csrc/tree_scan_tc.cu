@@ -315,7 +315,8 @@ cudaError_t launch_t(const TreeArgs &a, cudaStream_t s) {
     using C = Cfg<DK, DV, TP>;
     CUtensorMap ms, mk, mq;
     const long states = (a.slots ? a.num_slots : (long)a.B) * a.Hv;
-    if (!scan_map(&ms, a.state_in, true, DK, DV, states > 0 ? states : 1, 32, DV, 1) ||
+    // (without a state in the pool no sequence has one, and none is copied)
+    if (!scan_map(&ms, states > 0 ? (const void *)a.state_in : a.k, true, DK, DV, states > 0 ? states : 1, 32, DV, 1) ||
         !scan_map(&mk, a.k, false, DK, a.Hk, a.Ttot, DK < 64 ? DK : 64, 1, TP) ||
         !scan_map(&mq, a.q, false, DK, a.Hk, a.Ttot, DK < 64 ? DK : 64, 1, TP))
         return cudaErrorInvalidValue;

@@ -471,8 +471,9 @@ GDN_API int gdn_kv_keep(void *k_cache, void *v_cache, float *k_scale, float *v_s
  *   state : [B][Hv][dv][dk] fp32, or with slots a pool [num_slots][Hv][dv][dk].
  *   slots : device int32 [B] or NULL, as for gdn_decode_step_slots: sequence n's state is entry slots[n]; negative:
  *           padding, whose nodes' outputs are zeros.
- * With bf16 inputs the states enter the products with 16 bits of precision, the outputs' own rounding aside; with fp32
- * inputs all is fp32.
+ * With bf16 inputs the states, and the sums over a path, enter the products with 16 bits of precision, the outputs' own
+ * rounding aside; with fp32 inputs all is fp32. A key, value or gate that is not finite concerns the nodes whose path
+ * holds it, a query its own node.
  * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
  */
 GDN_API int gdn_tree_scan(const void *q, const void *k, const void *v, const void *g, const void *b,
@@ -485,7 +486,8 @@ GDN_API int gdn_tree_scan(const void *q, const void *k, const void *v, const voi
  *
  *   k, v, g, b : the step's packed inputs, as gdn_tree_scan took them.
  *   state_in, state_out : states, or with slots pools, as for gdn_tree_scan; may be the same (in place). A sequence
- *           with count 0 copies its state through; entries of a pool that no sequence names are left as they are.
+ *           with count 0 copies its state through; entries of a pool that no sequence names are left as they are, and two
+ *           sequences must not name the same entry (their updates would race).
  *   path, counts : above (the nodes in any order; each names one of the sequence's). A count or a node out of range is
  *           flagged, and the state passes through.
  * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.

@@ -62,6 +62,18 @@ def test_many_row_tiles(dtype, cache, Hkv, G):
     assert_attention(out, *tree_attention(case, q, trees, 64 ** -0.5))
 
 
+@pytest.mark.parametrize("dtype,cache,G", [("bf16", "same", 1), ("bf16", "same", 3), ("bf16", "fp8", 2), ("bf16", "int8", 5), ("f32", "fp8", 2)])
+def test_one_large_tree_among_single_tokens(dtype, cache, G):
+    """Few rows on average, so that the kernel for few rows takes a tree over many row tiles, whose nodes' ancestors are in earlier
+    tiles and whose positions lie in several chunks."""
+    r = np.random.RandomState(12)
+    trees = [[-1]] * 12 + [random_tree(r, 61, "deep", 2)] + [[-1]] * 20
+    lens = [int(x) for x in r.randint(1, 300, 12)] + [61 + 37] + [int(x) for x in r.randint(1, 90, 20)]
+    case = Paged(lens, 2, 128, 16, cache, dtype, seed=8)
+    q, out = run(case, trees, 2 * G)
+    assert_attention(out, *tree_attention(case, q, trees, 128 ** -0.5))
+
+
 @pytest.mark.parametrize("dtype,cache", [("bf16", "same"), ("bf16", "fp8"), ("f32", "int8"), ("f32", "same")])
 def test_a_chain_is_paged_attention(dtype, cache):
     """A tree without branches gives what gdn_paged_attn gives, bit for bit: the same positions are seen."""

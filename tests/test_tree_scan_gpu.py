@@ -232,12 +232,28 @@ def test_keys_and_queries_that_are_not_finite_stay_on_their_paths(which):
         assert torch.isnan(out[on]).all()
 
 
+def test_a_gate_that_is_not_finite_stays_on_its_paths():
+    trees = make("wide") + make("packed")
+    for dtype in ("bf16", "f32"):
+        x = inputs(trees, 1, 2, 128, 128, dtype, seed=9)
+        clean = scan(x, trees)
+        for which in (3, 4):
+            y = x[which].clone()
+            y[4] = float("nan")
+            out = scan([y if i == which else t for i, t in enumerate(x)], trees)
+            on = [i for i in range(63) if 4 in paths(trees[0])[i]]
+            off = [i for i in range(y.shape[0]) if i not in on]
+            assert torch.equal(out[off], clean[off])
+            assert torch.isnan(out[on]).all()
+
+
 @pytest.mark.parametrize("T", [5, 20, 50])
 @pytest.mark.parametrize("cycles", ["1", "3000"])
-def test_waits_that_run_out_are_reported_and_the_next_call_is_right(T, cycles, monkeypatch):
+@pytest.mark.parametrize("dv", [64, 128])
+def test_waits_that_run_out_are_reported_and_the_next_call_is_right(T, cycles, dv, monkeypatch):
     """GDN_TEST_WAIT_CYCLES shortens the limit of the kernel's waits for its copies."""
     trees = [random_tree(np.random.RandomState(n), T) for n in range(40)]
-    x = inputs(trees, 4, 8, 128, 128, "bf16", seed=14)
+    x = inputs(trees, 4, 8, 128, dv, "bf16", seed=14)
     q, k, v, g, b, S = (t.to(DEV) for t in x)
     parents, out = flat(trees), torch.empty_like(v)
     assert gdn.gdn_get_device_status() == gdn.GDN_OK
@@ -273,6 +289,41 @@ def test_a_tree_in_pieces():
     ref, mag = advance(*x[1:], [5, 5], accepted)
     assert_states(S, ref, mag, accepted, 128)
     assert_states(D, ref, mag, accepted, 128)
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_an_empty_pool(dtype, dk, dv):
+    """No state at all, and idle rows only: outputs are zeros, nothing is flagged."""
+    trees = make("few")
+    q, k, v, g, b, _ = (t.to(DEV) for t in inputs(trees, 2, 4, dk, dv, dtype))
+    S = torch.empty(0, 4, dv, dk, device=DEV)
+    out = torch.full(v.shape, float("nan"), dtype=v.dtype, device=DEV)
+    slots = torch.tensor([-1, -2], dtype=torch.int32, device=DEV)
+    gdn.gdn_tree_scan(q, k, v, g, b, S, flat(trees), out, slots=slots)
+    path, counts = tables([[0], [0, 1]])
+    gdn.gdn_tree_advance(k, v, g, b, S, S, path, counts, slots=slots)
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    assert not out.any()
+
+
+def test_calls_at_once():
+    """Several calls in flight on streams of their own share nothing."""
+    sets = []
+    for i in range(4):
+        trees = [random_tree(np.random.RandomState(10 * i + n), T) for n, T in enumerate([7, 16, 30, 64][i:] + [5, 64, 33][:i])]
+        x = inputs(trees, 4, 8, 128, 128, "bf16", seed=20 + i)
+        sets.append((trees, x, [t.to(DEV) for t in x], flat(trees), cu(trees), scan(x, trees)))
+    outs = [[torch.empty_like(s[2][2]) for _ in range(10)] for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for j in range(10):
+        for s, (trees, x, (q, k, v, g, b, S), parents, c, _), o in zip(streams, sets, outs):
+            gdn.gdn_tree_scan(q, k, v, g, b, S, parents, o[j], cu_seqlens=c, stream=s)
+    torch.cuda.synchronize()
+    assert gdn.gdn_get_device_status() == gdn.GDN_OK
+    for (*_, want), o in zip(sets, outs):
+        assert all(torch.equal(y, want) for y in o)
 
 
 def test_a_captured_graph_and_another_stream():
