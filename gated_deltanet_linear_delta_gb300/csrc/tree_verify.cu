@@ -10,7 +10,10 @@
 // What bounds it: a row or two of V fp32 per sequence, and for few sequences the chain of dependent steps (the tree, the
 // tokens' probabilities, a pass, the draw). A cluster of CTAs takes a sequence, each a run of the row, each warp a part
 // of that; what a pass finds is exchanged through distributed shared memory, and all CTAs take the same decisions.
-// Everything that the walk itself looks at is fetched at once beforehand.
+// Everything that the walk itself looks at is fetched at once beforehand. A lane's elements come through a ring of its own
+// in shared memory, asked for ahead of their use: registers hold two groups a lane, the ring six (64 sequences of up to 13
+// nodes with drafts, V = 131072: 38.5 us from registers, 33.5 so; the first pass over them all takes 12 of those, 67 MB at
+// 5.5 TB/s, the two later ones of the longest walks 4 to 5 each, and the meetings of a cluster's CTAs 1.5 to 3 each).
 //
 // Precision. A draw compares r times a sum with partial sums over V values that lie close to one another, so weights
 // and sums are kept as two floats each (48 bits). In fp64, of which an SM does two operations a cycle, the sums over the
@@ -23,11 +26,13 @@ namespace {
 
 constexpr int kVerThreads = 256, kVerWarps = kVerThreads / 32;
 
-// C: CTAs to a sequence. FLIGHT: groups of a row that a lane asks for at once. PER_SM: CTAs that an SM has to hold.
+// C: CTAs to a sequence. FLIGHT: pairs of groups of a row that a lane has on their way, in shared memory. PER_SM: CTAs that an SM
+// has to hold.
 template <bool DRAFT_, int C_, int FLIGHT_, int PER_SM_>
 struct Cfg {
     static constexpr bool DRAFT = DRAFT_;
     static constexpr int C = C_, FLIGHT = FLIGHT_, PER_SM = PER_SM_;
+    static constexpr int SLOT = (DRAFT ? 4 : 2) * kVerThreads * 16, RING_BYTES = FLIGHT * SLOT;  // [FLIGHT][2][p, q][thread]
     static constexpr int PARTS = kVerWarps * C, NP = PARTS / 32;                // warps of a sequence; ..' sums in a lane
     static constexpr int STEPS = kVerMaxVocab / 4 / PARTS / 32 + 2;             // of 32 groups of 4, per warp
 };
@@ -84,6 +89,11 @@ __device__ __forceinline__ void store_remote(Wide *at, uint32_t rank, Wide x) {
 struct Two {
     F2 hi, lo;
 };
+__device__ __forceinline__ float one_above_0(float x) {  // 1 if x > 0, else 0
+    float k;
+    asm("set.gt.f32.f32 %0, %1, 0f00000000;" : "=f"(k) : "f"(x));
+    return k;
+}
 __device__ __forceinline__ F2 less(F2 a, F2 b) { return f2_fma(b, f2(-1.f, -1.f), a); }  // a - b, rounded once
 __device__ __forceinline__ void add(Two &a, const Two &b) {
     const F2 s = f2_add(a.hi, b.hi), y = less(s, a.hi);
@@ -99,6 +109,24 @@ __device__ __forceinline__ void get(const Two &a, Wide &x, Wide &y) {
     y = plus(wide(h1), wide(l1));
 }
 
+// Copies to shared memory that the asking thread alone waits for and reads
+__device__ __forceinline__ void copy16(uint32_t to, const float *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const float *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // for all but the last N groups of copies
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float4 take16(uint32_t from) {
+    float4 x;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(from) : "memory");
+    return x;
+}
+
 template <typename C>
 struct VerSmem {
     Wide part[2][C::PARTS];  // a pass's sums by warp, two passes' by turns
@@ -111,15 +139,22 @@ struct VerSmem {
 template <bool DRAFT>
 struct Row {
     const float *p, *q;
-    int V, head;   // elements before p's first 16-byte boundary: group 0; group j > 0 has the 4 from head + 4 (j - 1)
+    int V, shift;  // group j has the elements from shift + 4 j, 4 from a 16-byte boundary of p (the first and the last: those
+                   // of them that there are)
     bool same;     // q's boundaries are p's
     Wide c;
     const int *gone;
     int ngone;     // (as far as they concern the warp at hand)
-    __device__ __forceinline__ int first(int j) const { return j == 0 ? 0 : head + 4 * (j - 1); }
+    __device__ __forceinline__ void place(const float *at, int n) {
+        p = at;
+        V = n;
+        shift = -(int)((reinterpret_cast<uintptr_t>(p) >> 2) & 3);
+    }
+    __device__ __forceinline__ int groups() const { return (V - shift + 3) / 4; }
+    __device__ __forceinline__ int first(int j) const { return max(shift + 4 * j, 0); }
     __device__ __forceinline__ void load(int j, float (&x)[4], float (&y)[4]) const {
-        const int e = first(j), n = j == 0 ? head : V - e;
-        if (j > 0 && n >= 4) {
+        const int e = first(j), n = min(shift + 4 * j + 4, V) - e;
+        if (n == 4) {
             const float4 a = __ldg(reinterpret_cast<const float4 *>(p + e));
             x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
             if (DRAFT && c.hi != 0.f) {
@@ -143,17 +178,14 @@ struct Row {
     __device__ __forceinline__ Two weights(float x0, float x1, float y0, float y1, int e) const {
         if constexpr (DRAFT) {
             if (c.hi != 0.f) {
-                const F2 x = f2(x0, x1), y = f2(y0, y1);
-                const F2 mh = f2_mul(f2(-c.hi, -c.hi), y);  // -c y = mh + ml
-                const F2 ml = f2_fma(f2(-c.lo, -c.lo), y, f2_fma(f2(-c.hi, -c.hi), y, f2_mul(mh, f2(-1.f, -1.f))));
-                const F2 s = f2_add(x, mh), z = less(x, s);  // x + mh and what that lost
-                const F2 lo = f2_add(f2_add(less(x, f2_add(s, z)), f2_add(z, mh)), ml);
-                float h0, h1, l0, l1;
-                f2_get(s, h0, h1);
-                f2_get(lo, l0, l1);
-                if (h0 + l0 <= 0.f) h0 = l0 = 0.f;
-                if (h1 + l1 <= 0.f) h1 = l1 = 0.f;
-                return Two{f2(h0, h1), f2(l0, l1)};
+                // Where p - c q is above 0, p >= fl(c q) >= 0, so that what the difference loses is found in two steps.
+                const F2 x = f2(x0, x1), y = f2(y0, y1), m = f2_mul(f2(c.hi, c.hi), y), d = less(x, m);
+                const F2 t = f2_fma(f2(-c.lo, -c.lo), y, f2_fma(f2(-c.hi, -c.hi), y, m));  // m - c y
+                const F2 lo = f2_add(less(less(x, d), m), t);
+                float h0, h1;
+                f2_get(f2_add(d, lo), h0, h1);
+                const F2 k = f2(one_above_0(h0), one_above_0(h1));  // (a NaN stays one: 0 times NaN)
+                return Two{f2_mul(d, k), f2_mul(lo, k)};
             }
         } else {
             for (int i = 0; i < ngone; ++i) {
@@ -170,6 +202,7 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
     constexpr bool DRAFT = C::DRAFT;
     constexpr int kFlight = C::FLIGHT, NP = C::NP;
     __shared__ VerSmem<C> sm;
+    extern __shared__ __align__(16) uint8_t ring[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockIdx.x / C::C;
     const uint32_t rank = cluster_rank();
     cluster_arrive();  // (waited for before anything is stored in another CTA)
@@ -224,16 +257,15 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
     Row<DRAFT> row;
     int g0 = 0, g1 = 0;        // this warp's groups
     Wide ends[NP];             // lane: the sums of all parts up to NP lane + i
+    const uint32_t mine_at = (uint32_t)__cvta_generic_to_shared(ring) + tid * 16;
     // Sums the current node's weights; the same result in every thread of the cluster.
     auto sum_row = [&]() -> Wide {
-        row.p = a.target + (bos + cur) * a.target_stride;
+        row.place(a.target + (bos + cur) * a.target_stride, a.V);
         row.q = DRAFT ? a.draft + (bos + cur) * a.draft_stride : nullptr;
-        row.V = a.V;
-        row.head = min((int)(-(reinterpret_cast<uintptr_t>(row.p) >> 2) & 3), a.V);
         row.same = ((reinterpret_cast<uintptr_t>(row.p) ^ reinterpret_cast<uintptr_t>(row.q)) & 15) == 0;
         row.c = c;
         row.gone = sm.gone;
-        const int groups = 1 + (a.V - row.head + 3) / 4, per = (groups + C::PARTS - 1) / C::PARTS;
+        const int groups = row.groups(), per = (groups + C::PARTS - 1) / C::PARTS;
         const int w = (int)rank * kVerWarps + warp;
         g0 = min(w * per, groups);
         g1 = min(g0 + per, groups);
@@ -244,19 +276,61 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
                 if (sm.gone[i] >= e0 && sm.gone[i] < e1) row.ngone = ngone;
         }
         Two acc[2] = {{f2(0.f, 0.f), f2(0.f, 0.f)}, {f2(0.f, 0.f), f2(0.f, 0.f)}};
-        for (int j = g0 + lane; j < g1; j += 32 * kFlight) {
-            float x[kFlight][4], y[kFlight][4];
+        const bool with_q = DRAFT && c.hi != 0.f;
+        const int whole0 = row.shift < 0, whole1 = (a.V - row.shift) / 4;  // groups of 4 elements
+        const int j0 = max(g0, whole0) + lane, end = min(g1, whole1);
+        const float *pp = row.p + row.first(j0), *pq = DRAFT ? row.q + row.first(j0) : nullptr;
+        int asked = j0;
+        uint32_t to = mine_at;
+        auto ask = [&] {
 #pragma unroll
-            for (int f = 0; f < kFlight; ++f) {
-                if (j + 32 * f < g1) row.load(j + 32 * f, x[f], y[f]);
-                else x[f][0] = x[f][1] = x[f][2] = x[f][3] = y[f][0] = y[f][1] = y[f][2] = y[f][3] = 0.f;
+            for (int u = 0; u < 2; ++u)
+                if (asked + 32 * u < end) {
+                    const uint32_t at = to + u * (C::SLOT / 2);
+                    copy16(at, pp + 128 * u);
+                    if (with_q) {
+                        if (row.same) copy16(at + kVerThreads * 16, pq + 128 * u);
+                        else
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) copy4(at + kVerThreads * 16 + 4 * i, pq + 128 * u + i);
+                    }
+                }
+            copies_end();
+            asked += 64;
+            pp += 256;
+            if (DRAFT) pq += 256;
+            to = to == mine_at + (kFlight - 1) * C::SLOT ? mine_at : to + C::SLOT;
+        };
+#pragma unroll 1
+        for (int f = 0; f < kFlight; ++f) ask();
+        if ((g0 < whole0 && lane == 0) || (g1 > max(max(g0, whole0), whole1) && lane == 1)) {
+            const int j = lane == 0 ? 0 : whole1;
+            float x[4], y[4];
+            row.load(j, x, y);
+            add(acc[0], row.weights(x[0], x[1], y[0], y[1], row.first(j)));
+            add(acc[1], row.weights(x[2], x[3], y[2], y[3], row.first(j) + 2));
+        }
+        uint32_t at = mine_at;
+#pragma unroll 1
+        for (int j = j0; j - lane < end; j += 64) {
+            copies_wait<kFlight - 1>();
+            float4 x[2], y[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j + 32 * u < end) {
+                    x[u] = take16(at + u * (C::SLOT / 2));
+                    if (with_q) y[u] = take16(at + u * (C::SLOT / 2) + kVerThreads * 16);
+                }
             }
 #pragma unroll
-            for (int f = 0; f < kFlight; ++f) {
-                const int e = row.first(j + 32 * f);
-                add(acc[0], row.weights(x[f][0], x[f][1], y[f][0], y[f][1], e));
-                add(acc[1], row.weights(x[f][2], x[f][3], y[f][2], y[f][3], e + 2));
+            for (int u = 0; u < 2; ++u) {
+                const int e = row.first(j + 32 * u);
+                add(acc[0], row.weights(x[u].x, x[u].y, y[u].x, y[u].y, e));
+                add(acc[1], row.weights(x[u].z, x[u].w, y[u].z, y[u].w, e + 2));
             }
+            ask();
+            at = to;
         }
         Wide s0, s1, s2, s3;
         get(acc[0], s0, s1);
@@ -344,7 +418,7 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
         if (owner > 0 && (owner - 1) % NP == i) base = e;
     }
     // its steps of 128 elements, by all warps; then the step, by one
-    const int groups = 1 + (a.V - row.head + 3) / 4, per = (groups + C::PARTS - 1) / C::PARTS;
+    const int groups = row.groups(), per = (groups + C::PARTS - 1) / C::PARTS;
     g0 = min(owner * per, groups);
     g1 = min(g0 + per, groups);
     row.ngone = ngone;
@@ -416,8 +490,10 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
 template <typename C>
 cudaError_t launch_t(const VerifyArgs &a, cudaStream_t s) {
     auto kernel = tree_verify_kernel<C>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::RING_BYTES);
+    if (e != cudaSuccess) return e;
     if (C::C > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -429,6 +505,7 @@ cudaError_t launch_t(const VerifyArgs &a, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3((unsigned)a.B * C::C);
     cfg.blockDim = dim3(kVerThreads);
+    cfg.dynamicSmemBytes = C::RING_BYTES;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -438,8 +515,8 @@ cudaError_t launch_t(const VerifyArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_verify(const VerifyArgs &a, cudaStream_t s) {
-    if (a.B <= 8) return a.draft ? launch_t<Cfg<true, 16, 5, 1>>(a, s) : launch_t<Cfg<false, 16, 10, 1>>(a, s);
-    return a.draft ? launch_t<Cfg<true, 8, 2, 4>>(a, s) : launch_t<Cfg<false, 8, 4, 4>>(a, s);
+    if (a.B <= 8) return a.draft ? launch_t<Cfg<true, 16, 5, 1>>(a, s) : launch_t<Cfg<false, 16, 5, 1>>(a, s);
+    return a.draft ? launch_t<Cfg<true, 8, 3, 4>>(a, s) : launch_t<Cfg<false, 8, 6, 4>>(a, s);
 }
 
 }  // namespace gdn

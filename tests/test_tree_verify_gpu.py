@@ -101,6 +101,17 @@ def test_rows_of_a_wider_tensor(strides):
     check(c, run(c, strides=strides, width=64))
 
 
+@pytest.mark.parametrize("sequences", [2, 9])
+@pytest.mark.parametrize("V", [3, 700, 20001, 40001, 70001, 131072])
+def test_many_passes_over_a_row(V, sequences):
+    """Siblings that are rejected one after another: each asks for the sum of what is left of the same rows."""
+    c = case([7] * sequences, V, True, "star", seed=V)
+    c["r"] = 0.9 + 0.1 * c["r"]
+    c["r"].clamp_(max=1 - 2.0 ** -24)
+    check(c, run(c))
+    check(c, run(c, strides=(V + 1, V + 2)))
+
+
 def test_a_large_vocabulary():
     for drafts in (True, False):
         c = case([3, 2], 1 << 20, drafts, seed=3)
