@@ -22,6 +22,13 @@ __device__ __forceinline__ bool tree_bounds(const int32_t *cu, int n, int B, lon
     return true;
 }
 
+// a + b as a rounded sum and what was lost
+__device__ __forceinline__ void add_exact(float &hi, float &lo, float x) {
+    const float s = hi + x, y = s - hi;
+    lo += (hi - (s - y)) + (x - y);
+    hi = s;
+}
+
 // The path of nodes `lane` and `lane + 32` (bit u: node u is on it), by a whole warp: each node knows the part of
 // its path below some ancestor, and takes over what that one knows, so that the part doubles every step.
 struct Paths {
@@ -35,10 +42,13 @@ struct Paths {
         return node & 32 ? (uint64_t)h1 << 32 | l1 : l0;  // (a node below 32 has none of 32.. on its path)
     }
 };
-__device__ __forceinline__ Paths tree_paths(int up0, int up1, int *status) {  // from the two nodes' parents
+// SUMS: hi + lo, at first a value of each of the two nodes, become the sums over the paths (0 over an empty one).
+// SECOND: whether there are nodes from 32 on.
+template <bool SUMS = false, bool SECOND = true>
+__device__ __forceinline__ Paths tree_paths(int up0, int up1, int *status, float *hi = nullptr, float *lo = nullptr) {
     const int lane = threadIdx.x & 31;
     Paths p;
-    int up[2] = {up0, up1};
+    int up[2] = {up0, SECOND ? up1 : -2};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = lane + 32 * i;
@@ -50,29 +60,51 @@ __device__ __forceinline__ Paths tree_paths(int up0, int up1, int *status) {  //
         p.hi[i] = i == 0 ? 0u : 1u << lane;
     }
     while (__any_sync(0xffffffffu, up[0] >= 0 || up[1] >= 0)) {
-        uint32_t lo[2], hi[2];
-        int next[2];
+        const uint32_t was_lo[2] = {p.lo[0], p.lo[1]}, was_hi = p.hi[1];
+        const int was_up[2] = {up[0], up[1]};
+        float was[2][2];
+        if constexpr (SUMS) was[0][0] = hi[0], was[0][1] = hi[1], was[1][0] = lo[0], was[1][1] = lo[1];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < (SECOND ? 2 : 1); ++i) {
+            // what its ancestor knows: a node below 32, for those from 32 on of either half
             const int src = up[i] & 31;
-            const uint32_t l0 = __shfl_sync(0xffffffffu, p.lo[0], src), l1 = __shfl_sync(0xffffffffu, p.lo[1], src);
-            const uint32_t h1 = __shfl_sync(0xffffffffu, p.hi[1], src);
-            const int u0 = __shfl_sync(0xffffffffu, up[0], src), u1 = __shfl_sync(0xffffffffu, up[1], src);
-            const bool second = up[i] & 32;
-            lo[i] = up[i] >= 0 ? (second ? l1 : l0) : 0u;
-            hi[i] = up[i] >= 0 && second ? h1 : 0u;
-            next[i] = up[i] >= 0 ? (second ? u1 : u0) : up[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            p.lo[i] |= lo[i];
-            p.hi[i] |= hi[i];
-            up[i] = next[i];
+            const bool second = i == 1 && (up[i] & 32);
+            uint32_t l = __shfl_sync(0xffffffffu, was_lo[0], src), h = 0u;
+            int next = __shfl_sync(0xffffffffu, was_up[0], src);
+            float s = 0.f, r = 0.f;
+            if constexpr (SUMS) {
+                s = __shfl_sync(0xffffffffu, was[0][0], src);
+                r = __shfl_sync(0xffffffffu, was[1][0], src);
+            }
+            if (i == 1) {
+                const uint32_t l1 = __shfl_sync(0xffffffffu, was_lo[1], src), h1 = __shfl_sync(0xffffffffu, was_hi, src);
+                const int next1 = __shfl_sync(0xffffffffu, was_up[1], src);
+                l = second ? l1 : l;
+                h = second ? h1 : 0u;
+                next = second ? next1 : next;
+                if constexpr (SUMS) {
+                    const float s1 = __shfl_sync(0xffffffffu, was[0][1], src), r1 = __shfl_sync(0xffffffffu, was[1][1], src);
+                    s = second ? s1 : s;
+                    r = second ? r1 : r;
+                }
+            }
+            if (up[i] >= 0) {
+                p.lo[i] |= l;
+                p.hi[i] |= h;
+                up[i] = next;
+                if constexpr (SUMS) {
+                    add_exact(hi[i], lo[i], s);
+                    lo[i] += r;
+                }
+            }
         }
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        if (up[i] != -1) p.lo[i] = p.hi[i] = 0u;
+        if (up[i] != -1) {
+            p.lo[i] = p.hi[i] = 0u;
+            if constexpr (SUMS) hi[i] = lo[i] = 0.f;
+        }
     return p;
 }
 
@@ -100,13 +132,6 @@ static __device__ __noinline__ uint64_t path_of(const int32_t *parents, int t) {
         t = up;
     }
     return t == -1 ? path : 0;
-}
-
-// a + b as a rounded sum and what was lost
-__device__ __forceinline__ void add_exact(float &hi, float &lo, float x) {
-    const float s = hi + x, y = s - hi;
-    lo += (hi - (s - y)) + (x - y);
-    hi = s;
 }
 
 // Pool entry of sequence n; -1 for padding (flagged if it names none)

@@ -129,48 +129,53 @@ struct Heads {
     }
 };
 
-// What the nodes' threads know of a node ahead: the last TP threads of the CTA; the last warp works the paths out.
+// What the nodes' threads know of a node ahead: the last TP threads of the CTA; the last warp works the paths out, and the
+// sums over them.
 template <int TP, int THREADS>
 struct Nodes {
-    int up0 = -2, up1 = -2;
-    float g = 0.f, b = 0.f;
+    int up[2] = {-2, -2};               // of nodes lane and lane + 32, in the last warp
+    float g[2] = {0.f, 0.f}, b = 0.f;   // .. theirs; of the thread's own node
     __device__ __forceinline__ static int node() { return (int)threadIdx.x - (THREADS - TP); }
     __device__ __forceinline__ void load(const TreeArgs &a, const Head &hd) {
-        up0 = up1 = -2;
-        g = b = 0.f;
+        up[0] = up[1] = -2;
+        g[0] = g[1] = b = 0.f;
         if (hd.slot < 0) return;
         const int t = node(), lane = threadIdx.x & 31;
-        if (t >= 0 && t < hd.nodes) {
-            g = to_f32(((const __nv_bfloat16 *)a.g)[(hd.bos + t) * a.Hv + hd.h]);
-            b = to_f32(((const __nv_bfloat16 *)a.b)[(hd.bos + t) * a.Hv + hd.h]);
-        }
-        if (threadIdx.x >= THREADS - 32) {
-            if (lane < hd.nodes) up0 = a.parents[hd.bos + lane];
-            if (TP > 32 && lane + 32 < hd.nodes) up1 = a.parents[hd.bos + lane + 32];
-        }
+        if (t >= 0 && t < hd.nodes) b = to_f32(((const __nv_bfloat16 *)a.b)[(hd.bos + t) * a.Hv + hd.h]);
+        if (threadIdx.x < THREADS - 32) return;
+#pragma unroll
+        for (int i = 0; i < (TP > 32 ? 2 : 1); ++i)
+            if (lane + 32 * i < hd.nodes) {
+                up[i] = a.parents[hd.bos + lane + 32 * i];
+                g[i] = to_f32(((const __nv_bfloat16 *)a.g)[(hd.bos + lane + 32 * i) * a.Hv + hd.h]);
+            }
     }
-    // Paths into `paths`, and the sum of g over the own node's; by the last warps alone.
-    __device__ __forceinline__ void sums(int T, uint64_t *paths, float *gs, int *status, float &hi, float &lo) const {
-        const int t = node(), lane = threadIdx.x & 31;
-        hi = lo = 0.f;
-        if (t < 0 && !(TP < 32 && threadIdx.x >= THREADS - 32)) return;
-        if (t >= 0) gs[t] = g;
-        if (threadIdx.x >= THREADS - 32) {
-            const Paths p = tree_paths(up0, up1, status);
-            if (lane < TP) paths[lane] = p.of(0);
-            if (TP > 32) paths[lane + 32] = p.of(1);
-        }
-        if (TP > 32) tc::bar_sync(1, 64);
-        else __syncwarp();
-        if (t >= 0 && t < T)
-            for (uint64_t m = paths[t]; m; m &= m - 1) add_exact(hi, lo, gs[__ffsll((long long)m) - 1]);
-        __syncwarp();
+    // Paths, and the sums of g over them; by the last warp alone.
+    __device__ __forceinline__ void sums(uint64_t *paths, Scalars<TP> &sc, int *status) const {
+        if (threadIdx.x < THREADS - 32) return;
+        const int lane = threadIdx.x & 31;
+        float hi[2] = {g[0], g[1]}, lo[2] = {0.f, 0.f};
+        const Paths p = tree_paths<true, (TP > 32)>(up[0], up[1], status, hi, lo);
+#pragma unroll
+        for (int i = 0; i < (TP > 32 ? 2 : 1); ++i)
+            if (lane + 32 * i < TP) {
+                paths[lane + 32 * i] = p.of(i);
+                sc.g[lane + 32 * i] = hi[i];
+                sc.g_lo[lane + 32 * i] = lo[i];
+            }
     }
     // ... and with the products' diagonals at hand, the rest
-    __device__ __forceinline__ void finish(int T, const CoefBlocks &kk, const float *qq, float hi, float lo, Scalars<TP> &sc) const {
+    __device__ __forceinline__ void finish(int T, const CoefBlocks &kk, const float *qq, Scalars<TP> &sc) const {
         const int t = node();
         if (t < 0) return;
-        const float k2 = t < T ? kk.raw(t, t & ~3)[t & 3] : 0.f;
+        float4 *row = reinterpret_cast<float4 *>(kk.raw(t, t & ~3));
+        const float4 x = *row;
+        const int e = t & 3;
+        const float k2 = t >= T ? 0.f : e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
+        // from the diagonal on, the block's row counts as zeros from here
+        *row = make_float4(e > 0 ? x.x : 0.f, e > 1 ? x.y : 0.f, e > 2 ? x.z : 0.f, 0.f);
+        for (int s = (t & ~3) + 4; s < (t & ~15) + 16; s += 4) *reinterpret_cast<float4 *>(kk.raw(t, s)) = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float hi = sc.g[t], lo = sc.g_lo[t];
         const float eg = __expf(hi + lo), beta = sigmoidf_(b);
         const float rk = rsqrtf(k2 + kNormEps), rq = rsqrtf(qq[t] + kNormEps);
         sc.beta[t] = beta;
@@ -179,8 +184,6 @@ struct Nodes {
         sc.rk[t] = rk;
         sc.rq[t] = rq;
         sc.b2[t] = beta * rk * rk;
-        sc.g[t] = hi;
-        sc.g_lo[t] = lo;
     }
 };
 
@@ -227,7 +230,7 @@ __device__ __forceinline__ void node_products(uint32_t kq, int nb, int *unit, co
     }
 }
 
-// Q K^T in wt becomes W, as two bf16 terms. A row by four lanes: lane `sub` holds columns 16 j + 4 sub .. + 3.
+// Q K^T in wt becomes W, as two bf16 terms. kk: K K^T, with zeros from the diagonal on in the blocks that it goes through. A row by four lanes: lane `sub` holds columns 16 j + 4 sub .. + 3.
 // (kPlain: as fp32.)
 template <int TP, int THREADS, typename KT, typename WT>
 __device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scalars<TP> &sc, const KT &kk, const WT &wt) {
@@ -247,22 +250,22 @@ __device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scala
         for (int j = NB - 1; j >= 0; --j) {
             uint32_t left = (uint32_t)(on >> (16 * j)) & 0xffffu;
             // (the warp's eight rows step together, each along its own path: rows that part ways would run one by one)
-            while (__any_sync(0xffffffffu, left != 0)) {
+            const int steps = (int)__reduce_max_sync(0xffffffffu, (unsigned)__popc(left));
+#pragma unroll 1
+            for (int i = 0; i < steps; ++i) {
                 const int s = 31 - __clz(left | 1);  // of the block's nodes; w_s is final
-                const int e = s & 3;
-                const float own = e == 0 ? w[j][0] : e == 1 ? w[j][1] : e == 2 ? w[j][2] : w[j][3];
+                const float own = s & 2 ? (s & 1 ? w[j][3] : w[j][2]) : (s & 1 ? w[j][1] : w[j][0]);
                 const float ws = -__shfl_sync(0xffffffffu, own, (lane & ~3) | (s >> 2)) * sc.b2[16 * j + s];
                 if (left != 0) {
-                    left &= ~(1u << s);
-                    const int before = s - 4 * sub;  // columns of this lane that stand before s, in s's own block
+                    left ^= 1u << s;
 #pragma unroll
                     for (int i = 0; i < NB; ++i) {
                         if (i > j) continue;
                         const float4 x = *reinterpret_cast<const float4 *>(kk.raw(16 * j + s, 16 * i + 4 * sub));
-                        w[i][0] = fmaf(ws, i < j || before > 0 ? x.x : 0.f, w[i][0]);
-                        w[i][1] = fmaf(ws, i < j || before > 1 ? x.y : 0.f, w[i][1]);
-                        w[i][2] = fmaf(ws, i < j || before > 2 ? x.z : 0.f, w[i][2]);
-                        w[i][3] = fmaf(ws, i < j || before > 3 ? x.w : 0.f, w[i][3]);
+                        w[i][0] = fmaf(ws, x.x, w[i][0]);  // (0 from s on)
+                        w[i][1] = fmaf(ws, x.y, w[i][1]);
+                        w[i][2] = fmaf(ws, x.z, w[i][2]);
+                        w[i][3] = fmaf(ws, x.w, w[i][3]);
                     }
                 }
             }
@@ -270,14 +273,21 @@ __device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scala
         __syncwarp();  // the row has been read by all of its lanes
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-            if (!WT::kWhole && j > t >> 4) continue;
+            if (j > t >> 4) {  // (the same for the whole warp)
+                if constexpr (WT::kWhole) wt.store(t, 16 * j + 4 * sub, make_uint2(0u, 0u), make_uint2(0u, 0u));
+                continue;
+            }
             const uint32_t mine = (uint32_t)(on >> (16 * j)) >> (4 * sub);
             const float4 sg = load4(sc.g + 16 * j + 4 * sub), sl = load4(sc.g_lo + 16 * j + 4 * sub), rk = load4(sc.rk + 16 * j + 4 * sub);
-            auto decay = [](float x) { return WT::kPlain ? expf(x) : __expf(x); };
-            w[j][0] = mine & 1u ? w[j][0] * (decay((g - sg.x) + (g_lo - sl.x)) * rk.x) : 0.f;
-            w[j][1] = mine & 2u ? w[j][1] * (decay((g - sg.y) + (g_lo - sl.y)) * rk.y) : 0.f;
-            w[j][2] = mine & 4u ? w[j][2] * (decay((g - sg.z) + (g_lo - sl.z)) * rk.z) : 0.f;
-            w[j][3] = mine & 8u ? w[j][3] * (decay((g - sg.w) + (g_lo - sl.w)) * rk.w) : 0.f;
+            // (by masks: selects became branches, which took as long as all steps above)
+            auto masked = [&](float x, float gs, float ls, float r, int i) {
+                const float d = (g - gs) + (g_lo - ls);
+                return __uint_as_float(__float_as_uint(x * ((WT::kPlain ? expf(d) : __expf(d)) * r)) & (0u - (mine >> i & 1u)));
+            };
+            w[j][0] = masked(w[j][0], sg.x, sl.x, rk.x, 0);
+            w[j][1] = masked(w[j][1], sg.y, sl.y, rk.y, 1);
+            w[j][2] = masked(w[j][2], sg.z, sl.z, rk.z, 2);
+            w[j][3] = masked(w[j][3], sg.w, sl.w, rk.w, 3);
             if constexpr (WT::kPlain) {
                 *reinterpret_cast<float4 *>(wt.raw(t, 16 * j + 4 * sub)) = make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
             } else {

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kScanThreads) tree_scan_kernel(const TreeArgs 
             x[0] = fmaf(ks.x, kt.x, x[0]); x[1] = fmaf(ks.y, kt.y, x[1]); x[2] = fmaf(ks.z, kt.z, x[2]); x[3] = fmaf(ks.w, kt.w, x[3]);
             y[0] = fmaf(ks.x, qt.x, y[0]); y[1] = fmaf(ks.y, qt.y, y[1]); y[2] = fmaf(ks.z, qt.z, y[2]); y[3] = fmaf(ks.w, qt.w, y[3]);
         }
-        *kk.raw(t, s) = (x[0] + x[1]) + (x[2] + x[3]);
+        *kk.raw(t, s) = s < t ? (x[0] + x[1]) + (x[2] + x[3]) : 0.f;  // (form_w wants zeros from the diagonal on)
         *w.raw(t, s) = (y[0] + y[1]) + (y[2] + y[3]);
     }
     __syncthreads();

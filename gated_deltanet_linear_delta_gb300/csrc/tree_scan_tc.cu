@@ -42,8 +42,7 @@ struct Cfg {
     static constexpr uint32_t SM_W = SM_A + BLOCKS * 1024;                     // Q K^T, then W, fp32, then W as two terms
     static constexpr uint32_t SM_SC = SM_W + BLOCKS * 1024;                    // per node: Scalars
     static constexpr uint32_t SM_PATH = SM_SC + TP * 32;                       // [TP] paths
-    static constexpr uint32_t SM_G = SM_PATH + TP * 8;                         // [TP] g
-    static constexpr uint32_t SM_R = SM_G + TP * 4;                            // [TP] |q|^2
+    static constexpr uint32_t SM_R = SM_PATH + TP * 8;                         // [TP] |q|^2
     static constexpr uint32_t SM_BAR = SM_R + TP * 4;                          // keys and queries; the slots
     static constexpr uint32_t SM_UNIT = SM_BAR + (1 + RING) * 8;               // the next block of products
     static constexpr uint32_t SM_BYTES = SM_UNIT + 8;
@@ -63,7 +62,7 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     Scalars<TP> &sc = *reinterpret_cast<Scalars<TP> *>(sm + C::SM_SC);
     uint64_t *paths = reinterpret_cast<uint64_t *>(sm + C::SM_PATH);
-    float *gs = reinterpret_cast<float *>(sm + C::SM_G), *qq = reinterpret_cast<float *>(sm + C::SM_R);
+    float *qq = reinterpret_cast<float *>(sm + C::SM_R);
     uint64_t *bar_kq = reinterpret_cast<uint64_t *>(sm + C::SM_BAR), *bar_s = bar_kq + 1;
     int *unit = reinterpret_cast<int *>(sm + C::SM_UNIT);
     const __nv_bfloat16 *v = (const __nv_bfloat16 *)a.v;
@@ -136,12 +135,11 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
             break;
         }
         // ---- the nodes: paths and gates, beside them the products; norms; W --------------------------------
-        float hi, lo;
-        nodes.sums(T, paths, gs, a.status, hi, lo);
+        nodes.sums(paths, sc, a.status);
         node_products<DK, TP>(sb + C::SM_KQ, nb, unit, kk, wt, qq);
         __syncthreads();
         if (tid == 0) *unit = 0;
-        nodes.finish(T, kk, qq, hi, lo, sc);
+        nodes.finish(T, kk, qq, sc);
         __syncthreads();
         form_w<TP, C::THREADS>(T, paths, sc, kk, wt);
         // ---- X = S_0 [K; Q]^T, and the values on their way ---------------------------------------

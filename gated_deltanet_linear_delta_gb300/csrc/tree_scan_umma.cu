@@ -43,8 +43,7 @@ struct Cfg {
     static constexpr uint32_t SM_SC = SM_V + TP * 256;                // per node: Scalars
     static constexpr uint32_t SM_PATH = SM_SC + TP * 32;
     static constexpr uint32_t SM_BAD = SM_PATH + TP * 8;              // [2][128] nodes whose R is not finite, by row
-    static constexpr uint32_t SM_G = SM_BAD + 1024;
-    static constexpr uint32_t SM_R = SM_G + TP * 4;                   // |q|^2
+    static constexpr uint32_t SM_R = SM_BAD + 1024;                  // |q|^2
     static constexpr uint32_t SM_BAR = SM_R + TP * 4;                 // keys, queries, values; [K; Q] K^T; X; D; the end
     static constexpr uint32_t SM_TMEM = SM_BAR + 5 * 8;
     static constexpr uint32_t SM_BYTES = SM_TMEM + 8;
@@ -74,7 +73,7 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
     Scalars<TP> &sc = *reinterpret_cast<Scalars<TP> *>(sm + C::SM_SC);
     uint64_t *paths = reinterpret_cast<uint64_t *>(sm + C::SM_PATH);
     uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::SM_BAD);
-    float *gs = reinterpret_cast<float *>(sm + C::SM_G), *qq = reinterpret_cast<float *>(sm + C::SM_R);
+    float *qq = reinterpret_cast<float *>(sm + C::SM_R);
     uint64_t *bar_in = reinterpret_cast<uint64_t *>(sm + C::SM_BAR), *bar_g = bar_in + 1, *bar_x = bar_in + 2, *bar_d = bar_in + 3,
              *bar_end = bar_in + 4;
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(sm + C::SM_TMEM);
@@ -199,8 +198,7 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
             product_x(0);
         }
         __syncwarp();
-        float hi, lo;
-        nodes.sums(T, paths, gs, a.status, hi, lo);
+        nodes.sums(paths, sc, a.status);
         if ((tid >> 2) < TP) {  // |q|^2, a node by four lanes
             const int t = tid >> 2;
             float s = 0.f;
@@ -239,7 +237,7 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         }
         tc_fence_before();  // (R is going to be where the products were)
         if (__syncthreads_or(!ok)) break;
-        nodes.finish(T, kk, qq, hi, lo, sc);
+        nodes.finish(T, kk, qq, sc);
         // ---- its second half; W beside its products -------------------------------------------------
         ok = warp_wait(bar_x, phase_x, budget);
         phase_x ^= 1;
