@@ -172,9 +172,7 @@ struct Nodes {
         const float4 x = *row;
         const int e = t & 3;
         const float k2 = t >= T ? 0.f : e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
-        // from the diagonal on, the block's row counts as zeros from here
-        *row = make_float4(e > 0 ? x.x : 0.f, e > 1 ? x.y : 0.f, e > 2 ? x.z : 0.f, 0.f);
-        for (int s = (t & ~3) + 4; s < (t & ~15) + 16; s += 4) *reinterpret_cast<float4 *>(kk.raw(t, s)) = make_float4(0.f, 0.f, 0.f, 0.f);
+        *row = make_float4(e > 0 ? x.x : 0.f, e > 1 ? x.y : 0.f, e > 2 ? x.z : 0.f, 0.f);  // (what follows in its block is 0)
         const float hi = sc.g[t], lo = sc.g_lo[t];
         const float eg = __expf(hi + lo), beta = sigmoidf_(b);
         const float rk = rsqrtf(k2 + kNormEps), rq = rsqrtf(qq[t] + kNormEps);
@@ -187,7 +185,8 @@ struct Nodes {
     }
 };
 
-// K K^T into kk, Q K^T into w, block by block of 16 x 16, and |q|^2 into qq. K's rows are 0 .. of the tile at shared address
+// K K^T into kk (zeros in the fours of a row past the diagonal's), Q K^T into w, block by block of 16 x 16, and |q|^2 into
+// qq. K's rows are 0 .. of the tile at shared address
 // kq, Q's TP .. . Warps take blocks from the counter `unit`, so that those which are late take fewer.
 template <int DK, int TP, typename W>
 __device__ __forceinline__ void node_products(uint32_t kq, int nb, int *unit, const CoefBlocks &kk, const W &w, float *qq) {
@@ -225,7 +224,8 @@ __device__ __forceinline__ void node_products(uint32_t kq, int nb, int *unit, co
             for (int half = 0; half < 2; ++half) {
                 const int t = 16 * i + g + 8 * half, s = 16 * j + 8 * n + 4 * (c >> 1);
                 float *to = (is_q ? w.raw(t, s) : kk.raw(t, s)) + 2 * (c & 1);
-                *reinterpret_cast<float2 *>(to) = make_float2(acc[n][2 * half], acc[n][2 * half + 1]);
+                const bool past = !is_q && s > t;
+                *reinterpret_cast<float2 *>(to) = past ? make_float2(0.f, 0.f) : make_float2(acc[n][2 * half], acc[n][2 * half + 1]);
             }
     }
 }

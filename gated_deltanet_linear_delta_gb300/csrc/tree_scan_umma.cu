@@ -230,8 +230,10 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
 #pragma unroll
                 for (int i = 0; i < C::CHUNK; i += 4) {
                     const int s = t_first + c0 + i;
+                    const bool past = !is_q && s > t;  // (zeros there: form_w)
                     if ((s >> 4) <= (t >> 4))
-                        *reinterpret_cast<float4 *>(is_q ? wt.raw(t, s) : kk.raw(t, s)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                        *reinterpret_cast<float4 *>(is_q ? wt.raw(t, s) : kk.raw(t, s)) =
+                            past ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                 }
             }
         }
