@@ -129,11 +129,11 @@ struct Heads {
     }
 };
 
-// What the nodes' threads know of a node ahead: the last TP threads of the CTA; the last warp works the paths out, and the
-// sums over them.
-template <int TP, int THREADS>
+// What the nodes' threads know of a node ahead: the last TP threads of the CTA; warp WARP works the paths out, and the sums
+// over them.
+template <int TP, int THREADS, int WARP>
 struct Nodes {
-    int up[2] = {-2, -2};               // of nodes lane and lane + 32, in the last warp
+    int up[2] = {-2, -2};               // of nodes lane and lane + 32, in that warp
     float g[2] = {0.f, 0.f}, b = 0.f;   // .. theirs; of the thread's own node
     __device__ __forceinline__ static int node() { return (int)threadIdx.x - (THREADS - TP); }
     __device__ __forceinline__ void load(const TreeArgs &a, const Head &hd) {
@@ -142,7 +142,7 @@ struct Nodes {
         if (hd.slot < 0) return;
         const int t = node(), lane = threadIdx.x & 31;
         if (t >= 0 && t < hd.nodes) b = to_f32(((const __nv_bfloat16 *)a.b)[(hd.bos + t) * a.Hv + hd.h]);
-        if (threadIdx.x < THREADS - 32) return;
+        if (threadIdx.x >> 5 != WARP) return;
 #pragma unroll
         for (int i = 0; i < (TP > 32 ? 2 : 1); ++i)
             if (lane + 32 * i < hd.nodes) {
@@ -150,9 +150,10 @@ struct Nodes {
                 g[i] = to_f32(((const __nv_bfloat16 *)a.g)[(hd.bos + lane + 32 * i) * a.Hv + hd.h]);
             }
     }
-    // Paths, and the sums of g over them; by the last warp alone.
-    __device__ __forceinline__ void sums(uint64_t *paths, Scalars<TP> &sc, int *status) const {
-        if (threadIdx.x < THREADS - 32) return;
+    // Paths, and the sums of g over them; by that warp alone. The own node's beta.
+    __device__ __forceinline__ void sums(uint64_t *paths, Scalars<TP> &sc, int *status) {
+        if (node() >= 0) b = sigmoidf_(b);
+        if (threadIdx.x >> 5 != WARP) return;
         const int lane = threadIdx.x & 31;
         float hi[2] = {g[0], g[1]}, lo[2] = {0.f, 0.f};
         const Paths p = tree_paths<true, (TP > 32)>(up[0], up[1], status, hi, lo);
@@ -162,6 +163,7 @@ struct Nodes {
                 paths[lane + 32 * i] = p.of(i);
                 sc.g[lane + 32 * i] = hi[i];
                 sc.g_lo[lane + 32 * i] = lo[i];
+                sc.z[lane + 32 * i] = __expf(hi[i] + lo[i]);
             }
     }
     // ... and with the products' diagonals at hand, the rest
@@ -173,8 +175,7 @@ struct Nodes {
         const int e = t & 3;
         const float k2 = t >= T ? 0.f : e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w;
         *row = make_float4(e > 0 ? x.x : 0.f, e > 1 ? x.y : 0.f, e > 2 ? x.z : 0.f, 0.f);  // (what follows in its block is 0)
-        const float hi = sc.g[t], lo = sc.g_lo[t];
-        const float eg = __expf(hi + lo), beta = sigmoidf_(b);
+        const float eg = sc.z[t], beta = b;
         const float rk = rsqrtf(k2 + kNormEps), rq = rsqrtf(qq[t] + kNormEps);
         sc.beta[t] = beta;
         sc.x[t] = beta * eg * rk;

@@ -30,8 +30,9 @@ template <int TP>
 struct Cfg {
     static constexpr int THREADS = 256, NB = TP / 16, HALF = TP / 2;  // blocks of nodes; a thread's nodes
     static constexpr int BLOCKS = NB * (NB + 1) / 2;
+    static constexpr int PATH_WARP = TP == 64 ? 4 : 7;                // one without products to take out of TMEM
     static constexpr int CHUNK = HALF < 16 ? HALF : 16;               // nodes that a thread has in registers
-    // TMEM columns: X of keys and of queries; [K; Q] K^T, then R's terms (two nodes a column); D
+    // TMEM columns: X of keys and of queries; [K; Q] [K; Q]^T, then R's terms (two nodes a column) and D
     static constexpr uint32_t TM_X = 0, TM_G = 2 * TP, TM_R = 2 * TP, TM_D = 3 * TP, COLS = 4 * TP;
     static constexpr uint32_t KQ_BLOCK = 2 * TP * 128, TERM = 128 * 128;
     // byte offsets
@@ -44,9 +45,9 @@ struct Cfg {
     static constexpr uint32_t SM_PATH = SM_SC + TP * 32;
     static constexpr uint32_t SM_BAD = SM_PATH + TP * 8;              // [2][128] nodes whose R is not finite, by row
     static constexpr uint32_t SM_R = SM_BAD + 1024;                  // |q|^2
-    static constexpr uint32_t SM_BAR = SM_R + TP * 4;                 // keys, queries, values; [K; Q] K^T; X; D; the end
-    static constexpr uint32_t SM_TMEM = SM_BAR + 5 * 8;
-    static constexpr uint32_t SM_BYTES = SM_TMEM + 8;
+    static constexpr uint32_t SM_BAR = SM_R + TP * 4;                 // keys and queries; values; [K; Q] [K; Q]^T; X; D; the end
+    static constexpr uint32_t SM_TMEM = SM_BAR + 6 * 8;
+    static constexpr uint32_t SM_BYTES = SM_TMEM + 16;
     static constexpr int PER_SM = TP >= 32 ? 2 : 3;
     static_assert(PER_SM * (SM_BYTES + 1024) <= 233472 && PER_SM * COLS <= 512, "CTAs to an SM");
 };
@@ -75,7 +76,7 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
     uint32_t *bad = reinterpret_cast<uint32_t *>(sm + C::SM_BAD);
     float *qq = reinterpret_cast<float *>(sm + C::SM_R);
     uint64_t *bar_in = reinterpret_cast<uint64_t *>(sm + C::SM_BAR), *bar_g = bar_in + 1, *bar_x = bar_in + 2, *bar_d = bar_in + 3,
-             *bar_end = bar_in + 4;
+             *bar_v = bar_in + 4, *bar_end = bar_in + 5;
     uint32_t *tmem_at = reinterpret_cast<uint32_t *>(sm + C::SM_TMEM);
     __nv_bfloat16 *out = (__nv_bfloat16 *)a.out;
     next_may_begin();
@@ -83,7 +84,7 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         prefetch_tmap(&mk);
         prefetch_tmap(&mq);
         prefetch_tmap(&mv);
-        for (int i = 0; i < 5; ++i) mbar_init(bar_in + i, 1);
+        for (int i = 0; i < 6; ++i) mbar_init(bar_in + i, 1);
         fence_mbar_init();
     }
     before_reading();  // (and before TMEM is asked for: a kernel that ends may still hold it)
@@ -100,22 +101,28 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
     bool ok = true;  // the same for a warp's lanes
 
     Heads<128, C::THREADS> heads(a);
-    Nodes<TP, C::THREADS> nodes;
+    Nodes<TP, C::THREADS, C::PATH_WARP> nodes;
     const CoefBlocks kk{sm + C::SM_A};
     const CoefRows<TP> wt{sm + C::SM_W};
-    uint32_t loads = 0;  // of keys, queries and values, begun
+    uint32_t loads = 0;  // begun: an odd number (bit 0) and any (1) of keys and queries, (2) and (3) of values
     auto load_in = [&](const Head &hd) {
         if (hd.slot < 0) return;
-        ++loads;
+        loads = (loads ^ 1u) | 2u;
         if (tid != 0) return;
         const int hk = hd.h / (a.Hv / a.Hk);
-        mbar_expect_tx(bar_in, 2 * C::KQ_BLOCK + TP * 256);
+        mbar_expect_tx(bar_in, 2 * C::KQ_BLOCK);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             tma_load_3d(sm + C::SM_KQ + b * C::KQ_BLOCK, &mk, 64 * b, hk, (int)hd.bos, bar_in);
             tma_load_3d(sm + C::SM_KQ + b * C::KQ_BLOCK + TP * 128, &mq, 64 * b, hk, (int)hd.bos, bar_in);
         }
-        tma_load_3d(sm + C::SM_V, &mv, 0, hd.h, (int)hd.bos, bar_in);
+    };
+    auto load_v = [&](const Head &hd) {
+        if (hd.slot < 0) return;
+        loads = (loads ^ 4u) | 8u;
+        if (tid != 0) return;
+        mbar_expect_tx(bar_v, TP * 256);
+        tma_load_3d(sm + C::SM_V, &mv, 0, hd.h, (int)hd.bos, bar_v);
     };
     // half of a state, 64 columns: this thread's 16 bytes (columns 4 ch ..) of 8 rows
     const int sr = tid >> 4, ch = tid & 15;
@@ -142,9 +149,9 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         }
         fence_async_smem();
     };
-    // [K; Q] K^T: rows of A past 2 TP are whatever follows in shared memory, and their results are not looked at
+    // [K; Q] [K; Q]^T: rows of A past 2 TP are whatever follows in shared memory, and their results are not looked at
     auto product_g = [&] {  // by one thread
-        constexpr uint32_t ID = idesc_bf16(128, TP, 0, 0);
+        constexpr uint32_t ID = idesc_bf16(128, 2 * TP, 0, 0);
         const uint64_t x = desc_sw128(sb + C::SM_KQ, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
@@ -180,9 +187,10 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
 
     Head cur = heads.find(a), next = heads.after(a, cur);
     load_in(cur);
+    load_v(cur);
     load_half(cur, 0);
     nodes.load(a, cur);
-    uint32_t phase_in = 0, phase_g = 0, phase_x = 0, phase_d = 0;
+    uint32_t phase_in = 0, phase_v = 0, phase_g = 0, phase_x = 0, phase_d = 0;
     while (cur.slot >= 0) {
         const int T = cur.nodes;
         // ---- the state's first half; then the nodes beside its products ---------------------------
@@ -199,32 +207,16 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         }
         __syncwarp();
         nodes.sums(paths, sc, a.status);
-        if ((tid >> 2) < TP) {  // |q|^2, a node by four lanes
-            const int t = tid >> 2;
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(sm + C::SM_KQ + row_piece<128, 2 * TP>(TP + t, 4 * (tid & 3) + i));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float y0 = __uint_as_float(w[j] << 16), y1 = __uint_as_float(w[j] & 0xffff0000u);
-                    s = fmaf(y0, y0, s);
-                    s = fmaf(y1, y1, s);
-                }
-            }
-            s += __shfl_xor_sync(0xffffffffu, s, 1);
-            s += __shfl_xor_sync(0xffffffffu, s, 2);
-            if ((tid & 3) == 0) qq[t] = s;
-        }
         ok = warp_wait(bar_g, phase_g, budget);
         phase_g ^= 1;
         tc_fence_after();
         if (32 * (warp & 3) < 2 * TP) {  // rows of K, then of Q: the products up to the row's own block
             const bool is_q = row >= TP;
             const int t = is_q ? row - TP : row;
+            const int first = (32 * (warp & 3)) & (TP - 1), t_last = TP < 32 ? TP - 1 : first + 31;  // of the warp's rows
 #pragma unroll
             for (int c0 = 0; c0 < C::HALF; c0 += C::CHUNK) {
+                if (t_first + c0 > t_last) continue;
                 float x[C::CHUNK];
                 tmem_load(tl + C::TM_G + t_first + c0, x);
 #pragma unroll
@@ -235,6 +227,20 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
                         *reinterpret_cast<float4 *>(is_q ? wt.raw(t, s) : kk.raw(t, s)) =
                             past ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
                 }
+            }
+        }
+        if (part == 1 && 32 * (warp & 3) < 2 * TP) {  // |q|^2: the diagonal of Q Q^T
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int t = 32 * (warp & 3) - TP + 16 * c;  // of 16 nodes
+                if (t < 0) continue;
+                float x[16];
+                tmem_load(tl + C::TM_G + TP + t, x);
+#pragma unroll
+                for (int bit = 8; bit > 0; bit >>= 1)
+#pragma unroll
+                    for (int i = 0; i < bit; ++i) x[i] = lane & bit ? x[i + bit] : x[i];
+                if ((lane >> 4) == c) qq[t + (lane & 15)] = x[0];
             }
         }
         tc_fence_before();  // (R is going to be where the products were)
@@ -256,6 +262,9 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         // ---- R ------------------------------------------------------------------------------------------
         ok = warp_wait(bar_x, phase_x, budget);
         phase_x ^= 1;
+        if (ok) load_in(next);  // (none but the products read keys and queries)
+        ok = warp_wait(bar_v, phase_v, budget) && ok;
+        phase_v ^= 1;
         tc_fence_after();
         uint32_t not_finite = 0;  // of this thread's nodes
 #pragma unroll
@@ -311,7 +320,7 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
             product_d();
         }
         __syncwarp();
-        load_in(next);
+        load_v(next);
         nodes.load(a, next);
         // ---- rows out ------------------------------------------------------------------------------------
         ok = warp_wait(bar_d, phase_d, budget);
@@ -349,7 +358,8 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         if (tid == 0) {
             flag_error(a.status);
             // copies and products in flight end before the CTA leaves
-            if (loads > 0) mbar_wait(bar_in, (loads - 1) & 1, kDrainBudget);
+            if (loads & 2u) mbar_wait(bar_in, ~loads & 1u, kDrainBudget);
+            if (loads & 8u) mbar_wait(bar_v, ~(loads >> 2) & 1u, kDrainBudget);
             mma_commit(bar_end);
             mbar_wait(bar_end, 0, kDrainBudget);
         }
