@@ -83,9 +83,10 @@ struct CoefPlain {
 template <int TP>
 struct __align__(16) Scalars {   // of each node (four nodes' are one access)
     float beta[TP], x[TP];       // beta;  beta e^G rk, the factor of X_k
-    float z[TP], rk[TP];         // e^G rq, the factor of X_q;  1 / |k|
+    float z[TP];                 // e^G rq, the factor of X_q
     float rq[TP], b2[TP];        // 1 / |q|;  beta rk^2
-    float g[TP], g_lo[TP];       // G as a sum of two
+    float g[TP], g_lo[TP];       // G as a sum of two (bf16 inputs: of its log2 e fold)
+    float gk[TP];                // g_lo less the logarithm of 1 / |k|, to the same base
 };
 
 struct Head {
@@ -161,9 +162,11 @@ struct Nodes {
         for (int i = 0; i < (TP > 32 ? 2 : 1); ++i)
             if (lane + 32 * i < TP) {
                 paths[lane + 32 * i] = p.of(i);
-                sc.g[lane + 32 * i] = hi[i];
-                sc.g_lo[lane + 32 * i] = lo[i];
-                sc.z[lane + 32 * i] = __expf(hi[i] + lo[i]);
+                // times log2 e, whose second float is 1.926e-8
+                const float x = hi[i] * kLog2e, y = fmaf(hi[i], 1.92596303e-8f, fmaf(lo[i], kLog2e, fmaf(hi[i], kLog2e, -x)));
+                sc.g[lane + 32 * i] = x;
+                sc.g_lo[lane + 32 * i] = y;
+                sc.z[lane + 32 * i] = ex2(x + y);
             }
     }
     // ... and with the products' diagonals at hand, the rest
@@ -180,7 +183,7 @@ struct Nodes {
         sc.beta[t] = beta;
         sc.x[t] = beta * eg * rk;
         sc.z[t] = eg * rq;
-        sc.rk[t] = rk;
+        sc.gk[t] = sc.g_lo[t] - __log2f(rk);
         sc.rq[t] = rq;
         sc.b2[t] = beta * rk * rk;
     }
@@ -279,16 +282,16 @@ __device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scala
                 continue;
             }
             const uint32_t mine = (uint32_t)(on >> (16 * j)) >> (4 * sub);
-            const float4 sg = load4(sc.g + 16 * j + 4 * sub), sl = load4(sc.g_lo + 16 * j + 4 * sub), rk = load4(sc.rk + 16 * j + 4 * sub);
+            const float4 sg = load4(sc.g + 16 * j + 4 * sub), sl = load4(sc.gk + 16 * j + 4 * sub);
             // (by masks: selects became branches, which took as long as all steps above)
-            auto masked = [&](float x, float gs, float ls, float r, int i) {
+            auto masked = [&](float x, float gs, float ls, int i) {
                 const float d = (g - gs) + (g_lo - ls);
-                return __uint_as_float(__float_as_uint(x * ((WT::kPlain ? expf(d) : __expf(d)) * r)) & (0u - (mine >> i & 1u)));
+                return __uint_as_float(__float_as_uint(x * (WT::kPlain ? expf(d) : ex2(d))) & (0u - (mine >> i & 1u)));
             };
-            w[j][0] = masked(w[j][0], sg.x, sl.x, rk.x, 0);
-            w[j][1] = masked(w[j][1], sg.y, sl.y, rk.y, 1);
-            w[j][2] = masked(w[j][2], sg.z, sl.z, rk.z, 2);
-            w[j][3] = masked(w[j][3], sg.w, sl.w, rk.w, 3);
+            w[j][0] = masked(w[j][0], sg.x, sl.x, 0);
+            w[j][1] = masked(w[j][1], sg.y, sl.y, 1);
+            w[j][2] = masked(w[j][2], sg.z, sl.z, 2);
+            w[j][3] = masked(w[j][3], sg.w, sl.w, 3);
             if constexpr (WT::kPlain) {
                 *reinterpret_cast<float4 *>(wt.raw(t, 16 * j + 4 * sub)) = make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
             } else {

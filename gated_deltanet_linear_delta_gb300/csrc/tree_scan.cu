@@ -91,9 +91,9 @@ __global__ void __launch_bounds__(kScanThreads) tree_scan_kernel(const TreeArgs 
         sm.sc.beta[tid] = sm.sc.b2[tid] = beta;
         sm.sc.x[tid] = beta * eg;
         sm.sc.z[tid] = eg;
-        sm.sc.rk[tid] = sm.sc.rq[tid] = 1.f;
+        sm.sc.rq[tid] = 1.f;
         sm.sc.g[tid] = hi;
-        sm.sc.g_lo[tid] = lo;
+        sm.sc.g_lo[tid] = sm.sc.gk[tid] = lo;
     }
     const CoefPlain kk{sm.kk}, w{sm.w};
     const int upto = (nodes + 15) & ~15;
