@@ -293,6 +293,13 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a_tmem, uint64_t
 }
 // the same, issued by the lane of the warp for which `lead` is true: the warp stays together around it,
 // so descriptors and addresses stay in uniform registers
+__device__ __forceinline__ void mma_f16_ss_by(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 q, %0, 0;\nsetp.ne.b32 p, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n}" ::"r"(lead),
+        "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
 __device__ __forceinline__ void mma_f16_ts_by(uint32_t lead, uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
                                               uint32_t acc) {
     asm volatile(

@@ -130,44 +130,73 @@ struct Heads {
     }
 };
 
-// What the nodes' threads know of a node ahead: the last TP threads of the CTA; warp WARP works the paths out, and the sums
-// over them.
-template <int TP, int THREADS, int WARP>
+// What a node's thread knows of it, a head ahead: the threads of warp W0, and for nodes from 32 on of W1.
+template <int TP, int W0, int W1>
 struct Nodes {
-    int up[2] = {-2, -2};               // of nodes lane and lane + 32, in that warp
-    float g[2] = {0.f, 0.f}, b = 0.f;   // .. theirs; of the thread's own node
-    __device__ __forceinline__ static int node() { return (int)threadIdx.x - (THREADS - TP); }
-    __device__ __forceinline__ void load(const TreeArgs &a, const Head &hd) {
-        up[0] = up[1] = -2;
-        g[0] = g[1] = b = 0.f;
-        if (hd.slot < 0) return;
-        const int t = node(), lane = threadIdx.x & 31;
-        if (t >= 0 && t < hd.nodes) b = to_f32(((const __nv_bfloat16 *)a.b)[(hd.bos + t) * a.Hv + hd.h]);
-        if (threadIdx.x >> 5 != WARP) return;
-#pragma unroll
-        for (int i = 0; i < (TP > 32 ? 2 : 1); ++i)
-            if (lane + 32 * i < hd.nodes) {
-                up[i] = a.parents[hd.bos + lane + 32 * i];
-                g[i] = to_f32(((const __nv_bfloat16 *)a.g)[(hd.bos + lane + 32 * i) * a.Hv + hd.h]);
-            }
+    int up = -2;
+    float g = 0.f, b = 0.f;
+    __device__ __forceinline__ static int node() {  // -1: none
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        return warp == W0 && lane < TP ? lane : TP > 32 && warp == W1 ? lane + 32 : -1;
     }
-    // Paths, and the sums of g over them; by that warp alone. The own node's beta.
+    __device__ __forceinline__ void load(const TreeArgs &a, const Head &hd) {
+        up = -2;
+        g = b = 0.f;
+        const int t = node();
+        if (hd.slot < 0 || t < 0 || t >= hd.nodes) return;
+        up = a.parents[hd.bos + t];
+        g = to_f32(((const __nv_bfloat16 *)a.g)[(hd.bos + t) * a.Hv + hd.h]);
+        b = to_f32(((const __nv_bfloat16 *)a.b)[(hd.bos + t) * a.Hv + hd.h]);
+    }
+    // Paths, and the sums of g over them, by those warps; b becomes beta.
     __device__ __forceinline__ void sums(uint64_t *paths, Scalars<TP> &sc, int *status) {
-        if (node() >= 0) b = sigmoidf_(b);
-        if (threadIdx.x >> 5 != WARP) return;
-        const int lane = threadIdx.x & 31;
-        float hi[2] = {g[0], g[1]}, lo[2] = {0.f, 0.f};
-        const Paths p = tree_paths<true, (TP > 32)>(up[0], up[1], status, hi, lo);
-#pragma unroll
-        for (int i = 0; i < (TP > 32 ? 2 : 1); ++i)
-            if (lane + 32 * i < TP) {
-                paths[lane + 32 * i] = p.of(i);
-                // times log2 e, whose second float is 1.926e-8
-                const float x = hi[i] * kLog2e, y = fmaf(hi[i], 1.92596303e-8f, fmaf(lo[i], kLog2e, fmaf(hi[i], kLog2e, -x)));
-                sc.g[lane + 32 * i] = x;
-                sc.g_lo[lane + 32 * i] = y;
-                sc.z[lane + 32 * i] = ex2(x + y);
+        const int warp = threadIdx.x >> 5, t = node();
+        if (warp != W0 && !(TP > 32 && warp == W1)) return;
+        b = sigmoidf_(b);
+        float hi = g, lo = 0.f;
+        uint64_t path;
+        if constexpr (TP <= 32) {
+            float his[2] = {hi, 0.f}, los[2] = {0.f, 0.f};
+            path = tree_paths<true, false>(up, -2, status, his, los).of(0);
+            hi = his[0];
+            lo = los[0];
+        } else {
+            // as tree_paths does it, through shared memory: what is known of each node, where the scalars are going to be
+            // (two nodes to a thread and shuffles: 67 us of 64 sequences of 61 nodes, 32 heads, and 64 so)
+            static_assert(TP == 64 && offsetof(Scalars<TP>, b2) == 1024, "room for what is known");
+            uint4 *known = reinterpret_cast<uint4 *>(&sc);  // path, parent of its last node, hi
+            float *known_lo = sc.b2;
+            if (up >= t) {  // no parent of its own
+                flag_error(status);
+                up = -2;
             }
+            path = 1ull << t;
+            while (true) {
+                known[t] = make_uint4((uint32_t)path, (uint32_t)(path >> 32), (uint32_t)up, __float_as_uint(hi));
+                known_lo[t] = lo;
+                if (!tc::bar_any(1, 64, up >= 0)) break;
+                if (up >= 0) {
+                    const uint4 k = known[up];
+                    const float l = known_lo[up];
+                    path |= (uint64_t)k.y << 32 | k.x;
+                    up = (int)k.z;
+                    add_exact(hi, lo, __uint_as_float(k.w));
+                    lo += l;
+                }
+                tc::bar_sync(1, 64);
+            }
+            if (up != -1) {
+                path = 0;
+                hi = lo = 0.f;
+            }
+        }
+        if (t < 0) return;
+        paths[t] = path;
+        // times log2 e, whose second float is 1.926e-8
+        const float x = hi * kLog2e, y = fmaf(hi, 1.92596303e-8f, fmaf(lo, kLog2e, fmaf(hi, kLog2e, -x)));
+        sc.g[t] = x;
+        sc.g_lo[t] = y;
+        sc.z[t] = ex2(x + y);
     }
     // ... and with the products' diagonals at hand, the rest
     __device__ __forceinline__ void finish(int T, const CoefBlocks &kk, const float *qq, Scalars<TP> &sc) const {
@@ -190,8 +219,8 @@ struct Nodes {
 };
 
 // K K^T into kk (zeros in the fours of a row past the diagonal's), Q K^T into w, block by block of 16 x 16, and |q|^2 into
-// qq. K's rows are 0 .. of the tile at shared address
-// kq, Q's TP .. . Warps take blocks from the counter `unit`, so that those which are late take fewer.
+// qq. K's rows are 0 .. of the tile at shared address kq, Q's TP .. . Warps take blocks from the counter `unit`, so that
+// those which are late take fewer.
 template <int DK, int TP, typename W>
 __device__ __forceinline__ void node_products(uint32_t kq, int nb, int *unit, const CoefBlocks &kk, const W &w, float *qq) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;

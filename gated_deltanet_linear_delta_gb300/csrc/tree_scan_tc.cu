@@ -106,7 +106,7 @@ tree_scan_tc_kernel(const __grid_constant__ CUtensorMap ms, const __grid_constan
         tma_load_3d(sm + C::SM_S + slot * C::SLOT, &ms, 32 * part, 0, state, bar_s + slot);
     };
     auto state_of = [&](const Head &hd) { return (int)(hd.slot * a.Hv + hd.h); };
-    Nodes<TP, C::THREADS, C::WARPS - 1> nodes;
+    Nodes<TP, C::WARPS - 1, C::WARPS - 2> nodes;
     const CoefBlocks kk{sm + C::SM_A}, wt{sm + C::SM_W};
 
     // Parts follow one another through the ring, head by head. When a head's products begin, as many parts as the ring

@@ -30,7 +30,7 @@ template <int TP>
 struct Cfg {
     static constexpr int THREADS = 256, NB = TP / 16, HALF = TP / 2;  // blocks of nodes; a thread's nodes
     static constexpr int BLOCKS = NB * (NB + 1) / 2;
-    static constexpr int PATH_WARP = TP == 64 ? 4 : 7;                // one without products to take out of TMEM
+    static constexpr int NODE_WARP = TP == 64 ? 4 : 7;                // (without products of nodes to take out of TMEM)
     static constexpr int CHUNK = HALF < 16 ? HALF : 16;               // nodes that a thread has in registers
     // TMEM columns: X of keys and of queries; [K; Q] [K; Q]^T, then R's terms (two nodes a column) and D
     static constexpr uint32_t TM_X = 0, TM_G = 2 * TP, TM_R = 2 * TP, TM_D = 3 * TP, COLS = 4 * TP;
@@ -99,9 +99,10 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         return;
     }
     bool ok = true;  // the same for a warp's lanes
+    const uint32_t lead = elect_one();
 
     Heads<128, C::THREADS> heads(a);
-    Nodes<TP, C::THREADS, C::PATH_WARP> nodes;
+    Nodes<TP, C::NODE_WARP, 6> nodes;
     const CoefBlocks kk{sm + C::SM_A};
     const CoefRows<TP> wt{sm + C::SM_W};
     uint32_t loads = 0;  // begun: an odd number (bit 0) and any (1) of keys and queries, (2) and (3) of values
@@ -150,37 +151,37 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         fence_async_smem();
     };
     // [K; Q] [K; Q]^T: rows of A past 2 TP are whatever follows in shared memory, and their results are not looked at
-    auto product_g = [&] {  // by one thread
+    auto product_g = [&] {  // by warp 0
         constexpr uint32_t ID = idesc_bf16(128, 2 * TP, 0, 0);
         const uint64_t x = desc_sw128(sb + C::SM_KQ, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
             const uint64_t at = x + (uint64_t)(((ks >> 2) * C::KQ_BLOCK + (ks & 3) * 32) >> 4);
-            mma_bf16(tmem + C::TM_G, at, at, ID, ks > 0);
+            mma_f16_ss_by(lead, tmem + C::TM_G, at, at, ID, ks > 0);
         }
-        mma_commit(bar_g);
+        mma_commit_by(lead, bar_g);
     };
-    auto product_x = [&](int h) {  // by one thread
+    auto product_x = [&](int h) {  // by warp 0
         constexpr uint32_t ID = idesc_bf16(128, 2 * TP, 0, 0);
         const uint64_t x = desc_sw128(sb + C::SM_X, 16, 1024), y = desc_sw128(sb + C::SM_KQ + h * C::KQ_BLOCK, 16, 1024);
 #pragma unroll
         for (int term = 0; term < 2; ++term)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-                mma_bf16(tmem + C::TM_X, x + (uint64_t)((term * C::TERM + ks * 32) >> 4), y + (uint64_t)(ks * 2), ID,
+                mma_f16_ss_by(lead, tmem + C::TM_X, x + (uint64_t)((term * C::TERM + ks * 32) >> 4), y + (uint64_t)(ks * 2), ID,
                          h > 0 || term > 0 || ks > 0);
-        mma_commit(bar_x);
+        mma_commit_by(lead, bar_x);
     };
-    auto product_d = [&] {  // by one thread
+    auto product_d = [&] {  // by warp 0
         constexpr uint32_t ID = idesc_bf16(128, TP, 0, 0);
         const uint64_t y = desc_sw128(sb + C::SM_W, 16, 1024);
 #pragma unroll
         for (int term = 0; term < 3; ++term)  // R upper W upper, R lower W upper, R upper W lower
 #pragma unroll
             for (int ks = 0; ks < TP / 16; ++ks)
-                mma_bf16_ts(tmem + C::TM_D, tmem + C::TM_R + (term == 1 ? TP / 2 : 0) + 8 * ks,
+                mma_f16_ts_by(lead, tmem + C::TM_D, tmem + C::TM_R + (term == 1 ? TP / 2 : 0) + 8 * ks,
                             y + (uint64_t)(((term == 2 ? TP * 128 : 0) + ks * 32) >> 4), ID, term > 0 || ks > 0);
-        mma_commit(bar_d);
+        mma_commit_by(lead, bar_d);
     };
     const int part = warp >> 2, row = 32 * (warp & 3) + lane, t_first = part * C::HALF;  // this thread's row and nodes
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -195,18 +196,18 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         const int T = cur.nodes;
         // ---- the state's first half; then the nodes beside its products ---------------------------
         split_half();
-        load_half(cur, 1);
         ok = warp_wait(bar_in, phase_in, budget) && ok;
         phase_in ^= 1;
         tc_fence_before();
         if (__syncthreads_or(!ok)) break;  // (and all that the head before has left has been read)
-        if (tid == 0) {
+        if (warp == 0) {
             tc_fence_after();
             product_g();
             product_x(0);
         }
         __syncwarp();
         nodes.sums(paths, sc, a.status);
+        load_half(cur, 1);  // (not before: the sums would wait for it)
         ok = warp_wait(bar_g, phase_g, budget);
         phase_g ^= 1;
         tc_fence_after();
@@ -250,15 +251,15 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         ok = warp_wait(bar_x, phase_x, budget);
         phase_x ^= 1;
         if (ok) split_half();
-        load_half(next, 0);
         if (__syncthreads_or(!ok)) break;
-        if (tid == 0) {
+        if (warp == 0) {
             tc_fence_after();
             product_x(1);
         }
         __syncwarp();
         form_w<TP, C::THREADS>(T, paths, sc, kk, wt);
         fence_async_smem();
+        load_half(next, 0);
         // ---- R ------------------------------------------------------------------------------------------
         ok = warp_wait(bar_x, phase_x, budget);
         phase_x ^= 1;
@@ -315,7 +316,7 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
             if (__syncthreads_or(!ok)) break;
             off = (uint64_t)bad[128 + row] << C::HALF | bad[row];
         }
-        if (tid == 0) {
+        if (warp == 0) {
             tc_fence_after();
             product_d();
         }
@@ -360,7 +361,9 @@ tree_scan_umma_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
             // copies and products in flight end before the CTA leaves
             if (loads & 2u) mbar_wait(bar_in, ~loads & 1u, kDrainBudget);
             if (loads & 8u) mbar_wait(bar_v, ~(loads >> 2) & 1u, kDrainBudget);
-            mma_commit(bar_end);
+        }
+        if (warp == 0) {
+            mma_commit_by(lead, bar_end);
             mbar_wait(bar_end, 0, kDrainBudget);
         }
         __syncthreads();
