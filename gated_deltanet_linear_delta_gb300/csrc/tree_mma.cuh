@@ -162,7 +162,7 @@ struct Nodes {
             lo = los[0];
         } else {
             // as tree_paths does it, through shared memory: what is known of each node, where the scalars are going to be
-            // (two nodes to a thread and shuffles: 67 us of 64 sequences of 61 nodes, 32 heads, and 64 so)
+            // (two nodes to a thread of one warp, and shuffles, is twice the instructions on the slowest warp's way)
             static_assert(TP == 64 && offsetof(Scalars<TP>, b2) == 1024, "room for what is known");
             uint4 *known = reinterpret_cast<uint4 *>(&sc);  // path, parent of its last node, hi
             float *known_lo = sc.b2;

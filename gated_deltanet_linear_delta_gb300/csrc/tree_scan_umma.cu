@@ -8,17 +8,20 @@
 // TMEM, forms R and puts it back, and takes X_q and D out at the end.
 //
 // Why this beside m16n8k16: there each warp feeds 16 rows with fragments of keys, queries and W, and its accumulators in
-// registers leave room for 16 warps to an SM. Here the products are 40 instructions of one thread. The same
-// calls, m16n8k16 and this (64 sequences, 32 heads): 61 nodes 120 and 84 us, 32 nodes 61 and 53, 16 nodes 48 and 39, 8
-// nodes 46 and 36; one sequence of 16 nodes 10.9 and 9.8 with a cold L2.
+// registers leave room for 16 warps to an SM. Here the products are 36 instructions of one warp. m16n8k16 took 120 us for 64
+// sequences of 61 nodes and 32 heads when this took 84 (32 nodes 61 and 53, 16 nodes 48 and 39, 8 nodes 46 and 36). This takes
+// 62 now (from a graph), and with an L2 that holds other data 63, 44, 35 and 34; chains of 61 nodes 106.
 //
-// What bounds it: S_0's bytes are 20 us of those; the rest is the dependent steps of a head (about 20,000 cycles for 61
-// nodes, of which W's rows 5,000, R 5,000 with the wait for the last rows of W, rows out 3,300), of which two CTAs' run
-// side by side on an SM.
+// What bounds it: S_0's bytes are 20 us of those, and with few nodes all but 8 us of the time go with the bytes. With many
+// it is the dependent steps of a head: about 14,500 cycles for 61 nodes, of which W's last rows 4,500, the paths and the
+// products of nodes beside them 2,700, R 1,900, rows out 1,900; those of two CTAs run side by side on an SM. A warp issues
+// an instruction every 9 cycles there, so that what counts is their number on the way of the slowest warp.
 //
 // A head's state comes to registers as two halves of 64 columns (the next head's first one early), and goes to shared
 // memory as terms, one half at a time, so that two CTAs fit an SM, and three with up to 16 nodes (two: 43 us instead of 39;
-// with up to 32, three leave 80 registers: 73 us instead of 53).
+// with up to 32, three leave 80 registers: 73 us instead of 53). Its loads are asked for where no other load is waited for
+// soon: the paths' parents, asked for long before, were waited for together with a half of the state (68 us instead of 64).
+// (All of a state asked for ahead into L2 by bulk prefetches: 41 us instead of 34 with 16 nodes.)
 #include "tree_mma.cuh"
 
 namespace gdn {
