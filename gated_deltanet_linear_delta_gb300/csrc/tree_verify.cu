@@ -9,15 +9,18 @@
 //
 // What bounds it: a row or two of V fp32 per sequence, and for few sequences the chain of dependent steps (the tree, the
 // tokens' probabilities, a pass, the draw). A cluster of CTAs takes a sequence, each a run of the row, each warp a part
-// of that; what a pass finds is exchanged through distributed shared memory, and all CTAs take the same decisions.
+// of that; what a pass finds is sent to all CTAs of the cluster, which take the same decisions.
 // Everything that the walk itself looks at is fetched at once beforehand. A lane's elements come through a ring of its own
 // in shared memory, asked for ahead of their use: registers hold two groups a lane, the ring six (64 sequences of up to 13
 // nodes with drafts, V = 131072: 38.5 us from registers, 33.5 so; the first pass over them all takes 12 of those, 67 MB at
-// 5.5 TB/s, the two later ones of the longest walks 4 to 5 each, and the meetings of a cluster's CTAs 1.5 to 3 each).
+// 5.5 TB/s, the two later ones of the longest walks 4 to 5 each). What a warp finds goes to all CTAs by asynchronous stores
+// that their barriers count, 0.4 us from the last one sent; by stores and a barrier of the cluster a pass took 1 us more.
+// One session of 16 nodes, V = 150001, no draft probabilities: 6.8 us from a graph.
 //
 // Precision. A draw compares r times a sum with partial sums over V values that lie close to one another, so weights
 // and sums are kept as two floats each (48 bits). In fp64, of which an SM does two operations a cycle, the sums over the
 // warps alone kept its unit busy for a third of the time.
+#include "attn_ops.cuh"
 #include "kv_pages.cuh"
 #include "tree.cuh"
 
@@ -79,10 +82,28 @@ __device__ __forceinline__ Wide warp_scan(Wide a) {  // inclusive
     }
     return a;
 }
-__device__ __forceinline__ void store_remote(Wide *at, uint32_t rank, Wide x) {
-    uint32_t to;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"((uint32_t)__cvta_generic_to_shared(at)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(x.hi), "f"(x.lo) : "memory");
+// To `at` in the shared memory of CTA `rank`, whose `bar` counts the bytes
+__device__ __forceinline__ void send(Wide *at, uint64_t *bar, uint32_t rank, Wide x) {
+    uint32_t to, to_bar;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(at)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to_bar) : "r"(tc::smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(x.hi), "f"(x.lo),
+                 "r"(to_bar)
+                 : "memory");
+}
+// Wait for what other CTAs send, with a limit in cycles
+__device__ __forceinline__ bool received(uint64_t *bar, uint32_t phase, long long budget) {
+    const long long t0 = clock64();
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 1000;\nselp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done)
+            : "r"(tc::smem_u32(bar)), "r"(phase)
+            : "memory");
+        if (done) return true;
+        if (clock64() - t0 > budget) return false;
+    }
 }
 
 // Two such numbers side by side, without the last step that brings them into shape: one packed operation serves both.
@@ -121,21 +142,20 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {  // for all but the last N groups of copies
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ float4 take16(uint32_t from) {
-    float4 x;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(from) : "memory");
-    return x;
+__device__ __forceinline__ void take16(uint32_t from, float (&x)[4]) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(from) : "memory");
 }
 
 template <typename C>
 struct VerSmem {
     Wide part[2][C::PARTS];  // a pass's sums by warp, two passes' by turns
+    uint64_t bar[2];         // .. arrivals
     Wide step[C::STEPS];
     int up[kTreeMax], token[kTreeMax], gone[kTreeMax], path[kTreeMax];
     float p[kTreeMax], q[kTreeMax], r[kTreeMax];
 };
 
-// The weights of a node's row: max(p - c q, 0) (DRAFT), or p without the tokens that are gone.
+// The weights of a node's row: max(p - c q, 0) (DRAFT), or p, from which strike takes the tokens that are gone.
 template <bool DRAFT>
 struct Row {
     const float *p, *q;
@@ -144,7 +164,8 @@ struct Row {
     bool same;     // q's boundaries are p's
     Wide c;
     const int *gone;
-    int ngone;     // (as far as they concern the warp at hand)
+    int ngone;     // (0 where none concerns the warp at hand)
+    int mine[2];   // lane: entries lane and lane + 32 of the list
     __device__ __forceinline__ void place(const float *at, int n) {
         p = at;
         V = n;
@@ -174,8 +195,7 @@ struct Row {
             }
         }
     }
-    // of elements e and e + 1
-    __device__ __forceinline__ Two weights(float x0, float x1, float y0, float y1, int e) const {
+    __device__ __forceinline__ Two weights(float x0, float x1, float y0, float y1) const {
         if constexpr (DRAFT) {
             if (c.hi != 0.f) {
                 // Where p - c q is above 0, p >= fl(c q) >= 0, so that what the difference loses is found in two steps.
@@ -187,25 +207,64 @@ struct Row {
                 const F2 k = f2(one_above_0(h0), one_above_0(h1));  // (a NaN stays one: 0 times NaN)
                 return Two{f2_mul(d, k), f2_mul(lo, k)};
             }
-        } else {
-            for (int i = 0; i < ngone; ++i) {
-                if (gone[i] == e) x0 = 0.f;
-                if (gone[i] == e + 1) x1 = 0.f;
-            }
         }
         return Two{f2(x0, x1), f2(0.f, 0.f)};
+    }
+    // Of elements e .. e + 3, by one thread
+    __device__ __forceinline__ void strike_alone(float (&x)[4], int e) const {
+        if constexpr (!DRAFT)
+            for (int i = 0; i < ngone; ++i)
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                    if (gone[i] == e + f) x[f] = 0.f;
+    }
+    // ... by a whole warp, whose lanes have 128 elements or less from `base` on. (Every token of the list compared with every
+    // element made the warps that a token of the list concerns 2.3 us later than all others, for 14 tokens.)
+    __device__ __forceinline__ void strike(float (&x)[4], int e, int base) const {
+        if constexpr (!DRAFT) {
+            if (ngone == 0) return;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                unsigned near = __ballot_sync(0xffffffffu, (unsigned)mine[i] - (unsigned)base < 128u);
+                while (near) {
+                    const int at = __shfl_sync(0xffffffffu, mine[i], __ffs(near) - 1) - e;
+                    near &= near - 1;
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        if (at == f) x[f] = 0.f;
+                }
+            }
+        }
+    }
+    // The list as far as it concerns the elements from e0 to e1
+    __device__ __forceinline__ void list(int count, int e0, int e1) {
+        if constexpr (!DRAFT) {
+            const int lane = threadIdx.x & 31;
+            bool any = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mine[i] = lane + 32 * i < count ? gone[lane + 32 * i] : -1;
+                any |= mine[i] >= e0 && mine[i] < e1;
+            }
+            ngone = __any_sync(0xffffffffu, any) ? count : 0;
+        }
     }
 };
 
 template <typename C>
-__global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(const VerifyArgs a, long long budget) {
     constexpr bool DRAFT = C::DRAFT;
     constexpr int kFlight = C::FLIGHT, NP = C::NP;
     __shared__ VerSmem<C> sm;
     extern __shared__ __align__(16) uint8_t ring[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockIdx.x / C::C;
     const uint32_t rank = cluster_rank();
-    cluster_arrive();  // (waited for before anything is stored in another CTA)
+    if (tid == 0) {
+        tc::mbar_init(&sm.bar[0], 1);
+        tc::mbar_init(&sm.bar[1], 1);
+        tc::fence_mbar_init();
+    }
+    cluster_arrive();  // (waited for before anything is sent to another CTA)
     next_may_begin();
     before_reading();
     long bos = 0;
@@ -253,6 +312,7 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
         return;
     }
     int cur = 0, count = 1, ngone = 0, pass = 0;
+    bool ok = true;  // the same in all threads of the CTA
     Wide c = wide(0.f), Z = wide(1.f);
     Row<DRAFT> row;
     int g0 = 0, g1 = 0;        // this warp's groups
@@ -269,12 +329,7 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
         const int w = (int)rank * kVerWarps + warp;
         g0 = min(w * per, groups);
         g1 = min(g0 + per, groups);
-        row.ngone = 0;
-        if (!DRAFT && ngone > 0) {
-            const int e0 = row.first(g0), e1 = row.first(g1);
-            for (int i = 0; i < ngone; ++i)
-                if (sm.gone[i] >= e0 && sm.gone[i] < e1) row.ngone = ngone;
-        }
+        row.list(ngone, row.first(g0), row.first(g1));
         Two acc[2] = {{f2(0.f, 0.f), f2(0.f, 0.f)}, {f2(0.f, 0.f), f2(0.f, 0.f)}};
         const bool with_q = DRAFT && c.hi != 0.f;
         const int whole0 = row.shift < 0, whole1 = (a.V - row.shift) / 4;  // groups of 4 elements
@@ -307,27 +362,26 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
             const int j = lane == 0 ? 0 : whole1;
             float x[4], y[4];
             row.load(j, x, y);
-            add(acc[0], row.weights(x[0], x[1], y[0], y[1], row.first(j)));
-            add(acc[1], row.weights(x[2], x[3], y[2], y[3], row.first(j) + 2));
+            row.strike_alone(x, row.first(j));
+            add(acc[0], row.weights(x[0], x[1], y[0], y[1]));
+            add(acc[1], row.weights(x[2], x[3], y[2], y[3]));
         }
         uint32_t at = mine_at;
 #pragma unroll 1
         for (int j = j0; j - lane < end; j += 64) {
             copies_wait<kFlight - 1>();
-            float4 x[2], y[2];
+            float x[2][4] = {}, y[2][4] = {};
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                x[u] = y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int u = 0; u < 2; ++u)
                 if (j + 32 * u < end) {
-                    x[u] = take16(at + u * (C::SLOT / 2));
-                    if (with_q) y[u] = take16(at + u * (C::SLOT / 2) + kVerThreads * 16);
+                    take16(at + u * (C::SLOT / 2), x[u]);
+                    if (with_q) take16(at + u * (C::SLOT / 2) + kVerThreads * 16, y[u]);
                 }
-            }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int e = row.first(j + 32 * u);
-                add(acc[0], row.weights(x[u].x, x[u].y, y[u].x, y[u].y, e));
-                add(acc[1], row.weights(x[u].z, x[u].w, y[u].z, y[u].w, e + 2));
+                row.strike(x[u], row.first(j + 32 * u), row.first(j - lane + 32 * u));
+                add(acc[0], row.weights(x[u][0], x[u][1], y[u][0], y[u][1]));
+                add(acc[1], row.weights(x[u][2], x[u][3], y[u][2], y[u][3]));
             }
             ask();
             at = to;
@@ -336,11 +390,17 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
         get(acc[0], s0, s1);
         get(acc[1], s2, s3);
         const Wide mine = warp_total(plus(plus(s0, s1), plus(s2, s3)));
+        // A CTA's pass p + 2 comes after it has all sums of p + 1, and those after their warps are done with the sums of p.
         Wide *part = sm.part[pass & 1];
+        uint64_t *bar = &sm.bar[pass & 1];
+        const uint32_t phase = (pass >> 1) & 1;
+        if (tid == 0) tc::mbar_expect_tx(bar, C::PARTS * (uint32_t)sizeof(Wide));
         if (pass++ == 0) cluster_wait();
-        if (lane < C::C) store_remote(part + w, (uint32_t)lane, mine);
-        cluster_arrive();
-        cluster_wait();
+        if (lane < C::C) send(part + w, bar, (uint32_t)lane, mine);
+        if (__syncthreads_or(!received(bar, phase, budget))) {
+            ok = false;
+            return wide(0.f);
+        }
         ends[0] = part[NP * lane];
 #pragma unroll
         for (int i = 1; i < NP; ++i) ends[i] = plus(ends[i - 1], part[NP * lane + i]);
@@ -350,10 +410,17 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
         return shuffle(ends[NP - 1], 31);
     };
     bool stale = false;  // Z is not yet known
-    for (int t = 1; t < nodes; ++t) {  // children come after their parents, so one walk over the nodes meets them in turn
-        if (sm.up[t] != cur) continue;
+    const int up0 = lane < nodes ? sm.up[lane] : -2, up1 = lane + 32 < nodes ? sm.up[lane + 32] : -2;
+    auto children = [&]() -> uint64_t {
+        return (uint64_t)__ballot_sync(0xffffffffu, up1 == cur) << 32 | __ballot_sync(0xffffffffu, up0 == cur);
+    };
+    uint64_t left = children();  // of the current node, in turn
+    while (left != 0) {
+        const int t = __ffsll((long long)left) - 1;
+        left &= left - 1;
         if (stale) {
             Z = sum_row();
+            if (!ok) break;
             stale = false;
         }
         const int x = sm.token[t];
@@ -374,6 +441,7 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
             Z = wide(1.f);
             if (!DRAFT) __syncthreads();  // (gone is read until here)
             ngone = 0;
+            left = children();
         } else if (DRAFT) {
             c = plus(c, Z);
             stale = true;
@@ -385,15 +453,28 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
             __syncthreads();
         }
     }
-    Wide total = sum_row();
-    if (!(total.hi > 0.f) && (c.hi > 0.f || ngone > 0)) {  // nothing is left of it: from p
+    Wide total = wide(0.f);
+    if (ok) total = sum_row();
+    if (ok && !(total.hi > 0.f) && (c.hi > 0.f || ngone > 0)) {  // nothing is left of it: from p
         c = wide(0.f);
         ngone = 0;
         total = sum_row();
     }
+    if (!ok) count = 0;  // (a wait has run out)
     if (rank == 0)
         for (int i = tid; i < a.path_stride; i += kVerThreads) path[i] = i < count ? sm.path[i] : -1;
     if (rank == 0 && tid == 0) a.counts[n] = count;
+    if (!ok) {
+        if (tid == 0) {
+            flag_error(a.status);
+            a.next[n] = -1;
+        }
+        // until no other CTA is going to send anything here: those which are done count as there
+        cluster_arrive();
+        cluster_wait();
+        __nanosleep(100000);
+        return;
+    }
     if (!(total.hi > 0.f && total.hi < INFINITY)) {
         flag_error(a.status);
         if (rank == 0 && tid == 0) a.next[n] = -1;
@@ -421,17 +502,14 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
     const int groups = row.groups(), per = (groups + C::PARTS - 1) / C::PARTS;
     g0 = min(owner * per, groups);
     g1 = min(g0 + per, groups);
-    row.ngone = ngone;
+    row.list(ngone, row.first(g0), row.first(g1));
     const int steps = (g1 - g0 + 31) / 32;
     auto group_weights = [&](int j, Wide (&w)[4]) -> Wide {
-        float x[4], y[4];
-        if (j < g1) {
-            row.load(j, x, y);
-            get(row.weights(x[0], x[1], y[0], y[1], row.first(j)), w[0], w[1]);
-            get(row.weights(x[2], x[3], y[2], y[3], row.first(j) + 2), w[2], w[3]);
-        } else {
-            w[0] = w[1] = w[2] = w[3] = wide(0.f);
-        }
+        float x[4] = {}, y[4] = {};
+        if (j < g1) row.load(j, x, y);
+        row.strike(x, row.first(j), row.first(j - lane));
+        get(row.weights(x[0], x[1], y[0], y[1]), w[0], w[1]);
+        get(row.weights(x[2], x[3], y[2], y[3]), w[2], w[3]);
         return plus(plus(w[0], w[1]), plus(w[2], w[3]));
     };
     for (int s = warp; s < steps; s += kVerWarps) {
@@ -509,7 +587,7 @@ cudaError_t launch_t(const VerifyArgs &a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return cudaLaunchKernelEx(&cfg, kernel, a, wait_budget());
 }
 
 }  // namespace

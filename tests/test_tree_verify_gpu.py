@@ -49,7 +49,8 @@ def run(c, width=None, status=gdn.GDN_OK, strides=(None, None)):
     gdn.gdn_tree_verify(spread(c["target"], strides[0], 0), None if c["draft"] is None else spread(c["draft"], strides[1], 0),
                         c["tokens"].to(DEV), parents, c["r"].to(DEV), c["r_last"].to(DEV), path, counts, token,
                         cu_seqlens=None if len(set(nodes)) == 1 else cu_of(nodes))
-    assert gdn.gdn_get_device_status() == status
+    found = gdn.gdn_get_device_status()
+    assert status is None or found == status
     return path.cpu(), counts.cpu(), token.cpu()
 
 
@@ -231,3 +232,14 @@ def test_a_captured_graph_and_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     check(c2, (path.cpu(), counts.cpu(), token.cpu()))
+
+
+@pytest.mark.parametrize("sequences", [1, 20])
+def test_waits_that_run_out_are_reported_and_the_next_call_is_right(sequences, monkeypatch):
+    """GDN_TEST_WAIT_CYCLES shortens the limit of the kernel's waits for what its CTAs send one another."""
+    c = case([9] * sequences, 5001, True, "star", seed=3)
+    monkeypatch.setenv("GDN_TEST_WAIT_CYCLES", "1")
+    path, counts, token = run(c, status=None)
+    monkeypatch.delenv("GDN_TEST_WAIT_CYCLES")
+    assert (counts[counts != 0] > 0).all() and (token >= -1).all()
+    check(c, run(c))
