@@ -80,12 +80,16 @@ struct CoefPlain {
 };
 
 // ---- the nodes of a head ---------------------------------------------------------------------------
+// A gate below this counts as it: nothing of what lies above the node is left either way, and what lies below takes its decays
+// from differences of sums, which keep their precision (-infinity's would have none, nor those of a type's lowest value).
+constexpr float kNoGate = -1e6f;
+
 template <int TP>
 struct __align__(16) Scalars {   // of each node (four nodes' are one access)
     float beta[TP], x[TP];       // beta;  beta e^G rk, the factor of X_k
     float z[TP];                 // e^G rq, the factor of X_q
     float rq[TP], b2[TP];        // 1 / |q|;  beta rk^2
-    float g[TP], g_lo[TP];       // G as a sum of two (bf16 inputs: of its log2 e fold)
+    float g[TP], g_lo[TP];       // G as a sum of two (bf16 inputs: its log2 e fold)
     float gk[TP];                // g_lo less the logarithm of 1 / |k|, to the same base
 };
 
@@ -153,10 +157,15 @@ struct Nodes {
         const int warp = threadIdx.x >> 5, t = node();
         if (warp != W0 && !(TP > 32 && warp == W1)) return;
         b = sigmoidf_(b);
-        float hi = g, lo = 0.f;
+        // g log2 e, whose second float is 1.926e-8
+        float hi = g * kLog2e, lo = fmaf(g, 1.92596303e-8f, fmaf(g, kLog2e, -hi));
+        if (hi < kNoGate) {
+            hi = kNoGate;
+            lo = 0.f;
+        }
         uint64_t path;
         if constexpr (TP <= 32) {
-            float his[2] = {hi, 0.f}, los[2] = {0.f, 0.f};
+            float his[2] = {hi, 0.f}, los[2] = {lo, 0.f};
             path = tree_paths<true, false>(up, -2, status, his, los).of(0);
             hi = his[0];
             lo = los[0];
@@ -192,11 +201,9 @@ struct Nodes {
         }
         if (t < 0) return;
         paths[t] = path;
-        // times log2 e, whose second float is 1.926e-8
-        const float x = hi * kLog2e, y = fmaf(hi, 1.92596303e-8f, fmaf(lo, kLog2e, fmaf(hi, kLog2e, -x)));
-        sc.g[t] = x;
-        sc.g_lo[t] = y;
-        sc.z[t] = ex2(x + y);
+        sc.g[t] = hi;
+        sc.g_lo[t] = lo;
+        sc.z[t] = ex2(hi + lo);
     }
     // ... and with the products' diagonals at hand, the rest
     __device__ __forceinline__ void finish(int T, const CoefBlocks &kk, const float *qq, Scalars<TP> &sc) const {
@@ -263,7 +270,8 @@ __device__ __forceinline__ void node_products(uint32_t kq, int nb, int *unit, co
     }
 }
 
-// Q K^T in wt becomes W, as two bf16 terms. kk: K K^T, with zeros from the diagonal on in the blocks that it goes through. A row by four lanes: lane `sub` holds columns 16 j + 4 sub .. + 3.
+// Q K^T in wt becomes W, as two bf16 terms. kk: K K^T, with zeros from the diagonal on in the blocks that it goes through. A
+// row by four lanes: lane `sub` holds columns 16 j + 4 sub .. + 3.
 // (kPlain: as fp32.)
 template <int TP, int THREADS, typename KT, typename WT>
 __device__ __forceinline__ void form_w(int T, const uint64_t *paths, const Scalars<TP> &sc, const KT &kk, const WT &wt) {

@@ -64,7 +64,10 @@ __global__ void __launch_bounds__(kScanThreads) tree_scan_kernel(const TreeArgs 
         sm.path[lane] = p.of(0);
         sm.path[lane + 32] = p.of(1);
     }
-    if (tid < nodes) sm.g[tid] = ((const float *)a.g)[(bos + tid) * a.Hv + h];
+    if (tid < nodes) {
+        const float g = ((const float *)a.g)[(bos + tid) * a.Hv + h];
+        sm.g[tid] = g < kNoGate ? kNoGate : g;
+    }
     for (int t = warp; t < nodes; t += WARPS) {
         const float *kr = k + ((bos + t) * a.Hk + hk) * DK, *qr = q + ((bos + t) * a.Hk + hk) * DK;
         float x[DK / 32], y[DK / 32], sk = 0.f, sq = 0.f;

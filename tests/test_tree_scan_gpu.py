@@ -373,3 +373,19 @@ def test_many_sequences():
             one = [t[at] for t in x[:5]] + [x[5][n:n + 1]]
             assert_scan(out[at], *tree_scan(*one, trees[n:n + 1]), 128)
     assert gdn.gdn_get_device_status() == gdn.GDN_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dv", [64, 128])
+@pytest.mark.parametrize("gate", [-float("inf"), "lowest", -1e20, -1e7, -300.0])
+def test_gates_that_leave_nothing(gate, dv, dtype):
+    """Gates so low that a node's state is what it writes itself: what lies below keeps its own decays."""
+    trees = make("wide") + make("packed")
+    x = list(inputs(trees, 1, 2, 128, dv, dtype, seed=21))
+    g = x[3].clone()
+    for node in (1, 4, 9, 70):
+        g[node] = torch.finfo(g.dtype).min if gate == "lowest" else gate
+    x[3] = g
+    out = scan(x, trees)
+    assert torch.isfinite(out).all()
+    assert_scan(out, *tree_scan(*x, trees), 128)
