@@ -22,10 +22,10 @@ __device__ __forceinline__ bool tree_bounds(const int32_t *cu, int n, int B, lon
     return true;
 }
 
-// a + b as a rounded sum and what was lost
+// hi + x as a rounded sum, and what that lost added to lo (no product that hi or x comes from may be drawn into it)
 __device__ __forceinline__ void add_exact(float &hi, float &lo, float x) {
-    const float s = hi + x, y = s - hi;
-    lo += (hi - (s - y)) + (x - y);
+    const float s = __fadd_rn(hi, x), y = __fsub_rn(s, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, y)), __fsub_rn(x, y)));
     hi = s;
 }
 

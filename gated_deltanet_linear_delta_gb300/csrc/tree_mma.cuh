@@ -158,7 +158,7 @@ struct Nodes {
         if (warp != W0 && !(TP > 32 && warp == W1)) return;
         b = sigmoidf_(b);
         // g log2 e, whose second float is 1.926e-8
-        float hi = g * kLog2e, lo = fmaf(g, 1.92596303e-8f, fmaf(g, kLog2e, -hi));
+        float hi = __fmul_rn(g, kLog2e), lo = fmaf(g, 1.92596303e-8f, fmaf(g, kLog2e, -hi));
         if (hi < kNoGate) {
             hi = kNoGate;
             lo = 0.f;

@@ -49,20 +49,25 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // ---- numbers of 48 bits: hi + lo, |lo| at most half a unit of hi -----------------------
+// (By operations that round on their own whatever the compiler makes of their neighbours: a product drawn into the sum after it
+// would leave lo beyond half a unit, and below() would compare the wrong hi.)
 struct Wide {
     float hi, lo;
 };
 __device__ __forceinline__ Wide wide(float x) { return Wide{x, 0.f}; }
+__device__ __forceinline__ Wide in_shape(float s, float e) {  // of s + e, e a unit or two of s at most
+    const float h = __fadd_rn(s, e);
+    return Wide{h, __fsub_rn(e, __fsub_rn(h, s))};
+}
 __device__ __forceinline__ Wide plus(Wide a, Wide b) {
-    const float s = a.hi + b.hi, y = s - a.hi;
-    const float e = ((a.hi - (s - y)) + (b.hi - y)) + (a.lo + b.lo);
-    const float h = s + e;
-    return Wide{h, e - (h - s)};
+    const float s = __fadd_rn(a.hi, b.hi), y = __fsub_rn(s, a.hi);
+    const float lost = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, y)), __fsub_rn(b.hi, y));
+    return in_shape(s, __fadd_rn(lost, __fadd_rn(a.lo, b.lo)));
 }
 __device__ __forceinline__ Wide minus(Wide a, Wide b) { return plus(a, Wide{-b.hi, -b.lo}); }
 __device__ __forceinline__ Wide times(Wide a, float f) {
-    const float p = a.hi * f, e = fmaf(a.lo, f, fmaf(a.hi, f, -p)), h = p + e;
-    return Wide{h, e - (h - p)};
+    const float p = __fmul_rn(a.hi, f);
+    return in_shape(p, __fmaf_rn(a.lo, f, __fmaf_rn(a.hi, f, -p)));
 }
 __device__ __forceinline__ bool below(Wide a, Wide b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
 __device__ __forceinline__ Wide shuffle(Wide a, int from) {
