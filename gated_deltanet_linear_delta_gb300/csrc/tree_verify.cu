@@ -15,7 +15,7 @@
 // nodes with drafts, V = 131072: 38.5 us from registers, 33.5 so; the first pass over them all takes 12 of those, 67 MB at
 // 5.5 TB/s, the two later ones of the longest walks 4 to 5 each). What a warp finds goes to all CTAs by asynchronous stores
 // that their barriers count, 0.4 us from the last one sent; by stores and a barrier of the cluster a pass took 1 us more.
-// One session of 16 nodes, V = 150001, no draft probabilities: 6.8 us from a graph.
+// One session of 16 nodes, V = 150001, no draft probabilities: 7.0 us from a graph.
 //
 // Precision. A draw compares r times a sum with partial sums over V values that lie close to one another, so weights
 // and sums are kept as two floats each (48 bits). In fp64, of which an SM does two operations a cycle, the sums over the
@@ -46,6 +46,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // ---- numbers of 48 bits: hi + lo, |lo| at most half a unit of hi -----------------------
@@ -96,19 +97,27 @@ __device__ __forceinline__ void send(Wide *at, uint64_t *bar, uint32_t rank, Wid
                  "r"(to_bar)
                  : "memory");
 }
-// Wait for what other CTAs send, with a limit in cycles
+__device__ __forceinline__ void tell(int *at, uint32_t rank, int x) {  // (seen after the next barrier of the cluster)
+    uint32_t to;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(tc::smem_u32(at)), "r"(rank));
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(to), "r"(x) : "memory");
+}
+__device__ __forceinline__ void count_off(uint64_t *bar, uint32_t bytes) {  // as if they had come
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(tc::smem_u32(bar)), "r"(bytes) : "memory");
+}
+// Wait for what other CTAs send, with a limit in cycles, which is looked at before the thread first sleeps
 __device__ __forceinline__ bool received(uint64_t *bar, uint32_t phase, long long budget) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(tc::smem_u32(bar)), "r"(phase)
+                 : "memory");
+    if (done) return true;
     const long long t0 = clock64();
-    while (true) {
-        uint32_t done;
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, 1000;\nselp.u32 %0, 1, 0, p;\n}"
-            : "=r"(done)
-            : "r"(tc::smem_u32(bar)), "r"(phase)
-            : "memory");
-        if (done) return true;
+    do {
         if (clock64() - t0 > budget) return false;
-    }
+    } while (!tc::mbar_try_wait_cluster(bar, phase, 1000u));
+    return true;
 }
 
 // Two such numbers side by side, without the last step that brings them into shape: one packed operation serves both.
@@ -155,6 +164,7 @@ template <typename C>
 struct VerSmem {
     Wide part[2][C::PARTS];  // a pass's sums by warp, two passes' by turns
     uint64_t bar[2];         // .. arrivals
+    int sent[C::C];          // of a CTA whose wait has run out: the passes whose sums it has sent; else 0
     Wide step[C::STEPS];
     int up[kTreeMax], token[kTreeMax], gone[kTreeMax], path[kTreeMax];
     float p[kTreeMax], q[kTreeMax], r[kTreeMax];
@@ -269,6 +279,8 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
         tc::mbar_init(&sm.bar[1], 1);
         tc::fence_mbar_init();
     }
+    if (tid < C::C) sm.sent[tid] = 0;
+    __syncwarp();
     cluster_arrive();  // (waited for before anything is sent to another CTA)
     next_may_begin();
     before_reading();
@@ -465,109 +477,135 @@ __global__ void __launch_bounds__(kVerThreads, C::PER_SM) tree_verify_kernel(con
         ngone = 0;
         total = sum_row();
     }
-    if (!ok) count = 0;  // (a wait has run out)
-    if (rank == 0)
-        for (int i = tid; i < a.path_stride; i += kVerThreads) path[i] = i < count ? sm.path[i] : -1;
-    if (rank == 0 && tid == 0) a.counts[n] = count;
-    if (!ok) {
-        if (tid == 0) {
-            flag_error(a.status);
-            a.next[n] = -1;
-        }
-        // until no other CTA is going to send anything here: those which are done count as there
+    // No CTA leaves while others may send to it, and a sequence has the results of all of its CTAs or none: each says here
+    // that it has every sum of the last pass, or that one of its waits has run out.
+    if (ok) {
+        cluster_arrive_relaxed();  // (nothing that it has written is for others: a release here took 0.4 us)
+    } else {
+        if (tid < C::C) tell(&sm.sent[rank], (uint32_t)tid, pass);
+        __syncwarp();
         cluster_arrive();
-        cluster_wait();
-        __nanosleep(100000);
-        return;
     }
-    if (!(total.hi > 0.f && total.hi < INFINITY)) {
-        flag_error(a.status);
-        if (rank == 0 && tid == 0) a.next[n] = -1;
-        return;
-    }
-    // the part that holds the draw: the first whose end is above it, or else the last that has weight
-    const Wide draw = times(total, r_last);
-    int owner = kVerWarps * C::C, last_live = -1;
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const bool live = sm.part[(pass - 1) & 1][NP * lane + i].hi > 0.f;
-        const unsigned at = __ballot_sync(0xffffffffu, live && below(draw, ends[i])), some = __ballot_sync(0xffffffffu, live);
-        if (at) owner = min(owner, NP * (__ffs(at) - 1) + i);
-        if (some) last_live = max(last_live, NP * (31 - __clz(some)) + i);
-    }
-    if (owner == kVerWarps * C::C) owner = max(last_live, 0);
-    if (owner / kVerWarps != (int)rank) return;
-    Wide base = wide(0.f);  // the sum of all parts before it
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-        const Wide e = shuffle(ends[i], (owner > 0 ? owner - 1 : 0) / NP);
-        if (owner > 0 && (owner - 1) % NP == i) base = e;
-    }
-    // its steps of 128 elements, by all warps; then the step, by one
-    const int groups = row.groups(), per = (groups + C::PARTS - 1) / C::PARTS;
-    g0 = min(owner * per, groups);
-    g1 = min(g0 + per, groups);
-    row.list(ngone, row.first(g0), row.first(g1));
-    const int steps = (g1 - g0 + 31) / 32;
-    auto group_weights = [&](int j, Wide (&w)[4]) -> Wide {
-        float x[4] = {}, y[4] = {};
-        if (j < g1) row.load(j, x, y);
-        row.strike(x, row.first(j), row.first(j - lane));
-        get(row.weights(x[0], x[1], y[0], y[1]), w[0], w[1]);
-        get(row.weights(x[2], x[3], y[2], y[3]), w[2], w[3]);
-        return plus(plus(w[0], w[1]), plus(w[2], w[3]));
-    };
-    for (int s = warp; s < steps; s += kVerWarps) {
-        Wide w[4];
-        const Wide x = warp_total(group_weights(g0 + 32 * s + lane, w));
-        if (lane == 0) sm.step[s] = x;
-    }
-    __syncthreads();
-    if (warp != 0) return;
-    int step = -1, fallback = -1;
-    Wide step_base = base, fallback_base = base;
-    for (int s = 0; s < steps && step < 0; s += 32) {
-        const Wide x = s + lane < steps ? sm.step[s + lane] : wide(0.f);
-        const Wide end = plus(base, warp_scan(x));
-        const unsigned hit = __ballot_sync(0xffffffffu, x.hi > 0.f && below(draw, end)), some = __ballot_sync(0xffffffffu, x.hi > 0.f);
-        const Wide begin = minus(end, x);
-        if (hit) {
-            step = s + __ffs(hit) - 1;
-            step_base = shuffle(begin, __ffs(hit) - 1);
-        } else if (some) {
-            fallback = s + 31 - __clz(some);
-            fallback_base = shuffle(begin, 31 - __clz(some));
-        }
-        base = shuffle(end, 31);
-    }
-    if (step < 0) {
-        step = fallback;
-        step_base = fallback_base;
-    }
-    if (step < 0) {  // (weights below zero, which the caller must not pass)
-        if (lane == 0) {
+    constexpr int kNone = -2;
+    // The next token, -1 if there is none (flagged), in one thread of the cluster; kNone in all others.
+    auto draw_token = [&]() -> int {
+        if (!(total.hi > 0.f && total.hi < INFINITY)) {
             flag_error(a.status);
-            a.next[n] = -1;
+            return rank == 0 && tid == 0 ? -1 : kNone;
         }
-        return;
-    }
-    Wide w[4];
-    const int j = g0 + 32 * step + lane;
-    const Wide x_all = group_weights(j, w);
-    Wide sum = minus(plus(step_base, warp_scan(x_all)), x_all);
-    int pick = -1, last = -1;
+        // the part that holds the draw: the first whose end is above it, or else the last that has weight
+        const Wide draw = times(total, r_last);
+        int owner = kVerWarps * C::C, last_live = -1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        sum = plus(sum, w[i]);
-        if (w[i].hi > 0.f) {
-            last = row.first(j) + i;
-            if (pick < 0 && below(draw, sum)) pick = last;
+        for (int i = 0; i < NP; ++i) {
+            const bool live = sm.part[(pass - 1) & 1][NP * lane + i].hi > 0.f;
+            const unsigned at = __ballot_sync(0xffffffffu, live && below(draw, ends[i])), some = __ballot_sync(0xffffffffu, live);
+            if (at) owner = min(owner, NP * (__ffs(at) - 1) + i);
+            if (some) last_live = max(last_live, NP * (31 - __clz(some)) + i);
+        }
+        if (owner == kVerWarps * C::C) owner = max(last_live, 0);
+        if (owner / kVerWarps != (int)rank) return kNone;
+        Wide base = wide(0.f);  // the sum of all parts before it
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const Wide e = shuffle(ends[i], (owner > 0 ? owner - 1 : 0) / NP);
+            if (owner > 0 && (owner - 1) % NP == i) base = e;
+        }
+        // its steps of 128 elements, by all warps; then the step, by one
+        const int groups = row.groups(), per = (groups + C::PARTS - 1) / C::PARTS;
+        g0 = min(owner * per, groups);
+        g1 = min(g0 + per, groups);
+        row.list(ngone, row.first(g0), row.first(g1));
+        const int steps = (g1 - g0 + 31) / 32;
+        auto group_weights = [&](int j, Wide (&w)[4]) -> Wide {
+            float x[4] = {}, y[4] = {};
+            if (j < g1) row.load(j, x, y);
+            row.strike(x, row.first(j), row.first(j - lane));
+            get(row.weights(x[0], x[1], y[0], y[1]), w[0], w[1]);
+            get(row.weights(x[2], x[3], y[2], y[3]), w[2], w[3]);
+            return plus(plus(w[0], w[1]), plus(w[2], w[3]));
+        };
+        for (int s = warp; s < steps; s += kVerWarps) {
+            Wide w[4];
+            const Wide x = warp_total(group_weights(g0 + 32 * s + lane, w));
+            if (lane == 0) sm.step[s] = x;
+        }
+        __syncthreads();
+        if (warp != 0) return kNone;
+        int step = -1, fallback = -1;
+        Wide step_base = base, fallback_base = base;
+        for (int s = 0; s < steps && step < 0; s += 32) {
+            const Wide x = s + lane < steps ? sm.step[s + lane] : wide(0.f);
+            const Wide end = plus(base, warp_scan(x));
+            const unsigned hit = __ballot_sync(0xffffffffu, x.hi > 0.f && below(draw, end)), some = __ballot_sync(0xffffffffu, x.hi > 0.f);
+            const Wide begin = minus(end, x);
+            if (hit) {
+                step = s + __ffs(hit) - 1;
+                step_base = shuffle(begin, __ffs(hit) - 1);
+            } else if (some) {
+                fallback = s + 31 - __clz(some);
+                fallback_base = shuffle(begin, 31 - __clz(some));
+            }
+            base = shuffle(end, 31);
+        }
+        if (step < 0) {
+            step = fallback;
+            step_base = fallback_base;
+        }
+        if (step < 0) {  // (weights below zero, which the caller must not pass)
+            flag_error(a.status);
+            return lane == 0 ? -1 : kNone;
+        }
+        Wide w[4];
+        const int j = g0 + 32 * step + lane;
+        const Wide x_all = group_weights(j, w);
+        Wide sum = minus(plus(step_base, warp_scan(x_all)), x_all);
+        int pick = -1, last = -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum = plus(sum, w[i]);
+            if (w[i].hi > 0.f) {
+                last = row.first(j) + i;
+                if (pick < 0 && below(draw, sum)) pick = last;
+            }
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, pick >= 0), some = __ballot_sync(0xffffffffu, last >= 0);
+        const int token = hit ? __shfl_sync(0xffffffffu, pick, __ffs(hit) - 1)
+                              : __shfl_sync(0xffffffffu, last, some ? 31 - __clz(some) : 0);
+        return lane == 0 ? token : kNone;
+    };
+    const int token = ok ? draw_token() : kNone;
+    __syncwarp();
+    cluster_wait();
+    bool whole = true;
+#pragma unroll
+    for (int r = 0; r < C::C; ++r) whole &= sm.sent[r] == 0;
+    if (!whole) count = 0;
+    if (rank == 0) {
+        for (int i = tid; i < a.path_stride; i += kVerThreads) path[i] = i < count ? sm.path[i] : -1;
+        if (tid == 0) a.counts[n] = count;
+        if (!whole && tid == 0) a.next[n] = -1;
+    }
+    if (whole && token != kNone) a.next[n] = token;
+    if (!ok && tid == 0) {
+        flag_error(a.status);
+        // What others have sent lands before this CTA leaves. Every CTA sends its sums of a pass before it waits for those of the
+        // others, so of the pass whose wait ran out all come but those of CTAs that gave up one pass before, which are counted
+        // off; and CTAs that went on have sent those of one pass more, since it takes all CTAs' to go on again.
+        int behind = 0, ahead = 0;
+        for (int r = 0; r < C::C; ++r) {
+            behind += sm.sent[r] != 0 && sm.sent[r] < pass;
+            ahead += sm.sent[r] > pass;
+        }
+        constexpr uint32_t kBytes = kVerWarps * (uint32_t)sizeof(Wide);  // of a CTA
+        uint64_t *bar = &sm.bar[(pass - 1) & 1], *next = &sm.bar[pass & 1];
+        if (behind > 0) count_off(bar, behind * kBytes);
+        received(bar, ((pass - 1) >> 1) & 1, kDrainBudget);
+        if (ahead > 0) {
+            tc::mbar_expect_tx(next, ahead * kBytes);
+            received(next, (pass >> 1) & 1, kDrainBudget);
         }
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, pick >= 0), some = __ballot_sync(0xffffffffu, last >= 0);
-    const int token = hit ? __shfl_sync(0xffffffffu, pick, __ffs(hit) - 1)
-                          : __shfl_sync(0xffffffffu, last, some ? 31 - __clz(some) : 0);
-    if (lane == 0) a.next[n] = token;
 }
 
 template <typename C>

@@ -518,6 +518,7 @@ GDN_API int gdn_tree_advance(const void *k, const void *v, const void *g, const 
  *             any sequence, at most 2^20.
  *   counts  : [B] int32: the entries of path. A sequence without nodes, or whose node 0 is padding, gets 0.
  *   next    : [B] int32: the next token; -1 where counts is 0, or where p's sum is 0 or not finite (flagged).
+ * (A sequence for which a wait inside of the kernel runs out is flagged; counts is 0 then, path -1 and next -1.)
  * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
  */
 GDN_API int gdn_tree_verify(const float *target_probs, const float *draft_probs, const int32_t *tokens,
