@@ -5,7 +5,9 @@
 // which leaves the accepted token distributed as p. Unrolled, w_{i+1} = max(p - c q, 0) with c = Z_1 + .. + Z_i, so
 // only one number is carried over the vocabulary, and a rejection followed by another child, or by the draw of the
 // next token from what is left, costs one pass over the two rows. Without draft probabilities q is one at the child's
-// token: a rejection takes that token out and needs no pass.
+// token: a rejection takes that token out, Z_{i+1} = Z_i - w_i(x_i), and needs no pass. (That counts p's sum as 1. Where it
+// is not, the children x_i still come with probability p(x_i), and all other tokens share 1 - p(x_1) - .. in p's
+// proportions; by the sum of what is left it would be the children whose odds are off.)
 //
 // What bounds it: a row or two of V fp32 per sequence, and for few sequences the chain of dependent steps (the tree, the
 // tokens' probabilities, a pass, the draw). A cluster of CTAs takes a sequence, each a run of the row, each warp a part

@@ -506,8 +506,11 @@ GDN_API int gdn_tree_advance(const void *k, const void *v, const void *g, const 
  *     else  w <- max(w - Z q, 0),  Z <- sum w.
  * With no child left the next token is the least x for which the sum of w up to x is above r_last[n] times the whole sum
  * (of p, if w has no weight left). If each node's children were drawn from its q, independently, the accepted and next
- * tokens are distributed as the target's. draft_probs NULL: each child was proposed for certain (q is one at its token).
- * Weights and sums are kept to 48 bits.
+ * tokens are distributed as the target's. Weights and sums are kept to 48 bits.
+ * draft_probs NULL: each child was proposed for certain, and its acceptance looks at the children's weights alone:
+ *     child i with token x is accepted if  r[i] Z < w(x);  else  Z <- Z - w(x),  w(x) <- 0.
+ * (With p's sum 1, Z is the sum of w.) So each child's token comes with probability p(x) whatever p's sum is, which fp32
+ * rows miss by about 1e-7, and the other tokens share what is left of 1.
  *
  *   target_probs, draft_probs : [Ttot][V] fp32, rows target_stride and draft_stride elements apart (at least V);
  *           not negative, each row's sum 1. V: 1 .. 4194304.
