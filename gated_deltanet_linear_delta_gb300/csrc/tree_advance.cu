@@ -24,8 +24,8 @@ constexpr int kAdvThreads = 256, kAdvWarps = kAdvThreads / 32, kAdvNodes = 8;
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(kAdvThreads, kAdvPerSm<DK, DV>) tree_advance_kernel(const TreeArgs a) {
     constexpr int P = DK / 32;                                        // pieces of a row in a lane
-    constexpr int ROWS = DV < 4 * kAdvWarps ? DV : 4 * kAdvWarps;     // rows a pass
-    constexpr int R = DV / ROWS;                                      // passes
+    constexpr int ROWS = 4 * kAdvWarps, R = DV / ROWS;                // rows a pass; passes
+    static_assert(DV % ROWS == 0, "every lane holds a piece of a row in every pass");
     __shared__ float kh[kAdvNodes][DK], vv[kAdvNodes][DV], alpha[kAdvNodes], beta[kAdvNodes];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = lane & 7;
     const int n = blockIdx.x / a.Hv, h = blockIdx.x % a.Hv, hk = h / (a.Hv / a.Hk);
@@ -36,14 +36,13 @@ __global__ void __launch_bounds__(kAdvThreads, kAdvPerSm<DK, DV>) tree_advance_k
     if (!tree_bounds(a.cu, n, a.B, a.cu ? a.Ttot : a.T, &bos, &nodes, a.status)) return;
     const long slot = state_slot(a, n);
     if (slot < 0) return;
-    const bool holds = warp * 4 < ROWS;  // (with 64 rows or fewer all warps do; 32 columns of values leave none out)
     const long at = ((slot * a.Hv + h) * DV + warp * 4 + (lane >> 3)) * DK + 4 * c;
     float4 s[R][P];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            if (holds) s[r][p] = __ldcs(reinterpret_cast<const float4 *>(a.state_in + at + (long)r * ROWS * DK + 32 * p));
+            s[r][p] = __ldcs(reinterpret_cast<const float4 *>(a.state_in + at + (long)r * ROWS * DK + 32 * p));
     int count = a.counts[n];
     bool bad = count < 0 || count > min(nodes, a.path_stride);
     const int32_t *path = a.path + (long)n * a.path_stride;
@@ -75,7 +74,6 @@ __global__ void __launch_bounds__(kAdvThreads, kAdvPerSm<DK, DV>) tree_advance_k
             }
         }
         __syncthreads();
-        if (!holds) continue;
         const int m = min(kAdvNodes, count - i0);
         for (int i = 0; i < m; ++i) {
             float4 x[P];
@@ -110,7 +108,7 @@ __global__ void __launch_bounds__(kAdvThreads, kAdvPerSm<DK, DV>) tree_advance_k
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int p = 0; p < P; ++p)
-            if (holds) __stcs(reinterpret_cast<float4 *>(a.state_out + at + (long)r * ROWS * DK + 32 * p), s[r][p]);
+            __stcs(reinterpret_cast<float4 *>(a.state_out + at + (long)r * ROWS * DK + 32 * p), s[r][p]);
 }
 
 template <typename T, int DK, int DV>
