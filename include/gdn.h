@@ -474,6 +474,8 @@ GDN_API int gdn_kv_keep(void *k_cache, void *v_cache, float *k_scale, float *v_s
  * With bf16 inputs the states, and the sums over a path, enter the products with 16 bits of precision, the outputs' own
  * rounding aside; with fp32 inputs all is fp32. A key, value or gate that is not finite concerns the nodes whose path
  * holds it, a query its own node. (A gate of -infinity is in order: nothing is left of what lies above.)
+ * Keys and queries have norms below 2^60 per head, here and for gdn_tree_advance; larger ones, whose squares and products
+ * fp32 may not hold, can make what they concern not finite, and nothing else.
  * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
  */
 GDN_API int gdn_tree_scan(const void *q, const void *k, const void *v, const void *g, const void *b,
