@@ -47,7 +47,8 @@ struct RCfg {
     // three cycles, so more warps help as long as registers and rings allow: int8, d = 128, 8 rows (32 sequences of
     // 8192 positions, 8 key heads): 113, 99 and 108 us with 8, 12 and 16 warps; fp8, d = 64 (twice the positions): 161,
     // 126 and 131. At d = 256 the output fills the registers (101, 102 and 106 us; 16 rows: 118 and 156 with 8 and 12
-    // warps), and bf16 is bound by memory with any number.
+    // warps), and bf16 is bound by memory with any number. (12 warps have 168 registers: 16 rows of 8-bit codes at d = 128 spill 56 and
+    // 84 bytes a thread, for trees 72 and 96.)
     static constexpr int WARPS = kCodes && D < 256 ? 12 : 8;
     static constexpr int THREADS = 32 * WARPS;
     static constexpr uint32_t RINGB = 196608 / WARPS;           // a warp's ring

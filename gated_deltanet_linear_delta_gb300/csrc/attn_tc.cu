@@ -19,7 +19,7 @@
 // 64 (1.64 PFLOP/s for 256, of 1.92 measured; 712 us and 1.50 PFLOP/s in a run so long that power caps the
 // clock), e4m3 875 us for 256 and 637 for 128 (int8 668). 8 prompts of 1024 tokens, 32 heads on 8, D = 128:
 // bf16 101, e4m3 203 us: 14 units of 4 or 5 tiles per CTA, whose starts and ends (Q in, rows out) count for
-// half of it. The kernels of 8-bit caches spill 76 to 118 bytes of stores a thread: 768 threads leave 80
+// half of it. The kernels of 8-bit caches spill 76 to 118 bytes of stores a thread (for trees 104 to 132): 768 threads leave 80
 // registers, and the softmax, which has 112 when it runs, is compiled within them.
 //
 // Layout. TMEM holds O (D columns), two S buffers (P_j overlays S_j) and Q as the 16-bit A operand,

@@ -9,15 +9,18 @@
 // one another, and the decays and norms stand outside of them: W_ts = e^{G_t-G_s} rk_s w_s, where from t upwards
 //     w_s = rq_t (q_t.k_s) - sum_{s' in on(t), s' > s} w_s' beta_s' rk_s'^2 (k_s'.k_s),
 // with the raw products of K K^T and Q K^T. So a row costs L^2 / 2 multiply-adds for a path of L nodes, by four lanes,
-// once per head; and the dv rows of the state take no elimination of their own, just products. (A version that
-// eliminated blocks of 16 nodes by shuffles, in each warp for its own rows, took 144 us where this one took 118, for 64
-// sequences of 61 nodes and 32 heads of 128 x 128.)
+// once per head; and the dv rows of the state take no elimination of their own, just products. (With heads of 128 x 128,
+// which ran here then, eliminating blocks of 16 nodes by shuffles in each warp for its own rows took 22% longer.)
 //
 // The products are m16n8k16 (mma.sync), 16 rows of the state to a warp: their accumulator, rows of the state by nodes, is
 // in the layout of the next product's operand, so that R goes from X to O within registers.
 //
-// What bounds it: S_0's bytes for few nodes; for many the dependent steps of a head and the instructions around the
-// products. CTAs are persistent, two or three to an SM, and S_0 comes by TMA in parts of 32 columns through a ring, the next
+// What bounds it: the dependent steps of a head and the instructions around the products (2930 a warp and head of 64 x 128 and 61
+// nodes, one every 2 cycles and scheduler), with few nodes S_0's bytes beside them. 64 sequences, 32 heads, from a graph:
+//     dk x dv             64 x 128    128 x 64    64 x 64    32 x 32
+//     16 nodes, us              31          28         22         18    (bytes alone: 13, 13, 7, 2)
+//     61 nodes, us              85          89         61         67    (22, 20, 12, 5)
+// One session of 16 nodes and 64 x 128 takes 5.0 us. CTAs are persistent, two or three to an SM, and S_0 comes by TMA in parts of 32 columns through a ring, the next
 // head's during the end of this one's work. Every wait has a limit, after which the call flags the status word.
 //
 // Values that are not finite stay on their paths: a product with a coefficient of 0 would spread them, so they are
@@ -328,7 +331,11 @@ cudaError_t launch_t(const TreeArgs &a, cudaStream_t s) {
 
 template <int DK, int DV>
 cudaError_t launch_tp(const TreeArgs &a, cudaStream_t s) {
-    const long most = a.cu ? a.Ttot : a.T;  // nodes of a sequence
+    // The most nodes that a sequence can have: of packed ones that is not known here, but their total is. Up to 16 take an
+    // instance with a quarter of the accumulators: 64 sequences of 5 and of 16 nodes, heads of 64 x 128, take 29 and 31 us in it, and
+    // 45 and 47 in that for 64 (128 x 64: 26, 27 and 43, 44; 64 x 64: 20, 22 and 29, 30; 32 x 32: 16, 18 and 25, 26). From 17 on it is
+    // 55 (53, 36, 35) to 59 (56, 37, 37) at 32. With 128 rows of values the one for 64 spills 28 (dk = 64) and 56 bytes (32) a thread.
+    const long most = a.cu ? a.Ttot : a.T;
     if (most <= 16) return launch_t<DK, DV, 16>(a, s);
     return launch_t<DK, DV, 64>(a, s);
 }

@@ -393,7 +393,10 @@ cudaError_t launch_t(const TreeArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_scan_umma(const TreeArgs &a, cudaStream_t s) {
-    const long most = a.cu ? a.Ttot : a.T;  // nodes of a sequence
+    // The most nodes that a sequence can have: of packed ones that is not known here, but their total is. 64 sequences of 8, 16
+    // and 32 nodes each take 32, 33 and 41 us; packed, of up to as many, 52, 53 and 55, in the instance for 64. (That for 16 has 80
+    // registers for three CTAs to an SM, and spills 24 bytes a thread.)
+    const long most = a.cu ? a.Ttot : a.T;
     return most <= 16 ? launch_t<16>(a, s) : most <= 32 ? launch_t<32>(a, s) : launch_t<64>(a, s);
 }
 

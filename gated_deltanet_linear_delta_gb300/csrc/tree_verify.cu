@@ -14,7 +14,7 @@
 // of that; what a pass finds is sent to all CTAs of the cluster, which take the same decisions.
 // Everything that the walk itself looks at is fetched at once beforehand. A lane's elements come through a ring of its own
 // in shared memory, asked for ahead of their use: registers hold two groups a lane, the ring six (64 sequences of up to 13
-// nodes with drafts, V = 131072: 38.5 us from registers, 33.5 so; the first pass over them all takes 12 of those, 67 MB at
+// nodes with drafts, V = 131072: 38.5 us from registers, 33.5 so, 32.8 now; the first pass over them all takes 12 of those, 67 MB at
 // 5.5 TB/s, the two later ones of the longest walks 4 to 5 each). What a warp finds goes to all CTAs by asynchronous stores
 // that their barriers count, 0.4 us from the last one sent; by stores and a barrier of the cluster a pass took 1 us more.
 // One session of 16 nodes, V = 150001, no draft probabilities: 7.0 us from a graph.
@@ -638,6 +638,14 @@ cudaError_t launch_t(const VerifyArgs &a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_tree_verify(const VerifyArgs &a, cudaStream_t s) {
+    // CTAs to a sequence: 16 against 8, us from a graph, sequences of 13 nodes.
+    //     sequences                       1          4          8          9         12         16         32
+    //     drafts, V = 131072       7.7  9.2  11.9 14.9  13.8 16.4  15.8 18.5  16.1 19.3  19.7 21.9  32.5 30.8
+    //     drafts, V = 32000        8.4  8.6  10.0 10.4  11.7 11.8  10.6 10.7  12.4 12.8  13.2 13.5  22.2 15.9
+    //     no drafts, V = 131072    6.3  7.4   6.7  7.9   7.5  7.9   7.4  8.2   8.8  8.7  10.2  9.5  13.5 11.8
+    //     no drafts, V = 32000     5.7  5.6   6.1  6.0   6.5  6.1   6.5  6.2   7.6  6.2   8.7  6.9  11.1  8.4
+    // (A cluster of 16 finds less room. Up to 16 sequences with drafts it would still be 10% ahead, without drafts behind.)
+    // The kernel for drafts and 8 CTAs has 64 registers, so that four CTAs fit an SM, and spills 24 bytes a thread.
     if (a.B <= 8) return a.draft ? launch_t<Cfg<true, 16, 5, 1>>(a, s) : launch_t<Cfg<false, 16, 5, 1>>(a, s);
     return a.draft ? launch_t<Cfg<true, 8, 3, 4>>(a, s) : launch_t<Cfg<false, 8, 6, 4>>(a, s);
 }
